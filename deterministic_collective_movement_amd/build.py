@@ -1,8 +1,8 @@
 """Build librog.so (the C-ABI library) in-tree for gfx950.
 
-``build_library()`` compiles the host planner and the HIP kernels (gathers and
-rank-ordered sums) with hipcc
-for gfx950, then links ``deterministic_collective_movement_amd/librog.so``.
+``build_library()`` compiles the host planners and the HIP kernels (gathers,
+rank-ordered sums, token log probabilities and the policy loss) with hipcc for
+gfx950, then links ``deterministic_collective_movement_amd/librog.so``.
 Intermediate objects go to ``_build/`` at the repository root.
 ``python -m deterministic_collective_movement_amd.build`` does the same.
 """
@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +22,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "librog.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
+
+HOST_SOURCES = ["rog_plan.cpp", "rog_head_plan.cpp"]
+HIP_SOURCES = ["rog_kernels.hip", "rog_reduce.hip", "rog_logprob.hip", "rog_logprob_grad.hip", "rog_policy.hip"]
 
 # Device code: gfx950 only; packed-FP32 instructions disabled.
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Werror",
@@ -44,15 +48,18 @@ def build_library(out: str = LIB_PATH, defines=(), build_dir: str = BUILD_DIR) -
     os.makedirs(build_dir, exist_ok=True)
     inc = ["-I", INCLUDE, "-I", CSRC, "-I", os.path.join(ROCM, "include")]
     dflags = ["-D" + d for d in defines]
-    plan_o = os.path.join(build_dir, "rog_plan.o")
-    kern_o = os.path.join(build_dir, "rog_kernels.o")
-    red_o = os.path.join(build_dir, "rog_reduce.o")
-    _run([hipcc] + HOST_FLAGS + dflags + inc + ["-c", os.path.join(CSRC, "rog_plan.cpp"), "-o", plan_o])
-    _run([hipcc] + HIP_FLAGS + dflags + inc + ["-c", os.path.join(CSRC, "rog_kernels.hip"), "-o", kern_o])
-    _run([hipcc] + HIP_FLAGS + dflags + inc + ["-c", os.path.join(CSRC, "rog_reduce.hip"), "-o", red_o])
+    # independent translation units, compiled side by side
+    jobs, objs = [], []
+    for src in HOST_SOURCES + HIP_SOURCES:
+        obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
+        flags = HOST_FLAGS if src in HOST_SOURCES else HIP_FLAGS
+        objs.append(obj)
+        jobs.append([hipcc] + flags + dflags + inc + ["-c", os.path.join(CSRC, src), "-o", obj])
+    with ThreadPoolExecutor(max_workers=4) as pool:
+        list(pool.map(_run, jobs))
     tmp = out + ".tmp%d" % os.getpid()
-    _run([hipcc, "-shared", "-fPIC", "--offload-arch=" + ARCH, plan_o, kern_o, red_o,
-          "-Wl,-soname,librog.so", "-Wl,-rpath," + os.path.join(ROCM, "lib"), "-Wl,--no-undefined", "-o", tmp])
+    _run([hipcc, "-shared", "-fPIC", "--offload-arch=" + ARCH] + objs +
+         ["-Wl,-soname,librog.so", "-Wl,-rpath," + os.path.join(ROCM, "lib"), "-Wl,--no-undefined", "-o", tmp])
     os.replace(tmp, out)
     return out
 

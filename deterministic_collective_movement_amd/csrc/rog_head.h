@@ -1,0 +1,115 @@
+// rog_head.h -- kernel arguments and launch plans of the vocabulary-side
+// operators (token log probabilities, their gradient, the policy loss), shared
+// by the host planner (rog_head_plan.cpp) and the HIP kernels.  Internal to
+// librog.so; the public interface is include/rog.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "rog_internal.h"
+
+namespace rog {
+
+// How a row of logits is cut.  The unit is a block: 2048 consecutive columns
+// of one shard (a shard's last block may be shorter), 32 columns per lane of
+// one wave.  Blocks are numbered through the shards in rank order; four
+// consecutive blocks make a quad, and quad q belongs to column q mod 4 of the
+// row.  The partial states are joined in one order, whatever the launch form:
+// the blocks of a quad as (0+1)+(2+3), the quads of a column one after the
+// other, the columns as (0+1)+(2+3), the lanes last.  So a row's bits depend
+// on its values, its shards' widths and the temperature alone, not on how
+// many rows a call has or which workgroups computed them.
+constexpr uint32_t kHeadBlock = 2048;      // columns of a block
+constexpr uint32_t kHeadQuad = 4;          // blocks of a quad, quads in flight per row (columns)
+constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per column (or per block of a quad)
+// Workgroups of a launch, at most: a dispatch counts work-items in 32 bits.
+// The kernels loop over the rest.
+constexpr uint32_t kHeadGridCap = 0xFFFFFFFFu / kHeadThreads;
+constexpr int kMaxTopK = 32;
+constexpr uint32_t kMaxVocab = 1u << 31;   // columns of a row: below this
+
+// The front of a workspace: one arrival counter per row of a split launch (the
+// first one for the policy loss), zero between calls.  Partial states follow.
+constexpr uint32_t kHeadCounters = 4096;
+constexpr size_t kHeadCounterBytes = kHeadCounters * sizeof(uint32_t);
+
+struct HeadShards {
+    const void *x[kMaxPeers];          // element (0, 0) of each shard
+    int64_t stride[kMaxPeers];         // bytes from a row to the next
+    uint32_t width[kMaxPeers];         // columns
+    uint32_t col0[kMaxPeers];          // the shard's first column in the row
+    uint32_t block0[kMaxPeers + 1];    // the shard's first block; [W]: all blocks
+};
+
+struct LogprobArgs {
+    HeadShards sh;
+    const int64_t *tokens;             // NULL: no token, every row scored
+    float *logp, *entropy, *lse, *top_logp;
+    int64_t *top_ids;
+    uint32_t *counters;                // split: one per row
+    float *part;                       // split: partial states
+    float scale;                       // log2(e) / temperature
+    float inv_t;                       // 1 / temperature
+    float bound;                       // |x| beyond this leaves the scaled range
+    uint32_t W, rows, blocks, quads;
+    uint32_t top_k;
+    uint32_t slot_shift;               // log2 of the blocks that one entry of the top-k table covers
+    uint32_t vocab;
+};
+
+struct LogprobGradArgs {
+    HeadShards sh;
+    void *g[kMaxPeers];
+    int64_t g_stride[kMaxPeers];       // bytes
+    const int64_t *tokens;
+    const float *lse, *entropy, *g_logp, *g_entropy;
+    float scale, inv_t;
+    uint32_t W, rows, blocks, quads, vocab;
+    uint64_t groups;                   // quads of all rows, one workgroup's turn each
+};
+
+struct PolicyArgs {
+    const float *logp, *old_logp, *adv, *weight, *ref, *entropy;
+    float *stats, *g_logp, *g_entropy;
+    uint32_t *counter;
+    double *part;                      // [groups][4]
+    uint64_t n;
+    float lo, hi;                      // log(1 - clip_low), log(1 + clip_high)
+    float ratio_lo, ratio_hi;          // e^lo, e^hi
+    float kl_coef, entropy_coef, grad_scale, w_all;
+    uint32_t groups;
+};
+
+static_assert(sizeof(LogprobArgs) <= 4096 && sizeof(LogprobGradArgs) <= 4096, "kernel arguments stay below 4 KiB");
+
+struct LogprobPlan {
+    rog_head_plan_info info;
+    LogprobArgs args;
+    rog_dtype dtype;
+};
+struct LogprobGradPlan {
+    uint32_t grid;
+    LogprobGradArgs args;
+    rog_dtype dtype;
+};
+struct PolicyPlan {
+    PolicyArgs args;
+};
+
+// Tokens of one workgroup of the policy loss.
+constexpr uint32_t kPolicyGroup = 2048;
+
+// Validate and plan (no HIP calls).
+rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype, float temperature,
+                        const int64_t *tokens, int top_k, const rog_logprob_out *out, void *workspace,
+                        size_t workspace_bytes, rog_logprob_form form, bool check_workspace, LogprobPlan *p);
+rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard *grads, int W, size_t rows,
+                             rog_dtype dtype, float temperature, const int64_t *tokens, const float *lse,
+                             const float *entropy, const float *g_logp, const float *g_entropy,
+                             LogprobGradPlan *p);
+rog_status plan_policy(const rog_policy_in *in, size_t n, const rog_policy_params *params,
+                       const rog_policy_out *out, void *workspace, size_t workspace_bytes, PolicyPlan *p);
+
+}  // namespace rog

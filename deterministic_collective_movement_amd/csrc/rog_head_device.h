@@ -1,0 +1,201 @@
+// rog_head_device.h -- device helpers of the vocabulary-side kernels: elements
+// of a block of logits in a lane's registers, and the partial states of a
+// softmax.
+#pragma once
+
+#include "rog_device.h"
+#include "rog_head.h"
+
+namespace rog {
+
+// Every multiply-add below is written out: the same expression has to give the
+// same bits in every kernel that it is inlined into.
+#pragma clang fp contract(off)
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// 16 bytes in the global address space at any byte alignment.
+typedef const __attribute__((address_space(1))) uint8_t gbyte;
+typedef uint32_t vec16any __attribute__((ext_vector_type(4), aligned(1)));
+typedef const __attribute__((address_space(1))) vec16any gvec16any;
+typedef __attribute__((address_space(1))) vec16any gvec16any_out;
+
+constexpr float kInf = __builtin_inff();
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ float bits_f32(uint32_t u) { return __builtin_bit_cast(float, u); }
+__device__ __forceinline__ uint32_t f32_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
+
+// 2^x in one instruction (results below 2^-126 are flushed to zero).
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// The larger of two; NaN if one is NaN (v_maximum3_f32).
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// Logits of type DT (a rog_dtype) as the kernels hold them.
+template <int DT>
+struct Logit {
+    static constexpr uint32_t kSize = DT == ROG_DTYPE_F32 ? 4 : 2;
+    static constexpr uint32_t kPerVec = 16 / kSize;                         // columns per 16-byte vector
+    static constexpr uint32_t kVecs = kHeadBlock / 64 / kPerVec;            // vectors per lane of a block
+    static constexpr uint32_t kMinusInf = DT == ROG_DTYPE_F32 ? 0xFF800000u // one or two logits of -inf
+                                          : DT == ROG_DTYPE_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+};
+
+// Two 2-byte logits, or one binary32, of a 32-bit word.
+template <int DT>
+__device__ __forceinline__ void widen_word(uint32_t w, float *x) {
+    if constexpr (DT == ROG_DTYPE_BF16) {
+        x[0] = bits_f32(w << 16);
+        x[1] = bits_f32(w & 0xFFFF0000u);
+    } else if constexpr (DT == ROG_DTYPE_F16) {
+        const f16x2 h = __builtin_bit_cast(f16x2, w);
+        x[0] = float(h.x);
+        x[1] = float(h.y);
+    } else {
+        x[0] = bits_f32(w);
+    }
+}
+
+// Rounds once, nearest-even.
+template <int DT>
+__device__ __forceinline__ uint32_t narrow_word(const float *x) {
+    if constexpr (DT == ROG_DTYPE_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[0], x[1]}, bf16x2));
+    else if constexpr (DT == ROG_DTYPE_F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[0], x[1]}, f16x2));
+    else return f32_bits(x[0]);
+}
+
+template <int DT>
+__device__ __forceinline__ void widen_vec(const vec16 &v, float *x) {
+    constexpr int n = Logit<DT>::kPerVec / 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) widen_word<DT>(v[i], x + n * i);
+}
+
+// One logit at an element address.
+template <int DT>
+__device__ __forceinline__ float load_logit(gbyte *p) {
+    if constexpr (DT == ROG_DTYPE_F32) return *(const __attribute__((address_space(1))) float *)p;
+    else {
+        float x[2];
+        widen_word<DT>(*(const __attribute__((address_space(1))) uint16_t *)p, x);
+        return x[0];
+    }
+}
+
+// A block of one row: its first column's address, how many columns it has
+// (1..2048) and the number of its first column in the row.
+struct BlockAt {
+    gbyte *p;
+    uint32_t n;
+    uint32_t col;
+    uint32_t shard;
+    uint32_t off;       // the first column's number in the shard
+};
+
+// The shard that holds block b (b below the row's blocks, wave-uniform); `from`
+// is a shard at or before it.
+__device__ __forceinline__ uint32_t shard_of(const HeadShards &h, uint32_t from, uint32_t b) {
+    while (h.block0[from + 1] <= b) ++from;
+    return from;
+}
+
+template <int DT>
+__device__ __forceinline__ BlockAt block_at(const HeadShards &h, uint32_t from, uint32_t row, uint32_t b) {
+    const uint32_t r = shard_of(h, from, b);
+    const uint32_t off = (b - h.block0[r]) * kHeadBlock;
+    const uint32_t left = h.width[r] - off;
+    gbyte *p = (gbyte *)h.x[r] + int64_t(row) * h.stride[r] + uint64_t(off) * Logit<DT>::kSize;
+    return BlockAt{p, left < kHeadBlock ? left : kHeadBlock, h.col0[r] + off, r, off};
+}
+
+// A lane's vector i of a block: columns (64 i + lane) * kPerVec and on.  Columns
+// at n or beyond read as -inf, and nothing is loaded for them.
+template <int DT>
+__device__ __forceinline__ vec16 load_vec(gbyte *p, uint32_t n, uint32_t i, uint32_t lane) {
+    constexpr uint32_t per = Logit<DT>::kPerVec;
+    const uint32_t c = (64 * i + lane) * per;
+    if (c + per <= n) return *(gvec16any *)(p + c * Logit<DT>::kSize);
+    vec16 v = {Logit<DT>::kMinusInf, Logit<DT>::kMinusInf, Logit<DT>::kMinusInf, Logit<DT>::kMinusInf};
+    if (c < n) {
+#pragma unroll
+        for (uint32_t e = 0; e < per; ++e) {
+            if (c + e >= n) continue;
+            if constexpr (DT == ROG_DTYPE_F32) {
+                v[e] = *(const __attribute__((address_space(1))) uint32_t *)(p + (c + e) * 4);
+            } else {
+                const uint32_t h = *(const __attribute__((address_space(1))) uint16_t *)(p + (c + e) * 2);
+                v[e / 2] = e & 1 ? (v[e / 2] & 0xFFFFu) | h << 16 : (v[e / 2] & 0xFFFF0000u) | h;
+            }
+        }
+    }
+    return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[Logit<DT>::kVecs]) {
+    if (b.n == kHeadBlock) {
+#pragma unroll
+        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i)
+            v[i] = *(gvec16any *)(b.p + (64 * i + lane) * 16);
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = load_vec<DT>(b.p, b.n, i, lane);
+    }
+}
+
+// The partial state of a softmax over some logits: m their largest (NaN if one
+// is NaN), and with z = x * scale, |x| held within `bound`, and R = ref(m):
+//     s = sum 2^(z - R),   t = sum 2^(z - R) (z - R).
+// R is the rounded product m * scale, and z - R is one fused
+// multiply-add, so the rounding of R cancels between s and what is read
+// against it.  No logits: m = -inf, s = t = 0.
+struct State {
+    float m, s, t;
+};
+
+struct Scaling {
+    float scale, bound;
+    // The reference for a largest logit m: finite for every m but +inf and NaN.
+    __device__ __forceinline__ float ref(float m) const {
+        const float r = __builtin_amdgcn_fmed3f(m, -bound, bound) * scale;
+        return m < kInf ? r : __builtin_nanf("");
+    }
+};
+
+// The state of 32 logits x[] in a lane.  bound * scale is 2^30: up to there the
+// rounding of R stays below 64, so that no term overflows.  Logits of -inf and
+// beyond -bound count as -bound: nothing against any reference but their own,
+// and finite, so that 0 * (z - R) stays 0.  A row whose largest logit is at a
+// bound or beyond is read again (the kernels' extreme rows).
+__device__ __forceinline__ State state_of(const float (&x)[32], const Scaling &c) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) m = max_nan(m, x[i]);
+    const float r = c.ref(m);
+    float s[4] = {0, 0, 0, 0}, t[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float y = __builtin_fmaf(__builtin_amdgcn_fmed3f(x[i], -c.bound, c.bound), c.scale, -r);
+        const float e = exp2_fast(y);
+        s[i & 3] = s[i & 3] + e;
+        t[i & 3] = __builtin_fmaf(e, y, t[i & 3]);
+    }
+    return State{m, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3])};
+}
+
+// The state of both sides' logits.  A side without logits leaves the other's
+// bits as they are.
+__device__ __forceinline__ State join(const State &a, const State &b, const Scaling &c) {
+    const float ra = c.ref(a.m), rb = c.ref(b.m);
+    const float r = max_nan(ra, rb);
+    const float da = ra - r, db = rb - r;
+    const float wa = exp2_fast(da), wb = exp2_fast(db);
+    return State{max_nan(a.m, b.m), __builtin_fmaf(a.s, wa, b.s * wb),
+                 __builtin_fmaf(wa, __builtin_fmaf(a.s, da, a.t), wb * __builtin_fmaf(b.s, db, b.t))};
+}
+
+__device__ __forceinline__ State no_state() { return State{-kInf, 0.0f, 0.0f}; }
+
+}  // namespace rog

@@ -19,6 +19,15 @@ Entry points keep the C names.  Tensor forms:
   ``rank``'s share of a reduce-scatter, i.e. ``rog_reduce`` over shard
   ``rank`` of each input (views; nothing is copied).
 
+* ``rog_logprob(shards, tokens=None, top_k=0, temperature=1.0, out=None, ...)``
+  -> ``RogLogprob``: log probabilities of given tokens over W vocabulary shards,
+  with entropy, log-sum-exp and the best alternatives;
+* ``rog_logprob_grad(shards, tokens, lse, entropy, g_logp, g_entropy=None, ...)``
+  -> the W shards' gradients;
+* ``rog_policy_loss(logp, old_logp, advantage, weight=None, ...)`` ->
+  ``RogPolicyLoss``: the clipped policy loss with its gradient;
+* ``rog_logprob_plan(shards, top_k=0, form=...)`` -> dict (no GPU work).
+
 Raw-pointer forms (``*_ptrs``) take integer device addresses, for callers that
 manage their own memory.
 
@@ -34,7 +43,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import List, Optional, Sequence
+import threading
+from typing import List, NamedTuple, Optional, Sequence
 
 import torch  # loads the process's HIP runtime before librog.so binds to it
 
@@ -62,6 +72,13 @@ ROG_DTYPE_F32 = 0
 ROG_DTYPE_BF16 = 1
 ROG_DTYPE_F16 = 2
 
+ROG_LOGPROB_AUTO = 0
+ROG_LOGPROB_ROW = 1
+ROG_LOGPROB_SPLIT = 2
+ROG_LOGPROB_WAVE = 3
+
+LOGPROB_FORM_NAMES = {ROG_LOGPROB_AUTO: "none", ROG_LOGPROB_ROW: "row", ROG_LOGPROB_SPLIT: "split",
+                      ROG_LOGPROB_WAVE: "wave"}
 PATH_NAMES = {ROG_PATH_AUTO: "auto", ROG_PATH_SINGLE_WG: "single_wg", ROG_PATH_MULTI_WG: "multi_wg"}
 KERNEL_NAMES = {ROG_KERNEL_NONE: "none", ROG_KERNEL_FLAT: "flat", ROG_KERNEL_PEER: "peer",
                 ROG_KERNEL_REDUCE: "reduce"}
@@ -100,6 +117,36 @@ class rog_plan_info(ctypes.Structure):
                 ("peer_sh2", ctypes.c_uint32), ("flags", ctypes.c_uint32)]
 
 
+class rog_logit_shard(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("width", ctypes.c_int64)]
+
+
+class rog_grad_shard(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("row_stride", ctypes.c_int64)]
+
+
+class rog_logprob_out(ctypes.Structure):
+    _fields_ = [("logp", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("top_logp", ctypes.c_void_p), ("top_ids", ctypes.c_void_p)]
+
+
+class rog_head_plan_info(ctypes.Structure):
+    _fields_ = [("form", ctypes.c_int32), ("grid", ctypes.c_uint32), ("block", ctypes.c_uint32),
+                ("blocks", ctypes.c_uint32), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class rog_policy_in(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("logp", "old_logp", "advantage", "weight", "ref_logp", "entropy")]
+
+
+class rog_policy_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in ("clip_low", "clip_high", "kl_coef", "entropy_coef", "grad_scale")]
+
+
+class rog_policy_out(ctypes.Structure):
+    _fields_ = [("stats", ctypes.c_void_p), ("g_logp", ctypes.c_void_p), ("g_entropy", ctypes.c_void_p)]
+
+
 def _hip_runtimes_mapped() -> set:
     paths = set()
     with open("/proc/self/maps") as f:
@@ -130,6 +177,19 @@ def _load() -> ctypes.CDLL:
     lib.rog_reduce_ex.argtypes = [ptrs, i32, sz, i32, vp, vp, i32]
     lib.rog_reduce_plan.argtypes = [ptrs, i32, sz, i32, vp, i32, ctypes.POINTER(rog_plan_info)]
     lib.rog_reduce_many.argtypes = [ctypes.POINTER(rog_reduce_desc), i32, i32, i32, vp]
+    f32, ref = ctypes.c_float, ctypes.POINTER
+    lib.rog_logprob_ex.argtypes = [ref(rog_logit_shard), i32, sz, i32, f32, vp, i32, ref(rog_logprob_out), vp, sz, vp, i32]
+    lib.rog_logprob.argtypes = lib.rog_logprob_ex.argtypes[:-1]
+    lib.rog_logprob_plan.argtypes = [ref(rog_logit_shard), i32, sz, i32, i32, i32, ref(rog_head_plan_info)]
+    lib.rog_logprob_grad.argtypes = [ref(rog_logit_shard), ref(rog_grad_shard), i32, sz, i32, f32, vp, vp, vp, vp, vp, vp]
+    lib.rog_policy_loss.argtypes = [ref(rog_policy_in), sz, ref(rog_policy_params), ref(rog_policy_out), vp, sz, vp]
+    lib.rog_policy_loss_workspace_bytes.argtypes = [sz]
+    lib.rog_policy_loss_workspace_bytes.restype = sz
+    for name in ("rog_logprob", "rog_logprob_ex", "rog_logprob_plan", "rog_logprob_grad", "rog_policy_loss"):
+        getattr(lib, name).restype = i32
+    for name in ("rog_max_top_k", "rog_logprob_max_split_rows"):
+        getattr(lib, name).argtypes = []
+        getattr(lib, name).restype = i32
     for name in ("rog_gather", "rog_gather_ex", "rog_gather_many", "rog_plan", "rog_reduce", "rog_reduce_ex",
                  "rog_reduce_plan", "rog_reduce_many"):
         getattr(lib, name).restype = i32
@@ -192,6 +252,18 @@ def rog_max_batch_pointers() -> int:
 
 def rog_last_hip_error() -> int:
     return int(_lib.rog_last_hip_error())
+
+
+def rog_max_top_k() -> int:
+    return int(_lib.rog_max_top_k())
+
+
+def rog_logprob_max_split_rows() -> int:
+    return int(_lib.rog_logprob_max_split_rows())
+
+
+def rog_policy_loss_workspace_bytes(n: int) -> int:
+    return int(_lib.rog_policy_loss_workspace_bytes(n))
 
 
 def rog_status_string(status: int) -> str:
@@ -512,3 +584,245 @@ def rog_reduce_many(batch: Sequence[Sequence[torch.Tensor]],
         rog_reduce_many_ptrs([[s.data_ptr() for s in b] for b in batch], counts,
                              [o.data_ptr() for o in ready], W, dt0, _stream_handle(stream, device))
     return ready
+
+
+# ---------------------------------------------------------------------------
+# The vocabulary side of a policy: token log probabilities, their gradient, the
+# policy loss
+# ---------------------------------------------------------------------------
+
+class RogLogprob(NamedTuple):
+    """rog_logprob's results; as ``out``, the tensors to write (None: not wanted)."""
+    logp: Optional[torch.Tensor]        # [rows] float32
+    entropy: Optional[torch.Tensor]     # [rows] float32
+    lse: Optional[torch.Tensor]         # [rows] float32
+    top_logp: Optional[torch.Tensor]    # [rows, top_k] float32
+    top_ids: Optional[torch.Tensor]     # [rows, top_k] int64
+
+
+class RogPolicyLoss(NamedTuple):
+    """rog_policy_loss's results; as ``out``, the tensors to write."""
+    stats: torch.Tensor                 # [4] float32: loss, sum w kl, sum w entropy, sum w [clipped]
+    g_logp: Optional[torch.Tensor]      # [n] float32
+    g_entropy: Optional[torch.Tensor]   # [n] float32
+
+
+# One workspace per stream, so that calls on different streams never share one;
+# zero-filled when it is made, as the library asks, and left ready by every call.
+_workspaces: dict = {}
+_workspaces_lock = threading.Lock()
+
+
+def rog_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
+    """A zero-filled workspace of at least ``nbytes`` for calls on ``stream``
+    (default: the current one), for callers that keep their own."""
+    device = torch.device("cuda", _current_device()) if device is None else torch.device(device)
+    if stream is None:
+        return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=device)
+
+
+def _workspace(workspace, nbytes: int, device: torch.device, stream, handle: int):
+    """(address, bytes) of the caller's workspace or of the stream's own one."""
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", device)
+        return workspace.data_ptr(), _nbytes(workspace)
+    if nbytes == 0:
+        return None, 0
+    if torch.cuda.is_current_stream_capturing():
+        # a graph's replays may run beside eager calls on this stream: the graph gets its own, cleared in the graph
+        t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        return t.data_ptr(), nbytes
+    key = (device.index, handle)
+    t = _workspaces.get(key)
+    if t is None or t.numel() < nbytes:
+        with _workspaces_lock:
+            t = _workspaces.get(key)
+            if t is None or t.numel() < nbytes:
+                t = rog_workspace(max(nbytes, 1 << 20), device, stream)
+                _workspaces[key] = t
+    return t.data_ptr(), t.numel()
+
+
+def _check_vector(t, what: str, n: int, dtype: torch.dtype, device: torch.device) -> int:
+    """Address of a contiguous vector of n elements (0 for None)."""
+    if t is None:
+        return 0
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index and t.is_contiguous()):
+        _check_tensor(t, what, device)
+    if t.dtype != dtype or t.numel() != n:
+        raise ValueError("%s must hold %d elements of %s (has %d of %s)" % (what, n, dtype, t.numel(), t.dtype))
+    return t.data_ptr()
+
+
+def _check_matrix(t, what: str, rows: int, dtype: torch.dtype, device: torch.device) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what)
+    if not t.is_cuda:
+        raise ValueError("%s must be on a GPU (got %s)" % (what, t.device))
+    if t.get_device() != device.index:
+        raise ValueError("%s is on %s, expected %s" % (what, t.device, device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s (got %s)" % (what, dtype, t.dtype))
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError("%s must be a matrix of %d rows (got %s)" % (what, rows, tuple(t.shape)))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s must be contiguous within its rows (any row stride)" % what)
+
+
+def _shard_array(shards):
+    """(device, rows, dtype code, array of rog_logit_shard) of W logits matrices."""
+    if len(shards) == 0:
+        raise ValueError("need at least one shard of logits")
+    first = shards[0]
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("shards[0] must be a torch.Tensor")
+    device, dtype = first.device, first.dtype
+    if dtype not in DTYPES:
+        raise ValueError("logits are float32, bfloat16 or float16 (got %s)" % dtype)
+    if first.dim() != 2:
+        raise ValueError("shards[0] must be a matrix (got %s)" % (tuple(first.shape),))
+    rows = first.shape[0]
+    arr = (rog_logit_shard * len(shards))()
+    for i, x in enumerate(shards):
+        _check_matrix(x, "shards[%d]" % i, rows, dtype, device)
+        s = arr[i]
+        s.logits, s.row_stride, s.width = x.data_ptr(), x.stride(0), x.shape[1]
+    return device, rows, DTYPES[dtype], arr
+
+
+def rog_logprob_plan(shards: Sequence[torch.Tensor], top_k: int = 0, form: int = ROG_LOGPROB_AUTO) -> dict:
+    """The launch rog_logprob_ex would make for these logits (no GPU work)."""
+    _, rows, dt, arr = _shard_array(shards)
+    return _logprob_plan(arr, rows, dt, top_k, form)
+
+
+def _logprob_plan(arr, rows: int, dtype: int, top_k: int, form: int) -> dict:
+    info = rog_head_plan_info()
+    _check(_lib.rog_logprob_plan(arr, len(arr), rows, dtype, top_k, form, ctypes.byref(info)), "rog_logprob_plan")
+    return {"form": LOGPROB_FORM_NAMES[info.form], "grid": info.grid, "block": info.block, "blocks": info.blocks,
+            "workspace_bytes": info.workspace_bytes}
+
+
+def rog_logprob_plan_widths(widths: Sequence[int], rows: int, dtype: int, top_k: int = 0,
+                            form: int = ROG_LOGPROB_AUTO) -> dict:
+    """rog_logprob_plan from the shards' widths alone."""
+    arr = (rog_logit_shard * max(1, len(widths)))()
+    for s, w in zip(arr, widths):
+        s.width = w
+    return _logprob_plan(arr, rows, dtype, top_k, form)
+
+
+def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor] = None, top_k: int = 0,
+                   temperature: float = 1.0, out: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None,
+                   form: int = ROG_LOGPROB_AUTO) -> RogLogprob:
+    """rog_logprob with the launch form forced (never changes the bits)."""
+    device, rows, dt, arr = _shard_array(shards)
+    if not 0 <= top_k <= rog_max_top_k():
+        raise ValueError("top_k must be in [0, %d]" % rog_max_top_k())
+    if out is None:
+        new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=device)  # noqa: E731
+        out = RogLogprob(new(rows) if tokens is not None else None, new(rows), new(rows),
+                         new(rows, top_k) if top_k else None,
+                         new(rows, top_k, dtype=torch.int64) if top_k else None)
+    elif not isinstance(out, RogLogprob):
+        out = RogLogprob(*out)
+    o = rog_logprob_out()
+    o.logp = _check_vector(out.logp, "out.logp", rows, torch.float32, device)
+    o.entropy = _check_vector(out.entropy, "out.entropy", rows, torch.float32, device)
+    o.lse = _check_vector(out.lse, "out.lse", rows, torch.float32, device)
+    o.top_logp = _check_vector(out.top_logp, "out.top_logp", rows * top_k, torch.float32, device)
+    o.top_ids = _check_vector(out.top_ids, "out.top_ids", rows * top_k, torch.int64, device)
+    tok = _check_vector(tokens, "tokens", rows, torch.int64, device)
+    info = rog_head_plan_info()
+    _check(_lib.rog_logprob_plan(arr, len(arr), rows, dt, top_k, form, ctypes.byref(info)), "rog_logprob")
+    with _on_device(device):
+        handle = _stream_handle(stream, device)
+        ws, ws_bytes = _workspace(workspace, info.workspace_bytes, device, stream, handle)
+        _check(_lib.rog_logprob_ex(arr, len(arr), rows, dt, temperature, tok or None, top_k, ctypes.byref(o), ws,
+                                   ws_bytes, handle, form), "rog_logprob")
+    return out
+
+
+def rog_logprob(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor] = None, top_k: int = 0,
+                temperature: float = 1.0, out: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> RogLogprob:
+    """Log probability of ``tokens[i]`` (int64; negative: the row is not scored)
+    in row i of the logits whose columns are ``shards`` in rank order, with the
+    row's entropy and log-sum-exp and its ``top_k`` best alternatives.
+
+    ``shards``: W matrices [rows, width_r] of one dtype (float32, bfloat16 or
+    float16), contiguous within rows, any row stride.  ``out``: a RogLogprob (or
+    five tensors) to write, None for what is not wanted."""
+    return rog_logprob_ex(shards, tokens, top_k, temperature, out, workspace, stream)
+
+
+def rog_logprob_grad(shards: Sequence[torch.Tensor], tokens: torch.Tensor, lse: torch.Tensor, entropy: torch.Tensor,
+                     g_logp: torch.Tensor, g_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                     out: Optional[Sequence[torch.Tensor]] = None, stream=None) -> List[torch.Tensor]:
+    """Gradient of sum_i (g_logp[i] logp[i] + g_entropy[i] entropy[i]) in every
+    shard, from rog_logprob's ``lse`` and ``entropy``.  ``out``: W matrices to
+    write; ``out[r]`` may be ``shards[r]`` (in place)."""
+    device, rows, dt, arr = _shard_array(shards)
+    if out is None:
+        out = [torch.empty(rows, x.shape[1], dtype=x.dtype, device=device) for x in shards]
+    out = list(out)
+    if len(out) != len(arr):
+        raise ValueError("one gradient per shard")
+    grads = (rog_grad_shard * len(arr))()
+    for i, (g, x) in enumerate(zip(out, shards)):
+        _check_matrix(g, "out[%d]" % i, rows, x.dtype, device)
+        if g.shape[1] != x.shape[1]:
+            raise ValueError("out[%d] must have the shape of shards[%d]" % (i, i))
+        grads[i].grad, grads[i].row_stride = g.data_ptr(), g.stride(0)
+    f32 = torch.float32
+    if tokens is None or lse is None or entropy is None or g_logp is None:
+        raise ValueError("tokens, lse, entropy and g_logp are needed")
+    args = [_check_vector(tokens, "tokens", rows, torch.int64, device),
+            _check_vector(lse, "lse", rows, f32, device), _check_vector(entropy, "entropy", rows, f32, device),
+            _check_vector(g_logp, "g_logp", rows, f32, device),
+            _check_vector(g_entropy, "g_entropy", rows, f32, device) or None]
+    with _on_device(device):
+        _check(_lib.rog_logprob_grad(arr, grads, len(arr), rows, dt, temperature, *args,
+                                     _stream_handle(stream, device)), "rog_logprob_grad")
+    return out
+
+
+def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Tensor,
+                    weight: Optional[torch.Tensor] = None, ref_logp: Optional[torch.Tensor] = None,
+                    entropy: Optional[torch.Tensor] = None, clip_low: float = 0.2, clip_high: float = 0.2,
+                    kl_coef: float = 0.0, entropy_coef: float = 0.0, grad_scale: float = 1.0,
+                    out: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> RogPolicyLoss:
+    """The clipped policy loss over n tokens (float32 vectors) with its gradients
+    in ``logp`` and ``entropy``.  ``weight[i]`` is the token's weight in the sums
+    (0: the token counts for nothing; None: 1 / n each)."""
+    if not isinstance(logp, torch.Tensor):
+        raise TypeError("logp must be a torch.Tensor")
+    device, n, f32 = logp.device, logp.numel(), torch.float32
+    i, o = rog_policy_in(), rog_policy_out()
+    i.logp = _check_vector(logp, "logp", n, f32, device)
+    i.old_logp = _check_vector(old_logp, "old_logp", n, f32, device)
+    i.advantage = _check_vector(advantage, "advantage", n, f32, device)
+    i.weight = _check_vector(weight, "weight", n, f32, device)
+    i.ref_logp = _check_vector(ref_logp, "ref_logp", n, f32, device)
+    i.entropy = _check_vector(entropy, "entropy", n, f32, device)
+    if out is None:
+        out = RogPolicyLoss(torch.empty(4, dtype=f32, device=device), torch.empty(n, dtype=f32, device=device),
+                            torch.empty(n, dtype=f32, device=device) if entropy is not None else None)
+    elif not isinstance(out, RogPolicyLoss):
+        out = RogPolicyLoss(*out)
+    o.stats = _check_vector(out.stats, "out.stats", 4, f32, device)
+    o.g_logp = _check_vector(out.g_logp, "out.g_logp", n, f32, device)
+    o.g_entropy = _check_vector(out.g_entropy, "out.g_entropy", n, f32, device)
+    k = rog_policy_params(clip_low, clip_high, kl_coef, entropy_coef, grad_scale)
+    with _on_device(device):
+        handle = _stream_handle(stream, device)
+        ws, ws_bytes = _workspace(workspace, _lib.rog_policy_loss_workspace_bytes(n), device, stream, handle)
+        _check(_lib.rog_policy_loss(ctypes.byref(i), n, ctypes.byref(k), ctypes.byref(o), ws, ws_bytes, handle),
+               "rog_policy_loss")
+    return out

@@ -303,6 +303,192 @@ typedef struct {
 ROG_API rog_status rog_reduce_many(const rog_reduce_desc *descs, int n, int W, rog_dtype dtype,
                                    hipStream_t stream);
 
+/* ===========================================================================
+ * The vocabulary side of a policy: log probabilities of given tokens over W
+ * vocabulary shards in rank order, their gradient, and the policy loss.
+ *
+ * A policy head that is split over W ranks leaves W shards of logits, rank r
+ * holding `width` columns of every row.  On one GPU the W ranks are W
+ * caller-owned device buffers, as above.  A row is its shards' columns one
+ * after the other in rank order; V is the sum of the widths.
+ *
+ * Beside the common rules:
+ *  - A row's result depends, bit for bit, on its logits, the shards' widths and
+ *    the temperature alone: not on how many rows a call has, the row's place
+ *    among them, the launch form, alignment or strides.  A token scored alone
+ *    and in a batch gets the same bits.
+ *  - A workspace is device memory of the caller, aligned to 16 bytes.  It is
+ *    zero-filled by the caller once, before its first use; every call leaves
+ *    it ready for the next.  Calls that may run at the same time (on different
+ *    streams) each need their own.
+ *  - All sums and row statistics are held in binary32 or binary64.
+ * ======================================================================== */
+
+/* One vocabulary shard: row i's columns are logits[i * row_stride + 0 .. width). */
+typedef struct {
+    const void *logits;        /* device pointer, aligned to the element size     */
+    int64_t row_stride;        /* elements from a row to the next; >= 0           */
+    int64_t width;             /* columns; 0 is allowed                           */
+} rog_logit_shard;
+
+/* One shard's gradient: the width of the logits' shard, a row stride of its own. */
+typedef struct {
+    void *grad;                /* device pointer, aligned to the element size     */
+    int64_t row_stride;        /* elements; >= width where there are rows         */
+} rog_grad_shard;
+
+/* What rog_logprob writes; any of them may be NULL (not wanted). */
+typedef struct {
+    float *logp;               /* [rows]        log probability of the row's token */
+    float *entropy;            /* [rows]        in nats                            */
+    float *lse;                /* [rows]        log-sum-exp of the scaled logits   */
+    float *top_logp;           /* [rows][top_k] log probabilities, best first      */
+    int64_t *top_ids;          /* [rows][top_k] their columns in the whole row     */
+} rog_logprob_out;
+
+typedef enum {
+    ROG_LOGPROB_AUTO = 0,
+    ROG_LOGPROB_ROW = 1,       /* one workgroup per row                           */
+    ROG_LOGPROB_SPLIT = 2,     /* one workgroup per 8192 columns of a row, the last
+                                  of a row to finish joins its parts              */
+    ROG_LOGPROB_WAVE = 3       /* one wave per row (rows of at most four blocks of
+                                  2048 columns)                                   */
+} rog_logprob_form;
+
+/* The launch a call would make. */
+typedef struct {
+    int32_t form;              /* resolved rog_logprob_form (AUTO: nothing to do)  */
+    uint32_t grid, block;      /* workgroups, threads per workgroup               */
+    uint32_t blocks;           /* blocks of at most 2048 columns per row          */
+    uint64_t workspace_bytes;  /* workspace that the call needs (0: none)         */
+} rog_head_plan_info;
+
+/*
+ * rog_logprob -- per row, with z_j = x_j / temperature over its V columns:
+ *
+ *     lse = log sum_j e^{z_j},  logp = z_token - lse,
+ *     entropy = -sum_j p_j log p_j  (p_j = e^{z_j - lse}),
+ *     the top_k largest x_j, ties to the lowest column, as (column, z_j - lse).
+ *
+ * tokens   device array of `rows` columns, or NULL (then out->logp must be NULL
+ *          and every row is scored).  A row whose token is negative is not
+ *          scored and not read: 0 in logp, entropy, lse and top_logp, -1 in
+ *          top_ids.  A token of V or more: the row's logp is NaN.
+ * top_k    0 .. rog_max_top_k().
+ *
+ * Logits of -inf have probability 0 and are never alternatives: where a row has
+ * fewer than top_k others, the rest is column -1, log probability -inf.  A row
+ * that its mask leaves nothing (only -inf, or V = 0): lse = logp = -inf,
+ * entropy 0.  A NaN or +inf anywhere in a row makes every number of it NaN and
+ * its alternatives' columns -1.  Rows masked with the type's lowest finite
+ * value keep their meaning (lse is held within the finite range).
+ *
+ * Errors (nothing enqueued):
+ *   ROG_ERR_INVALID_ARGUMENT  shards or out NULL; W out of range; dtype, form or
+ *                             top_k out of range; temperature outside
+ *                             [2^-10, 2^10]; a negative stride or width; a
+ *                             needed pointer NULL or misaligned; logp without
+ *                             tokens; a WAVE form for longer rows; a workspace
+ *                             that is NULL, misaligned or too small.
+ *   ROG_ERR_OVERLAP           an output overlaps a shard, the tokens, the
+ *                             workspace or another output.
+ *   ROG_ERR_TOO_LARGE         rows or V of 2^31 or more, or address overflow.
+ *   ROG_ERR_LAUNCH            hipLaunchKernel failed (rog_last_hip_error()).
+ * rows == 0: ROG_OK, nothing enqueued.
+ */
+ROG_API rog_status rog_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype,
+                               float temperature, const int64_t *tokens, int top_k,
+                               const rog_logprob_out *out, void *workspace, size_t workspace_bytes,
+                               hipStream_t stream);
+
+/* rog_logprob with the launch form forced (never changes the bits).  SPLIT takes
+ * at most rog_logprob_max_split_rows() rows. */
+ROG_API rog_status rog_logprob_ex(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype,
+                                  float temperature, const int64_t *tokens, int top_k,
+                                  const rog_logprob_out *out, void *workspace, size_t workspace_bytes,
+                                  hipStream_t stream, rog_logprob_form form);
+
+/* The launch form and the workspace that rog_logprob_ex would take for rows of
+ * these widths (only the shards' widths are read; no HIP call). */
+ROG_API rog_status rog_logprob_plan(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype,
+                                    int top_k, rog_logprob_form form, rog_head_plan_info *info);
+
+/*
+ * rog_logprob_grad -- the gradient of sum_i (g_logp_i logp_i + g_entropy_i
+ * entropy_i) in every logit, from what rog_logprob wrote:
+ *
+ *     dx_j = (g_logp (1[j = token] - p_j) - g_entropy p_j (log p_j + entropy)) / temperature
+ *
+ * rounded once to the logits' type.  lse and entropy are rog_logprob's of the
+ * same logits, widths and temperature.  g_entropy may be NULL (0).  A row that
+ * is not scored or that its mask leaves nothing gets zeros; a token of V or
+ * more, or a NaN in lse, NaN.
+ *
+ * grads    W gradients.  A gradient may be exactly its logits' shard (same
+ *          address and stride: in place); any other overlap is an error.
+ *          Bytes between the rows of a gradient are not written.
+ * Errors as rog_logprob; a row stride below the width is INVALID_ARGUMENT.
+ */
+ROG_API rog_status rog_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard *grads, int W, size_t rows,
+                                    rog_dtype dtype, float temperature, const int64_t *tokens, const float *lse,
+                                    const float *entropy, const float *g_logp, const float *g_entropy,
+                                    hipStream_t stream);
+
+/* Inputs of the policy loss: device arrays of n binary32 values. */
+typedef struct {
+    const float *logp;         /* log probability now                              */
+    const float *old_logp;     /* when the token was sampled                       */
+    const float *advantage;
+    const float *weight;       /* weight in the sums; 0: the token counts for nothing,
+                                  whatever its other values.  NULL: 1 / n each     */
+    const float *ref_logp;     /* under the reference policy; NULL: no KL term     */
+    const float *entropy;      /* NULL: no entropy term                            */
+} rog_policy_in;
+
+typedef struct {
+    float clip_low;            /* 0 <= clip_low <= 1                               */
+    float clip_high;           /* >= 0; infinity: not clipped above                */
+    float kl_coef;             /* finite                                           */
+    float entropy_coef;        /* finite                                           */
+    float grad_scale;          /* finite; factor of both gradients (not of stats)  */
+} rog_policy_params;
+
+typedef struct {
+    float *stats;              /* [4]: loss, sum w kl, sum w entropy, sum w [clipped] */
+    float *g_logp;             /* [n] or NULL                                      */
+    float *g_entropy;          /* [n] or NULL (NULL where entropy is NULL)         */
+} rog_policy_out;
+
+/*
+ * rog_policy_loss -- the clipped policy loss over n tokens and its gradient:
+ *
+ *     d = logp - old_logp, q = ref_logp - logp        (binary32 differences)
+ *     clipped = advantage > 0 ? d > hi : advantage < 0 && d < lo
+ *     l = -advantage e^{clipped ? the bound passed : d}
+ *         + kl_coef (e^q - 1 - q) - entropy_coef entropy
+ *     loss = sum_i weight_i l_i
+ *     g_logp_i = grad_scale weight_i (-advantage e^d [not clipped] - kl_coef (e^q - 1))
+ *     g_entropy_i = -grad_scale weight_i entropy_coef
+ *
+ * with lo = log(1 - clip_low) and hi = log(1 + clip_high) in binary32.  Weights
+ * carry the ragged batch: 1 / tokens for a mean over tokens, 1 / (sequences *
+ * length) for a mean over sequences, 0 for prompt and padding.  The sums are
+ * taken in binary64 in an order that depends on n alone, and rounded once.
+ *
+ * An output array may be exactly one of the input arrays; any other overlap is
+ * ROG_ERR_OVERLAP.  n == 0: stats are zero.  n of 2^34 or more: TOO_LARGE.
+ */
+ROG_API rog_status rog_policy_loss(const rog_policy_in *in, size_t n, const rog_policy_params *params,
+                                   const rog_policy_out *out, void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/* Workspace bytes of rog_policy_loss over n tokens (0: none is needed). */
+ROG_API size_t rog_policy_loss_workspace_bytes(size_t n);
+
+/* Limits; constants of the build. */
+ROG_API int rog_max_top_k(void);
+ROG_API int rog_logprob_max_split_rows(void);
+
 /* Largest W accepted: 64, the capacity of the kernel arguments, which carry
  * every source pointer.  The pages' collectives run over a same-host group of
  * at most eight ranks (RL-Align/RL-Kernel PR #491, "Security Architecture

@@ -1,0 +1,167 @@
+"""The policy loss on the GPU against a plain 64-bit form: lengths around a
+workgroup's share, masked tokens, clip limits, alignments, streams, graphs."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from deterministic_collective_movement_amd import rog
+from tests import head_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def make(n, seed):
+    r = np.random.RandomState(seed)
+    logp = -r.exponential(1.0, n).astype(np.float32)
+    old = (logp + 0.3 * r.randn(n)).astype(np.float32)
+    adv = r.randn(n).astype(np.float32)
+    adv[::17] = 0
+    w = (r.rand(n) < 0.7).astype(np.float32) / np.float32(max(1, n))
+    return logp, old, adv, w, (logp + 0.4 * r.randn(n)).astype(np.float32), r.exponential(1.0, n).astype(np.float32)
+
+
+def check(arrays, gpu, clip_low=0.2, clip_high=0.3, kl_coef=0.1, ent_coef=0.02, scale=1.0, weighted=True, kl=True, ent=True):
+    logp, old, adv, w, rf, h = arrays
+    dev = [torch.from_numpy(a).to(gpu) for a in arrays]
+    got = rog.rog_policy_loss(dev[0], dev[1], dev[2], weight=dev[3] if weighted else None, ref_logp=dev[4] if kl else None,
+                              entropy=dev[5] if ent else None, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
+                              entropy_coef=ent_coef, grad_scale=scale)
+    f = lambda v: float(np.float32(v))  # noqa: E731
+    # the bounds and coefficients as the C interface takes them, in binary32
+    lo = f(math.log1p(-f(clip_low))) if clip_low < 1 else -math.inf
+    hi = f(math.log1p(f(clip_high))) if math.isfinite(clip_high) else math.inf
+    want, tol = ref.policy64(logp, old, adv, w if weighted else None, rf if kl else None, h if ent else None, lo, hi,
+                             f(kl_coef), f(ent_coef) if ent else 0.0, f(scale))
+    for name, a, b, t in zip(got._fields, got, want, tol):
+        if a is None:
+            continue
+        a = a.cpu().numpy().astype(np.float64)
+        ok = (a == b) | (np.isnan(a) & np.isnan(b)) | (np.abs(a - b) <= t)
+        assert ok.all(), (name, a[~ok][:4], b[~ok][:4], t[~ok][:4])
+    return got
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 63, 1023, 2047, 2048, 2049, 4099, 100003, 600001])
+def test_lengths(gpu, n):
+    for kw in ({}, {"kl": False, "ent": False}, {"weighted": False, "scale": -3.0}, {"ent": False, "kl_coef": -0.5}):
+        check(make(n, n), gpu, **kw)
+
+
+def test_zero_tokens(gpu):
+    got = check(tuple(a[:0] for a in make(1, 0)), gpu)
+    assert got.stats.tolist() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("clip_low,clip_high", [(0.0, 0.0), (1.0, math.inf), (0.2, 10.0)])
+def test_clip_limits(gpu, clip_low, clip_high):
+    check(make(5000, 3), gpu, clip_low=clip_low, clip_high=clip_high)
+
+
+def test_masked_tokens_count_for_nothing(gpu):
+    arrays = make(10001, 4)
+    off = arrays[3] == 0
+    for a in (arrays[0], arrays[1], arrays[2], arrays[4], arrays[5]):
+        a[off] = np.resize(np.array([np.nan, np.inf, -np.inf, 3e38], np.float32), off.sum())
+    logp, old, adv, w, rf, h = arrays
+    dev = [torch.from_numpy(a).to(gpu) for a in arrays]
+    got = rog.rog_policy_loss(dev[0], dev[1], dev[2], weight=dev[3], ref_logp=dev[4], entropy=dev[5], kl_coef=0.1, entropy_coef=0.02)
+    clean = [np.where(off, np.float32(0), a) for a in arrays]
+    dev = [torch.from_numpy(a).to(gpu) for a in clean]
+    want = rog.rog_policy_loss(dev[0], dev[1], dev[2], weight=dev[3], ref_logp=dev[4], entropy=dev[5], kl_coef=0.1, entropy_coef=0.02)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool((got.g_logp[torch.from_numpy(off).to(gpu)] == 0).all())
+    none = rog.rog_policy_loss(dev[0], dev[1], dev[2], weight=torch.zeros(10001, device=gpu))
+    assert none.stats.tolist() == [0, 0, 0, 0] and bool((none.g_logp == 0).all())
+
+
+def test_alignment_place_and_repeats(gpu):
+    arrays = make(70001, 6)
+    want = check(arrays, gpu)
+    for shift in range(1, 4):
+        dev = []
+        for i, a in enumerate(arrays):
+            buf = torch.empty(len(a) + 16, device=gpu)
+            dev.append(buf[(shift + i) % 5:(shift + i) % 5 + len(a)])
+            dev[-1].copy_(torch.from_numpy(a))
+        pad = [torch.full((len(arrays[0]) + 16,), 5.5, device=gpu) for _ in range(2)]
+        out = (torch.empty(4, device=gpu), pad[0][shift:shift + 70001], pad[1][5:5 + 70001])
+        got = rog.rog_policy_loss(dev[0], dev[1], dev[2], weight=dev[3], ref_logp=dev[4], entropy=dev[5], clip_low=0.2,
+                                  clip_high=0.3, kl_coef=0.1, entropy_coef=0.02, out=out)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert bool((pad[0][:shift] == 5.5).all()) and bool((pad[0][shift + 70001:] == 5.5).all())
+        # in place: gradients over the inputs they belong to
+        got = rog.rog_policy_loss(dev[0], dev[1], dev[2], weight=dev[3], ref_logp=dev[4], entropy=dev[5], clip_low=0.2,
+                                  clip_high=0.3, kl_coef=0.1, entropy_coef=0.02, out=(out[0], dev[0], dev[5]))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_gradient_against_differences(gpu):
+    """Central differences of the kernel's own loss, one token at a time, away from the clip bounds."""
+    logp, old, adv, w, rf, h = make(40, 8)
+    d = logp - old
+    w[:] = 1.0
+    near = (np.abs(d - math.log(1.3)) < 0.03) | (np.abs(d - math.log(0.8)) < 0.03)
+    step = np.float32(2.0 ** -7)
+    dev = lambda a: torch.from_numpy(a).to(gpu)  # noqa: E731
+    kw = dict(weight=dev(w), ref_logp=dev(rf), clip_low=0.2, clip_high=0.3, kl_coef=0.1, entropy_coef=0.02)
+    got = rog.rog_policy_loss(dev(logp), dev(old), dev(adv), entropy=dev(h), **kw)
+    for i in range(40):
+        if near[i]:
+            continue
+        v = []
+        for s in (step, -step):
+            x = logp.copy()
+            x[i] += s
+            v.append(float(rog.rog_policy_loss(dev(x), dev(old), dev(adv), entropy=dev(h), **kw).stats[0]))
+        diff = (v[0] - v[1]) / (2 * float(step))
+        r = math.exp(d[i])
+        # truncation h^2 / 6 of the third derivative, and the stats' binary32 rounding over 2 h
+        tol = float(step) ** 2 / 6 * 2 * (abs(adv[i]) * r + 0.1 * math.exp(rf[i] - logp[i])) + 4 * ref.U * 60 / float(step)
+        assert abs(float(got.g_logp[i]) - diff) <= tol, i
+    assert torch.allclose(got.g_entropy, torch.full((40,), -0.02, device=gpu), rtol=1e-6)
+
+
+def test_streams_and_graph(gpu):
+    arrays = [torch.from_numpy(a).to(gpu) for a in make(50001, 9)]
+    call = lambda **k: rog.rog_policy_loss(arrays[0], arrays[1], arrays[2], weight=arrays[3], ref_logp=arrays[4],  # noqa: E731
+                                           entropy=arrays[5], kl_coef=0.1, entropy_coef=0.02, **k)
+    want = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for i in range(24):
+        with torch.cuda.stream(streams[i % 3]):
+            outs.append(call())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        r = call()
+    for k in range(3):
+        arrays[2].mul_(-1.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(r, call())), k
+
+
+def test_refusals(gpu):
+    a = [torch.zeros(8, device=gpu) for _ in range(3)]
+    z = torch.zeros(8, device=gpu)
+    bad = [lambda: rog.rog_policy_loss(a[0], a[1], a[2][:7]), lambda: rog.rog_policy_loss(a[0], a[1].double(), a[2]),
+           lambda: rog.rog_policy_loss(a[0], a[1], None), lambda: rog.rog_policy_loss(a[0].cpu(), a[1], a[2]),
+           lambda: rog.rog_policy_loss(*a, clip_low=1.5), lambda: rog.rog_policy_loss(*a, clip_low=-0.1),
+           lambda: rog.rog_policy_loss(*a, clip_high=math.nan), lambda: rog.rog_policy_loss(*a, kl_coef=math.inf),
+           lambda: rog.rog_policy_loss(*a, out=(z[:3], None, None)),
+           lambda: rog.rog_policy_loss(*a, out=(z[:4], z, None)),
+           lambda: rog.rog_policy_loss(*a, out=(torch.zeros(4, device=gpu), None, z)),
+           lambda: rog.rog_policy_loss(*a, out=(a[0][:4], None, None)),
+           lambda: rog.rog_policy_loss(a[0][::2], a[1][:4], a[2][:4])]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, TypeError)):
+            f()
+            pytest.fail("case %d was accepted" % i)
