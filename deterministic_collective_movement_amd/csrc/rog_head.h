@@ -14,20 +14,31 @@ namespace rog {
 
 // How a row of logits is cut.  The unit is a block: 2048 consecutive columns
 // of one shard (a shard's last block may be shorter), 32 columns per lane of
-// one wave.  Blocks are numbered through the shards in rank order; four
-// consecutive blocks make a quad, and quad q belongs to column q mod 4 of the
-// row.  The partial states are joined in one order, whatever the launch form:
-// the blocks of a quad as (0+1)+(2+3), the quads of a column one after the
-// other, the columns as (0+1)+(2+3), the lanes last.  So a row's bits depend
-// on its values, its shards' widths and the temperature alone, not on how
-// many rows a call has or which workgroups computed them.
+// one wave.  Blocks are numbered through the shards in rank order; block b
+// belongs to column b mod 4 of the row, and sixteen consecutive blocks make a
+// chunk.  The partial states are joined in one order, whatever the launch
+// form: the four blocks of a column within a chunk one after the other, a
+// column's chunks one after the other, the columns as (0+1)+(2+3), the lanes
+// last.  So a row's bits depend on its values, its shards' widths and the
+// temperature alone, not on how many rows a call has or which workgroups
+// computed them.
 constexpr uint32_t kHeadBlock = 2048;      // columns of a block
-constexpr uint32_t kHeadQuad = 4;          // blocks of a quad, quads in flight per row (columns)
-constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per column (or per block of a quad)
+constexpr uint32_t kHeadColumns = 4;
+constexpr uint32_t kHeadChunk = 16;        // blocks of a chunk
+constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per column
 // Workgroups of a launch, at most: a dispatch counts work-items in 32 bits.
 // The kernels loop over the rest.
 constexpr uint32_t kHeadGridCap = 0xFFFFFFFFu / kHeadThreads;
 constexpr int kMaxTopK = 32;
+constexpr uint32_t kTopSlots = 8;          // entries per lane and column in the top-k table
+
+// Tunables, measured on MI355X; a variant build may override one with -D.
+#ifndef ROG_SPLIT_MAX_GROUPS
+#define ROG_SPLIT_MAX_GROUPS 4096
+#endif
+#ifndef ROG_WAVE_MIN_ROWS
+#define ROG_WAVE_MIN_ROWS 512
+#endif
 constexpr uint32_t kMaxVocab = 1u << 31;   // columns of a row: below this
 
 // The front of a workspace: one arrival counter per row of a split launch (the
@@ -49,11 +60,12 @@ struct LogprobArgs {
     float *logp, *entropy, *lse, *top_logp;
     int64_t *top_ids;
     uint32_t *counters;                // split: one per row
-    float *part;                       // split: partial states
+    float *part;                       // split: partial states, [row][block][m, s, t][lane]
     float scale;                       // log2(e) / temperature
     float inv_t;                       // 1 / temperature
     float bound;                       // |x| beyond this leaves the scaled range
-    uint32_t W, rows, blocks, quads;
+    uint32_t W, rows, blocks;
+    uint32_t splits;                   // split: workgroups per row, four blocks each
     uint32_t top_k;
     uint32_t slot_shift;               // log2 of the blocks that one entry of the top-k table covers
     uint32_t vocab;
@@ -66,8 +78,9 @@ struct LogprobGradArgs {
     const int64_t *tokens;
     const float *lse, *entropy, *g_logp, *g_entropy;
     float scale, inv_t;
-    uint32_t W, rows, blocks, quads, vocab;
-    uint64_t groups;                   // quads of all rows, one workgroup's turn each
+    uint32_t W, rows, blocks, vocab;
+    uint32_t splits;                   // workgroup turns per row, four blocks each
+    uint64_t groups;                   // turns of all rows
 };
 
 struct PolicyArgs {

@@ -110,38 +110,75 @@ __device__ __forceinline__ BlockAt block_at(const HeadShards &h, uint32_t from, 
     return BlockAt{p, left < kHeadBlock ? left : kHeadBlock, h.col0[r] + off, r, off};
 }
 
-// A lane's vector i of a block: columns (64 i + lane) * kPerVec and on.  Columns
-// at n or beyond read as -inf, and nothing is loaded for them.
+// A lane's vector i of a block is columns (64 i + lane) * kPerVec and on.  Where
+// that runs past the block's end at n, the vector is read from the last place
+// where it fits, n - kPerVec: its first elements are then another lane's
+// columns (another's whole vector, where nothing of this one is left).  So a
+// tail takes the same loads as a full block, no byte past the row is read, and
+// element e belongs to the lane iff place + e >= its own first column.  A block
+// of fewer columns than one vector is read element by element.
 template <int DT>
-__device__ __forceinline__ vec16 load_vec(gbyte *p, uint32_t n, uint32_t i, uint32_t lane) {
-    constexpr uint32_t per = Logit<DT>::kPerVec;
-    const uint32_t c = (64 * i + lane) * per;
-    if (c + per <= n) return *(gvec16any *)(p + c * Logit<DT>::kSize);
+__device__ __forceinline__ uint32_t own_column(uint32_t i, uint32_t lane) { return (64 * i + lane) * Logit<DT>::kPerVec; }
+
+template <int DT>
+__device__ __forceinline__ uint32_t vec_place(uint32_t n, uint32_t i, uint32_t lane) {
+    const uint32_t c = own_column<DT>(i, lane), last = n - Logit<DT>::kPerVec;
+    return c < last ? c : last;
+}
+
+// The n < kPerVec columns of a tiny block, as every lane's vector (-inf behind them).
+template <int DT>
+__device__ __forceinline__ vec16 load_tiny(gbyte *p, uint32_t n) {
     vec16 v = {Logit<DT>::kMinusInf, Logit<DT>::kMinusInf, Logit<DT>::kMinusInf, Logit<DT>::kMinusInf};
-    if (c < n) {
 #pragma unroll
-        for (uint32_t e = 0; e < per; ++e) {
-            if (c + e >= n) continue;
-            if constexpr (DT == ROG_DTYPE_F32) {
-                v[e] = *(const __attribute__((address_space(1))) uint32_t *)(p + (c + e) * 4);
-            } else {
-                const uint32_t h = *(const __attribute__((address_space(1))) uint16_t *)(p + (c + e) * 2);
-                v[e / 2] = e & 1 ? (v[e / 2] & 0xFFFFu) | h << 16 : (v[e / 2] & 0xFFFF0000u) | h;
-            }
+    for (uint32_t e = 0; e + 1 < Logit<DT>::kPerVec; ++e) {
+        if (e >= n) continue;
+        if constexpr (DT == ROG_DTYPE_F32) {
+            v[e] = *(const __attribute__((address_space(1))) uint32_t *)(p + e * 4);
+        } else {
+            const uint32_t h = *(const __attribute__((address_space(1))) uint16_t *)(p + e * 2);
+            v[e / 2] = e & 1 ? (v[e / 2] & 0xFFFFu) | h << 16 : (v[e / 2] & 0xFFFF0000u) | h;
         }
     }
     return v;
 }
 
 template <int DT>
+__device__ __forceinline__ vec16 load_vec(gbyte *p, uint32_t n, uint32_t i, uint32_t lane) {
+    if (n < Logit<DT>::kPerVec) return load_tiny<DT>(p, n);
+    return *(gvec16any *)(p + vec_place<DT>(n, i, lane) * Logit<DT>::kSize);
+}
+
+template <int DT>
 __device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[Logit<DT>::kVecs]) {
-    if (b.n == kHeadBlock) {
+    if (b.n < Logit<DT>::kPerVec) {
+        const vec16 t = load_tiny<DT>(b.p, b.n);
 #pragma unroll
-        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i)
-            v[i] = *(gvec16any *)(b.p + (64 * i + lane) * 16);
+        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = t;
     } else {
 #pragma unroll
-        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = load_vec<DT>(b.p, b.n, i, lane);
+        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i)
+            v[i] = *(gvec16any *)(b.p + vec_place<DT>(b.n, i, lane) * Logit<DT>::kSize);
+    }
+}
+
+// Whether element e of the lane's vector i, read as above, is the lane's own.
+template <int DT>
+__device__ __forceinline__ bool owns(uint32_t n, uint32_t i, uint32_t lane, uint32_t e) {
+    const uint32_t c = own_column<DT>(i, lane);
+    if (n < Logit<DT>::kPerVec) return c + e < n;
+    return vec_place<DT>(n, i, lane) + e >= c;
+}
+
+// The elements of a block, -inf in the place of those that are not the lane's own.
+template <int DT>
+__device__ __forceinline__ void widen_block(const vec16 (&v)[Logit<DT>::kVecs], uint32_t n, uint32_t lane, float (&x)[32]) {
+    constexpr uint32_t per = Logit<DT>::kPerVec;
+#pragma unroll
+    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) widen_vec<DT>(v[i], x + i * per);
+    if (n < kHeadBlock) {
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i) x[i] = owns<DT>(n, i / per, lane, i % per) ? x[i] : -kInf;
     }
 }
 
@@ -159,8 +196,10 @@ struct Scaling {
     float scale, bound;
     // The reference for a largest logit m: finite for every m but +inf and NaN.
     __device__ __forceinline__ float ref(float m) const {
-        const float r = __builtin_amdgcn_fmed3f(m, -bound, bound) * scale;
-        return m < kInf ? r : __builtin_nanf("");
+        float r = __builtin_amdgcn_fmed3f(m, -bound, bound) * scale;
+        r = m < kInf ? r : __builtin_nanf("");
+        asm("" : "+v"(r));      // one select here, not one behind every use
+        return r;
     }
 };
 
@@ -197,5 +236,68 @@ __device__ __forceinline__ State join(const State &a, const State &b, const Scal
 }
 
 __device__ __forceinline__ State no_state() { return State{-kInf, 0.0f, 0.0f}; }
+
+// Reductions over the 64 lanes of a wave, all active: within rows of 16 lanes
+// by DPP exchanges (no shared memory), then over the four rows by lane reads.
+// The result is uniform.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return bits_f32(uint32_t(__builtin_amdgcn_update_dpp(0, int(f32_bits(x)), CTRL, 0xf, 0xf, false)));
+}
+__device__ __forceinline__ float lane_read(float x, int lane) {
+    return bits_f32(uint32_t(__builtin_amdgcn_readlane(int(f32_bits(x)), lane)));
+}
+template <typename F>
+__device__ __forceinline__ float reduce_lanes(float x, F f) {
+    x = f(x, dpp<0xB1>(x));      // quad_perm 1,0,3,2
+    x = f(x, dpp<0x4E>(x));      // quad_perm 2,3,0,1
+    x = f(x, dpp<0x141>(x));     // row_half_mirror
+    x = f(x, dpp<0x140>(x));     // row_mirror
+    return f(f(lane_read(x, 0), lane_read(x, 16)), f(lane_read(x, 32), lane_read(x, 48)));
+}
+
+// Joins the 64 lanes' states: their largest logit first, then two sums.
+__device__ __forceinline__ State join_lanes(const State &st, const Scaling &c) {
+    const float m = reduce_lanes(st.m, [](float a, float b) { return max_nan(a, b); });
+    const float d = c.ref(st.m) - c.ref(m);
+    const float w = exp2_fast(d);
+    const auto add = [](float a, float b) { return a + b; };
+    return State{m, reduce_lanes(st.s * w, add), reduce_lanes(w * __builtin_fmaf(st.s, d, st.t), add)};
+}
+
+// Values handed from workgroup to workgroup of one launch: stores and loads at
+// device scope, which go past the caches of the eight dies, so that no cache
+// has to be written back or emptied around them.
+__device__ __forceinline__ void publish(float *p, float v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish(double *p, double v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float collect(const float *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double collect(const double *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Called by every thread of a workgroup after its publish() stores: whether
+// this is the last of `groups` workgroups to get here, by a counter that is
+// zero before and after.  Each wave waits until its stores have reached
+// device scope before the barrier that the counting thread passes; the last
+// workgroup's collect() loads come after the counter's answer.
+__device__ __forceinline__ bool last_to_arrive(uint32_t *counter, uint32_t groups, uint32_t &flag) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        flag = before == groups - 1;
+        if (before == groups - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool last = flag != 0;
+    asm volatile("" ::: "memory");
+    return last;
+}
 
 }  // namespace rog

@@ -81,16 +81,31 @@ rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dty
     return rows >= kMaxVocab ? ROG_ERR_TOO_LARGE : ROG_OK;
 }
 
+// Bytes of partial states per row of a split launch: three per lane and block.
+uint64_t part_bytes(uint32_t blocks) { return uint64_t(blocks) * 3 * 64 * sizeof(float); }
+
+inline uint32_t splits_of(uint32_t blocks) { return uint32_t(ceil_div(blocks, kHeadColumns)); }
+
 // Launch form, grid and workspace of rog_logprob.
 rog_status choose_form(uint32_t blocks, size_t rows, int top_k, rog_logprob_form form, rog_head_plan_info *info) {
     if (form < ROG_LOGPROB_AUTO || form > ROG_LOGPROB_WAVE || top_k < 0 || top_k > kMaxTopK)
         return ROG_ERR_INVALID_ARGUMENT;
-    if (form == ROG_LOGPROB_SPLIT || form == ROG_LOGPROB_WAVE) return ROG_ERR_INVALID_ARGUMENT;   // not built
-    info->form = rows ? ROG_LOGPROB_ROW : ROG_LOGPROB_AUTO;
+    const bool may_split = rows <= kHeadCounters && blocks > kHeadColumns;
+    const bool may_wave = blocks <= kHeadColumns;
+    if ((form == ROG_LOGPROB_SPLIT && !may_split) || (form == ROG_LOGPROB_WAVE && !may_wave))
+        return ROG_ERR_INVALID_ARGUMENT;
+    if (form == ROG_LOGPROB_AUTO)
+        form = may_split && rows * splits_of(blocks) <= ROG_SPLIT_MAX_GROUPS ? ROG_LOGPROB_SPLIT
+               : may_wave && rows >= ROG_WAVE_MIN_ROWS                        ? ROG_LOGPROB_WAVE
+                                                                              : ROG_LOGPROB_ROW;
+    const uint64_t groups = form == ROG_LOGPROB_SPLIT  ? rows * uint64_t(splits_of(blocks))
+                            : form == ROG_LOGPROB_WAVE ? ceil_div(rows, kHeadThreads / 64) : rows;
+    info->form = rows ? form : ROG_LOGPROB_AUTO;
     info->blocks = blocks;
-    info->workspace_bytes = 0;
+    info->workspace_bytes = rows && form == ROG_LOGPROB_SPLIT ? kHeadCounterBytes + rows * part_bytes(blocks) : 0;
     info->block = kHeadThreads;
-    info->grid = uint32_t(std::min<uint64_t>(rows, kHeadGridCap));
+    info->grid = uint32_t(std::min<uint64_t>(groups, kHeadGridCap));
+    if (form == ROG_LOGPROB_SPLIT && groups > kHeadGridCap) return ROG_ERR_TOO_LARGE;
     return ROG_OK;
 }
 
@@ -147,12 +162,11 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     a.W = uint32_t(W);
     a.rows = uint32_t(rows);
     a.blocks = blocks;
-    a.quads = uint32_t(ceil_div(blocks, kHeadQuad));
+    a.splits = splits_of(blocks);
     a.top_k = uint32_t(top_k);
     // each of the four columns has eight entries per lane in the top-k table
-    const uint32_t column_blocks = uint32_t(ceil_div(a.quads, kHeadQuad)) * kHeadQuad;
     a.slot_shift = 0;
-    while ((std::max(column_blocks, 1u) - 1) >> a.slot_shift >= 8) ++a.slot_shift;
+    while ((std::max(a.splits, 1u) - 1) >> a.slot_shift >= kTopSlots) ++a.slot_shift;
     a.vocab = vocab;
     p->dtype = dtype;
     return ROG_OK;
@@ -209,9 +223,9 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     a.W = uint32_t(W);
     a.rows = uint32_t(rows);
     a.blocks = blocks;
-    a.quads = uint32_t(ceil_div(blocks, kHeadQuad));
     a.vocab = vocab;
-    a.groups = uint64_t(a.quads) * rows;
+    a.splits = splits_of(blocks);
+    a.groups = uint64_t(a.splits) * rows;
     p->grid = uint32_t(std::min<uint64_t>(a.groups, kHeadGridCap));
     p->dtype = dtype;
     return ROG_OK;

@@ -20,10 +20,10 @@ namespace {
 
 #pragma clang fp contract(off)
 
+#ifndef ROG_ROW_WAVES
+#define ROG_ROW_WAVES 1
+#endif
 constexpr uint32_t kWaves = kHeadThreads / 64;
-constexpr uint32_t kSlots = 8;                 // table entries per lane and column
-constexpr uint32_t kEntries = kWaves * kSlots * 64;
-constexpr uint32_t kListCap = 512;             // candidates held at once
 
 // Orders logits as unsigned numbers; -0 counts as +0.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -35,21 +35,44 @@ __device__ __forceinline__ float from_order(uint32_t o) {
 }
 constexpr uint32_t kOrderMinusInf = 0x007FFFFFu;   // order_of(-inf)
 
-// Shared memory of one workgroup.
-struct Shared {
-    float m[kWaves][64], s[kWaves][64], t[kWaves][64];   // the columns' states
-    float row[4];            // ref(M), L, M; written by the first wave
-    uint32_t count[4];       // hits, candidates, extreme rows' count
-    uint64_t floor_key;      // candidates are at or above it
-};
-struct SharedTop {
-    float tab[kEntries];           // [column][slot][lane]: largest logit
-    uint16_t hits[kEntries];
-    uint64_t list[kListCap];
+// The threads that finish one row together: a workgroup or one wave.
+template <int THREADS>
+struct Team {
+    static constexpr uint32_t kThreads = THREADS;
+    static constexpr uint32_t kTeamWaves = THREADS / 64;
+    static constexpr uint32_t kSlots = THREADS == 64 ? kHeadColumns : kHeadColumns * kTopSlots;   // table rows of 64 lanes
+    static constexpr uint32_t kEntries = kSlots * 64;
+    static constexpr uint32_t kListCap = THREADS == 64 ? 128 : 512;             // candidates held at once
+    static __device__ __forceinline__ uint32_t id() { return THREADS == 64 ? threadIdx.x & 63 : threadIdx.x; }
+    static __device__ __forceinline__ void sync() {
+        if constexpr (THREADS == 64) {
+            // a wave's shared-memory accesses complete in order; keep the compiler from moving them
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        } else {
+            __syncthreads();
+        }
+    }
 };
 
-template <bool TOP> struct SharedFor { typedef uint32_t type; };
-template <> struct SharedFor<true> { typedef SharedTop type; };
+struct Shared {
+    float m[kWaves][64], s[kWaves][64], t[kWaves][64];   // the columns' states
+    float row[4];              // ref(M), L, M, log2 entropy; written by the first wave
+    uint32_t equal;            // extreme rows: columns that equal the largest
+    uint32_t last;
+};
+template <typename T>
+struct SharedTop {
+    float tab[T::kEntries];    // [slot][lane]: largest logit of the slot's blocks in the lane's columns
+    uint64_t list[T::kListCap];
+    uint64_t floor_key;        // candidates are at or above it
+    uint32_t hit_count, count;
+    uint16_t hits[T::kEntries];
+};
+struct Nothing {};
+template <typename T, bool TOP> struct SharedFor { typedef Nothing type; };
+template <typename T> struct SharedFor<T, true> { typedef SharedTop<T> type; };
 
 constexpr float kMaxFinite = 3.40282347e38f;
 
@@ -67,25 +90,19 @@ struct Row {
     }
 };
 
-// Joins the 64 lanes' states (every lane ends with the same one up to the
-// order of its sums; lane 0's is taken).
-__device__ __forceinline__ State join_lanes(State st, const Scaling &c) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        st = join(st, State{__shfl_xor(st.m, d), __shfl_xor(st.s, d), __shfl_xor(st.t, d)}, c);
-    return State{bits_f32(uniform(f32_bits(st.m))), bits_f32(uniform(f32_bits(st.s))), bits_f32(uniform(f32_bits(st.t)))};
+// The block that table row `slot` holds at place i (of 1 << slot_shift).
+template <typename T>
+__device__ __forceinline__ uint32_t slot_block(uint32_t slot, uint32_t i, uint32_t shift) {
+    if constexpr (T::kThreads == 64) return slot;
+    else return (((slot % kTopSlots) << shift) + i) * kHeadColumns + slot / kTopSlots;
 }
 
-// The columns of one table entry: block j of column `w` is block
-// ((j / 4) * 4 + w) * 4 + j % 4 of the row.
-__device__ __forceinline__ uint32_t column_block(uint32_t w, uint32_t j) { return ((j / 4) * 4 + w) * 4 + (j & 3); }
-
-// The K best alternatives of a row from its table.  Called by the whole
-// workgroup; lane_m: in the first wave, the lane's largest logit in the row.
-template <int DT>
-__device__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, const Row &v, Shared &sh, SharedTop &top) {
+// The K best alternatives of a row from its table.  Called by the whole team;
+// lane_m: in the first wave, the lane's largest logit in the row.
+template <int DT, typename T>
+__device__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, const Row &v, SharedTop<T> &top) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
-    const uint32_t tid = threadIdx.x, K = a.top_k;
+    const uint32_t tid = T::id(), K = a.top_k;
     if (tid < 64) {
         // the K-th largest of the lanes' maxima, bit by bit
         const uint32_t o = order_of(lane_m);
@@ -95,54 +112,54 @@ __device__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, c
             if (uint32_t(__popcll(__ballot(o >= tryk))) >= K) k = tryk;
         }
         if (k <= kOrderMinusInf) k = kOrderMinusInf + 1;      // -inf is no alternative
-        if (tid == 0) sh.floor_key = uint64_t(k) << 32;
+        if (tid == 0) top.floor_key = uint64_t(k) << 32;
     }
-    uint64_t floor_key;
+    const uint32_t shift = T::kThreads == 64 ? 0 : a.slot_shift;
+    uint32_t n;
     for (;;) {
-        if (tid == 0) sh.count[0] = sh.count[1] = 0;
-        __syncthreads();
-        floor_key = sh.floor_key;
+        if (tid == 0) top.hit_count = top.count = 0;
+        T::sync();
+        const uint64_t floor_key = top.floor_key;
         const float floor_x = from_order(uint32_t(floor_key >> 32));
-        for (uint32_t e = tid; e < kEntries; e += kHeadThreads)
-            if (top.tab[e] >= floor_x) top.hits[atomicAdd(&sh.count[0], 1u)] = uint16_t(e);
-        __syncthreads();
-        const uint32_t vecs_shift = a.slot_shift + (Logit<DT>::kVecs == 8 ? 3 : 2);
-        const uint64_t tasks = uint64_t(sh.count[0]) << vecs_shift;
-        for (uint64_t q = tid; q < tasks; q += kHeadThreads) {
+        for (uint32_t e = tid; e < T::kEntries; e += T::kThreads)
+            if (top.tab[e] >= floor_x) top.hits[atomicAdd(&top.hit_count, 1u)] = uint16_t(e);
+        T::sync();
+        const uint32_t vecs_shift = shift + (Logit<DT>::kVecs == 8 ? 3 : 2);
+        const uint64_t tasks = uint64_t(top.hit_count) << vecs_shift;
+        for (uint64_t q = tid; q < tasks; q += T::kThreads) {
             const uint32_t e = top.hits[q >> vecs_shift], i = uint32_t(q) & ((1u << vecs_shift) - 1);
-            const uint32_t w = e / (kSlots * 64), slot = (e / 64) % kSlots, el = e % 64;
-            const uint32_t b = column_block(w, (slot << a.slot_shift) + i / Logit<DT>::kVecs);
+            const uint32_t b = slot_block<T>(e / 64, i / Logit<DT>::kVecs, shift), el = e % 64;
             if (b >= a.blocks) continue;
             const BlockAt at = block_at<DT>(a.sh, 0, row, b);
             const uint32_t vi = i % Logit<DT>::kVecs;
             const vec16 vec = load_vec<DT>(at.p, at.n, vi, el);
             float x[per];
             widen_vec<DT>(vec, x);
+            const uint32_t col = at.col + (at.n < per ? 0 : vec_place<DT>(at.n, vi, el));
 #pragma unroll
             for (uint32_t k = 0; k < per; ++k) {
-                const uint64_t key = uint64_t(order_of(x[k])) << 32 | uint32_t(~(at.col + (64 * vi + el) * per + k));
-                if (x[k] >= floor_x && key >= floor_key) {
-                    const uint32_t n = atomicAdd(&sh.count[1], 1u);
-                    if (n < kListCap) top.list[n] = key;
+                const uint64_t key = uint64_t(order_of(x[k])) << 32 | uint32_t(~(col + k));
+                if (owns<DT>(at.n, vi, el, k) && x[k] >= floor_x && key >= floor_key) {
+                    const uint32_t at_list = atomicAdd(&top.count, 1u);
+                    if (at_list < T::kListCap) top.list[at_list] = key;
                 }
             }
         }
-        __syncthreads();
-        const uint32_t n = sh.count[1];
-        if (n <= kListCap) break;
+        T::sync();
+        n = top.count;
+        if (n <= T::kListCap) break;
         // More columns reach the floor than the list holds (many equal logits):
         // the K-th best of those listed is a higher floor that K columns reach.
         // It rises with every turn, since the list holds more than K.
-        for (uint32_t q = tid; q < kListCap; q += kHeadThreads) {
+        for (uint32_t q = tid; q < T::kListCap; q += T::kThreads) {
             const uint64_t key = top.list[q];
             uint32_t above = 0;
-            for (uint32_t k = 0; k < kListCap; ++k) above += top.list[k] > key;
-            if (above == K - 1) sh.floor_key = key;
+            for (uint32_t k = 0; k < T::kListCap; ++k) above += top.list[k] > key;
+            if (above == K - 1) top.floor_key = key;
         }
-        __syncthreads();
+        T::sync();
     }
-    const uint32_t n = sh.count[1];
-    for (uint32_t q = tid; q < n; q += kHeadThreads) {
+    for (uint32_t q = tid; q < n; q += T::kThreads) {
         const uint64_t key = top.list[q];
         uint32_t above = 0;
         for (uint32_t k = 0; k < n; ++k) above += top.list[k] > key;
@@ -153,7 +170,7 @@ __device__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, c
             if (a.top_logp) a.top_logp[o] = v.logp(x, a);
         }
     }
-    for (uint32_t q = n + tid; q < K; q += kHeadThreads) {
+    for (uint32_t q = n + tid; q < K; q += T::kThreads) {
         const uint64_t o = uint64_t(row) * K + q;
         if (a.top_ids) a.top_ids[o] = -1;
         if (a.top_logp) a.top_logp[o] = -kInf;
@@ -183,58 +200,53 @@ __device__ __forceinline__ float token_logit(const LogprobArgs &a, uint32_t row,
     return load_logit<DT>((gbyte *)a.sh.x[r] + int64_t(row) * a.sh.stride[r] + uint64_t(tok - a.sh.col0[r]) * Logit<DT>::kSize);
 }
 
-// Everything after the partial states: called by the whole workgroup with the
-// columns' states in shared memory.
-template <int DT, bool TOP>
-__device__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, Shared &sh, SharedTop *top) {
-    const uint32_t tid = threadIdx.x, lane = tid & 63;
-    const Scaling c{a.scale, a.bound};
-    float lane_m = -kInf;
-    if (tid < 64) {
-        State st[kWaves];
-#pragma unroll
-        for (uint32_t w = 0; w < kWaves; ++w) st[w] = State{sh.m[w][lane], sh.s[w][lane], sh.t[w][lane]};
-        State all = join(join(st[0], st[1], c), join(st[2], st[3], c), c);
-        lane_m = all.m;
-        all = join_lanes(all, c);
-        if (tid == 0) {
-            sh.row[0] = c.ref(all.m);
-            sh.row[1] = log2f(all.s);
-            sh.row[2] = all.m;
-            sh.row[3] = sh.row[1] - all.t / all.s;
-            sh.count[2] = 0;
+// How many of a wave's share of a row's columns equal x: blocks first, first + step, ...
+template <int DT>
+__device__ uint32_t count_equal(const LogprobArgs &a, uint32_t row, uint32_t first, uint32_t step, uint32_t lane, float x) {
+    uint32_t n = 0, r = 0;
+    for (uint32_t b = first; b < a.blocks; b += step) {
+        const BlockAt at = block_at<DT>(a.sh, r, row, b);
+        r = at.shard;
+        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
+            float y[Logit<DT>::kPerVec];
+            widen_vec<DT>(load_vec<DT>(at.p, at.n, i, lane), y);
+            for (uint32_t k = 0; k < Logit<DT>::kPerVec; ++k) n += owns<DT>(at.n, i, lane, k) && y[k] == x;
         }
     }
-    __syncthreads();
-    Row v{sh.row[0], sh.row[1], sh.row[2], (sh.row[0] + sh.row[1]) * kLn2, false};
-    float entropy = sh.row[3] * kLn2;
+    return n;
+}
+
+// A row's numbers from the joined state of its lanes: called by the whole team,
+// with the same `all`.  equal: shared, zero.
+template <int DT, typename T, bool TOP>
+__device__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, const State &all, float lane_m, float log_s,
+                           uint32_t &equal, typename SharedFor<T, TOP>::type &top) {
+    const uint32_t tid = T::id();
+    const Scaling c{a.scale, a.bound};
     const float nan = __builtin_nanf("");
-    if (!(v.m < kInf)) {
-        write_plain_row(a, row, tid, kHeadThreads, nan, nan, nan, nan);
-        return;
-    }
     const bool token = tok < int64_t(a.vocab);      // tok < 0 never comes here, except for tokens == NULL
-    if (v.m == -kInf) {
-        write_plain_row(a, row, tid, kHeadThreads, token ? -kInf : nan, 0.0f, -kInf, -kInf);
+    if (!(all.m < kInf)) {
+        write_plain_row(a, row, tid, T::kThreads, nan, nan, nan, nan);
         return;
     }
-    if (v.m >= a.bound || v.m <= -a.bound) {
+    if (all.m == -kInf) {
+        write_plain_row(a, row, tid, T::kThreads, token ? -kInf : nan, 0.0f, -kInf, -kInf);
+        return;
+    }
+    Row v;
+    v.r = c.ref(all.m);
+    v.l = log_s;
+    v.m = all.m;
+    v.lse = (v.r + v.l) * kLn2;
+    v.extreme = false;
+    float entropy = (v.l - all.t / all.s) * kLn2;
+    if (all.m >= a.bound || all.m <= -a.bound) {
         // Logits this large lie so far apart that any but the largest has
         // probability 0: the row is uniform over the columns that equal it.
-        uint32_t n = 0, r = 0;
-        for (uint32_t b = tid / 64; b < a.blocks; b += kWaves) {
-            const BlockAt at = block_at<DT>(a.sh, r, row, b);
-            r = at.shard;
-            for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
-                float x[Logit<DT>::kPerVec];
-                widen_vec<DT>(load_vec<DT>(at.p, at.n, i, lane), x);
-                for (uint32_t k = 0; k < Logit<DT>::kPerVec; ++k) n += x[k] == v.m;
-            }
-        }
-        atomicAdd(&sh.count[2], n);
-        __syncthreads();
+        atomicAdd(&equal, count_equal<DT>(a, row, tid / 64, T::kTeamWaves, tid & 63, all.m));
+        T::sync();
         v.extreme = true;
-        v.l = log2f(float(sh.count[2]));
+        v.l = log2f(float(equal));
         v.lse = __builtin_amdgcn_fmed3f(__builtin_fmaf(v.m, a.inv_t, v.l * kLn2), -kMaxFinite, kMaxFinite);
         entropy = v.l * kLn2;
     }
@@ -243,57 +255,216 @@ __device__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, Shar
         if (a.entropy) a.entropy[row] = entropy;
         if (a.logp) a.logp[row] = token ? v.logp(token_logit<DT>(a, row, uint32_t(tok)), a) : nan;
     }
-    if constexpr (TOP) alternatives<DT>(a, row, lane_m, v, sh, *top);
+    if constexpr (TOP) alternatives<DT, T>(a, row, lane_m, v, top);
 }
 
-// One workgroup per row: wave w takes column w's quads in turn.
+// The same from the four columns' states in shared memory, by a workgroup.
 template <int DT, bool TOP>
-__global__ __launch_bounds__(kHeadThreads) void rog_logprob_row_kernel(LogprobArgs) {
+__device__ void finish_columns(const LogprobArgs &a, uint32_t row, int64_t tok, Shared &sh,
+                               typename SharedFor<Team<kHeadThreads>, TOP>::type &top) {
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    const Scaling c{a.scale, a.bound};
+    float lane_m = -kInf;
+    if (tid < 64) {
+        State st[kWaves];
+#pragma unroll
+        for (uint32_t w = 0; w < kWaves; ++w) st[w] = State{sh.m[w][lane], sh.s[w][lane], sh.t[w][lane]};
+        const State lanes = join(join(st[0], st[1], c), join(st[2], st[3], c), c);
+        lane_m = lanes.m;
+        const State all = join_lanes(lanes, c);
+        if (tid == 0) {
+            sh.row[0] = all.m;
+            sh.row[1] = all.s;
+            sh.row[2] = all.t;
+            sh.row[3] = log2f(all.s);
+            sh.equal = 0;
+        }
+    }
+    __syncthreads();
+    finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, State{sh.row[0], sh.row[1], sh.row[2]}, lane_m, sh.row[3], sh.equal, top);
+}
+
+// The state of one block of a row.
+template <int DT>
+__device__ __forceinline__ State block_state(const vec16 (&v)[Logit<DT>::kVecs], uint32_t n, uint32_t lane, const Scaling &c) {
+    float x[32];
+    widen_block<DT>(v, n, lane, x);
+    return state_of(x, c);
+}
+
+// Adds a column's j-th block (numbered within the column) to the states of its
+// chunk and of its earlier chunks; `end`: it is the column's last.
+struct Column {
+    State chunk, done;
+    __device__ __forceinline__ void add(const State &st, uint32_t j, bool end, const Scaling &c) {
+        constexpr uint32_t n = kHeadChunk / kHeadColumns;
+        chunk = j % n == 0 ? st : join(chunk, st, c);
+        if (j % n == n - 1 || end) done = j < n ? chunk : join(done, chunk, c);
+    }
+};
+
+__device__ __forceinline__ int64_t row_token(const LogprobArgs &a, uint32_t row) { return a.tokens ? a.tokens[row] : 0; }
+
+// One workgroup per row: wave w takes column w's blocks in turn, the next
+// block's loads in flight while it works on one.
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kHeadThreads, ROG_ROW_WAVES) void rog_logprob_row_kernel(LogprobArgs) {
+    typedef Team<kHeadThreads> T;
     const LogprobArgs &a = launch_args<LogprobArgs>();
     __shared__ Shared sh;
-    __shared__ typename SharedFor<TOP>::type top;
+    __shared__ typename SharedFor<T, TOP>::type top;
     const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
     const Scaling c{a.scale, a.bound};
     for (uint32_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const int64_t tok = a.tokens ? a.tokens[row] : 0;
+        const int64_t tok = row_token(a, row);
         if (tok < 0) {
             write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
             continue;
         }
         __syncthreads();                                   // the row before is done with the shared memory
         if constexpr (TOP) {
-            for (uint32_t e = tid; e < kEntries; e += kHeadThreads) top.tab[e] = -kInf;
-            __syncthreads();
+            // this wave's slots of the table
+            for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
         }
-        State column = no_state();
-        uint32_t r = 0;
-        for (uint32_t q = w; q < a.quads; q += kWaves) {
-            State quad[4];
+        Column col;
+        col.done = no_state();
+        const uint32_t mine = a.blocks > w ? (a.blocks - w + kHeadColumns - 1) / kHeadColumns : 0;
+        vec16 v[Logit<DT>::kVecs], next[Logit<DT>::kVecs];
+        BlockAt at;
+        at.shard = 0;
+        if (mine) {
+            at = block_at<DT>(a.sh, 0, row, w);
+            load_block<DT>(at, lane, next);
+        }
 #pragma unroll 1
-            for (uint32_t i = 0; i < 4; ++i) {
-                quad[i] = no_state();
-                const uint32_t b = 4 * q + i;
-                if (b >= a.blocks) continue;
-                const BlockAt at = block_at<DT>(a.sh, r, row, b);
-                r = at.shard;
-                vec16 v[Logit<DT>::kVecs];
-                load_block<DT>(at, lane, v);
-                float x[32];
+        for (uint32_t j = 0; j < mine; ++j) {
+            const uint32_t n = at.n;
 #pragma unroll
-                for (uint32_t k = 0; k < Logit<DT>::kVecs; ++k) widen_vec<DT>(v[k], x + k * Logit<DT>::kPerVec);
-                quad[i] = state_of(x, c);
-                if constexpr (TOP) {
-                    float &e = top.tab[(w * kSlots + (((q / kWaves) * 4 + i) >> a.slot_shift)) * 64 + lane];
-                    e = max_nan(e, quad[i].m);
-                }
+            for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = next[i];
+            if (j + 1 < mine) {
+                at = block_at<DT>(a.sh, at.shard, row, w + (j + 1) * kHeadColumns);
+                load_block<DT>(at, lane, next);
             }
-            column = join(column, join(join(quad[0], quad[1], c), join(quad[2], quad[3], c), c), c);
+            const State st = block_state<DT>(v, n, lane, c);
+            if constexpr (TOP) {
+                float &e = top.tab[(w * kTopSlots + (j >> a.slot_shift)) * 64 + lane];
+                e = max_nan(e, st.m);
+            }
+            col.add(st, j, j + 1 == mine, c);
         }
-        sh.m[w][lane] = column.m;
-        sh.s[w][lane] = column.s;
-        sh.t[w][lane] = column.t;
+        sh.m[w][lane] = col.done.m;
+        sh.s[w][lane] = col.done.s;
+        sh.t[w][lane] = col.done.t;
         __syncthreads();
-        finish_row<DT, TOP>(a, row, tok, sh, TOP ? (SharedTop *)&top : nullptr);
+        finish_columns<DT, TOP>(a, row, tok, sh, top);
+    }
+}
+
+// A row over several workgroups, four blocks each, one per wave; the last one
+// of the row to finish joins the blocks' states.
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(LogprobArgs) {
+    typedef Team<kHeadThreads> T;
+    const LogprobArgs &a = launch_args<LogprobArgs>();
+    __shared__ Shared sh;
+    __shared__ typename SharedFor<T, TOP>::type top;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
+    const Scaling c{a.scale, a.bound};
+    const uint32_t row = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
+    const int64_t tok = row_token(a, row);
+    if (tok < 0) {
+        if (part == 0) write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
+        return;
+    }
+    float *const states = a.part + uint64_t(row) * a.blocks * (3 * 64) + lane;
+    const uint32_t b = part * kHeadColumns + w;
+    if (b < a.blocks) {
+        vec16 v[Logit<DT>::kVecs];
+        const BlockAt at = block_at<DT>(a.sh, 0, row, b);
+        load_block<DT>(at, lane, v);
+        const State st = block_state<DT>(v, at.n, lane, c);
+        float *p = states + uint64_t(b) * (3 * 64);
+        publish(p, st.m);
+        publish(p + 64, st.s);
+        publish(p + 128, st.t);
+    }
+    if (!last_to_arrive(a.counters + row, a.splits, sh.last)) return;
+    if constexpr (TOP) {
+        for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
+    }
+    Column col;
+    col.done = no_state();
+    const uint32_t mine = a.blocks > w ? (a.blocks - w + kHeadColumns - 1) / kHeadColumns : 0;
+    for (uint32_t j0 = 0; j0 < mine; j0 += 4) {
+        State st[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            if (j0 + i >= mine) continue;
+            const float *p = states + uint64_t((j0 + i) * kHeadColumns + w) * (3 * 64);
+            st[i] = State{collect(p), collect(p + 64), collect(p + 128)};
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            if (j0 + i >= mine) continue;
+            if constexpr (TOP) {
+                float &e = top.tab[(w * kTopSlots + ((j0 + i) >> a.slot_shift)) * 64 + lane];
+                e = max_nan(e, st[i].m);
+            }
+            col.add(st[i], j0 + i, j0 + i + 1 == mine, c);
+        }
+    }
+    sh.m[w][lane] = col.done.m;
+    sh.s[w][lane] = col.done.s;
+    sh.t[w][lane] = col.done.t;
+    __syncthreads();
+    finish_columns<DT, TOP>(a, row, tok, sh, top);
+}
+
+// One wave per row of at most four blocks.
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kHeadThreads, ROG_ROW_WAVES) void rog_logprob_wave_kernel(LogprobArgs) {
+    typedef Team<64> T;
+    const LogprobArgs &a = launch_args<LogprobArgs>();
+    __shared__ uint32_t equal[kWaves];
+    __shared__ typename SharedFor<T, TOP>::type top[kWaves];
+    const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
+    const Scaling c{a.scale, a.bound};
+    const uint32_t step = gridDim.x * kWaves;
+    for (uint64_t row64 = blockIdx.x * kWaves + w; row64 < a.rows; row64 += step) {
+        const uint32_t row = uint32_t(row64);
+        const int64_t tok = row_token(a, row);
+        if (tok < 0) {
+            write_plain_row(a, row, lane, 64, 0.0f, 0.0f, 0.0f, 0.0f);
+            continue;
+        }
+        State st[kHeadColumns];
+        vec16 v[Logit<DT>::kVecs], next[Logit<DT>::kVecs];
+        BlockAt at;
+        if (a.blocks) {
+            at = block_at<DT>(a.sh, 0, row, 0);
+            load_block<DT>(at, lane, next);
+        }
+#pragma unroll
+        for (uint32_t b = 0; b < kHeadColumns; ++b) {
+            st[b] = no_state();
+            if constexpr (TOP) top[w].tab[b * 64 + lane] = -kInf;
+            if (b >= a.blocks) continue;
+            const uint32_t n = at.n;
+#pragma unroll
+            for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = next[i];
+            if (b + 1 < a.blocks) {
+                at = block_at<DT>(a.sh, at.shard, row, b + 1);
+                load_block<DT>(at, lane, next);
+            }
+            st[b] = block_state<DT>(v, n, lane, c);
+            if constexpr (TOP) top[w].tab[b * 64 + lane] = st[b].m;
+        }
+        const State lanes = join(join(st[0], st[1], c), join(st[2], st[3], c), c);
+        const State all = join_lanes(lanes, c);
+        if (lane == 0) equal[w] = 0;
+        T::sync();
+        finish_row<DT, T, TOP>(a, row, tok, all, lanes.m, log2f(all.s), equal[w], top[w]);
+        T::sync();
     }
 }
 
@@ -303,7 +474,11 @@ const void *kfn(K *k) { return reinterpret_cast<const void *>(k); }
 template <int DT>
 const void *logprob_kernel(const LogprobPlan &p) {
     const bool top = p.args.top_ids || p.args.top_logp;
-    return top ? kfn(&rog_logprob_row_kernel<DT, true>) : kfn(&rog_logprob_row_kernel<DT, false>);
+    switch (p.info.form) {
+    case ROG_LOGPROB_SPLIT: return top ? kfn(&rog_logprob_split_kernel<DT, true>) : kfn(&rog_logprob_split_kernel<DT, false>);
+    case ROG_LOGPROB_WAVE: return top ? kfn(&rog_logprob_wave_kernel<DT, true>) : kfn(&rog_logprob_wave_kernel<DT, false>);
+    default: return top ? kfn(&rog_logprob_row_kernel<DT, true>) : kfn(&rog_logprob_row_kernel<DT, false>);
+    }
 }
 
 rog_status launch_logprob(LogprobPlan &p, hipStream_t stream) {

@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobG
     constexpr uint32_t per = Logit<DT>::kPerVec, vecs = Logit<DT>::kVecs;
     const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
     for (uint64_t group = blockIdx.x; group < a.groups; group += gridDim.x) {
-        const uint32_t row = uint32_t(group / a.quads), b = uint32_t(group % a.quads) * 4 + w;
+        const uint32_t row = uint32_t(group / a.splits), b = uint32_t(group % a.splits) * 4 + w;
         if (b >= a.blocks) continue;
         const BlockAt at = block_at<DT>(a.sh, 0, row, b);
         typedef __attribute__((address_space(1))) uint8_t gout;
@@ -56,6 +56,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobG
             load_block<DT>(at, lane, v);
 #pragma unroll
             for (uint32_t i = 0; i < vecs; ++i) widen_vec<DT>(v[i], x + i * per);
+            const bool tiny = at.n < per;
             const float g = a.g_logp[row], h = a.g_entropy ? a.g_entropy[row] : 0.0f, H = a.entropy[row];
             Coeffs k;
             k.g = g * a.inv_t;
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobG
                 // the token is in this block
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i) {
-                    const uint32_t col = (64 * (i / per) + lane) * per + i % per;
+                    const uint32_t col = (tiny ? 0 : vec_place<DT>(at.n, i / per, lane)) + i % per;
                     x[i] = uint32_t(t) == col ? x[i] + k.g : x[i];
                 }
             }
@@ -95,18 +96,17 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobG
             vec16 v;
 #pragma unroll
             for (uint32_t d = 0; d < 4; ++d) v[d] = narrow_word<DT>(x + i * per + d * (per / 4));
-            const uint32_t col = (64 * i + lane) * per;
-            if (col + per <= at.n) {
-                *(gvec16any_out *)(o + col * Logit<DT>::kSize) = v;
-            } else if (col < at.n) {
+            if (at.n >= per) {
+                // where the vector was read: what it shares with other lanes' vectors, they write alike
+                *(gvec16any_out *)(o + vec_place<DT>(at.n, i, lane) * Logit<DT>::kSize) = v;
+            } else if (i == 0 && lane == 0) {
 #pragma unroll
-                for (uint32_t e = 0; e < per; ++e) {
-                    if (col + e >= at.n) continue;
+                for (uint32_t e = 0; e + 1 < per; ++e) {
+                    if (e >= at.n) continue;
                     if constexpr (DT == ROG_DTYPE_F32)
-                        *(__attribute__((address_space(1))) uint32_t *)(o + (col + e) * 4) = v[e];
+                        *(__attribute__((address_space(1))) uint32_t *)(o + e * 4) = v[e];
                     else
-                        *(__attribute__((address_space(1))) uint16_t *)(o + (col + e) * 2) =
-                            uint16_t(e & 1 ? v[e / 2] >> 16 : v[e / 2]);
+                        *(__attribute__((address_space(1))) uint16_t *)(o + e * 2) = uint16_t(e & 1 ? v[e / 2] >> 16 : v[e / 2]);
                 }
             }
         }

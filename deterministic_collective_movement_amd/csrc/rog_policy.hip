@@ -8,8 +8,7 @@
 // bytes read and 8 written per token with every term.
 #include <hip/hip_runtime.h>
 
-#include "rog_device.h"
-#include "rog_head.h"
+#include "rog_head_device.h"
 
 namespace rog {
 namespace {
@@ -132,24 +131,19 @@ __global__ __launch_bounds__(kHeadThreads) void rog_policy_kernel(PolicyArgs a) 
     }
     t = group_sum(t, sh);
     if (a.groups > 1) {
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < 4; ++i) a.part[uint64_t(blockIdx.x) * 4 + i] = t.v[i];
-            __threadfence();
-            last = atomicAdd(a.counter, 1u) == a.groups - 1;
-        }
-        __syncthreads();
-        if (!last) return;
-        __threadfence();
+        if (threadIdx.x == 0)
+            for (int i = 0; i < 4; ++i) publish(a.part + uint64_t(blockIdx.x) * 4 + i, t.v[i]);
+        if (!last_to_arrive(a.counter, a.groups, last)) return;
         t = Totals{{0, 0, 0, 0}};
         for (uint32_t b = threadIdx.x; b < a.groups; b += kHeadThreads) {
             Totals o;
-            for (int i = 0; i < 4; ++i) o.v[i] = a.part[uint64_t(b) * 4 + i];
+            for (int i = 0; i < 4; ++i) o.v[i] = collect(a.part + uint64_t(b) * 4 + i);
             t.add(o);
         }
         t = group_sum(t, sh);
-        if (threadIdx.x == 0) *a.counter = 0;
     }
-    if (threadIdx.x < 4) a.stats[threadIdx.x] = float(t.v[threadIdx.x]);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < 4; ++i) a.stats[i] = float(t.v[i]);
 }
 
 }  // namespace
