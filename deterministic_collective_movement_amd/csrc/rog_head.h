@@ -26,9 +26,14 @@ constexpr uint32_t kHeadBlock = 2048;      // columns of a block
 constexpr uint32_t kHeadColumns = 4;
 constexpr uint32_t kHeadChunk = 16;        // blocks of a chunk
 constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per column
-// Workgroups of a launch, at most: a dispatch counts work-items in 32 bits.
-// The kernels loop over the rest.
-constexpr uint32_t kHeadGridCap = 0xFFFFFFFFu / kHeadThreads;
+// The grid of a launch of `groups` workgroups (below 2^31): a dispatch counts the
+// work-items of each dimension in 32 bits, so more than 2^22 go over two.  The
+// kernels number a workgroup blockIdx.y * gridDim.x + blockIdx.x, and those
+// past the end leave at once.
+inline dim3 head_grid(uint32_t groups) {
+    const uint32_t most = 1u << 22;
+    return groups <= most ? dim3(groups) : dim3(most, (groups + most - 1) / most);
+}
 constexpr int kMaxTopK = 32;
 constexpr uint32_t kTopSlots = 8;          // entries per lane and column in the top-k table
 
@@ -79,8 +84,8 @@ struct LogprobGradArgs {
     const float *lse, *entropy, *g_logp, *g_entropy;
     float scale, inv_t;
     uint32_t W, rows, blocks, vocab;
-    uint32_t splits;                   // workgroup turns per row, four blocks each
-    uint64_t groups;                   // turns of all rows
+    uint32_t splits;                   // workgroups per row, four blocks each
+    uint32_t groups;                   // workgroups of all rows
 };
 
 struct PolicyArgs {

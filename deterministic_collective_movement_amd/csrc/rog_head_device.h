@@ -94,21 +94,32 @@ struct BlockAt {
     uint32_t off;       // the first column's number in the shard
 };
 
-// The shard that holds block b (b below the row's blocks, wave-uniform); `from`
-// is a shard at or before it.
-__device__ __forceinline__ uint32_t shard_of(const HeadShards &h, uint32_t from, uint32_t b) {
-    while (h.block0[from + 1] <= b) ++from;
-    return from;
-}
-
+// Walks through one row's blocks, in rising order: the current shard's layout
+// stays in scalar registers, and kernel arguments are read only where a shard
+// begins.
 template <int DT>
-__device__ __forceinline__ BlockAt block_at(const HeadShards &h, uint32_t from, uint32_t row, uint32_t b) {
-    const uint32_t r = shard_of(h, from, b);
-    const uint32_t off = (b - h.block0[r]) * kHeadBlock;
-    const uint32_t left = h.width[r] - off;
-    gbyte *p = (gbyte *)h.x[r] + int64_t(row) * h.stride[r] + uint64_t(off) * Logit<DT>::kSize;
-    return BlockAt{p, left < kHeadBlock ? left : kHeadBlock, h.col0[r] + off, r, off};
-}
+struct Cursor {
+    const HeadShards &h;
+    gbyte *base;                       // the row's first column in the shard
+    uint32_t row, shard, first, end;   // blocks [first, end) are the shard's
+    uint32_t width, col0;
+
+    __device__ __forceinline__ Cursor(const HeadShards &shards, uint32_t r) : h(shards), row(r) { enter(0); }
+    __device__ __forceinline__ void enter(uint32_t s) {
+        shard = s;
+        first = h.block0[s];
+        end = h.block0[s + 1];
+        width = h.width[s];
+        col0 = h.col0[s];
+        base = (gbyte *)h.x[s] + int64_t(row) * h.stride[s];
+    }
+    // Block b (below the row's blocks, not before the shard that the cursor is in).
+    __device__ __forceinline__ BlockAt at(uint32_t b) {
+        while (b >= end) enter(shard + 1);
+        const uint32_t off = (b - first) * kHeadBlock, left = width - off;
+        return BlockAt{base + uint64_t(off) * Logit<DT>::kSize, left < kHeadBlock ? left : kHeadBlock, col0 + off, shard, off};
+    }
+};
 
 // A lane's vector i of a block is columns (64 i + lane) * kPerVec and on.  Where
 // that runs past the block's end at n, the vector is read from the last place
@@ -149,16 +160,21 @@ __device__ __forceinline__ vec16 load_vec(gbyte *p, uint32_t n, uint32_t i, uint
     return *(gvec16any *)(p + vec_place<DT>(n, i, lane) * Logit<DT>::kSize);
 }
 
+// Issues the loads of a block.  They are issued whatever the block, so that no
+// branch joins registers that loads are still on their way to: a block of less
+// than one vector (read where it is used, tiny_state) reads the first bytes of
+// the kernel arguments instead, and with `real`
+// false every lane reads the block's first bytes.
 template <int DT>
-__device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[Logit<DT>::kVecs]) {
-    if (b.n < Logit<DT>::kPerVec) {
-        const vec16 t = load_tiny<DT>(b.p, b.n);
+__device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[Logit<DT>::kVecs], bool real = true) {
+    constexpr uint32_t per = Logit<DT>::kPerVec;
+    const bool tiny = b.n < per;
+    gbyte *const p = tiny ? (gbyte *)__builtin_amdgcn_kernarg_segment_ptr() : b.p;
+    const uint32_t last = tiny || !real ? 0 : b.n - per;
 #pragma unroll
-        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = t;
-    } else {
-#pragma unroll
-        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i)
-            v[i] = *(gvec16any *)(b.p + vec_place<DT>(b.n, i, lane) * Logit<DT>::kSize);
+    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
+        const uint32_t c = own_column<DT>(i, lane);
+        v[i] = *(gvec16any *)(p + (c < last ? c : last) * Logit<DT>::kSize);
     }
 }
 
@@ -170,15 +186,23 @@ __device__ __forceinline__ bool owns(uint32_t n, uint32_t i, uint32_t lane, uint
     return vec_place<DT>(n, i, lane) + e >= c;
 }
 
-// The elements of a block, -inf in the place of those that are not the lane's own.
+// The elements of a block of kPerVec columns or more, -inf in the place of
+// those that are not the lane's own.
 template <int DT>
-__device__ __forceinline__ void widen_block(const vec16 (&v)[Logit<DT>::kVecs], uint32_t n, uint32_t lane, float (&x)[32]) {
+__device__ __forceinline__ void widen_block(const vec16 (&v)[Logit<DT>::kVecs], float (&x)[32]) {
+#pragma unroll
+    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) widen_vec<DT>(v[i], x + i * Logit<DT>::kPerVec);
+}
+template <int DT>
+__device__ __forceinline__ void mask_tail(uint32_t n, uint32_t lane, float (&x)[32]) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
+    const uint32_t last = n - per;
 #pragma unroll
-    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) widen_vec<DT>(v[i], x + i * per);
-    if (n < kHeadBlock) {
+    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
+        const uint32_t c = own_column<DT>(i, lane);
+        const uint32_t others = c > last ? c - last : 0;       // leading elements that are another lane's
 #pragma unroll
-        for (uint32_t i = 0; i < 32; ++i) x[i] = owns<DT>(n, i / per, lane, i % per) ? x[i] : -kInf;
+        for (uint32_t e = 0; e < per; ++e) x[i * per + e] = e >= others ? x[i * per + e] : -kInf;
     }
 }
 
@@ -222,6 +246,29 @@ __device__ __forceinline__ State state_of(const float (&x)[32], const Scaling &c
         t[i & 3] = __builtin_fmaf(e, y, t[i & 3]);
     }
     return State{m, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3])};
+}
+
+// The state of a tiny block: the first lane has its columns.
+template <int DT>
+__device__ __forceinline__ State tiny_state(gbyte *p, uint32_t n, uint32_t lane, const Scaling &c) {
+    constexpr uint32_t per = Logit<DT>::kPerVec;
+    float x[per];
+    widen_vec<DT>(load_tiny<DT>(p, n), x);
+    float m = -kInf, s = 0, t = 0;
+#pragma unroll
+    for (uint32_t e = 0; e < per; ++e) {
+        x[e] = lane == 0 ? x[e] : -kInf;
+        m = max_nan(m, x[e]);
+    }
+    const float r = c.ref(m);
+#pragma unroll
+    for (uint32_t e = 0; e < per; ++e) {
+        const float y = __builtin_fmaf(__builtin_amdgcn_fmed3f(x[e], -c.bound, c.bound), c.scale, -r);
+        const float q = exp2_fast(y);
+        s = s + q;
+        t = __builtin_fmaf(q, y, t);
+    }
+    return State{m, s, t};
 }
 
 // The state of both sides' logits.  A side without logits leaves the other's

@@ -46,6 +46,7 @@ bool fits(uintptr_t at, uint64_t rows, uint64_t stride, uint64_t width) {
     return at <= UINTPTR_MAX - n;
 }
 
+constexpr uint64_t kMaxGroups = uint64_t(1) << 31;   // workgroups of one launch
 constexpr float kMinTemperature = 1.0f / 1024, kMaxTemperature = 1024.0f;
 constexpr double kLog2E = 1.4426950408889634;
 
@@ -104,8 +105,8 @@ rog_status choose_form(uint32_t blocks, size_t rows, int top_k, rog_logprob_form
     info->blocks = blocks;
     info->workspace_bytes = rows && form == ROG_LOGPROB_SPLIT ? kHeadCounterBytes + rows * part_bytes(blocks) : 0;
     info->block = kHeadThreads;
-    info->grid = uint32_t(std::min<uint64_t>(groups, kHeadGridCap));
-    if (form == ROG_LOGPROB_SPLIT && groups > kHeadGridCap) return ROG_ERR_TOO_LARGE;
+    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    info->grid = uint32_t(groups);
     return ROG_OK;
 }
 
@@ -225,8 +226,9 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     a.blocks = blocks;
     a.vocab = vocab;
     a.splits = splits_of(blocks);
-    a.groups = uint64_t(a.splits) * rows;
-    p->grid = uint32_t(std::min<uint64_t>(a.groups, kHeadGridCap));
+    const uint64_t groups = uint64_t(a.splits) * rows;
+    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    a.groups = p->grid = uint32_t(groups);
     p->dtype = dtype;
     return ROG_OK;
 }

@@ -100,7 +100,7 @@ __device__ __forceinline__ uint32_t slot_block(uint32_t slot, uint32_t i, uint32
 // The K best alternatives of a row from its table.  Called by the whole team;
 // lane_m: in the first wave, the lane's largest logit in the row.
 template <int DT, typename T>
-__device__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, const Row &v, SharedTop<T> &top) {
+__device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, const Row &v, SharedTop<T> &top) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const uint32_t tid = T::id(), K = a.top_k;
     if (tid < 64) {
@@ -130,7 +130,7 @@ __device__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, c
             const uint32_t e = top.hits[q >> vecs_shift], i = uint32_t(q) & ((1u << vecs_shift) - 1);
             const uint32_t b = slot_block<T>(e / 64, i / Logit<DT>::kVecs, shift), el = e % 64;
             if (b >= a.blocks) continue;
-            const BlockAt at = block_at<DT>(a.sh, 0, row, b);
+            const BlockAt at = Cursor<DT>(a.sh, row).at(b);
             const uint32_t vi = i % Logit<DT>::kVecs;
             const vec16 vec = load_vec<DT>(at.p, at.n, vi, el);
             float x[per];
@@ -202,16 +202,13 @@ __device__ __forceinline__ float token_logit(const LogprobArgs &a, uint32_t row,
 
 // How many of a wave's share of a row's columns equal x: blocks first, first + step, ...
 template <int DT>
-__device__ uint32_t count_equal(const LogprobArgs &a, uint32_t row, uint32_t first, uint32_t step, uint32_t lane, float x) {
-    uint32_t n = 0, r = 0;
+__device__ __forceinline__ uint32_t count_equal(const LogprobArgs &a, uint32_t row, uint32_t first, uint32_t step, uint32_t lane, float x) {
+    uint32_t n = 0;
+    Cursor<DT> cur(a.sh, row);
     for (uint32_t b = first; b < a.blocks; b += step) {
-        const BlockAt at = block_at<DT>(a.sh, r, row, b);
-        r = at.shard;
-        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
-            float y[Logit<DT>::kPerVec];
-            widen_vec<DT>(load_vec<DT>(at.p, at.n, i, lane), y);
-            for (uint32_t k = 0; k < Logit<DT>::kPerVec; ++k) n += owns<DT>(at.n, i, lane, k) && y[k] == x;
-        }
+        const BlockAt at = cur.at(b);
+#pragma unroll 1
+        for (uint32_t k = lane; k < at.n; k += 64) n += load_logit<DT>(at.p + k * Logit<DT>::kSize) == x;
     }
     return n;
 }
@@ -219,7 +216,7 @@ __device__ uint32_t count_equal(const LogprobArgs &a, uint32_t row, uint32_t fir
 // A row's numbers from the joined state of its lanes: called by the whole team,
 // with the same `all`.  equal: shared, zero.
 template <int DT, typename T, bool TOP>
-__device__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, const State &all, float lane_m, float log_s,
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, const State &all, float lane_m, float log_s,
                            uint32_t &equal, typename SharedFor<T, TOP>::type &top) {
     const uint32_t tid = T::id();
     const Scaling c{a.scale, a.bound};
@@ -260,7 +257,7 @@ __device__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, cons
 
 // The same from the four columns' states in shared memory, by a workgroup.
 template <int DT, bool TOP>
-__device__ void finish_columns(const LogprobArgs &a, uint32_t row, int64_t tok, Shared &sh,
+__device__ __forceinline__ void finish_columns(const LogprobArgs &a, uint32_t row, int64_t tok, Shared &sh,
                                typename SharedFor<Team<kHeadThreads>, TOP>::type &top) {
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const Scaling c{a.scale, a.bound};
@@ -284,11 +281,19 @@ __device__ void finish_columns(const LogprobArgs &a, uint32_t row, int64_t tok, 
     finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, State{sh.row[0], sh.row[1], sh.row[2]}, lane_m, sh.row[3], sh.equal, top);
 }
 
-// The state of one block of a row.
+// The state of the block at `at`, whose loads into v are in flight; then, with
+// `next` set, moves `at` on to block `b` of the row and issues its loads.
 template <int DT>
-__device__ __forceinline__ State block_state(const vec16 (&v)[Logit<DT>::kVecs], uint32_t n, uint32_t lane, const Scaling &c) {
+__device__ __forceinline__ State take_block(Cursor<DT> &cur, BlockAt &at, vec16 (&v)[Logit<DT>::kVecs], uint32_t lane,
+                                            const Scaling &c, bool next, uint32_t b) {
+    const uint32_t n = at.n;
+    gbyte *const p = at.p;
     float x[32];
-    widen_block<DT>(v, n, lane, x);
+    widen_block<DT>(v, x);
+    if (next) at = cur.at(b);
+    load_block<DT>(at, lane, v, next);
+    if (n < Logit<DT>::kPerVec) return tiny_state<DT>(p, n, lane, c);
+    if (n < kHeadBlock) mask_tail<DT>(n, lane, x);
     return state_of(x, c);
 }
 
@@ -315,49 +320,41 @@ __global__ __launch_bounds__(kHeadThreads, ROG_ROW_WAVES) void rog_logprob_row_k
     __shared__ typename SharedFor<T, TOP>::type top;
     const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
     const Scaling c{a.scale, a.bound};
-    for (uint32_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const int64_t tok = row_token(a, row);
-        if (tok < 0) {
-            write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
-            continue;
-        }
-        __syncthreads();                                   // the row before is done with the shared memory
-        if constexpr (TOP) {
-            // this wave's slots of the table
-            for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
-        }
-        Column col;
-        col.done = no_state();
-        const uint32_t mine = a.blocks > w ? (a.blocks - w + kHeadColumns - 1) / kHeadColumns : 0;
-        vec16 v[Logit<DT>::kVecs], next[Logit<DT>::kVecs];
-        BlockAt at;
-        at.shard = 0;
-        if (mine) {
-            at = block_at<DT>(a.sh, 0, row, w);
-            load_block<DT>(at, lane, next);
-        }
-#pragma unroll 1
-        for (uint32_t j = 0; j < mine; ++j) {
-            const uint32_t n = at.n;
-#pragma unroll
-            for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = next[i];
-            if (j + 1 < mine) {
-                at = block_at<DT>(a.sh, at.shard, row, w + (j + 1) * kHeadColumns);
-                load_block<DT>(at, lane, next);
-            }
-            const State st = block_state<DT>(v, n, lane, c);
-            if constexpr (TOP) {
-                float &e = top.tab[(w * kTopSlots + (j >> a.slot_shift)) * 64 + lane];
-                e = max_nan(e, st.m);
-            }
-            col.add(st, j, j + 1 == mine, c);
-        }
-        sh.m[w][lane] = col.done.m;
-        sh.s[w][lane] = col.done.s;
-        sh.t[w][lane] = col.done.t;
-        __syncthreads();
-        finish_columns<DT, TOP>(a, row, tok, sh, top);
+    const uint32_t row = blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= a.rows) return;
+    const int64_t tok = row_token(a, row);
+    if (tok < 0) {
+        write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
+        return;
     }
+    if constexpr (TOP) {
+        // this wave's slots of the table
+        for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
+    }
+    Column col;
+    col.done = no_state();
+    const uint32_t mine = a.blocks > w ? (a.blocks - w + kHeadColumns - 1) / kHeadColumns : 0;
+    vec16 v[Logit<DT>::kVecs];
+    Cursor<DT> cur(a.sh, row);
+    BlockAt at;
+    if (mine) {
+        at = cur.at(w);
+        load_block<DT>(at, lane, v);
+    }
+#pragma unroll 1
+    for (uint32_t j = 0; j < mine; ++j) {
+        const State st = take_block<DT>(cur, at, v, lane, c, j + 1 < mine, w + (j + 1) * kHeadColumns);
+        if constexpr (TOP) {
+            float &e = top.tab[(w * kTopSlots + (j >> a.slot_shift)) * 64 + lane];
+            e = max_nan(e, st.m);
+        }
+        col.add(st, j, j + 1 == mine, c);
+    }
+    sh.m[w][lane] = col.done.m;
+    sh.s[w][lane] = col.done.s;
+    sh.t[w][lane] = col.done.t;
+    __syncthreads();
+    finish_columns<DT, TOP>(a, row, tok, sh, top);
 }
 
 // A row over several workgroups, four blocks each, one per wave; the last one
@@ -370,7 +367,9 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
     __shared__ typename SharedFor<T, TOP>::type top;
     const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
     const Scaling c{a.scale, a.bound};
-    const uint32_t row = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
+    const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
+    const uint32_t row = group / a.splits, part = group % a.splits;
+    if (row >= a.rows) return;
     const int64_t tok = row_token(a, row);
     if (tok < 0) {
         if (part == 0) write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
@@ -380,9 +379,17 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
     const uint32_t b = part * kHeadColumns + w;
     if (b < a.blocks) {
         vec16 v[Logit<DT>::kVecs];
-        const BlockAt at = block_at<DT>(a.sh, 0, row, b);
+        const BlockAt at = Cursor<DT>(a.sh, row).at(b);
         load_block<DT>(at, lane, v);
-        const State st = block_state<DT>(v, at.n, lane, c);
+        float x[32];
+        widen_block<DT>(v, x);
+        State st;
+        if (at.n < Logit<DT>::kPerVec) {
+            st = tiny_state<DT>(at.p, at.n, lane, c);
+        } else {
+            if (at.n < kHeadBlock) mask_tail<DT>(at.n, lane, x);
+            st = state_of(x, c);
+        }
         float *p = states + uint64_t(b) * (3 * 64);
         publish(p, st.m);
         publish(p + 64, st.s);
@@ -429,43 +436,36 @@ __global__ __launch_bounds__(kHeadThreads, ROG_ROW_WAVES) void rog_logprob_wave_
     __shared__ typename SharedFor<T, TOP>::type top[kWaves];
     const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
     const Scaling c{a.scale, a.bound};
-    const uint32_t step = gridDim.x * kWaves;
-    for (uint64_t row64 = blockIdx.x * kWaves + w; row64 < a.rows; row64 += step) {
-        const uint32_t row = uint32_t(row64);
-        const int64_t tok = row_token(a, row);
-        if (tok < 0) {
-            write_plain_row(a, row, lane, 64, 0.0f, 0.0f, 0.0f, 0.0f);
-            continue;
-        }
-        State st[kHeadColumns];
-        vec16 v[Logit<DT>::kVecs], next[Logit<DT>::kVecs];
-        BlockAt at;
-        if (a.blocks) {
-            at = block_at<DT>(a.sh, 0, row, 0);
-            load_block<DT>(at, lane, next);
-        }
-#pragma unroll
-        for (uint32_t b = 0; b < kHeadColumns; ++b) {
-            st[b] = no_state();
-            if constexpr (TOP) top[w].tab[b * 64 + lane] = -kInf;
-            if (b >= a.blocks) continue;
-            const uint32_t n = at.n;
-#pragma unroll
-            for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) v[i] = next[i];
-            if (b + 1 < a.blocks) {
-                at = block_at<DT>(a.sh, at.shard, row, b + 1);
-                load_block<DT>(at, lane, next);
-            }
-            st[b] = block_state<DT>(v, n, lane, c);
-            if constexpr (TOP) top[w].tab[b * 64 + lane] = st[b].m;
-        }
-        const State lanes = join(join(st[0], st[1], c), join(st[2], st[3], c), c);
-        const State all = join_lanes(lanes, c);
-        if (lane == 0) equal[w] = 0;
-        T::sync();
-        finish_row<DT, T, TOP>(a, row, tok, all, lanes.m, log2f(all.s), equal[w], top[w]);
-        T::sync();
+    const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kWaves + w;
+    if (row >= a.rows) return;
+    const int64_t tok = row_token(a, row);
+    if (tok < 0) {
+        write_plain_row(a, row, lane, 64, 0.0f, 0.0f, 0.0f, 0.0f);
+        return;
     }
+    State even = no_state(), odd = no_state();         // columns 0 and 1, columns 2 and 3
+    vec16 v[Logit<DT>::kVecs];
+    Cursor<DT> cur(a.sh, row);
+    BlockAt at;
+    if (a.blocks) {
+        at = cur.at(0);
+        load_block<DT>(at, lane, v);
+    }
+#pragma unroll 1
+    for (uint32_t b = 0; b < a.blocks; ++b) {
+        const State st = take_block<DT>(cur, at, v, lane, c, b + 1 < a.blocks, b + 1);
+        if constexpr (TOP) top[w].tab[b * 64 + lane] = st.m;
+        if (b < 2) even = b == 0 ? st : join(even, st, c);
+        else odd = b == 2 ? st : join(odd, st, c);
+    }
+    if constexpr (TOP) {
+        for (uint32_t b = a.blocks; b < kHeadColumns; ++b) top[w].tab[b * 64 + lane] = -kInf;
+    }
+    const State lanes = join(even, odd, c);
+    const State all = join_lanes(lanes, c);
+    if (lane == 0) equal[w] = 0;
+    T::sync();
+    finish_row<DT, T, TOP>(a, row, tok, all, lanes.m, log2f(all.s), equal[w], top[w]);
 }
 
 template <typename K>
@@ -486,7 +486,7 @@ rog_status launch_logprob(LogprobPlan &p, hipStream_t stream) {
                     : p.dtype == ROG_DTYPE_F16 ? logprob_kernel<ROG_DTYPE_F16>(p)
                                                : logprob_kernel<ROG_DTYPE_F32>(p);
     void *params[] = {&p.args};
-    const hipError_t e = hipLaunchKernel(k, dim3(p.info.grid), dim3(p.info.block), params, 0, stream);
+    const hipError_t e = hipLaunchKernel(k, head_grid(p.info.grid), dim3(p.info.block), params, 0, stream);
     if (e != hipSuccess) {
         g_last_hip_error = int(e);
         return ROG_ERR_LAUNCH;

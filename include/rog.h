@@ -392,7 +392,8 @@ typedef struct {
  *                             that is NULL, misaligned or too small.
  *   ROG_ERR_OVERLAP           an output overlaps a shard, the tokens, the
  *                             workspace or another output.
- *   ROG_ERR_TOO_LARGE         rows or V of 2^31 or more, or address overflow.
+ *   ROG_ERR_TOO_LARGE         rows or V of 2^31 or more, address overflow, or 2^31
+ *                             workgroups or more.
  *   ROG_ERR_LAUNCH            hipLaunchKernel failed (rog_last_hip_error()).
  * rows == 0: ROG_OK, nothing enqueued.
  */
