@@ -12,20 +12,24 @@
 
 namespace rog {
 
-// How a row of logits is cut.  The unit is a block: 2048 consecutive columns
-// of one shard (a shard's last block may be shorter), 32 columns per lane of
-// one wave.  Blocks are numbered through the shards in rank order; block b
-// belongs to column b mod 4 of the row, and sixteen consecutive blocks make a
-// chunk.  The partial states are joined in one order, whatever the launch
-// form: the four blocks of a column within a chunk one after the other, a
-// column's chunks one after the other, the columns as (0+1)+(2+3), the lanes
-// last.  So a row's bits depend on its values, its shards' widths and the
-// temperature alone, not on how many rows a call has or which workgroups
-// computed them.
+// How a row of logits is cut.  A block is 2048 consecutive columns of one shard
+// (a shard's last one may be shorter), 32 columns per lane of one wave; blocks
+// are numbered through the shards in rank order.  A unit is four blocks that
+// one wave takes one after the other: a row of at most four blocks is one
+// unit; a longer row is cut into chunks of sixteen blocks, and unit w of a
+// chunk is every fourth of its blocks from the w-th on (so that the waves of a
+// workgroup share the row evenly).  The partial states are joined in one
+// order, whatever the launch form: the blocks of a unit one after the other in
+// each lane, then the unit's lanes; then units 64 apart one after the other,
+// and the 64 sums last.  So a row's bits depend on its values, its shards'
+// widths and the temperature alone, not on how many rows a call has or which
+// workgroups computed them.
 constexpr uint32_t kHeadBlock = 2048;      // columns of a block
-constexpr uint32_t kHeadColumns = 4;
-constexpr uint32_t kHeadChunk = 16;        // blocks of a chunk
-constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per column
+constexpr uint32_t kUnitBlocks = 4;
+constexpr uint32_t kChunkUnits = 4;
+constexpr uint32_t kChunkBlocks = kUnitBlocks * kChunkUnits;
+constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per unit of a chunk
+constexpr int kGradBlocks = kHeadThreads / 64;   // the gradient's workgroup: a block per wave
 // The grid of a launch of `groups` workgroups (below 2^31): a dispatch counts the
 // work-items of each dimension in 32 bits, so more than 2^22 go over two.  The
 // kernels number a workgroup blockIdx.y * gridDim.x + blockIdx.x, and those
@@ -35,21 +39,29 @@ inline dim3 head_grid(uint32_t groups) {
     return groups <= most ? dim3(groups) : dim3(most, (groups + most - 1) / most);
 }
 constexpr int kMaxTopK = 32;
-constexpr uint32_t kTopSlots = 8;          // entries per lane and column in the top-k table
+constexpr uint32_t kTopSlots = 8;          // entries per lane and wave in the top-k table
 
 // Tunables, measured on MI355X; a variant build may override one with -D.
 #ifndef ROG_SPLIT_MAX_GROUPS
-#define ROG_SPLIT_MAX_GROUPS 4096
+#define ROG_SPLIT_MAX_GROUPS 1024
 #endif
-#ifndef ROG_WAVE_MIN_ROWS
-#define ROG_WAVE_MIN_ROWS 512
+#ifndef ROG_HEAD_NT_MIN_BYTES
+#define ROG_HEAD_NT_MIN_BYTES (128ull << 20)
 #endif
+#ifndef ROG_WAVE_ROWS
+#define ROG_WAVE_ROWS 4
+#endif
+constexpr uint32_t kWaveRows = ROG_WAVE_ROWS;   // rows (waves) of a workgroup of the one-wave-per-row form
 constexpr uint32_t kMaxVocab = 1u << 31;   // columns of a row: below this
 
 // The front of a workspace: one arrival counter per row of a split launch (the
 // first one for the policy loss), zero between calls.  Partial states follow.
 constexpr uint32_t kHeadCounters = 4096;
 constexpr size_t kHeadCounterBytes = kHeadCounters * sizeof(uint32_t);
+
+// Floats of a split row's partial states: m, s, t of each unit (padded to 4),
+// then 64 lanes' maxima for each of four entries per unit.
+constexpr uint32_t kUnitFloats = 4 + 4 * 64;
 
 struct HeadShards {
     const void *x[kMaxPeers];          // element (0, 0) of each shard
@@ -65,14 +77,14 @@ struct LogprobArgs {
     float *logp, *entropy, *lse, *top_logp;
     int64_t *top_ids;
     uint32_t *counters;                // split: one per row
-    float *part;                       // split: partial states, [row][block][m, s, t][lane]
+    float *part;                       // split: per row, the units' states and their lanes' maxima
     float scale;                       // log2(e) / temperature
     float inv_t;                       // 1 / temperature
     float bound;                       // |x| beyond this leaves the scaled range
     uint32_t W, rows, blocks;
-    uint32_t splits;                   // split: workgroups per row, four blocks each
+    uint32_t chunks;
     uint32_t top_k;
-    uint32_t slot_shift;               // log2 of the blocks that one entry of the top-k table covers
+    uint32_t slot_shift;               // log2 of a wave's blocks that one entry of the top-k table covers
     uint32_t vocab;
 };
 
@@ -106,6 +118,7 @@ struct LogprobPlan {
     rog_head_plan_info info;
     LogprobArgs args;
     rog_dtype dtype;
+    bool nt_loads;                     // logits are streamed past the caches
 };
 struct LogprobGradPlan {
     uint32_t grid;

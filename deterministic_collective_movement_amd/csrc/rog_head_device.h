@@ -165,16 +165,18 @@ __device__ __forceinline__ vec16 load_vec(gbyte *p, uint32_t n, uint32_t i, uint
 // than one vector (read where it is used, tiny_state) reads the first bytes of
 // the kernel arguments instead, and with `real`
 // false every lane reads the block's first bytes.
-template <int DT>
+template <int DT, bool NT>
 __device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[Logit<DT>::kVecs], bool real = true) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const bool tiny = b.n < per;
     gbyte *const p = tiny ? (gbyte *)__builtin_amdgcn_kernarg_segment_ptr() : b.p;
-    const uint32_t last = tiny || !real ? 0 : b.n - per;
+    const uint32_t last = tiny || !real ? 0 : (b.n - per) * Logit<DT>::kSize;
 #pragma unroll
     for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
-        const uint32_t c = own_column<DT>(i, lane);
-        v[i] = *(gvec16any *)(p + (c < last ? c : last) * Logit<DT>::kSize);
+        const uint32_t c = (64 * i + lane) * 16;
+        gvec16any *const q = (gvec16any *)(p + (c < last ? c : last));
+        if constexpr (NT) v[i] = __builtin_nontemporal_load(q);
+        else v[i] = *q;
     }
 }
 
@@ -213,7 +215,7 @@ __device__ __forceinline__ void mask_tail(uint32_t n, uint32_t lane, float (&x)[
 // multiply-add, so the rounding of R cancels between s and what is read
 // against it.  No logits: m = -inf, s = t = 0.
 struct State {
-    float m, s, t;
+    float m, r, s, t;      // r = ref(m)
 };
 
 struct Scaling {
@@ -237,15 +239,15 @@ __device__ __forceinline__ State state_of(const float (&x)[32], const Scaling &c
 #pragma unroll
     for (int i = 1; i < 32; ++i) m = max_nan(m, x[i]);
     const float r = c.ref(m);
-    float s[4] = {0, 0, 0, 0}, t[4] = {0, 0, 0, 0};
+    float s[4], t[4];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const float y = __builtin_fmaf(__builtin_amdgcn_fmed3f(x[i], -c.bound, c.bound), c.scale, -r);
         const float e = exp2_fast(y);
-        s[i & 3] = s[i & 3] + e;
-        t[i & 3] = __builtin_fmaf(e, y, t[i & 3]);
+        s[i & 3] = i < 4 ? e : s[i & 3] + e;
+        t[i & 3] = i < 4 ? e * y : __builtin_fmaf(e, y, t[i & 3]);
     }
-    return State{m, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3])};
+    return State{m, r, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3])};
 }
 
 // The state of a tiny block: the first lane has its columns.
@@ -268,21 +270,21 @@ __device__ __forceinline__ State tiny_state(gbyte *p, uint32_t n, uint32_t lane,
         s = s + q;
         t = __builtin_fmaf(q, y, t);
     }
-    return State{m, s, t};
+    return State{m, r, s, t};
 }
 
 // The state of both sides' logits.  A side without logits leaves the other's
 // bits as they are.
-__device__ __forceinline__ State join(const State &a, const State &b, const Scaling &c) {
-    const float ra = c.ref(a.m), rb = c.ref(b.m);
-    const float r = max_nan(ra, rb);
-    const float da = ra - r, db = rb - r;
+__device__ __forceinline__ State join(const State &a, const State &b) {
+    const float r = max_nan(a.r, b.r);
+    const float da = a.r - r, db = b.r - r;
     const float wa = exp2_fast(da), wb = exp2_fast(db);
-    return State{max_nan(a.m, b.m), __builtin_fmaf(a.s, wa, b.s * wb),
+    return State{max_nan(a.m, b.m), r, __builtin_fmaf(a.s, wa, b.s * wb),
                  __builtin_fmaf(wa, __builtin_fmaf(a.s, da, a.t), wb * __builtin_fmaf(b.s, db, b.t))};
 }
 
-__device__ __forceinline__ State no_state() { return State{-kInf, 0.0f, 0.0f}; }
+__device__ __forceinline__ State no_state(const Scaling &c) { return State{-kInf, c.ref(-kInf), 0.0f, 0.0f}; }
+__device__ __forceinline__ State make_state(float m, float s, float t, const Scaling &c) { return State{m, c.ref(m), s, t}; }
 
 // Reductions over the 64 lanes of a wave, all active: within rows of 16 lanes
 // by DPP exchanges (no shared memory), then over the four rows by lane reads.
@@ -306,10 +308,10 @@ __device__ __forceinline__ float reduce_lanes(float x, F f) {
 // Joins the 64 lanes' states: their largest logit first, then two sums.
 __device__ __forceinline__ State join_lanes(const State &st, const Scaling &c) {
     const float m = reduce_lanes(st.m, [](float a, float b) { return max_nan(a, b); });
-    const float d = c.ref(st.m) - c.ref(m);
+    const float r = c.ref(m), d = st.r - r;
     const float w = exp2_fast(d);
     const auto add = [](float a, float b) { return a + b; };
-    return State{m, reduce_lanes(st.s * w, add), reduce_lanes(w * __builtin_fmaf(st.s, d, st.t), add)};
+    return State{m, r, reduce_lanes(st.s * w, add), reduce_lanes(w * __builtin_fmaf(st.s, d, st.t), add)};
 }
 
 // Values handed from workgroup to workgroup of one launch: stores and loads at

@@ -82,30 +82,26 @@ rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dty
     return rows >= kMaxVocab ? ROG_ERR_TOO_LARGE : ROG_OK;
 }
 
-// Bytes of partial states per row of a split launch: three per lane and block.
-uint64_t part_bytes(uint32_t blocks) { return uint64_t(blocks) * 3 * 64 * sizeof(float); }
-
-inline uint32_t splits_of(uint32_t blocks) { return uint32_t(ceil_div(blocks, kHeadColumns)); }
+inline uint32_t chunks_of(uint32_t blocks) { return uint32_t(ceil_div(blocks, kChunkBlocks)); }
 
 // Launch form, grid and workspace of rog_logprob.
 rog_status choose_form(uint32_t blocks, size_t rows, int top_k, rog_logprob_form form, rog_head_plan_info *info) {
     if (form < ROG_LOGPROB_AUTO || form > ROG_LOGPROB_WAVE || top_k < 0 || top_k > kMaxTopK)
         return ROG_ERR_INVALID_ARGUMENT;
-    const bool may_split = rows <= kHeadCounters && blocks > kHeadColumns;
-    const bool may_wave = blocks <= kHeadColumns;
-    if ((form == ROG_LOGPROB_SPLIT && !may_split) || (form == ROG_LOGPROB_WAVE && !may_wave))
-        return ROG_ERR_INVALID_ARGUMENT;
+    const uint32_t chunks = chunks_of(blocks);
+    const bool wave = blocks <= kUnitBlocks, may_split = rows <= kHeadCounters && chunks > 1;
     if (form == ROG_LOGPROB_AUTO)
-        form = may_split && rows * splits_of(blocks) <= ROG_SPLIT_MAX_GROUPS ? ROG_LOGPROB_SPLIT
-               : may_wave && rows >= ROG_WAVE_MIN_ROWS                        ? ROG_LOGPROB_WAVE
-                                                                              : ROG_LOGPROB_ROW;
-    const uint64_t groups = form == ROG_LOGPROB_SPLIT  ? rows * uint64_t(splits_of(blocks))
-                            : form == ROG_LOGPROB_WAVE ? ceil_div(rows, kHeadThreads / 64) : rows;
+        form = wave ? ROG_LOGPROB_WAVE
+               : may_split && rows * chunks <= ROG_SPLIT_MAX_GROUPS ? ROG_LOGPROB_SPLIT : ROG_LOGPROB_ROW;
+    if ((form == ROG_LOGPROB_SPLIT && !may_split) || (form == ROG_LOGPROB_WAVE) != wave) return ROG_ERR_INVALID_ARGUMENT;
+    const uint64_t groups = form == ROG_LOGPROB_SPLIT  ? rows * uint64_t(chunks)
+                            : form == ROG_LOGPROB_WAVE ? ceil_div(rows, kWaveRows) : rows;
+    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     info->form = rows ? form : ROG_LOGPROB_AUTO;
     info->blocks = blocks;
-    info->workspace_bytes = rows && form == ROG_LOGPROB_SPLIT ? kHeadCounterBytes + rows * part_bytes(blocks) : 0;
-    info->block = kHeadThreads;
-    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    info->workspace_bytes = rows && form == ROG_LOGPROB_SPLIT
+                                ? kHeadCounterBytes + rows * chunks * kChunkUnits * kUnitFloats * sizeof(float) : 0;
+    info->block = form == ROG_LOGPROB_WAVE ? 64 * kWaveRows : kHeadThreads;
     info->grid = uint32_t(groups);
     return ROG_OK;
 }
@@ -163,13 +159,13 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     a.W = uint32_t(W);
     a.rows = uint32_t(rows);
     a.blocks = blocks;
-    a.splits = splits_of(blocks);
+    a.chunks = chunks_of(blocks);
     a.top_k = uint32_t(top_k);
-    // each of the four columns has eight entries per lane in the top-k table
     a.slot_shift = 0;
-    while ((std::max(a.splits, 1u) - 1) >> a.slot_shift >= kTopSlots) ++a.slot_shift;
+    while ((a.chunks * kUnitBlocks - (blocks ? 1 : 0)) >> a.slot_shift >= kTopSlots) ++a.slot_shift;
     a.vocab = vocab;
     p->dtype = dtype;
+    p->nt_loads = rows * uint64_t(vocab) * esize(dtype) >= ROG_HEAD_NT_MIN_BYTES;
     return ROG_OK;
 }
 
@@ -225,7 +221,7 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     a.rows = uint32_t(rows);
     a.blocks = blocks;
     a.vocab = vocab;
-    a.splits = splits_of(blocks);
+    a.splits = uint32_t(ceil_div(blocks, kGradBlocks));
     const uint64_t groups = uint64_t(a.splits) * rows;
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     a.groups = p->grid = uint32_t(groups);

@@ -20,9 +20,6 @@ namespace {
 
 #pragma clang fp contract(off)
 
-#ifndef ROG_ROW_WAVES
-#define ROG_ROW_WAVES 1
-#endif
 constexpr uint32_t kWaves = kHeadThreads / 64;
 
 // Orders logits as unsigned numbers; -0 counts as +0.
@@ -40,7 +37,7 @@ template <int THREADS>
 struct Team {
     static constexpr uint32_t kThreads = THREADS;
     static constexpr uint32_t kTeamWaves = THREADS / 64;
-    static constexpr uint32_t kSlots = THREADS == 64 ? kHeadColumns : kHeadColumns * kTopSlots;   // table rows of 64 lanes
+    static constexpr uint32_t kSlots = THREADS == 64 ? kUnitBlocks : kTeamWaves * kTopSlots;     // table rows of 64 lanes
     static constexpr uint32_t kEntries = kSlots * 64;
     static constexpr uint32_t kListCap = THREADS == 64 ? 128 : 512;             // candidates held at once
     static __device__ __forceinline__ uint32_t id() { return THREADS == 64 ? threadIdx.x & 63 : threadIdx.x; }
@@ -57,9 +54,10 @@ struct Team {
 };
 
 struct Shared {
-    float m[kWaves][64], s[kWaves][64], t[kWaves][64];   // the columns' states
-    float row[4];              // ref(M), L, M, log2 entropy; written by the first wave
-    uint32_t equal;            // extreme rows: columns that equal the largest
+    float m[64], s[64], t[64];   // the states of units 64 apart, joined
+    float lane_m[kWaves][64];    // the lanes' largest logits, by wave
+    float row[4];                // m, s, t and log2 s of the row, written by the first wave
+    uint32_t equal;              // extreme rows: columns that equal the largest
     uint32_t last;
 };
 template <typename T>
@@ -90,11 +88,14 @@ struct Row {
     }
 };
 
+// Block j (in its order) of the blocks that wave w of a workgroup takes.
+__device__ __forceinline__ uint32_t wave_block(uint32_t w, uint32_t j) { return j * kChunkUnits + w; }
+
 // The block that table row `slot` holds at place i (of 1 << slot_shift).
 template <typename T>
 __device__ __forceinline__ uint32_t slot_block(uint32_t slot, uint32_t i, uint32_t shift) {
     if constexpr (T::kThreads == 64) return slot;
-    else return (((slot % kTopSlots) << shift) + i) * kHeadColumns + slot / kTopSlots;
+    else return wave_block(slot / kTopSlots, ((slot % kTopSlots) << shift) + i);
 }
 
 // The K best alternatives of a row from its table.  Called by the whole team;
@@ -104,12 +105,13 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const uint32_t tid = T::id(), K = a.top_k;
     if (tid < 64) {
-        // the K-th largest of the lanes' maxima, bit by bit
+        // the K-th largest of the lanes' maxima, bit by bit, to 16 bits (the rest zero: a little lower)
         const uint32_t o = order_of(lane_m);
         uint32_t k = 0;
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t tryk = k | 1u << bit;
-            if (uint32_t(__popcll(__ballot(o >= tryk))) >= K) k = tryk;
+#pragma unroll
+        for (int bit = 31; bit >= 16; --bit) {
+            const uint32_t higher = k | 1u << bit;
+            k = uint32_t(__popcll(__ballot(o >= higher))) >= K ? higher : k;
         }
         if (k <= kOrderMinusInf) k = kOrderMinusInf + 1;      // -inf is no alternative
         if (tid == 0) top.floor_key = uint64_t(k) << 32;
@@ -162,6 +164,7 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
     for (uint32_t q = tid; q < n; q += T::kThreads) {
         const uint64_t key = top.list[q];
         uint32_t above = 0;
+#pragma unroll 8
         for (uint32_t k = 0; k < n; ++k) above += top.list[k] > key;
         if (above < K) {
             const float x = from_order(uint32_t(key >> 32));
@@ -192,9 +195,12 @@ __device__ __forceinline__ void write_plain_row(const LogprobArgs &a, uint32_t r
     }
 }
 
-// The logit of column `tok` of a row (tok below V).
+// The logit of column `tok` of a row; 0 for a column past the end.  Read at the
+// start of a kernel and used at its end.
 template <int DT>
-__device__ __forceinline__ float token_logit(const LogprobArgs &a, uint32_t row, uint32_t tok) {
+__device__ __forceinline__ float token_logit(const LogprobArgs &a, uint32_t row, int64_t token) {
+    if (token >= int64_t(a.vocab)) return 0.0f;
+    const uint32_t tok = uint32_t(token);
     uint32_t r = 0;
     while (r + 1 < a.W && a.sh.col0[r + 1] <= tok) ++r;
     return load_logit<DT>((gbyte *)a.sh.x[r] + int64_t(row) * a.sh.stride[r] + uint64_t(tok - a.sh.col0[r]) * Logit<DT>::kSize);
@@ -216,10 +222,9 @@ __device__ __forceinline__ uint32_t count_equal(const LogprobArgs &a, uint32_t r
 // A row's numbers from the joined state of its lanes: called by the whole team,
 // with the same `all`.  equal: shared, zero.
 template <int DT, typename T, bool TOP>
-__device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, const State &all, float lane_m, float log_s,
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, float tx, const State &all, float lane_m, float log_s,
                            uint32_t &equal, typename SharedFor<T, TOP>::type &top) {
     const uint32_t tid = T::id();
-    const Scaling c{a.scale, a.bound};
     const float nan = __builtin_nanf("");
     const bool token = tok < int64_t(a.vocab);      // tok < 0 never comes here, except for tokens == NULL
     if (!(all.m < kInf)) {
@@ -231,7 +236,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
         return;
     }
     Row v;
-    v.r = c.ref(all.m);
+    v.r = all.r;
     v.l = log_s;
     v.m = all.m;
     v.lse = (v.r + v.l) * kLn2;
@@ -250,25 +255,23 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
     if (tid == 0) {
         if (a.lse) a.lse[row] = v.lse;
         if (a.entropy) a.entropy[row] = entropy;
-        if (a.logp) a.logp[row] = token ? v.logp(token_logit<DT>(a, row, uint32_t(tok)), a) : nan;
+        if (a.logp) a.logp[row] = token ? v.logp(tx, a) : nan;
     }
     if constexpr (TOP) alternatives<DT, T>(a, row, lane_m, v, top);
 }
 
-// The same from the four columns' states in shared memory, by a workgroup.
+// The same from the units' states and the lanes' maxima in shared memory, by a
+// workgroup.
 template <int DT, bool TOP>
-__device__ __forceinline__ void finish_columns(const LogprobArgs &a, uint32_t row, int64_t tok, Shared &sh,
-                               typename SharedFor<Team<kHeadThreads>, TOP>::type &top) {
+__device__ __forceinline__ void finish_units(const LogprobArgs &a, uint32_t row, int64_t tok, float tx, Shared &sh,
+                                             typename SharedFor<Team<kHeadThreads>, TOP>::type &top) {
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const Scaling c{a.scale, a.bound};
     float lane_m = -kInf;
     if (tid < 64) {
-        State st[kWaves];
-#pragma unroll
-        for (uint32_t w = 0; w < kWaves; ++w) st[w] = State{sh.m[w][lane], sh.s[w][lane], sh.t[w][lane]};
-        const State lanes = join(join(st[0], st[1], c), join(st[2], st[3], c), c);
-        lane_m = lanes.m;
-        const State all = join_lanes(lanes, c);
+        if constexpr (TOP)
+            lane_m = fmaxf(fmaxf(sh.lane_m[0][lane], sh.lane_m[1][lane]), fmaxf(sh.lane_m[2][lane], sh.lane_m[3][lane]));
+        const State all = join_lanes(make_state(sh.m[lane], sh.s[lane], sh.t[lane], c), c);
         if (tid == 0) {
             sh.row[0] = all.m;
             sh.row[1] = all.s;
@@ -278,12 +281,13 @@ __device__ __forceinline__ void finish_columns(const LogprobArgs &a, uint32_t ro
         }
     }
     __syncthreads();
-    finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, State{sh.row[0], sh.row[1], sh.row[2]}, lane_m, sh.row[3], sh.equal, top);
+    finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, tx, make_state(sh.row[0], sh.row[1], sh.row[2], c), lane_m,
+                                            sh.row[3], sh.equal, top);
 }
 
 // The state of the block at `at`, whose loads into v are in flight; then, with
 // `next` set, moves `at` on to block `b` of the row and issues its loads.
-template <int DT>
+template <int DT, bool NT>
 __device__ __forceinline__ State take_block(Cursor<DT> &cur, BlockAt &at, vec16 (&v)[Logit<DT>::kVecs], uint32_t lane,
                                             const Scaling &c, bool next, uint32_t b) {
     const uint32_t n = at.n;
@@ -291,29 +295,18 @@ __device__ __forceinline__ State take_block(Cursor<DT> &cur, BlockAt &at, vec16 
     float x[32];
     widen_block<DT>(v, x);
     if (next) at = cur.at(b);
-    load_block<DT>(at, lane, v, next);
+    load_block<DT, NT>(at, lane, v, next);
     if (n < Logit<DT>::kPerVec) return tiny_state<DT>(p, n, lane, c);
     if (n < kHeadBlock) mask_tail<DT>(n, lane, x);
     return state_of(x, c);
 }
 
-// Adds a column's j-th block (numbered within the column) to the states of its
-// chunk and of its earlier chunks; `end`: it is the column's last.
-struct Column {
-    State chunk, done;
-    __device__ __forceinline__ void add(const State &st, uint32_t j, bool end, const Scaling &c) {
-        constexpr uint32_t n = kHeadChunk / kHeadColumns;
-        chunk = j % n == 0 ? st : join(chunk, st, c);
-        if (j % n == n - 1 || end) done = j < n ? chunk : join(done, chunk, c);
-    }
-};
-
 __device__ __forceinline__ int64_t row_token(const LogprobArgs &a, uint32_t row) { return a.tokens ? a.tokens[row] : 0; }
 
-// One workgroup per row: wave w takes column w's blocks in turn, the next
-// block's loads in flight while it works on one.
-template <int DT, bool TOP>
-__global__ __launch_bounds__(kHeadThreads, ROG_ROW_WAVES) void rog_logprob_row_kernel(LogprobArgs) {
+// One workgroup per row: wave w takes unit w of every chunk, the next block's
+// loads in flight while it works on one.
+template <int DT, bool TOP, bool NT>
+__global__ __launch_bounds__(kHeadThreads) void rog_logprob_row_kernel(LogprobArgs) {
     typedef Team<kHeadThreads> T;
     const LogprobArgs &a = launch_args<LogprobArgs>();
     __shared__ Shared sh;
@@ -327,38 +320,52 @@ __global__ __launch_bounds__(kHeadThreads, ROG_ROW_WAVES) void rog_logprob_row_k
         write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
         return;
     }
+    const float tx = token_logit<DT>(a, row, tok);
+    // this wave's places in the tables
+    if (lane % kWaves == w) {
+        sh.m[lane] = -kInf;
+        sh.s[lane] = sh.t[lane] = 0.0f;
+    }
     if constexpr (TOP) {
-        // this wave's slots of the table
         for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
     }
-    Column col;
-    col.done = no_state();
-    const uint32_t mine = a.blocks > w ? (a.blocks - w + kHeadColumns - 1) / kHeadColumns : 0;
+    const uint32_t mine = a.blocks > w ? (a.blocks - w + kChunkUnits - 1) / kChunkUnits : 0;
     vec16 v[Logit<DT>::kVecs];
     Cursor<DT> cur(a.sh, row);
     BlockAt at;
+    State unit = no_state(c);
+    float lane_m = -kInf;
     if (mine) {
-        at = cur.at(w);
-        load_block<DT>(at, lane, v);
+        at = cur.at(wave_block(w, 0));
+        load_block<DT, NT>(at, lane, v);
     }
 #pragma unroll 1
     for (uint32_t j = 0; j < mine; ++j) {
-        const State st = take_block<DT>(cur, at, v, lane, c, j + 1 < mine, w + (j + 1) * kHeadColumns);
+        const State st = take_block<DT, NT>(cur, at, v, lane, c, j + 1 < mine, wave_block(w, j + 1));
         if constexpr (TOP) {
             float &e = top.tab[(w * kTopSlots + (j >> a.slot_shift)) * 64 + lane];
             e = max_nan(e, st.m);
+            lane_m = max_nan(lane_m, st.m);
         }
-        col.add(st, j, j + 1 == mine, c);
+        unit = j % kUnitBlocks == 0 ? st : join(unit, st);
+        if (j % kUnitBlocks == kUnitBlocks - 1 || j + 1 == mine) {
+            State all = join_lanes(unit, c);
+            const uint32_t u = j / kUnitBlocks * kChunkUnits + w, slot = u % 64;
+            if (u >= 64) all = join(make_state(sh.m[slot], sh.s[slot], sh.t[slot], c), all);
+            if (lane == 0) {
+                sh.m[slot] = all.m;
+                sh.s[slot] = all.s;
+                sh.t[slot] = all.t;
+            }
+        }
     }
-    sh.m[w][lane] = col.done.m;
-    sh.s[w][lane] = col.done.s;
-    sh.t[w][lane] = col.done.t;
+    if constexpr (TOP) sh.lane_m[w][lane] = lane_m;
     __syncthreads();
-    finish_columns<DT, TOP>(a, row, tok, sh, top);
+    finish_units<DT, TOP>(a, row, tok, tx, sh, top);
 }
 
-// A row over several workgroups, four blocks each, one per wave; the last one
-// of the row to finish joins the blocks' states.
+// A row over several workgroups, a chunk each, a unit per wave; the last one
+// of the row to finish joins the units' states.
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(LogprobArgs) {
     typedef Team<kHeadThreads> T;
@@ -368,104 +375,127 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
     const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
     const Scaling c{a.scale, a.bound};
     const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
-    const uint32_t row = group / a.splits, part = group % a.splits;
+    const uint32_t row = group / a.chunks, chunk = group % a.chunks;
     if (row >= a.rows) return;
+    const uint32_t first = chunk * kChunkBlocks + w;
+    const uint32_t mine = a.blocks > first ? min(kUnitBlocks, (a.blocks - first + kChunkUnits - 1) / kChunkUnits) : 0;
+    // the loads first: the token only says whether they count
+    vec16 v[Logit<DT>::kVecs];
+    Cursor<DT> cur(a.sh, row);
+    BlockAt at;
+    if (mine) {
+        at = cur.at(first);
+        load_block<DT, false>(at, lane, v);
+    }
     const int64_t tok = row_token(a, row);
     if (tok < 0) {
-        if (part == 0) write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
+        if (chunk == 0) write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
         return;
     }
-    float *const states = a.part + uint64_t(row) * a.blocks * (3 * 64) + lane;
-    const uint32_t b = part * kHeadColumns + w;
-    if (b < a.blocks) {
-        vec16 v[Logit<DT>::kVecs];
-        const BlockAt at = Cursor<DT>(a.sh, row).at(b);
-        load_block<DT>(at, lane, v);
-        float x[32];
-        widen_block<DT>(v, x);
-        State st;
-        if (at.n < Logit<DT>::kPerVec) {
-            st = tiny_state<DT>(at.p, at.n, lane, c);
-        } else {
-            if (at.n < kHeadBlock) mask_tail<DT>(at.n, lane, x);
-            st = state_of(x, c);
-        }
-        float *p = states + uint64_t(b) * (3 * 64);
-        publish(p, st.m);
-        publish(p + 64, st.s);
-        publish(p + 128, st.t);
-    }
-    if (!last_to_arrive(a.counters + row, a.splits, sh.last)) return;
-    if constexpr (TOP) {
-        for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
-    }
-    Column col;
-    col.done = no_state();
-    const uint32_t mine = a.blocks > w ? (a.blocks - w + kHeadColumns - 1) / kHeadColumns : 0;
-    for (uint32_t j0 = 0; j0 < mine; j0 += 4) {
-        State st[4];
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            if (j0 + i >= mine) continue;
-            const float *p = states + uint64_t((j0 + i) * kHeadColumns + w) * (3 * 64);
-            st[i] = State{collect(p), collect(p + 64), collect(p + 128)};
-        }
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            if (j0 + i >= mine) continue;
-            if constexpr (TOP) {
-                float &e = top.tab[(w * kTopSlots + ((j0 + i) >> a.slot_shift)) * 64 + lane];
-                e = max_nan(e, st[i].m);
+    const float tx = token_logit<DT>(a, row, tok);
+    const uint32_t units = a.chunks * kChunkUnits, u = chunk * kChunkUnits + w;
+    float *const states = a.part + uint64_t(row) * units * kUnitFloats;     // [unit][4]
+    float *const maxima = states + units * 4;                               // [unit][entry][lane]
+    // entries of a unit in the table: as many as its blocks, or fewer, wider ones
+    const uint32_t entry_shift = min(a.slot_shift, 2u), entry_log = 2 - entry_shift, entries = 1u << entry_log;
+    State unit = no_state(c);
+    float entry = -kInf;
+#pragma unroll 1
+    for (uint32_t j = 0; j < mine; ++j) {
+        const State st = take_block<DT, false>(cur, at, v, lane, c, j + 1 < mine, first + (j + 1) * kChunkUnits);
+        unit = j == 0 ? st : join(unit, st);
+        if constexpr (TOP) {
+            entry = max_nan(entry, st.m);
+            if (((j + 1) & ((1u << entry_shift) - 1)) == 0 || j + 1 == mine) {
+                publish(maxima + (u * entries + (j >> entry_shift)) * 64 + lane, entry);
+                entry = -kInf;
             }
-            col.add(st[i], j0 + i, j0 + i + 1 == mine, c);
         }
     }
-    sh.m[w][lane] = col.done.m;
-    sh.s[w][lane] = col.done.s;
-    sh.t[w][lane] = col.done.t;
+    if (mine) {
+        const State all = join_lanes(unit, c);
+        if (lane < 3) publish(states + u * 4 + lane, lane == 0 ? all.m : lane == 1 ? all.s : all.t);
+    }
+    if (!last_to_arrive(a.counters + row, a.chunks, sh.last)) return;
+    const uint32_t used = a.chunks * kChunkUnits - (a.blocks % kChunkBlocks ? max(int(kChunkUnits) - int(a.blocks % kChunkBlocks), 0) : 0);
+    if constexpr (TOP) {
+        float lane_m = -kInf;
+        for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
+        // this wave's units' entries, sixteen loads in flight
+        constexpr uint32_t kAtOnce = 16;
+        const uint32_t all = a.chunks * entries;
+        for (uint32_t k0 = 0; k0 < all; k0 += kAtOnce) {
+            float m[kAtOnce];
+#pragma unroll
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+                const uint32_t k = k0 + i, n = k >> entry_log, e = k & (entries - 1);
+                const bool real = k < all && n * kChunkBlocks + (e << entry_shift) * kChunkUnits + w < a.blocks;
+                m[i] = collect(maxima + (real ? (n * kChunkUnits + w) * entries + e : w * entries) * 64 + lane);
+                if (!real) m[i] = -kInf;
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+                const uint32_t k = k0 + i, n = k >> entry_log, e = k & (entries - 1);
+                if (k >= all) continue;
+                float &slot = top.tab[(w * kTopSlots + ((n * kUnitBlocks + (e << entry_shift)) >> a.slot_shift)) * 64 + lane];
+                slot = max_nan(slot, m[i]);
+                lane_m = max_nan(lane_m, m[i]);
+            }
+        }
+        sh.lane_m[w][lane] = lane_m;
+    }
+    if (w == 0) {
+        State st = no_state(c);
+        for (uint32_t q = lane; q < used; q += 64) {
+            const State other = make_state(collect(states + q * 4), collect(states + q * 4 + 1), collect(states + q * 4 + 2), c);
+            st = q < 64 ? other : join(st, other);
+        }
+        sh.m[lane] = st.m;
+        sh.s[lane] = st.s;
+        sh.t[lane] = st.t;
+    }
     __syncthreads();
-    finish_columns<DT, TOP>(a, row, tok, sh, top);
+    finish_units<DT, TOP>(a, row, tok, tx, sh, top);
 }
 
-// One wave per row of at most four blocks.
-template <int DT, bool TOP>
-__global__ __launch_bounds__(kHeadThreads, ROG_ROW_WAVES) void rog_logprob_wave_kernel(LogprobArgs) {
+// One wave per row of at most four blocks: a single unit.
+template <int DT, bool TOP, bool NT>
+__global__ __launch_bounds__(64 * kWaveRows) void rog_logprob_wave_kernel(LogprobArgs) {
     typedef Team<64> T;
     const LogprobArgs &a = launch_args<LogprobArgs>();
-    __shared__ uint32_t equal[kWaves];
-    __shared__ typename SharedFor<T, TOP>::type top[kWaves];
+    __shared__ uint32_t equal[kWaveRows];
+    __shared__ typename SharedFor<T, TOP>::type top[kWaveRows];
     const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
     const Scaling c{a.scale, a.bound};
-    const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kWaves + w;
+    const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kWaveRows + w;
     if (row >= a.rows) return;
     const int64_t tok = row_token(a, row);
     if (tok < 0) {
         write_plain_row(a, row, lane, 64, 0.0f, 0.0f, 0.0f, 0.0f);
         return;
     }
-    State even = no_state(), odd = no_state();         // columns 0 and 1, columns 2 and 3
+    const float tx = token_logit<DT>(a, row, tok);
+    State unit = no_state(c);
     vec16 v[Logit<DT>::kVecs];
     Cursor<DT> cur(a.sh, row);
     BlockAt at;
     if (a.blocks) {
         at = cur.at(0);
-        load_block<DT>(at, lane, v);
+        load_block<DT, NT>(at, lane, v);
     }
 #pragma unroll 1
     for (uint32_t b = 0; b < a.blocks; ++b) {
-        const State st = take_block<DT>(cur, at, v, lane, c, b + 1 < a.blocks, b + 1);
+        const State st = take_block<DT, NT>(cur, at, v, lane, c, b + 1 < a.blocks, b + 1);
         if constexpr (TOP) top[w].tab[b * 64 + lane] = st.m;
-        if (b < 2) even = b == 0 ? st : join(even, st, c);
-        else odd = b == 2 ? st : join(odd, st, c);
+        unit = b == 0 ? st : join(unit, st);
     }
     if constexpr (TOP) {
-        for (uint32_t b = a.blocks; b < kHeadColumns; ++b) top[w].tab[b * 64 + lane] = -kInf;
+        for (uint32_t b = a.blocks; b < kUnitBlocks; ++b) top[w].tab[b * 64 + lane] = -kInf;
     }
-    const State lanes = join(even, odd, c);
-    const State all = join_lanes(lanes, c);
+    const State all = join_lanes(unit, c);
     if (lane == 0) equal[w] = 0;
     T::sync();
-    finish_row<DT, T, TOP>(a, row, tok, all, lanes.m, log2f(all.s), equal[w], top[w]);
+    finish_row<DT, T, TOP>(a, row, tok, tx, all, unit.m, log2f(all.s), equal[w], top[w]);
 }
 
 template <typename K>
@@ -473,11 +503,15 @@ const void *kfn(K *k) { return reinterpret_cast<const void *>(k); }
 
 template <int DT>
 const void *logprob_kernel(const LogprobPlan &p) {
-    const bool top = p.args.top_ids || p.args.top_logp;
+    const bool top = p.args.top_ids || p.args.top_logp, nt = p.nt_loads;
     switch (p.info.form) {
     case ROG_LOGPROB_SPLIT: return top ? kfn(&rog_logprob_split_kernel<DT, true>) : kfn(&rog_logprob_split_kernel<DT, false>);
-    case ROG_LOGPROB_WAVE: return top ? kfn(&rog_logprob_wave_kernel<DT, true>) : kfn(&rog_logprob_wave_kernel<DT, false>);
-    default: return top ? kfn(&rog_logprob_row_kernel<DT, true>) : kfn(&rog_logprob_row_kernel<DT, false>);
+    case ROG_LOGPROB_WAVE:
+        return top ? (nt ? kfn(&rog_logprob_wave_kernel<DT, true, true>) : kfn(&rog_logprob_wave_kernel<DT, true, false>))
+                   : (nt ? kfn(&rog_logprob_wave_kernel<DT, false, true>) : kfn(&rog_logprob_wave_kernel<DT, false, false>));
+    default:
+        return top ? (nt ? kfn(&rog_logprob_row_kernel<DT, true, true>) : kfn(&rog_logprob_row_kernel<DT, true, false>))
+                   : (nt ? kfn(&rog_logprob_row_kernel<DT, false, true>) : kfn(&rog_logprob_row_kernel<DT, false, false>));
     }
 }
 

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobG
     const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
     const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
     if (group >= a.groups) return;
-    const uint32_t row = group / a.splits, b = group % a.splits * 4 + w;
+    const uint32_t row = group / a.splits, b = group % a.splits * kGradBlocks + w;
     if (b >= a.blocks) return;
     const BlockAt at = Cursor<DT>(a.sh, row).at(b);
     typedef __attribute__((address_space(1))) uint8_t gout;
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobG
         for (int i = 0; i < 32; ++i) x[i] = 0.0f;
     } else {
         vec16 v[vecs];
-        load_block<DT>(at, lane, v);
+        load_block<DT, false>(at, lane, v);
         const bool tiny = at.n < per;
         if (tiny) v[0] = load_tiny<DT>(at.p, at.n);
         widen_block<DT>(v, x);

@@ -349,10 +349,10 @@ typedef struct {
 typedef enum {
     ROG_LOGPROB_AUTO = 0,
     ROG_LOGPROB_ROW = 1,       /* one workgroup per row                           */
-    ROG_LOGPROB_SPLIT = 2,     /* one workgroup per 8192 columns of a row, the last
-                                  of a row to finish joins its parts              */
-    ROG_LOGPROB_WAVE = 3       /* one wave per row (rows of at most four blocks of
-                                  2048 columns)                                   */
+    ROG_LOGPROB_SPLIT = 2,     /* one workgroup per 16 blocks of a row, the last of a
+                                  row to finish joins them (rows of more blocks)  */
+    ROG_LOGPROB_WAVE = 3       /* one wave per row: all rows of at most 4 blocks, and
+                                  no others                                       */
 } rog_logprob_form;
 
 /* The launch a call would make. */
@@ -372,7 +372,7 @@ typedef struct {
  *
  * tokens   device array of `rows` columns, or NULL (then out->logp must be NULL
  *          and every row is scored).  A row whose token is negative is not
- *          scored and not read: 0 in logp, entropy, lse and top_logp, -1 in
+ *          scored, whatever its logits: 0 in logp, entropy, lse and top_logp, -1 in
  *          top_ids.  A token of V or more: the row's logp is NaN.
  * top_k    0 .. rog_max_top_k().
  *
