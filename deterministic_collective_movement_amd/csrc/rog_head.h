@@ -43,7 +43,7 @@ constexpr uint32_t kTopSlots = 8;          // entries per lane and wave in the t
 
 // Tunables, measured on MI355X; a variant build may override one with -D.
 #ifndef ROG_SPLIT_MAX_GROUPS
-#define ROG_SPLIT_MAX_GROUPS 1024
+#define ROG_SPLIT_MAX_GROUPS 3072
 #endif
 #ifndef ROG_HEAD_NT_MIN_BYTES
 #define ROG_HEAD_NT_MIN_BYTES (128ull << 20)
@@ -54,10 +54,15 @@ constexpr uint32_t kTopSlots = 8;          // entries per lane and wave in the t
 constexpr uint32_t kWaveRows = ROG_WAVE_ROWS;   // rows (waves) of a workgroup of the one-wave-per-row form
 constexpr uint32_t kMaxVocab = 1u << 31;   // columns of a row: below this
 
-// The front of a workspace: one arrival counter per row of a split launch (the
-// first one for the policy loss), zero between calls.  Partial states follow.
-constexpr uint32_t kHeadCounters = 4096;
-constexpr size_t kHeadCounterBytes = kHeadCounters * sizeof(uint32_t);
+// The front of a workspace: arrival counters, zero between calls, each in a
+// 128-byte line of its own (counters that share a line are counted one after
+// the other: 64 rows of 131072 columns took 12.2 us with their counters packed,
+// 8.9 apart).  A split launch counts row r's workgroups in counter r; the
+// policy loss counts in counters 1 and on, and those in counter 0.  Partial
+// states follow.
+constexpr uint32_t kHeadCounters = 1024;
+constexpr uint32_t kCounterStride = 128 / sizeof(uint32_t);
+constexpr size_t kHeadCounterBytes = size_t(kHeadCounters) * kCounterStride * sizeof(uint32_t);
 
 // Floats of a split row's partial states: m, s, t of each unit (padded to 4),
 // then 64 lanes' maxima for each of four entries per unit.
@@ -82,7 +87,7 @@ struct LogprobArgs {
     float inv_t;                       // 1 / temperature
     float bound;                       // |x| beyond this leaves the scaled range
     uint32_t W, rows, blocks;
-    uint32_t chunks;
+    uint32_t chunks, units;            // units that have blocks
     uint32_t top_k;
     uint32_t slot_shift;               // log2 of a wave's blocks that one entry of the top-k table covers
     uint32_t vocab;
@@ -110,6 +115,7 @@ struct PolicyArgs {
     float ratio_lo, ratio_hi;          // e^lo, e^hi
     float kl_coef, entropy_coef, grad_scale, w_all;
     uint32_t groups;
+    uint32_t tiles;                    // tiles per workgroup
 };
 
 static_assert(sizeof(LogprobArgs) <= 4096 && sizeof(LogprobGradArgs) <= 4096, "kernel arguments stay below 4 KiB");
@@ -129,8 +135,16 @@ struct PolicyPlan {
     PolicyArgs args;
 };
 
-// Tokens of one workgroup of the policy loss.
-constexpr uint32_t kPolicyGroup = 2048;
+// The policy loss: tiles of 1024 tokens, four per thread of a workgroup; up to
+// kPolicyGroups workgroups, each with a run of consecutive tiles.  With more
+// than kPolicyRoots of them, workgroup g counts itself in counter
+// 1 + g mod kPolicyRoots, and the last of those in counter 0.
+constexpr uint32_t kPolicyTile = 1024;
+#ifndef ROG_POLICY_GROUPS
+#define ROG_POLICY_GROUPS 512
+#endif
+constexpr uint32_t kPolicyGroups = ROG_POLICY_GROUPS;
+constexpr uint32_t kPolicyRoots = 16;
 
 // Validate and plan (no HIP calls).
 rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype, float temperature,

@@ -82,25 +82,30 @@ rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dty
     return rows >= kMaxVocab ? ROG_ERR_TOO_LARGE : ROG_OK;
 }
 
+// Units that have blocks, of a row of more than one.
+inline uint32_t units_of(uint32_t blocks) {
+    const uint32_t rest = blocks % kChunkBlocks;
+    return blocks / kChunkBlocks * kChunkUnits + std::min(rest, kChunkUnits);
+}
 inline uint32_t chunks_of(uint32_t blocks) { return uint32_t(ceil_div(blocks, kChunkBlocks)); }
 
 // Launch form, grid and workspace of rog_logprob.
 rog_status choose_form(uint32_t blocks, size_t rows, int top_k, rog_logprob_form form, rog_head_plan_info *info) {
     if (form < ROG_LOGPROB_AUTO || form > ROG_LOGPROB_WAVE || top_k < 0 || top_k > kMaxTopK)
         return ROG_ERR_INVALID_ARGUMENT;
-    const uint32_t chunks = chunks_of(blocks);
-    const bool wave = blocks <= kUnitBlocks, may_split = rows <= kHeadCounters && chunks > 1;
+    const uint32_t units = units_of(blocks);
+    const bool wave = blocks <= kUnitBlocks, may_split = rows <= kHeadCounters && !wave;
     if (form == ROG_LOGPROB_AUTO)
         form = wave ? ROG_LOGPROB_WAVE
-               : may_split && rows * chunks <= ROG_SPLIT_MAX_GROUPS ? ROG_LOGPROB_SPLIT : ROG_LOGPROB_ROW;
+               : may_split && rows * units <= ROG_SPLIT_MAX_GROUPS ? ROG_LOGPROB_SPLIT : ROG_LOGPROB_ROW;
     if ((form == ROG_LOGPROB_SPLIT && !may_split) || (form == ROG_LOGPROB_WAVE) != wave) return ROG_ERR_INVALID_ARGUMENT;
-    const uint64_t groups = form == ROG_LOGPROB_SPLIT  ? rows * uint64_t(chunks)
+    const uint64_t groups = form == ROG_LOGPROB_SPLIT  ? rows * uint64_t(units)
                             : form == ROG_LOGPROB_WAVE ? ceil_div(rows, kWaveRows) : rows;
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     info->form = rows ? form : ROG_LOGPROB_AUTO;
     info->blocks = blocks;
     info->workspace_bytes = rows && form == ROG_LOGPROB_SPLIT
-                                ? kHeadCounterBytes + rows * chunks * kChunkUnits * kUnitFloats * sizeof(float) : 0;
+                                ? kHeadCounterBytes + rows * units * kUnitFloats * sizeof(float) : 0;
     info->block = form == ROG_LOGPROB_WAVE ? 64 * kWaveRows : kHeadThreads;
     info->grid = uint32_t(groups);
     return ROG_OK;
@@ -160,6 +165,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     a.rows = uint32_t(rows);
     a.blocks = blocks;
     a.chunks = chunks_of(blocks);
+    a.units = units_of(blocks);
     a.top_k = uint32_t(top_k);
     a.slot_shift = 0;
     while ((a.chunks * kUnitBlocks - (blocks ? 1 : 0)) >> a.slot_shift >= kTopSlots) ++a.slot_shift;
@@ -230,9 +236,17 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
 }
 
 namespace {
-uint64_t policy_groups(uint64_t n) { return std::max<uint64_t>(1, ceil_div(n, kPolicyGroup)); }
+// Tiles per workgroup and workgroups: the order of the sums hangs on them, so
+// both go by n alone.
+struct PolicySplit {
+    uint64_t tiles, groups;
+};
+PolicySplit policy_split(uint64_t n) {
+    const uint64_t all = std::max<uint64_t>(1, ceil_div(n, kPolicyTile)), tiles = ceil_div(all, kPolicyGroups);
+    return PolicySplit{tiles, ceil_div(all, tiles)};
+}
 size_t policy_workspace(uint64_t n) {
-    const uint64_t g = policy_groups(n);
+    const uint64_t g = policy_split(n).groups;
     return g <= 1 ? 0 : kHeadCounterBytes + g * 4 * sizeof(double);
 }
 }  // namespace
@@ -287,7 +301,8 @@ rog_status plan_policy(const rog_policy_in *in, size_t n, const rog_policy_param
     a.entropy_coef = k->entropy_coef;
     a.grad_scale = k->grad_scale;
     a.w_all = n ? float(1.0 / double(n)) : 0.0f;
-    a.groups = uint32_t(policy_groups(n));   // n < 2^34: at most 2^23
+    a.tiles = uint32_t(policy_split(n).tiles);   // n < 2^34: at most 2^15
+    a.groups = uint32_t(policy_split(n).groups);
     return ROG_OK;
 }
 

@@ -56,10 +56,53 @@ struct Team {
 struct Shared {
     float m[64], s[64], t[64];   // the states of units 64 apart, joined
     float lane_m[kWaves][64];    // the lanes' largest logits, by wave
+    float lane_s[kWaves][64], lane_t[kWaves][64];   // split: with them, the states of a unit's blocks
     float row[4];                // m, s, t and log2 s of the row, written by the first wave
     uint32_t equal;              // extreme rows: columns that equal the largest
     uint32_t last;
 };
+// Where a row's blocks are, for lanes that each look for another: per shard for a
+// workgroup's row, per block for a wave's (at most four).
+template <int THREADS>
+struct Places {
+    uint64_t x[kMaxPeers];         // element (0, 0)
+    int64_t stride[kMaxPeers];
+    uint32_t width[kMaxPeers], col0[kMaxPeers], block0[kMaxPeers];
+    // by one wave, lane r bringing shard r; the LDS writes wait for the kernel arguments
+    __device__ __forceinline__ void fill(const LogprobArgs &a, uint32_t lane) {
+        if (lane < a.W) {
+            x[lane] = reinterpret_cast<uint64_t>(a.sh.x[lane]);
+            stride[lane] = a.sh.stride[lane];
+            width[lane] = a.sh.width[lane];
+            col0[lane] = a.sh.col0[lane];
+            block0[lane] = a.sh.block0[lane];
+        }
+    }
+    template <int DT>
+    __device__ __forceinline__ BlockAt at(const LogprobArgs &a, uint32_t row, uint32_t b) const {
+        uint32_t r = 0;            // the last shard that begins at or before block b
+        for (uint32_t step = kMaxPeers / 2; step; step /= 2)
+            if (step < a.W && r + step < a.W && block0[r + step] <= b) r += step;
+        const uint32_t off = (b - block0[r]) * kHeadBlock, left = width[r] - off;
+        return BlockAt{(gbyte *)(x[r] + uint64_t(int64_t(row) * stride[r]) + uint64_t(off) * Logit<DT>::kSize),
+                       left < kHeadBlock ? left : kHeadBlock, col0[r] + off, r, off};
+    }
+};
+template <>
+struct Places<64> {
+    uint64_t p[kUnitBlocks];
+    uint32_t n[kUnitBlocks], col[kUnitBlocks];
+    __device__ __forceinline__ void set(uint32_t b, const BlockAt &at) {
+        p[b] = reinterpret_cast<uint64_t>((const uint8_t *)at.p);
+        n[b] = at.n;
+        col[b] = at.col;
+    }
+    template <int DT>
+    __device__ __forceinline__ BlockAt at(const LogprobArgs &, uint32_t, uint32_t b) const {
+        return BlockAt{(gbyte *)p[b], n[b], col[b], 0, 0};
+    }
+};
+
 template <typename T>
 struct SharedTop {
     float tab[T::kEntries];    // [slot][lane]: largest logit of the slot's blocks in the lane's columns
@@ -67,6 +110,7 @@ struct SharedTop {
     uint64_t floor_key;        // candidates are at or above it
     uint32_t hit_count, count;
     uint16_t hits[T::kEntries];
+    Places<int(T::kThreads)> places;
 };
 struct Nothing {};
 template <typename T, bool TOP> struct SharedFor { typedef Nothing type; };
@@ -98,31 +142,36 @@ __device__ __forceinline__ uint32_t slot_block(uint32_t slot, uint32_t i, uint32
     else return wave_block(slot / kTopSlots, ((slot % kTopSlots) << shift) + i);
 }
 
-// The K best alternatives of a row from its table.  Called by the whole team;
-// lane_m: in the first wave, the lane's largest logit in the row.
+// Sets the first floor of the candidates, by one wave: the K-th largest of the
+// 64 lanes' largest logits, bit by bit, to 16 bits (the rest zero: a little lower).
+template <typename T>
+__device__ __forceinline__ void set_floor(float lane_m, uint32_t K, SharedTop<T> &top) {
+    const uint32_t o = order_of(lane_m);
+    uint32_t k = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t higher = k | 1u << bit;
+        k = uint32_t(__popcll(__ballot(o >= higher))) >= K ? higher : k;
+    }
+    if (k <= kOrderMinusInf) k = kOrderMinusInf + 1;      // -inf is no alternative
+    if ((threadIdx.x & 63) == 0) {
+        top.floor_key = uint64_t(k) << 32;
+        top.hit_count = top.count = 0;
+    }
+}
+
+// The K best alternatives of a row from its table.  Called by the whole team,
+// after set_floor.
 template <int DT, typename T>
-__device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row, float lane_m, const Row &v, SharedTop<T> &top) {
+__device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row, const Row &v, SharedTop<T> &top) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const uint32_t tid = T::id(), K = a.top_k;
-    if (tid < 64) {
-        // the K-th largest of the lanes' maxima, bit by bit, to 16 bits (the rest zero: a little lower)
-        const uint32_t o = order_of(lane_m);
-        uint32_t k = 0;
-#pragma unroll
-        for (int bit = 31; bit >= 16; --bit) {
-            const uint32_t higher = k | 1u << bit;
-            k = uint32_t(__popcll(__ballot(o >= higher))) >= K ? higher : k;
-        }
-        if (k <= kOrderMinusInf) k = kOrderMinusInf + 1;      // -inf is no alternative
-        if (tid == 0) top.floor_key = uint64_t(k) << 32;
-    }
     const uint32_t shift = T::kThreads == 64 ? 0 : a.slot_shift;
     uint32_t n;
     for (;;) {
-        if (tid == 0) top.hit_count = top.count = 0;
-        T::sync();
         const uint64_t floor_key = top.floor_key;
         const float floor_x = from_order(uint32_t(floor_key >> 32));
+#pragma unroll
         for (uint32_t e = tid; e < T::kEntries; e += T::kThreads)
             if (top.tab[e] >= floor_x) top.hits[atomicAdd(&top.hit_count, 1u)] = uint16_t(e);
         T::sync();
@@ -132,7 +181,7 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
             const uint32_t e = top.hits[q >> vecs_shift], i = uint32_t(q) & ((1u << vecs_shift) - 1);
             const uint32_t b = slot_block<T>(e / 64, i / Logit<DT>::kVecs, shift), el = e % 64;
             if (b >= a.blocks) continue;
-            const BlockAt at = Cursor<DT>(a.sh, row).at(b);
+            const BlockAt at = top.places.template at<DT>(a, row, b);
             const uint32_t vi = i % Logit<DT>::kVecs;
             const vec16 vec = load_vec<DT>(at.p, at.n, vi, el);
             float x[per];
@@ -150,6 +199,7 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
         T::sync();
         n = top.count;
         if (n <= T::kListCap) break;
+        T::sync();
         // More columns reach the floor than the list holds (many equal logits):
         // the K-th best of those listed is a higher floor that K columns reach.
         // It rises with every turn, since the list holds more than K.
@@ -159,6 +209,7 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
             for (uint32_t k = 0; k < T::kListCap; ++k) above += top.list[k] > key;
             if (above == K - 1) top.floor_key = key;
         }
+        if (tid == 0) top.hit_count = top.count = 0;
         T::sync();
     }
     for (uint32_t q = tid; q < n; q += T::kThreads) {
@@ -222,7 +273,7 @@ __device__ __forceinline__ uint32_t count_equal(const LogprobArgs &a, uint32_t r
 // A row's numbers from the joined state of its lanes: called by the whole team,
 // with the same `all`.  equal: shared, zero.
 template <int DT, typename T, bool TOP>
-__device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, float tx, const State &all, float lane_m, float log_s,
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, float tx, const State &all, float log_s,
                            uint32_t &equal, typename SharedFor<T, TOP>::type &top) {
     const uint32_t tid = T::id();
     const float nan = __builtin_nanf("");
@@ -257,7 +308,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
         if (a.entropy) a.entropy[row] = entropy;
         if (a.logp) a.logp[row] = token ? v.logp(tx, a) : nan;
     }
-    if constexpr (TOP) alternatives<DT, T>(a, row, lane_m, v, top);
+    if constexpr (TOP) alternatives<DT, T>(a, row, v, top);
 }
 
 // The same from the units' states and the lanes' maxima in shared memory, by a
@@ -267,10 +318,7 @@ __device__ __forceinline__ void finish_units(const LogprobArgs &a, uint32_t row,
                                              typename SharedFor<Team<kHeadThreads>, TOP>::type &top) {
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const Scaling c{a.scale, a.bound};
-    float lane_m = -kInf;
     if (tid < 64) {
-        if constexpr (TOP)
-            lane_m = fmaxf(fmaxf(sh.lane_m[0][lane], sh.lane_m[1][lane]), fmaxf(sh.lane_m[2][lane], sh.lane_m[3][lane]));
         const State all = join_lanes(make_state(sh.m[lane], sh.s[lane], sh.t[lane], c), c);
         if (tid == 0) {
             sh.row[0] = all.m;
@@ -279,10 +327,14 @@ __device__ __forceinline__ void finish_units(const LogprobArgs &a, uint32_t row,
             sh.row[3] = log2f(all.s);
             sh.equal = 0;
         }
+    } else if (TOP && tid < 128) {
+        if constexpr (TOP)
+            set_floor(fmaxf(fmaxf(sh.lane_m[0][lane], sh.lane_m[1][lane]), fmaxf(sh.lane_m[2][lane], sh.lane_m[3][lane])),
+                      a.top_k, top);
     }
     __syncthreads();
-    finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, tx, make_state(sh.row[0], sh.row[1], sh.row[2], c), lane_m,
-                                            sh.row[3], sh.equal, top);
+    finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, tx, make_state(sh.row[0], sh.row[1], sh.row[2], c), sh.row[3],
+                                            sh.equal, top);
 }
 
 // The state of the block at `at`, whose loads into v are in flight; then, with
@@ -339,6 +391,9 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_row_kernel(LogprobAr
         at = cur.at(wave_block(w, 0));
         load_block<DT, NT>(at, lane, v);
     }
+    if constexpr (TOP) {
+        if (w == 0) top.places.fill(a, lane);
+    }
 #pragma unroll 1
     for (uint32_t j = 0; j < mine; ++j) {
         const State st = take_block<DT, NT>(cur, at, v, lane, c, j + 1 < mine, wave_block(w, j + 1));
@@ -364,8 +419,8 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_row_kernel(LogprobAr
     finish_units<DT, TOP>(a, row, tok, tx, sh, top);
 }
 
-// A row over several workgroups, a chunk each, a unit per wave; the last one
-// of the row to finish joins the units' states.
+// A row over several workgroups, a unit each, a block per wave; the last one of
+// the row to finish joins the units' states.
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(LogprobArgs) {
     typedef Team<kHeadThreads> T;
@@ -375,84 +430,92 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
     const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
     const Scaling c{a.scale, a.bound};
     const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
-    const uint32_t row = group / a.chunks, chunk = group % a.chunks;
+    const uint32_t row = group / a.units, u = group % a.units;
     if (row >= a.rows) return;
-    const uint32_t first = chunk * kChunkBlocks + w;
-    const uint32_t mine = a.blocks > first ? min(kUnitBlocks, (a.blocks - first + kChunkUnits - 1) / kChunkUnits) : 0;
+    const uint32_t first = u / kChunkUnits * kChunkBlocks + u % kChunkUnits, b = first + w * kChunkUnits;
     // the loads first: the token only says whether they count
     vec16 v[Logit<DT>::kVecs];
     Cursor<DT> cur(a.sh, row);
     BlockAt at;
-    if (mine) {
-        at = cur.at(first);
+    if (b < a.blocks) {
+        at = cur.at(b);
         load_block<DT, false>(at, lane, v);
     }
     const int64_t tok = row_token(a, row);
     if (tok < 0) {
-        if (chunk == 0) write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
+        if (u == 0) write_plain_row(a, row, tid, kHeadThreads, 0.0f, 0.0f, 0.0f, 0.0f);
         return;
     }
     const float tx = token_logit<DT>(a, row, tok);
-    const uint32_t units = a.chunks * kChunkUnits, u = chunk * kChunkUnits + w;
-    float *const states = a.part + uint64_t(row) * units * kUnitFloats;     // [unit][4]
-    float *const maxima = states + units * 4;                               // [unit][entry][lane]
+    float *const states = a.part + uint64_t(row) * a.units * kUnitFloats;   // [unit][4]
+    float *const maxima = states + a.units * 4;                             // [unit][entry][lane]
     // entries of a unit in the table: as many as its blocks, or fewer, wider ones
     const uint32_t entry_shift = min(a.slot_shift, 2u), entry_log = 2 - entry_shift, entries = 1u << entry_log;
-    State unit = no_state(c);
-    float entry = -kInf;
-#pragma unroll 1
-    for (uint32_t j = 0; j < mine; ++j) {
-        const State st = take_block<DT, false>(cur, at, v, lane, c, j + 1 < mine, first + (j + 1) * kChunkUnits);
-        unit = j == 0 ? st : join(unit, st);
-        if constexpr (TOP) {
-            entry = max_nan(entry, st.m);
-            if (((j + 1) & ((1u << entry_shift) - 1)) == 0 || j + 1 == mine) {
-                publish(maxima + (u * entries + (j >> entry_shift)) * 64 + lane, entry);
-                entry = -kInf;
-            }
-        }
-    }
-    if (mine) {
+    State st = no_state(c);
+    if (b < a.blocks) st = take_block<DT, false>(cur, at, v, lane, c, false, 0);
+    sh.lane_m[w][lane] = st.m;
+    sh.lane_s[w][lane] = st.s;
+    sh.lane_t[w][lane] = st.t;
+    __syncthreads();
+    if (w == 0) {
+        State unit = st;
+#pragma unroll
+        for (uint32_t i = 1; i < kUnitBlocks; ++i)
+            if (first + i * kChunkUnits < a.blocks)
+                unit = join(unit, make_state(sh.lane_m[i][lane], sh.lane_s[i][lane], sh.lane_t[i][lane], c));
         const State all = join_lanes(unit, c);
         if (lane < 3) publish(states + u * 4 + lane, lane == 0 ? all.m : lane == 1 ? all.s : all.t);
+    } else if (TOP && w == 1) {
+        for (uint32_t e = 0; e < entries; ++e) {
+            float m = sh.lane_m[e << entry_shift][lane];
+            for (uint32_t i = 1; i < 1u << entry_shift; ++i) m = max_nan(m, sh.lane_m[(e << entry_shift) + i][lane]);
+            publish(maxima + (u * entries + e) * 64 + lane, m);
+        }
     }
-    if (!last_to_arrive(a.counters + row, a.chunks, sh.last)) return;
-    const uint32_t used = a.chunks * kChunkUnits - (a.blocks % kChunkBlocks ? max(int(kChunkUnits) - int(a.blocks % kChunkBlocks), 0) : 0);
+    if (!last_to_arrive(a.counters + row * kCounterStride, a.units, sh.last)) return;
+    // one round trip: the first 64 units' states, and of the maxima as many as the table has entries
+    float jm = -kInf, js = 0.0f, jt = 0.0f;
+    if (w == 0 && lane < a.units) {
+        jm = collect(states + lane * 4);
+        js = collect(states + lane * 4 + 1);
+        jt = collect(states + lane * 4 + 2);
+    }
     if constexpr (TOP) {
         float lane_m = -kInf;
-        for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
-        // this wave's units' entries, sixteen loads in flight
-        constexpr uint32_t kAtOnce = 16;
-        const uint32_t all = a.chunks * entries;
-        for (uint32_t k0 = 0; k0 < all; k0 += kAtOnce) {
-            float m[kAtOnce];
+        const uint32_t all = a.chunks * entries;      // this wave's units' entries
+        const bool alone = a.slot_shift <= 2;         // one entry per slot of the table
+        if (!alone) {
+            for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
+        }
+        for (uint32_t k0 = 0; k0 < all || k0 == 0; k0 += kTopSlots) {
+            float m[kTopSlots];
 #pragma unroll
-            for (uint32_t i = 0; i < kAtOnce; ++i) {
-                const uint32_t k = k0 + i, n = k >> entry_log, e = k & (entries - 1);
-                const bool real = k < all && n * kChunkBlocks + (e << entry_shift) * kChunkUnits + w < a.blocks;
-                m[i] = collect(maxima + (real ? (n * kChunkUnits + w) * entries + e : w * entries) * 64 + lane);
-                if (!real) m[i] = -kInf;
+            for (uint32_t i = 0; i < kTopSlots; ++i) {
+                const uint32_t k = k0 + i, q = (k >> entry_log) * kChunkUnits + w;
+                m[i] = -kInf;
+                if (k < all && q < a.units) m[i] = collect(maxima + (q * entries + (k & (entries - 1))) * 64 + lane);
             }
 #pragma unroll
-            for (uint32_t i = 0; i < kAtOnce; ++i) {
-                const uint32_t k = k0 + i, n = k >> entry_log, e = k & (entries - 1);
-                if (k >= all) continue;
-                float &slot = top.tab[(w * kTopSlots + ((n * kUnitBlocks + (e << entry_shift)) >> a.slot_shift)) * 64 + lane];
-                slot = max_nan(slot, m[i]);
+            for (uint32_t i = 0; i < kTopSlots; ++i) {
                 lane_m = max_nan(lane_m, m[i]);
+                if (alone) {
+                    top.tab[(w * kTopSlots + i) * 64 + lane] = m[i];
+                } else if (k0 + i < all) {
+                    float &slot = top.tab[(w * kTopSlots + (((k0 + i) << entry_shift) >> a.slot_shift)) * 64 + lane];
+                    slot = max_nan(slot, m[i]);
+                }
             }
         }
         sh.lane_m[w][lane] = lane_m;
+        if (w == 1) top.places.fill(a, lane);
     }
     if (w == 0) {
-        State st = no_state(c);
-        for (uint32_t q = lane; q < used; q += 64) {
-            const State other = make_state(collect(states + q * 4), collect(states + q * 4 + 1), collect(states + q * 4 + 2), c);
-            st = q < 64 ? other : join(st, other);
-        }
-        sh.m[lane] = st.m;
-        sh.s[lane] = st.s;
-        sh.t[lane] = st.t;
+        State joined = make_state(jm, js, jt, c);
+        for (uint32_t q = lane + 64; q < a.units; q += 64)
+            joined = join(joined, make_state(collect(states + q * 4), collect(states + q * 4 + 1), collect(states + q * 4 + 2), c));
+        sh.m[lane] = joined.m;
+        sh.s[lane] = joined.s;
+        sh.t[lane] = joined.t;
     }
     __syncthreads();
     finish_units<DT, TOP>(a, row, tok, tx, sh, top);
@@ -485,6 +548,9 @@ __global__ __launch_bounds__(64 * kWaveRows) void rog_logprob_wave_kernel(Logpro
     }
 #pragma unroll 1
     for (uint32_t b = 0; b < a.blocks; ++b) {
+        if constexpr (TOP) {
+            if (lane == 0) top[w].places.set(b, at);
+        }
         const State st = take_block<DT, NT>(cur, at, v, lane, c, b + 1 < a.blocks, b + 1);
         if constexpr (TOP) top[w].tab[b * 64 + lane] = st.m;
         unit = b == 0 ? st : join(unit, st);
@@ -494,8 +560,9 @@ __global__ __launch_bounds__(64 * kWaveRows) void rog_logprob_wave_kernel(Logpro
     }
     const State all = join_lanes(unit, c);
     if (lane == 0) equal[w] = 0;
+    if constexpr (TOP) set_floor(unit.m, a.top_k, top[w]);
     T::sync();
-    finish_row<DT, T, TOP>(a, row, tok, tx, all, unit.m, log2f(all.s), equal[w], top[w]);
+    finish_row<DT, T, TOP>(a, row, tok, tx, all, log2f(all.s), equal[w], top[w]);
 }
 
 template <typename K>

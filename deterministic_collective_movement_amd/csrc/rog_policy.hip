@@ -2,9 +2,10 @@
 // entry point that launches it.
 //
 // Per token: d = logp - old, l = -A e^{clipped ? bound : d} + beta (e^q - 1 - q)
-// - c_H H and its derivative.  A workgroup takes 2048 tokens, eight per thread,
-// and sums its four totals in binary64 over a fixed tree; the last workgroup to
-// finish joins the workgroups' totals in their order.  Bandwidth bound: 24
+// - c_H H and its derivative.  A workgroup takes a run of tiles of 1024 tokens,
+// four tokens per thread, and sums its four totals in binary64 over a fixed
+// tree; the last workgroup to finish joins the workgroups' totals in their
+// order.  Bandwidth bound: 24
 // bytes read and 8 written per token with every term.
 #include <hip/hip_runtime.h>
 
@@ -22,21 +23,32 @@ typedef const __attribute__((address_space(1))) f32x4u gvec;
 typedef __attribute__((address_space(1))) float gfloat_out;
 typedef __attribute__((address_space(1))) f32x4u gvec_out;
 
-// e^q - 1 - q without cancellation: its Taylor series to q^9 / 9! for |q| <= 1/2
-// (what is left out is below 2^-27 of the sum), e^q - 1 - q in binary64 beyond.
-__device__ __forceinline__ float kl_term(float q) {
-    if (fabsf(q) <= 0.5f) {
-        float p = 1.0f / 362880.0f;
-        p = __builtin_fmaf(p, q, 1.0f / 40320.0f);
-        p = __builtin_fmaf(p, q, 1.0f / 5040.0f);
-        p = __builtin_fmaf(p, q, 1.0f / 720.0f);
-        p = __builtin_fmaf(p, q, 1.0f / 120.0f);
-        p = __builtin_fmaf(p, q, 1.0f / 24.0f);
-        p = __builtin_fmaf(p, q, 1.0f / 6.0f);
-        p = __builtin_fmaf(p, q, 0.5f);
-        return p * q * q;
-    }
-    return float(double(expf(q)) - 1.0 - double(q));
+// e^x: 2^(x log2 e), the product's rounding put back as a factor (e^x to about
+// two units in the last place; results below 2^-126 are zero).
+__device__ __forceinline__ float exp_of(float x) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;      // log2 e
+    const float y = x * kHi;
+    const float e = exp2_fast(y);
+    const float rest = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -y));
+    return fabsf(x) < 100.0f ? __builtin_fmaf(e, rest * kLn2, e) : e;
+}
+
+// kl = e^q - 1 - q and grow = e^q - 1 without cancellation: the Taylor series of
+// kl to q^9 / 9! for |q| <= 1/2 (what is left out is below 2^-27 of it), the
+// exponential beyond.
+__device__ __forceinline__ void kl_of(float q, float &kl, float &grow) {
+    float p = 1.0f / 362880.0f;
+    p = __builtin_fmaf(p, q, 1.0f / 40320.0f);
+    p = __builtin_fmaf(p, q, 1.0f / 5040.0f);
+    p = __builtin_fmaf(p, q, 1.0f / 720.0f);
+    p = __builtin_fmaf(p, q, 1.0f / 120.0f);
+    p = __builtin_fmaf(p, q, 1.0f / 24.0f);
+    p = __builtin_fmaf(p, q, 1.0f / 6.0f);
+    p = __builtin_fmaf(p, q, 0.5f);
+    const float series = p * q * q, far = exp_of(q) - 1.0f;
+    const bool near = fabsf(q) <= 0.5f;
+    kl = near ? series : far - q;
+    grow = near ? series + q : far;
 }
 
 struct Totals {
@@ -65,75 +77,104 @@ __device__ __forceinline__ Totals group_sum(Totals t, double (&sh)[4][4]) {
     return t;
 }
 
-__device__ __forceinline__ f32x4 load4(const float *p, uint64_t at, uint32_t n, float none) {
-    f32x4 v = {none, none, none, none};
-    if (!p) return v;
-    gfloat *q = (gfloat *)p + at;
+// Four tokens of a thread, as loaded.
+struct Four {
+    f32x4 logp, old, adv, w, ref, ent;
+};
+
+// A thread's four tokens start at `at`; where that runs past n they are read
+// from n - 4, and the first at - (n - 4) of them are other threads' (they may
+// be overwritten meanwhile where gradients go in place, and are not used).
+// Fewer than four tokens in all are read one by one.
+__device__ __forceinline__ uint64_t place_of(uint64_t at, uint64_t n) { return n < 4 ? 0 : at < n - 4 ? at : n - 4; }
+
+__device__ __forceinline__ f32x4 load4(const float *p, uint64_t place, uint64_t n, float none) {
+    if (!p) return f32x4{none, none, none, none};
+    gfloat *q = (gfloat *)p + place;
     if (n >= 4) return *(gvec *)q;
+    f32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
+    for (uint32_t i = 0; i < 3; ++i)
         if (i < n) v[i] = q[i];
     return v;
 }
 
-__device__ __forceinline__ void store4(float *p, uint64_t at, uint32_t n, f32x4 v) {
+__device__ __forceinline__ Four load_four(const PolicyArgs &a, uint64_t at) {
+    const uint64_t place = place_of(at, a.n);
+    return Four{load4(a.logp, place, a.n, 0), load4(a.old_logp, place, a.n, 0), load4(a.adv, place, a.n, 0),
+                load4(a.weight, place, a.n, a.w_all), load4(a.ref, place, a.n, 0), load4(a.entropy, place, a.n, 0)};
+}
+
+// The thread's own of four values, at the tokens they were read from.
+__device__ __forceinline__ void store4(float *p, uint64_t place, uint32_t first, uint32_t end, f32x4 v) {
     if (!p) return;
-    gfloat_out *q = (gfloat_out *)p + at;
-    if (n >= 4) {
+    gfloat_out *q = (gfloat_out *)p + place;
+    if (first == 0 && end == 4) {
         *(gvec_out *)q = v;
         return;
     }
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i)
-        if (i < n) q[i] = v[i];
+        if (i >= first && i < end) q[i] = v[i];
 }
 
 __global__ __launch_bounds__(kHeadThreads) void rog_policy_kernel(PolicyArgs a) {
     __shared__ double sh[4][4];
     __shared__ uint32_t last;
     Totals t = {{0, 0, 0, 0}};
-    for (uint32_t k = 0; k < 2; ++k) {
-        const uint64_t at = uint64_t(blockIdx.x) * kPolicyGroup + 4 * (k * kHeadThreads + threadIdx.x);
-        if (at >= a.n) continue;
-        const uint32_t n = a.n - at < 4 ? uint32_t(a.n - at) : 4;
-        const f32x4 logp = load4(a.logp, at, n, 0), old = load4(a.old_logp, at, n, 0), adv = load4(a.adv, at, n, 0);
-        f32x4 w = load4(a.weight, at, n, a.w_all);
-        const f32x4 ref = load4(a.ref, at, n, 0), ent = load4(a.entropy, at, n, 0);
+    const uint64_t begin = uint64_t(blockIdx.x) * a.tiles * kPolicyTile + 4 * threadIdx.x;
+    Four next = load_four(a, begin);
+    for (uint32_t k = 0; k < a.tiles; ++k) {
+        const uint64_t at = begin + uint64_t(k) * kPolicyTile;
+        const Four x = next;
+        // the next tile's loads in flight (after the last, the same again)
+        next = load_four(a, k + 1 < a.tiles ? at + kPolicyTile : at);
+        if (at >= a.n) break;
+        const uint64_t place = place_of(at, a.n);
+        const uint32_t first = uint32_t(at - place), end = a.n < 4 ? uint32_t(a.n) : 4;
         f32x4 g, gh;
+        float sums[4] = {0, 0, 0, 0};
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
-            const bool kept = i < n && w[i] != 0.0f;
-            const float d = logp[i] - old[i];
-            const bool over = adv[i] > 0.0f && d > a.hi, under = adv[i] < 0.0f && d < a.lo;
-            const float ratio = over ? a.ratio_hi : under ? a.ratio_lo : expf(d);
-            const float pg = -adv[i] * ratio;
-            float loss = pg, slope = over || under ? 0.0f : pg, kl = 0.0f;
+            const float w = i >= first && i < end ? x.w[i] : 0.0f;
+            const bool kept = w != 0.0f;
+            const float d = x.logp[i] - x.old[i], adv = x.adv[i];
+            const bool over = adv > 0.0f && d > a.hi, under = adv < 0.0f && d < a.lo, clipped = over || under;
+            const float pg = -adv * (over ? a.ratio_hi : under ? a.ratio_lo : exp_of(d));
+            float loss = pg, slope = clipped ? 0.0f : pg, kl = 0.0f;
             if (a.ref) {
-                const float q = ref[i] - logp[i];
-                kl = kl_term(q);
+                float grow;
+                kl_of(x.ref[i] - x.logp[i], kl, grow);
                 loss = __builtin_fmaf(a.kl_coef, kl, loss);
-                slope = __builtin_fmaf(-a.kl_coef, expm1f(q), slope);
+                slope = __builtin_fmaf(-a.kl_coef, grow, slope);
             }
-            const float e = a.entropy ? ent[i] : 0.0f;
-            loss = __builtin_fmaf(-a.entropy_coef, e, loss);
-            g[i] = kept ? a.grad_scale * w[i] * slope : 0.0f;
-            gh[i] = kept ? -(a.grad_scale * w[i] * a.entropy_coef) : 0.0f;
-            if (kept) {
-                const double wd = double(w[i]);
-                t.v[0] += wd * double(loss);
-                t.v[1] += wd * double(kl);
-                t.v[2] += wd * double(e);
-                t.v[3] += over || under ? wd : 0.0;
-            }
+            if (a.entropy) loss = __builtin_fmaf(-a.entropy_coef, x.ent[i], loss);
+            const float gw = a.grad_scale * w;
+            g[i] = kept ? gw * slope : 0.0f;
+            gh[i] = -(gw * a.entropy_coef);
+            // four tokens' terms in binary32, all else in binary64
+            sums[0] += kept ? w * loss : 0.0f;
+            sums[1] += kept ? w * kl : 0.0f;
+            sums[2] += kept ? w * x.ent[i] : 0.0f;
+            sums[3] += clipped ? w : 0.0f;
         }
-        store4(a.g_logp, at, n, g);
-        store4(a.g_entropy, at, n, gh);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t.v[i] += double(sums[i]);
+        store4(a.g_logp, place, first, end, g);
+        store4(a.g_entropy, place, first, end, gh);
     }
     t = group_sum(t, sh);
     if (a.groups > 1) {
         if (threadIdx.x == 0)
             for (int i = 0; i < 4; ++i) publish(a.part + uint64_t(blockIdx.x) * 4 + i, t.v[i]);
-        if (!last_to_arrive(a.counter, a.groups, last)) return;
+        if (a.groups > kPolicyRoots) {
+            const uint32_t root = blockIdx.x % kPolicyRoots;
+            const uint32_t members = (a.groups - root + kPolicyRoots - 1) / kPolicyRoots;
+            if (!last_to_arrive(a.counter + (1 + root) * kCounterStride, members, last)) return;
+            if (!last_to_arrive(a.counter, kPolicyRoots, last)) return;
+        } else if (!last_to_arrive(a.counter, a.groups, last)) {
+            return;
+        }
         t = Totals{{0, 0, 0, 0}};
         for (uint32_t b = threadIdx.x; b < a.groups; b += kHeadThreads) {
             Totals o;

@@ -349,8 +349,8 @@ typedef struct {
 typedef enum {
     ROG_LOGPROB_AUTO = 0,
     ROG_LOGPROB_ROW = 1,       /* one workgroup per row                           */
-    ROG_LOGPROB_SPLIT = 2,     /* one workgroup per 16 blocks of a row, the last of a
-                                  row to finish joins them (rows of more blocks)  */
+    ROG_LOGPROB_SPLIT = 2,     /* one workgroup per 4 blocks of a row, the last of a
+                                  row to finish joins them (longer rows only)      */
     ROG_LOGPROB_WAVE = 3       /* one wave per row: all rows of at most 4 blocks, and
                                   no others                                       */
 } rog_logprob_form;
