@@ -29,7 +29,7 @@ constexpr uint32_t kUnitBlocks = 4;
 constexpr uint32_t kChunkUnits = 4;
 constexpr uint32_t kChunkBlocks = kUnitBlocks * kChunkUnits;
 constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per unit of a chunk
-constexpr int kGradBlocks = kHeadThreads / 64;   // the gradient's workgroup: a block per wave
+constexpr uint32_t kGradPieceBytes = 2048; // the gradient's piece of a row: two 16-byte vectors per lane of one wave
 // The grid of a launch of `groups` workgroups (below 2^31): a dispatch counts the
 // work-items of each dimension in 32 bits, so more than 2^22 go over two.  The
 // kernels number a workgroup blockIdx.y * gridDim.x + blockIdx.x, and those
@@ -74,6 +74,8 @@ struct HeadShards {
     uint32_t width[kMaxPeers];         // columns
     uint32_t col0[kMaxPeers];          // the shard's first column in the row
     uint32_t block0[kMaxPeers + 1];    // the shard's first block; [W]: all blocks
+    uint32_t even;                     // blocks of every shard where they have as many each, else 0
+    Divider even_div;                  // divides by it
 };
 
 struct LogprobArgs {
@@ -85,7 +87,7 @@ struct LogprobArgs {
     float *part;                       // split: per row, the units' states and their lanes' maxima
     float scale;                       // log2(e) / temperature
     float inv_t;                       // 1 / temperature
-    float bound;                       // |x| beyond this leaves the scaled range
+    float bound;                       // |x| that leaves the scaled range; binary16: its largest
     uint32_t W, rows, blocks;
     uint32_t chunks, units;            // units that have blocks
     uint32_t top_k;
@@ -100,9 +102,10 @@ struct LogprobGradArgs {
     const int64_t *tokens;
     const float *lse, *entropy, *g_logp, *g_entropy;
     float scale, inv_t;
-    uint32_t W, rows, blocks, vocab;
-    uint32_t splits;                   // workgroups per row, four blocks each
-    uint32_t groups;                   // workgroups of all rows
+    uint32_t W, rows, vocab;
+    uint32_t pieces;                   // of a row (HeadShards' blocks are pieces here)
+    Divider pieces_div;
+    uint32_t groups;                   // pieces of all rows
 };
 
 struct PolicyArgs {
@@ -130,6 +133,7 @@ struct LogprobGradPlan {
     uint32_t grid;
     LogprobGradArgs args;
     rog_dtype dtype;
+    bool nt_loads;
 };
 struct PolicyPlan {
     PolicyArgs args;

@@ -94,30 +94,41 @@ struct BlockAt {
     uint32_t off;       // the first column's number in the shard
 };
 
-// Walks through one row's blocks, in rising order: the current shard's layout
+// Walks through one row's blocks (of COLUMNS columns), in rising order: the current shard's layout
 // stays in scalar registers, and kernel arguments are read only where a shard
 // begins.
-template <int DT>
+template <int DT, uint32_t COLUMNS = kHeadBlock>
 struct Cursor {
     const HeadShards &h;
     gbyte *base;                       // the row's first column in the shard
     uint32_t row, shard, first, end;   // blocks [first, end) are the shard's
     uint32_t width, col0;
 
-    __device__ __forceinline__ Cursor(const HeadShards &shards, uint32_t r) : h(shards), row(r) { enter(0); }
+    __device__ __forceinline__ Cursor(const HeadShards &shards, uint32_t r) : h(shards), row(r), shard(0), end(0) {}
     __device__ __forceinline__ void enter(uint32_t s) {
         shard = s;
-        first = h.block0[s];
-        end = h.block0[s + 1];
         width = h.width[s];
         col0 = h.col0[s];
         base = (gbyte *)h.x[s] + int64_t(row) * h.stride[s];
     }
     // Block b (below the row's blocks, not before the shard that the cursor is in).
     __device__ __forceinline__ BlockAt at(uint32_t b) {
-        while (b >= end) enter(shard + 1);
-        const uint32_t off = (b - first) * kHeadBlock, left = width - off;
-        return BlockAt{base + uint64_t(off) * Logit<DT>::kSize, left < kHeadBlock ? left : kHeadBlock, col0 + off, shard, off};
+        if (b >= end) {
+            if (h.even) {
+                const uint32_t s = divide(b, h.even_div);
+                first = s * h.even;
+                end = first + h.even;
+                enter(s);
+            } else {
+                uint32_t s = shard;
+                while (h.block0[s + 1] <= b) ++s;
+                first = h.block0[s];
+                end = h.block0[s + 1];
+                enter(s);
+            }
+        }
+        const uint32_t off = (b - first) * COLUMNS, left = width - off;
+        return BlockAt{base + uint64_t(off) * Logit<DT>::kSize, left < COLUMNS ? left : COLUMNS, col0 + off, shard, off};
     }
 };
 
@@ -165,14 +176,14 @@ __device__ __forceinline__ vec16 load_vec(gbyte *p, uint32_t n, uint32_t i, uint
 // than one vector (read where it is used, tiny_state) reads the first bytes of
 // the kernel arguments instead, and with `real`
 // false every lane reads the block's first bytes.
-template <int DT, bool NT>
-__device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[Logit<DT>::kVecs], bool real = true) {
+template <int DT, bool NT, uint32_t VECS>
+__device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[VECS], bool real = true) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const bool tiny = b.n < per;
     gbyte *const p = tiny ? (gbyte *)__builtin_amdgcn_kernarg_segment_ptr() : b.p;
     const uint32_t last = tiny || !real ? 0 : (b.n - per) * Logit<DT>::kSize;
 #pragma unroll
-    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
+    for (uint32_t i = 0; i < VECS; ++i) {
         const uint32_t c = (64 * i + lane) * 16;
         gvec16any *const q = (gvec16any *)(p + (c < last ? c : last));
         if constexpr (NT) v[i] = __builtin_nontemporal_load(q);
@@ -188,23 +199,21 @@ __device__ __forceinline__ bool owns(uint32_t n, uint32_t i, uint32_t lane, uint
     return vec_place<DT>(n, i, lane) + e >= c;
 }
 
-// The elements of a block of kPerVec columns or more, -inf in the place of
-// those that are not the lane's own.
+// Puts -inf in the place of the elements of a tail that are not the lane's own
+// (a block of kPerVec columns or more, its vectors as loaded).
 template <int DT>
-__device__ __forceinline__ void widen_block(const vec16 (&v)[Logit<DT>::kVecs], float (&x)[32]) {
-#pragma unroll
-    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) widen_vec<DT>(v[i], x + i * Logit<DT>::kPerVec);
-}
-template <int DT>
-__device__ __forceinline__ void mask_tail(uint32_t n, uint32_t lane, float (&x)[32]) {
-    constexpr uint32_t per = Logit<DT>::kPerVec;
+__device__ __forceinline__ void mask_tail(uint32_t n, uint32_t lane, vec16 (&v)[Logit<DT>::kVecs]) {
+    constexpr uint32_t per = Logit<DT>::kPerVec, pack = per / 4;      // elements per word
     const uint32_t last = n - per;
 #pragma unroll
     for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) {
         const uint32_t c = own_column<DT>(i, lane);
         const uint32_t others = c > last ? c - last : 0;       // leading elements that are another lane's
 #pragma unroll
-        for (uint32_t e = 0; e < per; ++e) x[i * per + e] = e >= others ? x[i * per + e] : -kInf;
+        for (uint32_t d = 0; d < 4; ++d) {
+            const uint32_t keep = others <= pack * d ? ~0u : pack == 2 && others == 2 * d + 1 ? 0xFFFF0000u : 0u;
+            v[i][d] = (v[i][d] & keep) | (Logit<DT>::kMinusInf & ~keep);
+        }
     }
 }
 
@@ -229,20 +238,82 @@ struct Scaling {
     }
 };
 
-// The state of 32 logits x[] in a lane.  bound * scale is 2^30: up to there the
-// rounding of R stays below 64, so that no term overflows.  Logits of -inf and
-// beyond -bound count as -bound: nothing against any reference but their own,
-// and finite, so that 0 * (z - R) stays 0.  A row whose largest logit is at a
-// bound or beyond is read again (the kernels' extreme rows).
-__device__ __forceinline__ State state_of(const float (&x)[32], const Scaling &c) {
-    float m = x[0];
+// Logits of a lane as they are used one by one: binary16 stays packed in its
+// words (v_fma_mix_f32 widens it on the way), the others are widened first.
+template <int DT>
+struct Lane32 {
+    float x[32];
+    __device__ __forceinline__ explicit Lane32(const vec16 (&v)[Logit<DT>::kVecs]) {
 #pragma unroll
-    for (int i = 1; i < 32; ++i) m = max_nan(m, x[i]);
+        for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) widen_vec<DT>(v[i], x + i * Logit<DT>::kPerVec);
+    }
+    __device__ __forceinline__ float at(int i) const { return x[i]; }
+    __device__ __forceinline__ float largest() const {
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) m = max_nan(m, x[i]);
+        return m;
+    }
+    __device__ __forceinline__ float smallest() const {
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) m = __builtin_elementwise_minimum(m, x[i]);
+        return m;
+    }
+    __device__ __forceinline__ void raise(float low) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = fmaxf(x[i], low);
+    }
+};
+template <>
+struct Lane32<ROG_DTYPE_F16> {
+    f16x2 h[16];
+    __device__ __forceinline__ explicit Lane32(const vec16 (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t word = v[i / 4][i % 4];
+            h[i] = __builtin_bit_cast(f16x2, word);
+        }
+    }
+    __device__ __forceinline__ float at(int i) const { return float(i & 1 ? h[i / 2].y : h[i / 2].x); }
+    __device__ __forceinline__ float largest() const {
+        f16x2 m = h[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m = __builtin_elementwise_maximum(m, h[i]);
+        return max_nan(float(m.x), float(m.y));
+    }
+    __device__ __forceinline__ float smallest() const {
+        f16x2 m = h[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m = __builtin_elementwise_minimum(m, h[i]);
+        return __builtin_elementwise_minimum(float(m.x), float(m.y));
+    }
+    __device__ __forceinline__ void raise(float) {
+        const f16x2 low = {-65504.0f16, -65504.0f16};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[i] = __builtin_elementwise_max(h[i], low);
+    }
+};
+
+// The state of a lane's 32 logits of a block.  bound * scale is 2^30 (binary16:
+// less): up to there the rounding of R stays below 64, so that no term
+// overflows.  Where
+// any lane of the wave holds a logit below -bound (-inf, or a mask of the
+// lowest finite value; looking for the smallest costs half of raising all),
+// those count as -bound: nothing against
+// any reference but their own, and finite, so that 0 * (z - R) stays 0.  A row
+// whose largest logit is at a bound or beyond is read again (the kernels'
+// extreme rows).
+template <int DT>
+__device__ __forceinline__ State state_of(const vec16 (&v)[Logit<DT>::kVecs], const Scaling &c) {
+    Lane32<DT> x(v);
+    const float m = x.largest();
     const float r = c.ref(m);
+    if (__ballot(x.smallest() < -c.bound)) x.raise(-c.bound);
     float s[4], t[4];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const float y = __builtin_fmaf(__builtin_amdgcn_fmed3f(x[i], -c.bound, c.bound), c.scale, -r);
+        const float y = __builtin_fmaf(x.at(i), c.scale, -r);
         const float e = exp2_fast(y);
         s[i & 3] = i < 4 ? e : s[i & 3] + e;
         t[i & 3] = i < 4 ? e * y : __builtin_fmaf(e, y, t[i & 3]);

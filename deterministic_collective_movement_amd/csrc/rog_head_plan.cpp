@@ -52,7 +52,7 @@ constexpr double kLog2E = 1.4426950408889634;
 
 // Shared checks of the logits, and their layout into the kernel arguments.
 rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype, bool addresses,
-                      HeadShards *h, uint32_t *vocab, uint32_t *blocks) {
+                      uint32_t block, HeadShards *h, uint32_t *vocab, uint32_t *blocks) {
     if (!shards || W < 1 || W > kMaxPeers || !known(dtype)) return ROG_ERR_INVALID_ARGUMENT;
     const uint32_t es = esize(dtype);
     uint64_t v = 0, b = 0;
@@ -69,7 +69,7 @@ rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dty
         h->col0[r] = uint32_t(v);
         h->block0[r] = uint32_t(b);
         v += uint64_t(s.width);
-        b += ceil_div(uint64_t(s.width), kHeadBlock);
+        b += ceil_div(uint64_t(s.width), block);
         if (addresses) {
             if (uint64_t(s.row_stride) >= uint64_t(1) << 48) return ROG_ERR_TOO_LARGE;
             h->stride[r] = s.row_stride * es;
@@ -77,6 +77,10 @@ rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dty
         }
     }
     h->block0[W] = uint32_t(b);
+    h->even = h->block0[1];
+    for (int r = 1; r < W; ++r)
+        if (h->block0[r + 1] - h->block0[r] != h->even) h->even = 0;
+    h->even_div = make_divider(std::max(h->even, 1u));
     *vocab = uint32_t(v);
     *blocks = uint32_t(b);
     return rows >= kMaxVocab ? ROG_ERR_TOO_LARGE : ROG_OK;
@@ -119,7 +123,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     LogprobArgs &a = p->args;
     uint32_t vocab = 0, blocks = 0;
     if (!out || !(temperature >= kMinTemperature && temperature <= kMaxTemperature)) return ROG_ERR_INVALID_ARGUMENT;
-    rog_status st = lay_shards(shards, W, rows, dtype, true, &a.sh, &vocab, &blocks);
+    rog_status st = lay_shards(shards, W, rows, dtype, true, kHeadBlock, &a.sh, &vocab, &blocks);
     if (st != ROG_OK) return st;
     st = choose_form(blocks, rows, top_k, form, &p->info);
     if (st != ROG_OK || rows == 0) return st;
@@ -160,7 +164,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     a.part = need ? reinterpret_cast<float *>(static_cast<char *>(workspace) + kHeadCounterBytes) : nullptr;
     a.scale = float(kLog2E / double(temperature));
     a.inv_t = float(1.0 / double(temperature));
-    a.bound = float(ldexp(double(temperature) / kLog2E, 30));
+    a.bound = dtype == ROG_DTYPE_F16 ? 65504.0f : float(ldexp(double(temperature) / kLog2E, 30));
     a.W = uint32_t(W);
     a.rows = uint32_t(rows);
     a.blocks = blocks;
@@ -183,7 +187,7 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     uint32_t vocab = 0, blocks = 0;
     p->grid = 0;
     if (!grads || !(temperature >= kMinTemperature && temperature <= kMaxTemperature)) return ROG_ERR_INVALID_ARGUMENT;
-    rog_status st = lay_shards(shards, W, rows, dtype, true, &a.sh, &vocab, &blocks);
+    rog_status st = lay_shards(shards, W, rows, dtype, true, kGradPieceBytes / (known(dtype) ? esize(dtype) : 4), &a.sh, &vocab, &blocks);
     if (st != ROG_OK) return st;
     if (rows == 0 || vocab == 0) return ROG_OK;
     if (!tokens || !lse || !entropy || !g_logp || addr(tokens) % 8 ||
@@ -225,12 +229,13 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     a.inv_t = float(1.0 / double(temperature));
     a.W = uint32_t(W);
     a.rows = uint32_t(rows);
-    a.blocks = blocks;
     a.vocab = vocab;
-    a.splits = uint32_t(ceil_div(blocks, kGradBlocks));
-    const uint64_t groups = uint64_t(a.splits) * rows;
-    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
-    a.groups = p->grid = uint32_t(groups);
+    a.pieces = blocks;
+    a.pieces_div = make_divider(blocks);
+    const uint64_t pieces = uint64_t(blocks) * rows;
+    if (pieces >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    a.groups = p->grid = uint32_t(pieces);
+    p->nt_loads = rows * uint64_t(vocab) * es >= ROG_HEAD_NT_MIN_BYTES;
     p->dtype = dtype;
     return ROG_OK;
 }
@@ -315,7 +320,7 @@ ROG_API rog_status rog_logprob_plan(const rog_logit_shard *shards, int W, size_t
     if (!info) return ROG_ERR_INVALID_ARGUMENT;
     rog::HeadShards h;
     uint32_t vocab = 0, blocks = 0;
-    const rog_status st = rog::lay_shards(shards, W, rows, dtype, false, &h, &vocab, &blocks);
+    const rog_status st = rog::lay_shards(shards, W, rows, dtype, false, rog::kHeadBlock, &h, &vocab, &blocks);
     return st != ROG_OK ? st : rog::choose_form(blocks, rows, top_k, form, info);
 }
 

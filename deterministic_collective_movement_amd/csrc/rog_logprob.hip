@@ -293,9 +293,11 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
     v.lse = (v.r + v.l) * kLn2;
     v.extreme = false;
     float entropy = (v.l - all.t / all.s) * kLn2;
-    if (all.m >= a.bound || all.m <= -a.bound) {
+    if ((DT != ROG_DTYPE_F16 && all.m >= a.bound) || all.m <= -a.bound) {
         // Logits this large lie so far apart that any but the largest has
         // probability 0: the row is uniform over the columns that equal it.
+        // (binary16 stays in the scaled range; its lowest value may be mixed
+        // with -inf, which counts as it in the states.)
         atomicAdd(&equal, count_equal<DT>(a, row, tid / 64, T::kTeamWaves, tid & 63, all.m));
         T::sync();
         v.extreme = true;
@@ -344,13 +346,14 @@ __device__ __forceinline__ State take_block(Cursor<DT> &cur, BlockAt &at, vec16 
                                             const Scaling &c, bool next, uint32_t b) {
     const uint32_t n = at.n;
     gbyte *const p = at.p;
-    float x[32];
-    widen_block<DT>(v, x);
+    vec16 x[Logit<DT>::kVecs];
+#pragma unroll
+    for (uint32_t i = 0; i < Logit<DT>::kVecs; ++i) x[i] = v[i];
     if (next) at = cur.at(b);
     load_block<DT, NT>(at, lane, v, next);
     if (n < Logit<DT>::kPerVec) return tiny_state<DT>(p, n, lane, c);
     if (n < kHeadBlock) mask_tail<DT>(n, lane, x);
-    return state_of(x, c);
+    return state_of<DT>(x, c);
 }
 
 __device__ __forceinline__ int64_t row_token(const LogprobArgs &a, uint32_t row) { return a.tokens ? a.tokens[row] : 0; }

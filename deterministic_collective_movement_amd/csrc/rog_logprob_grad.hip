@@ -18,88 +18,75 @@ constexpr float kLog2EHi = 1.44269502f;                 // log2(e) in two parts
 constexpr float kLog2ELo = 1.92596303e-8f;
 constexpr float kExtreme = 7.442609e8f;                 // 2^30 ln 2, where rog_logprob's extreme rows begin
 
-// A row's coefficients.
-struct Coeffs {
-    float a, b, g;        // A, B, g / T
-    float hi, lo;         // lse log2(e) = hi + lo
-};
-
-// One block's gradient in place of its logits x[].
-__device__ __forceinline__ void block_grad(float (&x)[32], const Coeffs &k, float scale) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        // z - lse in base 2; -200 stands for anything less (p is zero there)
-        const float y = fmaxf(__builtin_fmaf(x[i], scale, -k.hi) - k.lo, -200.0f);
-        x[i] = exp2_fast(y) * __builtin_fmaf(k.b, y, k.a);
-    }
-}
-
-template <int DT>
-__global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobGradArgs) {
+// One wave, a workgroup of its own, per piece of a row: 4096 x 131072 bf16 over
+// eight shards took 334 us with pieces of 2 KB, against 358 with four waves of
+// 4 KB each, 372 with 1 KB, and 365 and more where waves took several pieces
+// in turn.
+template <int DT, bool NT>
+__global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
     const LogprobGradArgs &a = launch_args<LogprobGradArgs>();
-    constexpr uint32_t per = Logit<DT>::kPerVec, vecs = Logit<DT>::kVecs;
-    const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
+    constexpr uint32_t per = Logit<DT>::kPerVec, vecs = kGradPieceBytes / (64 * 16), each = vecs * per;
+    const uint32_t lane = threadIdx.x;
     const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
     if (group >= a.groups) return;
-    const uint32_t row = group / a.splits, b = group % a.splits * kGradBlocks + w;
-    if (b >= a.blocks) return;
-    const BlockAt at = Cursor<DT>(a.sh, row).at(b);
-    typedef __attribute__((address_space(1))) uint8_t gout;
-    gout *o = (gout *)a.g[at.shard] + int64_t(row) * a.g_stride[at.shard] + uint64_t(at.off) * Logit<DT>::kSize;
+    const uint32_t row = divide(group, a.pieces_div), piece = group - row * a.pieces;
+    // everything that a wave needs of its row, asked for at once
     const int64_t tok = a.tokens[row];
-    const float lse = a.lse[row];
-    float x[32];
-    if (tok < 0 || lse == -kInf) {
+    const float lse = a.lse[row], H = a.entropy[row], g = a.g_logp[row], h = a.g_entropy ? a.g_entropy[row] : 0.0f;
+    const BlockAt at = Cursor<DT, 64 * each>(a.sh, row).at(piece);
+    typedef __attribute__((address_space(1))) uint8_t gout;
+    gout *const o = (gout *)a.g[at.shard] + int64_t(row) * a.g_stride[at.shard] + uint64_t(at.off) * Logit<DT>::kSize;
+    const bool none = tok < 0 || lse == -kInf, bad = tok >= int64_t(a.vocab) || !(lse < kInf);
+    const bool tiny = at.n < per;
+    float x[each];
+    if (none || bad) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+        for (uint32_t i = 0; i < each; ++i) x[i] = none ? 0.0f : __builtin_nanf("");
     } else {
         vec16 v[vecs];
-        load_block<DT, false>(at, lane, v);
-        const bool tiny = at.n < per;
+        load_block<DT, NT>(at, lane, v);
         if (tiny) v[0] = load_tiny<DT>(at.p, at.n);
-        widen_block<DT>(v, x);
-        const float g = a.g_logp[row], h = a.g_entropy ? a.g_entropy[row] : 0.0f, H = a.entropy[row];
-        Coeffs k;
-        k.g = g * a.inv_t;
-        k.a = -(g + h * H) * a.inv_t;
-        k.b = -h * a.inv_t * kLn2;
-        k.hi = lse * kLog2EHi;
-        k.lo = __builtin_fmaf(lse, kLog2ELo, __builtin_fmaf(lse, kLog2EHi, -k.hi));
-        const bool bad = tok >= int64_t(a.vocab) || !(lse < kInf);
-        if (bad) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __builtin_nanf("");
-        } else if (fabsf(lse) >= kExtreme) {
+        for (uint32_t i = 0; i < vecs; ++i) widen_vec<DT>(v[i], x + i * per);
+        const float scaled = g * a.inv_t, A = -(g + h * H) * a.inv_t, B = -h * a.inv_t * kLn2;
+        if (fabsf(lse) >= kExtreme) {
             // Logits this large lie so far apart that only those equal to the
             // largest have any probability, the same for each: e^{-H}.
             const float p = expf(-H);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (uint32_t i = 0; i < each; ++i) {
                 // rog_logprob's own lse of such a row, if x[i] is its largest logit
                 const float z = __builtin_amdgcn_fmed3f(__builtin_fmaf(x[i], a.inv_t, H), -3.40282347e38f, 3.40282347e38f);
-                x[i] = x[i] > -kInf && z == lse ? -k.g * p : 0.0f;
+                x[i] = x[i] > -kInf && z == lse ? -scaled * p : 0.0f;
             }
         } else {
-            block_grad(x, k, a.scale);
+            const float hi = lse * kLog2EHi;            // lse log2(e) = hi + lo
+            const float lo = __builtin_fmaf(lse, kLog2ELo, __builtin_fmaf(lse, kLog2EHi, -hi));
+#pragma unroll
+            for (uint32_t i = 0; i < each; ++i) {
+                // -200 stands for anything less (p is zero there), so that 0 * y stays 0
+                const float y = fmaxf(__builtin_fmaf(x[i], a.scale, -hi) - lo, -200.0f);
+                x[i] = exp2_fast(y) * __builtin_fmaf(B, y, A);
+            }
         }
         const int64_t t = tok - int64_t(at.col);
-        if (!bad && t >= 0 && t < int64_t(at.n)) {
-            // the token is in this block
+        if (t >= 0 && t < int64_t(at.n)) {
+            // the token is in this piece
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) {
+            for (uint32_t i = 0; i < each; ++i) {
                 const uint32_t col = (tiny ? 0 : vec_place<DT>(at.n, i / per, lane)) + i % per;
-                x[i] = uint32_t(t) == col ? x[i] + k.g : x[i];
+                x[i] = uint32_t(t) == col ? x[i] + scaled : x[i];
             }
         }
     }
 #pragma unroll
     for (uint32_t i = 0; i < vecs; ++i) {
-        vec16 v;
+        vec16any v;
 #pragma unroll
         for (uint32_t d = 0; d < 4; ++d) v[d] = narrow_word<DT>(x + i * per + d * (per / 4));
-        if (at.n >= per) {
+        if (!tiny) {
             // where the vector was read: what it shares with other lanes' vectors, they write alike
-            *(gvec16any_out *)(o + vec_place<DT>(at.n, i, lane) * Logit<DT>::kSize) = v;
+            __builtin_nontemporal_store(v, (gvec16any_out *)(o + vec_place<DT>(at.n, i, lane) * Logit<DT>::kSize));
         } else if (i == 0 && lane == 0) {
 #pragma unroll
             for (uint32_t e = 0; e + 1 < per; ++e) {
@@ -113,8 +100,11 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_grad_kernel(LogprobG
     }
 }
 
-template <typename K>
-const void *kfn(K *k) { return reinterpret_cast<const void *>(k); }
+template <int DT>
+const void *grad_kernel(bool nt) {
+    return nt ? reinterpret_cast<const void *>(&rog_logprob_grad_kernel<DT, true>)
+              : reinterpret_cast<const void *>(&rog_logprob_grad_kernel<DT, false>);
+}
 
 }  // namespace
 }  // namespace rog
@@ -129,11 +119,11 @@ ROG_API rog_status rog_logprob_grad(const rog_logit_shard *shards, const rog_gra
     const rog_status st = rog::plan_logprob_grad(shards, grads, W, rows, dtype, temperature, tokens, lse, entropy,
                                                  g_logp, g_entropy, &p);
     if (st != ROG_OK || p.grid == 0) return st;
-    const void *k = dtype == ROG_DTYPE_BF16  ? rog::kfn(&rog::rog_logprob_grad_kernel<ROG_DTYPE_BF16>)
-                    : dtype == ROG_DTYPE_F16 ? rog::kfn(&rog::rog_logprob_grad_kernel<ROG_DTYPE_F16>)
-                                             : rog::kfn(&rog::rog_logprob_grad_kernel<ROG_DTYPE_F32>);
+    const void *k = dtype == ROG_DTYPE_BF16  ? rog::grad_kernel<ROG_DTYPE_BF16>(p.nt_loads)
+                    : dtype == ROG_DTYPE_F16 ? rog::grad_kernel<ROG_DTYPE_F16>(p.nt_loads)
+                                             : rog::grad_kernel<ROG_DTYPE_F32>(p.nt_loads);
     void *params[] = {&p.args};
-    const hipError_t e = hipLaunchKernel(k, rog::head_grid(p.grid), dim3(rog::kHeadThreads), params, 0, stream);
+    const hipError_t e = hipLaunchKernel(k, rog::head_grid(p.grid), dim3(64), params, 0, stream);
     if (e != hipSuccess) {
         rog::g_last_hip_error = int(e);
         return ROG_ERR_LAUNCH;

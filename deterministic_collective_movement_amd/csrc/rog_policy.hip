@@ -110,7 +110,7 @@ __device__ __forceinline__ void store4(float *p, uint64_t place, uint32_t first,
     if (!p) return;
     gfloat_out *q = (gfloat_out *)p + place;
     if (first == 0 && end == 4) {
-        *(gvec_out *)q = v;
+        __builtin_nontemporal_store(v, (gvec_out *)q);   // 34 -> 31 us at 4194307 tokens; even at small sizes
         return;
     }
 #pragma unroll
