@@ -42,9 +42,21 @@ constexpr int kMaxTopK = 32;
 constexpr uint32_t kTopSlots = 8;          // entries per lane and wave in the top-k table
 
 // Tunables, measured on MI355X; a variant build may override one with -D.
-#ifndef ROG_SPLIT_MAX_GROUPS
-#define ROG_SPLIT_MAX_GROUPS 3072
+// When a row of `units` units is split over workgroups: a workgroup per row
+// takes about 4.5 us + 0.7 us per unit up to 256 rows (a wave takes its blocks
+// one after the other), a split launch about 5.5 us + 3.6 ns per workgroup, so
+// for rows + kSplitCost / units <= kSplitRows.  Measured, split against not:
+// 64 x 131072 9.4 against 15.7 us, 128 12.9 / 16.3, 192 16.0 / 16.5, 256
+// 19.1 / 16.4; 64 x 50257 6.7 / 9.2, 128 9.2 / 9.7, 256 12.3 / 10.2; 64 x 12000
+// 5.9 / 5.8; 128 x 32000 binary32 8.4 / 7.8.
+#ifndef ROG_SPLIT_ROWS
+#define ROG_SPLIT_ROWS 176
 #endif
+constexpr uint32_t kSplitRows = ROG_SPLIT_ROWS, kSplitCost = 256;
+// Logits' bytes from which their loads are streamed past the caches: 4096 x
+// 131072 bf16 166 us streamed against 186 cached, 8627 x 8192 26.8 against
+// 29.2; below, repeated calls find them in the Infinity Cache (1021 x 50257
+// 23.2 cached against 24.9, 509 x 32003 binary32 20.4 against 22.0).
 #ifndef ROG_HEAD_NT_MIN_BYTES
 #define ROG_HEAD_NT_MIN_BYTES (128ull << 20)
 #endif
