@@ -43,6 +43,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import List, NamedTuple, Optional, Sequence
 
@@ -117,34 +118,9 @@ class rog_plan_info(ctypes.Structure):
                 ("peer_sh2", ctypes.c_uint32), ("flags", ctypes.c_uint32)]
 
 
-class rog_logit_shard(ctypes.Structure):
-    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("width", ctypes.c_int64)]
-
-
-class rog_grad_shard(ctypes.Structure):
-    _fields_ = [("grad", ctypes.c_void_p), ("row_stride", ctypes.c_int64)]
-
-
-class rog_logprob_out(ctypes.Structure):
-    _fields_ = [("logp", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("lse", ctypes.c_void_p),
-                ("top_logp", ctypes.c_void_p), ("top_ids", ctypes.c_void_p)]
-
-
 class rog_head_plan_info(ctypes.Structure):
     _fields_ = [("form", ctypes.c_int32), ("grid", ctypes.c_uint32), ("block", ctypes.c_uint32),
                 ("blocks", ctypes.c_uint32), ("workspace_bytes", ctypes.c_uint64)]
-
-
-class rog_policy_in(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("logp", "old_logp", "advantage", "weight", "ref_logp", "entropy")]
-
-
-class rog_policy_params(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_float) for n in ("clip_low", "clip_high", "kl_coef", "entropy_coef", "grad_scale")]
-
-
-class rog_policy_out(ctypes.Structure):
-    _fields_ = [("stats", ctypes.c_void_p), ("g_logp", ctypes.c_void_p), ("g_entropy", ctypes.c_void_p)]
 
 
 def _hip_runtimes_mapped() -> set:
@@ -177,12 +153,13 @@ def _load() -> ctypes.CDLL:
     lib.rog_reduce_ex.argtypes = [ptrs, i32, sz, i32, vp, vp, i32]
     lib.rog_reduce_plan.argtypes = [ptrs, i32, sz, i32, vp, i32, ctypes.POINTER(rog_plan_info)]
     lib.rog_reduce_many.argtypes = [ctypes.POINTER(rog_reduce_desc), i32, i32, i32, vp]
-    f32, ref = ctypes.c_float, ctypes.POINTER
-    lib.rog_logprob_ex.argtypes = [ref(rog_logit_shard), i32, sz, i32, f32, vp, i32, ref(rog_logprob_out), vp, sz, vp, i32]
+    # host structures go in as packed bytes or by reference
+    f32 = ctypes.c_float
+    lib.rog_logprob_ex.argtypes = [vp, i32, sz, i32, f32, vp, i32, vp, vp, sz, vp, i32]
     lib.rog_logprob.argtypes = lib.rog_logprob_ex.argtypes[:-1]
-    lib.rog_logprob_plan.argtypes = [ref(rog_logit_shard), i32, sz, i32, i32, i32, ref(rog_head_plan_info)]
-    lib.rog_logprob_grad.argtypes = [ref(rog_logit_shard), ref(rog_grad_shard), i32, sz, i32, f32, vp, vp, vp, vp, vp, vp]
-    lib.rog_policy_loss.argtypes = [ref(rog_policy_in), sz, ref(rog_policy_params), ref(rog_policy_out), vp, sz, vp]
+    lib.rog_logprob_plan.argtypes = [vp, i32, sz, i32, i32, i32, vp]
+    lib.rog_logprob_grad.argtypes = [vp, vp, i32, sz, i32, f32, vp, vp, vp, vp, vp, vp]
+    lib.rog_policy_loss.argtypes = [vp, sz, vp, vp, vp, sz, vp]
     lib.rog_policy_loss_workspace_bytes.argtypes = [sz]
     lib.rog_policy_loss_workspace_bytes.restype = sz
     for name in ("rog_logprob", "rog_logprob_ex", "rog_logprob_plan", "rog_logprob_grad", "rog_policy_loss"):
@@ -607,10 +584,23 @@ class RogPolicyLoss(NamedTuple):
     g_entropy: Optional[torch.Tensor]   # [n] float32
 
 
+# The C structures of these calls as packed bytes, which cost less per call than
+# ctypes structures: rog_logit_shard (address, row stride, width) and
+# rog_grad_shard (address, row stride) once per shard, rog_logprob_out,
+# rog_policy_in, rog_policy_params, rog_policy_out.
+_PACK_SHARDS = [struct.Struct("=" + "Qqq" * w).pack for w in range(_lib.rog_max_peers() + 1)]
+_PACK_GRADS = [struct.Struct("=" + "Qq" * w).pack for w in range(_lib.rog_max_peers() + 1)]
+_pack_addresses5 = struct.Struct("=5Q").pack
+_pack_addresses6 = struct.Struct("=6Q").pack
+_pack_addresses3 = struct.Struct("=3Q").pack
+_pack_floats5 = struct.Struct("=5f").pack
+_MAX_TOP_K = int(_lib.rog_max_top_k())
+
 # One workspace per stream, so that calls on different streams never share one;
 # zero-filled when it is made, as the library asks, and left ready by every call.
 _workspaces: dict = {}
 _workspaces_lock = threading.Lock()
+_NO_WORKSPACE = (None, 0)
 
 
 def rog_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
@@ -625,40 +615,73 @@ def rog_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
         return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=device)
 
 
-def _workspace(workspace, nbytes: int, device: torch.device, stream, handle: int):
-    """(address, bytes) of the caller's workspace or of the stream's own one."""
-    if workspace is not None:
-        _check_tensor(workspace, "workspace", device)
-        return workspace.data_ptr(), _nbytes(workspace)
+def _own_workspace(nbytes: int, device: torch.device, stream, handle: int):
+    """(address, bytes) of the stream's workspace, made or grown to hold ``nbytes``."""
     if nbytes == 0:
-        return None, 0
-    if torch.cuda.is_current_stream_capturing():
+        return _NO_WORKSPACE
+    if _capturing(stream, device):
         # a graph's replays may run beside eager calls on this stream: the graph gets its own, cleared in the graph
-        t = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        t = rog_workspace(nbytes, device, stream)
         return t.data_ptr(), nbytes
     key = (device.index, handle)
-    t = _workspaces.get(key)
-    if t is None or t.numel() < nbytes:
-        with _workspaces_lock:
-            t = _workspaces.get(key)
-            if t is None or t.numel() < nbytes:
-                t = rog_workspace(max(nbytes, 1 << 20), device, stream)
-                _workspaces[key] = t
-    return t.data_ptr(), t.numel()
+    with _workspaces_lock:
+        got = _workspaces.get(key)
+        if got is None or got[1] < nbytes:
+            t = rog_workspace(max(nbytes, 1 << 20), device, stream)
+            got = _workspaces[key] = (t.data_ptr(), t.numel(), t)
+    return got[:2]
 
 
-def _check_vector(t, what: str, n: int, dtype: torch.dtype, device: torch.device) -> int:
+_is_capturing = torch.cuda.is_current_stream_capturing
+
+
+def _capturing(stream, device: torch.device) -> bool:
+    if stream is None:
+        return _is_capturing()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return _is_capturing()
+
+
+def _with_workspace(call, need, what: str, workspace, device: torch.device, stream, handle: int) -> None:
+    """``call(address, bytes)`` with the caller's workspace or the stream's own.
+    The library refuses one that is too small before it enqueues anything, so
+    ``need()``, the bytes it asks for, is only looked up where the stream's own
+    does not do."""
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", device)
+        _check(call(workspace.data_ptr(), _nbytes(workspace)), what)
+        return
+    if not _capturing(stream, device):
+        got = _workspaces.get((device.index, handle), _NO_WORKSPACE)
+        status = call(got[0], got[1])
+        if status == ROG_OK:
+            return
+        if status != ROG_ERR_INVALID_ARGUMENT or got[1] >= need():
+            _check(status, what)
+    _check(call(*_own_workspace(need(), device, stream, handle)), what)
+
+
+def _vector_error(t, what: str, n: int, dtype: torch.dtype, device: torch.device):
+    """The first thing wrong with what should be a contiguous vector of n elements."""
+    _check_tensor(t, what, device)
+    raise ValueError("%s must hold %d elements of %s (has %d of %s)" % (what, n, dtype, t.numel(), t.dtype))
+
+
+def _vector(t, what: str, n: int, dtype: torch.dtype, device: torch.device, idx: int) -> int:
     """Address of a contiguous vector of n elements (0 for None)."""
     if t is None:
         return 0
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == device.index and t.is_contiguous()):
-        _check_tensor(t, what, device)
-    if t.dtype != dtype or t.numel() != n:
-        raise ValueError("%s must hold %d elements of %s (has %d of %s)" % (what, n, dtype, t.numel(), t.dtype))
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == idx and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _vector_error(t, what, n, dtype, device)
 
 
-def _check_matrix(t, what: str, rows: int, dtype: torch.dtype, device: torch.device) -> None:
+def _matrix_error(t, what: str, rows: int, dtype: torch.dtype, device: torch.device):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % what)
     if not t.is_cuda:
@@ -669,14 +692,15 @@ def _check_matrix(t, what: str, rows: int, dtype: torch.dtype, device: torch.dev
         raise ValueError("%s must be %s (got %s)" % (what, dtype, t.dtype))
     if t.dim() != 2 or t.shape[0] != rows:
         raise ValueError("%s must be a matrix of %d rows (got %s)" % (what, rows, tuple(t.shape)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("%s must be contiguous within its rows (any row stride)" % what)
+    raise ValueError("%s must be contiguous within its rows (any row stride)" % what)
 
 
-def _shard_array(shards):
-    """(device, rows, dtype code, array of rog_logit_shard) of W logits matrices."""
+def _shard_bytes(shards):
+    """(device, its index, rows, torch dtype, packed rog_logit_shard array) of W logits matrices."""
     if len(shards) == 0:
         raise ValueError("need at least one shard of logits")
+    if len(shards) > rog_max_peers():
+        raise ValueError("at most %d shards (got %d)" % (rog_max_peers(), len(shards)))
     first = shards[0]
     if not isinstance(first, torch.Tensor):
         raise TypeError("shards[0] must be a torch.Tensor")
@@ -685,35 +709,45 @@ def _shard_array(shards):
         raise ValueError("logits are float32, bfloat16 or float16 (got %s)" % dtype)
     if first.dim() != 2:
         raise ValueError("shards[0] must be a matrix (got %s)" % (tuple(first.shape),))
-    rows = first.shape[0]
-    arr = (rog_logit_shard * len(shards))()
+    rows, idx = first.size(0), first.get_device()
+    if idx < 0:
+        _matrix_error(first, "shards[0]", rows, dtype, device)
+    vals = []
     for i, x in enumerate(shards):
-        _check_matrix(x, "shards[%d]" % i, rows, dtype, device)
-        s = arr[i]
-        s.logits, s.row_stride, s.width = x.data_ptr(), x.stride(0), x.shape[1]
-    return device, rows, DTYPES[dtype], arr
+        try:
+            n, width = x.shape
+            stride, step = x.stride()
+            ok = n == rows and x.dtype is dtype and x.get_device() == idx and (step == 1 or width <= 1)
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            _matrix_error(x, "shards[%d]" % i, rows, dtype, device)
+        vals += (x.data_ptr(), stride, width)
+    return device, idx, rows, dtype, _PACK_SHARDS[len(shards)](*vals)
+
+
+def _logprob_plan(packed, W: int, rows: int, dtype: int, top_k: int, form: int) -> rog_head_plan_info:
+    info = rog_head_plan_info()
+    _check(_lib.rog_logprob_plan(packed, W, rows, dtype, top_k, form, ctypes.byref(info)), "rog_logprob_plan")
+    return info
+
+
+def _logprob_plan_dict(info) -> dict:
+    return {"form": LOGPROB_FORM_NAMES[info.form], "grid": info.grid, "block": info.block, "blocks": info.blocks,
+            "workspace_bytes": info.workspace_bytes}
 
 
 def rog_logprob_plan(shards: Sequence[torch.Tensor], top_k: int = 0, form: int = ROG_LOGPROB_AUTO) -> dict:
     """The launch rog_logprob_ex would make for these logits (no GPU work)."""
-    _, rows, dt, arr = _shard_array(shards)
-    return _logprob_plan(arr, rows, dt, top_k, form)
-
-
-def _logprob_plan(arr, rows: int, dtype: int, top_k: int, form: int) -> dict:
-    info = rog_head_plan_info()
-    _check(_lib.rog_logprob_plan(arr, len(arr), rows, dtype, top_k, form, ctypes.byref(info)), "rog_logprob_plan")
-    return {"form": LOGPROB_FORM_NAMES[info.form], "grid": info.grid, "block": info.block, "blocks": info.blocks,
-            "workspace_bytes": info.workspace_bytes}
+    _, _, rows, dtype, packed = _shard_bytes(shards)
+    return _logprob_plan_dict(_logprob_plan(packed, len(shards), rows, DTYPES[dtype], top_k, form))
 
 
 def rog_logprob_plan_widths(widths: Sequence[int], rows: int, dtype: int, top_k: int = 0,
                             form: int = ROG_LOGPROB_AUTO) -> dict:
     """rog_logprob_plan from the shards' widths alone."""
-    arr = (rog_logit_shard * max(1, len(widths)))()
-    for s, w in zip(arr, widths):
-        s.width = w
-    return _logprob_plan(arr, rows, dtype, top_k, form)
+    packed = struct.pack("=" + "Qqq" * len(widths), *(v for w in widths for v in (0, 0, w)))
+    return _logprob_plan_dict(_logprob_plan(packed, len(widths), rows, dtype, top_k, form))
 
 
 def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor] = None, top_k: int = 0,
@@ -721,30 +755,29 @@ def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor
                    workspace: Optional[torch.Tensor] = None, stream=None,
                    form: int = ROG_LOGPROB_AUTO) -> RogLogprob:
     """rog_logprob with the launch form forced (never changes the bits)."""
-    device, rows, dt, arr = _shard_array(shards)
-    if not 0 <= top_k <= rog_max_top_k():
-        raise ValueError("top_k must be in [0, %d]" % rog_max_top_k())
+    device, idx, rows, dtype, packed = _shard_bytes(shards)
+    if not 0 <= top_k <= _MAX_TOP_K:
+        raise ValueError("top_k must be in [0, %d]" % _MAX_TOP_K)
+    f32, i64 = torch.float32, torch.int64
     if out is None:
-        new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=device)  # noqa: E731
+        new = lambda *shape, dtype=f32: torch.empty(*shape, dtype=dtype, device=device)  # noqa: E731
         out = RogLogprob(new(rows) if tokens is not None else None, new(rows), new(rows),
-                         new(rows, top_k) if top_k else None,
-                         new(rows, top_k, dtype=torch.int64) if top_k else None)
+                         new(rows, top_k) if top_k else None, new(rows, top_k, dtype=i64) if top_k else None)
     elif not isinstance(out, RogLogprob):
         out = RogLogprob(*out)
-    o = rog_logprob_out()
-    o.logp = _check_vector(out.logp, "out.logp", rows, torch.float32, device)
-    o.entropy = _check_vector(out.entropy, "out.entropy", rows, torch.float32, device)
-    o.lse = _check_vector(out.lse, "out.lse", rows, torch.float32, device)
-    o.top_logp = _check_vector(out.top_logp, "out.top_logp", rows * top_k, torch.float32, device)
-    o.top_ids = _check_vector(out.top_ids, "out.top_ids", rows * top_k, torch.int64, device)
-    tok = _check_vector(tokens, "tokens", rows, torch.int64, device)
-    info = rog_head_plan_info()
-    _check(_lib.rog_logprob_plan(arr, len(arr), rows, dt, top_k, form, ctypes.byref(info)), "rog_logprob")
+    tops = rows * top_k
+    outs = _pack_addresses5(_vector(out.logp, "out.logp", rows, f32, device, idx),
+                            _vector(out.entropy, "out.entropy", rows, f32, device, idx),
+                            _vector(out.lse, "out.lse", rows, f32, device, idx),
+                            _vector(out.top_logp, "out.top_logp", tops, f32, device, idx),
+                            _vector(out.top_ids, "out.top_ids", tops, i64, device, idx))
+    tok = _vector(tokens, "tokens", rows, i64, device, idx) or None
+    W, dt = len(shards), DTYPES[dtype]
     with _on_device(device):
         handle = _stream_handle(stream, device)
-        ws, ws_bytes = _workspace(workspace, info.workspace_bytes, device, stream, handle)
-        _check(_lib.rog_logprob_ex(arr, len(arr), rows, dt, temperature, tok or None, top_k, ctypes.byref(o), ws,
-                                   ws_bytes, handle, form), "rog_logprob")
+        _with_workspace(lambda ws, n: _lib.rog_logprob_ex(packed, W, rows, dt, temperature, tok, top_k, outs, ws, n, handle, form),
+                        lambda: _logprob_plan(packed, W, rows, dt, top_k, form).workspace_bytes,
+                        "rog_logprob", workspace, device, stream, handle)
     return out
 
 
@@ -767,29 +800,35 @@ def rog_logprob_grad(shards: Sequence[torch.Tensor], tokens: torch.Tensor, lse: 
     """Gradient of sum_i (g_logp[i] logp[i] + g_entropy[i] entropy[i]) in every
     shard, from rog_logprob's ``lse`` and ``entropy``.  ``out``: W matrices to
     write; ``out[r]`` may be ``shards[r]`` (in place)."""
-    device, rows, dt, arr = _shard_array(shards)
+    device, idx, rows, dtype, packed = _shard_bytes(shards)
     if out is None:
-        out = [torch.empty(rows, x.shape[1], dtype=x.dtype, device=device) for x in shards]
-    out = list(out)
-    if len(out) != len(arr):
+        out = [torch.empty(rows, x.shape[1], dtype=dtype, device=device) for x in shards]
+    W = len(shards)
+    if len(out) != W:
         raise ValueError("one gradient per shard")
-    grads = (rog_grad_shard * len(arr))()
-    for i, (g, x) in enumerate(zip(out, shards)):
-        _check_matrix(g, "out[%d]" % i, rows, x.dtype, device)
-        if g.shape[1] != x.shape[1]:
-            raise ValueError("out[%d] must have the shape of shards[%d]" % (i, i))
-        grads[i].grad, grads[i].row_stride = g.data_ptr(), g.stride(0)
-    f32 = torch.float32
+    vals = []
+    for i, g in enumerate(out):
+        try:
+            shape = g.shape
+            stride, step = g.stride()
+            ok = shape == shards[i].shape and g.dtype is dtype and g.get_device() == idx and (step == 1 or shape[1] <= 1)
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            if isinstance(g, torch.Tensor) and g.dim() == 2 and g.shape != shards[i].shape:
+                raise ValueError("out[%d] must have the shape of shards[%d]" % (i, i))
+            _matrix_error(g, "out[%d]" % i, rows, dtype, device)
+        vals += (g.data_ptr(), stride)
     if tokens is None or lse is None or entropy is None or g_logp is None:
         raise ValueError("tokens, lse, entropy and g_logp are needed")
-    args = [_check_vector(tokens, "tokens", rows, torch.int64, device),
-            _check_vector(lse, "lse", rows, f32, device), _check_vector(entropy, "entropy", rows, f32, device),
-            _check_vector(g_logp, "g_logp", rows, f32, device),
-            _check_vector(g_entropy, "g_entropy", rows, f32, device) or None]
+    f32 = torch.float32
+    tok = _vector(tokens, "tokens", rows, torch.int64, device, idx)
+    vec = [_vector(t, what, rows, f32, device, idx) for t, what in
+           ((lse, "lse"), (entropy, "entropy"), (g_logp, "g_logp"), (g_entropy, "g_entropy"))]
     with _on_device(device):
-        _check(_lib.rog_logprob_grad(arr, grads, len(arr), rows, dt, temperature, *args,
-                                     _stream_handle(stream, device)), "rog_logprob_grad")
-    return out
+        _check(_lib.rog_logprob_grad(packed, _PACK_GRADS[W](*vals), W, rows, DTYPES[dtype], temperature, tok, vec[0], vec[1],
+                                     vec[2], vec[3] or None, _stream_handle(stream, device)), "rog_logprob_grad")
+    return out if isinstance(out, list) else list(out)
 
 
 def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Tensor,
@@ -803,26 +842,24 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
     (0: the token counts for nothing; None: 1 / n each)."""
     if not isinstance(logp, torch.Tensor):
         raise TypeError("logp must be a torch.Tensor")
-    device, n, f32 = logp.device, logp.numel(), torch.float32
-    i, o = rog_policy_in(), rog_policy_out()
-    i.logp = _check_vector(logp, "logp", n, f32, device)
-    i.old_logp = _check_vector(old_logp, "old_logp", n, f32, device)
-    i.advantage = _check_vector(advantage, "advantage", n, f32, device)
-    i.weight = _check_vector(weight, "weight", n, f32, device)
-    i.ref_logp = _check_vector(ref_logp, "ref_logp", n, f32, device)
-    i.entropy = _check_vector(entropy, "entropy", n, f32, device)
+    device, n, f32, idx = logp.device, logp.numel(), torch.float32, logp.get_device()
+    if idx < 0:
+        _check_tensor(logp, "logp", device)
+    if old_logp is None or advantage is None:
+        raise ValueError("old_logp and advantage are needed")
+    ins = _pack_addresses6(_vector(logp, "logp", n, f32, device, idx), _vector(old_logp, "old_logp", n, f32, device, idx),
+                           _vector(advantage, "advantage", n, f32, device, idx), _vector(weight, "weight", n, f32, device, idx),
+                           _vector(ref_logp, "ref_logp", n, f32, device, idx), _vector(entropy, "entropy", n, f32, device, idx))
     if out is None:
         out = RogPolicyLoss(torch.empty(4, dtype=f32, device=device), torch.empty(n, dtype=f32, device=device),
                             torch.empty(n, dtype=f32, device=device) if entropy is not None else None)
     elif not isinstance(out, RogPolicyLoss):
         out = RogPolicyLoss(*out)
-    o.stats = _check_vector(out.stats, "out.stats", 4, f32, device)
-    o.g_logp = _check_vector(out.g_logp, "out.g_logp", n, f32, device)
-    o.g_entropy = _check_vector(out.g_entropy, "out.g_entropy", n, f32, device)
-    k = rog_policy_params(clip_low, clip_high, kl_coef, entropy_coef, grad_scale)
+    outs = _pack_addresses3(_vector(out.stats, "out.stats", 4, f32, device, idx), _vector(out.g_logp, "out.g_logp", n, f32, device, idx),
+                            _vector(out.g_entropy, "out.g_entropy", n, f32, device, idx))
+    params = _pack_floats5(clip_low, clip_high, kl_coef, entropy_coef, grad_scale)
     with _on_device(device):
         handle = _stream_handle(stream, device)
-        ws, ws_bytes = _workspace(workspace, _lib.rog_policy_loss_workspace_bytes(n), device, stream, handle)
-        _check(_lib.rog_policy_loss(ctypes.byref(i), n, ctypes.byref(k), ctypes.byref(o), ws, ws_bytes, handle),
-               "rog_policy_loss")
+        _with_workspace(lambda ws, b: _lib.rog_policy_loss(ins, n, params, outs, ws, b, handle),
+                        lambda: _lib.rog_policy_loss_workspace_bytes(n), "rog_policy_loss", workspace, device, stream, handle)
     return out
