@@ -32,10 +32,12 @@ constexpr int kHeadThreads = 256;          // a workgroup: four waves, one per u
 constexpr uint32_t kGradPieceBytes = 2048; // the gradient's piece of a row: two 16-byte vectors per lane of one wave
 // The grid of a launch of `groups` workgroups (below 2^31): a dispatch counts the
 // work-items of each dimension in 32 bits, so more than 2^22 go over two.  The
-// kernels number a workgroup blockIdx.y * gridDim.x + blockIdx.x, and those
-// past the end leave at once.
+// kernels number a workgroup by head_group() (a constant row length: the grid's
+// own would be one more line of kernel arguments), and those past the end leave
+// at once.
+constexpr uint32_t kGridRowLog = 22;
 inline dim3 head_grid(uint32_t groups) {
-    const uint32_t most = 1u << 22;
+    const uint32_t most = 1u << kGridRowLog;
     return groups <= most ? dim3(groups) : dim3(most, (groups + most - 1) / most);
 }
 constexpr int kMaxTopK = 32;
@@ -80,44 +82,52 @@ constexpr size_t kHeadCounterBytes = size_t(kHeadCounters) * kCounterStride * si
 // then 64 lanes' maxima for each of four entries per unit.
 constexpr uint32_t kUnitFloats = 4 + 4 * 64;
 
+struct Shard {
+    const void *x;                     // element (0, 0)
+    int64_t stride;                    // bytes from a row to the next
+    uint32_t width;                    // columns
+    uint32_t col0;                     // the shard's first column in the row
+};
+// The shards of a row, cut into blocks.
 struct HeadShards {
-    const void *x[kMaxPeers];          // element (0, 0) of each shard
-    int64_t stride[kMaxPeers];         // bytes from a row to the next
-    uint32_t width[kMaxPeers];         // columns
-    uint32_t col0[kMaxPeers];          // the shard's first column in the row
-    uint32_t block0[kMaxPeers + 1];    // the shard's first block; [W]: all blocks
+    uint32_t W;
+    uint32_t blocks;                   // of a row
     uint32_t even;                     // blocks of every shard where they have as many each, else 0
     Divider even_div;                  // divides by it
+    Shard s[kMaxPeers];
+    uint32_t block0[kMaxPeers + 1];    // the shard's first block; [W]: all blocks
 };
 
+// What every workgroup reads first stands together at the front (the first
+// read of each 64-byte line of the arguments takes more than half a
+// microsecond), up to the first shard.
 struct LogprobArgs {
-    HeadShards sh;
     const int64_t *tokens;             // NULL: no token, every row scored
+    uint32_t rows;
+    uint32_t chunks, units;            // units that have blocks
+    uint32_t slot_shift;               // log2 of a wave's blocks that one entry of the top-k table covers
+    uint32_t top_k;
+    uint32_t vocab;
+    float scale;                       // log2(e) / temperature
+    float inv_t;                       // 1 / temperature
+    float bound;                       // |x| that leaves the scaled range; binary16: its largest
     float *logp, *entropy, *lse, *top_logp;
     int64_t *top_ids;
     uint32_t *counters;                // split: one per row
     float *part;                       // split: per row, the units' states and their lanes' maxima
-    float scale;                       // log2(e) / temperature
-    float inv_t;                       // 1 / temperature
-    float bound;                       // |x| that leaves the scaled range; binary16: its largest
-    uint32_t W, rows, blocks;
-    uint32_t chunks, units;            // units that have blocks
-    uint32_t top_k;
-    uint32_t slot_shift;               // log2 of a wave's blocks that one entry of the top-k table covers
-    uint32_t vocab;
+    HeadShards sh;
 };
 
 struct LogprobGradArgs {
-    HeadShards sh;
-    void *g[kMaxPeers];
-    int64_t g_stride[kMaxPeers];       // bytes
     const int64_t *tokens;
     const float *lse, *entropy, *g_logp, *g_entropy;
     float scale, inv_t;
-    uint32_t W, rows, vocab;
-    uint32_t pieces;                   // of a row (HeadShards' blocks are pieces here)
-    Divider pieces_div;
+    uint32_t rows, vocab;
     uint32_t groups;                   // pieces of all rows
+    Divider pieces_div;                // divides by sh.blocks, the pieces of a row
+    HeadShards sh;                     // its blocks are pieces here
+    void *g[kMaxPeers];
+    int64_t g_stride[kMaxPeers];       // bytes
 };
 
 struct PolicyArgs {

@@ -94,6 +94,20 @@ struct BlockAt {
     uint32_t off;       // the first column's number in the shard
 };
 
+__device__ __forceinline__ uint32_t head_group() { return blockIdx.y << kGridRowLog | blockIdx.x; }
+
+// Has the front of the arguments read in one go, into scalar registers and the
+// scalar cache, before anything waits for a part of it.
+__device__ __forceinline__ void hold_front(const LogprobArgs &a) {
+    asm volatile("" ::"s"(a.tokens), "s"(a.rows), "s"(a.units), "s"(a.scale), "s"(a.bound), "s"(a.lse), "s"(a.part), "s"(a.sh.W),
+                 "s"(a.sh.blocks), "s"(a.sh.even), "s"(a.sh.s[0].x), "s"(a.sh.s[0].stride), "s"(a.sh.s[0].width));
+}
+__device__ __forceinline__ void hold_front(const LogprobGradArgs &a) {
+    asm volatile("" ::"s"(a.tokens), "s"(a.lse), "s"(a.entropy), "s"(a.g_logp), "s"(a.g_entropy), "s"(a.scale), "s"(a.inv_t),
+                 "s"(a.groups), "s"(a.sh.W), "s"(a.sh.blocks), "s"(a.sh.even), "s"(a.sh.s[0].x), "s"(a.sh.s[0].stride),
+                 "s"(a.sh.s[0].width));
+}
+
 // Walks through one row's blocks (of COLUMNS columns), in rising order: the current shard's layout
 // stays in scalar registers, and kernel arguments are read only where a shard
 // begins.
@@ -105,26 +119,31 @@ struct Cursor {
     uint32_t width, col0;
 
     __device__ __forceinline__ Cursor(const HeadShards &shards, uint32_t r) : h(shards), row(r), shard(0), end(0) {}
-    __device__ __forceinline__ void enter(uint32_t s) {
-        shard = s;
-        width = h.width[s];
-        col0 = h.col0[s];
-        base = (gbyte *)h.x[s] + int64_t(row) * h.stride[s];
+    __device__ __forceinline__ void enter(uint32_t r) {
+        const Shard &s = h.s[r];
+        shard = r;
+        width = s.width;
+        col0 = s.col0;
+        base = (gbyte *)s.x + int64_t(row) * s.stride;
     }
     // Block b (below the row's blocks, not before the shard that the cursor is in).
     __device__ __forceinline__ BlockAt at(uint32_t b) {
         if (b >= end) {
-            if (h.even) {
-                const uint32_t s = divide(b, h.even_div);
-                first = s * h.even;
+            if (h.W == 1) {
+                first = 0;
+                end = h.blocks;
+                enter(0);
+            } else if (h.even) {
+                const uint32_t r = divide(b, h.even_div);
+                first = r * h.even;
                 end = first + h.even;
-                enter(s);
+                enter(r);
             } else {
-                uint32_t s = shard;
-                while (h.block0[s + 1] <= b) ++s;
-                first = h.block0[s];
-                end = h.block0[s + 1];
-                enter(s);
+                uint32_t r = shard;
+                while (h.block0[r + 1] <= b) ++r;
+                first = h.block0[r];
+                end = h.block0[r + 1];
+                enter(r);
             }
         }
         const uint32_t off = (b - first) * COLUMNS, left = width - off;

@@ -64,19 +64,20 @@ rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dty
             if (rows && s.width && (!s.logits || addr(s.logits) % es)) return ROG_ERR_INVALID_ARGUMENT;
         }
         if (uint64_t(s.width) >= kMaxVocab || v + uint64_t(s.width) >= kMaxVocab) return ROG_ERR_TOO_LARGE;
-        h->x[r] = s.logits;
-        h->width[r] = uint32_t(s.width);
-        h->col0[r] = uint32_t(v);
+        Shard &o = h->s[r];
+        o = Shard{s.logits, 0, uint32_t(s.width), uint32_t(v)};
         h->block0[r] = uint32_t(b);
         v += uint64_t(s.width);
         b += ceil_div(uint64_t(s.width), block);
         if (addresses) {
             if (uint64_t(s.row_stride) >= uint64_t(1) << 48) return ROG_ERR_TOO_LARGE;
-            h->stride[r] = s.row_stride * es;
-            if (!fits(addr(s.logits), rows, uint64_t(h->stride[r]), uint64_t(s.width) * es)) return ROG_ERR_TOO_LARGE;
+            o.stride = s.row_stride * es;
+            if (!fits(addr(s.logits), rows, uint64_t(o.stride), uint64_t(s.width) * es)) return ROG_ERR_TOO_LARGE;
         }
     }
     h->block0[W] = uint32_t(b);
+    h->W = uint32_t(W);
+    h->blocks = uint32_t(b);
     h->even = h->block0[1];
     for (int r = 1; r < W; ++r)
         if (h->block0[r + 1] - h->block0[r] != h->even) h->even = 0;
@@ -150,7 +151,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
             if (overlap(outs[i], outs[j])) return ROG_ERR_OVERLAP;
         if (tokens && overlap(outs[i], flat(tokens, rows * 8))) return ROG_ERR_OVERLAP;
         for (int r = 0; r < W; ++r)
-            if (overlap(outs[i], Strip{addr(a.sh.x[r]), rows, uint64_t(a.sh.stride[r]), uint64_t(a.sh.width[r]) * esize(dtype)}))
+            if (overlap(outs[i], Strip{addr(a.sh.s[r].x), rows, uint64_t(a.sh.s[r].stride), uint64_t(a.sh.s[r].width) * esize(dtype)}))
                 return ROG_ERR_OVERLAP;
     }
 
@@ -165,9 +166,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     a.scale = float(kLog2E / double(temperature));
     a.inv_t = float(1.0 / double(temperature));
     a.bound = dtype == ROG_DTYPE_F16 ? 65504.0f : float(ldexp(double(temperature) / kLog2E, 30));
-    a.W = uint32_t(W);
     a.rows = uint32_t(rows);
-    a.blocks = blocks;
     a.chunks = chunks_of(blocks);
     a.units = units_of(blocks);
     a.top_k = uint32_t(top_k);
@@ -195,12 +194,12 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
         return ROG_ERR_INVALID_ARGUMENT;
     const uint32_t es = esize(dtype);
     for (int r = 0; r < W; ++r) {
-        const uint64_t width = uint64_t(a.sh.width[r]) * es;
+        const uint64_t width = uint64_t(a.sh.s[r].width) * es;
         a.g[r] = grads[r].grad;
         a.g_stride[r] = 0;
         if (!width) continue;
         if (!grads[r].grad || addr(grads[r].grad) % es || grads[r].row_stride < 0 ||
-            (rows > 1 && uint64_t(grads[r].row_stride) < a.sh.width[r]))
+            (rows > 1 && uint64_t(grads[r].row_stride) < a.sh.s[r].width))
             return ROG_ERR_INVALID_ARGUMENT;
         if (uint64_t(grads[r].row_stride) >= uint64_t(1) << 48) return ROG_ERR_TOO_LARGE;
         a.g_stride[r] = grads[r].row_stride * es;
@@ -208,12 +207,12 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     }
     const float *const vectors[4] = {lse, entropy, g_logp, g_entropy};
     for (int r = 0; r < W; ++r) {
-        const Strip g{addr(a.g[r]), rows, uint64_t(a.g_stride[r]), uint64_t(a.sh.width[r]) * es};
+        const Strip g{addr(a.g[r]), rows, uint64_t(a.g_stride[r]), uint64_t(a.sh.s[r].width) * es};
         for (int q = 0; q < W; ++q) {
-            const Strip x{addr(a.sh.x[q]), rows, uint64_t(a.sh.stride[q]), uint64_t(a.sh.width[q]) * es};
+            const Strip x{addr(a.sh.s[q].x), rows, uint64_t(a.sh.s[q].stride), uint64_t(a.sh.s[q].width) * es};
             const bool in_place = q == r && g.at == x.at && (rows == 1 || g.stride == x.stride);
             if (!in_place && overlap(g, x)) return ROG_ERR_OVERLAP;
-            if (q < r && overlap(g, Strip{addr(a.g[q]), rows, uint64_t(a.g_stride[q]), uint64_t(a.sh.width[q]) * es}))
+            if (q < r && overlap(g, Strip{addr(a.g[q]), rows, uint64_t(a.g_stride[q]), uint64_t(a.sh.s[q].width) * es}))
                 return ROG_ERR_OVERLAP;
         }
         for (const float *v : vectors)
@@ -227,10 +226,8 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     a.g_entropy = g_entropy;
     a.scale = float(kLog2E / double(temperature));
     a.inv_t = float(1.0 / double(temperature));
-    a.W = uint32_t(W);
     a.rows = uint32_t(rows);
     a.vocab = vocab;
-    a.pieces = blocks;
     a.pieces_div = make_divider(blocks);
     const uint64_t pieces = uint64_t(blocks) * rows;
     if (pieces >= kMaxGroups) return ROG_ERR_TOO_LARGE;

@@ -70,11 +70,12 @@ struct Places {
     uint32_t width[kMaxPeers], col0[kMaxPeers], block0[kMaxPeers];
     // by one wave, lane r bringing shard r; the LDS writes wait for the kernel arguments
     __device__ __forceinline__ void fill(const LogprobArgs &a, uint32_t lane) {
-        if (lane < a.W) {
-            x[lane] = reinterpret_cast<uint64_t>(a.sh.x[lane]);
-            stride[lane] = a.sh.stride[lane];
-            width[lane] = a.sh.width[lane];
-            col0[lane] = a.sh.col0[lane];
+        if (lane < a.sh.W) {
+            const Shard &s = a.sh.s[lane];
+            x[lane] = reinterpret_cast<uint64_t>(s.x);
+            stride[lane] = s.stride;
+            width[lane] = s.width;
+            col0[lane] = s.col0;
             block0[lane] = a.sh.block0[lane];
         }
     }
@@ -82,7 +83,7 @@ struct Places {
     __device__ __forceinline__ BlockAt at(const LogprobArgs &a, uint32_t row, uint32_t b) const {
         uint32_t r = 0;            // the last shard that begins at or before block b
         for (uint32_t step = kMaxPeers / 2; step; step /= 2)
-            if (step < a.W && r + step < a.W && block0[r + step] <= b) r += step;
+            if (step < a.sh.W && r + step < a.sh.W && block0[r + step] <= b) r += step;
         const uint32_t off = (b - block0[r]) * kHeadBlock, left = width[r] - off;
         return BlockAt{(gbyte *)(x[r] + uint64_t(int64_t(row) * stride[r]) + uint64_t(off) * Logit<DT>::kSize),
                        left < kHeadBlock ? left : kHeadBlock, col0[r] + off, r, off};
@@ -180,7 +181,7 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
         for (uint64_t q = tid; q < tasks; q += T::kThreads) {
             const uint32_t e = top.hits[q >> vecs_shift], i = uint32_t(q) & ((1u << vecs_shift) - 1);
             const uint32_t b = slot_block<T>(e / 64, i / Logit<DT>::kVecs, shift), el = e % 64;
-            if (b >= a.blocks) continue;
+            if (b >= a.sh.blocks) continue;
             const BlockAt at = top.places.template at<DT>(a, row, b);
             const uint32_t vi = i % Logit<DT>::kVecs;
             const vec16 vec = load_vec<DT>(at.p, at.n, vi, el);
@@ -253,8 +254,9 @@ __device__ __forceinline__ float token_logit(const LogprobArgs &a, uint32_t row,
     if (token >= int64_t(a.vocab)) return 0.0f;
     const uint32_t tok = uint32_t(token);
     uint32_t r = 0;
-    while (r + 1 < a.W && a.sh.col0[r + 1] <= tok) ++r;
-    return load_logit<DT>((gbyte *)a.sh.x[r] + int64_t(row) * a.sh.stride[r] + uint64_t(tok - a.sh.col0[r]) * Logit<DT>::kSize);
+    while (r + 1 < a.sh.W && a.sh.s[r + 1].col0 <= tok) ++r;
+    const Shard &s = a.sh.s[r];
+    return load_logit<DT>((gbyte *)s.x + int64_t(row) * s.stride + uint64_t(tok - s.col0) * Logit<DT>::kSize);
 }
 
 // How many of a wave's share of a row's columns equal x: blocks first, first + step, ...
@@ -262,7 +264,7 @@ template <int DT>
 __device__ __forceinline__ uint32_t count_equal(const LogprobArgs &a, uint32_t row, uint32_t first, uint32_t step, uint32_t lane, float x) {
     uint32_t n = 0;
     Cursor<DT> cur(a.sh, row);
-    for (uint32_t b = first; b < a.blocks; b += step) {
+    for (uint32_t b = first; b < a.sh.blocks; b += step) {
         const BlockAt at = cur.at(b);
 #pragma unroll 1
         for (uint32_t k = lane; k < at.n; k += 64) n += load_logit<DT>(at.p + k * Logit<DT>::kSize) == x;
@@ -392,14 +394,15 @@ template <int DT, bool TOP, bool NT>
 __global__ __launch_bounds__(kHeadThreads) void rog_logprob_row_kernel(LogprobArgs) {
     typedef Team<kHeadThreads> T;
     const LogprobArgs &a = launch_args<LogprobArgs>();
+    hold_front(a);
     __shared__ Shared sh;
     __shared__ typename SharedFor<T, TOP>::type top;
     const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
     const Scaling c{a.scale, a.bound};
-    const uint32_t row = blockIdx.y * gridDim.x + blockIdx.x;
+    const uint32_t row = head_group();
     if (row >= a.rows) return;
     // the loads first: the token only says whether they count
-    const uint32_t mine = a.blocks > w ? (a.blocks - w + kChunkUnits - 1) / kChunkUnits : 0;
+    const uint32_t mine = a.sh.blocks > w ? (a.sh.blocks - w + kChunkUnits - 1) / kChunkUnits : 0;
     BlockStream<DT, NT> blocks(a, row, wave_block(w, 0), kChunkUnits, mine, lane);
     const int64_t tok = row_token(a, row);
     if (tok < 0) {
@@ -449,18 +452,19 @@ template <int DT, bool TOP>
 __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(LogprobArgs) {
     typedef Team<kHeadThreads> T;
     const LogprobArgs &a = launch_args<LogprobArgs>();
+    hold_front(a);
     __shared__ Shared sh;
     __shared__ typename SharedFor<T, TOP>::type top;
     const uint32_t tid = threadIdx.x, lane = tid & 63, w = uniform(tid / 64);
     const Scaling c{a.scale, a.bound};
-    const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
+    const uint32_t group = head_group();
     const uint32_t row = group / a.units, u = group % a.units;
     if (row >= a.rows) return;
     const uint32_t first = u / kChunkUnits * kChunkBlocks + u % kChunkUnits, b = first + w * kChunkUnits;
     // the loads first: the token only says whether they count
     vec16 v[Logit<DT>::kVecs];
     BlockAt at;
-    if (b < a.blocks) {
+    if (b < a.sh.blocks) {
         at = Cursor<DT>(a.sh, row).at(b);
         load_block<DT, false>(at, lane, v);
     }
@@ -475,7 +479,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
     // entries of a unit in the table: as many as its blocks, or fewer, wider ones
     const uint32_t entry_shift = min(a.slot_shift, 2u), entry_log = 2 - entry_shift, entries = 1u << entry_log;
     State st = no_state(c);
-    if (b < a.blocks) st = block_state<DT>(at.p, at.n, v, lane, c);
+    if (b < a.sh.blocks) st = block_state<DT>(at.p, at.n, v, lane, c);
     sh.lane_m[w][lane] = st.m;
     sh.lane_s[w][lane] = st.s;
     sh.lane_t[w][lane] = st.t;
@@ -484,7 +488,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
         State unit = st;
 #pragma unroll
         for (uint32_t i = 1; i < kUnitBlocks; ++i)
-            if (first + i * kChunkUnits < a.blocks)
+            if (first + i * kChunkUnits < a.sh.blocks)
                 unit = join(unit, make_state(sh.lane_m[i][lane], sh.lane_s[i][lane], sh.lane_t[i][lane], c));
         const State all = join_lanes(unit, c);
         if (lane < 3) publish(states + u * 4 + lane, lane == 0 ? all.m : lane == 1 ? all.s : all.t);
@@ -549,13 +553,14 @@ template <int DT, bool TOP, bool NT>
 __global__ __launch_bounds__(64 * kWaveRows) void rog_logprob_wave_kernel(LogprobArgs) {
     typedef Team<64> T;
     const LogprobArgs &a = launch_args<LogprobArgs>();
+    hold_front(a);
     __shared__ uint32_t equal[kWaveRows];
     __shared__ typename SharedFor<T, TOP>::type top[kWaveRows];
     const uint32_t lane = threadIdx.x & 63, w = uniform(threadIdx.x / 64);
     const Scaling c{a.scale, a.bound};
-    const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kWaveRows + w;
+    const uint32_t row = head_group() * kWaveRows + w;
     if (row >= a.rows) return;
-    BlockStream<DT, NT> blocks(a, row, 0, 1, a.blocks, lane);
+    BlockStream<DT, NT> blocks(a, row, 0, 1, a.sh.blocks, lane);
     const int64_t tok = row_token(a, row);
     if (tok < 0) {
         write_plain_row(a, row, lane, 64, 0.0f, 0.0f, 0.0f, 0.0f);
@@ -565,7 +570,7 @@ __global__ __launch_bounds__(64 * kWaveRows) void rog_logprob_wave_kernel(Logpro
     State unit = no_state(c);
     if constexpr (TOP) {
         Cursor<DT> cur(a.sh, row);
-        for (uint32_t b = 0; b < a.blocks; ++b) {
+        for (uint32_t b = 0; b < a.sh.blocks; ++b) {
             const BlockAt at = cur.at(b);
             if (lane == 0) top[w].places.set(b, at);
         }
@@ -575,7 +580,7 @@ __global__ __launch_bounds__(64 * kWaveRows) void rog_logprob_wave_kernel(Logpro
         unit = b == 0 ? st : join(unit, st);
     });
     if constexpr (TOP) {
-        for (uint32_t b = a.blocks; b < kUnitBlocks; ++b) top[w].tab[b * 64 + lane] = -kInf;
+        for (uint32_t b = a.sh.blocks; b < kUnitBlocks; ++b) top[w].tab[b * 64 + lane] = -kInf;
     }
     const State all = join_lanes(unit, c);
     if (lane == 0) equal[w] = 0;

@@ -25,11 +25,12 @@ constexpr float kExtreme = 7.442609e8f;                 // 2^30 ln 2, where rog_
 template <int DT, bool NT>
 __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
     const LogprobGradArgs &a = launch_args<LogprobGradArgs>();
+    hold_front(a);
     constexpr uint32_t per = Logit<DT>::kPerVec, vecs = kGradPieceBytes / (64 * 16), each = vecs * per;
     const uint32_t lane = threadIdx.x;
-    const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
+    const uint32_t group = head_group();
     if (group >= a.groups) return;
-    const uint32_t row = divide(group, a.pieces_div), piece = group - row * a.pieces;
+    const uint32_t row = divide(group, a.pieces_div), piece = group - row * a.sh.blocks;
     // everything that a wave needs of its row, asked for at once
     const int64_t tok = a.tokens[row];
     const float lse = a.lse[row], H = a.entropy[row], g = a.g_logp[row], h = a.g_entropy ? a.g_entropy[row] : 0.0f;
