@@ -92,6 +92,7 @@ struct BlockAt {
     uint32_t col;
     uint32_t shard;
     uint32_t off;       // the first column's number in the shard
+    bool shift;         // a full block of 2-byte logits between two 32-bit words
 };
 
 __device__ __forceinline__ uint32_t head_group() { return blockIdx.y << kGridRowLog | blockIdx.x; }
@@ -147,7 +148,8 @@ struct Cursor {
             }
         }
         const uint32_t off = (b - first) * COLUMNS, left = width - off;
-        return BlockAt{base + uint64_t(off) * Logit<DT>::kSize, left < COLUMNS ? left : COLUMNS, col0 + off, shard, off};
+        const bool shift = DT != ROG_DTYPE_F32 && left >= COLUMNS && (reinterpret_cast<uintptr_t>((const uint8_t *)base) & 2) != 0;
+        return BlockAt{base + uint64_t(off) * Logit<DT>::kSize, left < COLUMNS ? left : COLUMNS, col0 + off, shard, off, shift};
     }
 };
 
@@ -190,23 +192,58 @@ __device__ __forceinline__ vec16 load_vec(gbyte *p, uint32_t n, uint32_t i, uint
     return *(gvec16any *)(p + vec_place<DT>(n, i, lane) * Logit<DT>::kSize);
 }
 
+// A block's vectors as loaded, and the 32-bit word behind them.
+template <uint32_t VECS>
+struct Loaded {
+    vec16 v[VECS];
+    uint32_t behind;
+};
+
 // Issues the loads of a block.  They are issued whatever the block, so that no
 // branch joins registers that loads are still on their way to: a block of less
 // than one vector (read where it is used, tiny_state) reads the first bytes of
-// the kernel arguments instead, and with `real`
-// false every lane reads the block's first bytes.
+// the kernel arguments instead, and with `real` false every lane reads the
+// block's first bytes.
+//
+// 16-byte loads at odd multiples of two bytes are slow (4000 x 100003 bf16,
+// where every other row begins so: 165 us against 127 for 100002 columns).  A
+// full block there (`shift`) is read from the 32-bit word before, two bytes
+// early, with one word more behind it (whose other half may lie past the row,
+// never past the word); aligned_block puts the columns where they belong.
 template <int DT, bool NT, uint32_t VECS>
-__device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, vec16 (&v)[VECS], bool real = true) {
+__device__ __forceinline__ void load_block(const BlockAt &b, uint32_t lane, Loaded<VECS> &l, bool real = true) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const bool tiny = b.n < per;
-    gbyte *const p = tiny ? (gbyte *)__builtin_amdgcn_kernarg_segment_ptr() : b.p;
+    gbyte *const p = tiny ? (gbyte *)__builtin_amdgcn_kernarg_segment_ptr() : b.p - (b.shift ? 2 : 0);
     const uint32_t last = tiny || !real ? 0 : (b.n - per) * Logit<DT>::kSize;
 #pragma unroll
     for (uint32_t i = 0; i < VECS; ++i) {
         const uint32_t c = (64 * i + lane) * 16;
         gvec16any *const q = (gvec16any *)(p + (c < last ? c : last));
-        if constexpr (NT) v[i] = __builtin_nontemporal_load(q);
-        else v[i] = *q;
+        if constexpr (NT) l.v[i] = __builtin_nontemporal_load(q);
+        else l.v[i] = *q;
+    }
+    if constexpr (DT != ROG_DTYPE_F32) {
+        typedef const __attribute__((address_space(1))) uint32_t gword;
+        if (b.shift) l.behind = *(gword *)(p + (real ? VECS * 1024 : 0));
+    }
+}
+
+// The vectors of a block as if they had been loaded at their own address: of a
+// shifted one, each lane's 16 bytes from the two words they straddle, the last
+// of them from the next lane or vector.
+template <int DT, uint32_t VECS>
+__device__ __forceinline__ void aligned_block(bool shift, Loaded<VECS> &l) {
+    if constexpr (DT != ROG_DTYPE_F32) {
+        if (!shift) return;
+#pragma unroll
+        for (uint32_t i = 0; i < VECS; ++i) {
+            const uint32_t first = i + 1 < VECS ? uniform(l.v[i + 1 < VECS ? i + 1 : i].x) : uniform(l.behind);
+            const uint32_t x = l.v[i].x, y = l.v[i].y, z = l.v[i].z, w = l.v[i].w;
+            // lane 63 keeps `first`: wave_shl:1, as from_next_lane
+            const uint32_t next = uint32_t(__builtin_amdgcn_update_dpp(int(first), int(x), 0x130, 0xf, 0xf, false));
+            l.v[i] = vec16{align_bytes(y, x, 2), align_bytes(z, y, 2), align_bytes(w, z, 2), align_bytes(next, w, 2)};
+        }
     }
 }
 

@@ -86,7 +86,7 @@ struct Places {
             if (step < a.sh.W && r + step < a.sh.W && block0[r + step] <= b) r += step;
         const uint32_t off = (b - block0[r]) * kHeadBlock, left = width[r] - off;
         return BlockAt{(gbyte *)(x[r] + uint64_t(int64_t(row) * stride[r]) + uint64_t(off) * Logit<DT>::kSize),
-                       left < kHeadBlock ? left : kHeadBlock, col0[r] + off, r, off};
+                       left < kHeadBlock ? left : kHeadBlock, col0[r] + off, r, off, false};
     }
 };
 template <>
@@ -100,7 +100,7 @@ struct Places<64> {
     }
     template <int DT>
     __device__ __forceinline__ BlockAt at(const LogprobArgs &, uint32_t, uint32_t b) const {
-        return BlockAt{(gbyte *)p[b], n[b], col[b], 0, 0};
+        return BlockAt{(gbyte *)p[b], n[b], col[b], 0, 0, false};
     }
 };
 
@@ -343,10 +343,12 @@ __device__ __forceinline__ void finish_units(const LogprobArgs &a, uint32_t row,
 
 // The state of a block of n columns at p from its vectors.
 template <int DT>
-__device__ __forceinline__ State block_state(gbyte *p, uint32_t n, vec16 (&x)[Logit<DT>::kVecs], uint32_t lane, const Scaling &c) {
+__device__ __forceinline__ State block_state(gbyte *p, uint32_t n, bool shift, Loaded<Logit<DT>::kVecs> &x, uint32_t lane,
+                                             const Scaling &c) {
     if (n < Logit<DT>::kPerVec) return tiny_state<DT>(p, n, lane, c);
-    if (n < kHeadBlock) mask_tail<DT>(n, lane, x);
-    return state_of<DT>(x, c);
+    aligned_block<DT>(shift, x);
+    if (n < kHeadBlock) mask_tail<DT>(n, lane, x.v);
+    return state_of<DT>(x.v, c);
 }
 
 // Some of a row's blocks, taken one after the other by one wave with the next
@@ -358,7 +360,7 @@ template <int DT, bool NT>
 struct BlockStream {
     Cursor<DT> cur;
     BlockAt at;
-    vec16 v[Logit<DT>::kVecs];
+    Loaded<Logit<DT>::kVecs> v;
     uint32_t next, step, count;
 
     __device__ __forceinline__ BlockStream(const LogprobArgs &a, uint32_t row, uint32_t first, uint32_t by, uint32_t n, uint32_t lane)
@@ -374,14 +376,13 @@ struct BlockStream {
         for (uint32_t j = 0; j < count; ++j) {
             const uint32_t n = at.n;
             gbyte *const p = at.p;
-            vec16 x[Logit<DT>::kVecs];
-#pragma unroll
-            for (uint32_t k = 0; k < Logit<DT>::kVecs; ++k) x[k] = v[k];
+            const bool shift = at.shift;
+            Loaded<Logit<DT>::kVecs> x = v;
             const bool more = j + 1 < count;
             if (more) at = cur.at(next);
             next += step;
             load_block<DT, NT>(at, lane, v, more);
-            use(j, block_state<DT>(p, n, x, lane, c));
+            use(j, block_state<DT>(p, n, shift, x, lane, c));
         }
     }
 };
@@ -462,7 +463,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
     if (row >= a.rows) return;
     const uint32_t first = u / kChunkUnits * kChunkBlocks + u % kChunkUnits, b = first + w * kChunkUnits;
     // the loads first: the token only says whether they count
-    vec16 v[Logit<DT>::kVecs];
+    Loaded<Logit<DT>::kVecs> v;
     BlockAt at;
     if (b < a.sh.blocks) {
         at = Cursor<DT>(a.sh, row).at(b);
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
     // entries of a unit in the table: as many as its blocks, or fewer, wider ones
     const uint32_t entry_shift = min(a.slot_shift, 2u), entry_log = 2 - entry_shift, entries = 1u << entry_log;
     State st = no_state(c);
-    if (b < a.sh.blocks) st = block_state<DT>(at.p, at.n, v, lane, c);
+    if (b < a.sh.blocks) st = block_state<DT>(at.p, at.n, at.shift, v, lane, c);
     sh.lane_m[w][lane] = st.m;
     sh.lane_s[w][lane] = st.s;
     sh.lane_t[w][lane] = st.t;

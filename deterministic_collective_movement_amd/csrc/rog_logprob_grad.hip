@@ -44,11 +44,12 @@ __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
 #pragma unroll
         for (uint32_t i = 0; i < each; ++i) x[i] = none ? 0.0f : __builtin_nanf("");
     } else {
-        vec16 v[vecs];
-        load_block<DT, NT>(at, lane, v);
-        if (tiny) v[0] = load_tiny<DT>(at.p, at.n);
+        Loaded<vecs> l;
+        load_block<DT, NT>(at, lane, l);
+        aligned_block<DT>(at.shift, l);
+        if (tiny) l.v[0] = load_tiny<DT>(at.p, at.n);
 #pragma unroll
-        for (uint32_t i = 0; i < vecs; ++i) widen_vec<DT>(v[i], x + i * per);
+        for (uint32_t i = 0; i < vecs; ++i) widen_vec<DT>(l.v[i], x + i * per);
         const float scaled = g * a.inv_t, A = -(g + h * H) * a.inv_t, B = -h * a.inv_t * kLn2;
         if (fabsf(lse) >= kExtreme) {
             // Logits this large lie so far apart that only those equal to the
