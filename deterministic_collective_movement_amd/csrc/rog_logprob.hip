@@ -108,7 +108,7 @@ template <typename T>
 struct SharedTop {
     float tab[T::kEntries];    // [slot][lane]: largest logit of the slot's blocks in the lane's columns
     uint64_t list[T::kListCap];
-    uint64_t floor_key;        // candidates are at or above it
+    uint64_t floor_key;        // a later floor, as found by one lane
     uint32_t hit_count, count;
     uint16_t hits[T::kEntries];
     Places<int(T::kThreads)> places;
@@ -143,10 +143,10 @@ __device__ __forceinline__ uint32_t slot_block(uint32_t slot, uint32_t i, uint32
     else return wave_block(slot / kTopSlots, ((slot % kTopSlots) << shift) + i);
 }
 
-// Sets the first floor of the candidates, by one wave: the K-th largest of the
-// 64 lanes' largest logits, bit by bit, to 16 bits (the rest zero: a little lower).
-template <typename T>
-__device__ __forceinline__ void set_floor(float lane_m, uint32_t K, SharedTop<T> &top) {
+// The first floor of the candidates, the same in every lane of a wave: the K-th
+// largest of the 64 lanes' largest logits, bit by bit, to 16 bits (the rest
+// zero: a little lower).
+__device__ __forceinline__ uint64_t first_floor(float lane_m, uint32_t K) {
     const uint32_t o = order_of(lane_m);
     uint32_t k = 0;
 #pragma unroll
@@ -155,45 +155,45 @@ __device__ __forceinline__ void set_floor(float lane_m, uint32_t K, SharedTop<T>
         k = uint32_t(__popcll(__ballot(o >= higher))) >= K ? higher : k;
     }
     if (k <= kOrderMinusInf) k = kOrderMinusInf + 1;      // -inf is no alternative
-    if ((threadIdx.x & 63) == 0) {
-        top.floor_key = uint64_t(k) << 32;
-        top.hit_count = top.count = 0;
-    }
+    return uint64_t(k) << 32;
+}
+
+// The table's entries that reach a floor.  Counts are zero before.
+template <typename T>
+__device__ __forceinline__ void find_hits(uint64_t floor_key, SharedTop<T> &top) {
+    const float floor_x = from_order(uint32_t(floor_key >> 32));
+#pragma unroll
+    for (uint32_t e = T::id(); e < T::kEntries; e += T::kThreads)
+        if (top.tab[e] >= floor_x) top.hits[atomicAdd(&top.hit_count, 1u)] = uint16_t(e);
 }
 
 // The K best alternatives of a row from its table.  Called by the whole team,
-// after set_floor.
+// after find_hits with this floor and a sync.
 template <int DT, typename T>
-__device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row, const Row &v, SharedTop<T> &top) {
+__device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row, uint64_t floor_key, const Row &v,
+                                             SharedTop<T> &top) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const uint32_t tid = T::id(), K = a.top_k;
     const uint32_t shift = T::kThreads == 64 ? 0 : a.slot_shift;
+    const uint32_t vecs_shift = shift + (Logit<DT>::kVecs == 8 ? 3 : 2);
     uint32_t n;
     for (;;) {
-        const uint64_t floor_key = top.floor_key;
         const float floor_x = from_order(uint32_t(floor_key >> 32));
-#pragma unroll
-        for (uint32_t e = tid; e < T::kEntries; e += T::kThreads)
-            if (top.tab[e] >= floor_x) top.hits[atomicAdd(&top.hit_count, 1u)] = uint16_t(e);
-        T::sync();
-        const uint32_t vecs_shift = shift + (Logit<DT>::kVecs == 8 ? 3 : 2);
         const uint64_t tasks = uint64_t(top.hit_count) << vecs_shift;
         for (uint64_t q = tid; q < tasks; q += T::kThreads) {
             const uint32_t e = top.hits[q >> vecs_shift], i = uint32_t(q) & ((1u << vecs_shift) - 1);
-            const uint32_t b = slot_block<T>(e / 64, i / Logit<DT>::kVecs, shift), el = e % 64;
+            const uint32_t b = slot_block<T>(e / 64, i / Logit<DT>::kVecs, shift), el = e % 64, vi = i % Logit<DT>::kVecs;
             if (b >= a.sh.blocks) continue;
             const BlockAt at = top.places.template at<DT>(a, row, b);
-            const uint32_t vi = i % Logit<DT>::kVecs;
-            const vec16 vec = load_vec<DT>(at.p, at.n, vi, el);
             float x[per];
-            widen_vec<DT>(vec, x);
+            widen_vec<DT>(load_vec<DT>(at.p, at.n, vi, el), x);
             const uint32_t col = at.col + (at.n < per ? 0 : vec_place<DT>(at.n, vi, el));
 #pragma unroll
             for (uint32_t k = 0; k < per; ++k) {
                 const uint64_t key = uint64_t(order_of(x[k])) << 32 | uint32_t(~(col + k));
-                if (owns<DT>(at.n, vi, el, k) && x[k] >= floor_x && key >= floor_key) {
-                    const uint32_t at_list = atomicAdd(&top.count, 1u);
-                    if (at_list < T::kListCap) top.list[at_list] = key;
+                if (x[k] >= floor_x && owns<DT>(at.n, vi, el, k) && key >= floor_key) {
+                    const uint32_t place = atomicAdd(&top.count, 1u);
+                    if (place < T::kListCap) top.list[place] = key;
                 }
             }
         }
@@ -211,6 +211,9 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
             if (above == K - 1) top.floor_key = key;
         }
         if (tid == 0) top.hit_count = top.count = 0;
+        T::sync();
+        floor_key = top.floor_key;
+        find_hits<T>(floor_key, top);
         T::sync();
     }
     for (uint32_t q = tid; q < n; q += T::kThreads) {
@@ -276,7 +279,7 @@ __device__ __forceinline__ uint32_t count_equal(const LogprobArgs &a, uint32_t r
 // with the same `all`.  equal: shared, zero.
 template <int DT, typename T, bool TOP>
 __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, int64_t tok, float tx, const State &all, float log_s,
-                           uint32_t &equal, typename SharedFor<T, TOP>::type &top) {
+                                           uint64_t floor_key, uint32_t &equal, typename SharedFor<T, TOP>::type &top) {
     const uint32_t tid = T::id();
     const float nan = __builtin_nanf("");
     const bool token = tok < int64_t(a.vocab);      // tok < 0 never comes here, except for tokens == NULL
@@ -312,7 +315,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
         if (a.entropy) a.entropy[row] = entropy;
         if (a.logp) a.logp[row] = token ? v.logp(tx, a) : nan;
     }
-    if constexpr (TOP) alternatives<DT, T>(a, row, v, top);
+    if constexpr (TOP) alternatives<DT, T>(a, row, floor_key, v, top);
 }
 
 // The same from the units' states and the lanes' maxima in shared memory, by a
@@ -322,6 +325,12 @@ __device__ __forceinline__ void finish_units(const LogprobArgs &a, uint32_t row,
                                              typename SharedFor<Team<kHeadThreads>, TOP>::type &top) {
     const uint32_t tid = threadIdx.x, lane = tid & 63;
     const Scaling c{a.scale, a.bound};
+    uint64_t floor_key = 0;
+    if constexpr (TOP) {
+        floor_key = first_floor(fmaxf(fmaxf(sh.lane_m[0][lane], sh.lane_m[1][lane]), fmaxf(sh.lane_m[2][lane], sh.lane_m[3][lane])),
+                                a.top_k);
+        find_hits<Team<kHeadThreads>>(floor_key, top);
+    }
     if (tid < 64) {
         const State all = join_lanes(make_state(sh.m[lane], sh.s[lane], sh.t[lane], c), c);
         if (tid == 0) {
@@ -331,13 +340,9 @@ __device__ __forceinline__ void finish_units(const LogprobArgs &a, uint32_t row,
             sh.row[3] = log2f(all.s);
             sh.equal = 0;
         }
-    } else if (TOP && tid < 128) {
-        if constexpr (TOP)
-            set_floor(fmaxf(fmaxf(sh.lane_m[0][lane], sh.lane_m[1][lane]), fmaxf(sh.lane_m[2][lane], sh.lane_m[3][lane])),
-                      a.top_k, top);
     }
     __syncthreads();
-    finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, tx, make_state(sh.row[0], sh.row[1], sh.row[2], c), sh.row[3],
+    finish_row<DT, Team<kHeadThreads>, TOP>(a, row, tok, tx, make_state(sh.row[0], sh.row[1], sh.row[2], c), sh.row[3], floor_key,
                                             sh.equal, top);
 }
 
@@ -418,8 +423,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_row_kernel(LogprobAr
     }
     if constexpr (TOP) {
         for (uint32_t e = 0; e < kTopSlots; ++e) top.tab[(w * kTopSlots + e) * 64 + lane] = -kInf;
-    }
-    if constexpr (TOP) {
+        if (tid == 0) top.hit_count = top.count = 0;
         if (w == 3) top.places.fill(a, lane);
     }
     State unit = no_state(c);
@@ -536,6 +540,7 @@ __global__ __launch_bounds__(kHeadThreads) void rog_logprob_split_kernel(Logprob
         }
         sh.lane_m[w][lane] = lane_m;
         if (w == 1) top.places.fill(a, lane);
+        if (tid == 0) top.hit_count = top.count = 0;
     }
     if (w == 0) {
         State joined = make_state(jm, js, jt, c);
@@ -584,10 +589,16 @@ __global__ __launch_bounds__(64 * kWaveRows) void rog_logprob_wave_kernel(Logpro
         for (uint32_t b = a.sh.blocks; b < kUnitBlocks; ++b) top[w].tab[b * 64 + lane] = -kInf;
     }
     const State all = join_lanes(unit, c);
+    uint64_t floor_key = 0;
     if (lane == 0) equal[w] = 0;
-    if constexpr (TOP) set_floor(unit.m, a.top_k, top[w]);
+    if constexpr (TOP) {
+        if (lane == 0) top[w].hit_count = top[w].count = 0;
+        T::sync();
+        floor_key = first_floor(unit.m, a.top_k);
+        find_hits<T>(floor_key, top[w]);
+    }
     T::sync();
-    finish_row<DT, T, TOP>(a, row, tok, tx, all, log2f(all.s), equal[w], top[w]);
+    finish_row<DT, T, TOP>(a, row, tok, tx, all, log2f(all.s), floor_key, equal[w], top[w]);
 }
 
 template <typename K>
