@@ -30,7 +30,7 @@ __device__ __forceinline__ float exp_of(float x) {
     const float y = x * kHi;
     const float e = exp2_fast(y);
     const float rest = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -y));
-    return fabsf(x) < 100.0f ? __builtin_fmaf(e, rest * kLn2, e) : e;
+    return fabsf(x) < 87.0f ? __builtin_fmaf(e, rest * kLn2, e) : e;     // beyond, e may be infinite or zero
 }
 
 // kl = e^q - 1 - q and grow = e^q - 1 without cancellation: the Taylor series of

@@ -41,6 +41,7 @@ include/rog.h.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -601,6 +602,9 @@ _MAX_TOP_K = int(_lib.rog_max_top_k())
 _workspaces: dict = {}
 _workspaces_lock = threading.Lock()
 _NO_WORKSPACE = (None, 0)
+_HERE = contextlib.nullcontext()       # the tensors' device is the current one
+_OUT_NAMES = ("out.logp", "out.entropy", "out.lse", "out.top_logp", "out.top_ids")
+_LOSS_NAMES = ("logp", "old_logp", "advantage", "weight", "ref_logp", "entropy", "out.g_logp", "out.g_entropy")
 
 
 def rog_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
@@ -653,8 +657,10 @@ def _with_workspace(call, need, what: str, workspace, device: torch.device, stre
         _check_tensor(workspace, "workspace", device)
         _check(call(workspace.data_ptr(), _nbytes(workspace)), what)
         return
-    if not _capturing(stream, device):
-        got = _workspaces.get((device.index, handle), _NO_WORKSPACE)
+    # the stream's own, if it has one and this is no capture (of a stream that is
+    # not the current one it takes a look at that stream)
+    got = _workspaces.get((device.index, handle), _NO_WORKSPACE)
+    if got[1] == 0 or not _capturing(stream, device):
         status = call(got[0], got[1])
         if status == ROG_OK:
             return
@@ -669,16 +675,23 @@ def _vector_error(t, what: str, n: int, dtype: torch.dtype, device: torch.device
     raise ValueError("%s must hold %d elements of %s (has %d of %s)" % (what, n, dtype, t.numel(), t.dtype))
 
 
-def _vector(t, what: str, n: int, dtype: torch.dtype, device: torch.device, idx: int) -> int:
-    """Address of a contiguous vector of n elements (0 for None)."""
-    if t is None:
-        return 0
+def _addresses(tensors, names, n: int, dtype: torch.dtype, device: torch.device, idx: int) -> list:
+    """Addresses of contiguous vectors of n elements (0 for None): one pass of
+    cheap checks, the full ones name what is wrong."""
+    got = []
     try:
-        if t.dtype is dtype and t.get_device() == idx and t.numel() == n and t.is_contiguous():
-            return t.data_ptr()
+        for t in tensors:
+            if t is None:
+                got.append(0)
+            elif t.dtype is dtype and t.get_device() == idx and t.numel() == n and t.is_contiguous():
+                got.append(t.data_ptr())
+            else:
+                break
+        else:
+            return got
     except AttributeError:
         pass
-    _vector_error(t, what, n, dtype, device)
+    _vector_error(tensors[len(got)], names[len(got)], n, dtype, device)
 
 
 def _matrix_error(t, what: str, rows: int, dtype: torch.dtype, device: torch.device):
@@ -765,15 +778,18 @@ def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor
                          new(rows, top_k) if top_k else None, new(rows, top_k, dtype=i64) if top_k else None)
     elif not isinstance(out, RogLogprob):
         out = RogLogprob(*out)
-    tops = rows * top_k
-    outs = _pack_addresses5(_vector(out.logp, "out.logp", rows, f32, device, idx),
-                            _vector(out.entropy, "out.entropy", rows, f32, device, idx),
-                            _vector(out.lse, "out.lse", rows, f32, device, idx),
-                            _vector(out.top_logp, "out.top_logp", tops, f32, device, idx),
-                            _vector(out.top_ids, "out.top_ids", tops, i64, device, idx))
-    tok = _vector(tokens, "tokens", rows, i64, device, idx) or None
+    addr = _addresses(out[:3], _OUT_NAMES, rows, f32, device, idx)
+    if top_k:
+        addr += _addresses(out[3:4], _OUT_NAMES[3:], rows * top_k, f32, device, idx)
+        addr += _addresses(out[4:], _OUT_NAMES[4:], rows * top_k, i64, device, idx)
+        outs = _pack_addresses5(*addr)
+    elif out[3] is None and out[4] is None:
+        outs = _pack_addresses5(*addr, 0, 0)
+    else:
+        raise ValueError("out.top_logp and out.top_ids need a top_k")
+    tok = None if tokens is None else _addresses((tokens,), ("tokens",), rows, i64, device, idx)[0]
     W, dt = len(shards), DTYPES[dtype]
-    with _on_device(device):
+    with _on_device(device) if _current_device() != idx else _HERE:
         handle = _stream_handle(stream, device)
         _with_workspace(lambda ws, n: _lib.rog_logprob_ex(packed, W, rows, dt, temperature, tok, top_k, outs, ws, n, handle, form),
                         lambda: _logprob_plan(packed, W, rows, dt, top_k, form).workspace_bytes,
@@ -821,13 +837,12 @@ def rog_logprob_grad(shards: Sequence[torch.Tensor], tokens: torch.Tensor, lse: 
         vals += (g.data_ptr(), stride)
     if tokens is None or lse is None or entropy is None or g_logp is None:
         raise ValueError("tokens, lse, entropy and g_logp are needed")
-    f32 = torch.float32
-    tok = _vector(tokens, "tokens", rows, torch.int64, device, idx)
-    vec = [_vector(t, what, rows, f32, device, idx) for t, what in
-           ((lse, "lse"), (entropy, "entropy"), (g_logp, "g_logp"), (g_entropy, "g_entropy"))]
-    with _on_device(device):
-        _check(_lib.rog_logprob_grad(packed, _PACK_GRADS[W](*vals), W, rows, DTYPES[dtype], temperature, tok, vec[0], vec[1],
-                                     vec[2], vec[3] or None, _stream_handle(stream, device)), "rog_logprob_grad")
+    tok = _addresses((tokens,), ("tokens",), rows, torch.int64, device, idx)[0]
+    vec = _addresses((lse, entropy, g_logp, g_entropy), ("lse", "entropy", "g_logp", "g_entropy"), rows, torch.float32,
+                     device, idx)
+    with _on_device(device) if _current_device() != idx else _HERE:
+        _check(_lib.rog_logprob_grad(packed, _PACK_GRADS[W](*vals), W, rows, DTYPES[dtype], temperature, tok, *vec,
+                                     _stream_handle(stream, device)), "rog_logprob_grad")
     return out if isinstance(out, list) else list(out)
 
 
@@ -847,18 +862,16 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
         _check_tensor(logp, "logp", device)
     if old_logp is None or advantage is None:
         raise ValueError("old_logp and advantage are needed")
-    ins = _pack_addresses6(_vector(logp, "logp", n, f32, device, idx), _vector(old_logp, "old_logp", n, f32, device, idx),
-                           _vector(advantage, "advantage", n, f32, device, idx), _vector(weight, "weight", n, f32, device, idx),
-                           _vector(ref_logp, "ref_logp", n, f32, device, idx), _vector(entropy, "entropy", n, f32, device, idx))
     if out is None:
         out = RogPolicyLoss(torch.empty(4, dtype=f32, device=device), torch.empty(n, dtype=f32, device=device),
                             torch.empty(n, dtype=f32, device=device) if entropy is not None else None)
     elif not isinstance(out, RogPolicyLoss):
         out = RogPolicyLoss(*out)
-    outs = _pack_addresses3(_vector(out.stats, "out.stats", 4, f32, device, idx), _vector(out.g_logp, "out.g_logp", n, f32, device, idx),
-                            _vector(out.g_entropy, "out.g_entropy", n, f32, device, idx))
+    addr = _addresses((logp, old_logp, advantage, weight, ref_logp, entropy, out[1], out[2]), _LOSS_NAMES, n, f32, device, idx)
+    ins = _pack_addresses6(*addr[:6])
+    outs = _pack_addresses3(_addresses(out[:1], ("out.stats",), 4, f32, device, idx)[0], *addr[6:])
     params = _pack_floats5(clip_low, clip_high, kl_coef, entropy_coef, grad_scale)
-    with _on_device(device):
+    with _on_device(device) if _current_device() != idx else _HERE:
         handle = _stream_handle(stream, device)
         _with_workspace(lambda ws, b: _lib.rog_policy_loss(ins, n, params, outs, ws, b, handle),
                         lambda: _lib.rog_policy_loss_workspace_bytes(n), "rog_policy_loss", workspace, device, stream, handle)

@@ -322,6 +322,8 @@ ROG_API rog_status rog_reduce_many(const rog_reduce_desc *descs, int n, int W, r
  *    it ready for the next.  Calls that may run at the same time (on different
  *    streams) each need their own.
  *  - All sums and row statistics are held in binary32 or binary64.
+ *  - Logits are read inside their rows, or inside the aligned 32-bit word that
+ *    holds some of a row's bytes; what is read beyond a row is never used.
  * ======================================================================== */
 
 /* One vocabulary shard: row i's columns are logits[i * row_stride + 0 .. width). */
@@ -427,6 +429,8 @@ ROG_API rog_status rog_logprob_plan(const rog_logit_shard *shards, int W, size_t
  *
  * grads    W gradients.  A gradient may be exactly its logits' shard (same
  *          address and stride: in place); any other overlap is an error.
+ *          Column slices of one matrix are told apart; slices with different
+ *          row strides overlap here if their whole extents do.
  *          Bytes between the rows of a gradient are not written.
  * Errors as rog_logprob; a row stride below the width is INVALID_ARGUMENT.
  */

@@ -221,6 +221,34 @@ def test_offsets_past_32_bits(gpu):
     assert torch.equal(a, view)
 
 
+def test_very_long_rows(gpu):
+    """A hundred million columns: thousands of units, wide table entries, columns past 2^26."""
+    V = 100_000_003
+    gen = torch.Generator(device=gpu)
+    gen.manual_seed(1)
+    x = torch.empty(2, V, dtype=BF16, device=gpu)
+    x.normal_(0, 2, generator=gen)
+    x[0, V - 1] = 40.0
+    tokens = torch.tensor([V - 1, 77_777_777], device=gpu)
+    got = rog.rog_logprob([x], tokens, 3)
+    split = rog.rog_logprob_ex([x[:, : V // 2], x[:, V // 2:]], tokens, 3, form=rog.ROG_LOGPROB_ROW)
+    for i in range(2):
+        z = x[i].double()
+        lse = torch.logsumexp(z, 0)
+        best = torch.topk(z, 3).values
+        p = torch.exp(z - lse)
+        h = lse - (p * z).sum()
+        # as logprob_tol, with some 2000 more additions above each term
+        tol = ref.U * (6 * 40 + 2500)
+        for r in (got, split):
+            assert abs(float(r.lse[i]) - float(lse)) <= tol + 2 * ref.U * abs(float(lse))
+            assert abs(float(r.logp[i]) - float(z[tokens[i]] - lse)) <= tol + 2 * ref.U * abs(float(r.logp[i]))
+            assert abs(float(r.entropy[i]) - float(h)) <= tol * (2 + 2 * float(h))
+            assert torch.equal(z[r.top_ids[i]], best)
+        assert torch.equal(got.top_ids[i], split.top_ids[i])
+    assert same_bits(got, rog.rog_logprob_ex([x], tokens, 3, form=rog.ROG_LOGPROB_ROW))
+
+
 def test_outputs_stay_in_their_arrays(gpu):
     shards = make(5, [2500, 1], F16, 21, gpu)
     tokens = some_tokens(5, 2501, 21, gpu)

@@ -77,6 +77,26 @@ def test_masked_tokens_count_for_nothing(gpu):
     assert none.stats.tolist() == [0, 0, 0, 0] and bool((none.g_logp == 0).all())
 
 
+def test_large_log_ratios(gpu):
+    """Exponents up to and past the binary32 range: infinite, zero, never NaN."""
+    d = np.array([80, 86.9, 87.1, 88.5, 88.8, 95, 120, 1e30, -80, -87.1, -95, -200, -1e30], np.float32)
+    n = len(d)
+    old = torch.zeros(n, device=gpu)
+    adv = torch.full((n,), -1.0, device=gpu)          # not clipped above
+    got = rog.rog_policy_loss(torch.from_numpy(d).to(gpu), old, adv, weight=torch.ones(n, device=gpu), clip_low=1.0, clip_high=math.inf)
+    with np.errstate(over="ignore"):
+        want = np.exp(d.astype(np.float64))
+        want[want > float(np.finfo(np.float32).max)] = np.inf
+    g = got.g_logp.cpu().numpy().astype(np.float64)
+    assert np.array_equal(np.isinf(g), np.isinf(want)) and not np.isnan(g).any()
+    fin = np.isfinite(want)
+    # the exponent's own rounding, 87 u, where it is not put back; below 2^-126 zero
+    assert (np.abs(g[fin] - want[fin]) <= 2 * 90 * ref.U * want[fin] + 2.0 ** -125).all()
+    q = torch.from_numpy(d).to(gpu)
+    kl = rog.rog_policy_loss(old, old, old, weight=torch.ones(n, device=gpu), ref_logp=q, kl_coef=1.0).g_logp.cpu().numpy()
+    assert not np.isnan(kl).any() and np.isinf(kl[6]) and kl[-1] == 1.0
+
+
 def test_alignment_place_and_repeats(gpu):
     arrays = make(70001, 6)
     want = check(arrays, gpu)
