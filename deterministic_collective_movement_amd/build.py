@@ -38,6 +38,10 @@ HOST_FLAGS = ["-x", "hip", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-W
               "-Wno-unused-command-line-argument"]
 
 
+BINDING_SOURCE = "rog_binding.cpp"
+BINDING_PATH = os.path.join(PKG, "_rog_binding.so")
+
+
 def _run(cmd):
     subprocess.check_call(cmd)
 
@@ -64,5 +68,36 @@ def build_library(out: str = LIB_PATH, defines=(), build_dir: str = BUILD_DIR) -
     return out
 
 
+def build_binding(out: str = BINDING_PATH) -> str:
+    """Compile and link _rog_binding.so, the CPython module beside librog.so (host
+    code only; against the installed torch's headers and libraries)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [f for d in [INCLUDE, os.path.join(ROCM, "include"), sysconfig.get_paths()["include"]] + cpp_extension.include_paths()
+           for f in ("-isystem", d)]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = out + ".tmp%d" % os.getpid()
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra", "-Werror",
+          "-D__HIP_PLATFORM_AMD__", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + inc +
+         [os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, out)
+    return out
+
+
+def build_all() -> None:
+    """Everything the package loads."""
+    with ThreadPoolExecutor(max_workers=1) as pool:
+        binding = pool.submit(build_binding)
+        build_library()
+        binding.result()
+
+
 if __name__ == "__main__":
-    print(build_library(defines=sys.argv[1:]))
+    if sys.argv[1:]:
+        print(build_library(defines=sys.argv[1:]))
+    else:
+        build_all()
+        print(LIB_PATH)
+        print(BINDING_PATH)

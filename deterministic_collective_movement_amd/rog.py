@@ -43,6 +43,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 import struct
 import threading
@@ -50,7 +51,7 @@ from typing import List, NamedTuple, Optional, Sequence
 
 import torch  # loads the process's HIP runtime before librog.so binds to it
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 ROG_OK = 0
 ROG_ERR_INVALID_ARGUMENT = 1
@@ -183,6 +184,20 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+
+
+def _load_binding():
+    """The module that marshals ordinary calls (csrc/rog_binding.cpp)."""
+    if not os.path.exists(BINDING_PATH):
+        raise ImportError("_rog_binding.so is not built (%s); run __graft_entry__.build() or "
+                          "python -m deterministic_collective_movement_amd.build" % BINDING_PATH)
+    spec = importlib.util.spec_from_file_location("_rog_binding", BINDING_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+_binding = _load_binding()
 
 
 def library_path() -> str:
@@ -631,12 +646,18 @@ def _own_workspace(nbytes: int, device: torch.device, stream, handle: int):
     with _workspaces_lock:
         got = _workspaces.get(key)
         if got is None or got[1] < nbytes:
-            t = rog_workspace(max(nbytes, 1 << 20), device, stream)
-            got = _workspaces[key] = (t.data_ptr(), t.numel(), t)
+            # at least twice as large each time, and the smaller ones are kept: another
+            # thread may be about to launch on this stream with one
+            t = rog_workspace(max(nbytes, 1 << 20, 2 * got[1] if got else 0), device, stream)
+            got = _workspaces[key] = (t.data_ptr(), t.numel(), t, got)
+            _binding.workspace(device.index, handle, t.data_ptr(), t.numel())
     return got[:2]
 
 
-_is_capturing = torch.cuda.is_current_stream_capturing
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
+_raw_stream_of = _raw_stream or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rog_logprob_ex, _lib.rog_logprob_grad, _lib.rog_policy_loss)),
+              _lib.rog_max_peers(), _current_device, _raw_stream_of, _is_capturing)
 
 
 def _capturing(stream, device: torch.device) -> bool:
@@ -768,6 +789,11 @@ def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor
                    workspace: Optional[torch.Tensor] = None, stream=None,
                    form: int = ROG_LOGPROB_AUTO) -> RogLogprob:
     """rog_logprob with the launch form forced (never changes the bits)."""
+    if out is not None and workspace is None and stream is None:
+        if type(out) is not RogLogprob:
+            out = RogLogprob(*out)
+        if _binding.logprob(shards, tokens, top_k, temperature, out, form):
+            return out
     device, idx, rows, dtype, packed = _shard_bytes(shards)
     if not 0 <= top_k <= _MAX_TOP_K:
         raise ValueError("top_k must be in [0, %d]" % _MAX_TOP_K)
@@ -776,7 +802,7 @@ def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor
         new = lambda *shape, dtype=f32: torch.empty(*shape, dtype=dtype, device=device)  # noqa: E731
         out = RogLogprob(new(rows) if tokens is not None else None, new(rows), new(rows),
                          new(rows, top_k) if top_k else None, new(rows, top_k, dtype=i64) if top_k else None)
-    elif not isinstance(out, RogLogprob):
+    elif type(out) is not RogLogprob:
         out = RogLogprob(*out)
     addr = _addresses(out[:3], _OUT_NAMES, rows, f32, device, idx)
     if top_k:
@@ -816,6 +842,8 @@ def rog_logprob_grad(shards: Sequence[torch.Tensor], tokens: torch.Tensor, lse: 
     """Gradient of sum_i (g_logp[i] logp[i] + g_entropy[i] entropy[i]) in every
     shard, from rog_logprob's ``lse`` and ``entropy``.  ``out``: W matrices to
     write; ``out[r]`` may be ``shards[r]`` (in place)."""
+    if out is not None and stream is None and _binding.grad(shards, tokens, lse, entropy, g_logp, g_entropy, temperature, out):
+        return out if isinstance(out, list) else list(out)
     device, idx, rows, dtype, packed = _shard_bytes(shards)
     if out is None:
         out = [torch.empty(rows, x.shape[1], dtype=dtype, device=device) for x in shards]
@@ -855,6 +883,11 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
     """The clipped policy loss over n tokens (float32 vectors) with its gradients
     in ``logp`` and ``entropy``.  ``weight[i]`` is the token's weight in the sums
     (0: the token counts for nothing; None: 1 / n each)."""
+    if out is not None and workspace is None and stream is None:
+        if type(out) is not RogPolicyLoss:
+            out = RogPolicyLoss(*out)
+        if _binding.loss(logp, old_logp, advantage, weight, ref_logp, entropy, clip_low, clip_high, kl_coef, entropy_coef, grad_scale, out):
+            return out
     if not isinstance(logp, torch.Tensor):
         raise TypeError("logp must be a torch.Tensor")
     device, n, f32, idx = logp.device, logp.numel(), torch.float32, logp.get_device()
@@ -865,7 +898,7 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
     if out is None:
         out = RogPolicyLoss(torch.empty(4, dtype=f32, device=device), torch.empty(n, dtype=f32, device=device),
                             torch.empty(n, dtype=f32, device=device) if entropy is not None else None)
-    elif not isinstance(out, RogPolicyLoss):
+    elif type(out) is not RogPolicyLoss:
         out = RogPolicyLoss(*out)
     addr = _addresses((logp, old_logp, advantage, weight, ref_logp, entropy, out[1], out[2]), _LOSS_NAMES, n, f32, device, idx)
     ins = _pack_addresses6(*addr[:6])

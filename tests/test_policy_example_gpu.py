@@ -1,5 +1,5 @@
 """The policy-step example learns, and repeats bit for bit; the operators under
-several host threads."""
+several host threads, and by both ways through the binding."""
 from __future__ import annotations
 
 import importlib.util
@@ -60,3 +60,52 @@ def test_host_threads_on_their_own_streams(gpu):
     for t in threads:
         t.join()
     assert not bad, bad[:3]
+
+
+def test_both_ways_through_the_binding(gpu):
+    """Calls with outputs in hand go through the compiled marshalling, others through Python: the same bits, in graphs too."""
+    gen = torch.Generator(device=gpu)
+    gen.manual_seed(3)
+    x = torch.randn(6, 40007, generator=gen, device=gpu).half()
+    shards = [x[:, :20000], x[:, 20000:]]
+    tokens = torch.randint(0, 40007, (6,), generator=gen, device=gpu)
+    n = 30001
+    logp, old, adv, h = (torch.randn(n, generator=gen, device=gpu) for _ in range(4))
+    s = torch.cuda.current_stream()
+    want = rog.rog_logprob(shards, tokens, 5, 0.9, stream=s)
+    d_want = rog.rog_logprob_grad(shards, tokens, want.lse, want.entropy, want.logp, temperature=0.9, stream=s)
+    l_want = rog.rog_policy_loss(logp, old, adv, entropy=h, entropy_coef=0.1, stream=s)
+    out = tuple(torch.full_like(t, 3) for t in want)
+    d_out = [torch.full_like(t, 3) for t in d_want]
+    l_out = tuple(torch.full_like(t, 3) for t in l_want)
+
+    def call():
+        r = rog.rog_logprob(shards, tokens, 5, 0.9, out=out)
+        d = rog.rog_logprob_grad(shards, tokens, r.lse, r.entropy, r.logp, temperature=0.9, out=d_out)
+        return r, d, rog.rog_policy_loss(logp, old, adv, entropy=h, entropy_coef=0.1, out=l_out)
+
+    def check():
+        torch.cuda.synchronize()
+        for got, ref in ((out, want), (d_out, d_want), (l_out, l_want)):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+            for t in got:
+                t.fill_(3)
+
+    r, d, l = call()
+    assert r.logp is out[0] and d is d_out and l.stats is l_out[0]
+    check()
+    call()      # the stream has a workspace by now
+    check()
+    side = torch.cuda.Stream()
+    side.wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for _ in range(3):
+        graph.replay()
+        check()
+        call()
+        check()
+    with torch.cuda.stream(side):
+        call()
+    check()
