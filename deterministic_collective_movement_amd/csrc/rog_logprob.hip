@@ -81,10 +81,16 @@ struct Places {
     }
     template <int DT>
     __device__ __forceinline__ BlockAt at(const LogprobArgs &a, uint32_t row, uint32_t b) const {
-        uint32_t r = 0;            // the last shard that begins at or before block b
-        for (uint32_t step = kMaxPeers / 2; step; step /= 2)
-            if (step < a.sh.W && r + step < a.sh.W && block0[r + step] <= b) r += step;
-        const uint32_t off = (b - block0[r]) * kHeadBlock, left = width[r] - off;
+        uint32_t r = 0, first = 0;
+        if (a.sh.even) {
+            r = divide(b, a.sh.even_div);
+            first = r * a.sh.even;
+        } else {                   // the last shard that begins at or before block b
+            for (uint32_t step = kMaxPeers / 2; step; step /= 2)
+                if (step < a.sh.W && r + step < a.sh.W && block0[r + step] <= b) r += step;
+            first = block0[r];
+        }
+        const uint32_t off = (b - first) * kHeadBlock, left = width[r] - off;
         return BlockAt{(gbyte *)(x[r] + uint64_t(int64_t(row) * stride[r]) + uint64_t(off) * Logit<DT>::kSize),
                        left < kHeadBlock ? left : kHeadBlock, col0[r] + off, r, off, false};
     }
@@ -167,16 +173,16 @@ __device__ __forceinline__ void find_hits(uint64_t floor_key, SharedTop<T> &top)
         if (top.tab[e] >= floor_x) top.hits[atomicAdd(&top.hit_count, 1u)] = uint16_t(e);
 }
 
-// The K best alternatives of a row from its table.  Called by the whole team,
-// after find_hits with this floor and a sync.
+// Lists the candidates for a row's K best alternatives from its table, and
+// returns how many: every column that reaches the floor, so K at least where
+// the row has as many.  Called by the whole team, after find_hits with this
+// floor and a sync; leaves the list in sync.
 template <int DT, typename T>
-__device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row, uint64_t floor_key, const Row &v,
-                                             SharedTop<T> &top) {
+__device__ __forceinline__ uint32_t list_candidates(const LogprobArgs &a, uint32_t row, uint64_t floor_key, SharedTop<T> &top) {
     constexpr uint32_t per = Logit<DT>::kPerVec;
     const uint32_t tid = T::id(), K = a.top_k;
     const uint32_t shift = T::kThreads == 64 ? 0 : a.slot_shift;
     const uint32_t vecs_shift = shift + (Logit<DT>::kVecs == 8 ? 3 : 2);
-    uint32_t n;
     for (;;) {
         const float floor_x = from_order(uint32_t(floor_key >> 32));
         const uint64_t tasks = uint64_t(top.hit_count) << vecs_shift;
@@ -198,8 +204,8 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
             }
         }
         T::sync();
-        n = top.count;
-        if (n <= T::kListCap) break;
+        const uint32_t n = top.count;
+        if (n <= T::kListCap) return n;
         T::sync();
         // More columns reach the floor than the list holds (many equal logits):
         // the K-th best of those listed is a higher floor that K columns reach.
@@ -216,6 +222,12 @@ __device__ __forceinline__ void alternatives(const LogprobArgs &a, uint32_t row,
         find_hits<T>(floor_key, top);
         T::sync();
     }
+}
+
+// Writes the K best of the n candidates, each at the place of its rank.
+template <typename T>
+__device__ __forceinline__ void write_alternatives(const LogprobArgs &a, uint32_t row, uint32_t n, const Row &v, const SharedTop<T> &top) {
+    const uint32_t tid = T::id(), K = a.top_k;
     for (uint32_t q = tid; q < n; q += T::kThreads) {
         const uint64_t key = top.list[q];
         uint32_t above = 0;
@@ -291,6 +303,8 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
         write_plain_row(a, row, tid, T::kThreads, token ? -kInf : nan, 0.0f, -kInf, -kInf);
         return;
     }
+    uint32_t candidates = 0;
+    if constexpr (TOP) candidates = list_candidates<DT, T>(a, row, floor_key, top);
     Row v;
     v.r = all.r;
     v.l = log_s;
@@ -310,12 +324,12 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
         v.lse = __builtin_amdgcn_fmed3f(__builtin_fmaf(v.m, a.inv_t, v.l * kLn2), -kMaxFinite, kMaxFinite);
         entropy = v.l * kLn2;
     }
-    if (tid == 0) {
+    if (tid == T::kThreads - 1) {      // in the last wave, where the first one ranks the alternatives
         if (a.lse) a.lse[row] = v.lse;
         if (a.entropy) a.entropy[row] = entropy;
         if (a.logp) a.logp[row] = token ? v.logp(tx, a) : nan;
     }
-    if constexpr (TOP) alternatives<DT, T>(a, row, floor_key, v, top);
+    if constexpr (TOP) write_alternatives<T>(a, row, candidates, v, top);
 }
 
 // The same from the units' states and the lanes' maxima in shared memory, by a
