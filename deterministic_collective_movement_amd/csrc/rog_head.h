@@ -71,9 +71,8 @@ constexpr uint32_t kMaxVocab = 1u << 31;   // columns of a row: below this
 // The front of a workspace: arrival counters, zero between calls, each in a
 // 128-byte line of its own (counters that share a line are counted one after
 // the other: 64 rows of 131072 columns took 12.2 us with their counters packed,
-// 8.9 apart).  A split launch counts row r's workgroups in counter r; the
-// policy loss counts in counters 1 and on, and those in counter 0.  Partial
-// states follow.
+// 8.9 apart).  A split launch counts row r's workgroups in counter r, the policy
+// loss its own in counter 0.  Partial states follow.
 constexpr uint32_t kHeadCounters = 1024;
 constexpr uint32_t kCounterStride = 128 / sizeof(uint32_t);
 constexpr size_t kHeadCounterBytes = size_t(kHeadCounters) * kCounterStride * sizeof(uint32_t);
@@ -162,15 +161,9 @@ struct PolicyPlan {
 };
 
 // The policy loss: tiles of 1024 tokens, four per thread of a workgroup; up to
-// kPolicyGroups workgroups, each with a run of consecutive tiles.  With more
-// than kPolicyRoots of them, workgroup g counts itself in counter
-// 1 + g mod kPolicyRoots, and the last of those in counter 0.
+// kPolicyGroups workgroups, each with a run of consecutive tiles.
 constexpr uint32_t kPolicyTile = 1024;
-#ifndef ROG_POLICY_GROUPS
-#define ROG_POLICY_GROUPS 512
-#endif
-constexpr uint32_t kPolicyGroups = ROG_POLICY_GROUPS;
-constexpr uint32_t kPolicyRoots = 16;
+constexpr uint32_t kPolicyGroups = 512;
 
 // Validate and plan (no HIP calls).
 rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype, float temperature,
