@@ -45,20 +45,27 @@ constexpr uint32_t kTopSlots = 8;          // entries per lane and wave in the t
 
 // Tunables, measured on MI355X; a variant build may override one with -D.
 // When a row of `units` units is split over workgroups: a workgroup per row
-// takes about 4.5 us + 0.7 us per unit up to 256 rows (a wave takes its blocks
-// one after the other), a split launch about 5.5 us + 3.6 ns per workgroup, so
-// for rows + kSplitCost / units <= kSplitRows.  Measured, split against not:
-// 64 x 131072 9.4 against 15.7 us, 128 12.9 / 16.3, 192 16.0 / 16.5, 256
-// 19.1 / 16.4; 64 x 50257 6.7 / 9.2, 128 9.2 / 9.7, 256 12.3 / 10.2; 64 x 12000
-// 5.9 / 5.8; 128 x 32000 binary32 8.4 / 7.8.
+// takes about 4 us + 0.8 us per unit up to 256 rows (a wave takes its blocks one
+// after the other), a split launch about 5.5 us + 2.9 ns per workgroup, with
+// alternatives 8.5 us + 3.9 ns; so for rows + kSplitCost / units <= kSplitRows.
+// Measured in us, split against not: 131072 bf16 columns (16 units), 64 rows
+// 8.5 / 17.0, 192 14.4 / 17.5, 224 16.1 / 17.5, 256 17.2 / 17.8; 50257 (7), 64
+// 5.8 / 9.1, 176 9.8 / 10.0, 208 10.6 / 10.1; 32000 binary32 (4), 80 6.1 / 6.9,
+// 112 7.0 / 7.1, 144 8.2 / 7.2.  With 8 alternatives: 131072, 192 20.2 / 20.8,
+// 224 22.8 / 21.3; 50257, 64 9.6 / 12, 144 13.8 / 13.1; 32000 binary32, 64
+// 8.6 / 9.2, 96 9.8 / 8.9.
 #ifndef ROG_SPLIT_ROWS
-#define ROG_SPLIT_ROWS 176
+#define ROG_SPLIT_ROWS 270
 #endif
-constexpr uint32_t kSplitRows = ROG_SPLIT_ROWS, kSplitCost = 256;
+#ifndef ROG_SPLIT_ROWS_TOP
+#define ROG_SPLIT_ROWS_TOP 205
+#endif
+constexpr uint32_t kSplitRows = ROG_SPLIT_ROWS, kSplitRowsTop = ROG_SPLIT_ROWS_TOP, kSplitCost = 600;
 // Logits' bytes from which their loads are streamed past the caches: 4096 x
-// 131072 bf16 166 us streamed against 186 cached, 8627 x 8192 26.8 against
-// 29.2; below, repeated calls find them in the Infinity Cache (1021 x 50257
-// 23.2 cached against 24.9, 509 x 32003 binary32 20.4 against 22.0).
+// 131072 bf16 163-170 us streamed against 186 cached, its gradient 330 against
+// 349, 8627 x 8192 26.2 against 29.6; below, the Infinity Cache may hold them
+// (1021 x 50257 binary16 20.4 cached against 21.0, its gradient after it 30.0
+// against 34.8).
 #ifndef ROG_HEAD_NT_MIN_BYTES
 #define ROG_HEAD_NT_MIN_BYTES (128ull << 20)
 #endif

@@ -100,9 +100,10 @@ rog_status choose_form(uint32_t blocks, size_t rows, int top_k, rog_logprob_form
         return ROG_ERR_INVALID_ARGUMENT;
     const uint32_t units = units_of(blocks);
     const bool wave = blocks <= kUnitBlocks, may_split = rows <= kHeadCounters && !wave;
+    const uint64_t split_rows = top_k ? kSplitRowsTop : kSplitRows;
     if (form == ROG_LOGPROB_AUTO)
         form = wave ? ROG_LOGPROB_WAVE
-               : may_split && rows * units + kSplitCost <= kSplitRows * uint64_t(units) ? ROG_LOGPROB_SPLIT : ROG_LOGPROB_ROW;
+               : may_split && rows * units + kSplitCost <= split_rows * units ? ROG_LOGPROB_SPLIT : ROG_LOGPROB_ROW;
     if ((form == ROG_LOGPROB_SPLIT && !may_split) || (form == ROG_LOGPROB_WAVE) != wave) return ROG_ERR_INVALID_ARGUMENT;
     const uint64_t groups = form == ROG_LOGPROB_SPLIT  ? rows * uint64_t(units)
                             : form == ROG_LOGPROB_WAVE ? ceil_div(rows, kWaveRows) : rows;

@@ -108,11 +108,13 @@ def test_logprob_workspace():
 def test_forms():
     plan = rog.rog_logprob_plan_widths
     for widths, rows, form in (([1], 1, "wave"), ([8192], 100000, "wave"), ([2048] * 4, 5, "wave"), ([2048] * 5, 5, "split"),
-                               ([131072], 1, "split"), ([131072], 160, "split"), ([131072], 161, "row"), ([10000], 4096, "row"),
+                               ([131072], 1, "split"), ([131072], 232, "split"), ([131072], 233, "row"), ([10000], 4096, "row"),
                                ([500] * 64, 3, "split"), ([0, 0], 3, "wave")):
         p = plan(widths, rows, BF16)
         assert p["form"] == form, (widths, rows, p)
         assert (p["workspace_bytes"] > 0) == (form == "split")
+    for rows, form in ((1, "split"), (167, "split"), (168, "row")):      # alternatives cost a split row more
+        assert plan([131072], rows, BF16, 8)["form"] == form
     assert plan([131072], 0, BF16)["form"] == "none"
     # a row's blocks follow its shards' widths, not the type
     assert plan([2049, 1], 3, BF16)["blocks"] == plan([2049, 1], 3, F32)["blocks"] == 3
