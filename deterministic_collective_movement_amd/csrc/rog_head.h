@@ -127,7 +127,7 @@ struct LogprobArgs {
 struct LogprobGradArgs {
     const int64_t *tokens;
     const float *lse, *entropy, *g_logp, *g_entropy;
-    float scale, inv_t;
+    float inv_t;                       // 1 / temperature
     uint32_t rows, vocab;
     uint32_t groups;                   // pieces of all rows
     Divider pieces_div;                // divides by sh.blocks, the pieces of a row

@@ -225,7 +225,6 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     a.entropy = entropy;
     a.g_logp = g_logp;
     a.g_entropy = g_entropy;
-    a.scale = float(kLog2E / double(temperature));
     a.inv_t = float(1.0 / double(temperature));
     a.rows = uint32_t(rows);
     a.vocab = vocab;

@@ -2,9 +2,12 @@
 // for gfx950 (CDNA4) and the C entry point that launches it.
 //
 //     dx_j = (g (1[j = token] - p_j) - h p_j (log p_j + H)) / T,  p_j = e^{x_j / T - lse}
-//          = p_j (A + B y_j) + [j = token] g / T,   y_j = log2 p_j,
-//     A = -(g + h H) / T,  B = -h ln 2 / T:
-// one read and one write of every logit, nothing joined between columns.
+//          = p_j (A + B z_j) + [j = token] g / T,   z_j = log p_j = x_j / T - lse,
+//     A = -(g + h H) / T,  B = -h / T:
+// one read and one write of every logit, nothing joined between columns.  z is
+// rounded once, so where p is large, and z near 0, p keeps its last bits (in
+// units of log2, with log2(e) / T rounded before it meets x, a binary32 gradient
+// was 2e-7 off; so it is 5e-8).
 #include <hip/hip_runtime.h>
 
 #include "rog_head_device.h"
@@ -14,14 +17,16 @@ namespace {
 
 #pragma clang fp contract(off)
 
-constexpr float kLog2EHi = 1.44269502f;                 // log2(e) in two parts
-constexpr float kLog2ELo = 1.92596303e-8f;
+constexpr float kLog2E32 = 1.44269502f;
 constexpr float kExtreme = 7.442609e8f;                 // 2^30 ln 2, where rog_logprob's extreme rows begin
 
-// One wave, a workgroup of its own, per piece of a row: 4096 x 131072 bf16 over
-// eight shards took 334 us with pieces of 2 KB, against 358 with four waves of
-// 4 KB each, 372 with 1 KB, and 365 and more where waves took several pieces
-// in turn.
+// One wave, a workgroup of its own, per piece of a row, its stores streamed.
+// Bound by HBM: 4096 x 131072 bf16 over eight shards (2.15 GB) take 327-333 us = 6.5
+// TB/s with pieces of 2 KB, against 358 with four waves of 4 KB each, 372 with
+// 1 KB, and 365 and more where waves took several pieces in turn; read once and
+// written once (counted: 1.0 times the bytes).  1021 x 50257 binary16, whose logits a
+// forward pass left in the Infinity Cache, 30 us (192 MB); 33 x 32003 binary32
+// 3.7 us, a launch and one round trip.
 template <int DT, bool NT>
 __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
     const LogprobGradArgs &a = launch_args<LogprobGradArgs>();
@@ -50,7 +55,7 @@ __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
         if (tiny) l.v[0] = load_tiny<DT>(at.p, at.n);
 #pragma unroll
         for (uint32_t i = 0; i < vecs; ++i) widen_vec<DT>(l.v[i], x + i * per);
-        const float scaled = g * a.inv_t, A = -(g + h * H) * a.inv_t, B = -h * a.inv_t * kLn2;
+        const float scaled = g * a.inv_t, A = -(g + h * H) * a.inv_t, B = -h * a.inv_t;
         if (fabsf(lse) >= kExtreme) {
             // Logits this large lie so far apart that only those equal to the
             // largest have any probability, the same for each: e^{-H}.
@@ -62,13 +67,11 @@ __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
                 x[i] = x[i] > -kInf && z == lse ? -scaled * p : 0.0f;
             }
         } else {
-            const float hi = lse * kLog2EHi;            // lse log2(e) = hi + lo
-            const float lo = __builtin_fmaf(lse, kLog2ELo, __builtin_fmaf(lse, kLog2EHi, -hi));
 #pragma unroll
             for (uint32_t i = 0; i < each; ++i) {
-                // -200 stands for anything less (p is zero there), so that 0 * y stays 0
-                const float y = fmaxf(__builtin_fmaf(x[i], a.scale, -hi) - lo, -200.0f);
-                x[i] = exp2_fast(y) * __builtin_fmaf(B, y, A);
+                // -140 stands for anything less (p is zero there), so that 0 * z stays 0
+                const float z = fmaxf(__builtin_fmaf(x[i], a.inv_t, -lse), -140.0f);
+                x[i] = exp2_fast(z * kLog2E32) * __builtin_fmaf(B, z, A);
             }
         }
         const int64_t t = tok - int64_t(at.col);
