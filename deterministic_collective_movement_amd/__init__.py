@@ -1,5 +1,6 @@
 """deterministic_collective_movement_amd -- rank-ordered gather and rank-ordered
-sum (rog) for MI355X.
+sum (rog) for MI355X, and the vocabulary side of a policy head over rank shards:
+token log probabilities, their gradient and the policy loss.
 
 The library is the C-ABI shared object ``librog.so`` (declared in
 ``include/rog.h``) built from the hand-written HIP kernels under ``csrc/``.
