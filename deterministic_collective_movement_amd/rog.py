@@ -626,12 +626,16 @@ def rog_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
     """A zero-filled workspace of at least ``nbytes`` for calls on ``stream``
     (default: the current one), for callers that keep their own."""
     device = torch.device("cuda", _current_device()) if device is None else torch.device(device)
+    with _made_on(stream, device):
+        return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=device)
+
+
+def _made_on(stream, device: torch.device):
+    """Where a call makes its outputs: on the stream that writes them, so that
+    their memory is none that another stream's earlier work still uses."""
     if stream is None:
-        return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=device)
+        return _HERE
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device))
 
 
 def _own_workspace(nbytes: int, device: torch.device, stream, handle: int):
@@ -800,8 +804,9 @@ def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor
     f32, i64 = torch.float32, torch.int64
     if out is None:
         new = lambda *shape, dtype=f32: torch.empty(*shape, dtype=dtype, device=device)  # noqa: E731
-        out = RogLogprob(new(rows) if tokens is not None else None, new(rows), new(rows),
-                         new(rows, top_k) if top_k else None, new(rows, top_k, dtype=i64) if top_k else None)
+        with _made_on(stream, device):
+            out = RogLogprob(new(rows) if tokens is not None else None, new(rows), new(rows),
+                             new(rows, top_k) if top_k else None, new(rows, top_k, dtype=i64) if top_k else None)
     elif type(out) is not RogLogprob:
         out = RogLogprob(*out)
     addr = _addresses(out[:3], _OUT_NAMES, rows, f32, device, idx)
@@ -846,7 +851,8 @@ def rog_logprob_grad(shards: Sequence[torch.Tensor], tokens: torch.Tensor, lse: 
         return out if isinstance(out, list) else list(out)
     device, idx, rows, dtype, packed = _shard_bytes(shards)
     if out is None:
-        out = [torch.empty(rows, x.shape[1], dtype=dtype, device=device) for x in shards]
+        with _made_on(stream, device):
+            out = [torch.empty(rows, x.shape[1], dtype=dtype, device=device) for x in shards]
     W = len(shards)
     if len(out) != W:
         raise ValueError("one gradient per shard")
@@ -896,8 +902,9 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
     if old_logp is None or advantage is None:
         raise ValueError("old_logp and advantage are needed")
     if out is None:
-        out = RogPolicyLoss(torch.empty(4, dtype=f32, device=device), torch.empty(n, dtype=f32, device=device),
-                            torch.empty(n, dtype=f32, device=device) if entropy is not None else None)
+        with _made_on(stream, device):
+            out = RogPolicyLoss(torch.empty(4, dtype=f32, device=device), torch.empty(n, dtype=f32, device=device),
+                                torch.empty(n, dtype=f32, device=device) if entropy is not None else None)
     elif type(out) is not RogPolicyLoss:
         out = RogPolicyLoss(*out)
     addr = _addresses((logp, old_logp, advantage, weight, ref_logp, entropy, out[1], out[2]), _LOSS_NAMES, n, f32, device, idx)

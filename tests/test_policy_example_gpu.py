@@ -109,3 +109,26 @@ def test_both_ways_through_the_binding(gpu):
     with torch.cuda.stream(side):
         call()
     check()
+
+
+def test_outputs_belong_to_the_stream_that_writes_them(gpu):
+    """A call on another stream takes no memory that the current stream has just given back."""
+    n = 300000
+    x, tokens = torch.randn(3, n, device=gpu), torch.zeros(3, dtype=torch.int64, device=gpu)
+    vectors = [torch.randn(n, device=gpu) for _ in range(3)]
+    row = torch.randn(3, device=gpu)
+    want, d_want, l_want = (rog.rog_logprob([x], tokens), rog.rog_logprob_grad([x], tokens, row, row, row), rog.rog_policy_loss(*vectors))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        freed = set()
+        for shape in ((3,), (n,), (3, n)):
+            t = torch.empty(*shape, device=gpu)
+            freed.add(t.data_ptr())
+            del t
+        got = [*rog.rog_logprob([x], tokens, stream=stream)[:3], *rog.rog_logprob_grad([x], tokens, row, row, row, stream=stream),
+               *rog.rog_policy_loss(*vectors, stream=stream)[:2]]
+        assert not freed & {t.data_ptr() for t in got}
+        side.synchronize()
+        for a, b in zip(got, [*want[:3], *d_want, *l_want[:2]]):
+            assert torch.equal(a, b)
