@@ -116,7 +116,7 @@ struct LogprobArgs {
     uint32_t vocab;
     float scale;                       // log2(e) / temperature
     float inv_t;                       // 1 / temperature
-    float bound;                       // |x| that leaves the scaled range; binary16: its largest
+    float bound;                       // |x| that leaves the scaled range (no binary16 does)
     float *logp, *entropy, *lse, *top_logp;
     int64_t *top_ids;
     uint32_t *counters;                // split: one per row

@@ -351,25 +351,42 @@ struct Lane32<ROG_DTYPE_F16> {
     }
 };
 
-// The state of a lane's 32 logits of a block.  bound * scale is 2^30 (binary16:
-// less): up to there the rounding of R stays below 64, so that no term
-// overflows.  Where
-// any lane of the wave holds a logit below -bound (-inf, or a mask of the
-// lowest finite value; looking for the smallest costs half of raising all),
-// those count as -bound: nothing against
-// any reference but their own, and finite, so that 0 * (z - R) stays 0.  A row
-// whose largest logit is at a bound or beyond is read again (the kernels'
-// extreme rows).
+// The state of a lane's 32 logits of a block.  bound * scale is 2^30: up to
+// there the rounding of R stays below 64, so that no term overflows.  Where any
+// lane of the wave holds a logit below -bound (-inf, or a mask of the lowest
+// finite value; looking for the smallest costs half of raising all), those count
+// as -bound: nothing against any reference but their own, and finite, so that
+// 0 * (z - R) stays 0.  A row whose largest logit is at a bound or beyond is read
+// again (the kernels' extreme rows).
+//
+// binary16, packed as it is, counts -inf as its lowest value instead: at most
+// 2^-64 against a largest logit that is as far above; with one that is nearer
+// in some lane, -inf is looked for column by column.  A lane that holds only
+// -inf takes a reference of 2^30, against which all of it is nothing.
 template <int DT>
 __device__ __forceinline__ State state_of(const vec16 (&v)[Logit<DT>::kVecs], const Scaling &c) {
     Lane32<DT> x(v);
     const float m = x.largest();
     const float r = c.ref(m);
-    if (__ballot(x.smallest() < -c.bound)) x.raise(-c.bound);
-    float s[4], t[4];
+    float s[4], t[4], from = r;
+    if (__ballot(x.smallest() < -c.bound)) {
+        if constexpr (DT == ROG_DTYPE_F16) {
+            if (__ballot(m > -kInf && (m + 65504.0f) * c.scale < 64.0f)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float z = x.at(i), y = z > -kInf ? __builtin_fmaf(z, c.scale, -r) : -200.0f, e = exp2_fast(y);
+                    s[i & 3] = i < 4 ? e : s[i & 3] + e;
+                    t[i & 3] = i < 4 ? e * y : __builtin_fmaf(e, y, t[i & 3]);
+                }
+                return State{m, r, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3])};
+            }
+            from = m > -kInf ? r : 1073741824.0f;
+        }
+        x.raise(-c.bound);
+    }
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const float y = __builtin_fmaf(x.at(i), c.scale, -r);
+        const float y = __builtin_fmaf(x.at(i), c.scale, -from);
         const float e = exp2_fast(y);
         s[i & 3] = i < 4 ? e : s[i & 3] + e;
         t[i & 3] = i < 4 ? e * y : __builtin_fmaf(e, y, t[i & 3]);

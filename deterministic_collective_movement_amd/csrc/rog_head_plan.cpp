@@ -166,7 +166,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     a.part = need ? reinterpret_cast<float *>(static_cast<char *>(workspace) + kHeadCounterBytes) : nullptr;
     a.scale = float(kLog2E / double(temperature));
     a.inv_t = float(1.0 / double(temperature));
-    a.bound = dtype == ROG_DTYPE_F16 ? 65504.0f : float(ldexp(double(temperature) / kLog2E, 30));
+    a.bound = float(ldexp(double(temperature) / kLog2E, 30));
     a.rows = uint32_t(rows);
     a.chunks = chunks_of(blocks);
     a.units = units_of(blocks);

@@ -312,11 +312,9 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
     v.lse = (v.r + v.l) * kLn2;
     v.extreme = false;
     float entropy = (v.l - all.t / all.s) * kLn2;
-    if ((DT != ROG_DTYPE_F16 && all.m >= a.bound) || all.m <= -a.bound) {
+    if (DT != ROG_DTYPE_F16 && fabsf(all.m) >= a.bound) {
         // Logits this large lie so far apart that any but the largest has
         // probability 0: the row is uniform over the columns that equal it.
-        // (binary16 stays in the scaled range; its lowest value may be mixed
-        // with -inf, which counts as it in the states.)
         atomicAdd(&equal, count_equal<DT>(a, row, tid / 64, T::kTeamWaves, tid & 63, all.m));
         T::sync();
         v.extreme = true;

@@ -142,6 +142,24 @@ def test_masks_and_infinities(gpu, widths, dtype):
     assert bool((got.top_ids[6] == torch.arange(k, device=gpu)).all())
 
 
+@pytest.mark.parametrize("T", [1.0, 8.0, 1024.0])
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("widths", [[3], [37], [3000], [9001, 9000], [70001]], ids=str)
+def test_lowest_logits_beside_infinities(gpu, widths, dtype, T):
+    """-inf stays nothing where the others are binary16's lowest values, however small a temperature makes the distance."""
+    V = sum(widths)
+    ramp = (-65504.0 + 32.0 * torch.arange(V, device=gpu).remainder(8)).to(dtype)
+    x = torch.full((6, V), -math.inf, dtype=dtype, device=gpu)
+    x[0, V // 2] = -65472.0
+    x[1, ::2] = ramp[::2]
+    x[2, V - 1] = -65504.0
+    x[3, 3 * V // 4:] = ramp[3 * V // 4:]
+    x[4, :2] = ramp[:2]
+    x[5, ::3] = -60000.0
+    tokens = torch.tensor([V // 2, 0, V - 1, 0, 1, 0], device=gpu)
+    check(list(torch.split(x, widths, 1)), tokens, T, 5)
+
+
 @pytest.mark.parametrize("k", [1, 3, 20, 31, 32])
 def test_alternatives_under_ties(gpu, k):
     """Few distinct values, so that far more columns reach the K-th best value than are wanted."""
