@@ -127,8 +127,8 @@ struct Cursor {
         col0 = s.col0;
         base = (gbyte *)s.x + int64_t(row) * s.stride;
     }
-    // Block b (below the row's blocks, not before the shard that the cursor is in).
-    __device__ __forceinline__ BlockAt at(uint32_t b) {
+    // To the shard of block b (below the row's blocks, not before the shard that the cursor is in).
+    __device__ __forceinline__ void seek(uint32_t b) {
         if (b >= end) {
             if (h.W == 1) {
                 first = 0;
@@ -147,9 +147,17 @@ struct Cursor {
                 enter(r);
             }
         }
+    }
+    // The n columns of the shard from off on.
+    __device__ __forceinline__ BlockAt columns(uint32_t off, uint32_t n) const {
+        gbyte *const p = base + uint64_t(off) * Logit<DT>::kSize;
+        const bool shift = DT != ROG_DTYPE_F32 && n == COLUMNS && (reinterpret_cast<uintptr_t>((const uint8_t *)p) & 2) != 0;
+        return BlockAt{p, n, col0 + off, shard, off, shift};
+    }
+    __device__ __forceinline__ BlockAt at(uint32_t b) {
+        seek(b);
         const uint32_t off = (b - first) * COLUMNS, left = width - off;
-        const bool shift = DT != ROG_DTYPE_F32 && left >= COLUMNS && (reinterpret_cast<uintptr_t>((const uint8_t *)base) & 2) != 0;
-        return BlockAt{base + uint64_t(off) * Logit<DT>::kSize, left < COLUMNS ? left : COLUMNS, col0 + off, shard, off, shift};
+        return columns(off, left < COLUMNS ? left : COLUMNS);
     }
 };
 

@@ -51,8 +51,9 @@ constexpr float kMinTemperature = 1.0f / 1024, kMaxTemperature = 1024.0f;
 constexpr double kLog2E = 1.4426950408889634;
 
 // Shared checks of the logits, and their layout into the kernel arguments.
+// heads: columns by which the blocks of each shard may begin early (NULL: none do).
 rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype, bool addresses,
-                      uint32_t block, HeadShards *h, uint32_t *vocab, uint32_t *blocks) {
+                      uint32_t block, const uint32_t *heads, HeadShards *h, uint32_t *vocab, uint32_t *blocks) {
     if (!shards || W < 1 || W > kMaxPeers || !known(dtype)) return ROG_ERR_INVALID_ARGUMENT;
     const uint32_t es = esize(dtype);
     uint64_t v = 0, b = 0;
@@ -68,7 +69,7 @@ rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dty
         o = Shard{s.logits, 0, uint32_t(s.width), uint32_t(v)};
         h->block0[r] = uint32_t(b);
         v += uint64_t(s.width);
-        b += ceil_div(uint64_t(s.width), block);
+        b += s.width ? ceil_div(uint64_t(s.width) + (heads ? heads[r] : 0), block) : 0;
         if (addresses) {
             if (uint64_t(s.row_stride) >= uint64_t(1) << 48) return ROG_ERR_TOO_LARGE;
             o.stride = s.row_stride * es;
@@ -125,7 +126,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     LogprobArgs &a = p->args;
     uint32_t vocab = 0, blocks = 0;
     if (!out || !(temperature >= kMinTemperature && temperature <= kMaxTemperature)) return ROG_ERR_INVALID_ARGUMENT;
-    rog_status st = lay_shards(shards, W, rows, dtype, true, kHeadBlock, &a.sh, &vocab, &blocks);
+    rog_status st = lay_shards(shards, W, rows, dtype, true, kHeadBlock, nullptr, &a.sh, &vocab, &blocks);
     if (st != ROG_OK) return st;
     st = choose_form(blocks, rows, top_k, form, &p->info);
     if (st != ROG_OK || rows == 0) return st;
@@ -187,7 +188,14 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     uint32_t vocab = 0, blocks = 0;
     p->grid = 0;
     if (!grads || !(temperature >= kMinTemperature && temperature <= kMaxTemperature)) return ROG_ERR_INVALID_ARGUMENT;
-    rog_status st = lay_shards(shards, W, rows, dtype, true, kGradPieceBytes / (known(dtype) ? esize(dtype) : 4), &a.sh, &vocab, &blocks);
+    // Pieces begin with the gradient's 128-byte lines: as many columns early as a row's first line may hold of others.
+    const uint32_t size = known(dtype) ? esize(dtype) : 4;
+    uint32_t heads[kMaxPeers] = {};
+    for (int r = 0; r < W && r < kMaxPeers; ++r) {
+        const uint64_t places = addr(grads[r].grad) | uint64_t(grads[r].row_stride) * size | 128;
+        heads[r] = uint32_t(128 - (places & -places)) / size;
+    }
+    rog_status st = lay_shards(shards, W, rows, dtype, true, kGradPieceBytes / size, heads, &a.sh, &vocab, &blocks);
     if (st != ROG_OK) return st;
     if (rows == 0 || vocab == 0) return ROG_OK;
     if (!tokens || !lse || !entropy || !g_logp || addr(tokens) % 8 ||
@@ -317,7 +325,7 @@ ROG_API rog_status rog_logprob_plan(const rog_logit_shard *shards, int W, size_t
     if (!info) return ROG_ERR_INVALID_ARGUMENT;
     rog::HeadShards h;
     uint32_t vocab = 0, blocks = 0;
-    const rog_status st = rog::lay_shards(shards, W, rows, dtype, false, rog::kHeadBlock, &h, &vocab, &blocks);
+    const rog_status st = rog::lay_shards(shards, W, rows, dtype, false, rog::kHeadBlock, nullptr, &h, &vocab, &blocks);
     return st != ROG_OK ? st : rog::choose_form(blocks, rows, top_k, form, info);
 }
 

@@ -21,12 +21,14 @@ constexpr float kLog2E32 = 1.44269502f;
 constexpr float kExtreme = 7.442609e8f;                 // 2^30 ln 2, where rog_logprob's extreme rows begin
 
 // One wave, a workgroup of its own, per piece of a row, its stores streamed.
-// Bound by HBM: 4096 x 131072 bf16 over eight shards (2.15 GB) take 327-333 us = 6.5
-// TB/s with pieces of 2 KB, against 358 with four waves of 4 KB each, 372 with
-// 1 KB, and 365 and more where waves took several pieces in turn; read once and
-// written once (counted: 1.0 times the bytes).  1021 x 50257 binary16, whose logits a
-// forward pass left in the Infinity Cache, 30 us (192 MB); 33 x 32003 binary32
-// 3.7 us, a launch and one round trip.
+// Bound by HBM: 4096 x 131072 bf16 over eight shards (2.15 GB) take 325-331 us =
+// 6.5-6.6 TB/s with pieces of 2 KB, against 358 with four waves of 4 KB each, 372
+// with 1 KB, and 365 and more where waves took several pieces in turn; read once
+// and written once (counted: 1.0 times the bytes).  Pieces begin with lines of the
+// gradient, whatever the row's alignment: 4000 x 100003 bf16 278 us, against 321
+// with pieces counted from the row's beginning, whose ends share lines.
+// 1021 x 50257 binary16, whose logits a forward pass left in the Infinity Cache,
+// 29-30 us (192 MB); 33 x 32003 binary32 3.6 us, a launch and one round trip.
 template <int DT, bool NT>
 __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
     const LogprobGradArgs &a = launch_args<LogprobGradArgs>();
@@ -39,9 +41,17 @@ __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
     // everything that a wave needs of its row, asked for at once
     const int64_t tok = a.tokens[row];
     const float lse = a.lse[row], H = a.entropy[row], g = a.g_logp[row], h = a.g_entropy ? a.g_entropy[row] : 0.0f;
-    const BlockAt at = Cursor<DT, 64 * each>(a.sh, row).at(piece);
+    Cursor<DT, 64 * each> cur(a.sh, row);
+    cur.seek(piece);
     typedef __attribute__((address_space(1))) uint8_t gout;
-    gout *const o = (gout *)a.g[at.shard] + int64_t(row) * a.g_stride[at.shard] + uint64_t(at.off) * Logit<DT>::kSize;
+    gout *const line = (gout *)a.g[cur.shard] + int64_t(row) * a.g_stride[cur.shard];
+    // pieces begin where the gradient's 128-byte lines do, but for the first
+    const uint32_t head = uint32_t(reinterpret_cast<uintptr_t>((uint8_t *)line) % 128) / Logit<DT>::kSize;
+    const uint32_t begin = (piece - cur.first) * (64 * each), end = begin + 64 * each - head;
+    const uint32_t off = begin > head ? begin - head : 0;
+    if (off >= cur.width) return;
+    const BlockAt at = cur.columns(off, (end < cur.width ? end : cur.width) - off);
+    gout *const o = line + uint64_t(off) * Logit<DT>::kSize;
     const bool none = tok < 0 || lse == -kInf, bad = tok >= int64_t(a.vocab) || !(lse < kInf);
     const bool tiny = at.n < per;
     float x[each];

@@ -399,6 +399,35 @@ def test_gradient_masks(gpu, dtype):
     assert torch.equal(whole.view(torch.uint8), got[0].view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=["bf16", "f16", "f32"])
+def test_gradient_at_every_place_of_a_line(gpu, dtype):
+    """Rows that begin anywhere in a 128-byte line, with pieces that end anywhere: the same bits, nothing beside them, in place too."""
+    size = 4 if dtype is F32 else 2
+    piece, line = 2048 // size, 128 // size
+    rows = 3
+    gen = torch.Generator(device=gpu)
+    gen.manual_seed(9)
+    g, gh = (torch.randn(rows, generator=gen, device=gpu) for _ in range(2))
+    for width in (1, line - 1, piece - line + 1, piece - 1, piece + 2, 2 * piece + 5):
+        x = make(rows, [width], dtype, width, gpu)[0]
+        tokens = some_tokens(rows, width, width, gpu)
+        r = rog.rog_logprob([x], tokens)
+        want = rog.rog_logprob_grad([x], tokens, r.lse, r.entropy, g, gh)[0]
+        stride = width + 3 + line // 2
+        for offset in range(0, line + 1):
+            buf = torch.full((rows * stride + 2 * line,), 7.0, dtype=dtype, device=gpu)
+            view = torch.as_strided(buf, (rows, width), (stride, 1), offset)
+            rog.rog_logprob_grad([x], tokens, r.lse, r.entropy, g, gh, out=[view])
+            assert torch.equal(view.contiguous().view(torch.uint8), want.view(torch.uint8)), (width, offset)
+            view.fill_(7.0)
+            assert bool((buf == 7.0).all()), (width, offset)
+            view.copy_(x)
+            rog.rog_logprob_grad([view], tokens, r.lse, r.entropy, g, gh, out=[view])
+            assert torch.equal(view.contiguous().view(torch.uint8), want.view(torch.uint8)), (width, offset)
+            view.fill_(7.0)
+            assert bool((buf == 7.0).all()), (width, offset)
+
+
 def test_gradient_against_differences(gpu):
     """Central differences of the kernel's own log probability and entropy."""
     V, rows, T, h = 301, 3, 0.8, 2.0 ** -4
