@@ -117,6 +117,7 @@ struct LogprobArgs {
     float scale;                       // log2(e) / temperature
     float inv_t;                       // 1 / temperature
     float bound;                       // |x| that leaves the scaled range (no binary16 does)
+    float inv_t_rest;                  // 1 / temperature - inv_t
     float *logp, *entropy, *lse, *top_logp;
     int64_t *top_ids;
     uint32_t *counters;                // split: one per row
@@ -128,7 +129,8 @@ struct LogprobGradArgs {
     const int64_t *tokens;
     const float *lse, *entropy, *g_logp, *g_entropy;
     float inv_t;                       // 1 / temperature
-    uint32_t rows, vocab;
+    float inv_t_rest;                  // and what its rounding left off
+    uint32_t vocab;
     uint32_t groups;                   // pieces of all rows
     Divider pieces_div;                // divides by sh.blocks, the pieces of a row
     HeadShards sh;                     // its blocks are pieces here

@@ -105,7 +105,7 @@ __device__ __forceinline__ void hold_front(const LogprobArgs &a) {
 }
 __device__ __forceinline__ void hold_front(const LogprobGradArgs &a) {
     asm volatile("" ::"s"(a.tokens), "s"(a.lse), "s"(a.entropy), "s"(a.g_logp), "s"(a.g_entropy), "s"(a.inv_t),
-                 "s"(a.groups), "s"(a.sh.W), "s"(a.sh.blocks), "s"(a.sh.even), "s"(a.sh.s[0].x), "s"(a.sh.s[0].stride),
+                 "s"(a.inv_t_rest), "s"(a.groups), "s"(a.sh.W), "s"(a.sh.blocks), "s"(a.sh.even), "s"(a.sh.s[0].x), "s"(a.sh.s[0].stride),
                  "s"(a.sh.s[0].width));
 }
 

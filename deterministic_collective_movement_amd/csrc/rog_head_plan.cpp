@@ -50,6 +50,13 @@ constexpr uint64_t kMaxGroups = uint64_t(1) << 31;   // workgroups of one launch
 constexpr float kMinTemperature = 1.0f / 1024, kMaxTemperature = 1024.0f;
 constexpr double kLog2E = 1.4426950408889634;
 
+// 1 / temperature as a binary32 number and the rest, to 2^-48 of it together.
+void invert(float temperature, float *inv, float *rest) {
+    const double t = 1.0 / double(temperature);
+    *inv = float(t);
+    *rest = float(t - double(*inv));
+}
+
 // Shared checks of the logits, and their layout into the kernel arguments.
 // heads: columns by which the blocks of each shard may begin early (NULL: none do).
 rog_status lay_shards(const rog_logit_shard *shards, int W, size_t rows, rog_dtype dtype, bool addresses,
@@ -166,7 +173,7 @@ rog_status plan_logprob(const rog_logit_shard *shards, int W, size_t rows, rog_d
     a.counters = static_cast<uint32_t *>(workspace);
     a.part = need ? reinterpret_cast<float *>(static_cast<char *>(workspace) + kHeadCounterBytes) : nullptr;
     a.scale = float(kLog2E / double(temperature));
-    a.inv_t = float(1.0 / double(temperature));
+    invert(temperature, &a.inv_t, &a.inv_t_rest);
     a.bound = float(ldexp(double(temperature) / kLog2E, 30));
     a.rows = uint32_t(rows);
     a.chunks = chunks_of(blocks);
@@ -233,8 +240,7 @@ rog_status plan_logprob_grad(const rog_logit_shard *shards, const rog_grad_shard
     a.entropy = entropy;
     a.g_logp = g_logp;
     a.g_entropy = g_entropy;
-    a.inv_t = float(1.0 / double(temperature));
-    a.rows = uint32_t(rows);
+    invert(temperature, &a.inv_t, &a.inv_t_rest);
     a.vocab = vocab;
     a.pieces_div = make_divider(blocks);
     const uint64_t pieces = uint64_t(blocks) * rows;

@@ -4,8 +4,10 @@
 // Per row of V logits x_j, z_j = x_j log2(e) / T, in one pass over the row:
 // every lane keeps the partial states (m, s, t) of its columns (rog_head_device.h),
 // states are joined in a fixed order, and with M, S, T' of the whole row
-//     L = log2 S,  lse = (ref(M) + L) ln 2,  logp = ((z_token - ref(M)) - L) ln 2,
-//     entropy = (L - T' / S) ln 2.
+//     L = log2 S,  lse = M / T + (L - (M log2(e) / T - ref(M))) ln 2,
+//     logp = ((z_token - ref(M)) - L) ln 2,  entropy = (L - T' / S) ln 2.
+// M / T is rounded together with the rest, once, so that lse is off by half a
+// unit in its last place and what the sums leave, however large M is.
 // The K best alternatives come without a second pass over the row: each lane
 // leaves the maxima of its blocks in a table in shared memory.  The K-th largest
 // of the 64 lanes' row maxima is a value that at least K columns reach, so only
@@ -131,6 +133,10 @@ constexpr float kMaxFinite = 3.40282347e38f;
 struct Row {
     float r, l, m, lse;
     bool extreme;
+    // m / T + x: 1 / T in two parts, one rounding of the size of the result
+    __device__ __forceinline__ float above_largest(float x, const LogprobArgs &a) const {
+        return __builtin_fmaf(m, a.inv_t, __builtin_fmaf(m, a.inv_t_rest, x));
+    }
     // log probability of a logit of the row
     __device__ __forceinline__ float logp(float x, const LogprobArgs &a) const {
         if (extreme) return (x - m) * a.inv_t - l * kLn2;
@@ -309,7 +315,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
     v.r = all.r;
     v.l = log_s;
     v.m = all.m;
-    v.lse = (v.r + v.l) * kLn2;
+    v.lse = v.above_largest((v.l - __builtin_fmaf(v.m, a.scale, -v.r)) * kLn2, a);
     v.extreme = false;
     float entropy = (v.l - all.t / all.s) * kLn2;
     if (DT != ROG_DTYPE_F16 && fabsf(all.m) >= a.bound) {
@@ -319,8 +325,8 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, uint32_t row, i
         T::sync();
         v.extreme = true;
         v.l = log2f(float(equal));
-        v.lse = __builtin_amdgcn_fmed3f(__builtin_fmaf(v.m, a.inv_t, v.l * kLn2), -kMaxFinite, kMaxFinite);
         entropy = v.l * kLn2;
+        v.lse = __builtin_amdgcn_fmed3f(v.above_largest(entropy, a), -kMaxFinite, kMaxFinite);
     }
     if (tid == T::kThreads - 1) {      // in the last wave, where the first one ranks the alternatives
         if (a.lse) a.lse[row] = v.lse;

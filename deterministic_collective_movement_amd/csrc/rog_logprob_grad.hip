@@ -7,7 +7,10 @@
 // one read and one write of every logit, nothing joined between columns.  z is
 // rounded once, so where p is large, and z near 0, p keeps its last bits (in
 // units of log2, with log2(e) / T rounded before it meets x, a binary32 gradient
-// was 2e-7 off; so it is 5e-8).
+// was 2e-7 off; so it is 5e-8).  lse is one rounded number for the row, which
+// leaves a factor of e^{2^(e - 24)} open in every p at |lse| = 2^e, up to 2^e = 64
+// about as much as the rounding of 1 / T does; from there on 1 / T comes in two
+// parts, and rows that are uniform over their largest logits are held to that.
 #include <hip/hip_runtime.h>
 
 #include "rog_head_device.h"
@@ -18,7 +21,15 @@ namespace {
 #pragma clang fp contract(off)
 
 constexpr float kLog2E32 = 1.44269502f;
-constexpr float kExtreme = 7.442609e8f;                 // 2^30 ln 2, where rog_logprob's extreme rows begin
+// |lse| above that of any row whose largest logit is below rog_logprob's bound
+// (2^30 ln 2, log 2^31, and the roundings of bound, T and lse).
+constexpr float kExtreme = 744261248.0f;
+// |lse| from which its rounding (2^-18 and more) is looked after: a row that is
+// uniform over its largest logits (masked as a whole, or sure of one token) has
+// log p = -H at each of them, so a z that lies within the rounding of -H is taken
+// to be -H.  Any other z that happens to lie there moves by less than one more
+// rounding of lse.
+constexpr float kLarge = 64.0f;
 
 // One wave, a workgroup of its own, per piece of a row, its stores streamed.
 // Bound by HBM: 4096 x 131072 bf16 over eight shards (2.15 GB) take 325-331 us =
@@ -73,16 +84,28 @@ __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
 #pragma unroll
             for (uint32_t i = 0; i < each; ++i) {
                 // rog_logprob's own lse of such a row, if x[i] is its largest logit
-                const float z = __builtin_amdgcn_fmed3f(__builtin_fmaf(x[i], a.inv_t, H), -3.40282347e38f, 3.40282347e38f);
-                x[i] = x[i] > -kInf && z == lse ? -scaled * p : 0.0f;
+                const float z = __builtin_fmaf(x[i], a.inv_t, __builtin_fmaf(x[i], a.inv_t_rest, H));
+                x[i] = x[i] > -kInf && __builtin_amdgcn_fmed3f(z, -3.40282347e38f, 3.40282347e38f) == lse ? -scaled * p : 0.0f;
             }
         } else {
+            // -140 stands for anything less (p is zero there), so that 0 * z stays 0; p is at most 1
+            if (fabsf(lse) >= kLarge) {
+                // half a unit in the last place of lse, and what its sums and H's leave
+                const float half = bits_f32((f32_bits(lse) & 0x7F800000u) - (24u << 23));
+                const float open = __builtin_fmaf(half, 1.0f / 64, half) + 0x1p-18f;
 #pragma unroll
-            for (uint32_t i = 0; i < each; ++i) {
-                // -140 stands for anything less (p is zero there), so that 0 * z stays 0
-                const float z = fmaxf(__builtin_fmaf(x[i], a.inv_t, -lse), -140.0f);
-                x[i] = exp2_fast(z * kLog2E32) * __builtin_fmaf(B, z, A);
+                for (uint32_t i = 0; i < each; ++i) {
+                    // the rest of 1 / T times -inf may be NaN: that ends at -140 too
+                    const float z = __builtin_fmaf(x[i], a.inv_t_rest, __builtin_fmaf(x[i], a.inv_t, -lse));
+                    x[i] = fminf(fmaxf(z, -140.0f), 0.0f);
+                    x[i] = fabsf(x[i] + H) <= open ? -H : x[i];
+                }
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < each; ++i) x[i] = fminf(fmaxf(__builtin_fmaf(x[i], a.inv_t, -lse), -140.0f), 0.0f);
             }
+#pragma unroll
+            for (uint32_t i = 0; i < each; ++i) x[i] = exp2_fast(x[i] * kLog2E32) * __builtin_fmaf(B, x[i], A);
         }
         const int64_t t = tok - int64_t(at.col);
         if (t >= 0 && t < int64_t(at.n)) {

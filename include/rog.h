@@ -385,6 +385,10 @@ typedef struct {
  * its alternatives' columns -1.  Rows masked with the type's lowest finite
  * value keep their meaning (lse is held within the finite range).
  *
+ * lse is one binary32 number, so at |lse| = 2^e its rounding leaves up to
+ * 2^(e - 24) of it open: 0.002 at 65504, 4 at 10^8.  logp, entropy and top_logp
+ * are formed from the row's sums, not from lse, and have none of that.
+ *
  * Errors (nothing enqueued):
  *   ROG_ERR_INVALID_ARGUMENT  shards or out NULL; W out of range; dtype, form or
  *                             top_k out of range; temperature outside
@@ -426,6 +430,15 @@ ROG_API rog_status rog_logprob_plan(const rog_logit_shard *shards, int W, size_t
  * same logits, widths and temperature.  g_entropy may be NULL (0).  A row that
  * is not scored or that its mask leaves nothing gets zeros; a token of V or
  * more, or a NaN in lse, NaN.
+ *
+ * p_j = e^{x_j / temperature - lse} has lse's rounding in it: at |lse| = 2^e it is
+ * held to a factor of e^{2^(e - 23)} (2^-17 for |lse| up to 64, 0.4 % at 65504;
+ * binary32 logits beyond 10^6 that differ by little are not resolved).  Rows that
+ * are uniform over their largest logits -- all of a row masked with one value, or
+ * a row that is sure of one token -- have p_j = e^{-entropy} there and are right
+ * at any size.  Where a temperature below 1 takes a row's largest logit past the
+ * binary32 range, lse is held at the range's end and every logit that passes it
+ * counts as a largest one.
  *
  * grads    W gradients.  A gradient may be exactly its logits' shard (same
  *          address and stride: in place); any other overlap is an error.
