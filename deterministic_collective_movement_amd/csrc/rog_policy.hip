@@ -146,7 +146,8 @@ __global__ __launch_bounds__(kHeadThreads) void rog_policy_kernel(PolicyArgs a) 
             const bool kept = w != 0.0f;
             const float d = x.logp[i] - x.old[i], adv = x.adv[i];
             const bool over = adv > 0.0f && d > a.hi, under = adv < 0.0f && d < a.lo, clipped = over || under;
-            const float pg = -adv * (over ? a.ratio_hi : under ? a.ratio_lo : exp_of(d));
+            // no advantage, no term: a finite ratio that binary32 holds as infinite included
+            const float pg = -adv * (over ? a.ratio_hi : under ? a.ratio_lo : exp_of(adv == 0.0f && d < kInf ? 0.0f : d));
             float loss = pg, slope = clipped ? 0.0f : pg, kl = 0.0f;
             if (a.ref) {
                 float grow;
