@@ -152,8 +152,10 @@ __global__ __launch_bounds__(kHeadThreads) void rog_policy_kernel(PolicyArgs a) 
             if (a.ref) {
                 float grow;
                 kl_of(x.ref[i] - x.logp[i], kl, grow);
-                loss = __builtin_fmaf(a.kl_coef, kl, loss);
-                slope = __builtin_fmaf(-a.kl_coef, grow, slope);
+                if (a.kl_coef != 0.0f) {        // else it is only watched, and may be infinite
+                    loss = __builtin_fmaf(a.kl_coef, kl, loss);
+                    slope = __builtin_fmaf(-a.kl_coef, grow, slope);
+                }
             }
             if (a.entropy) loss = __builtin_fmaf(-a.entropy_coef, x.ent[i], loss);
             const float gw = a.grad_scale * w;

@@ -494,7 +494,8 @@ typedef struct {
  * taken in binary64 in an order that depends on n alone, and rounded once.
  *
  * e^d and e^q are binary32: infinite past log of its largest value, 88.72.  A token
- * of advantage 0 adds nothing of its ratio, however large.
+ * of advantage 0 adds nothing of its ratio, however large, and with kl_coef 0 the
+ * KL is in the stats alone.
  *
  * An output array may be exactly one of the input arrays; any other overlap is
  * ROG_ERR_OVERLAP.  n == 0: stats are zero.  n of 2^34 or more: TOO_LARGE.

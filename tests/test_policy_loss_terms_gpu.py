@@ -40,3 +40,18 @@ def test_an_advantage_of_nothing_hides_no_nan(gpu):
     zero = torch.zeros(3, device=gpu)
     got = rog.rog_policy_loss(vec([0.0, math.nan, 0.0], gpu), zero, zero, weight=torch.ones(3, device=gpu))
     assert math.isnan(got.stats[0].item()) and [math.isnan(v) for v in got.g_logp.tolist()] == [False, True, False]
+
+
+def test_kl_that_is_only_watched(gpu):
+    """kl_coef 0 with a reference: stats hold the KL, the loss and the gradient nothing of it."""
+    q = vec(RATIOS, gpu)
+    n = len(RATIOS)
+    zero, one = torch.zeros(n, device=gpu), torch.ones(n, device=gpu)
+    got = rog.rog_policy_loss(zero, zero, -one, weight=one, ref_logp=q, kl_coef=0.0)
+    plain = rog.rog_policy_loss(zero, zero, -one, weight=one)
+    assert got.stats[0].item() == plain.stats[0].item() == n and torch.equal(got.g_logp, plain.g_logp)
+    assert got.stats[1].item() == math.inf
+    some = rog.rog_policy_loss(zero[:3], zero[:3], -one[:3], weight=one[:3], ref_logp=q[:3], kl_coef=0.0)
+    want = sum(math.expm1(v) - v for v in RATIOS[:3])
+    # e^88 as a product with a rounded exponent: 88 u put back, a few roundings left
+    assert abs(float(some.stats[1]) - want) <= 2 * 90 * ref.U * want
