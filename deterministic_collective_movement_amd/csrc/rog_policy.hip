@@ -4,8 +4,9 @@
 // Per token: d = logp - old, l = -A e^{clipped ? bound : d} + beta (e^q - 1 - q)
 // - c_H H and its derivative.  A workgroup takes a run of tiles of 1024 tokens,
 // four tokens per thread with the next tile's loads in flight, and sums its
-// four totals in binary64 over a fixed tree; the last workgroup to finish joins
-// the workgroups' totals in their order.
+// four totals in binary64 over a fixed tree (in binary32 even four tokens whose
+// advantages cancel would lose the small ones; 0.2 of 31.5 us); the last workgroup
+// to finish joins the workgroups' totals in their order.
 //
 // Bandwidth bound: 24 bytes read and 8 written per token with every term, about
 // 83 vector instructions.  4194307 tokens (134 MB) take 31 us = 4.3 TB/s:
@@ -139,7 +140,6 @@ __global__ __launch_bounds__(kHeadThreads) void rog_policy_kernel(PolicyArgs a) 
         const uint64_t place = place_of(at, a.n);
         const uint32_t first = uint32_t(at - place), end = a.n < 4 ? uint32_t(a.n) : 4;
         f32x4 g, gh;
-        float sums[4] = {0, 0, 0, 0};
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
             const float w = i >= first && i < end ? x.w[i] : 0.0f;
@@ -161,14 +161,13 @@ __global__ __launch_bounds__(kHeadThreads) void rog_policy_kernel(PolicyArgs a) 
             const float gw = a.grad_scale * w;
             g[i] = kept ? gw * slope : 0.0f;
             gh[i] = -(gw * a.entropy_coef);
-            // four tokens' terms in binary32, all else in binary64
-            sums[0] += kept ? w * loss : 0.0f;
-            sums[1] += kept ? w * kl : 0.0f;
-            sums[2] += kept ? w * x.ent[i] : 0.0f;
-            sums[3] += clipped ? w : 0.0f;
+            // a token's own numbers in binary32, its weighted terms exactly and their sums in binary64
+            const double wd = double(w);
+            t.v[0] = __builtin_fma(wd, double(kept ? loss : 0.0f), t.v[0]);
+            if (a.ref) t.v[1] = __builtin_fma(wd, double(kept ? kl : 0.0f), t.v[1]);
+            if (a.entropy) t.v[2] = __builtin_fma(wd, double(kept ? x.ent[i] : 0.0f), t.v[2]);
+            t.v[3] += clipped ? wd : 0.0;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t.v[i] += double(sums[i]);
         store4(a.g_logp, place, first, end, g);
         store4(a.g_entropy, place, first, end, gh);
     }

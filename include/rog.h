@@ -490,8 +490,9 @@ typedef struct {
  *
  * with lo = log(1 - clip_low) and hi = log(1 + clip_high) in binary32.  Weights
  * carry the ragged batch: 1 / tokens for a mean over tokens, 1 / (sequences *
- * length) for a mean over sequences, 0 for prompt and padding.  The sums are
- * taken in binary64 in an order that depends on n alone, and rounded once.
+ * length) for a mean over sequences, 0 for prompt and padding.  A token's own
+ * l, KL and entropy are binary32; weighted they are exact in binary64, where the
+ * sums are taken in an order that depends on n alone, and rounded once.
  *
  * e^d and e^q are binary32: infinite past log of its largest value, 88.72.  A token
  * of advantage 0 adds nothing of its ratio, however large, and with kl_coef 0 the

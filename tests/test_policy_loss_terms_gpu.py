@@ -55,3 +55,30 @@ def test_kl_that_is_only_watched(gpu):
     want = sum(math.expm1(v) - v for v in RATIOS[:3])
     # e^88 as a product with a rounded exponent: 88 u put back, a few roundings left
     assert abs(float(some.stats[1]) - want) <= 2 * 90 * ref.U * want
+
+
+def test_tokens_that_cancel(gpu):
+    """Terms that are exact in binary32 and whose sum is: the sums lose nothing of them, wherever the tokens stand."""
+    for n in (4, 5, 1027, 4099, 300001):
+        for at in {0, min(1, n - 4), max(0, n // 2 - 2), n - 4}:
+            adv = torch.zeros(n, device=gpu)
+            adv[at:at + 4] = vec([1e8, 1.0, -1e8, 0.0], gpu)
+            same = torch.zeros(n, device=gpu)
+            got = rog.rog_policy_loss(same, same, adv, weight=torch.ones(n, device=gpu))
+            assert got.stats.tolist() == [-1.0, 0.0, 0.0, 0.0], (n, at)
+            assert torch.equal(got.g_logp, -adv)
+
+
+def test_entropy_and_clip_sums_cancel_too(gpu):
+    """Weights of both signs: sum w entropy and sum w [clipped] of exact terms, exactly."""
+    w = vec([1e8, 1.0, -1e8, 0.5], gpu)
+    one, old = torch.ones(4, device=gpu), torch.zeros(4, device=gpu)
+    got = rog.rog_policy_loss(one, old, one, weight=w, entropy=one, clip_high=0.5)
+    assert got.stats[2:].tolist() == [1.5, 1.5]
+
+
+def test_large_weighted_terms_do_not_overflow_on_the_way(gpu):
+    adv = vec([3e38, 3e38, -3e38, -3e38, 2.0], gpu)
+    same = torch.zeros(5, device=gpu)
+    got = rog.rog_policy_loss(same, same, adv, weight=torch.ones(5, device=gpu))
+    assert got.stats[0].item() == -2.0
