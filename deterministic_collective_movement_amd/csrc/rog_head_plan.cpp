@@ -283,6 +283,9 @@ rog_status plan_policy(const rog_policy_in *in, size_t n, const rog_policy_param
         if (addr(q) % 4) return ROG_ERR_INVALID_ARGUMENT;
     const size_t need = policy_workspace(n);
     if (need && (!workspace || addr(workspace) % 16 || workspace_bytes < need)) return ROG_ERR_INVALID_ARGUMENT;
+    if (need)
+        for (const float *q : ins)
+            if (q && overlap(flat(workspace, need), flat(q, n * 4))) return ROG_ERR_OVERLAP;
     for (int i = 0; i < 3; ++i) {
         if (!outs[i]) continue;
         if (addr(outs[i]) % 4) return ROG_ERR_INVALID_ARGUMENT;

@@ -498,8 +498,8 @@ typedef struct {
  * of advantage 0 adds nothing of its ratio, however large, and with kl_coef 0 the
  * KL is in the stats alone.
  *
- * An output array may be exactly one of the input arrays; any other overlap is
- * ROG_ERR_OVERLAP.  n == 0: stats are zero.  n of 2^34 or more: TOO_LARGE.
+ * An output array may be exactly one of the input arrays; any other overlap, of the
+ * workspace with any array too, is ROG_ERR_OVERLAP.  n == 0: stats are zero.  n of 2^34 or more: TOO_LARGE.
  */
 ROG_API rog_status rog_policy_loss(const rog_policy_in *in, size_t n, const rog_policy_params *params,
                                    const rog_policy_out *out, void *workspace, size_t workspace_bytes,
