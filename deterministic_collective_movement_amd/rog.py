@@ -47,6 +47,7 @@ import importlib.util
 import os
 import struct
 import threading
+import warnings
 from typing import List, NamedTuple, Optional, Sequence
 
 import torch  # loads the process's HIP runtime before librog.so binds to it
@@ -187,13 +188,19 @@ _lib = _load()
 
 
 def _load_binding():
-    """The module that marshals ordinary calls (csrc/rog_binding.cpp)."""
+    """The module that marshals ordinary calls (csrc/rog_binding.cpp), or None: it
+    is built against one torch, and only saves a few microseconds of calls that
+    this file makes as well.  The kernels are librog.so's either way."""
     if not os.path.exists(BINDING_PATH):
-        raise ImportError("_rog_binding.so is not built (%s); run __graft_entry__.build() or "
-                          "python -m deterministic_collective_movement_amd.build" % BINDING_PATH)
-    spec = importlib.util.spec_from_file_location("_rog_binding", BINDING_PATH)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+        return None
+    try:
+        spec = importlib.util.spec_from_file_location("_rog_binding", BINDING_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except ImportError as e:
+        warnings.warn("_rog_binding.so does not load (%s): calls go through ctypes, a few microseconds slower; "
+                      "python -m deterministic_collective_movement_amd.build makes it anew" % e, RuntimeWarning)
+        return None
     return mod
 
 
@@ -654,14 +661,16 @@ def _own_workspace(nbytes: int, device: torch.device, stream, handle: int):
             # thread may be about to launch on this stream with one
             t = rog_workspace(max(nbytes, 1 << 20, 2 * got[1] if got else 0), device, stream)
             got = _workspaces[key] = (t.data_ptr(), t.numel(), t, got)
-            _binding.workspace(device.index, handle, t.data_ptr(), t.numel())
+            if _binding is not None:
+                _binding.workspace(device.index, handle, t.data_ptr(), t.numel())
     return got[:2]
 
 
 _is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 _raw_stream_of = _raw_stream or (lambda device: torch.cuda.current_stream(device).cuda_stream)
-_binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rog_logprob_ex, _lib.rog_logprob_grad, _lib.rog_policy_loss)),
-              _lib.rog_max_peers(), _current_device, _raw_stream_of, _is_capturing)
+if _binding is not None:
+    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rog_logprob_ex, _lib.rog_logprob_grad, _lib.rog_policy_loss)),
+                  _lib.rog_max_peers(), _current_device, _raw_stream_of, _is_capturing)
 
 
 def _capturing(stream, device: torch.device) -> bool:
@@ -796,7 +805,7 @@ def rog_logprob_ex(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor
     if out is not None and workspace is None and stream is None:
         if type(out) is not RogLogprob:
             out = RogLogprob(*out)
-        if _binding.logprob(shards, tokens, top_k, temperature, out, form):
+        if _binding is not None and _binding.logprob(shards, tokens, top_k, temperature, out, form):
             return out
     device, idx, rows, dtype, packed = _shard_bytes(shards)
     if not 0 <= top_k <= _MAX_TOP_K:
@@ -847,7 +856,8 @@ def rog_logprob_grad(shards: Sequence[torch.Tensor], tokens: torch.Tensor, lse: 
     """Gradient of sum_i (g_logp[i] logp[i] + g_entropy[i] entropy[i]) in every
     shard, from rog_logprob's ``lse`` and ``entropy``.  ``out``: W matrices to
     write; ``out[r]`` may be ``shards[r]`` (in place)."""
-    if out is not None and stream is None and _binding.grad(shards, tokens, lse, entropy, g_logp, g_entropy, temperature, out):
+    if out is not None and stream is None and _binding is not None and _binding.grad(shards, tokens, lse, entropy, g_logp, g_entropy,
+                                                                                     temperature, out):
         return out if isinstance(out, list) else list(out)
     device, idx, rows, dtype, packed = _shard_bytes(shards)
     if out is None:
@@ -892,7 +902,8 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
     if out is not None and workspace is None and stream is None:
         if type(out) is not RogPolicyLoss:
             out = RogPolicyLoss(*out)
-        if _binding.loss(logp, old_logp, advantage, weight, ref_logp, entropy, clip_low, clip_high, kl_coef, entropy_coef, grad_scale, out):
+        if _binding is not None and _binding.loss(logp, old_logp, advantage, weight, ref_logp, entropy, clip_low, clip_high, kl_coef,
+                                                  entropy_coef, grad_scale, out):
             return out
     if not isinstance(logp, torch.Tensor):
         raise TypeError("logp must be a torch.Tensor")
