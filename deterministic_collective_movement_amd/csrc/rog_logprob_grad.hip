@@ -32,14 +32,14 @@ constexpr float kExtreme = 744261248.0f;
 constexpr float kLarge = 64.0f;
 
 // One wave, a workgroup of its own, per piece of a row, its stores streamed.
-// Bound by HBM: 4096 x 131072 bf16 over eight shards (2.15 GB) take 325-331 us =
+// Bound by HBM: 4096 x 131072 bf16 over eight shards (2.15 GB) take 327-332 us =
 // 6.5-6.6 TB/s with pieces of 2 KB, against 358 with four waves of 4 KB each, 372
 // with 1 KB, and 365 and more where waves took several pieces in turn; read once
 // and written once (counted: 1.0 times the bytes).  Pieces begin with lines of the
 // gradient, whatever the row's alignment: 4000 x 100003 bf16 278 us, against 321
 // with pieces counted from the row's beginning, whose ends share lines.
 // 1021 x 50257 binary16, whose logits a forward pass left in the Infinity Cache,
-// 29-30 us (192 MB); 33 x 32003 binary32 3.6 us, a launch and one round trip.
+// 31-31.5 us (192 MB); 33 x 32003 binary32 3.6 us, a launch and one round trip.
 template <int DT, bool NT>
 __global__ __launch_bounds__(64) void rog_logprob_grad_kernel(LogprobGradArgs) {
     const LogprobGradArgs &a = launch_args<LogprobGradArgs>();

@@ -9,11 +9,12 @@
 // to finish joins the workgroups' totals in their order.
 //
 // Bandwidth bound: 24 bytes read and 8 written per token with every term, about
-// 83 vector instructions.  4194307 tokens (134 MB) take 31 us = 4.3 TB/s:
-// some 3 us to start, 3.5 us for the join (131072 tokens take 6.6 us, 1021, one
-// workgroup, 3.0), the rest at 5.6 TB/s over eight arrays.  Twice or eight times
-// as many workgroups, two tiles in flight, streamed loads, arrival counted over
-// 16 to 128 counters: all within 5 % of it.
+// 93 vector instructions.  4194307 tokens (134 MB) take 31.5 us = 4.3 TB/s:
+// some 3 us to start, 3.5 us for the join (131072 tokens take 6.8 us, 1021, one
+// workgroup, 3.1), the rest over eight arrays.  The 4097 tiles are 456 runs of
+// nine, so some CUs get 18 tiles and the mean is 16.  Two tiles in flight,
+// streamed loads, arrival counted over 16 to 128 counters and 768 to 4096
+// workgroups, whose runs come out as uneven, were all within 5 % of it.
 #include <hip/hip_runtime.h>
 
 #include "rog_head_device.h"

@@ -846,7 +846,10 @@ def rog_logprob(shards: Sequence[torch.Tensor], tokens: Optional[torch.Tensor] =
 
     ``shards``: W matrices [rows, width_r] of one dtype (float32, bfloat16 or
     float16), contiguous within rows, any row stride.  ``out``: a RogLogprob (or
-    five tensors) to write, None for what is not wanted."""
+    five tensors) to write, None for what is not wanted.
+
+    The outputs have no gradient function, whatever the logits require:
+    ``rog_logprob_grad`` gives the logits' gradients."""
     return rog_logprob_ex(shards, tokens, top_k, temperature, out, workspace, stream)
 
 
@@ -854,8 +857,9 @@ def rog_logprob_grad(shards: Sequence[torch.Tensor], tokens: torch.Tensor, lse: 
                      g_logp: torch.Tensor, g_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
                      out: Optional[Sequence[torch.Tensor]] = None, stream=None) -> List[torch.Tensor]:
     """Gradient of sum_i (g_logp[i] logp[i] + g_entropy[i] entropy[i]) in every
-    shard, from rog_logprob's ``lse`` and ``entropy``.  ``out``: W matrices to
-    write; ``out[r]`` may be ``shards[r]`` (in place)."""
+    shard, from rog_logprob's ``lse`` and ``entropy`` of the same logits, widths
+    and temperature.  ``out``: W matrices to write; ``out[r]`` may be
+    ``shards[r]`` (in place)."""
     if out is not None and stream is None and _binding is not None and _binding.grad(shards, tokens, lse, entropy, g_logp, g_entropy,
                                                                                      temperature, out):
         return out if isinstance(out, list) else list(out)
@@ -898,7 +902,8 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
                     workspace: Optional[torch.Tensor] = None, stream=None) -> RogPolicyLoss:
     """The clipped policy loss over n tokens (float32 vectors) with its gradients
     in ``logp`` and ``entropy``.  ``weight[i]`` is the token's weight in the sums
-    (0: the token counts for nothing; None: 1 / n each)."""
+    (0: the token counts for nothing; None: 1 / n each).  The outputs have no
+    gradient function: ``g_logp`` and ``g_entropy`` go to ``rog_logprob_grad``."""
     if out is not None and workspace is None and stream is None:
         if type(out) is not RogPolicyLoss:
             out = RogPolicyLoss(*out)
