@@ -1,7 +1,8 @@
 """Build librog.so (the C-ABI library) in-tree for gfx950.
 
 ``build_library()`` compiles the host planners and the HIP kernels (gathers,
-rank-ordered sums, token log probabilities and the policy loss) with hipcc for
+rank-ordered sums, token log probabilities, the policy loss and the policy
+head's products) with hipcc for
 gfx950, then links ``deterministic_collective_movement_amd/librog.so``.
 Intermediate objects go to ``_build/`` at the repository root.
 ``python -m deterministic_collective_movement_amd.build`` does the same.
@@ -23,8 +24,9 @@ LIB_PATH = os.path.join(PKG, "librog.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
-HOST_SOURCES = ["rog_plan.cpp", "rog_head_plan.cpp"]
-HIP_SOURCES = ["rog_kernels.hip", "rog_reduce.hip", "rog_logprob.hip", "rog_logprob_grad.hip", "rog_policy.hip"]
+HOST_SOURCES = ["rog_plan.cpp", "rog_head_plan.cpp", "rog_linear_plan.cpp"]
+HIP_SOURCES = ["rog_kernels.hip", "rog_reduce.hip", "rog_logprob.hip", "rog_logprob_grad.hip", "rog_policy.hip",
+               "rog_linear_score.hip", "rog_linear_grad.hip", "rog_linear_i8.hip"]
 
 # Device code: gfx950 only; packed-FP32 instructions disabled.
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Werror",
@@ -59,7 +61,7 @@ def build_library(out: str = LIB_PATH, defines=(), build_dir: str = BUILD_DIR) -
         flags = HOST_FLAGS if src in HOST_SOURCES else HIP_FLAGS
         objs.append(obj)
         jobs.append([hipcc] + flags + dflags + inc + ["-c", os.path.join(CSRC, src), "-o", obj])
-    with ThreadPoolExecutor(max_workers=4) as pool:
+    with ThreadPoolExecutor(max_workers=8) as pool:
         list(pool.map(_run, jobs))
     tmp = out + ".tmp%d" % os.getpid()
     _run([hipcc, "-shared", "-fPIC", "--offload-arch=" + ARCH] + objs +

@@ -1,0 +1,218 @@
+// rog_linear.h -- kernel arguments and launch plans of the policy head's
+// products (token log probabilities from hidden states, their gradient, the
+// product of 8-bit integers), shared by the host planner (rog_linear_plan.cpp)
+// and the HIP kernels.  Internal to librog.so; the public interface is
+// include/rog.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "rog_head.h"
+
+namespace rog {
+
+// How a product is cut.  A slab is 128 bytes of K (64 elements of two bytes, 128
+// of one): a matrix instruction takes half a slab of 16 rows.  A leaf is 32
+// consecutive columns of one shard, a block four leaves.  Every logit is one
+// chain of matrix instructions over the slabs in rising order, whatever the
+// tile, so its bits do not depend on how many rows a call has; the statistics
+// of a row are joined leaf by leaf over one tree (rog_linear_device.h).
+constexpr uint32_t kSlabBytes = 128;
+constexpr uint32_t kLeaf = 32;
+constexpr uint32_t kLinearBlock = 128;
+constexpr uint64_t kMaxLinearStride = uint64_t(1) << 22;   // bytes from a row to the next: tiles are addressed in 32 bits
+constexpr uint32_t kMaxDim = 1u << 17;
+
+// A head's weight shards, cut into tiles of `tile` columns (the launch's).
+struct WeightShard {
+    const void *w;                     // element (0, 0)
+    int64_t stride;                    // bytes from a column's weights to the next column's
+    uint32_t width;                    // columns
+    uint32_t col0;                     // the shard's first column in the row
+};
+struct WeightShards {
+    uint32_t W;
+    uint32_t vocab;
+    WeightShard s[kMaxPeers];
+    uint32_t tile0[kMaxPeers + 1];     // the shard's first tile; [W]: all tiles
+    uint32_t block0[kMaxPeers + 1];    // the shard's first block of 128 columns
+};
+
+// The states of a call: rows of `dim` elements.
+struct LinearRows {
+    const void *x;
+    int64_t stride;                    // bytes
+    const uint32_t *count;             // device: how many rows there are (NULL: `rows`)
+    uint32_t rows;
+    uint32_t kbytes;                   // bytes of a row
+};
+
+struct ScoreArgs {
+    LinearRows a;
+    const int64_t *tokens;             // of row i (NULL: none)
+    const uint32_t *index;             // packed rows: the caller's row (NULL: row i itself)
+    float scale;                       // log2(e) / temperature
+    float *target;                     // [rows] scaled logit of the row's token
+    float *states;                     // [units][rows_pad][4]: m, s, t
+    uint32_t rows_pad;
+    uint32_t unit_leaves;              // leaves of a unit: 1, 2 or 4
+    WeightShards sh;
+};
+
+// Joins the units of every row.
+struct JoinArgs {
+    const int64_t *tokens;
+    const uint32_t *index, *count;
+    const float *target, *states;
+    float *logp, *entropy, *lse;
+    uint32_t rows, rows_pad;
+    uint32_t vocab, blocks;
+    uint32_t unit_leaves;
+    float scale;
+};
+
+// Packs the rows that are scored, one after the other, K padded with zeros to whole slabs.
+struct PackArgs {
+    const void *x;
+    int64_t stride;
+    const int64_t *tokens;
+    uint32_t rows, kbytes;             // bytes of a caller's row
+    uint32_t packed_bytes;             // of a packed one, a multiple of a slab
+    uint32_t *index, *count;
+    void *packed;
+    float *logp, *entropy, *lse;       // zeroed where the row is not scored
+    void *zero;                        // rows of kbytes, likewise
+    int64_t zero_stride;
+    const float *g_logp, *g_entropy;   // binary16: the largest of them sets the scale
+    float *g_scale;
+    float inv_t;
+};
+
+struct GradArgs {
+    LinearRows a;                      // packed
+    const int64_t *tokens;
+    const uint32_t *index;
+    const float *lse, *entropy, *g_logp, *g_entropy, *g_scale;
+    float inv_t;
+    void *g;                           // [rows][g_stride / 2] coefficients of the piece's columns
+    int64_t g_stride;                  // bytes
+    uint32_t tile_begin;               // the piece's first tile
+    uint32_t tiles;                    // and how many it has
+    WeightShards sh;
+};
+
+// One launch of the gradient's products for a piece.
+struct BackArgs {
+    LinearRows a;                      // packed
+    const uint32_t *index;
+    const float *g_scale;
+    const void *g;
+    int64_t g_stride;
+    uint32_t tile_begin, tiles;
+    uint32_t seg_begin, segs;          // segments of the piece
+    uint32_t row_tiles, dim_tiles;     // upper bounds of the grid
+    float *part;                       // partial sums of d_hidden: [segs][rows][dim_pad], or one running sum
+    uint64_t part_seg;                 // floats from a segment's to the next (0: running)
+    uint32_t dim_pad;
+    uint32_t first, last;              // the running sum's first and last piece
+    void *d_hidden;
+    int64_t d_stride;
+    uint32_t dim;
+    WeightShards sh;
+    uint32_t seg0[kMaxPeers + 1];      // a shard's first segment
+    uint32_t seg_tiles;                // tiles of a segment
+    void *dw[kMaxPeers];
+    int64_t dw_stride[kMaxPeers];      // bytes
+};
+
+struct BackJoinArgs {
+    const float *part;
+    uint64_t part_seg;
+    uint32_t segs, dim_pad, dim;
+    const uint32_t *index, *count;
+    const float *g_scale;
+    uint32_t rows;
+    void *d_hidden;
+    int64_t d_stride;
+};
+
+struct QuantizeArgs {
+    const void *x;
+    int64_t stride;                    // bytes
+    int8_t *q;
+    int64_t q_stride;
+    float *scale;
+    uint32_t rows, dim;
+};
+
+struct LinearI8Args {
+    LinearRows a;
+    const float *row_scale;
+    WeightShards sh;
+    const float *scale[kMaxPeers];
+    void *out[kMaxPeers];
+    int64_t out_stride[kMaxPeers];     // bytes
+};
+
+// Tiles of a product: columns x rows.
+enum LinearForm {
+    kTileFew = 0,      // 128 x 64
+    kTileMid = 1,      // 128 x 128
+    kTileWide = 2,     // 256 x 256
+};
+
+struct ScorePlan {
+    int32_t form;
+    uint32_t grid;
+    bool direct, packs;
+    PackArgs pack;
+    ScoreArgs args;
+    JoinArgs join;
+    uint64_t workspace_bytes;
+};
+
+// Columns of a tile of the gradient's pieces.
+constexpr uint32_t kGradTile = 256;
+
+struct GradPlan {
+    rog_dtype dtype;
+    bool direct, wide, running;
+    uint32_t pieces, piece_tiles;      // tiles of a piece: whole segments' or all
+    PackArgs pack;
+    GradArgs coef;
+    BackArgs back;
+    BackJoinArgs join;
+    uint32_t join_grid;
+    uint64_t workspace_bytes;
+};
+
+struct LinearI8Plan {
+    int32_t form;
+    uint32_t grid;
+    bool direct;
+    LinearI8Args args;
+};
+
+// Validate and plan (no HIP calls); without `addresses` only what the shapes decide.
+rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim, const rog_weight_shard *shards, int W,
+                               rog_dtype dtype, float temperature, const int64_t *tokens, const rog_logprob_out *out, void *workspace,
+                               size_t workspace_bytes, bool addresses, bool has_tokens, ScorePlan *p);
+rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim, const rog_weight_shard *shards, int W,
+                            rog_dtype dtype, float temperature, const int64_t *tokens, const float *lse, const float *entropy,
+                            const float *g_logp, const float *g_entropy, void *d_hidden, int64_t d_hidden_stride,
+                            const rog_grad_shard *d_weights, void *workspace, size_t workspace_bytes, bool addresses, GradPlan *p);
+// Sets coef and back to piece i, and their grids.
+void lay_piece(GradPlan *p, uint32_t i, uint32_t *coef_grid, uint32_t *back_grid);
+rog_status plan_quantize(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q, int64_t q_stride,
+                         float *scale, QuantizeArgs *a);
+rog_status plan_linear_i8(const int8_t *q, int64_t q_stride, const float *scale, size_t rows, int64_t dim, const rog_i8_shard *shards, int W,
+                          rog_dtype out_dtype, const rog_grad_shard *out, LinearI8Plan *p);
+
+hipError_t launch_pack(const PackArgs &a, hipStream_t s);
+hipError_t launch_coefficients(const GradPlan &p, const GradArgs &a, uint32_t grid, hipStream_t s);
+
+static_assert(sizeof(BackArgs) <= 4096 && sizeof(LinearI8Args) <= 4096, "kernel arguments stay below 4 KiB");
+
+}  // namespace rog

@@ -1,0 +1,226 @@
+// rog_linear_grad.hip -- HIP kernels of the gradient of token log probabilities
+// in hidden states and head weights for gfx950 (CDNA4), and the C entry point
+// that launches them.
+//
+// With the coefficients G_ij = (g_i (1[j = t_i] - p_ij) - e_i p_ij (log p_ij + H_i)) / T
+// (rog_linear_score.hip makes them anew from the states and weights, a piece of
+// the vocabulary at a time, rounded to the weights' type as the matrix units take
+// them):
+//     dw_j = sum_i G_ij h_i          dh_i = sum_j G_ij w_j
+// One launch takes both products of a piece; they share nothing but G.
+#include <hip/hip_runtime.h>
+
+#include "rog_linear_device.h"
+
+namespace rog {
+namespace {
+
+#pragma clang fp contract(off)
+
+typedef __attribute__((address_space(1))) vec16 gvec16_out;
+typedef __attribute__((address_space(1))) f32x4 gf32x4_out;
+typedef __attribute__((address_space(1))) uint16_t gu16_out;
+
+// Eight outputs, rounded once, to `to` (the first `n` of them).
+template <int DT>
+__device__ __forceinline__ void put8(uint8_t *to, const float (&x)[8], uint32_t n, bool wide) {
+    vec16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(x + 2 * i);
+    if (wide && n >= 8) {
+        *(gvec16_out *)to = v;
+        return;
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+        if (i < n) ((gu16_out *)to)[i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
+}
+
+constexpr int kBM = 256;   // elements of the states and weights of a tile
+
+template <int DT, int BN, int WM, int WN, bool DIRECT>
+__device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint32_t rows, uint8_t *a0, uint8_t *a1, uint8_t *b0, uint8_t *b1) {
+    constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
+    typedef ColSlab<true, kBM, THREADS, DIRECT> A;
+    typedef RowSlab<false, BN, THREADS, true, 2> B;
+    const uint32_t tn = (rows + BN - 1) / BN, each = p.dim_tiles * tn;
+    const bool running = p.part_seg == 0;              // one workgroup takes all segments of the piece, in their order
+    const uint32_t in = id % each, d0 = in % p.dim_tiles * kBM, n0 = in / p.dim_tiles * BN;
+    const uint32_t begin = running ? 0 : id / each, end = running ? p.segs : begin + 1;
+    const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    const float inv = p.g_scale ? 1.0f / *p.g_scale : 1.0f;
+    const bool wide = ((uintptr_t(p.d_hidden) | uint64_t(p.d_stride)) & 15) == 0;
+    for (uint32_t s = begin; s < end; ++s) {
+        const uint32_t seg = p.seg_begin + s;
+        uint32_t r = 0;
+        while (seg >= p.seg0[r + 1]) ++r;
+        const WeightShard sh = p.sh.s[r];
+        const uint32_t tile = (seg - p.seg0[r]) * p.seg_tiles, v0 = tile * kGradTile;
+        const uint32_t cols = sh.width - v0 < p.seg_tiles * kGradTile ? sh.width - v0 : p.seg_tiles * kGradTile;
+        const uint64_t g_col = uint64_t(p.sh.tile0[r] + tile - p.tile_begin) * kGradTile * 2;
+        const A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride) + d0 * 2, sh.stride, cols, p.dim - d0);
+        const B b(static_cast<const uint8_t *>(p.g) + uint64_t(n0) * uint64_t(p.g_stride) + g_col, p.g_stride, rows - n0,
+                  p.seg_tiles * kGradTile * 2);
+        f32x4 acc[FM][FN] = {};
+        if (s != begin) __syncthreads();               // the last slab's readers
+        tile_product<DT, FM, FN>(a, b, (cols + 63) / 64, m0, w0, a0, a1, b0, b1, acc);
+
+        const bool first = running && p.first && s == 0, last = running && p.last && s + 1 == p.segs;
+        float *part = p.part + uint64_t(s) * p.part_seg;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t n = n0 + w0 + 16 * j + l % 16;
+            if (n >= rows) continue;
+            uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(p.index[n]) * uint64_t(p.d_stride);
+#pragma unroll
+            for (int f = 0; f < FM / 2; ++f) {
+                const uint32_t d = d0 + m0 + 32 * f + l / 16 * 8;
+                if (d >= p.dim) continue;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4];
+                gf32x4_out *at = (gf32x4_out *)(part + uint64_t(n) * p.dim_pad + d);
+                if (running && !first) {
+                    const f32x4 lo = at[0], hi = at[1];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = (i < 4 ? lo[i % 4] : hi[i % 4]) + x[i];
+                }
+                if (last) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] *= inv;
+                    put8<DT>(out + d * 2, x, p.dim - d, wide);
+                } else {
+                    at[0] = f32x4{x[0], x[1], x[2], x[3]};
+                    at[1] = f32x4{x[4], x[5], x[6], x[7]};
+                }
+            }
+        }
+    }
+}
+
+template <int DT, int BN, int WM, int WN>
+__device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uint32_t rows, uint8_t *a0, uint8_t *a1, uint8_t *b0, uint8_t *b1) {
+    constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
+    typedef ColSlab<true, kBM, THREADS, true> A;
+    typedef ColSlab<false, BN, THREADS, true> B;
+    const TileAt at = tile_at(id, p.dim_tiles, p.tiles * (256 / BN));
+    const uint32_t tile = p.tile_begin + at.n / (256 / BN), d0 = at.m * kBM;
+    const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * 256 + at.n % (256 / BN) * BN;
+    const uint32_t width = p.sh.s[r].width;
+    if (v0 >= width) return;
+    const A a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
+    const B b(static_cast<const uint8_t *>(p.g) + uint64_t(at.n) * BN * 2, p.g_stride, rows, BN);
+    const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    f32x4 acc[FM][FN] = {};
+    tile_product<DT, FM, FN>(a, b, (rows + 63) / 64, m0, w0, a0, a1, b0, b1, acc);
+
+    const float inv = p.g_scale ? 1.0f / *p.g_scale : 1.0f;
+    const bool wide = ((uintptr_t(p.dw[r]) | uint64_t(p.dw_stride[r])) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const uint32_t v = v0 + w0 + 16 * j + l % 16;
+        if (v >= width) continue;
+        uint8_t *out = static_cast<uint8_t *>(p.dw[r]) + uint64_t(v) * uint64_t(p.dw_stride[r]);
+#pragma unroll
+        for (int f = 0; f < FM / 2; ++f) {
+            const uint32_t d = d0 + m0 + 32 * f + l / 16 * 8;
+            if (d >= p.dim) continue;
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4] * inv;
+            put8<DT>(out + d * 2, x, p.dim - d, wide);
+        }
+    }
+}
+
+// The states' tiles first: their chains are the longer ones of all but large batches.
+template <int DT, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
+    constexpr int BV = BN < 128 ? 128 : BN;
+    __shared__ __attribute__((aligned(16))) uint8_t a0[kBM * kSlabBytes], a1[kBM * kSlabBytes], b0[BV * kSlabBytes], b1[BV * kSlabBytes];
+    const uint32_t rows = *p.a.count, states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
+    if (blockIdx.x < states) {
+        back_states<DT, BN, WM, WN, DIRECT>(p, blockIdx.x, rows, a0, a1, b0, b1);
+        return;
+    }
+    const uint32_t id = blockIdx.x - states;
+    if (id < p.dim_tiles * p.tiles * (256 / BV)) back_weights<DT, BV, WM, WN>(p, id, rows, a0, a1, b0, b1);
+}
+
+// Adds the segments' partial sums of a row in their order.
+template <int DT>
+__global__ __launch_bounds__(256) void rog_linear_back_join_kernel(BackJoinArgs p) {
+    const uint32_t rows = *p.count, vecs = p.dim_pad / 8;
+    const uint64_t id = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t n = uint32_t(id / vecs), d = uint32_t(id % vecs) * 8;
+    if (n >= rows || d >= p.dim) return;
+    const float *part = p.part + uint64_t(n) * p.dim_pad + d;
+    typedef const __attribute__((address_space(1))) f32x4 gf32x4;
+    float x[8];
+    for (uint32_t s = 0; s < p.segs; ++s) {
+        const f32x4 lo = ((gf32x4 *)(part + s * p.part_seg))[0], hi = ((gf32x4 *)(part + s * p.part_seg))[1];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = i < 4 ? lo[i % 4] : hi[i % 4];
+            x[i] = s ? x[i] + v : v;
+        }
+    }
+    const float inv = p.g_scale ? 1.0f / *p.g_scale : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= inv;
+    uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(p.index[n]) * uint64_t(p.d_stride);
+    put8<DT>(out + d * 2, x, p.dim - d, ((uintptr_t(p.d_hidden) | uint64_t(p.d_stride)) & 15) == 0);
+}
+
+template <class Args>
+hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
+    void *list[] = {const_cast<Args *>(&args)};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
+}
+
+template <int DT>
+hipError_t launch_back(const GradPlan &p, const BackArgs &a, uint32_t grid, hipStream_t s) {
+    if (p.wide)
+        return p.direct ? launch(rog_linear_back_kernel<DT, 256, 2, 4, true>, grid, 512, a, s)
+                        : launch(rog_linear_back_kernel<DT, 256, 2, 4, false>, grid, 512, a, s);
+    return p.direct ? launch(rog_linear_back_kernel<DT, 64, 4, 1, true>, grid, 256, a, s)
+                    : launch(rog_linear_back_kernel<DT, 64, 4, 1, false>, grid, 256, a, s);
+}
+
+}  // namespace
+}  // namespace rog
+
+extern "C" {
+
+ROG_API rog_status rog_linear_logprob_grad(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim,
+                                           const rog_weight_shard *shards, int W, rog_dtype dtype, float temperature,
+                                           const int64_t *tokens, const float *lse, const float *entropy, const float *g_logp,
+                                           const float *g_entropy, void *d_hidden, int64_t d_hidden_stride,
+                                           const rog_grad_shard *d_weights, void *workspace, size_t workspace_bytes,
+                                           hipStream_t stream) {
+    using namespace rog;
+    GradPlan p;
+    const rog_status st = plan_linear_grad(hidden, hidden_stride, rows, dim, shards, W, dtype, temperature, tokens, lse, entropy, g_logp,
+                                           g_entropy, d_hidden, d_hidden_stride, d_weights, workspace, workspace_bytes, true, &p);
+    if (st != ROG_OK || rows == 0) return st;
+    hipError_t e = launch_pack(p.pack, stream);
+    for (uint32_t i = 0; i < p.pieces && e == hipSuccess; ++i) {
+        uint32_t coef_grid = 0, back_grid = 0;
+        lay_piece(&p, i, &coef_grid, &back_grid);
+        e = launch_coefficients(p, p.coef, coef_grid, stream);
+        if (e == hipSuccess) e = dtype == ROG_DTYPE_BF16 ? launch_back<ROG_DTYPE_BF16>(p, p.back, back_grid, stream)
+                                                         : launch_back<ROG_DTYPE_F16>(p, p.back, back_grid, stream);
+    }
+    if (e == hipSuccess && p.join_grid)
+        e = dtype == ROG_DTYPE_BF16 ? launch(rog_linear_back_join_kernel<ROG_DTYPE_BF16>, p.join_grid, 256, p.join, stream)
+                                    : launch(rog_linear_back_join_kernel<ROG_DTYPE_F16>, p.join_grid, 256, p.join, stream);
+    if (e != hipSuccess) {
+        g_last_hip_error = int(e);
+        return ROG_ERR_LAUNCH;
+    }
+    return ROG_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,169 @@
+// rog_linear_i8.hip -- HIP kernels of the product of 8-bit integers with a scale
+// for each token and channel for gfx950 (CDNA4), of the quantization of rows, and
+// the C entry points that launch them.
+//
+//     s_i = max(max_k |x_ik| / 127, 2^-126), q_ik = x_ik / s_i to the nearest integer
+//     y_ij = (sum_k q_ik u_jk) s_i r_j
+// The sum is exact in 32-bit integers, so y has three roundings of binary32 and
+// one to the output's type whatever the order.
+#include <hip/hip_runtime.h>
+
+#include "rog_linear_device.h"
+
+namespace rog {
+namespace {
+
+#pragma clang fp contract(off)
+
+// A row per workgroup: the largest magnitude, then the quotients; a row is read twice, the second time from the caches.
+constexpr uint32_t kQuantThreads = 256;
+template <int DT>
+__global__ __launch_bounds__(kQuantThreads) void rog_quantize_kernel(QuantizeArgs p) {
+    constexpr uint32_t ES = Logit<DT>::kSize;
+    __shared__ float most[kQuantThreads / 64];
+    gbyte *row = (gbyte *)p.x + uint64_t(blockIdx.x) * uint64_t(p.stride);
+    const uint32_t t = threadIdx.x;
+    float m = 0;
+    for (uint32_t i = t; i < p.dim; i += kQuantThreads) m = max_nan(m, fabsf(load_logit<DT>(row + i * ES)));
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = max_nan(m, __shfl_xor(m, d));
+    if (t % 64 == 0) most[t / 64] = m;
+    __syncthreads();
+    m = max_nan(max_nan(most[0], most[1]), max_nan(most[2], most[3]));
+    const float s = m < kInf ? fmaxf(m / 127.0f, 0x1p-126f) : __builtin_nanf("");
+    if (t == 0) p.scale[blockIdx.x] = s;
+    int8_t *q = p.q + uint64_t(blockIdx.x) * uint64_t(p.q_stride);
+    for (uint32_t i = t; i < p.dim; i += kQuantThreads) {
+        const float v = load_logit<DT>(row + i * ES) / s;
+        q[i] = v == v ? int8_t(int(__builtin_rintf(v))) : int8_t(0);
+    }
+}
+
+template <int OT>
+__device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32_t n, bool wide) {
+    typedef __attribute__((address_space(1))) vec16 gvec16_out;
+    typedef __attribute__((address_space(1))) uint16_t gu16_out;
+    typedef __attribute__((address_space(1))) float gf_out;
+    if constexpr (OT == ROG_DTYPE_F32) {
+        if (wide && n >= 8) {
+            vec16 v[2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = f32_bits(x[i]);
+            ((gvec16_out *)to)[0] = v[0];
+            ((gvec16_out *)to)[1] = v[1];
+            return;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i)
+            if (i < n) ((gf_out *)to)[i] = x[i];
+    } else {
+        vec16 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = narrow_word<OT>(x + 2 * i);
+        if (wide && n >= 8) {
+            *(gvec16_out *)to = v;
+            return;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i)
+            if (i < n) ((gu16_out *)to)[i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
+    }
+}
+
+template <int OT, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void rog_linear_i8_kernel(LinearI8Args p) {
+    constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+    typedef RowSlab<true, BM, THREADS, DIRECT, 1> A;
+    typedef RowSlab<false, BN, THREADS, DIRECT, 1> B;
+    __shared__ __attribute__((aligned(16))) uint8_t a0[A::kBytes], a1[A::kBytes], b0[B::kBytes], b1[B::kBytes];
+    const uint32_t rows = p.a.rows, tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
+    const TileAt at = tile_at(blockIdx.x, tm, tn);
+    const uint32_t r = shard_of_tile(p.sh, at.m), v0 = (at.m - p.sh.tile0[r]) * BM, n0 = at.n * BN;
+    const WeightShard sh = p.sh.s[r];
+    const A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    const B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
+    const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    i32x4 acc[FM][FN] = {};
+    tile_product<kTypeI8, FM, FN>(a, b, (p.a.kbytes + kSlabBytes - 1) / kSlabBytes, m0, w0, a0, a1, b0, b1, acc);
+
+    constexpr uint32_t OS = Logit<OT>::kSize;
+    const bool wide = ((uintptr_t(p.out[r]) | uint64_t(p.out_stride[r])) & 15) == 0;
+#pragma unroll
+    for (int f = 0; f < FM / 2; ++f) {
+        const uint32_t v = v0 + m0 + 32 * f + l / 16 * 8;
+        if (v >= sh.width) continue;
+        const uint32_t left = sh.width - v;
+        float scale[8];
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) scale[i] = i < left ? p.scale[r][v + i] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t n = n0 + w0 + 16 * j + l % 16;
+            if (n >= rows) continue;
+            const float s = p.row_scale[n];
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = float(acc[2 * f + i / 4][j][i % 4]) * s * scale[i];
+            put_out<OT>(static_cast<uint8_t *>(p.out[r]) + uint64_t(n) * uint64_t(p.out_stride[r]) + uint64_t(v) * OS, x, left, wide);
+        }
+    }
+}
+
+template <class Args>
+hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
+    void *list[] = {const_cast<Args *>(&args)};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
+}
+
+template <int OT, bool DIRECT>
+hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
+    switch (p.form) {
+    case kTileWide: return launch(rog_linear_i8_kernel<OT, 256, 256, 2, 4, DIRECT>, p.grid, 512, p.args, s);
+    case kTileMid: return launch(rog_linear_i8_kernel<OT, 128, 128, 2, 2, DIRECT>, p.grid, 256, p.args, s);
+    default: return launch(rog_linear_i8_kernel<OT, 128, 64, 4, 1, DIRECT>, p.grid, 256, p.args, s);
+    }
+}
+template <int OT>
+hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
+    return p.direct ? launch_i8<OT, true>(p, s) : launch_i8<OT, false>(p, s);
+}
+
+rog_status launched(hipError_t e) {
+    if (e == hipSuccess) return ROG_OK;
+    g_last_hip_error = int(e);
+    return ROG_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace rog
+
+extern "C" {
+
+ROG_API rog_status rog_quantize_i8(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q,
+                                   int64_t q_stride, float *scale, hipStream_t stream) {
+    using namespace rog;
+    QuantizeArgs a;
+    const rog_status st = plan_quantize(x, row_stride, rows, dim, dtype, q, q_stride, scale, &a);
+    if (st != ROG_OK || rows == 0) return st;
+    switch (dtype) {
+    case ROG_DTYPE_BF16: return launched(launch(rog_quantize_kernel<ROG_DTYPE_BF16>, a.rows, kQuantThreads, a, stream));
+    case ROG_DTYPE_F16: return launched(launch(rog_quantize_kernel<ROG_DTYPE_F16>, a.rows, kQuantThreads, a, stream));
+    default: return launched(launch(rog_quantize_kernel<ROG_DTYPE_F32>, a.rows, kQuantThreads, a, stream));
+    }
+}
+
+ROG_API rog_status rog_linear_i8(const int8_t *q, int64_t q_stride, const float *scale, size_t rows, int64_t dim,
+                                 const rog_i8_shard *shards, int W, rog_dtype out_dtype, const rog_grad_shard *out, hipStream_t stream) {
+    using namespace rog;
+    LinearI8Plan p;
+    const rog_status st = plan_linear_i8(q, q_stride, scale, rows, dim, shards, W, out_dtype, out, &p);
+    if (st != ROG_OK || p.grid == 0) return st;
+    switch (out_dtype) {
+    case ROG_DTYPE_BF16: return launched(launch_i8<ROG_DTYPE_BF16>(p, stream));
+    case ROG_DTYPE_F16: return launched(launch_i8<ROG_DTYPE_F16>(p, stream));
+    default: return launched(launch_i8<ROG_DTYPE_F32>(p, stream));
+    }
+}
+
+}  // extern "C"

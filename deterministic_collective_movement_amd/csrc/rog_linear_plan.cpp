@@ -1,0 +1,435 @@
+// rog_linear_plan.cpp -- argument validation, tiles and workspaces of the policy
+// head's products.  Pure host code: no HIP calls, so every decision here can be
+// checked on a machine without a GPU.
+#include <math.h>
+
+#include <algorithm>
+
+#include "rog_head_checks.h"
+#include "rog_linear.h"
+
+namespace rog {
+namespace {
+
+constexpr uint64_t kMaxGroups = uint64_t(1) << 22;   // workgroups of a launch (of 512 threads, below 2^32 work-items)
+constexpr float kMinTemperature = 1.0f / 1024, kMaxTemperature = 1024.0f;
+constexpr double kLog2E = 1.4426950408889634;
+
+// Tunables, measured on MI355X; a variant build may override one with -D.
+// Bytes of the coefficients' piece of the vocabulary (one segment at least).
+#ifndef ROG_LINEAR_PIECE_BYTES
+#define ROG_LINEAR_PIECE_BYTES (256ull << 20)
+#endif
+
+inline bool product_type(rog_dtype t) { return t == ROG_DTYPE_BF16 || t == ROG_DTYPE_F16; }
+inline uint64_t up(uint64_t v, uint64_t unit) { return ceil_div(v, unit) * unit; }
+
+// A matrix of `rows` rows of `width` elements: address, stride and extent.
+rog_status check_matrix(const void *p, int64_t stride, uint64_t rows, uint64_t width, uint32_t es, bool spread) {
+    if (stride < 0) return ROG_ERR_INVALID_ARGUMENT;
+    if (rows && width && (!p || addr(p) % es)) return ROG_ERR_INVALID_ARGUMENT;
+    if (spread && rows > 1 && uint64_t(stride) < width) return ROG_ERR_INVALID_ARGUMENT;
+    if (uint64_t(stride) * es >= kMaxLinearStride) return ROG_ERR_TOO_LARGE;
+    return fits(addr(p), rows, uint64_t(stride) * es, width * es) ? ROG_OK : ROG_ERR_TOO_LARGE;
+}
+
+// Loads of 16 bytes go straight to the shared memory where rows begin and end with them.
+bool aligned(const void *p, uint64_t stride_bytes, uint64_t row_bytes) { return (addr(p) | stride_bytes | row_bytes) % 16 == 0; }
+
+template <class Shard>
+rog_status lay_weights(const Shard *shards, int W, int64_t dim, uint32_t es, bool addresses, WeightShards *h, bool *direct) {
+    if (!shards || W < 1 || W > kMaxPeers || dim < 1) return ROG_ERR_INVALID_ARGUMENT;
+    if (uint64_t(dim) >= kMaxDim) return ROG_ERR_TOO_LARGE;
+    uint64_t v = 0;
+    for (int r = 0; r < W; ++r) {
+        if (shards[r].width < 0) return ROG_ERR_INVALID_ARGUMENT;
+        if (uint64_t(shards[r].width) >= kMaxVocab || v + uint64_t(shards[r].width) >= kMaxVocab) return ROG_ERR_TOO_LARGE;
+        if (addresses) {
+            const rog_status st = check_matrix(shards[r].weight, shards[r].row_stride, uint64_t(shards[r].width), uint64_t(dim), es, false);
+            if (st != ROG_OK) return st;
+        }
+        h->s[r] = WeightShard{shards[r].weight, shards[r].row_stride * es, uint32_t(shards[r].width), uint32_t(v)};
+        if (shards[r].width && !aligned(shards[r].weight, shards[r].width > 1 ? uint64_t(h->s[r].stride) : 0, uint64_t(dim) * es)) *direct = false;
+        v += uint64_t(shards[r].width);
+    }
+    h->W = uint32_t(W);
+    h->vocab = uint32_t(v);
+    return ROG_OK;
+}
+
+void lay_tiles(WeightShards *h, uint32_t tile) {
+    uint32_t t = 0, b = 0;
+    for (uint32_t r = 0; r < h->W; ++r) {
+        h->tile0[r] = t;
+        h->block0[r] = b;
+        t += uint32_t(ceil_div(h->s[r].width, tile));
+        b += uint32_t(ceil_div(h->s[r].width, kLinearBlock));
+    }
+    h->tile0[h->W] = t;
+    h->block0[h->W] = b;
+}
+
+// The tile for so many rows.
+int32_t form_of(uint64_t rows) { return rows <= 64 ? kTileFew : rows <= 128 ? kTileMid : kTileWide; }
+uint32_t tile_columns(int32_t form) { return form == kTileWide ? 256 : 128; }
+uint32_t tile_rows(int32_t form) { return form == kTileWide ? 256 : form == kTileMid ? 128 : 64; }
+
+constexpr uint64_t kPackFrom = 65;   // rows from which the scored ones are packed
+
+// A workspace, laid out front to back: behind the arrival counters of the other operators, which stay zero.
+struct Layout {
+    uint64_t at = kHeadCounterBytes;
+    uint64_t take(uint64_t bytes) {
+        const uint64_t p = at;
+        at = up(at + bytes, 256);
+        return p;
+    }
+};
+template <class T>
+T *in(void *workspace, uint64_t at) { return reinterpret_cast<T *>(static_cast<char *>(workspace) + at); }
+
+Strip matrix(const void *p, uint64_t rows, int64_t stride_bytes, uint64_t row_bytes) {
+    return Strip{addr(p), rows, uint64_t(stride_bytes), row_bytes};
+}
+
+}  // namespace
+
+rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim, const rog_weight_shard *shards, int W,
+                               rog_dtype dtype, float temperature, const int64_t *tokens, const rog_logprob_out *out, void *workspace,
+                               size_t workspace_bytes, bool addresses, bool has_tokens, ScorePlan *p) {
+    if (!product_type(dtype)) return ROG_ERR_INVALID_ARGUMENT;
+    if (!(temperature >= kMinTemperature && temperature <= kMaxTemperature)) return ROG_ERR_INVALID_ARGUMENT;
+    ScoreArgs &a = p->args;
+    p->direct = true;
+    rog_status st = lay_weights(shards, W, dim, 2, addresses, &a.sh, &p->direct);
+    if (st != ROG_OK) return st;
+    if (rows >= kMaxVocab) return ROG_ERR_TOO_LARGE;
+    if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false);
+    if (st != ROG_OK) return st;
+    p->form = form_of(rows);
+    p->packs = has_tokens && rows >= kPackFrom;
+    lay_tiles(&a.sh, tile_columns(p->form));
+    const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kSlabBytes);
+    if (!p->packs && !aligned(hidden, rows > 1 ? uint64_t(hidden_stride) * 2 : 0, kbytes)) p->direct = false;
+    const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
+    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    p->grid = uint32_t(groups);
+    a.unit_leaves = p->form == kTileWide ? 4 : p->form == kTileMid ? 2 : 1;
+    a.rows_pad = uint32_t(up(rows, 16));
+    const uint32_t blocks = a.sh.block0[W];
+    Layout w;
+    const uint64_t target = w.take(rows * 4), states = w.take(uint64_t(blocks) * (4 / a.unit_leaves) * a.rows_pad * 16);
+    const uint64_t index = w.take(p->packs ? rows * 4 : 0), count = w.take(p->packs ? 4 : 0), rows_at = w.take(p->packs ? rows * packed : 0);
+    p->workspace_bytes = rows ? w.at : 0;
+    if (rows == 0 || !addresses) return ROG_OK;
+
+    if (!out || out->top_logp || out->top_ids || (out->logp && !tokens)) return ROG_ERR_INVALID_ARGUMENT;
+    if (addr(tokens) % 8 || (addr(out->logp) | addr(out->entropy) | addr(out->lse)) % 4) return ROG_ERR_INVALID_ARGUMENT;
+    if (!workspace || addr(workspace) % 16 || workspace_bytes < p->workspace_bytes) return ROG_ERR_INVALID_ARGUMENT;
+    const Strip outs[4] = {flat(out->logp, out->logp ? rows * 4 : 0), flat(out->entropy, out->entropy ? rows * 4 : 0),
+                           flat(out->lse, out->lse ? rows * 4 : 0), flat(workspace, p->workspace_bytes)};
+    for (int i = 0; i < 4; ++i) {
+        if (outs[i].at > UINTPTR_MAX - outs[i].width) return ROG_ERR_TOO_LARGE;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return ROG_ERR_OVERLAP;
+        if (tokens && overlap(outs[i], flat(tokens, rows * 8))) return ROG_ERR_OVERLAP;
+        if (overlap(outs[i], matrix(hidden, rows, hidden_stride * 2, kbytes))) return ROG_ERR_OVERLAP;
+        for (int r = 0; r < W; ++r)
+            if (overlap(outs[i], matrix(a.sh.s[r].w, a.sh.s[r].width, a.sh.s[r].stride, kbytes))) return ROG_ERR_OVERLAP;
+    }
+    a.a = LinearRows{hidden, hidden_stride * 2, nullptr, uint32_t(rows), uint32_t(kbytes)};
+    a.tokens = tokens;
+    a.index = nullptr;
+    a.scale = float(kLog2E / double(temperature));
+    a.target = in<float>(workspace, target);
+    a.states = in<float>(workspace, states);
+    if (p->packs) {
+        p->pack = PackArgs{};
+        p->pack.x = hidden;
+        p->pack.stride = hidden_stride * 2;
+        p->pack.tokens = tokens;
+        p->pack.rows = uint32_t(rows);
+        p->pack.kbytes = uint32_t(kbytes);
+        p->pack.packed_bytes = uint32_t(packed);
+        p->pack.index = in<uint32_t>(workspace, index);
+        p->pack.count = in<uint32_t>(workspace, count);
+        p->pack.packed = in<void>(workspace, rows_at);
+        p->pack.logp = out->logp;
+        p->pack.entropy = out->entropy;
+        p->pack.lse = out->lse;
+        a.a = LinearRows{p->pack.packed, int64_t(packed), p->pack.count, uint32_t(rows), uint32_t(kbytes)};
+        a.index = p->pack.index;
+    }
+    p->join = JoinArgs{tokens, a.index, a.a.count, a.target, a.states, out->logp, out->entropy, out->lse, uint32_t(rows), a.rows_pad,
+                       a.sh.vocab, blocks, a.unit_leaves, a.scale};
+    return ROG_OK;
+}
+
+rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim, const rog_weight_shard *shards, int W,
+                            rog_dtype dtype, float temperature, const int64_t *tokens, const float *lse, const float *entropy,
+                            const float *g_logp, const float *g_entropy, void *d_hidden, int64_t d_hidden_stride,
+                            const rog_grad_shard *d_weights, void *workspace, size_t workspace_bytes, bool addresses, GradPlan *p) {
+    if (!product_type(dtype)) return ROG_ERR_INVALID_ARGUMENT;
+    if (!(temperature >= kMinTemperature && temperature <= kMaxTemperature)) return ROG_ERR_INVALID_ARGUMENT;
+    GradArgs &a = p->coef;
+    BackArgs &k = p->back;
+    p->dtype = dtype;
+    p->direct = true;
+    rog_status st = lay_weights(shards, W, dim, 2, addresses, &a.sh, &p->direct);
+    if (st != ROG_OK) return st;
+    if (a.sh.vocab == 0) return ROG_ERR_INVALID_ARGUMENT;
+    if (rows >= kMaxVocab) return ROG_ERR_TOO_LARGE;
+    if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false);
+    if (st != ROG_OK) return st;
+    lay_tiles(&a.sh, kGradTile);
+    const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kSlabBytes);
+    p->wide = rows > 64;
+    const uint32_t bn = p->wide ? 256 : 64;
+    k = BackArgs{};
+    k.sh = a.sh;
+    k.dim = uint32_t(dim);
+    k.dim_pad = uint32_t(packed / 2);
+    k.dim_tiles = uint32_t(ceil_div(uint64_t(dim), 256));
+    k.row_tiles = uint32_t(ceil_div(rows, bn));
+    // Segments go by the width of the states alone, so that the sums' order does.
+    k.seg_tiles = dim >= 2048 ? 32 : dim >= 512 ? 16 : 8;
+    uint32_t segs = 0;
+    for (int r = 0; r < W; ++r) {
+        k.seg0[r] = segs;
+        segs += uint32_t(ceil_div(a.sh.tile0[r + 1] - a.sh.tile0[r], k.seg_tiles));
+    }
+    k.seg0[W] = segs;
+    p->running = uint64_t(k.dim_tiles) * k.row_tiles >= 128;
+    // Pieces are runs of whole segments: as many as the bytes allow.
+    const uint64_t tile_bytes = std::max<uint64_t>(1, rows) * kGradTile * 2;
+    uint64_t tiles = std::max<uint64_t>(1, ROG_LINEAR_PIECE_BYTES / tile_bytes);
+    p->piece_tiles = uint32_t(std::min<uint64_t>(std::max<uint64_t>(tiles, k.seg_tiles), 4096));
+    // Count them as lay_piece() walks.
+    p->pieces = 0;
+    uint32_t most_tiles = 0, most_segs = 0;
+    for (uint32_t s = 0; s < segs;) {
+        uint32_t t = 0, n = 0;
+        for (int r = 0; r < W && s < segs; ++r)
+            while (s >= k.seg0[r] && s < k.seg0[r + 1]) {
+                const uint32_t left = a.sh.tile0[r + 1] - a.sh.tile0[r] - (s - k.seg0[r]) * k.seg_tiles, here = std::min(left, k.seg_tiles);
+                if (n && t + here > p->piece_tiles) goto full;
+                t += here;
+                ++n;
+                ++s;
+            }
+    full:
+        most_tiles = std::max(most_tiles, t);
+        most_segs = std::max(most_segs, n);
+        ++p->pieces;
+    }
+    p->piece_tiles = std::max(p->piece_tiles, 1u);
+    const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles;
+    const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 2;
+    if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    Layout w;
+    const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), rows_at = w.take(rows * packed);
+    const uint64_t g = w.take(rows * uint64_t(most_tiles) * kGradTile * 2);
+    const uint64_t seg_floats = rows * uint64_t(k.dim_pad);
+    const uint64_t part = w.take(seg_floats * 4 * (p->running ? 1 : segs));
+    p->workspace_bytes = rows ? w.at : 0;
+    if (rows == 0 || !addresses) return ROG_OK;
+
+    if (!tokens || !lse || !entropy || !g_logp || !d_weights || addr(tokens) % 8 ||
+        (addr(lse) | addr(entropy) | addr(g_logp) | addr(g_entropy)) % 4)
+        return ROG_ERR_INVALID_ARGUMENT;
+    st = check_matrix(d_hidden, d_hidden_stride, rows, uint64_t(dim), 2, true);
+    if (st != ROG_OK) return st;
+    if (!workspace || addr(workspace) % 16 || workspace_bytes < p->workspace_bytes) return ROG_ERR_INVALID_ARGUMENT;
+    const Strip work = flat(workspace, p->workspace_bytes), dh = matrix(d_hidden, rows, d_hidden_stride * 2, kbytes);
+    if (work.at > UINTPTR_MAX - work.width) return ROG_ERR_TOO_LARGE;
+    const Strip x = matrix(hidden, rows, hidden_stride * 2, kbytes);
+    const Strip vectors[5] = {flat(lse, rows * 4), flat(entropy, rows * 4), flat(g_logp, rows * 4),
+                              flat(g_entropy, g_entropy ? rows * 4 : 0), flat(tokens, rows * 8)};
+    if (overlap(work, dh) || overlap(work, x) || overlap(dh, x)) return ROG_ERR_OVERLAP;
+    for (const Strip &v : vectors)
+        if (overlap(work, v) || overlap(dh, v)) return ROG_ERR_OVERLAP;
+    for (int r = 0; r < W; ++r) {
+        const uint64_t width = a.sh.s[r].width;
+        if (width) {
+            st = check_matrix(d_weights[r].grad, d_weights[r].row_stride, width, uint64_t(dim), 2, true);
+            if (st != ROG_OK) return st;
+        }
+        k.dw[r] = d_weights[r].grad;
+        k.dw_stride[r] = width ? d_weights[r].row_stride * 2 : 0;
+        const Strip dw = matrix(k.dw[r], width, k.dw_stride[r], kbytes), wr = matrix(a.sh.s[r].w, width, a.sh.s[r].stride, kbytes);
+        if (overlap(dw, work) || overlap(dw, dh) || overlap(dw, x) || overlap(wr, work) || overlap(wr, dh)) return ROG_ERR_OVERLAP;
+        for (const Strip &v : vectors)
+            if (overlap(dw, v)) return ROG_ERR_OVERLAP;
+        for (int q = 0; q < W; ++q)
+            if (overlap(dw, matrix(a.sh.s[q].w, a.sh.s[q].width, a.sh.s[q].stride, kbytes)) ||
+                (q < r && overlap(dw, matrix(k.dw[q], a.sh.s[q].width, k.dw_stride[q], kbytes))))
+                return ROG_ERR_OVERLAP;
+    }
+
+    PackArgs &c = p->pack;
+    c = PackArgs{};
+    c.x = hidden;
+    c.stride = hidden_stride * 2;
+    c.tokens = tokens;
+    c.rows = uint32_t(rows);
+    c.kbytes = uint32_t(kbytes);
+    c.packed_bytes = uint32_t(packed);
+    c.index = in<uint32_t>(workspace, index);
+    c.count = in<uint32_t>(workspace, count);
+    c.packed = in<void>(workspace, rows_at);
+    c.zero = d_hidden;
+    c.zero_stride = d_hidden_stride * 2;
+    c.g_logp = g_logp;
+    c.g_entropy = g_entropy;
+    c.g_scale = dtype == ROG_DTYPE_F16 ? in<float>(workspace, g_scale) : nullptr;
+    c.inv_t = float(1.0 / double(temperature));
+    a.a = LinearRows{c.packed, int64_t(packed), c.count, uint32_t(rows), uint32_t(kbytes)};
+    a.tokens = tokens;
+    a.index = c.index;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.g_logp = g_logp;
+    a.g_entropy = g_entropy;
+    a.g_scale = c.g_scale;
+    a.inv_t = c.inv_t;
+    a.g = in<void>(workspace, g);
+    a.g_stride = int64_t(most_tiles) * kGradTile * 2;
+    k.a = a.a;
+    k.index = a.index;
+    k.g_scale = a.g_scale;
+    k.g = a.g;
+    k.g_stride = a.g_stride;
+    k.part = in<float>(workspace, part);
+    k.part_seg = p->running ? 0 : seg_floats;
+    k.d_hidden = d_hidden;
+    k.d_stride = d_hidden_stride * 2;
+    p->join_grid = 0;
+    if (!p->running) {
+        const uint64_t groups = ceil_div(rows * (k.dim_pad / 8), 256);
+        if (groups >= uint64_t(1) << 24) return ROG_ERR_TOO_LARGE;
+        p->join_grid = uint32_t(groups);
+        p->join = BackJoinArgs{k.part, k.part_seg, segs, k.dim_pad, k.dim, k.index, c.count, k.g_scale, uint32_t(rows), d_hidden, k.d_stride};
+    }
+    a.tile_begin = a.tiles = k.seg_begin = k.segs = 0;
+    return ROG_OK;
+}
+
+void lay_piece(GradPlan *p, uint32_t i, uint32_t *coef_grid, uint32_t *back_grid) {
+    GradArgs &a = p->coef;
+    BackArgs &k = p->back;
+    const uint32_t W = a.sh.W, segs = k.seg0[W];
+    float *const part = p->back.part;
+    uint32_t s = k.seg_begin + k.segs;          // where the last piece ended
+    k.tile_begin = a.tile_begin + a.tiles;
+    k.part = part + (p->running ? 0 : uint64_t(k.segs) * k.part_seg);
+    k.seg_begin = s;
+    k.segs = k.tiles = 0;
+    for (uint32_t r = 0; r < W && s < segs; ++r)
+        while (s >= k.seg0[r] && s < k.seg0[r + 1]) {
+            const uint32_t left = a.sh.tile0[r + 1] - a.sh.tile0[r] - (s - k.seg0[r]) * k.seg_tiles, here = std::min(left, k.seg_tiles);
+            if (k.segs && k.tiles + here > p->piece_tiles) goto full;
+            k.tiles += here;
+            ++k.segs;
+            ++s;
+        }
+full:
+    k.first = i == 0;
+    k.last = s == segs;
+    a.tile_begin = k.tile_begin;
+    a.tiles = k.tiles;
+    *coef_grid = k.tiles * k.row_tiles;
+    *back_grid = (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles + k.dim_tiles * k.tiles * (p->wide ? 1 : 2);
+}
+
+rog_status plan_quantize(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q, int64_t q_stride,
+                         float *scale, QuantizeArgs *a) {
+    if (!known(dtype) || dim < 1) return ROG_ERR_INVALID_ARGUMENT;
+    if (rows >= uint64_t(1) << 23 || uint64_t(dim) >= kMaxDim) return ROG_ERR_TOO_LARGE;
+    const uint32_t es = esize(dtype);
+    rog_status st = check_matrix(x, row_stride, rows, uint64_t(dim), es, false);
+    if (st == ROG_OK) st = check_matrix(q, q_stride, rows, uint64_t(dim), 1, true);
+    if (st != ROG_OK || rows == 0) return st;
+    if (!scale || addr(scale) % 4) return ROG_ERR_INVALID_ARGUMENT;
+    const Strip xs = matrix(x, rows, row_stride * es, uint64_t(dim) * es), qs = matrix(q, rows, q_stride, uint64_t(dim)), s = flat(scale, rows * 4);
+    if (s.at > UINTPTR_MAX - s.width) return ROG_ERR_TOO_LARGE;
+    if (overlap(xs, qs) || overlap(xs, s) || overlap(qs, s)) return ROG_ERR_OVERLAP;
+    *a = QuantizeArgs{x, row_stride * es, q, q_stride, scale, uint32_t(rows), uint32_t(dim)};
+    return ROG_OK;
+}
+
+rog_status plan_linear_i8(const int8_t *q, int64_t q_stride, const float *scale, size_t rows, int64_t dim, const rog_i8_shard *shards, int W,
+                          rog_dtype out_dtype, const rog_grad_shard *out, LinearI8Plan *p) {
+    LinearI8Args &a = p->args;
+    p->direct = true;
+    p->grid = 0;
+    if (!known(out_dtype)) return ROG_ERR_INVALID_ARGUMENT;
+    rog_status st = lay_weights(shards, W, dim, 1, true, &a.sh, &p->direct);
+    if (st != ROG_OK) return st;
+    if (rows >= kMaxVocab) return ROG_ERR_TOO_LARGE;
+    st = check_matrix(q, q_stride, rows, uint64_t(dim), 1, false);
+    if (st != ROG_OK || rows == 0) return st;
+    if (!scale || addr(scale) % 4 || !out) return ROG_ERR_INVALID_ARGUMENT;
+    const uint32_t os = esize(out_dtype);
+    const Strip qs = matrix(q, rows, q_stride, uint64_t(dim)), ss = flat(scale, rows * 4);
+    for (int r = 0; r < W; ++r) {
+        const uint64_t width = a.sh.s[r].width;
+        a.scale[r] = shards[r].scale;
+        a.out[r] = out[r].grad;
+        a.out_stride[r] = 0;
+        if (!width) continue;
+        if (!shards[r].scale || addr(shards[r].scale) % 4 || !out[r].grad || addr(out[r].grad) % os || out[r].row_stride < 0 ||
+            (rows > 1 && uint64_t(out[r].row_stride) < width))
+            return ROG_ERR_INVALID_ARGUMENT;
+        if (uint64_t(out[r].row_stride) >= uint64_t(1) << 48) return ROG_ERR_TOO_LARGE;
+        a.out_stride[r] = out[r].row_stride * os;
+        if (!fits(addr(a.out[r]), rows, uint64_t(a.out_stride[r]), width * os)) return ROG_ERR_TOO_LARGE;
+    }
+    for (int r = 0; r < W; ++r) {
+        const Strip o = matrix(a.out[r], rows, a.out_stride[r], uint64_t(a.sh.s[r].width) * os);
+        if (overlap(o, qs) || overlap(o, ss)) return ROG_ERR_OVERLAP;
+        for (int s = 0; s < W; ++s)
+            if (overlap(o, matrix(a.sh.s[s].w, a.sh.s[s].width, a.sh.s[s].stride, uint64_t(dim))) ||
+                overlap(o, flat(a.scale[s], uint64_t(a.sh.s[s].width) * 4)) ||
+                (s < r && overlap(o, matrix(a.out[s], rows, a.out_stride[s], uint64_t(a.sh.s[s].width) * os))))
+                return ROG_ERR_OVERLAP;
+    }
+    p->form = form_of(rows);
+    lay_tiles(&a.sh, tile_columns(p->form));
+    if (!aligned(q, rows > 1 ? uint64_t(q_stride) : 0, uint64_t(dim))) p->direct = false;
+    const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
+    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    p->grid = uint32_t(groups);
+    a.a = LinearRows{q, q_stride, nullptr, uint32_t(rows), uint32_t(dim)};
+    a.row_scale = scale;
+    return ROG_OK;
+}
+
+}  // namespace rog
+
+extern "C" {
+
+ROG_API rog_status rog_linear_logprob_plan(const rog_weight_shard *shards, int W, size_t rows, int64_t dim, rog_dtype dtype, int tokens,
+                                           rog_linear_plan_info *info) {
+    if (!info) return ROG_ERR_INVALID_ARGUMENT;
+    rog::ScorePlan p;
+    const rog_status st = rog::plan_linear_logprob(nullptr, 0, rows, dim, shards, W, dtype, 1.0f, nullptr, nullptr, nullptr, 0, false,
+                                                   tokens != 0, &p);
+    if (st != ROG_OK) return st;
+    *info = rog_linear_plan_info{rows ? rog::tile_columns(p.form) : 0, rows ? rog::tile_rows(p.form) : 0, rows ? 1u : 0u,
+                                 rows ? 1u + (p.grid != 0) + p.packs : 0u, p.workspace_bytes};
+    return ROG_OK;
+}
+
+ROG_API rog_status rog_linear_logprob_grad_plan(const rog_weight_shard *shards, int W, size_t rows, int64_t dim, rog_dtype dtype,
+                                                rog_linear_plan_info *info) {
+    if (!info) return ROG_ERR_INVALID_ARGUMENT;
+    rog::GradPlan p;
+    const rog_status st = rog::plan_linear_grad(nullptr, 0, rows, dim, shards, W, dtype, 1.0f, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                                nullptr, 0, nullptr, nullptr, 0, false, &p);
+    if (st != ROG_OK) return st;
+    *info = rog_linear_plan_info{rows ? rog::kGradTile : 0, rows ? (p.wide ? 256u : 64u) : 0, rows ? p.pieces : 0,
+                                 rows ? 1 + 2 * p.pieces + !p.running : 0, p.workspace_bytes};
+    return ROG_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,364 @@
+// rog_linear_score.hip -- HIP kernels of token log probabilities from hidden
+// states for gfx950 (CDNA4), and the C entry point that launches them.
+//
+// x_ij = h_i . w_j over K, z = x / T; per row lse, entropy and the log
+// probability of one token, with no logit ever written: a tile's logits stay in
+// the accumulators, where each leaf of 32 columns gives the state
+//     m = max x log2(e) / T,  s = sum 2^{x log2(e) / T - m},  t = sum 2^{..} (..)
+// of its columns, and the leaves' states are joined over one tree.
+#include <hip/hip_runtime.h>
+
+#include "rog_linear_device.h"
+
+namespace rog {
+namespace {
+
+#pragma clang fp contract(off)
+
+// Joined states of some columns, in the log2 domain.  No columns (or all at -inf): m = -inf, s = t = 0.
+struct Part {
+    float m, s, t;
+};
+constexpr float kFar = -1000.0f;   // 2^kFar is 0, and 0 times it is 0
+
+__device__ __forceinline__ float base_of(float m) { return m == -kInf ? 0.0f : m; }
+
+__device__ __forceinline__ Part join(const Part &a, const Part &b) {
+    const float m = max_nan(a.m, b.m), at = base_of(m);
+    const float da = fmaxf(a.m - at, kFar), db = fmaxf(b.m - at, kFar);
+    const float fa = exp2_fast(a.m - at), fb = exp2_fast(b.m - at);
+    Part o;
+    o.m = m;
+    o.s = __builtin_fmaf(a.s, fa, b.s * fb);
+    o.t = __builtin_fmaf(__builtin_fmaf(a.s, da, a.t), fa, __builtin_fmaf(b.s, db, b.t) * fb);
+    return o;
+}
+
+// The state of a leaf from the eight logits of it that each lane holds: lanes 16, 32 and 48 on hold the rest.
+__device__ __forceinline__ Part leaf_of(const float (&x)[8], float scale) {
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = max_nan(top, x[i]);
+    top = max_nan(top, __shfl_xor(top, 16));
+    top = max_nan(top, __shfl_xor(top, 32));
+    Part p;
+    p.m = top * scale;
+    const float at = base_of(p.m);
+    float s[8], t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float d = __builtin_fmaf(x[i], scale, -at);
+        s[i] = exp2_fast(d);
+        t[i] = s[i] * fmaxf(d, kFar);
+    }
+#pragma unroll
+    for (int d = 4; d; d /= 2)
+#pragma unroll
+        for (int i = 0; i < d; ++i) {
+            s[i] += s[i + d];
+            t[i] += t[i + d];
+        }
+    s[0] += __shfl_xor(s[0], 16);
+    t[0] += __shfl_xor(t[0], 16);
+    p.s = s[0] + __shfl_xor(s[0], 32);
+    p.t = t[0] + __shfl_xor(t[0], 32);
+    return p;
+}
+
+__device__ __forceinline__ void put_part(float *states, uint64_t at, const Part &p) {
+    typedef __attribute__((address_space(1))) f32x4 gstate;
+    *((gstate *)states + at) = f32x4{p.m, p.s, p.t, 0};
+}
+
+template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void rog_linear_score_kernel(ScoreArgs p) {
+    constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16, LEAVES = FM / 2;
+    typedef RowSlab<true, BM, THREADS, DIRECT, 2> A;
+    typedef RowSlab<false, BN, THREADS, DIRECT, 2> B;
+    __shared__ __attribute__((aligned(16))) uint8_t a0[A::kBytes], a1[A::kBytes], b0[B::kBytes], b1[B::kBytes];
+    const uint32_t rows = p.a.count ? *p.a.count : p.a.rows;
+    const uint32_t tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
+    if (blockIdx.x >= tm * tn) return;
+    const TileAt at = tile_at(blockIdx.x, tm, tn);
+    const uint32_t r = shard_of_tile(p.sh, at.m), v0 = (at.m - p.sh.tile0[r]) * BM, n0 = at.n * BN;
+    const WeightShard sh = p.sh.s[r];
+    const A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    const B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
+    const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    typename Mat<DT>::Acc acc[FM][FN] = {};
+    tile_product<DT, FM, FN>(a, b, (p.a.kbytes + kSlabBytes - 1) / kSlabBytes, m0, w0, a0, a1, b0, b1, acc);
+
+    // lane l holds columns v0 + m0 + 32 f + 8 (l / 16) + 0 .. 7 of leaf f, row n0 + w0 + 16 j + l % 16
+    const uint32_t first = v0 + m0 + l / 16 * 8;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const uint32_t n = n0 + w0 + 16 * j + l % 16;
+        int64_t tok = -1;
+        if (p.tokens && n < rows) tok = p.tokens[p.index ? p.index[n] : n];
+        const int64_t own = tok - int64_t(sh.col0) - int64_t(first);
+        Part part[LEAVES];
+#pragma unroll
+        for (int f = 0; f < LEAVES; ++f) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4];
+            if (own >= 32 * f && own < 32 * f + 8 && first + uint32_t(own) < sh.width) {
+                float hit = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hit = own - 32 * f == i ? x[i] : hit;
+                p.target[n] = hit;
+            }
+            if (v0 + m0 + 32 * f + 32 > sh.width)
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i)
+                    if (first + 32 * f + i >= sh.width) x[i] = -kInf;
+            part[f] = leaf_of(x, p.scale);
+        }
+#pragma unroll
+        for (int d = 1; d < LEAVES; d *= 2)
+#pragma unroll
+            for (int f = 0; f + d < LEAVES; f += 2 * d) part[f] = join(part[f], part[f + d]);
+        const uint32_t block = p.sh.block0[r] + (v0 + m0) / kLinearBlock;
+        if (l < 16 && n < rows && block < p.sh.block0[r + 1])
+            put_part(p.states, (uint64_t(block) * (4 / LEAVES) + (v0 + m0) % kLinearBlock / (32 * LEAVES)) * p.rows_pad + n, part[0]);
+    }
+}
+
+// Joins a row's blocks: chunk c of 64 takes every 64th block from the c-th on, one
+// after the other, and the chunks are joined in pairs 32, 16, .. 1 apart.
+constexpr uint32_t kJoinRows = 16, kJoinThreads = 64 * kJoinRows;
+__global__ __launch_bounds__(kJoinThreads) void rog_linear_join_kernel(JoinArgs p) {
+    __shared__ float sm[kJoinThreads], ss[kJoinThreads], st[kJoinThreads];
+    typedef const __attribute__((address_space(1))) f32x4 gstate;
+    const uint32_t rows = p.count ? *p.count : p.rows, chunk = threadIdx.x / kJoinRows;
+    const uint32_t n = blockIdx.x * kJoinRows + threadIdx.x % kJoinRows;
+    if (blockIdx.x * kJoinRows >= rows) return;
+    Part all = {-kInf, 0, 0};
+    if (n < rows) {
+        gstate *from = (gstate *)p.states + n;
+        const uint32_t units = 4 / p.unit_leaves;
+        const auto get = [&](uint64_t unit) {
+            const f32x4 v = from[unit * p.rows_pad];
+            return Part{v[0], v[1], v[2]};
+        };
+        for (uint32_t b = chunk; b < p.blocks; b += 64) {
+            Part o = get(uint64_t(b) * units);
+            if (units > 1) o = join(o, get(uint64_t(b) * units + 1));
+            if (units > 2) o = join(o, join(get(uint64_t(b) * units + 2), get(uint64_t(b) * units + 3)));
+            all = b == chunk ? o : join(all, o);
+        }
+    }
+    for (uint32_t d = 32; d; d /= 2) {
+        __syncthreads();
+        if (chunk >= d && chunk < 2 * d) {
+            sm[threadIdx.x] = all.m;
+            ss[threadIdx.x] = all.s;
+            st[threadIdx.x] = all.t;
+        }
+        __syncthreads();
+        const uint32_t o = threadIdx.x + d * kJoinRows;
+        if (chunk < d) all = join(all, Part{sm[o], ss[o], st[o]});
+    }
+    if (chunk || n >= rows) return;
+    const uint32_t row = p.index ? p.index[n] : n;
+    const int64_t tok = p.tokens ? p.tokens[row] : 0;
+    float logp = 0, entropy = 0, lse = 0;
+    if (tok >= 0) {
+        const float log_s = log2f(all.s), at = base_of(all.m);
+        const bool empty = all.m == -kInf;
+        lse = empty ? -kInf : (all.m + log_s) * kLn2;
+        entropy = empty ? 0.0f : fmaxf(0.0f, (log_s - all.t / all.s) * kLn2);
+        if (!(all.s == all.s)) entropy = all.s;
+        if (p.logp) {
+            logp = tok >= int64_t(p.vocab) ? __builtin_nanf("")
+                   : empty                 ? -kInf : (__builtin_fmaf(p.target[n], p.scale, -at) - log_s) * kLn2;
+        }
+    }
+    if (p.logp) p.logp[row] = logp;
+    if (p.entropy) p.entropy[row] = entropy;
+    if (p.lse) p.lse[row] = lse;
+}
+
+// Packs the scored rows in their order: a workgroup counts those before its rows, then copies its own.
+constexpr uint32_t kPackRows = 32, kPackThreads = 256;
+__global__ __launch_bounds__(kPackThreads) void rog_linear_pack_kernel(PackArgs p) {
+    __shared__ uint32_t sums[kPackThreads / 64], own[kPackRows];
+    __shared__ float most[kPackThreads / 64];
+    const uint32_t row0 = blockIdx.x * kPackRows, t = threadIdx.x;
+    uint32_t before = 0;
+    for (uint32_t i = t; i < row0; i += kPackThreads) before += p.tokens[i] >= 0;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
+    if (t % 64 == 0) sums[t / 64] = before;
+    if (t < kPackRows) own[t] = row0 + t < p.rows && p.tokens[row0 + t] >= 0;
+    __syncthreads();
+    before = 0;
+    for (uint32_t i = 0; i < kPackThreads / 64; ++i) before += sums[i];
+    const uint32_t wave = t / 64, l = t % 64;
+    for (uint32_t i = 0; i < kPackRows && row0 + i < p.rows; ++i) {
+        const uint32_t row = row0 + i;
+        const bool kept = own[i];
+        if (i % (kPackThreads / 64) == wave) {
+            gbyte *from = (gbyte *)p.x + uint64_t(row) * uint64_t(p.stride);
+            if (kept) {
+                __attribute__((address_space(1))) uint8_t *to =
+                    (__attribute__((address_space(1))) uint8_t *)p.packed + uint64_t(before) * p.packed_bytes;
+                for (uint32_t at = l * 16; at < p.packed_bytes; at += 1024)
+                    *(gvec16any_out *)(to + at) = row_bytes<2>(from, at, p.kbytes);
+                if (l == 0) p.index[before] = row;
+            } else {
+                if (p.zero) {
+                    __attribute__((address_space(1))) uint16_t *to =
+                        (__attribute__((address_space(1))) uint16_t *)((uint8_t *)p.zero + uint64_t(row) * uint64_t(p.zero_stride));
+                    for (uint32_t at = l; at < p.kbytes / 2; at += 64) to[at] = 0;
+                }
+                if (l == 0) {
+                    if (p.logp) p.logp[row] = 0;
+                    if (p.entropy) p.entropy[row] = 0;
+                    if (p.lse) p.lse[row] = 0;
+                }
+            }
+        }
+        before += kept;
+    }
+    if (t == 0 && row0 + kPackRows >= p.rows) *p.count = before;
+    if (!p.g_scale || blockIdx.x) return;
+    // the power of two that brings the largest coefficient there can be into [2^14, 2^15]
+    float m = 0;
+    for (uint32_t i = t; i < p.rows; i += kPackThreads)
+        if (p.tokens[i] >= 0)
+            m = fmaxf(m, fabsf(p.g_logp[i]) + (p.g_entropy ? 22.0f * fabsf(p.g_entropy[i]) : 0.0f));
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    if (l == 0) most[wave] = m;
+    __syncthreads();
+    if (t == 0) {
+        for (uint32_t i = 1; i < kPackThreads / 64; ++i) m = fmaxf(m, most[i]);
+        m *= p.inv_t;
+        int e = 0;
+        if (m > 0 && m < kInf) e = 14 - (int(f32_bits(m) >> 23) - 127);
+        e = e > 100 ? 100 : e < -100 ? -100 : e;
+        *p.g_scale = __builtin_ldexpf(1.0f, e);
+    }
+}
+
+template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN) void rog_linear_coef_kernel(GradArgs p) {
+    constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16, LEAVES = FM / 2;
+    typedef RowSlab<true, BM, THREADS, DIRECT, 2> A;
+    typedef RowSlab<false, BN, THREADS, true, 2> B;
+    __shared__ __attribute__((aligned(16))) uint8_t a0[A::kBytes], a1[A::kBytes], b0[B::kBytes], b1[B::kBytes];
+    const uint32_t rows = *p.a.count, tm = p.tiles, tn = (rows + BN - 1) / BN;
+    if (blockIdx.x >= tm * tn) return;
+    TileAt at = tile_at(blockIdx.x, tm, tn);
+    const uint32_t tile = p.tile_begin + at.m;
+    const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * BM, n0 = at.n * BN;
+    const WeightShard sh = p.sh.s[r];
+    const A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    const B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, uint32_t(p.a.stride));
+    const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    typename Mat<DT>::Acc acc[FM][FN] = {};
+    tile_product<DT, FM, FN>(a, b, (p.a.kbytes + kSlabBytes - 1) / kSlabBytes, m0, w0, a0, a1, b0, b1, acc);
+
+    constexpr float kLog2E = 1.44269504088896341f;
+    const float scale = p.inv_t * kLog2E, out = p.g_scale ? *p.g_scale * p.inv_t : p.inv_t;
+    const uint32_t first = v0 + m0 + l / 16 * 8;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const uint32_t n = n0 + w0 + 16 * j + l % 16;
+        if (n >= rows) continue;
+        const uint32_t row = p.index[n];
+        const int64_t tok = p.tokens[row];
+        const int64_t own = tok - int64_t(sh.col0) - int64_t(first);
+        const float lse = p.lse[row], h = p.entropy[row];
+        float g = p.g_logp[row] * out, gh = p.g_entropy ? p.g_entropy[row] * out : 0.0f;
+        if (tok >= int64_t(p.sh.vocab)) g = __builtin_nanf("");
+        const bool empty = lse == -kInf;
+        if (empty) g = gh = 0.0f;
+        const float at2 = empty ? kInf : lse * kLog2E;
+        const float c0 = __builtin_fmaf(gh, h, g), c1 = gh * kLn2;       // -G = p (g + gh (log p + H))
+#pragma unroll
+        for (int f = 0; f < LEAVES; ++f) {
+            float d[8];
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                const float y = __builtin_fmaf(acc[2 * f + i / 4][j][i % 4], scale, -at2);
+                const float q = exp2_fast(y);
+                d[i] = -q * __builtin_fmaf(c1, fmaxf(y, kFar), c0);
+                if (own == 32 * f + i) d[i] += g;
+                if (first + 32 * f + i >= sh.width) d[i] = 0.0f;
+            }
+            vec16 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(d + 2 * i);
+            typedef __attribute__((address_space(1))) vec16 gvec16_out;
+            *(gvec16_out *)((uint8_t *)p.g + uint64_t(n) * uint64_t(p.g_stride) + (uint64_t(at.m) * BM + m0 + l / 16 * 8 + 32 * f) * 2) = v;
+        }
+    }
+}
+
+rog_status launched(hipError_t e) {
+    if (e == hipSuccess) return ROG_OK;
+    g_last_hip_error = int(e);
+    return ROG_ERR_LAUNCH;
+}
+
+template <class Args>
+hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
+    void *list[] = {const_cast<Args *>(&args)};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
+}
+
+template <int DT, bool DIRECT>
+hipError_t launch_score(const ScorePlan &p, hipStream_t s) {
+    switch (p.form) {
+    case kTileWide: return launch(rog_linear_score_kernel<DT, 256, 256, 2, 4, DIRECT>, p.grid, 512, p.args, s);
+    case kTileMid: return launch(rog_linear_score_kernel<DT, 128, 128, 2, 2, DIRECT>, p.grid, 256, p.args, s);
+    default: return launch(rog_linear_score_kernel<DT, 128, 64, 4, 1, DIRECT>, p.grid, 256, p.args, s);
+    }
+}
+
+template <int DT, bool DIRECT>
+hipError_t launch_coef(const GradPlan &p, const GradArgs &a, uint32_t grid, hipStream_t s) {
+    if (p.wide) return launch(rog_linear_coef_kernel<DT, 256, 256, 2, 4, DIRECT>, grid, 512, a, s);
+    return launch(rog_linear_coef_kernel<DT, 256, 64, 4, 1, DIRECT>, grid, 256, a, s);
+}
+
+}  // namespace
+
+hipError_t launch_pack(const PackArgs &a, hipStream_t s) {
+    return launch(rog_linear_pack_kernel, (a.rows + kPackRows - 1) / kPackRows, kPackThreads, a, s);
+}
+
+hipError_t launch_coefficients(const GradPlan &p, const GradArgs &a, uint32_t grid, hipStream_t s) {
+    if (p.dtype == ROG_DTYPE_BF16)
+        return p.direct ? launch_coef<ROG_DTYPE_BF16, true>(p, a, grid, s) : launch_coef<ROG_DTYPE_BF16, false>(p, a, grid, s);
+    return p.direct ? launch_coef<ROG_DTYPE_F16, true>(p, a, grid, s) : launch_coef<ROG_DTYPE_F16, false>(p, a, grid, s);
+}
+
+}  // namespace rog
+
+extern "C" {
+
+ROG_API rog_status rog_linear_logprob(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim,
+                                      const rog_weight_shard *shards, int W, rog_dtype dtype, float temperature,
+                                      const int64_t *tokens, const rog_logprob_out *out, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream) {
+    rog::ScorePlan p;
+    const rog_status st = rog::plan_linear_logprob(hidden, hidden_stride, rows, dim, shards, W, dtype, temperature, tokens, out,
+                                                   workspace, workspace_bytes, true, tokens != nullptr, &p);
+    if (st != ROG_OK || rows == 0) return st;
+    using namespace rog;
+    hipError_t e = hipSuccess;
+    if (p.packs) e = launch_pack(p.pack, stream);
+    if (e == hipSuccess && p.grid) {
+        if (dtype == ROG_DTYPE_BF16) e = p.direct ? launch_score<ROG_DTYPE_BF16, true>(p, stream) : launch_score<ROG_DTYPE_BF16, false>(p, stream);
+        else e = p.direct ? launch_score<ROG_DTYPE_F16, true>(p, stream) : launch_score<ROG_DTYPE_F16, false>(p, stream);
+    }
+    if (e == hipSuccess) e = launch(rog_linear_join_kernel, uint32_t((rows + kJoinRows - 1) / kJoinRows), kJoinThreads, p.join, stream);
+    return launched(e);
+}
+
+}  // extern "C"

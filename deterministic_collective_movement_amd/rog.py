@@ -28,6 +28,16 @@ Entry points keep the C names.  Tensor forms:
   ``RogPolicyLoss``: the clipped policy loss with its gradient;
 * ``rog_logprob_plan(shards, top_k=0, form=...)`` -> dict (no GPU work).
 
+* ``rog_linear_logprob(hidden, weights, tokens=None, temperature=1.0, out=None, ...)``
+  -> ``RogLogprob``: the same from hidden states and W shards of head weights,
+  without writing the logits;
+* ``rog_linear_logprob_grad(hidden, weights, tokens, lse, entropy, g_logp, ...)``
+  -> ``RogLinearGrad``: its gradient in the hidden states and the weights;
+* ``rog_quantize_i8(x, out=None)`` -> ``RogQuantized``: rows in 8-bit integers;
+* ``rog_linear_i8(q, scale, weights, weight_scales, dtype=..., out=None)`` -> W
+  shards of logits of a head held in 8-bit integers;
+* ``rog_linear_logprob_plan``, ``rog_linear_logprob_grad_plan`` -> dict (no GPU work).
+
 Raw-pointer forms (``*_ptrs``) take integer device addresses, for callers that
 manage their own memory.
 
@@ -126,6 +136,11 @@ class rog_head_plan_info(ctypes.Structure):
                 ("blocks", ctypes.c_uint32), ("workspace_bytes", ctypes.c_uint64)]
 
 
+class rog_linear_plan_info(ctypes.Structure):
+    _fields_ = [("tile_columns", ctypes.c_uint32), ("tile_rows", ctypes.c_uint32), ("pieces", ctypes.c_uint32),
+                ("launches", ctypes.c_uint32), ("workspace_bytes", ctypes.c_uint64)]
+
+
 def _hip_runtimes_mapped() -> set:
     paths = set()
     with open("/proc/self/maps") as f:
@@ -165,7 +180,15 @@ def _load() -> ctypes.CDLL:
     lib.rog_policy_loss.argtypes = [vp, sz, vp, vp, vp, sz, vp]
     lib.rog_policy_loss_workspace_bytes.argtypes = [sz]
     lib.rog_policy_loss_workspace_bytes.restype = sz
-    for name in ("rog_logprob", "rog_logprob_ex", "rog_logprob_plan", "rog_logprob_grad", "rog_policy_loss"):
+    i64 = ctypes.c_int64
+    lib.rog_linear_logprob.argtypes = [vp, i64, sz, i64, vp, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.rog_linear_logprob_plan.argtypes = [vp, i32, sz, i64, i32, i32, vp]
+    lib.rog_linear_logprob_grad.argtypes = [vp, i64, sz, i64, vp, i32, i32, f32, vp, vp, vp, vp, vp, vp, i64, vp, vp, sz, vp]
+    lib.rog_linear_logprob_grad_plan.argtypes = [vp, i32, sz, i64, i32, vp]
+    lib.rog_quantize_i8.argtypes = [vp, i64, sz, i64, i32, vp, i64, vp, vp]
+    lib.rog_linear_i8.argtypes = [vp, i64, vp, sz, i64, vp, i32, i32, vp, vp]
+    for name in ("rog_linear_logprob", "rog_linear_logprob_plan", "rog_linear_logprob_grad", "rog_linear_logprob_grad_plan",
+                 "rog_quantize_i8", "rog_linear_i8", "rog_logprob", "rog_logprob_ex", "rog_logprob_plan", "rog_logprob_grad", "rog_policy_loss"):
         getattr(lib, name).restype = i32
     for name in ("rog_max_top_k", "rog_logprob_max_split_rows"):
         getattr(lib, name).argtypes = []
@@ -932,3 +955,226 @@ def rog_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantage: torch
         _with_workspace(lambda ws, b: _lib.rog_policy_loss(ins, n, params, outs, ws, b, handle),
                         lambda: _lib.rog_policy_loss_workspace_bytes(n), "rog_policy_loss", workspace, device, stream, handle)
     return out
+
+
+# ---------------------------------------------------------------------------
+# The policy head's products: log probabilities from hidden states, their
+# gradient, logits of 8-bit weights
+# ---------------------------------------------------------------------------
+
+class RogLinearGrad(NamedTuple):
+    """rog_linear_logprob_grad's results; as ``out``, the tensors to write."""
+    d_hidden: torch.Tensor              # [rows, dim]
+    d_weights: List[torch.Tensor]       # W matrices [width, dim]
+
+
+class RogQuantized(NamedTuple):
+    """rog_quantize_i8's results; as ``out``, the tensors to write."""
+    q: torch.Tensor                     # [rows, dim] int8
+    scale: torch.Tensor                 # [rows] float32
+
+
+_PACK_I8 = [struct.Struct("=" + "QqqQ" * w).pack for w in range(_lib.rog_max_peers() + 1)]
+_PRODUCT_DTYPES = (torch.bfloat16, torch.float16)
+
+
+def _row_matrix(t, what: str, rows: Optional[int], cols: Optional[int], dtype: torch.dtype, device: torch.device):
+    """(address, row stride) of a matrix that is contiguous within its rows; None: any size."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % what)
+    if not t.is_cuda:
+        raise ValueError("%s must be on a GPU (got %s)" % (what, t.device))
+    if t.get_device() != device.index:
+        raise ValueError("%s is on %s, expected %s" % (what, t.device, device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s (got %s)" % (what, dtype, t.dtype))
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError("%s must be a matrix of %s x %s (got %s)" % (what, "any" if rows is None else rows, "any" if cols is None else cols,
+                                                                      tuple(t.shape)))
+    stride, step = t.stride()
+    if step != 1 and t.shape[1] > 1:
+        raise ValueError("%s must be contiguous within its rows (any row stride)" % what)
+    return t.data_ptr(), stride
+
+
+def _head_bytes(hidden, weights, dtypes):
+    """(device, its index, rows, dim, dtype, address and stride of the states, packed rog_weight_shard array)."""
+    if not isinstance(hidden, torch.Tensor):
+        raise TypeError("hidden must be a torch.Tensor")
+    device, dtype = hidden.device, hidden.dtype
+    if dtype not in dtypes:
+        raise ValueError("hidden states are %s (got %s)" % (" or ".join(str(d)[6:] for d in dtypes), dtype))
+    at, stride = _row_matrix(hidden, "hidden", None, None, dtype, device)
+    rows, dim = hidden.shape
+    if len(weights) == 0:
+        raise ValueError("need at least one shard of weights")
+    if len(weights) > rog_max_peers():
+        raise ValueError("at most %d shards (got %d)" % (rog_max_peers(), len(weights)))
+    vals = []
+    for i, w in enumerate(weights):
+        a, s = _row_matrix(w, "weights[%d]" % i, None, dim, dtype, device)
+        vals += (a, s, w.shape[0])
+    return device, hidden.get_device(), rows, dim, dtype, at, stride, _PACK_SHARDS[len(weights)](*vals)
+
+
+def _linear_plan(call, what: str, *args) -> rog_linear_plan_info:
+    info = rog_linear_plan_info()
+    _check(call(*args, ctypes.byref(info)), what)
+    return info
+
+
+def _linear_plan_dict(info) -> dict:
+    return {"tile": (info.tile_columns, info.tile_rows), "pieces": info.pieces, "launches": info.launches,
+            "workspace_bytes": info.workspace_bytes}
+
+
+def _widths_bytes(widths: Sequence[int]) -> bytes:
+    return struct.pack("=" + "Qqq" * len(widths), *(v for w in widths for v in (0, 0, w)))
+
+
+def rog_linear_logprob_plan(widths: Sequence[int], rows: int, dim: int, dtype: int = ROG_DTYPE_BF16, tokens: bool = True) -> dict:
+    """The launches rog_linear_logprob would make for shards of these widths (no GPU work)."""
+    return _linear_plan_dict(_linear_plan(_lib.rog_linear_logprob_plan, "rog_linear_logprob_plan", _widths_bytes(widths), len(widths), rows,
+                                          dim, dtype, int(tokens)))
+
+
+def rog_linear_logprob_grad_plan(widths: Sequence[int], rows: int, dim: int, dtype: int = ROG_DTYPE_BF16) -> dict:
+    """The launches rog_linear_logprob_grad would make for shards of these widths (no GPU work)."""
+    return _linear_plan_dict(_linear_plan(_lib.rog_linear_logprob_grad_plan, "rog_linear_logprob_grad_plan", _widths_bytes(widths),
+                                          len(widths), rows, dim, dtype))
+
+
+def rog_linear_logprob(hidden: torch.Tensor, weights: Sequence[torch.Tensor], tokens: Optional[torch.Tensor] = None,
+                       temperature: float = 1.0, out: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> RogLogprob:
+    """``rog_logprob`` of the logits ``hidden @ cat(weights).T`` without writing them:
+    log probability of ``tokens[i]`` (int64; negative: the row is not scored, and
+    its state not used), entropy and log-sum-exp of every row.
+
+    ``hidden``: [rows, dim] bfloat16 or float16; ``weights``: W shards
+    [width_r, dim] of the same dtype in rank order; contiguous within rows, any
+    row stride.  ``out``: a RogLogprob (or five tensors, the last two None) to
+    write, None for what is not wanted.  The outputs have no gradient function:
+    ``rog_linear_logprob_grad`` gives the gradients."""
+    device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, weights, _PRODUCT_DTYPES)
+    f32 = torch.float32
+    if out is None:
+        new = lambda: torch.empty(rows, dtype=f32, device=device)  # noqa: E731
+        with _made_on(stream, device):
+            out = RogLogprob(new() if tokens is not None else None, new(), new(), None, None)
+    elif type(out) is not RogLogprob:
+        out = RogLogprob(*out)
+    if out[3] is not None or out[4] is not None:
+        raise ValueError("rog_linear_logprob gives no alternatives: out.top_logp and out.top_ids must be None")
+    outs = _pack_addresses5(*_addresses(out[:3], _OUT_NAMES, rows, f32, device, idx), 0, 0)
+    tok = None if tokens is None else _addresses((tokens,), ("tokens",), rows, torch.int64, device, idx)[0]
+    W, dt = len(weights), DTYPES[dtype]
+    with _on_device(device) if _current_device() != idx else _HERE:
+        handle = _stream_handle(stream, device)
+        _with_workspace(lambda ws, n: _lib.rog_linear_logprob(at, stride, rows, dim, packed, W, dt, temperature, tok, outs, ws, n, handle),
+                        lambda: _linear_plan(_lib.rog_linear_logprob_plan, "rog_linear_logprob", packed, W, rows, dim, dt,
+                                             int(tokens is not None)).workspace_bytes,
+                        "rog_linear_logprob", workspace, device, stream, handle)
+    return out
+
+
+def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor], tokens: torch.Tensor, lse: torch.Tensor,
+                            entropy: torch.Tensor, g_logp: torch.Tensor, g_entropy: Optional[torch.Tensor] = None,
+                            temperature: float = 1.0, out: Optional[Sequence] = None, workspace: Optional[torch.Tensor] = None,
+                            stream=None) -> RogLinearGrad:
+    """Gradient of sum_i (g_logp[i] logp[i] + g_entropy[i] entropy[i]) in the hidden
+    states and in every shard's weights, from rog_linear_logprob's ``lse`` and
+    ``entropy`` of the same states, weights and temperature.  Rows that are not
+    scored get zeros.  ``out``: a RogLinearGrad (or (d_hidden, W matrices)) to write."""
+    device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, weights, _PRODUCT_DTYPES)
+    W = len(weights)
+    if out is None:
+        with _made_on(stream, device):
+            out = RogLinearGrad(torch.empty(rows, dim, dtype=dtype, device=device),
+                                [torch.empty(w.shape[0], dim, dtype=dtype, device=device) for w in weights])
+    elif type(out) is not RogLinearGrad:
+        out = RogLinearGrad(out[0], list(out[1]))
+    if len(out.d_weights) != W:
+        raise ValueError("one gradient per shard")
+    d_at, d_stride = _row_matrix(out.d_hidden, "out.d_hidden", rows, dim, dtype, device)
+    vals = []
+    for i, g in enumerate(out.d_weights):
+        vals += _row_matrix(g, "out.d_weights[%d]" % i, weights[i].shape[0], dim, dtype, device)
+    if tokens is None or lse is None or entropy is None or g_logp is None:
+        raise ValueError("tokens, lse, entropy and g_logp are needed")
+    tok = _addresses((tokens,), ("tokens",), rows, torch.int64, device, idx)[0]
+    vec = _addresses((lse, entropy, g_logp, g_entropy), ("lse", "entropy", "g_logp", "g_entropy"), rows, torch.float32, device, idx)
+    grads, dt = _PACK_GRADS[W](*vals), DTYPES[dtype]
+    with _on_device(device) if _current_device() != idx else _HERE:
+        handle = _stream_handle(stream, device)
+        _with_workspace(lambda ws, n: _lib.rog_linear_logprob_grad(at, stride, rows, dim, packed, W, dt, temperature, tok, *vec, d_at,
+                                                                   d_stride, grads, ws, n, handle),
+                        lambda: _linear_plan(_lib.rog_linear_logprob_grad_plan, "rog_linear_logprob_grad", packed, W, rows, dim,
+                                             dt).workspace_bytes,
+                        "rog_linear_logprob_grad", workspace, device, stream, handle)
+    return out
+
+
+def rog_quantize_i8(x: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None, stream=None) -> RogQuantized:
+    """Rows of ``x`` (float32, bfloat16 or float16) in 8-bit integers with a scale
+    each: ``scale = max(max |x| / 127, 2^-126)``, ``q = x / scale`` to the nearest,
+    ties to even.  A row with a NaN or an infinity gets scale NaN and q 0.  For a
+    head's weights the rows are its columns.  ``out``: a RogQuantized to write."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    device, dtype = x.device, x.dtype
+    if dtype not in DTYPES:
+        raise ValueError("x is float32, bfloat16 or float16 (got %s)" % dtype)
+    at, stride = _row_matrix(x, "x", None, None, dtype, device)
+    rows, dim = x.shape
+    idx = x.get_device()
+    if out is None:
+        with _made_on(stream, device):
+            out = RogQuantized(torch.empty(rows, dim, dtype=torch.int8, device=device), torch.empty(rows, dtype=torch.float32, device=device))
+    elif type(out) is not RogQuantized:
+        out = RogQuantized(*out)
+    q_at, q_stride = _row_matrix(out.q, "out.q", rows, dim, torch.int8, device)
+    s_at = _addresses(out[1:], ("out.scale",), rows, torch.float32, device, idx)[0]
+    with _on_device(device) if _current_device() != idx else _HERE:
+        _check(_lib.rog_quantize_i8(at, stride, rows, dim, DTYPES[dtype], q_at, q_stride, s_at, _stream_handle(stream, device)),
+               "rog_quantize_i8")
+    return out
+
+
+def rog_linear_i8(q: torch.Tensor, scale: torch.Tensor, weights: Sequence[torch.Tensor], weight_scales: Sequence[torch.Tensor],
+                  dtype: torch.dtype = torch.bfloat16, out: Optional[Sequence[torch.Tensor]] = None, stream=None) -> List[torch.Tensor]:
+    """Logits of a head held in 8-bit integers, as shards that ``rog_logprob`` takes:
+    ``out[r][i, j] = (q[i] . weights[r][j]) * scale[i] * weight_scales[r][j]``, the
+    sum exact, the result rounded to ``dtype`` (float32, bfloat16 or float16; that of
+    ``out`` where it is given).
+
+    ``q``: [rows, dim] int8 and ``scale``: [rows] float32, as rog_quantize_i8 gives
+    them; ``weights``: W shards [width_r, dim] int8; ``weight_scales``: W vectors
+    [width_r] float32."""
+    device, idx, rows, dim, _, at, stride, _ = _head_bytes(q, weights, (torch.int8,))
+    W = len(weights)
+    if out is None:
+        if dtype not in DTYPES:
+            raise ValueError("logits are float32, bfloat16 or float16 (got %s)" % dtype)
+        with _made_on(stream, device):
+            out = [torch.empty(rows, w.shape[0], dtype=dtype, device=device) for w in weights]
+    elif len(out) and isinstance(out[0], torch.Tensor):
+        dtype = out[0].dtype
+        if dtype not in DTYPES:
+            raise ValueError("logits are float32, bfloat16 or float16 (got %s)" % dtype)
+    if len(out) != W or len(weight_scales) != W:
+        raise ValueError("one vector of scales and one output per shard")
+    s_at = _addresses((scale,), ("scale",), rows, torch.float32, device, idx)[0]
+    if scale is None:
+        raise ValueError("scale is needed")
+    shards, outs = [], []
+    for i, w in enumerate(weights):
+        if weight_scales[i] is None:
+            raise ValueError("weight_scales[%d] is needed" % i)
+        shards += (w.data_ptr(), w.stride(0), w.shape[0],
+                   _addresses(weight_scales[i:i + 1], ("weight_scales[%d]" % i,), w.shape[0], torch.float32, device, idx)[0])
+        outs += _row_matrix(out[i], "out[%d]" % i, rows, w.shape[0], dtype, device)
+    with _on_device(device) if _current_device() != idx else _HERE:
+        _check(_lib.rog_linear_i8(at, stride, s_at, rows, dim, _PACK_I8[W](*shards), W, DTYPES[dtype], _PACK_GRADS[W](*outs),
+                                  _stream_handle(stream, device)), "rog_linear_i8")
+    return out if isinstance(out, list) else list(out)

@@ -30,8 +30,8 @@
  *  - All argument errors are returned before anything is enqueued: on error no
  *    byte of any output is written and no HIP call has been made.
  *  - Success means the work has been enqueued on `stream` (asynchronous), as
- *    exactly one kernel launch; nothing else is enqueued, so calls can be
- *    captured into a HIP graph.
+ *    exactly one kernel launch (the policy head's products: several); nothing
+ *    else is enqueued, so calls can be captured into a HIP graph.
  *  - The library allocates no device or host memory, keeps no state except a
  *    thread-local copy of the last HIP error, and may be called from any thread.
  *  - Bytes outside the output range (out, W*S bytes for a gather; count
@@ -507,6 +507,135 @@ ROG_API rog_status rog_policy_loss(const rog_policy_in *in, size_t n, const rog_
 
 /* Workspace bytes of rog_policy_loss over n tokens (0: none is needed). */
 ROG_API size_t rog_policy_loss_workspace_bytes(size_t n);
+
+/* ===========================================================================
+ * The policy head's products: token log probabilities straight from hidden
+ * states and the head's weights, their gradient in both, and the logits of a head
+ * held in 8-bit integers.
+ *
+ * The head's weights are W vocabulary shards in rank order, rank r holding the
+ * vectors of `width` columns, each of `dim` elements.  A logit is
+ * x_ij = sum_k hidden_ik weight_jk, products exact, sums binary32.
+ *
+ * Beside the common rules and those of the vocabulary side:
+ *  - A row's result (its log probabilities, its gradient in the hidden states, its
+ *    8-bit logits) depends, bit for bit, on its own state, the weights, the widths
+ *    and the temperature alone: not on how many rows a call has, on the other rows,
+ *    or on alignment or strides.
+ *  - A call may be several kernel launches on `stream`, one after the other;
+ *    nothing else is enqueued.
+ *  - The workspaces need no clearing of their own; the one that rog_workspace-style
+ *    callers keep zero-filled for the other operators may serve these too (its
+ *    arrival counters are left zero).
+ *  - dim is 1 .. 2^17 - 1; row strides are below 2^22 bytes (ROG_ERR_TOO_LARGE).
+ *    Any alignment to the element; calls whose rows all begin and end on 16 bytes
+ *    are faster.
+ * ======================================================================== */
+
+/* One shard of a head: column j's weights are weight[j * row_stride + 0 .. dim). */
+typedef struct {
+    const void *weight;        /* device pointer, aligned to the element size     */
+    int64_t row_stride;        /* elements from a column to the next; >= 0        */
+    int64_t width;             /* columns; 0 is allowed                           */
+} rog_weight_shard;
+
+/* One shard of a head in 8-bit integers: column j's weights are weight[..] * scale[j]. */
+typedef struct {
+    const int8_t *weight;
+    int64_t row_stride;
+    int64_t width;
+    const float *scale;        /* [width]                                         */
+} rog_i8_shard;
+
+/* The launches a call would make. */
+typedef struct {
+    uint32_t tile_columns, tile_rows;  /* of a workgroup                          */
+    uint32_t pieces;                   /* pieces of the vocabulary                */
+    uint32_t launches;
+    uint64_t workspace_bytes;
+} rog_linear_plan_info;
+
+/*
+ * rog_linear_logprob -- rog_logprob of the logits hidden x weights, of which none
+ * is written to memory: lse, log probability of the row's token, entropy, as
+ * defined there (without alternatives: out->top_logp and out->top_ids are NULL).
+ *
+ * hidden   [rows][dim] of dtype (ROG_DTYPE_BF16 or ROG_DTYPE_F16), the weights'.
+ * tokens   as rog_logprob; the state of a row that is not scored is not used,
+ *          and such rows take no time where there are more than 64 rows.
+ *
+ * Logits are binary32 and not rounded to the states' type, so a row's numbers
+ * are nearer to the formula than rog_logprob's over logits of two bytes.  A NaN or
+ * +inf among a row's logits makes its numbers NaN.
+ *
+ * Errors as rog_logprob.
+ */
+ROG_API rog_status rog_linear_logprob(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim,
+                                      const rog_weight_shard *shards, int W, rog_dtype dtype, float temperature,
+                                      const int64_t *tokens, const rog_logprob_out *out, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* The launches and the workspace (only the shards' widths are read; tokens: whether
+ * there are any). */
+ROG_API rog_status rog_linear_logprob_plan(const rog_weight_shard *shards, int W, size_t rows, int64_t dim, rog_dtype dtype,
+                                           int tokens, rog_linear_plan_info *info);
+
+/*
+ * rog_linear_logprob_grad -- the gradient of sum_i (g_logp_i logp_i + g_entropy_i
+ * entropy_i) in the hidden states and in every shard's weights, from what
+ * rog_linear_logprob wrote:
+ *
+ *     G_ij = (g_logp_i (1[j = token_i] - p_ij) - g_entropy_i p_ij (log p_ij + entropy_i)) / temperature
+ *     d_hidden_i = sum_j G_ij weight_j,     d_weight_j = sum_i G_ij hidden_i
+ *
+ * The logits are made anew, a piece of the vocabulary at a time.  G is rounded to
+ * the states' type (binary16 after a power of two that puts the largest possible
+ * |G| of the call at 2^14 to 2^15), the sums are binary32, and each output is
+ * rounded once.  g_entropy may be NULL (0).
+ *
+ * A row that is not scored gets zeros and its state is not used.  A token of V or
+ * more, or a NaN in the row's inputs, makes the row's gradient and every weight's
+ * NaN, as the formula has it.  V is at least 1.  d_weight's bits depend on the
+ * scored rows in their order.
+ *
+ * d_weights  W gradients [width][dim], row strides of their own (>= dim).
+ * Errors as rog_logprob_grad; no output may overlap an input or another output.
+ */
+ROG_API rog_status rog_linear_logprob_grad(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim,
+                                           const rog_weight_shard *shards, int W, rog_dtype dtype, float temperature,
+                                           const int64_t *tokens, const float *lse, const float *entropy,
+                                           const float *g_logp, const float *g_entropy, void *d_hidden,
+                                           int64_t d_hidden_stride, const rog_grad_shard *d_weights, void *workspace,
+                                           size_t workspace_bytes, hipStream_t stream);
+
+ROG_API rog_status rog_linear_logprob_grad_plan(const rog_weight_shard *shards, int W, size_t rows, int64_t dim,
+                                                rog_dtype dtype, rog_linear_plan_info *info);
+
+/*
+ * rog_quantize_i8 -- rows in 8-bit integers with a scale each:
+ *
+ *     scale_i = max(max_k |x_ik| / 127, 2^-126),  q_ik = x_ik / scale_i
+ *
+ * both quotients in binary32, the second rounded to the nearest integer, ties to
+ * even (so |q| <= 127).  x is binary32, bfloat16 or binary16.  A row that holds a
+ * NaN or an infinity gets scale NaN and q 0.  q's row stride is at least dim;
+ * bytes between its rows are not written.  rows: below 2^23.
+ */
+ROG_API rog_status rog_quantize_i8(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q,
+                                   int64_t q_stride, float *scale, hipStream_t stream);
+
+/*
+ * rog_linear_i8 -- logits of a head in 8-bit integers:
+ *
+ *     out_r[i][j] = (sum_k q_ik weight_jk) * scale_i * shard_r.scale_j
+ *
+ * The sum is exact (32-bit integers), converted to binary32, multiplied by the
+ * row's scale, then by the column's, and rounded to out_dtype.  out: W matrices
+ * [rows][width], which rog_logprob takes as its shards.  Values of -128 are allowed.
+ */
+ROG_API rog_status rog_linear_i8(const int8_t *q, int64_t q_stride, const float *scale, size_t rows, int64_t dim,
+                                 const rog_i8_shard *shards, int W, rog_dtype out_dtype, const rog_grad_shard *out,
+                                 hipStream_t stream);
 
 /* Limits; constants of the build. */
 ROG_API int rog_max_top_k(void);
