@@ -140,12 +140,20 @@ struct RowSlab {
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
         }
     }
-    // Fragment f of the wave's rows from row0 (a multiple of 32) on, half `ks` of the slab.
-    static __device__ __forceinline__ vec16 frag(const uint8_t *from, uint32_t row0, uint32_t f, uint32_t ks) {
-        const uint32_t l = threadIdx.x % 64, row = row0 + frag_row<M_SIDE>(f, l % 16);
-        const uint32_t u = (ks * 4 + l / 16) ^ swizzle<M_SIDE>(row);
-        return *(const lvec16 *)((const lbyte *)from + row * kSlabBytes + u * 16);
-    }
+    // Reads fragments of a wave's rows from row0 (a multiple of 32) on: f and the half slab ks are constants,
+    // so that a fragment's address is one of two registers and an offset in the instruction.
+    struct Reader {
+        uint32_t at[2];
+        __device__ __forceinline__ explicit Reader(uint32_t row0) {
+            const uint32_t l = threadIdx.x % 64, row = frag_row<M_SIDE>(0, l % 16);
+            at[0] = (row0 + row) * kSlabBytes + (l / 16 ^ swizzle<M_SIDE>(row)) * 16;
+            at[1] = at[0] ^ 64;
+        }
+        __device__ __forceinline__ vec16 get(const uint8_t *from, int f, int ks) const {
+            const int row = M_SIDE ? 32 * (f / 2) + 4 * (f & 1) : 16 * f;
+            return *(const lvec16 *)((const lbyte *)from + at[ks] + row * int(kSlabBytes));
+        }
+    };
 };
 
 // ---------------------------------------------------------------------------
@@ -173,7 +181,7 @@ struct ColSlab {
         unit = (threadIdx.x % kUnits ^ 4 * (row % 4)) * 16;
     }
     __device__ __forceinline__ void stage(uint8_t *to, uint32_t k) const {
-        const uint32_t left = rows - k * 64;
+        const uint32_t left = rows > k * 64 ? rows - k * 64 : 0;
         const uint8_t *from = base + uint64_t(k) * 64 * uint64_t(stride);
         if constexpr (DIRECT) {
             // the last row ends with the columns that are read: nothing past it is in the window
@@ -195,16 +203,25 @@ struct ColSlab {
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
         }
     }
-    static __device__ __forceinline__ vec16 frag(const uint8_t *from, uint32_t col0, uint32_t f, uint32_t ks) {
-        const uint32_t l = threadIdx.x % 64, j = l % 16;
-        const uint32_t col = col0 + (M_SIDE ? 32 * (f / 2) + 8 * (j % 4) + 4 * (f & 1) : 16 * f + 4 * (j % 4));
-        const uint32_t k = ks * 32 + l / 16 * 8 + j / 4;                 // and four on
-        const uint32_t in = (col / 8 ^ 4 * (k % 4)) * 16 + col % 8 * 2;
-        const lbyte *p = (const lbyte *)from + k * (COLS * 2) + in;
-        struct { s16x4 lo, hi; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)p),
-                                      __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)(p + 4 * COLS * 2))};
-        return __builtin_bit_cast(vec16, v);
-    }
+    // Fragments of a wave's columns from col0 (a multiple of 64) on: the 64 bytes that hold fragments 2 i and
+    // 2 i + 1 stand at i ^ (row % 4) of four.
+    struct Reader {
+        static constexpr int kAts = 4;
+        uint32_t at[kAts];
+        __device__ __forceinline__ explicit Reader(uint32_t col0) {
+            const uint32_t l = threadIdx.x % 64, j = l % 16, k = l / 16 * 8 + j / 4;
+            const uint32_t in = M_SIDE ? 16 * (j % 4) : 8 * (j % 4);
+#pragma unroll
+            for (uint32_t i = 0; i < kAts; ++i) at[i] = k * (COLS * 2) + ((col0 / 32 + i) ^ j / 4) * 64 + in;
+        }
+        __device__ __forceinline__ vec16 get(const uint8_t *from, int f, int ks) const {
+            const int off = ks * 32 * COLS * 2 + (f / 8) * 256 + (f & 1) * (M_SIDE ? 8 : 32);
+            const lbyte *p = (const lbyte *)from + at[f / 2 % kAts] + off;
+            struct { s16x4 lo, hi; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)p),
+                                          __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)(p + 4 * COLS * 2))};
+            return __builtin_bit_cast(vec16, v);
+        }
+    };
 };
 
 // ---------------------------------------------------------------------------
@@ -213,14 +230,15 @@ struct ColSlab {
 
 // FM x FN fragments of a wave at (m0, n0) of the tile, over `slabs` slabs.
 template <int DT, int FM, int FN, class A, class B, class Acc>
-__device__ __forceinline__ void multiply(const uint8_t *pa, const uint8_t *pb, uint32_t m0, uint32_t n0, Acc (&acc)[FM][FN]) {
+__device__ __forceinline__ void multiply(const uint8_t *pa, const uint8_t *pb, const typename A::Reader &ra, const typename B::Reader &rb,
+                                         Acc (&acc)[FM][FN]) {
 #pragma unroll
-    for (uint32_t ks = 0; ks < 2; ++ks) {
+    for (int ks = 0; ks < 2; ++ks) {
         vec16 a[FM], b[FN];
 #pragma unroll
-        for (int i = 0; i < FM; ++i) a[i] = A::frag(pa, m0, i, ks);
+        for (int i = 0; i < FM; ++i) a[i] = ra.get(pa, i, ks);
 #pragma unroll
-        for (int i = 0; i < FN; ++i) b[i] = B::frag(pb, n0, i, ks);
+        for (int i = 0; i < FN; ++i) b[i] = rb.get(pb, i, ks);
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -231,25 +249,25 @@ __device__ __forceinline__ void multiply(const uint8_t *pa, const uint8_t *pb, u
 template <int DT, int FM, int FN, class A, class B, class Acc>
 __device__ __forceinline__ void tile_product(const A &a, const B &b, uint32_t slabs, uint32_t m0, uint32_t n0, uint8_t *a0, uint8_t *a1,
                                              uint8_t *b0, uint8_t *b1, Acc (&acc)[FM][FN]) {
+    const typename A::Reader ra(m0);
+    const typename B::Reader rb(n0);
     if (slabs) {
         a.stage(a0, 0);
         b.stage(b0, 0);
     }
-    for (uint32_t k = 0; k < slabs; k += 2) {
+    // One way in and out of the loop: the accumulators stay where they are.  Past the last slab zeros are brought.
+    for (uint32_t k = 0; k + 1 < slabs; k += 2) {
         __syncthreads();
-        if (k + 1 < slabs) {
-            a.stage(a1, k + 1);
-            b.stage(b1, k + 1);
-        }
-        multiply<DT, FM, FN, A, B>(a0, b0, m0, n0, acc);
-        if (k + 1 >= slabs) break;
+        a.stage(a1, k + 1);
+        b.stage(b1, k + 1);
+        multiply<DT, FM, FN, A, B>(a0, b0, ra, rb, acc);
         __syncthreads();
-        if (k + 2 < slabs) {
-            a.stage(a0, k + 2);
-            b.stage(b0, k + 2);
-        }
-        multiply<DT, FM, FN, A, B>(a1, b1, m0, n0, acc);
+        a.stage(a0, k + 2);
+        b.stage(b0, k + 2);
+        multiply<DT, FM, FN, A, B>(a1, b1, ra, rb, acc);
     }
+    __syncthreads();
+    if (slabs & 1) multiply<DT, FM, FN, A, B>(a0, b0, ra, rb, acc);
 }
 
 // Workgroups to tiles: consecutive workgroups go to the eight XCDs in turn, each
