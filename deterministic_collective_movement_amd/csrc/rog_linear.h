@@ -13,13 +13,14 @@
 
 namespace rog {
 
-// How a product is cut.  A slab is 128 bytes of K (64 elements of two bytes, 128
-// of one): a matrix instruction takes half a slab of 16 rows.  A leaf is 32
+// How a product is cut.  A step is 64 bytes of K (32 elements of two bytes, 64 of
+// one), what a matrix instruction takes of 16 rows.  A leaf is 32
 // consecutive columns of one shard, a block four leaves.  Every logit is one
-// chain of matrix instructions over the slabs in rising order, whatever the
+// chain of matrix instructions over the steps in rising order, whatever the
 // tile, so its bits do not depend on how many rows a call has; the statistics
 // of a row are joined leaf by leaf over one tree (rog_linear_device.h).
-constexpr uint32_t kSlabBytes = 128;
+constexpr uint32_t kStepBytes = 64;
+constexpr uint32_t kPackUnit = 128;        // bytes of a packed row are a multiple of these, a line
 constexpr uint32_t kLeaf = 32;
 constexpr uint32_t kLinearBlock = 128;
 constexpr uint64_t kMaxLinearStride = uint64_t(1) << 22;   // bytes from a row to the next: tiles are addressed in 32 bits
@@ -73,13 +74,13 @@ struct JoinArgs {
     float scale;
 };
 
-// Packs the rows that are scored, one after the other, K padded with zeros to whole slabs.
+// Packs the rows that are scored, one after the other, K padded with zeros to whole lines.
 struct PackArgs {
     const void *x;
     int64_t stride;
     const int64_t *tokens;
     uint32_t rows, kbytes;             // bytes of a caller's row
-    uint32_t packed_bytes;             // of a packed one, a multiple of a slab
+    uint32_t packed_bytes;             // of a packed one
     uint32_t *index, *count;
     void *packed;
     float *logp, *entropy, *lse;       // zeroed where the row is not scored
@@ -96,7 +97,8 @@ struct GradArgs {
     const uint32_t *index;
     const float *lse, *entropy, *g_logp, *g_entropy, *g_scale;
     float inv_t;
-    void *g;                           // [rows][g_stride / 2] coefficients of the piece's columns
+    void *g, *g_all;                   // [rows][g_stride / 2] coefficients of the piece's columns; binary16: by the rows' own
+                                       // scales, and by that of all (else one array)
     int64_t g_stride;                  // bytes
     uint32_t tile_begin;               // the piece's first tile
     uint32_t tiles;                    // and how many it has
@@ -107,8 +109,9 @@ struct GradArgs {
 struct BackArgs {
     LinearRows a;                      // packed
     const uint32_t *index;
-    const float *g_scale;
-    const void *g;
+    const float *g_logp, *g_entropy, *g_scale;
+    float inv_t;
+    const void *g, *g_all;
     int64_t g_stride;
     uint32_t tile_begin, tiles;
     uint32_t seg_begin, segs;          // segments of the piece
@@ -132,7 +135,8 @@ struct BackJoinArgs {
     uint64_t part_seg;
     uint32_t segs, dim_pad, dim;
     const uint32_t *index, *count;
-    const float *g_scale;
+    const float *g_logp, *g_entropy;
+    float inv_t;
     uint32_t rows;
     void *d_hidden;
     int64_t d_stride;

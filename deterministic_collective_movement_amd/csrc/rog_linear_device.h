@@ -83,75 +83,75 @@ __device__ __forceinline__ vec16 row_bytes(gbyte *row, uint32_t at, uint32_t end
 // Operands that come as rows along K
 // ---------------------------------------------------------------------------
 
-// A slab of ROWS rows of 128 bytes.  The eight 16-byte units of a row stand in
-// the order u ^ swizzle(row), so that the sixteen rows of a fragment read at one
-// unit fall on different banks: M's fragments take the rows 8 a + b (a, b < 4) of
-// 32 (or four on), N's sixteen consecutive ones.
+// A step of ROWS rows of 64 bytes.  The four 16-byte units of a row stand at
+// u ^ swizzle(row), so that the sixteen rows of a fragment read at one unit fall
+// on different banks (four rows are 256 bytes, all of them): M's fragments take
+// the rows 8 a + b (a, b < 4) of 32 (or four on), N's sixteen consecutive ones.
 template <bool M_SIDE>
 __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-    return M_SIDE ? (row >> 1 & 1) | (row >> 3 & 3) << 1 : row >> 1 & 7;
-}
-// The row that lane l holds of fragment f.
-template <bool M_SIDE>
-__device__ __forceinline__ uint32_t frag_row(uint32_t f, uint32_t l16) {
-    return M_SIDE ? 32 * (f / 2) + 8 * (l16 / 4) + 4 * (f & 1) + l16 % 4 : 16 * f + l16;
+    return row >> (M_SIDE ? 3 : 2) & 3;
 }
 
 template <bool M_SIDE, int ROWS, int THREADS, bool DIRECT, int ES>
-struct RowSlab {
-    static constexpr int kBytes = ROWS * int(kSlabBytes);
-    static constexpr int kLoads = ROWS * 8 / THREADS;
-    static_assert(ROWS * 8 % THREADS == 0, "whole waves");
+struct RowSteps {
+    static constexpr int kBytes = ROWS * int(kStepBytes);
+    static constexpr int kRows = THREADS / 4;            // rows of one load of the workgroup
+    static constexpr int kLoads = ROWS / kRows;
+    static constexpr int kReads = 1;                     // shared memory instructions of a fragment
+    static_assert(ROWS % kRows == 0 && kRows % 32 == 0, "whole waves, one swizzle for all of a lane's rows");
     const uint8_t *base;
     uint64_t rows_bytes;               // of the rows that there are
     uint32_t kbytes;
     int64_t stride;
-    uint32_t voff;                     // the lane's first unit
-    uint32_t unit;                     // its place in the slab's rows, in bytes
+    uint32_t voff[kLoads];             // the lane's units
+    uint32_t unit;                     // their place in the rows, in bytes
     // rows_left: rows from `base` on that exist
-    __device__ __forceinline__ RowSlab(const void *b, int64_t s, uint32_t rows_left, uint32_t kb)
+    __device__ __forceinline__ RowSteps(const void *b, int64_t s, uint32_t rows_left, uint32_t kb)
         : base(static_cast<const uint8_t *>(b)), rows_bytes(uint64_t(rows_left) * uint64_t(s)), kbytes(kb), stride(s) {
-        const uint32_t row = threadIdx.x / 8;
-        unit = (threadIdx.x % 8 ^ swizzle<M_SIDE>(row)) * 16;
-        voff = row * uint32_t(s) + unit;
+        const uint32_t row = threadIdx.x / 4;
+        unit = (threadIdx.x % 4 ^ swizzle<M_SIDE>(row)) * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) voff[i] = (row + i * kRows) * uint32_t(s) + unit;
     }
-    // Slab `k` to `to`.  Rows 8 * kWave apart have the same swizzle where THREADS / 8 is a multiple of 32.
+    // Brings step k to `to`, zeros past the rows.  Steps that are not whole are brought with TAIL, zeros past K.
+    template <bool TAIL>
     __device__ __forceinline__ void stage(uint8_t *to, uint32_t k) const {
-        static_assert(THREADS / 8 % 32 == 0, "one swizzle for all of a lane's rows");
-        const uint32_t at = k * kSlabBytes;
         if constexpr (DIRECT) {
+            // past the last whole step: that one again, which nobody reads
+            const uint32_t whole = kbytes / kStepBytes, at = (TAIL || k < whole ? k : whole ? whole - 1 : 0) * kStepBytes;
             const auto r = window(base, rows_bytes);
-            uint32_t v = voff;
-            if (at + kSlabBytes > kbytes && at + unit >= kbytes) v = kOutside;
+            const bool inside = !TAIL || at + unit < kbytes;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                lbyte *p = (lbyte *)to + (i * THREADS + threadIdx.x / 64 * 64) * 16;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16,
-                                                         v == kOutside ? v : v + uint32_t(i) * (THREADS / 8) * uint32_t(stride), at, 0, 0);
+                lbyte *p = (lbyte *)to + (i * THREADS + uniform(threadIdx.x / 64) * 64) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16, inside ? voff[i] : kOutside, at, 0, 0);
             }
         } else {
+            const uint32_t at = k * kStepBytes;
             vec16 v[kLoads];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const uint64_t off = uint64_t(threadIdx.x / 8 + i * (THREADS / 8)) * uint64_t(stride);
+                const uint64_t off = uint64_t(threadIdx.x / 4 + i * kRows) * uint64_t(stride);
                 v[i] = off < rows_bytes ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes) : vec16{0, 0, 0, 0};
             }
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
         }
     }
-    // Reads fragments of a wave's rows from row0 (a multiple of 32) on: f and the half slab ks are constants,
-    // so that a fragment's address is one of two registers and an offset in the instruction.
+    // Reads fragments of a wave's rows from row0 (a multiple of 32) on: f is a constant, so that
+    // a fragment's address is one register and an offset in the instruction.  The offset has 16
+    // bits: HIGH is added to the register for arrays that lie beyond.
+    template <uint32_t HIGH>
     struct Reader {
-        uint32_t at[2];
+        uint32_t at;
         __device__ __forceinline__ explicit Reader(uint32_t row0) {
-            const uint32_t l = threadIdx.x % 64, row = frag_row<M_SIDE>(0, l % 16);
-            at[0] = (row0 + row) * kSlabBytes + (l / 16 ^ swizzle<M_SIDE>(row)) * 16;
-            at[1] = at[0] ^ 64;
+            const uint32_t l = threadIdx.x % 64, j = l % 16, row = M_SIDE ? 8 * (j / 4) + j % 4 : j;
+            at = (row0 + row) * kStepBytes + (l / 16 ^ swizzle<M_SIDE>(row)) * 16 + HIGH;
+            asm("" : "+v"(at));
         }
-        __device__ __forceinline__ vec16 get(const uint8_t *from, int f, int ks) const {
+        __device__ __forceinline__ vec16 get(const uint8_t *from, int f) const {
             const int row = M_SIDE ? 32 * (f / 2) + 4 * (f & 1) : 16 * f;
-            return *(const lvec16 *)((const lbyte *)from + at[ks] + row * int(kSlabBytes));
+            return *(const lvec16 *)((const lbyte *)from + (int(at) + row * int(kStepBytes) - int(HIGH)));
         }
     };
 };
@@ -160,38 +160,41 @@ struct RowSlab {
 // Operands that come as K along rows (two-byte elements)
 // ---------------------------------------------------------------------------
 
-// A slab of 64 rows of K, COLS elements each, in units of 16 bytes at
+// A step of 32 rows of K, COLS elements each, in units of 16 bytes at
 // u ^ 4 (row % 4).  ds_read_b64_tr_b16 gives lane l of a quarter wave the column l
 // of four rows of sixteen elements: lane j of the quarter names the 8 bytes of
 // row j / 4 that hold its elements 4 (j % 4) and on.
 template <bool M_SIDE, int COLS, int THREADS, bool DIRECT>
-struct ColSlab {
-    static constexpr int kBytes = COLS * int(kSlabBytes);
+struct ColSteps {
+    static constexpr int kBytes = COLS * int(kStepBytes);
     static constexpr int kUnits = COLS / 8;              // of a row
-    static constexpr int kLoads = 64 * kUnits / THREADS;
+    static constexpr int kLoads = 32 * kUnits / THREADS;
     static constexpr int kRows = THREADS / kUnits;       // rows of one load of the workgroup
-    static_assert(kRows % 4 == 0, "one swizzle for all of a lane's rows");
+    static constexpr int kReads = 2;
+    static_assert(kRows % 4 == 0 && kLoads * THREADS == 32 * kUnits && kUnits >= 16, "one swizzle for all of a lane's rows");
     const uint8_t *base;
     uint32_t rows, col_bytes;          // rows of K, bytes of a row from `base` on
     int64_t stride;
     uint32_t row, unit;
-    __device__ __forceinline__ ColSlab(const void *b, int64_t s, uint32_t rows_, uint32_t cols_left)
+    uint32_t voff[kLoads];
+    __device__ __forceinline__ ColSteps(const void *b, int64_t s, uint32_t rows_, uint32_t cols_left)
         : base(static_cast<const uint8_t *>(b)), rows(rows_), col_bytes(cols_left * 2), stride(s) {
         row = threadIdx.x / kUnits;
         unit = (threadIdx.x % kUnits ^ 4 * (row % 4)) * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) voff[i] = unit < col_bytes ? (row + i * kRows) * uint32_t(s) + unit : kOutside;
     }
+    template <bool TAIL>
     __device__ __forceinline__ void stage(uint8_t *to, uint32_t k) const {
-        const uint32_t left = rows > k * 64 ? rows - k * 64 : 0;
-        const uint8_t *from = base + uint64_t(k) * 64 * uint64_t(stride);
+        const uint32_t left = rows > k * 32 ? rows - k * 32 : 0;
+        const uint8_t *from = base + uint64_t(k) * 32 * uint64_t(stride);
         if constexpr (DIRECT) {
-            // the last row ends with the columns that are read: nothing past it is in the window
-            const auto r = window(from, uint64_t(left < 64 ? left : 64) * uint64_t(stride));
-            const uint32_t v = unit < col_bytes ? row * uint32_t(stride) + unit : kOutside;
+            // a row past the last is past the window; in the last, nothing past the columns is read
+            const auto r = window(from, uint64_t(left < 32 ? left : 32) * uint64_t(stride));
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                lbyte *p = (lbyte *)to + (i * THREADS + threadIdx.x / 64 * 64) * 16;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16,
-                                                         v == kOutside ? v : v + uint32_t(i) * kRows * uint32_t(stride), 0, 0, 0);
+                lbyte *p = (lbyte *)to + (i * THREADS + uniform(threadIdx.x / 64) * 64) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16, voff[i], 0, 0, 0);
             }
         } else {
             vec16 v[kLoads];
@@ -205,18 +208,21 @@ struct ColSlab {
     }
     // Fragments of a wave's columns from col0 (a multiple of 64) on: the 64 bytes that hold fragments 2 i and
     // 2 i + 1 stand at i ^ (row % 4) of four.
+    template <uint32_t HIGH>
     struct Reader {
-        static constexpr int kAts = 4;
-        uint32_t at[kAts];
+        uint32_t at[4];
         __device__ __forceinline__ explicit Reader(uint32_t col0) {
             const uint32_t l = threadIdx.x % 64, j = l % 16, k = l / 16 * 8 + j / 4;
             const uint32_t in = M_SIDE ? 16 * (j % 4) : 8 * (j % 4);
 #pragma unroll
-            for (uint32_t i = 0; i < kAts; ++i) at[i] = k * (COLS * 2) + ((col0 / 32 + i) ^ j / 4) * 64 + in;
+            for (uint32_t i = 0; i < 4; ++i) {
+                at[i] = k * (COLS * 2) + ((col0 / 32 + i) ^ j / 4) * 64 + in + HIGH;
+                asm("" : "+v"(at[i]));
+            }
         }
-        __device__ __forceinline__ vec16 get(const uint8_t *from, int f, int ks) const {
-            const int off = ks * 32 * COLS * 2 + (f / 8) * 256 + (f & 1) * (M_SIDE ? 8 : 32);
-            const lbyte *p = (const lbyte *)from + at[f / 2 % kAts] + off;
+        __device__ __forceinline__ vec16 get(const uint8_t *from, int f) const {
+            const int off = (f / 8) * 256 + (f & 1) * (M_SIDE ? 8 : 32);
+            const lbyte *p = (const lbyte *)from + (int(at[f / 2 % 4]) + off - int(HIGH));
             struct { s16x4 lo, hi; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)p),
                                           __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)(p + 4 * COLS * 2))};
             return __builtin_bit_cast(vec16, v);
@@ -228,46 +234,124 @@ struct ColSlab {
 // A tile
 // ---------------------------------------------------------------------------
 
-// FM x FN fragments of a wave at (m0, n0) of the tile, over `slabs` slabs.
-template <int DT, int FM, int FN, class A, class B, class Acc>
-__device__ __forceinline__ void multiply(const uint8_t *pa, const uint8_t *pb, const typename A::Reader &ra, const typename B::Reader &rb,
-                                         Acc (&acc)[FM][FN]) {
+// Waits until at most LOADS loads of this wave are in flight and its shared memory accesses are done, then for the other waves.
+template <int LOADS>
+__device__ __forceinline__ void arrive() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((LOADS & 15) | 7 << 4 | (LOADS >> 4) << 14);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// The order of a step's instructions: loads to the shared memory and reads from it dealt among the matrix instructions.
+template <int N, int LOADS, int READS, int I>
+struct Deal {
+    static __device__ __forceinline__ void slot() {
+        constexpr int kMfma = 8, kVmem = 16, kLds = 256, kSlots = LOADS + READS;
+        constexpr int kCount = N * (I + 1) / kSlots - N * I / kSlots;
+        if constexpr (kCount > 0) __builtin_amdgcn_sched_group_barrier(kMfma, kCount, 0);
+        __builtin_amdgcn_sched_group_barrier(I * LOADS / kSlots != (I + 1) * LOADS / kSlots ? kVmem : kLds, 1, 0);
+        if constexpr (I + 1 < kSlots) Deal<N, LOADS, READS, I + 1>::slot();
+    }
+};
+
+constexpr int kStages = 4;
+
+// The shared memory of a tile: arrays of their own, so that the compiler can tell a
+// load in flight to one from a read of another (through one array it waits for all).
+#define ROG_TILE_MEMORY(A, B)                                                                                   \
+    __shared__ __attribute__((aligned(16))) uint8_t a0[A], a1[A], a2[A], a3[A], b0[B], b1[B], b2[B], b3[B];     \
+    const TileMemory memory = {{a0, a1, a2, a3}, {b0, b1, b2, b3}}
+struct TileMemory {
+    uint8_t *a[kStages], *b[kStages];
+};
+
+// FM x FN fragments of a wave at (m0, n0) of the tile, over `steps` whole steps of K and, if `tail`, a last one that is not.
+// While a step is multiplied from registers, the next one's fragments are read,
+// and up to three further steps are in flight to the shared memory: a step's
+// memory is free as soon as every wave has its fragments.
+template <int DT, int FM, int FN, class A, class B>
+struct Tile {
+    typedef typename Mat<DT>::Acc Acc;
+    vec16 fa[2][FM], fb[2][FN];
+
+    static constexpr uint32_t kHigh = A::kBytes * kStages >= 65536 ? 65536 : 0;
+    typedef typename A::template Reader<0> ReadA;
+    typedef typename B::template Reader<kHigh> ReadB;
+
+    __device__ __forceinline__ void read(const ReadA &ra, const ReadB &rb, const uint8_t *pa, const uint8_t *pb, int set) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-        vec16 a[FM], b[FN];
+        for (int i = 0; i < FM; ++i) fa[set][i] = ra.get(pa, i);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) a[i] = ra.get(pa, i, ks);
-#pragma unroll
-        for (int i = 0; i < FN; ++i) b[i] = rb.get(pb, i, ks);
+        for (int i = 0; i < FN; ++i) fb[set][i] = rb.get(pb, i);
+    }
+    __device__ __forceinline__ void multiply(int set, Acc (&acc)[FM][FN]) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = Mat<DT>::mma(a[i], b[j], acc[i][j]);
+            for (int j = 0; j < FN; ++j) acc[i][j] = Mat<DT>::mma(fa[set][i], fb[set][j], acc[i][j]);
     }
-}
+    __device__ __forceinline__ void run(const A &a, const B &b, uint32_t steps, bool tail, uint32_t m0, uint32_t n0, const TileMemory &mem,
+                                        Acc (&acc)[FM][FN]) {
+#if defined(__HIP_DEVICE_COMPILE__)   // the compiler's host pass loses some kernels' stubs over what is in here
+        constexpr int kEach = A::kLoads + B::kLoads;
+        const ReadA ra(m0);
+        const ReadB rb(n0);
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) {
+            a.template stage<false>(mem.a[i], i);
+            b.template stage<false>(mem.b[i], i);
+        }
+        arrive<3 * kEach>();
+        read(ra, rb, mem.a[0], mem.b[0], 0);
+        // One way in and out of the loop, so that the accumulators stay where they are.
+        for (uint32_t k = 0; k + 4 <= steps; k += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                arrive<2 * kEach>();
+                a.template stage<false>(mem.a[i], k + i + 4);
+                b.template stage<false>(mem.b[i], k + i + 4);
+                read(ra, rb, mem.a[(i + 1) % 4], mem.b[(i + 1) % 4], (i + 1) % 2);
+                multiply(i % 2, acc);
+                Deal<FM * FN, kEach, FM * A::kReads + FN * B::kReads, 0>::slot();
+            }
+        }
+        const uint32_t rest = steps % 4;
+        if (rest > 0) multiply(0, acc);
+        arrive<0>();
+        if (rest > 1) {
+            read(ra, rb, mem.a[1], mem.b[1], 1);
+            multiply(1, acc);
+        }
+        if (rest > 2) {
+            read(ra, rb, mem.a[2], mem.b[2], 0);
+            multiply(0, acc);
+        }
+        if (tail) {
+            a.template stage<true>(mem.a[3], steps);
+            b.template stage<true>(mem.b[3], steps);
+            arrive<0>();
+            read(ra, rb, mem.a[3], mem.b[3], 1);
+            multiply(1, acc);
+        }
+#else
+        (void)a, (void)b, (void)steps, (void)tail, (void)m0, (void)n0, (void)mem, (void)acc;
+#endif
+    }
+};
 
-template <int DT, int FM, int FN, class A, class B, class Acc>
-__device__ __forceinline__ void tile_product(const A &a, const B &b, uint32_t slabs, uint32_t m0, uint32_t n0, uint8_t *a0, uint8_t *a1,
-                                             uint8_t *b0, uint8_t *b1, Acc (&acc)[FM][FN]) {
-    const typename A::Reader ra(m0);
-    const typename B::Reader rb(n0);
-    if (slabs) {
-        a.stage(a0, 0);
-        b.stage(b0, 0);
-    }
-    // One way in and out of the loop: the accumulators stay where they are.  Past the last slab zeros are brought.
-    for (uint32_t k = 0; k + 1 < slabs; k += 2) {
-        __syncthreads();
-        a.stage(a1, k + 1);
-        b.stage(b1, k + 1);
-        multiply<DT, FM, FN, A, B>(a0, b0, ra, rb, acc);
-        __syncthreads();
-        a.stage(a0, k + 2);
-        b.stage(b0, k + 2);
-        multiply<DT, FM, FN, A, B>(a1, b1, ra, rb, acc);
-    }
-    __syncthreads();
-    if (slabs & 1) multiply<DT, FM, FN, A, B>(a0, b0, ra, rb, acc);
+// The power of two that brings `most` into [2^14, 2^15): binary16 holds coefficients of at most `most` after it.
+__device__ __forceinline__ float power_for(float most) {
+    int e = 0;
+    if (most > 0 && most < kInf) e = 14 - (int(f32_bits(most) >> 23) - 127);
+    e = e > 100 ? 100 : e < -100 ? -100 : e;
+    return __builtin_ldexpf(1.0f, e);
+}
+// The largest |G| that a row can have: p |log p| is at most 1 / e, p H at most log V < 21.5.
+__device__ __forceinline__ float most_of(float g, float gh, float inv_t) {
+    return (fabsf(g) + 22.0f * fabsf(gh)) * inv_t;
 }
 
 // Workgroups to tiles: consecutive workgroups go to the eight XCDs in turn, each

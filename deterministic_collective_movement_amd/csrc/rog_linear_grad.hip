@@ -17,18 +17,17 @@ namespace {
 
 #pragma clang fp contract(off)
 
-typedef __attribute__((address_space(1))) vec16 gvec16_out;
 typedef __attribute__((address_space(1))) f32x4 gf32x4_out;
 typedef __attribute__((address_space(1))) uint16_t gu16_out;
 
 // Eight outputs, rounded once, to `to` (the first `n` of them).
 template <int DT>
-__device__ __forceinline__ void put8(uint8_t *to, const float (&x)[8], uint32_t n, bool wide) {
+__device__ __forceinline__ void put8(uint8_t *to, const float (&x)[8], uint32_t n) {
     vec16 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(x + 2 * i);
-    if (wide && n >= 8) {
-        *(gvec16_out *)to = v;
+    if (n >= 8) {
+        *(gvec16any_out *)to = v;      // at any alignment
         return;
     }
 #pragma unroll
@@ -38,19 +37,24 @@ __device__ __forceinline__ void put8(uint8_t *to, const float (&x)[8], uint32_t 
 
 constexpr int kBM = 256;   // elements of the states and weights of a tile
 
+// What takes the scale of a row's coefficients off again.
+template <int DT, class Args>
+__device__ __forceinline__ float unscale(const Args &p, uint32_t row) {
+    if constexpr (DT != ROG_DTYPE_F16) return 1.0f;
+    else return 1.0f / power_for(most_of(p.g_logp[row], p.g_entropy ? p.g_entropy[row] : 0.0f, p.inv_t));
+}
+
 template <int DT, int BN, int WM, int WN, bool DIRECT>
-__device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint32_t rows, uint8_t *a0, uint8_t *a1, uint8_t *b0, uint8_t *b1) {
+__device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint32_t rows, const TileMemory &memory) {
     constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
-    typedef ColSlab<true, kBM, THREADS, DIRECT> A;
-    typedef RowSlab<false, BN, THREADS, true, 2> B;
+    typedef ColSteps<true, kBM, THREADS, DIRECT> A;
+    typedef RowSteps<false, BN, THREADS, true, 2> B;
     const uint32_t tn = (rows + BN - 1) / BN, each = p.dim_tiles * tn;
     const bool running = p.part_seg == 0;              // one workgroup takes all segments of the piece, in their order
     const uint32_t in = id % each, d0 = in % p.dim_tiles * kBM, n0 = in / p.dim_tiles * BN;
     const uint32_t begin = running ? 0 : id / each, end = running ? p.segs : begin + 1;
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
-    const float inv = p.g_scale ? 1.0f / *p.g_scale : 1.0f;
-    const bool wide = ((uintptr_t(p.d_hidden) | uint64_t(p.d_stride)) & 15) == 0;
     for (uint32_t s = begin; s < end; ++s) {
         const uint32_t seg = p.seg_begin + s;
         uint32_t r = 0;
@@ -64,7 +68,7 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
                   p.seg_tiles * kGradTile * 2);
         f32x4 acc[FM][FN] = {};
         if (s != begin) __syncthreads();               // the last slab's readers
-        tile_product<DT, FM, FN>(a, b, (cols + 63) / 64, m0, w0, a0, a1, b0, b1, acc);
+        Tile<DT, FM, FN, A, B>().run(a, b, (cols + 31) / 32, false, m0, w0, memory, acc);
 
         const bool first = running && p.first && s == 0, last = running && p.last && s + 1 == p.segs;
         float *part = p.part + uint64_t(s) * p.part_seg;
@@ -72,7 +76,9 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
         for (int j = 0; j < FN; ++j) {
             const uint32_t n = n0 + w0 + 16 * j + l % 16;
             if (n >= rows) continue;
-            uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(p.index[n]) * uint64_t(p.d_stride);
+            const uint32_t row = p.index[n];
+            const float inv = last ? unscale<DT>(p, row) : 1.0f;
+            uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
 #pragma unroll
             for (int f = 0; f < FM / 2; ++f) {
                 const uint32_t d = d0 + m0 + 32 * f + l / 16 * 8;
@@ -89,7 +95,7 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
                 if (last) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] *= inv;
-                    put8<DT>(out + d * 2, x, p.dim - d, wide);
+                    put8<DT>(out + d * 2, x, p.dim - d);
                 } else {
                     at[0] = f32x4{x[0], x[1], x[2], x[3]};
                     at[1] = f32x4{x[4], x[5], x[6], x[7]};
@@ -100,24 +106,23 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
 }
 
 template <int DT, int BN, int WM, int WN>
-__device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uint32_t rows, uint8_t *a0, uint8_t *a1, uint8_t *b0, uint8_t *b1) {
+__device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uint32_t rows, const TileMemory &memory) {
     constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
-    typedef ColSlab<true, kBM, THREADS, true> A;
-    typedef ColSlab<false, BN, THREADS, true> B;
+    typedef ColSteps<true, kBM, THREADS, true> A;
+    typedef ColSteps<false, BN, THREADS, true> B;
     const TileAt at = tile_at(id, p.dim_tiles, p.tiles * (256 / BN));
     const uint32_t tile = p.tile_begin + at.n / (256 / BN), d0 = at.m * kBM;
     const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * 256 + at.n % (256 / BN) * BN;
     const uint32_t width = p.sh.s[r].width;
     if (v0 >= width) return;
     const A a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
-    const B b(static_cast<const uint8_t *>(p.g) + uint64_t(at.n) * BN * 2, p.g_stride, rows, BN);
+    const B b(static_cast<const uint8_t *>(p.g_all) + uint64_t(at.n) * BN * 2, p.g_stride, rows, BN);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     f32x4 acc[FM][FN] = {};
-    tile_product<DT, FM, FN>(a, b, (rows + 63) / 64, m0, w0, a0, a1, b0, b1, acc);
+    Tile<DT, FM, FN, A, B>().run(a, b, (rows + 31) / 32, false, m0, w0, memory, acc);
 
-    const float inv = p.g_scale ? 1.0f / *p.g_scale : 1.0f;
-    const bool wide = ((uintptr_t(p.dw[r]) | uint64_t(p.dw_stride[r])) & 15) == 0;
+    const float inv = DT == ROG_DTYPE_F16 ? 1.0f / *p.g_scale : 1.0f;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
         const uint32_t v = v0 + w0 + 16 * j + l % 16;
@@ -130,7 +135,7 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4] * inv;
-            put8<DT>(out + d * 2, x, p.dim - d, wide);
+            put8<DT>(out + d * 2, x, p.dim - d);
         }
     }
 }
@@ -139,14 +144,14 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
 template <int DT, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
     constexpr int BV = BN < 128 ? 128 : BN;
-    __shared__ __attribute__((aligned(16))) uint8_t a0[kBM * kSlabBytes], a1[kBM * kSlabBytes], b0[BV * kSlabBytes], b1[BV * kSlabBytes];
-    const uint32_t rows = *p.a.count, states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
+    ROG_TILE_MEMORY(kBM * kStepBytes, BV * kStepBytes);
+    const uint32_t rows = uniform(*p.a.count), states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
     if (blockIdx.x < states) {
-        back_states<DT, BN, WM, WN, DIRECT>(p, blockIdx.x, rows, a0, a1, b0, b1);
+        back_states<DT, BN, WM, WN, DIRECT>(p, blockIdx.x, rows, memory);
         return;
     }
     const uint32_t id = blockIdx.x - states;
-    if (id < p.dim_tiles * p.tiles * (256 / BV)) back_weights<DT, BV, WM, WN>(p, id, rows, a0, a1, b0, b1);
+    if (id < p.dim_tiles * p.tiles * (256 / BV)) back_weights<DT, BV, WM, WN>(p, id, rows, memory);
 }
 
 // Adds the segments' partial sums of a row in their order.
@@ -167,11 +172,12 @@ __global__ __launch_bounds__(256) void rog_linear_back_join_kernel(BackJoinArgs 
             x[i] = s ? x[i] + v : v;
         }
     }
-    const float inv = p.g_scale ? 1.0f / *p.g_scale : 1.0f;
+    const uint32_t row = p.index[n];
+    const float inv = unscale<DT>(p, row);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] *= inv;
-    uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(p.index[n]) * uint64_t(p.d_stride);
-    put8<DT>(out + d * 2, x, p.dim - d, ((uintptr_t(p.d_hidden) | uint64_t(p.d_stride)) & 15) == 0);
+    uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
+    put8<DT>(out + d * 2, x, p.dim - d);
 }
 
 template <class Args>

@@ -40,17 +40,16 @@ __global__ __launch_bounds__(kQuantThreads) void rog_quantize_kernel(QuantizeArg
 }
 
 template <int OT>
-__device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32_t n, bool wide) {
-    typedef __attribute__((address_space(1))) vec16 gvec16_out;
+__device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32_t n) {
     typedef __attribute__((address_space(1))) uint16_t gu16_out;
     typedef __attribute__((address_space(1))) float gf_out;
     if constexpr (OT == ROG_DTYPE_F32) {
-        if (wide && n >= 8) {
+        if (n >= 8) {
             vec16 v[2];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = f32_bits(x[i]);
-            ((gvec16_out *)to)[0] = v[0];
-            ((gvec16_out *)to)[1] = v[1];
+            ((gvec16any_out *)to)[0] = v[0];     // at any alignment
+            ((gvec16any_out *)to)[1] = v[1];
             return;
         }
 #pragma unroll
@@ -60,8 +59,8 @@ __device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32
         vec16 v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = narrow_word<OT>(x + 2 * i);
-        if (wide && n >= 8) {
-            *(gvec16_out *)to = v;
+        if (n >= 8) {
+            *(gvec16any_out *)to = v;
             return;
         }
 #pragma unroll
@@ -73,9 +72,9 @@ __device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32
 template <int OT, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_i8_kernel(LinearI8Args p) {
     constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
-    typedef RowSlab<true, BM, THREADS, DIRECT, 1> A;
-    typedef RowSlab<false, BN, THREADS, DIRECT, 1> B;
-    __shared__ __attribute__((aligned(16))) uint8_t a0[A::kBytes], a1[A::kBytes], b0[B::kBytes], b1[B::kBytes];
+    typedef RowSteps<true, BM, THREADS, DIRECT, 1> A;
+    typedef RowSteps<false, BN, THREADS, DIRECT, 1> B;
+    ROG_TILE_MEMORY(A::kBytes, B::kBytes);
     const uint32_t rows = p.a.rows, tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
     const TileAt at = tile_at(blockIdx.x, tm, tn);
     const uint32_t r = shard_of_tile(p.sh, at.m), v0 = (at.m - p.sh.tile0[r]) * BM, n0 = at.n * BN;
@@ -85,10 +84,9 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_i8_kernel(LinearI8Arg
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     i32x4 acc[FM][FN] = {};
-    tile_product<kTypeI8, FM, FN>(a, b, (p.a.kbytes + kSlabBytes - 1) / kSlabBytes, m0, w0, a0, a1, b0, b1, acc);
+    Tile<kTypeI8, FM, FN, A, B>().run(a, b, p.a.kbytes / kStepBytes, p.a.kbytes % kStepBytes != 0, m0, w0, memory, acc);
 
     constexpr uint32_t OS = Logit<OT>::kSize;
-    const bool wide = ((uintptr_t(p.out[r]) | uint64_t(p.out_stride[r])) & 15) == 0;
 #pragma unroll
     for (int f = 0; f < FM / 2; ++f) {
         const uint32_t v = v0 + m0 + 32 * f + l / 16 * 8;
@@ -105,7 +103,7 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_i8_kernel(LinearI8Arg
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = float(acc[2 * f + i / 4][j][i % 4]) * s * scale[i];
-            put_out<OT>(static_cast<uint8_t *>(p.out[r]) + uint64_t(n) * uint64_t(p.out_stride[r]) + uint64_t(v) * OS, x, left, wide);
+            put_out<OT>(static_cast<uint8_t *>(p.out[r]) + uint64_t(n) * uint64_t(p.out_stride[r]) + uint64_t(v) * OS, x, left);
         }
     }
 }

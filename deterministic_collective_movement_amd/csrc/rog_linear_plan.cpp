@@ -109,7 +109,7 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     p->form = form_of(rows);
     p->packs = has_tokens && rows >= kPackFrom;
     lay_tiles(&a.sh, tile_columns(p->form));
-    const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kSlabBytes);
+    const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
     if (!p->packs && !aligned(hidden, rows > 1 ? uint64_t(hidden_stride) * 2 : 0, kbytes)) p->direct = false;
     const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
@@ -182,7 +182,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false);
     if (st != ROG_OK) return st;
     lay_tiles(&a.sh, kGradTile);
-    const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kSlabBytes);
+    const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
     p->wide = rows > 64;
     const uint32_t bn = p->wide ? 256 : 64;
     k = BackArgs{};
@@ -228,7 +228,8 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
     const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), rows_at = w.take(rows * packed);
-    const uint64_t g = w.take(rows * uint64_t(most_tiles) * kGradTile * 2);
+    const uint64_t g_bytes = rows * uint64_t(most_tiles) * kGradTile * 2;
+    const uint64_t g = w.take(g_bytes), g_all = dtype == ROG_DTYPE_F16 ? w.take(g_bytes) : g;
     const uint64_t seg_floats = rows * uint64_t(k.dim_pad);
     const uint64_t part = w.take(seg_floats * 4 * (p->running ? 1 : segs));
     p->workspace_bytes = rows ? w.at : 0;
@@ -293,11 +294,16 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     a.g_scale = c.g_scale;
     a.inv_t = c.inv_t;
     a.g = in<void>(workspace, g);
+    a.g_all = in<void>(workspace, g_all);
     a.g_stride = int64_t(most_tiles) * kGradTile * 2;
     k.a = a.a;
     k.index = a.index;
+    k.g_logp = g_logp;
+    k.g_entropy = g_entropy;
     k.g_scale = a.g_scale;
+    k.inv_t = c.inv_t;
     k.g = a.g;
+    k.g_all = a.g_all;
     k.g_stride = a.g_stride;
     k.part = in<float>(workspace, part);
     k.part_seg = p->running ? 0 : seg_floats;
@@ -308,7 +314,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
         const uint64_t groups = ceil_div(rows * (k.dim_pad / 8), 256);
         if (groups >= uint64_t(1) << 24) return ROG_ERR_TOO_LARGE;
         p->join_grid = uint32_t(groups);
-        p->join = BackJoinArgs{k.part, k.part_seg, segs, k.dim_pad, k.dim, k.index, c.count, k.g_scale, uint32_t(rows), d_hidden, k.d_stride};
+        p->join = BackJoinArgs{k.part, k.part_seg, segs, k.dim_pad, k.dim, k.index, c.count, g_logp, g_entropy, c.inv_t, uint32_t(rows), d_hidden, k.d_stride};
     }
     a.tile_begin = a.tiles = k.seg_begin = k.segs = 0;
     return ROG_OK;

@@ -73,10 +73,10 @@ __device__ __forceinline__ void put_part(float *states, uint64_t at, const Part 
 template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_score_kernel(ScoreArgs p) {
     constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16, LEAVES = FM / 2;
-    typedef RowSlab<true, BM, THREADS, DIRECT, 2> A;
-    typedef RowSlab<false, BN, THREADS, DIRECT, 2> B;
-    __shared__ __attribute__((aligned(16))) uint8_t a0[A::kBytes], a1[A::kBytes], b0[B::kBytes], b1[B::kBytes];
-    const uint32_t rows = p.a.count ? *p.a.count : p.a.rows;
+    typedef RowSteps<true, BM, THREADS, DIRECT, 2> A;
+    typedef RowSteps<false, BN, THREADS, DIRECT, 2> B;
+    ROG_TILE_MEMORY(A::kBytes, B::kBytes);
+    const uint32_t rows = uniform(p.a.count ? *p.a.count : p.a.rows);
     const uint32_t tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
     if (blockIdx.x >= tm * tn) return;
     const TileAt at = tile_at(blockIdx.x, tm, tn);
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_score_kernel(ScoreArg
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     typename Mat<DT>::Acc acc[FM][FN] = {};
-    tile_product<DT, FM, FN>(a, b, (p.a.kbytes + kSlabBytes - 1) / kSlabBytes, m0, w0, a0, a1, b0, b1, acc);
+    Tile<DT, FM, FN, A, B>().run(a, b, p.a.kbytes / kStepBytes, p.a.kbytes % kStepBytes != 0, m0, w0, memory, acc);
 
     // lane l holds columns v0 + m0 + 32 f + 8 (l / 16) + 0 .. 7 of leaf f, row n0 + w0 + 16 j + l % 16
     const uint32_t first = v0 + m0 + l / 16 * 8;
@@ -224,32 +224,28 @@ __global__ __launch_bounds__(kPackThreads) void rog_linear_pack_kernel(PackArgs 
     }
     if (t == 0 && row0 + kPackRows >= p.rows) *p.count = before;
     if (!p.g_scale || blockIdx.x) return;
-    // the power of two that brings the largest coefficient there can be into [2^14, 2^15]
+    // one scale of all rows' coefficients, for the products that sum over rows
     float m = 0;
     for (uint32_t i = t; i < p.rows; i += kPackThreads)
         if (p.tokens[i] >= 0)
-            m = fmaxf(m, fabsf(p.g_logp[i]) + (p.g_entropy ? 22.0f * fabsf(p.g_entropy[i]) : 0.0f));
+            m = fmaxf(m, most_of(p.g_logp[i], p.g_entropy ? p.g_entropy[i] : 0.0f, p.inv_t));
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
     if (l == 0) most[wave] = m;
     __syncthreads();
     if (t == 0) {
         for (uint32_t i = 1; i < kPackThreads / 64; ++i) m = fmaxf(m, most[i]);
-        m *= p.inv_t;
-        int e = 0;
-        if (m > 0 && m < kInf) e = 14 - (int(f32_bits(m) >> 23) - 127);
-        e = e > 100 ? 100 : e < -100 ? -100 : e;
-        *p.g_scale = __builtin_ldexpf(1.0f, e);
+        *p.g_scale = power_for(m);
     }
 }
 
 template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_coef_kernel(GradArgs p) {
     constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16, LEAVES = FM / 2;
-    typedef RowSlab<true, BM, THREADS, DIRECT, 2> A;
-    typedef RowSlab<false, BN, THREADS, true, 2> B;
-    __shared__ __attribute__((aligned(16))) uint8_t a0[A::kBytes], a1[A::kBytes], b0[B::kBytes], b1[B::kBytes];
-    const uint32_t rows = *p.a.count, tm = p.tiles, tn = (rows + BN - 1) / BN;
+    typedef RowSteps<true, BM, THREADS, DIRECT, 2> A;
+    typedef RowSteps<false, BN, THREADS, true, 2> B;
+    ROG_TILE_MEMORY(A::kBytes, B::kBytes);
+    const uint32_t rows = uniform(*p.a.count), tm = p.tiles, tn = (rows + BN - 1) / BN;
     if (blockIdx.x >= tm * tn) return;
     TileAt at = tile_at(blockIdx.x, tm, tn);
     const uint32_t tile = p.tile_begin + at.m;
@@ -260,10 +256,10 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_coef_kernel(GradArgs 
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     typename Mat<DT>::Acc acc[FM][FN] = {};
-    tile_product<DT, FM, FN>(a, b, (p.a.kbytes + kSlabBytes - 1) / kSlabBytes, m0, w0, a0, a1, b0, b1, acc);
+    Tile<DT, FM, FN, A, B>().run(a, b, p.a.kbytes / kStepBytes, p.a.kbytes % kStepBytes != 0, m0, w0, memory, acc);
 
     constexpr float kLog2E = 1.44269504088896341f;
-    const float scale = p.inv_t * kLog2E, out = p.g_scale ? *p.g_scale * p.inv_t : p.inv_t;
+    const float scale = p.inv_t * kLog2E, all = DT == ROG_DTYPE_F16 ? *p.g_scale : 1.0f;
     const uint32_t first = v0 + m0 + l / 16 * 8;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -273,7 +269,11 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_coef_kernel(GradArgs 
         const int64_t tok = p.tokens[row];
         const int64_t own = tok - int64_t(sh.col0) - int64_t(first);
         const float lse = p.lse[row], h = p.entropy[row];
-        float g = p.g_logp[row] * out, gh = p.g_entropy ? p.g_entropy[row] * out : 0.0f;
+        float g = p.g_logp[row], gh = p.g_entropy ? p.g_entropy[row] : 0.0f;
+        // binary16: one copy by a scale of the row's own for d_hidden, one by that of all rows for d_weights
+        const float by = DT == ROG_DTYPE_F16 ? power_for(most_of(g, gh, p.inv_t)) : 1.0f, again = all / by;
+        g *= p.inv_t * by;
+        gh *= p.inv_t * by;
         if (tok >= int64_t(p.sh.vocab)) g = __builtin_nanf("");
         const bool empty = lse == -kInf;
         if (empty) g = gh = 0.0f;
@@ -294,7 +294,15 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_coef_kernel(GradArgs 
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(d + 2 * i);
             typedef __attribute__((address_space(1))) vec16 gvec16_out;
-            *(gvec16_out *)((uint8_t *)p.g + uint64_t(n) * uint64_t(p.g_stride) + (uint64_t(at.m) * BM + m0 + l / 16 * 8 + 32 * f) * 2) = v;
+            const uint64_t to = uint64_t(n) * uint64_t(p.g_stride) + (uint64_t(at.m) * BM + m0 + l / 16 * 8 + 32 * f) * 2;
+            *(gvec16_out *)((uint8_t *)p.g + to) = v;
+            if constexpr (DT == ROG_DTYPE_F16) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] *= again;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(d + 2 * i);
+                *(gvec16_out *)((uint8_t *)p.g_all + to) = v;
+            }
         }
     }
 }

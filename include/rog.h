@@ -590,8 +590,8 @@ ROG_API rog_status rog_linear_logprob_plan(const rog_weight_shard *shards, int W
  *
  * The logits are made anew, a piece of the vocabulary at a time.  G is rounded to
  * the states' type (binary16 after a power of two that puts the largest possible
- * |G| of the call at 2^14 to 2^15), the sums are binary32, and each output is
- * rounded once.  g_entropy may be NULL (0).
+ * |G| at 2^14 to 2^15: of the row for d_hidden, of the call for d_weight), the
+ * sums are binary32, and each output is rounded once.  g_entropy may be NULL (0).
  *
  * A row that is not scored gets zeros and its state is not used.  A token of V or
  * more, or a NaN in the row's inputs, makes the row's gradient and every weight's
