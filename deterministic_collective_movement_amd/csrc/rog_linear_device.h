@@ -11,6 +11,21 @@
 // rows of M for one column of N, and fragments come in pairs whose rows are dealt
 // so that a lane holds eight consecutive outputs.
 #pragma once
+#ifndef ROG_G
+#define ROG_G 8
+#endif
+#ifndef ROG_WM
+#define ROG_WM 2
+#endif
+#ifndef ROG_WN
+#define ROG_WN 4
+#endif
+#ifndef ROG_DEAL
+#define ROG_DEAL 0
+#endif
+#ifndef ROG_PRIO
+#define ROG_PRIO 0
+#endif
 
 #include "rog_head_device.h"
 #include "rog_linear.h"
@@ -252,7 +267,7 @@ struct Deal {
         constexpr int kMfma = 8, kVmem = 16, kLds = 256, kSlots = LOADS + READS;
         constexpr int kCount = N * (I + 1) / kSlots - N * I / kSlots;
         if constexpr (kCount > 0) __builtin_amdgcn_sched_group_barrier(kMfma, kCount, 0);
-        __builtin_amdgcn_sched_group_barrier(I * LOADS / kSlots != (I + 1) * LOADS / kSlots ? kVmem : kLds, 1, 0);
+        __builtin_amdgcn_sched_group_barrier((ROG_DEAL == 1 ? I < LOADS : ROG_DEAL == 2 ? I >= READS : I * LOADS / kSlots != (I + 1) * LOADS / kSlots) ? kVmem : kLds, 1, 0);
         if constexpr (I + 1 < kSlots) Deal<N, LOADS, READS, I + 1>::slot();
     }
 };
@@ -314,7 +329,9 @@ struct Tile {
                 a.template stage<false>(mem.a[i], k + i + 4);
                 b.template stage<false>(mem.b[i], k + i + 4);
                 read(ra, rb, mem.a[(i + 1) % 4], mem.b[(i + 1) % 4], (i + 1) % 2);
+                if (ROG_PRIO) __builtin_amdgcn_s_setprio(1);
                 multiply(i % 2, acc);
+                if (ROG_PRIO) __builtin_amdgcn_s_setprio(0);
                 Deal<FM * FN, kEach, FM * A::kReads + FN * B::kReads, 0>::slot();
             }
         }
@@ -362,7 +379,7 @@ struct TileAt {
     uint32_t m, n;
 };
 __device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tm, uint32_t tn) {
-    constexpr uint32_t kXcds = 8, kGroup = 4;
+    constexpr uint32_t kXcds = 8, kGroup = ROG_G;
     const uint32_t all = tm * tn, per = all / kXcds, more = all % kXcds;
     const uint32_t x = id % kXcds, t = x * per + (x < more ? x : more) + id / kXcds;
     const uint32_t group = t / (kGroup * tn), in = t % (kGroup * tn);

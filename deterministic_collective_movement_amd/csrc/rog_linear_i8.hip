@@ -117,7 +117,7 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
 template <int OT, bool DIRECT>
 hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
     switch (p.form) {
-    case kTileWide: return launch(rog_linear_i8_kernel<OT, 256, 256, 2, 4, DIRECT>, p.grid, 512, p.args, s);
+    case kTileWide: return launch(rog_linear_i8_kernel<OT, 256, 256, ROG_WM, ROG_WN, DIRECT>, p.grid, 64 * ROG_WM * ROG_WN, p.args, s);
     case kTileMid: return launch(rog_linear_i8_kernel<OT, 128, 128, 2, 2, DIRECT>, p.grid, 256, p.args, s);
     default: return launch(rog_linear_i8_kernel<OT, 128, 64, 4, 1, DIRECT>, p.grid, 256, p.args, s);
     }

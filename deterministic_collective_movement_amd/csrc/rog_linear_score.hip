@@ -322,7 +322,7 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
 template <int DT, bool DIRECT>
 hipError_t launch_score(const ScorePlan &p, hipStream_t s) {
     switch (p.form) {
-    case kTileWide: return launch(rog_linear_score_kernel<DT, 256, 256, 2, 4, DIRECT>, p.grid, 512, p.args, s);
+    case kTileWide: return launch(rog_linear_score_kernel<DT, 256, 256, ROG_WM, ROG_WN, DIRECT>, p.grid, 64 * ROG_WM * ROG_WN, p.args, s);
     case kTileMid: return launch(rog_linear_score_kernel<DT, 128, 128, 2, 2, DIRECT>, p.grid, 256, p.args, s);
     default: return launch(rog_linear_score_kernel<DT, 128, 64, 4, 1, DIRECT>, p.grid, 256, p.args, s);
     }
@@ -330,7 +330,7 @@ hipError_t launch_score(const ScorePlan &p, hipStream_t s) {
 
 template <int DT, bool DIRECT>
 hipError_t launch_coef(const GradPlan &p, const GradArgs &a, uint32_t grid, hipStream_t s) {
-    if (p.wide) return launch(rog_linear_coef_kernel<DT, 256, 256, 2, 4, DIRECT>, grid, 512, a, s);
+    if (p.wide) return launch(rog_linear_coef_kernel<DT, 256, 256, ROG_WM, ROG_WN, DIRECT>, grid, 64 * ROG_WM * ROG_WN, a, s);
     return launch(rog_linear_coef_kernel<DT, 256, 64, 4, 1, DIRECT>, grid, 256, a, s);
 }
 
