@@ -69,8 +69,20 @@ struct Mat<kTypeI8> {
     }
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void *base, uint64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(bytes < 0x7fffffffu ? bytes : 0x7fffffffu), kBufferWord3);
+// The same address in all lanes.
+__device__ __forceinline__ const uint8_t *uniform(const void *p) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return reinterpret_cast<const uint8_t *>(uintptr_t(uniform(uint32_t(b >> 32))) << 32 | uniform(uint32_t(b)));
+}
+// The thread's number, to derive anew from what would else be held in registers over a product.
+__device__ __forceinline__ uint32_t fresh_thread() {
+    uint32_t t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+// A window on [base, base + bytes), the same for all lanes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const uint8_t *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(uniform(base)), 0, int(uniform(bytes)), kBufferWord3);
 }
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every window: reads as zero
 
@@ -98,13 +110,17 @@ __device__ __forceinline__ vec16 row_bytes(gbyte *row, uint32_t at, uint32_t end
 // Operands that come as rows along K
 // ---------------------------------------------------------------------------
 
-// A step of ROWS rows of 64 bytes.  The four 16-byte units of a row stand at
-// u ^ swizzle(row), so that the sixteen rows of a fragment read at one unit fall
-// on different banks (four rows are 256 bytes, all of them): M's fragments take
-// the rows 8 a + b (a, b < 4) of 32 (or four on), N's sixteen consecutive ones.
+// A step of ROWS rows of 64 bytes.  A 16-byte read of a wave goes in four rounds
+// of sixteen lanes, each of which can take all 256 bytes of the banks: lanes 0-3,
+// 12-15, 20-27; 4-11, 16-19, 28-31; and the same 32 on.  So the four 16-byte units
+// of a row stand at u ^ swizzle(row), which puts a round's lanes on sixteen different
+// places: N's fragments take sixteen consecutive rows, M's the rows 8 a + b (a, b < 4) of
+// 32 (or four on), lane 16 u + 4 a + b unit u.  (u ^ a instead: every read twice
+// as long, 8192 x 131072 x 4096 bf16 6.37 ms.)
 template <bool M_SIDE>
 __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-    return row >> (M_SIDE ? 3 : 2) & 3;
+    const uint32_t a = row >> (M_SIDE ? 3 : 2) & 3;
+    return ((a << 1 | a >> 1) & 3) ^ (a & 2);          // 0, 2, 3, 1
 }
 
 template <bool M_SIDE, int ROWS, int THREADS, bool DIRECT, int ES>
@@ -115,25 +131,33 @@ struct RowSteps {
     static constexpr int kReads = 1;                     // shared memory instructions of a fragment
     static_assert(ROWS % kRows == 0 && kRows % 32 == 0, "whole waves, one swizzle for all of a lane's rows");
     const uint8_t *base;
-    uint64_t rows_bytes;               // of the rows that there are
+    uint32_t rows_bytes;               // of the rows that there are (a tile's are below 2^30)
     uint32_t kbytes;
     int64_t stride;
     uint32_t voff[kLoads];             // the lane's units
     uint32_t unit;                     // their place in the rows, in bytes
+    uint32_t k = 0;                    // the next step
     // rows_left: rows from `base` on that exist
     __device__ __forceinline__ RowSteps(const void *b, int64_t s, uint32_t rows_left, uint32_t kb)
-        : base(static_cast<const uint8_t *>(b)), rows_bytes(uint64_t(rows_left) * uint64_t(s)), kbytes(kb), stride(s) {
+        : base(uniform(b)), rows_bytes(uniform((rows_left < ROWS ? rows_left : ROWS) * uint32_t(s))), kbytes(uniform(kb)), stride(s) {
         const uint32_t row = threadIdx.x / 4;
         unit = (threadIdx.x % 4 ^ swizzle<M_SIDE>(row)) * 16;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) voff[i] = (row + i * kRows) * uint32_t(s) + unit;
     }
-    // Brings step k to `to`, zeros past the rows.  Steps that are not whole are brought with TAIL, zeros past K.
+    // Brings the next step to `to`, zeros past the rows.
+    __device__ __forceinline__ void stage(uint8_t *to) {
+        // past the last whole step: that one again, which nobody reads
+        const uint32_t whole = kbytes / kStepBytes, last = whole ? whole - 1 : 0;
+        bring<false>(to, k < last ? k : last);
+        ++k;
+    }
+    // Brings the last step, which is not whole: zeros past K.
+    __device__ __forceinline__ void stage_tail(uint8_t *to) const { bring<true>(to, kbytes / kStepBytes); }
     template <bool TAIL>
-    __device__ __forceinline__ void stage(uint8_t *to, uint32_t k) const {
+    __device__ __forceinline__ void bring(uint8_t *to, uint32_t step) const {
+        const uint32_t at = step * kStepBytes;
         if constexpr (DIRECT) {
-            // past the last whole step: that one again, which nobody reads
-            const uint32_t whole = kbytes / kStepBytes, at = (TAIL || k < whole ? k : whole ? whole - 1 : 0) * kStepBytes;
             const auto r = window(base, rows_bytes);
             const bool inside = !TAIL || at + unit < kbytes;
 #pragma unroll
@@ -142,7 +166,6 @@ struct RowSteps {
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16, inside ? voff[i] : kOutside, at, 0, 0);
             }
         } else {
-            const uint32_t at = k * kStepBytes;
             vec16 v[kLoads];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -168,6 +191,7 @@ struct RowSteps {
             const int row = M_SIDE ? 32 * (f / 2) + 4 * (f & 1) : 16 * f;
             return *(const lvec16 *)((const lbyte *)from + (int(at) + row * int(kStepBytes) - int(HIGH)));
         }
+        __device__ __forceinline__ void refresh() {}
     };
 };
 
@@ -175,37 +199,41 @@ struct RowSteps {
 // Operands that come as K along rows (two-byte elements)
 // ---------------------------------------------------------------------------
 
-// A step of 32 rows of K, COLS elements each, in units of 16 bytes at
-// u ^ 4 (row % 4).  ds_read_b64_tr_b16 gives lane l of a quarter wave the column l
-// of four rows of sixteen elements: lane j of the quarter names the 8 bytes of
-// row j / 4 that hold its elements 4 (j % 4) and on.
-template <bool M_SIDE, int COLS, int THREADS, bool DIRECT>
+// A step of 32 rows of K, COLS elements each.  ds_read_b64_tr_b16 gives lane l of a
+// quarter wave the column l of four rows of sixteen elements: lane j of the
+// quarter names the 8 bytes of row j / 4 that hold its elements 4 (j % 4) and on.
+// Half a wave goes at once: rows 0-3 and 8-11 (or 16 on, or four on), 32 bytes
+// each, which stand at different places of the 256 bytes of the banks as the
+// 32-byte pieces p of a row are at p ^ (2 (row % 4) + (row / 8) % 2).
+template <int COLS, int THREADS, bool DIRECT>
 struct ColSteps {
     static constexpr int kBytes = COLS * int(kStepBytes);
-    static constexpr int kUnits = COLS / 8;              // of a row
+    static constexpr int kUnits = COLS / 8;              // 16-byte units of a row
     static constexpr int kLoads = 32 * kUnits / THREADS;
     static constexpr int kRows = THREADS / kUnits;       // rows of one load of the workgroup
     static constexpr int kReads = 2;
-    static_assert(kRows % 4 == 0 && kLoads * THREADS == 32 * kUnits && kUnits >= 16, "one swizzle for all of a lane's rows");
-    const uint8_t *base;
-    uint32_t rows, col_bytes;          // rows of K, bytes of a row from `base` on
+    static_assert(kRows % 16 == 0 || kRows == 8 || kRows == 4, "see `turn`");
+    static_assert(kLoads * THREADS == 32 * kUnits && kUnits >= 16, "whole loads of rows of 256 bytes and more");
+    const uint8_t *from;               // of the next step
+    uint32_t left, col_bytes;          // rows of K from there on, bytes of a row
     int64_t stride;
     uint32_t row, unit;
-    uint32_t voff[kLoads];
+    uint32_t voff[kLoads];             // the lane's units
+    static __device__ __forceinline__ uint32_t turn(uint32_t row) { return 4 * (row % 4) + 2 * (row / 8 % 2); }   // of units
     __device__ __forceinline__ ColSteps(const void *b, int64_t s, uint32_t rows_, uint32_t cols_left)
-        : base(static_cast<const uint8_t *>(b)), rows(rows_), col_bytes(cols_left * 2), stride(s) {
+        : from(uniform(b)), left(uniform(rows_)), col_bytes(cols_left * 2), stride(s) {
         row = threadIdx.x / kUnits;
-        unit = (threadIdx.x % kUnits ^ 4 * (row % 4)) * 16;
+        unit = threadIdx.x % kUnits;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) voff[i] = unit < col_bytes ? (row + i * kRows) * uint32_t(s) + unit : kOutside;
+        for (int i = 0; i < kLoads; ++i) voff[i] = at(i) < col_bytes ? (row + i * kRows) * uint32_t(s) + at(i) : kOutside;
     }
-    template <bool TAIL>
-    __device__ __forceinline__ void stage(uint8_t *to, uint32_t k) const {
-        const uint32_t left = rows > k * 32 ? rows - k * 32 : 0;
-        const uint8_t *from = base + uint64_t(k) * 32 * uint64_t(stride);
+    // The bytes of the lane's unit in row `row + i * kRows` of a step.
+    __device__ __forceinline__ uint32_t at(int i) const { return (unit ^ turn(row + uint32_t(i) * kRows)) * 16; }
+    // Brings the next step to `to`, zeros past the rows.
+    __device__ __forceinline__ void stage(uint8_t *to) {
         if constexpr (DIRECT) {
             // a row past the last is past the window; in the last, nothing past the columns is read
-            const auto r = window(from, uint64_t(left < 32 ? left : 32) * uint64_t(stride));
+            const auto r = window(from, (left < 32 ? left : 32) * uint32_t(stride));
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 lbyte *p = (lbyte *)to + (i * THREADS + uniform(threadIdx.x / 64) * 64) * 16;
@@ -215,35 +243,44 @@ struct ColSteps {
             vec16 v[kLoads];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                v[i] = row + i * kRows < left ? row_bytes<2>((gbyte *)from + uint64_t(row + i * kRows) * uint64_t(stride), unit, col_bytes)
+                v[i] = row + i * kRows < left ? row_bytes<2>((gbyte *)from + uint64_t(row + i * kRows) * uint64_t(stride), at(i), col_bytes)
                                               : vec16{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
         }
+        from += 32 * uint32_t(stride);
+        left = left > 32 ? left - 32 : 0;
     }
-    // Fragments of a wave's columns from col0 (a multiple of 64) on: the 64 bytes that hold fragments 2 i and
-    // 2 i + 1 stand at i ^ (row % 4) of four.
+    __device__ __forceinline__ void stage_tail(uint8_t *to) { stage(to); }   // K ends with a row
+    // Fragments (sixteen consecutive columns) of a wave's columns from col0 on, a multiple of its fragments' columns
+    // (4, 8 or more fragments): bits 5 to 7 of an address are the low ones of its fragment's number, turned.
     template <uint32_t HIGH>
     struct Reader {
-        uint32_t at[4];
+        uint32_t lane;                 // fragment 0
         __device__ __forceinline__ explicit Reader(uint32_t col0) {
             const uint32_t l = threadIdx.x % 64, j = l % 16, k = l / 16 * 8 + j / 4;
-            const uint32_t in = M_SIDE ? 16 * (j % 4) : 8 * (j % 4);
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-                at[i] = k * (COLS * 2) + ((col0 / 32 + i) ^ j / 4) * 64 + in + HIGH;
-                asm("" : "+v"(at[i]));
-            }
+            lane = k * (COLS * 2) + (col0 * 2 ^ turn(k) * 16) + 8 * (j % 4) + HIGH;
         }
         __device__ __forceinline__ vec16 get(const uint8_t *from, int f) const {
-            const int off = (f / 8) * 256 + (f & 1) * (M_SIDE ? 8 : 32);
-            const lbyte *p = (const lbyte *)from + (int(at[f / 2 % 4]) + off - int(HIGH));
+            const uint32_t at = (lane ^ f % 8 * 32) + f / 8 * 256;
+            const lbyte *p = (const lbyte *)from + (int(at) - int(HIGH));
             struct { s16x4 lo, hi; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)p),
                                           __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)(p + 4 * COLS * 2))};
             return __builtin_bit_cast(vec16, v);
         }
+        // The fragments' addresses are made anew in every step: kept, they take the registers that hold fragments.
+        __device__ __forceinline__ void refresh() { asm volatile("" : "+v"(lane)); }
     };
 };
+
+// Two fragments of sixteen consecutive rows of M each, a and b, in a lane of quarter q rows 4 q and on of each: has
+// the lane hold eight consecutive ones, from row 8 * eight_of(q) of the 32 on, in a and then b.
+__device__ __forceinline__ void pair_up(float &a, float &b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(f32_bits(a), f32_bits(b), false, false);
+    a = bits_f32(r[0]);
+    b = bits_f32(r[1]);
+}
+__device__ __forceinline__ uint32_t eight_of(uint32_t quarter) { return quarter / 2 + quarter % 2 * 2; }
 
 // ---------------------------------------------------------------------------
 // A tile
@@ -308,16 +345,16 @@ struct Tile {
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = Mat<DT>::mma(fa[set][i], fb[set][j], acc[i][j]);
     }
-    __device__ __forceinline__ void run(const A &a, const B &b, uint32_t steps, bool tail, uint32_t m0, uint32_t n0, const TileMemory &mem,
+    __device__ __forceinline__ void run(A &a, B &b, uint32_t steps, bool tail, uint32_t m0, uint32_t n0, const TileMemory &mem,
                                         Acc (&acc)[FM][FN]) {
 #if defined(__HIP_DEVICE_COMPILE__)   // the compiler's host pass loses some kernels' stubs over what is in here
         constexpr int kEach = A::kLoads + B::kLoads;
-        const ReadA ra(m0);
-        const ReadB rb(n0);
+        ReadA ra(m0);
+        ReadB rb(n0);
 #pragma unroll
         for (int i = 0; i < kStages; ++i) {
-            a.template stage<false>(mem.a[i], i);
-            b.template stage<false>(mem.b[i], i);
+            a.stage(mem.a[i]);
+            b.stage(mem.b[i]);
         }
         arrive<3 * kEach>();
         read(ra, rb, mem.a[0], mem.b[0], 0);
@@ -326,8 +363,10 @@ struct Tile {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 arrive<2 * kEach>();
-                a.template stage<false>(mem.a[i], k + i + 4);
-                b.template stage<false>(mem.b[i], k + i + 4);
+                a.stage(mem.a[i]);
+                b.stage(mem.b[i]);
+                ra.refresh();
+                rb.refresh();
                 read(ra, rb, mem.a[(i + 1) % 4], mem.b[(i + 1) % 4], (i + 1) % 2);
                 if (ROG_PRIO) __builtin_amdgcn_s_setprio(1);
                 multiply(i % 2, acc);
@@ -347,8 +386,8 @@ struct Tile {
             multiply(0, acc);
         }
         if (tail) {
-            a.template stage<true>(mem.a[3], steps);
-            b.template stage<true>(mem.b[3], steps);
+            a.stage_tail(mem.a[3]);
+            b.stage_tail(mem.b[3]);
             arrive<0>();
             read(ra, rb, mem.a[3], mem.b[3], 1);
             multiply(1, acc);

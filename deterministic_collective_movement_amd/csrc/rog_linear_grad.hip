@@ -35,6 +35,21 @@ __device__ __forceinline__ void put8(uint8_t *to, const float (&x)[8], uint32_t 
         if (i < n) ((gu16_out *)to)[i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
 }
 
+template <int FM, int FN>
+__device__ __forceinline__ void pair_all(f32x4 (&acc)[FM][FN]) {
+#pragma unroll
+    for (int f = 0; f < FM; f += 2)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float a = acc[f][j][i], b = acc[f + 1][j][i];
+                pair_up(a, b);
+                acc[f][j][i] = a;
+                acc[f + 1][j][i] = b;
+            }
+}
+
 constexpr int kBM = 256;   // elements of the states and weights of a tile
 
 // What takes the scale of a row's coefficients off again.
@@ -47,14 +62,12 @@ __device__ __forceinline__ float unscale(const Args &p, uint32_t row) {
 template <int DT, int BN, int WM, int WN, bool DIRECT>
 __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint32_t rows, const TileMemory &memory) {
     constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
-    typedef ColSteps<true, kBM, THREADS, DIRECT> A;
+    typedef ColSteps<kBM, THREADS, DIRECT> A;
     typedef RowSteps<false, BN, THREADS, true, 2> B;
     const uint32_t tn = (rows + BN - 1) / BN, each = p.dim_tiles * tn;
     const bool running = p.part_seg == 0;              // one workgroup takes all segments of the piece, in their order
     const uint32_t in = id % each, d0 = in % p.dim_tiles * kBM, n0 = in / p.dim_tiles * BN;
     const uint32_t begin = running ? 0 : id / each, end = running ? p.segs : begin + 1;
-    const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
-    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     for (uint32_t s = begin; s < end; ++s) {
         const uint32_t seg = p.seg_begin + s;
         uint32_t r = 0;
@@ -63,13 +76,16 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
         const uint32_t tile = (seg - p.seg0[r]) * p.seg_tiles, v0 = tile * kGradTile;
         const uint32_t cols = sh.width - v0 < p.seg_tiles * kGradTile ? sh.width - v0 : p.seg_tiles * kGradTile;
         const uint64_t g_col = uint64_t(p.sh.tile0[r] + tile - p.tile_begin) * kGradTile * 2;
-        const A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride) + d0 * 2, sh.stride, cols, p.dim - d0);
-        const B b(static_cast<const uint8_t *>(p.g) + uint64_t(n0) * uint64_t(p.g_stride) + g_col, p.g_stride, rows - n0,
+        A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride) + d0 * 2, sh.stride, cols, p.dim - d0);
+        B b(static_cast<const uint8_t *>(p.g) + uint64_t(n0) * uint64_t(p.g_stride) + g_col, p.g_stride, rows - n0,
                   p.seg_tiles * kGradTile * 2);
         f32x4 acc[FM][FN] = {};
+        const uint32_t wave = fresh_thread() / 64;
         if (s != begin) __syncthreads();               // the last slab's readers
-        Tile<DT, FM, FN, A, B>().run(a, b, (cols + 31) / 32, false, m0, w0, memory, acc);
+        Tile<DT, FM, FN, A, B>().run(a, b, (cols + 31) / 32, false, wave / WN * (FM * 16), wave % WN * (FN * 16), memory, acc);
 
+        pair_all(acc);
+        const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
         const bool first = running && p.first && s == 0, last = running && p.last && s + 1 == p.segs;
         float *part = p.part + uint64_t(s) * p.part_seg;
 #pragma unroll
@@ -81,7 +97,7 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
             uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
 #pragma unroll
             for (int f = 0; f < FM / 2; ++f) {
-                const uint32_t d = d0 + m0 + 32 * f + l / 16 * 8;
+                const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
                 if (d >= p.dim) continue;
                 float x[8];
 #pragma unroll
@@ -108,20 +124,21 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
 template <int DT, int BN, int WM, int WN>
 __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uint32_t rows, const TileMemory &memory) {
     constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
-    typedef ColSteps<true, kBM, THREADS, true> A;
-    typedef ColSteps<false, BN, THREADS, true> B;
+    typedef ColSteps<kBM, THREADS, true> A;
+    typedef ColSteps<BN, THREADS, true> B;
     const TileAt at = tile_at(id, p.dim_tiles, p.tiles * (256 / BN));
     const uint32_t tile = p.tile_begin + at.n / (256 / BN), d0 = at.m * kBM;
     const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * 256 + at.n % (256 / BN) * BN;
     const uint32_t width = p.sh.s[r].width;
     if (v0 >= width) return;
-    const A a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
-    const B b(static_cast<const uint8_t *>(p.g_all) + uint64_t(at.n) * BN * 2, p.g_stride, rows, BN);
+    A a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
+    B b(static_cast<const uint8_t *>(p.g_all) + uint64_t(at.n) * BN * 2, p.g_stride, rows, BN);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     f32x4 acc[FM][FN] = {};
     Tile<DT, FM, FN, A, B>().run(a, b, (rows + 31) / 32, false, m0, w0, memory, acc);
 
+    pair_all(acc);
     const float inv = DT == ROG_DTYPE_F16 ? 1.0f / *p.g_scale : 1.0f;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -130,7 +147,7 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
         uint8_t *out = static_cast<uint8_t *>(p.dw[r]) + uint64_t(v) * uint64_t(p.dw_stride[r]);
 #pragma unroll
         for (int f = 0; f < FM / 2; ++f) {
-            const uint32_t d = d0 + m0 + 32 * f + l / 16 * 8;
+            const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
             if (d >= p.dim) continue;
             float x[8];
 #pragma unroll

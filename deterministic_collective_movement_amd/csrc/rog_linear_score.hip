@@ -82,8 +82,8 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_score_kernel(ScoreArg
     const TileAt at = tile_at(blockIdx.x, tm, tn);
     const uint32_t r = shard_of_tile(p.sh, at.m), v0 = (at.m - p.sh.tile0[r]) * BM, n0 = at.n * BN;
     const WeightShard sh = p.sh.s[r];
-    const A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
-    const B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
+    A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     typename Mat<DT>::Acc acc[FM][FN] = {};
@@ -251,8 +251,8 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_coef_kernel(GradArgs 
     const uint32_t tile = p.tile_begin + at.m;
     const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * BM, n0 = at.n * BN;
     const WeightShard sh = p.sh.s[r];
-    const A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
-    const B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, uint32_t(p.a.stride));
+    A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
     typename Mat<DT>::Acc acc[FM][FN] = {};
