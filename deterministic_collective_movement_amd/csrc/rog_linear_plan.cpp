@@ -17,6 +17,12 @@ constexpr double kLog2E = 1.4426950408889634;
 
 // Tunables, measured on MI355X; a variant build may override one with -D.
 // Bytes of the coefficients' piece of the vocabulary (one segment at least).
+// Bytes behind a row of coefficients, whose own are a multiple of 512: with rows 2^16 bytes apart a tile's
+// rows fall on few of the memory's channels (4096 rows of 65536 x 4096: 5.78 ms without, 5.24 with 256,
+// 5.29 / 5.51 / 5.32 with 128 / 512 / 1024).
+#ifndef ROG_LINEAR_ROW_PAD
+#define ROG_LINEAR_ROW_PAD 256
+#endif
 #ifndef ROG_LINEAR_PIECE_BYTES
 #define ROG_LINEAR_PIECE_BYTES (256ull << 20)
 #endif
@@ -188,7 +194,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     k = BackArgs{};
     k.sh = a.sh;
     k.dim = uint32_t(dim);
-    k.dim_pad = uint32_t(packed / 2);
+    k.dim_pad = uint32_t(up(uint64_t(dim), 64));
     k.dim_tiles = uint32_t(ceil_div(uint64_t(dim), 256));
     k.row_tiles = uint32_t(ceil_div(rows, bn));
     // Segments go by the width of the states alone, so that the sums' order does.
@@ -228,7 +234,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
     const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), rows_at = w.take(rows * packed);
-    const uint64_t g_bytes = rows * uint64_t(most_tiles) * kGradTile * 2;
+    const uint64_t g_row = uint64_t(most_tiles) * kGradTile * 2 + ROG_LINEAR_ROW_PAD, g_bytes = rows * g_row;
     const uint64_t g = w.take(g_bytes), g_all = dtype == ROG_DTYPE_F16 ? w.take(g_bytes) : g;
     const uint64_t seg_floats = rows * uint64_t(k.dim_pad);
     const uint64_t part = w.take(seg_floats * 4 * (p->running ? 1 : segs));
@@ -295,7 +301,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     a.inv_t = c.inv_t;
     a.g = in<void>(workspace, g);
     a.g_all = in<void>(workspace, g_all);
-    a.g_stride = int64_t(most_tiles) * kGradTile * 2;
+    a.g_stride = int64_t(g_row);
     k.a = a.a;
     k.index = a.index;
     k.g_logp = g_logp;
