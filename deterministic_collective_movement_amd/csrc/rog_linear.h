@@ -56,9 +56,8 @@ struct ScoreArgs {
     const uint32_t *index;             // packed rows: the caller's row (NULL: row i itself)
     float scale;                       // log2(e) / temperature
     float *target;                     // [rows] scaled logit of the row's token
-    float *states;                     // [units][rows_pad][4]: m, s, t
-    uint32_t rows_pad;
-    uint32_t unit_leaves;              // leaves of a unit: 1, 2 or 4
+    float *states;                     // m, s, t, 0 of a row's block at row * row_step + block * block_step, in fours
+    uint32_t row_step, block_step;
     WeightShards sh;
 };
 
@@ -68,9 +67,8 @@ struct JoinArgs {
     const uint32_t *index, *count;
     const float *target, *states;
     float *logp, *entropy, *lse;
-    uint32_t rows, rows_pad;
+    uint32_t rows, row_step, block_step;
     uint32_t vocab, blocks;
-    uint32_t unit_leaves;
     float scale;
 };
 
@@ -160,12 +158,22 @@ struct LinearI8Args {
     int64_t out_stride[kMaxPeers];     // bytes
 };
 
-// Tiles of a product: columns x rows.
-enum LinearForm {
-    kTileFew = 0,      // 128 x 64
-    kTileMid = 1,      // 128 x 128
-    kTileWide = 2,     // 256 x 256
+// Tiles of a product of weights and states: columns x rows of a workgroup, waves along each, stages of K in the
+// shared memory (kWide: steps of 64 bytes multiplied from registers, else lines of 128).
+template <int COLUMNS, int ROWS, int WM, int WN, int STAGES, bool WIDE>
+struct Form {
+    static constexpr int kColumns = COLUMNS, kRows = ROWS, kWM = WM, kWN = WN, kStages = STAGES, kThreads = 64 * WM * WN;
+    static constexpr int kFM = COLUMNS / WM / 16, kFN = ROWS / WN / 16;
+    static constexpr bool kWide = WIDE;
+    // waves that share a block of columns
+    static constexpr int kShare = COLUMNS / WM < int(kLinearBlock) ? int(kLinearBlock) / (COLUMNS / WM) : 1;
+    static_assert(COLUMNS % kLinearBlock == 0 && COLUMNS / WM % 32 == 0 && COLUMNS / WM <= int(kLinearBlock), "whole leaves, blocks");
 };
+typedef Form<128, 32, 4, 1, 4, false> FormFew;
+typedef Form<128, 64, 4, 1, 3, false> FormSome;
+typedef Form<128, 128, 2, 2, 4, true> FormMid;
+typedef Form<256, 256, 2, 4, 4, true> FormWide;
+enum { kFormFew = 0, kFormSome = 1, kFormMid = 2, kFormWide = 3 };
 
 struct ScorePlan {
     int32_t form;
@@ -182,7 +190,8 @@ constexpr uint32_t kGradTile = 256;
 
 struct GradPlan {
     rog_dtype dtype;
-    bool direct, wide, running;
+    int32_t form;                      // few, some or wide
+    bool direct, running;
     uint32_t pieces, piece_tiles;      // tiles of a piece: whole segments' or all
     PackArgs pack;
     GradArgs coef;

@@ -11,21 +11,6 @@
 // rows of M for one column of N, and fragments come in pairs whose rows are dealt
 // so that a lane holds eight consecutive outputs.
 #pragma once
-#ifndef ROG_G
-#define ROG_G 8
-#endif
-#ifndef ROG_WM
-#define ROG_WM 2
-#endif
-#ifndef ROG_WN
-#define ROG_WN 4
-#endif
-#ifndef ROG_DEAL
-#define ROG_DEAL 0
-#endif
-#ifndef ROG_PRIO
-#define ROG_PRIO 0
-#endif
 
 #include "rog_head_device.h"
 #include "rog_linear.h"
@@ -304,7 +289,7 @@ struct Deal {
         constexpr int kMfma = 8, kVmem = 16, kLds = 256, kSlots = LOADS + READS;
         constexpr int kCount = N * (I + 1) / kSlots - N * I / kSlots;
         if constexpr (kCount > 0) __builtin_amdgcn_sched_group_barrier(kMfma, kCount, 0);
-        __builtin_amdgcn_sched_group_barrier((ROG_DEAL == 1 ? I < LOADS : ROG_DEAL == 2 ? I >= READS : I * LOADS / kSlots != (I + 1) * LOADS / kSlots) ? kVmem : kLds, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(I * LOADS / kSlots != (I + 1) * LOADS / kSlots ? kVmem : kLds, 1, 0);
         if constexpr (I + 1 < kSlots) Deal<N, LOADS, READS, I + 1>::slot();
     }
 };
@@ -313,8 +298,9 @@ constexpr int kStages = 4;
 
 // The shared memory of a tile: arrays of their own, so that the compiler can tell a
 // load in flight to one from a read of another (through one array it waits for all).
-#define ROG_TILE_MEMORY(A, B)                                                                                   \
-    __shared__ __attribute__((aligned(16))) uint8_t a0[A], a1[A], a2[A], a3[A], b0[B], b1[B], b2[B], b3[B];     \
+#define ROG_TILE_MEMORY(STAGES, A, B)                                                                           \
+    __shared__ __attribute__((aligned(16))) uint8_t a0[A], a1[A], a2[A], b0[B], b1[B], b2[B];                   \
+    __shared__ __attribute__((aligned(16))) uint8_t a3[(STAGES) > 3 ? (A) : 16], b3[(STAGES) > 3 ? (B) : 16];   \
     const TileMemory memory = {{a0, a1, a2, a3}, {b0, b1, b2, b3}}
 struct TileMemory {
     uint8_t *a[kStages], *b[kStages];
@@ -368,9 +354,7 @@ struct Tile {
                 ra.refresh();
                 rb.refresh();
                 read(ra, rb, mem.a[(i + 1) % 4], mem.b[(i + 1) % 4], (i + 1) % 2);
-                if (ROG_PRIO) __builtin_amdgcn_s_setprio(1);
                 multiply(i % 2, acc);
-                if (ROG_PRIO) __builtin_amdgcn_s_setprio(0);
                 Deal<FM * FN, kEach, FM * A::kReads + FN * B::kReads, 0>::slot();
             }
         }
@@ -398,6 +382,124 @@ struct Tile {
     }
 };
 
+// ---------------------------------------------------------------------------
+// Tiles of few rows: bound by the weights' bytes
+// ---------------------------------------------------------------------------
+
+// A step of ROWS rows of 128 bytes, a line each.  Two rows are the 256 bytes of the
+// banks: the eight 16-byte units u of a row stand at u ^ turn(row), where a read's
+// rounds of sixteen lanes (see swizzle()) meet every place once.
+template <bool M_SIDE, int ROWS, int THREADS, bool DIRECT, int ES>
+struct RowLines {
+    static constexpr int kBytes = ROWS * 128;
+    static constexpr int kRows = THREADS / 8;
+    static constexpr int kLoads = ROWS / kRows;
+    static_assert(ROWS % kRows == 0, "whole waves");
+    static __device__ __forceinline__ uint32_t turn(uint32_t row) {
+        // the row's place among the sixteen of its fragment, halved
+        const uint32_t q = M_SIDE ? (row >> 1 & 1) | (row >> 3 & 3) << 1 : row >> 1 & 7;
+        return (q & 1) | (q >> 2 & 1) << 1 | ((q >> 1 ^ q >> 2) & 1) << 2;
+    }
+    const uint8_t *base;
+    uint32_t rows_bytes, kbytes;
+    int64_t stride;
+    uint32_t at = 0;                   // of the next step in the rows
+    __device__ __forceinline__ RowLines(const void *b, int64_t s, uint32_t rows_left, uint32_t kb)
+        : base(uniform(b)), rows_bytes(uniform((rows_left < ROWS ? rows_left : ROWS) * uint32_t(s))), kbytes(uniform(kb)), stride(s) {}
+    // Brings the next step to `to`, zeros past the rows and past K.
+    __device__ __forceinline__ void stage(uint8_t *to) {
+        const uint32_t row = threadIdx.x / 8;
+        if constexpr (DIRECT) {
+            const auto r = window(base, rows_bytes);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint32_t unit = (threadIdx.x % 8 ^ turn(row + i * kRows)) * 16;
+                const uint32_t v = at + unit < kbytes ? (row + i * kRows) * uint32_t(stride) + unit : kOutside;
+                lbyte *p = (lbyte *)to + (i * THREADS + uniform(threadIdx.x / 64) * 64) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16, v, at < kbytes ? at : 0, 0, 0);
+            }
+        } else {
+            vec16 v[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint32_t unit = (threadIdx.x % 8 ^ turn(row + i * kRows)) * 16, off = (row + i * kRows) * uint32_t(stride);
+                v[i] = off < rows_bytes ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes) : vec16{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
+        }
+        at += 128;
+    }
+    // Fragment f, half ks of the step, of a wave's rows from row0 (a multiple of 32) on.
+    static __device__ __forceinline__ vec16 get(const uint8_t *from, uint32_t row0, int f, int ks) {
+        const uint32_t l = threadIdx.x % 64, j = l % 16, row = M_SIDE ? 8 * (j / 4) + j % 4 : j;
+        const uint32_t first = (row0 + row) * 128 + ((ks * 4 + l / 16) ^ turn(row)) * 16;
+        return *(const lvec16 *)((const lbyte *)from + first + (M_SIDE ? 32 * (f / 2) + 4 * (f & 1) : 16 * f) * 128);
+    }
+};
+
+// FM x FN fragments of a wave at (m0, n0) over `lines` steps of 128 bytes of K, STAGES - 1 of them in flight.
+template <int DT, int FM, int FN, int STAGES, class A, class B>
+struct Stream {
+    typedef typename Mat<DT>::Acc Acc;
+    static __device__ __forceinline__ void run(A &a, B &b, uint32_t lines, uint32_t m0, uint32_t n0, const TileMemory &mem, Acc (&acc)[FM][FN]) {
+#if defined(__HIP_DEVICE_COMPILE__)   // as in Tile
+        constexpr int kEach = A::kLoads + B::kLoads;
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            a.stage(mem.a[i]);
+            b.stage(mem.b[i]);
+        }
+        // past the last step zeros are multiplied, which leaves the sums as they are
+        for (uint32_t k = 0; k < lines; k += STAGES) {
+#pragma unroll
+            for (int i = 0; i < STAGES; ++i) {
+                arrive<(STAGES - 2) * kEach>();
+                a.stage(mem.a[(i + STAGES - 1) % STAGES]);
+                b.stage(mem.b[(i + STAGES - 1) % STAGES]);
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    vec16 fa[FM], fb[FN];
+#pragma unroll
+                    for (int f = 0; f < FM; ++f) fa[f] = A::get(mem.a[i], m0, f, ks);
+#pragma unroll
+                    for (int f = 0; f < FN; ++f) fb[f] = B::get(mem.b[i], n0, f, ks);
+#pragma unroll
+                    for (int f = 0; f < FM; ++f)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) acc[f][j] = Mat<DT>::mma(fa[f], fb[j], acc[f][j]);
+                }
+            }
+        }
+        arrive<0>();
+#else
+        (void)a, (void)b, (void)lines, (void)m0, (void)n0, (void)mem, (void)acc;
+#endif
+    }
+};
+
+// A product of rows and rows (weights and states) in the form F.
+template <int DT, class F, bool DIRECT, int ES, bool WIDE>
+struct RowProduct;
+template <int DT, class F, bool DIRECT, int ES>
+struct RowProduct<DT, F, DIRECT, ES, true> {
+    typedef RowSteps<true, F::kColumns, F::kThreads, DIRECT, ES> A;
+    typedef RowSteps<false, F::kRows, F::kThreads, DIRECT, ES> B;
+    template <class Acc>
+    static __device__ __forceinline__ void run(A &a, B &b, uint32_t kbytes, uint32_t m0, uint32_t n0, const TileMemory &mem, Acc &acc) {
+        Tile<DT, F::kFM, F::kFN, A, B>().run(a, b, kbytes / kStepBytes, kbytes % kStepBytes != 0, m0, n0, mem, acc);
+    }
+};
+template <int DT, class F, bool DIRECT, int ES>
+struct RowProduct<DT, F, DIRECT, ES, false> {
+    typedef RowLines<true, F::kColumns, F::kThreads, DIRECT, ES> A;
+    typedef RowLines<false, F::kRows, F::kThreads, DIRECT, ES> B;
+    template <class Acc>
+    static __device__ __forceinline__ void run(A &a, B &b, uint32_t kbytes, uint32_t m0, uint32_t n0, const TileMemory &mem, Acc &acc) {
+        Stream<DT, F::kFM, F::kFN, F::kStages, A, B>::run(a, b, (kbytes + 127) / 128, m0, n0, mem, acc);
+    }
+};
+
 // The power of two that brings `most` into [2^14, 2^15): binary16 holds coefficients of at most `most` after it.
 __device__ __forceinline__ float power_for(float most) {
     int e = 0;
@@ -418,7 +520,7 @@ struct TileAt {
     uint32_t m, n;
 };
 __device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tm, uint32_t tn) {
-    constexpr uint32_t kXcds = 8, kGroup = ROG_G;
+    constexpr uint32_t kXcds = 8, kGroup = 8;
     const uint32_t all = tm * tn, per = all / kXcds, more = all % kXcds;
     const uint32_t x = id % kXcds, t = x * per + (x < more ? x : more) + id / kXcds;
     const uint32_t group = t / (kGroup * tn), in = t % (kGroup * tn);

@@ -161,7 +161,7 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
 template <int DT, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
     constexpr int BV = BN < 128 ? 128 : BN;
-    ROG_TILE_MEMORY(kBM * kStepBytes, BV * kStepBytes);
+    ROG_TILE_MEMORY(kStages, kBM * kStepBytes, BV * kStepBytes);
     const uint32_t rows = uniform(*p.a.count), states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
     if (blockIdx.x < states) {
         back_states<DT, BN, WM, WN, DIRECT>(p, blockIdx.x, rows, memory);
@@ -205,9 +205,9 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
 
 template <int DT>
 hipError_t launch_back(const GradPlan &p, const BackArgs &a, uint32_t grid, hipStream_t s) {
-    if (p.wide)
-        return p.direct ? launch(rog_linear_back_kernel<DT, 256, ROG_WM, ROG_WN, true>, grid, 64 * ROG_WM * ROG_WN, a, s)
-                        : launch(rog_linear_back_kernel<DT, 256, ROG_WM, ROG_WN, false>, grid, 64 * ROG_WM * ROG_WN, a, s);
+    if (p.form == kFormWide)
+        return p.direct ? launch(rog_linear_back_kernel<DT, 256, 2, 4, true>, grid, 512, a, s)
+                        : launch(rog_linear_back_kernel<DT, 256, 2, 4, false>, grid, 512, a, s);
     return p.direct ? launch(rog_linear_back_kernel<DT, 64, 4, 1, true>, grid, 256, a, s)
                     : launch(rog_linear_back_kernel<DT, 64, 4, 1, false>, grid, 256, a, s);
 }

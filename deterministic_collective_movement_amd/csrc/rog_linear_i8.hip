@@ -69,12 +69,13 @@ __device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32
     }
 }
 
-template <int OT, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void rog_linear_i8_kernel(LinearI8Args p) {
-    constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
-    typedef RowSteps<true, BM, THREADS, DIRECT, 1> A;
-    typedef RowSteps<false, BN, THREADS, DIRECT, 1> B;
-    ROG_TILE_MEMORY(A::kBytes, B::kBytes);
+template <int OT, class F, bool DIRECT>
+__global__ __launch_bounds__(F::kThreads) void rog_linear_i8_kernel(LinearI8Args p) {
+    constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN;
+    typedef RowProduct<kTypeI8, F, DIRECT, 1, F::kWide> Product;
+    typedef typename Product::A A;
+    typedef typename Product::B B;
+    ROG_TILE_MEMORY(F::kStages, A::kBytes, B::kBytes);
     const uint32_t rows = p.a.rows, tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
     const TileAt at = tile_at(blockIdx.x, tm, tn);
     const uint32_t r = shard_of_tile(p.sh, at.m), v0 = (at.m - p.sh.tile0[r]) * BM, n0 = at.n * BN;
@@ -82,9 +83,9 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_i8_kernel(LinearI8Arg
     A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
     B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
-    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
     i32x4 acc[FM][FN] = {};
-    Tile<kTypeI8, FM, FN, A, B>().run(a, b, p.a.kbytes / kStepBytes, p.a.kbytes % kStepBytes != 0, m0, w0, memory, acc);
+    Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
     constexpr uint32_t OS = Logit<OT>::kSize;
 #pragma unroll
@@ -117,9 +118,10 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
 template <int OT, bool DIRECT>
 hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
     switch (p.form) {
-    case kTileWide: return launch(rog_linear_i8_kernel<OT, 256, 256, ROG_WM, ROG_WN, DIRECT>, p.grid, 64 * ROG_WM * ROG_WN, p.args, s);
-    case kTileMid: return launch(rog_linear_i8_kernel<OT, 128, 128, 2, 2, DIRECT>, p.grid, 256, p.args, s);
-    default: return launch(rog_linear_i8_kernel<OT, 128, 64, 4, 1, DIRECT>, p.grid, 256, p.args, s);
+    case kFormWide: return launch(rog_linear_i8_kernel<OT, FormWide, DIRECT>, p.grid, FormWide::kThreads, p.args, s);
+    case kFormMid: return launch(rog_linear_i8_kernel<OT, FormMid, DIRECT>, p.grid, FormMid::kThreads, p.args, s);
+    case kFormSome: return launch(rog_linear_i8_kernel<OT, FormSome, DIRECT>, p.grid, FormSome::kThreads, p.args, s);
+    default: return launch(rog_linear_i8_kernel<OT, FormFew, DIRECT>, p.grid, FormFew::kThreads, p.args, s);
     }
 }
 template <int OT>

@@ -76,9 +76,13 @@ void lay_tiles(WeightShards *h, uint32_t tile) {
 }
 
 // The tile for so many rows.
-int32_t form_of(uint64_t rows) { return rows <= 64 ? kTileFew : rows <= 128 ? kTileMid : kTileWide; }
-uint32_t tile_columns(int32_t form) { return form == kTileWide ? 256 : 128; }
-uint32_t tile_rows(int32_t form) { return form == kTileWide ? 256 : form == kTileMid ? 128 : 64; }
+int32_t form_of(uint64_t rows) {
+    return rows <= FormFew::kRows ? kFormFew : rows <= FormSome::kRows ? kFormSome : rows <= FormMid::kRows ? kFormMid : kFormWide;
+}
+constexpr uint32_t kFormColumns[] = {FormFew::kColumns, FormSome::kColumns, FormMid::kColumns, FormWide::kColumns};
+constexpr uint32_t kFormRows[] = {FormFew::kRows, FormSome::kRows, FormMid::kRows, FormWide::kRows};
+uint32_t tile_columns(int32_t form) { return kFormColumns[form]; }
+uint32_t tile_rows(int32_t form) { return kFormRows[form]; }
 
 constexpr uint64_t kPackFrom = 65;   // rows from which the scored ones are packed
 
@@ -120,11 +124,12 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);
-    a.unit_leaves = p->form == kTileWide ? 4 : p->form == kTileMid ? 2 : 1;
-    a.rows_pad = uint32_t(up(rows, 16));
-    const uint32_t blocks = a.sh.block0[W];
+    const uint32_t blocks = a.sh.block0[W], rows_pad = uint32_t(up(rows, 16));
+    // a row's states together where a wave joins a row, else a block's
+    a.row_step = p->form == kFormWide ? 1 : blocks;
+    a.block_step = p->form == kFormWide ? rows_pad : 1;
     Layout w;
-    const uint64_t target = w.take(rows * 4), states = w.take(uint64_t(blocks) * (4 / a.unit_leaves) * a.rows_pad * 16);
+    const uint64_t target = w.take(rows * 4), states = w.take(uint64_t(blocks) * rows_pad * 16);
     const uint64_t index = w.take(p->packs ? rows * 4 : 0), count = w.take(p->packs ? 4 : 0), rows_at = w.take(p->packs ? rows * packed : 0);
     p->workspace_bytes = rows ? w.at : 0;
     if (rows == 0 || !addresses) return ROG_OK;
@@ -166,8 +171,8 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
         a.a = LinearRows{p->pack.packed, int64_t(packed), p->pack.count, uint32_t(rows), uint32_t(kbytes)};
         a.index = p->pack.index;
     }
-    p->join = JoinArgs{tokens, a.index, a.a.count, a.target, a.states, out->logp, out->entropy, out->lse, uint32_t(rows), a.rows_pad,
-                       a.sh.vocab, blocks, a.unit_leaves, a.scale};
+    p->join = JoinArgs{tokens, a.index, a.a.count, a.target, a.states, out->logp, out->entropy, out->lse, uint32_t(rows), a.row_step,
+                       a.block_step, a.sh.vocab, blocks, a.scale};
     return ROG_OK;
 }
 
@@ -189,8 +194,8 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (st != ROG_OK) return st;
     lay_tiles(&a.sh, kGradTile);
     const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
-    p->wide = rows > 64;
-    const uint32_t bn = p->wide ? 256 : 64;
+    p->form = rows <= FormFew::kRows ? kFormFew : rows <= FormSome::kRows ? kFormSome : kFormWide;
+    const uint32_t bn = p->form == kFormWide ? 256 : 64;
     k = BackArgs{};
     k.sh = a.sh;
     k.dim = uint32_t(dim);
@@ -229,7 +234,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
         ++p->pieces;
     }
     p->piece_tiles = std::max(p->piece_tiles, 1u);
-    const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles;
+    const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2;
     const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 2;
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
@@ -349,8 +354,8 @@ full:
     k.last = s == segs;
     a.tile_begin = k.tile_begin;
     a.tiles = k.tiles;
-    *coef_grid = k.tiles * k.row_tiles;
-    *back_grid = (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles + k.dim_tiles * k.tiles * (p->wide ? 1 : 2);
+    *coef_grid = k.tiles * k.row_tiles * (kGradTile / tile_columns(p->form));
+    *back_grid = (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles + k.dim_tiles * k.tiles * (p->form == kFormWide ? 1 : 2);
 }
 
 rog_status plan_quantize(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q, int64_t q_stride,
@@ -439,7 +444,7 @@ ROG_API rog_status rog_linear_logprob_grad_plan(const rog_weight_shard *shards, 
     const rog_status st = rog::plan_linear_grad(nullptr, 0, rows, dim, shards, W, dtype, 1.0f, nullptr, nullptr, nullptr, nullptr, nullptr,
                                                 nullptr, 0, nullptr, nullptr, 0, false, &p);
     if (st != ROG_OK) return st;
-    *info = rog_linear_plan_info{rows ? rog::kGradTile : 0, rows ? (p.wide ? 256u : 64u) : 0, rows ? p.pieces : 0,
+    *info = rog_linear_plan_info{rows ? rog::kGradTile : 0, rows ? (p.form == rog::kFormWide ? 256u : 64u) : 0, rows ? p.pieces : 0,
                                  rows ? 1 + 2 * p.pieces + !p.running : 0, p.workspace_bytes};
     return ROG_OK;
 }

@@ -70,12 +70,13 @@ __device__ __forceinline__ void put_part(float *states, uint64_t at, const Part 
     *((gstate *)states + at) = f32x4{p.m, p.s, p.t, 0};
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void rog_linear_score_kernel(ScoreArgs p) {
-    constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16, LEAVES = FM / 2;
-    typedef RowSteps<true, BM, THREADS, DIRECT, 2> A;
-    typedef RowSteps<false, BN, THREADS, DIRECT, 2> B;
-    ROG_TILE_MEMORY(A::kBytes, B::kBytes);
+template <int DT, class F, bool DIRECT>
+__global__ __launch_bounds__(F::kThreads) void rog_linear_score_kernel(ScoreArgs p) {
+    constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2;
+    typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
+    typedef typename Product::A A;
+    typedef typename Product::B B;
+    ROG_TILE_MEMORY(F::kStages, A::kBytes, B::kBytes);
     const uint32_t rows = uniform(p.a.count ? *p.a.count : p.a.rows);
     const uint32_t tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
     if (blockIdx.x >= tm * tn) return;
@@ -85,11 +86,12 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_score_kernel(ScoreArg
     A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
     B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
-    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
     typename Mat<DT>::Acc acc[FM][FN] = {};
-    Tile<DT, FM, FN, A, B>().run(a, b, p.a.kbytes / kStepBytes, p.a.kbytes % kStepBytes != 0, m0, w0, memory, acc);
+    Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
     // lane l holds columns v0 + m0 + 32 f + 8 (l / 16) + 0 .. 7 of leaf f, row n0 + w0 + 16 j + l % 16
+    __shared__ Part shared_parts[F::kShare][F::kShare > 1 ? BN : 1];
     const uint32_t first = v0 + m0 + l / 16 * 8;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -119,46 +121,61 @@ __global__ __launch_bounds__(64 * WM * WN) void rog_linear_score_kernel(ScoreArg
         for (int d = 1; d < LEAVES; d *= 2)
 #pragma unroll
             for (int f = 0; f + d < LEAVES; f += 2 * d) part[f] = join(part[f], part[f + d]);
-        const uint32_t block = p.sh.block0[r] + (v0 + m0) / kLinearBlock;
-        if (l < 16 && n < rows && block < p.sh.block0[r + 1])
-            put_part(p.states, (uint64_t(block) * (4 / LEAVES) + (v0 + m0) % kLinearBlock / (32 * LEAVES)) * p.rows_pad + n, part[0]);
+        if constexpr (F::kShare == 1) {
+            const uint32_t block = p.sh.block0[r] + (v0 + m0) / kLinearBlock;
+            if (l < 16 && n < rows && block < p.sh.block0[r + 1])
+                put_part(p.states, uint64_t(n) * p.row_step + uint64_t(block) * p.block_step, part[0]);
+        } else if (l < 16) {
+            shared_parts[m0 / (FM * 16)][w0 + 16 * j + l] = part[0];
+        }
+    }
+    if constexpr (F::kShare > 1) {
+        // the waves of a block join their leaves; a tile has one block
+        static_assert(BM == int(kLinearBlock), "one block");
+        __syncthreads();
+        const uint32_t n = n0 + threadIdx.x;
+        if (threadIdx.x < BN && n < rows) {
+            Part all = join(shared_parts[0][threadIdx.x], shared_parts[1][threadIdx.x]);
+            if constexpr (F::kShare == 4) all = join(all, join(shared_parts[2][threadIdx.x], shared_parts[3][threadIdx.x]));
+            put_part(p.states, uint64_t(n) * p.row_step + uint64_t(p.sh.block0[r] + v0 / kLinearBlock) * p.block_step, all);
+        }
     }
 }
 
 // Joins a row's blocks: chunk c of 64 takes every 64th block from the c-th on, one
-// after the other, and the chunks are joined in pairs 32, 16, .. 1 apart.
-constexpr uint32_t kJoinRows = 16, kJoinThreads = 64 * kJoinRows;
-__global__ __launch_bounds__(kJoinThreads) void rog_linear_join_kernel(JoinArgs p) {
-    __shared__ float sm[kJoinThreads], ss[kJoinThreads], st[kJoinThreads];
+// after the other, and the chunks are joined in pairs 32, 16, .. 1 apart.  With
+// ROWS 1 a wave has a row, its lanes the chunks; with 16 a workgroup has 16 rows
+// whose states of a block stand together.
+constexpr uint32_t kJoinWide = 16;
+template <uint32_t ROWS>
+__global__ __launch_bounds__(ROWS == 1 ? 256 : 64 * ROWS) void rog_linear_join_kernel(JoinArgs p) {
+    constexpr uint32_t THREADS = ROWS == 1 ? 256 : 64 * ROWS, EACH = ROWS == 1 ? 4 : ROWS, DEEP = 4;
+    __shared__ Part others[ROWS == 1 ? 1 : THREADS];
     typedef const __attribute__((address_space(1))) f32x4 gstate;
-    const uint32_t rows = p.count ? *p.count : p.rows, chunk = threadIdx.x / kJoinRows;
-    const uint32_t n = blockIdx.x * kJoinRows + threadIdx.x % kJoinRows;
-    if (blockIdx.x * kJoinRows >= rows) return;
+    const uint32_t rows = p.count ? *p.count : p.rows, chunk = ROWS == 1 ? threadIdx.x % 64 : threadIdx.x / ROWS;
+    const uint32_t n = blockIdx.x * EACH + (ROWS == 1 ? threadIdx.x / 64 : threadIdx.x % ROWS);
+    if (blockIdx.x * EACH >= rows) return;
     Part all = {-kInf, 0, 0};
     if (n < rows) {
-        gstate *from = (gstate *)p.states + n;
-        const uint32_t units = 4 / p.unit_leaves;
-        const auto get = [&](uint64_t unit) {
-            const f32x4 v = from[unit * p.rows_pad];
-            return Part{v[0], v[1], v[2]};
-        };
-        for (uint32_t b = chunk; b < p.blocks; b += 64) {
-            Part o = get(uint64_t(b) * units);
-            if (units > 1) o = join(o, get(uint64_t(b) * units + 1));
-            if (units > 2) o = join(o, join(get(uint64_t(b) * units + 2), get(uint64_t(b) * units + 3)));
-            all = b == chunk ? o : join(all, o);
+        gstate *from = (gstate *)p.states + uint64_t(n) * p.row_step;
+        // a few blocks' loads at a time; past the last an empty state, which changes nothing
+        for (uint32_t b = chunk; b < p.blocks; b += 64 * DEEP) {
+            f32x4 v[DEEP];
+#pragma unroll
+            for (uint32_t i = 0; i < DEEP; ++i) v[i] = b + 64 * i < p.blocks ? from[uint64_t(b + 64 * i) * p.block_step] : f32x4{-kInf, 0, 0, 0};
+#pragma unroll
+            for (uint32_t i = 0; i < DEEP; ++i) all = join(all, Part{v[i][0], v[i][1], v[i][2]});
         }
     }
     for (uint32_t d = 32; d; d /= 2) {
-        __syncthreads();
-        if (chunk >= d && chunk < 2 * d) {
-            sm[threadIdx.x] = all.m;
-            ss[threadIdx.x] = all.s;
-            st[threadIdx.x] = all.t;
+        if constexpr (ROWS == 1) {
+            all = join(all, Part{__shfl_xor(all.m, d), __shfl_xor(all.s, d), __shfl_xor(all.t, d)});
+        } else {
+            __syncthreads();
+            if (chunk >= d && chunk < 2 * d) others[threadIdx.x] = all;
+            __syncthreads();
+            if (chunk < d) all = join(all, others[threadIdx.x + d * ROWS]);
         }
-        __syncthreads();
-        const uint32_t o = threadIdx.x + d * kJoinRows;
-        if (chunk < d) all = join(all, Part{sm[o], ss[o], st[o]});
     }
     if (chunk || n >= rows) return;
     const uint32_t row = p.index ? p.index[n] : n;
@@ -239,24 +256,26 @@ __global__ __launch_bounds__(kPackThreads) void rog_linear_pack_kernel(PackArgs 
     }
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN) void rog_linear_coef_kernel(GradArgs p) {
-    constexpr int THREADS = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16, LEAVES = FM / 2;
-    typedef RowSteps<true, BM, THREADS, DIRECT, 2> A;
-    typedef RowSteps<false, BN, THREADS, true, 2> B;
-    ROG_TILE_MEMORY(A::kBytes, B::kBytes);
-    const uint32_t rows = uniform(*p.a.count), tm = p.tiles, tn = (rows + BN - 1) / BN;
+template <int DT, class F, bool DIRECT>
+__global__ __launch_bounds__(F::kThreads) void rog_linear_coef_kernel(GradArgs p) {
+    constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2, SPLIT = int(kGradTile) / BM;
+    typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
+    typedef typename Product::A A;
+    typedef typename Product::B B;
+    ROG_TILE_MEMORY(F::kStages, A::kBytes, B::kBytes);
+    const uint32_t rows = uniform(*p.a.count), tm = p.tiles * SPLIT, tn = (rows + BN - 1) / BN;
     if (blockIdx.x >= tm * tn) return;
-    TileAt at = tile_at(blockIdx.x, tm, tn);
-    const uint32_t tile = p.tile_begin + at.m;
-    const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * BM, n0 = at.n * BN;
+    const TileAt at = tile_at(blockIdx.x, tm, tn);
+    const uint32_t tile = p.tile_begin + at.m / SPLIT;
+    const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * kGradTile + at.m % SPLIT * BM, n0 = at.n * BN;
     const WeightShard sh = p.sh.s[r];
+    if (v0 >= sh.width) return;        // nobody reads the coefficients of such a part
     A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
     B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
-    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
     typename Mat<DT>::Acc acc[FM][FN] = {};
-    Tile<DT, FM, FN, A, B>().run(a, b, p.a.kbytes / kStepBytes, p.a.kbytes % kStepBytes != 0, m0, w0, memory, acc);
+    Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
     constexpr float kLog2E = 1.44269504088896341f;
     const float scale = p.inv_t * kLog2E, all = DT == ROG_DTYPE_F16 ? *p.g_scale : 1.0f;
@@ -322,16 +341,20 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
 template <int DT, bool DIRECT>
 hipError_t launch_score(const ScorePlan &p, hipStream_t s) {
     switch (p.form) {
-    case kTileWide: return launch(rog_linear_score_kernel<DT, 256, 256, ROG_WM, ROG_WN, DIRECT>, p.grid, 64 * ROG_WM * ROG_WN, p.args, s);
-    case kTileMid: return launch(rog_linear_score_kernel<DT, 128, 128, 2, 2, DIRECT>, p.grid, 256, p.args, s);
-    default: return launch(rog_linear_score_kernel<DT, 128, 64, 4, 1, DIRECT>, p.grid, 256, p.args, s);
+    case kFormWide: return launch(rog_linear_score_kernel<DT, FormWide, DIRECT>, p.grid, FormWide::kThreads, p.args, s);
+    case kFormMid: return launch(rog_linear_score_kernel<DT, FormMid, DIRECT>, p.grid, FormMid::kThreads, p.args, s);
+    case kFormSome: return launch(rog_linear_score_kernel<DT, FormSome, DIRECT>, p.grid, FormSome::kThreads, p.args, s);
+    default: return launch(rog_linear_score_kernel<DT, FormFew, DIRECT>, p.grid, FormFew::kThreads, p.args, s);
     }
 }
 
 template <int DT, bool DIRECT>
 hipError_t launch_coef(const GradPlan &p, const GradArgs &a, uint32_t grid, hipStream_t s) {
-    if (p.wide) return launch(rog_linear_coef_kernel<DT, 256, 256, ROG_WM, ROG_WN, DIRECT>, grid, 64 * ROG_WM * ROG_WN, a, s);
-    return launch(rog_linear_coef_kernel<DT, 256, 64, 4, 1, DIRECT>, grid, 256, a, s);
+    switch (p.form) {
+    case kFormWide: return launch(rog_linear_coef_kernel<DT, FormWide, DIRECT>, grid, FormWide::kThreads, a, s);
+    case kFormSome: return launch(rog_linear_coef_kernel<DT, FormSome, DIRECT>, grid, FormSome::kThreads, a, s);
+    default: return launch(rog_linear_coef_kernel<DT, FormFew, DIRECT>, grid, FormFew::kThreads, a, s);
+    }
 }
 
 }  // namespace
@@ -365,7 +388,9 @@ ROG_API rog_status rog_linear_logprob(const void *hidden, int64_t hidden_stride,
         if (dtype == ROG_DTYPE_BF16) e = p.direct ? launch_score<ROG_DTYPE_BF16, true>(p, stream) : launch_score<ROG_DTYPE_BF16, false>(p, stream);
         else e = p.direct ? launch_score<ROG_DTYPE_F16, true>(p, stream) : launch_score<ROG_DTYPE_F16, false>(p, stream);
     }
-    if (e == hipSuccess) e = launch(rog_linear_join_kernel, uint32_t((rows + kJoinRows - 1) / kJoinRows), kJoinThreads, p.join, stream);
+    if (e == hipSuccess)
+        e = p.form == kFormWide ? launch(rog_linear_join_kernel<kJoinWide>, uint32_t((rows + kJoinWide - 1) / kJoinWide), 64 * kJoinWide, p.join, stream)
+                                : launch(rog_linear_join_kernel<1>, uint32_t((rows + 3) / 4), 256, p.join, stream);
     return launched(e);
 }
 
