@@ -191,7 +191,7 @@ constexpr uint32_t kGradTile = 256;
 struct GradPlan {
     rog_dtype dtype;
     int32_t form;                      // few, some or wide
-    bool direct, running;
+    bool direct, direct_back, running;
     uint32_t pieces, piece_tiles;      // tiles of a piece: whole segments' or all
     PackArgs pack;
     GradArgs coef;

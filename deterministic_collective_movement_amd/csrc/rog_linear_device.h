@@ -82,7 +82,8 @@ __device__ __forceinline__ vec16 row_bytes(gbyte *row, uint32_t at, uint32_t end
         for (uint32_t i = 0; i < 16; i += ES) {
             uint32_t e = 0;
             if (at + i < end) {
-                if constexpr (ES == 2) e = *(const __attribute__((address_space(1))) uint16_t *)(row + at + i);
+                if constexpr (ES == 4) e = *(const __attribute__((address_space(1))) uint32_t *)(row + at + i);
+                else if constexpr (ES == 2) e = *(const __attribute__((address_space(1))) uint16_t *)(row + at + i);
                 else e = row[at + i];
             }
             v[i / 4] |= e << (8 * (i % 4));
@@ -138,12 +139,15 @@ struct RowSteps {
         ++k;
     }
     // Brings the last step, which is not whole: zeros past K.
-    __device__ __forceinline__ void stage_tail(uint8_t *to) const { bring<true>(to, kbytes / kStepBytes); }
-    template <bool TAIL>
+    __device__ __forceinline__ void stage_tail(uint8_t *to) const {
+        if (kbytes % 16) bring<true, false>(to, kbytes / kStepBytes);   // a row ends inside a unit
+        else bring<true>(to, kbytes / kStepBytes);
+    }
+    template <bool TAIL, bool STRAIGHT = DIRECT>
     __device__ __forceinline__ void bring(uint8_t *to, uint32_t step) const {
         const uint32_t at = step * kStepBytes;
-        if constexpr (DIRECT) {
-            const auto r = window(base, rows_bytes);
+        if constexpr (STRAIGHT) {
+            const auto r = window(base, TAIL || kbytes >= kStepBytes ? rows_bytes : 0);   // no whole step: nothing is read
             const bool inside = !TAIL || at + unit < kbytes;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -154,7 +158,7 @@ struct RowSteps {
             vec16 v[kLoads];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const uint64_t off = uint64_t(threadIdx.x / 4 + i * kRows) * uint64_t(stride);
+                const uint32_t off = (threadIdx.x / 4 + i * kRows) * uint32_t(stride);
                 v[i] = off < rows_bytes ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes) : vec16{0, 0, 0, 0};
             }
 #pragma unroll
@@ -408,8 +412,16 @@ struct RowLines {
         : base(uniform(b)), rows_bytes(uniform((rows_left < ROWS ? rows_left : ROWS) * uint32_t(s))), kbytes(uniform(kb)), stride(s) {}
     // Brings the next step to `to`, zeros past the rows and past K.
     __device__ __forceinline__ void stage(uint8_t *to) {
+        // A step in which a row ends inside 16 bytes goes through registers.  Its loads are waited for, and
+        // with them all before them, so that counting loads in flight stays right.
+        if (DIRECT && !(kbytes % 16 && at < kbytes && at + 128 > kbytes)) bring<true>(to);
+        else bring<false>(to);
+        at += 128;
+    }
+    template <bool STRAIGHT>
+    __device__ __forceinline__ void bring(uint8_t *to) const {
         const uint32_t row = threadIdx.x / 8;
-        if constexpr (DIRECT) {
+        if constexpr (STRAIGHT) {
             const auto r = window(base, rows_bytes);
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -428,7 +440,6 @@ struct RowLines {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
         }
-        at += 128;
     }
     // Fragment f, half ks of the step, of a wave's rows from row0 (a multiple of 32) on.
     static __device__ __forceinline__ vec16 get(const uint8_t *from, uint32_t row0, int f, int ks) {

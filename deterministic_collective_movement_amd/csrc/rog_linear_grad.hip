@@ -206,9 +206,9 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
 template <int DT>
 hipError_t launch_back(const GradPlan &p, const BackArgs &a, uint32_t grid, hipStream_t s) {
     if (p.form == kFormWide)
-        return p.direct ? launch(rog_linear_back_kernel<DT, 256, 2, 4, true>, grid, 512, a, s)
+        return p.direct_back ? launch(rog_linear_back_kernel<DT, 256, 2, 4, true>, grid, 512, a, s)
                         : launch(rog_linear_back_kernel<DT, 256, 2, 4, false>, grid, 512, a, s);
-    return p.direct ? launch(rog_linear_back_kernel<DT, 64, 4, 1, true>, grid, 256, a, s)
+    return p.direct_back ? launch(rog_linear_back_kernel<DT, 64, 4, 1, true>, grid, 256, a, s)
                     : launch(rog_linear_back_kernel<DT, 64, 4, 1, false>, grid, 256, a, s);
 }
 

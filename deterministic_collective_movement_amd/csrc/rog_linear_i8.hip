@@ -15,16 +15,58 @@ namespace {
 
 #pragma clang fp contract(off)
 
-// A row per workgroup: the largest magnitude, then the quotients; a row is read twice, the second time from the caches.
+// A row per workgroup: the largest magnitude, then the quotients.  Rows of up to
+// kHeld vectors of 16 bytes per thread stay in registers between the two, longer ones are
+// read again from the caches.
 constexpr uint32_t kQuantThreads = 256;
+constexpr int kHeld = 4;
+
+// 8-bit integers of the elements of a vector, in order.
 template <int DT>
+__device__ __forceinline__ void put_quotients(__attribute__((address_space(1))) uint8_t *to, const vec16 &v, float s, uint32_t n) {
+    constexpr int E = Logit<DT>::kPerVec;
+    float x[E];
+    widen_vec<DT>(v, x);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const float q = __builtin_rintf(x[i] / s);
+        w[i / 4] |= (uint32_t(q == q ? int(q) : 0) & 0xFF) << (8 * (i % 4));
+    }
+    typedef uint32_t word2any __attribute__((ext_vector_type(2), aligned(1)));
+    typedef uint32_t wordany __attribute__((aligned(1)));
+    if (n >= uint32_t(E)) {
+        if constexpr (E == 8) *(__attribute__((address_space(1))) word2any *)to = word2any{w[0], w[1]};
+        else *(__attribute__((address_space(1))) wordany *)to = w[0];
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < uint32_t(E); ++i)
+            if (i < n) to[i] = uint8_t(w[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+template <int DT, bool HELD>
 __global__ __launch_bounds__(kQuantThreads) void rog_quantize_kernel(QuantizeArgs p) {
-    constexpr uint32_t ES = Logit<DT>::kSize;
+    constexpr uint32_t ES = Logit<DT>::kSize, E = Logit<DT>::kPerVec;
     __shared__ float most[kQuantThreads / 64];
     gbyte *row = (gbyte *)p.x + uint64_t(blockIdx.x) * uint64_t(p.stride);
-    const uint32_t t = threadIdx.x;
+    const uint32_t t = threadIdx.x, bytes = p.dim * ES;
+    vec16 held[kHeld];
     float m = 0;
-    for (uint32_t i = t; i < p.dim; i += kQuantThreads) m = max_nan(m, fabsf(load_logit<DT>(row + i * ES)));
+    const auto largest = [&](const vec16 &v) {
+        float x[E];
+        widen_vec<DT>(v, x);
+#pragma unroll
+        for (uint32_t i = 0; i < E; ++i) m = max_nan(m, fabsf(x[i]));
+    };
+    if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = row_bytes<ES>(row, (t + i * kQuantThreads) * 16, bytes);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) largest(held[i]);
+    } else {
+        for (uint32_t at = t * 16; at < bytes; at += kQuantThreads * 16) largest(row_bytes<ES>(row, at, bytes));
+    }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) m = max_nan(m, __shfl_xor(m, d));
     if (t % 64 == 0) most[t / 64] = m;
@@ -32,10 +74,15 @@ __global__ __launch_bounds__(kQuantThreads) void rog_quantize_kernel(QuantizeArg
     m = max_nan(max_nan(most[0], most[1]), max_nan(most[2], most[3]));
     const float s = m < kInf ? fmaxf(m / 127.0f, 0x1p-126f) : __builtin_nanf("");
     if (t == 0) p.scale[blockIdx.x] = s;
-    int8_t *q = p.q + uint64_t(blockIdx.x) * uint64_t(p.q_stride);
-    for (uint32_t i = t; i < p.dim; i += kQuantThreads) {
-        const float v = load_logit<DT>(row + i * ES) / s;
-        q[i] = v == v ? int8_t(int(__builtin_rintf(v))) : int8_t(0);
+    __attribute__((address_space(1))) uint8_t *q = (__attribute__((address_space(1))) uint8_t *)p.q + uint64_t(blockIdx.x) * uint64_t(p.q_stride);
+    const auto put = [&](uint32_t first, const vec16 &v) {
+        if (first < p.dim) put_quotients<DT>(q + first, v, s, p.dim - first);
+    };
+    if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) put((t + i * kQuantThreads) * E, held[i]);
+    } else {
+        for (uint32_t at = t * 16; at < bytes; at += kQuantThreads * 16) put(at / ES, row_bytes<ES>(row, at, bytes));
     }
 }
 
@@ -115,6 +162,12 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
     return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
 }
 
+template <int DT>
+hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t s) {
+    const bool held = uint64_t(a.dim) * Logit<DT>::kSize <= kHeld * kQuantThreads * 16;
+    return held ? launch(rog_quantize_kernel<DT, true>, a.rows, kQuantThreads, a, s) : launch(rog_quantize_kernel<DT, false>, a.rows, kQuantThreads, a, s);
+}
+
 template <int OT, bool DIRECT>
 hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
     switch (p.form) {
@@ -147,9 +200,9 @@ ROG_API rog_status rog_quantize_i8(const void *x, int64_t row_stride, size_t row
     const rog_status st = plan_quantize(x, row_stride, rows, dim, dtype, q, q_stride, scale, &a);
     if (st != ROG_OK || rows == 0) return st;
     switch (dtype) {
-    case ROG_DTYPE_BF16: return launched(launch(rog_quantize_kernel<ROG_DTYPE_BF16>, a.rows, kQuantThreads, a, stream));
-    case ROG_DTYPE_F16: return launched(launch(rog_quantize_kernel<ROG_DTYPE_F16>, a.rows, kQuantThreads, a, stream));
-    default: return launched(launch(rog_quantize_kernel<ROG_DTYPE_F32>, a.rows, kQuantThreads, a, stream));
+    case ROG_DTYPE_BF16: return launched(launch_quantize<ROG_DTYPE_BF16>(a, stream));
+    case ROG_DTYPE_F16: return launched(launch_quantize<ROG_DTYPE_F16>(a, stream));
+    default: return launched(launch_quantize<ROG_DTYPE_F32>(a, stream));
     }
 }
 

@@ -39,8 +39,8 @@ rog_status check_matrix(const void *p, int64_t stride, uint64_t rows, uint64_t w
     return fits(addr(p), rows, uint64_t(stride) * es, width * es) ? ROG_OK : ROG_ERR_TOO_LARGE;
 }
 
-// Loads of 16 bytes go straight to the shared memory where rows begin and end with them.
-bool aligned(const void *p, uint64_t stride_bytes, uint64_t row_bytes) { return (addr(p) | stride_bytes | row_bytes) % 16 == 0; }
+// Loads of 16 bytes go straight to the shared memory from rows that begin on 4 bytes.
+bool aligned(const void *p, uint64_t stride_bytes) { return (addr(p) | stride_bytes) % 4 == 0; }
 
 template <class Shard>
 rog_status lay_weights(const Shard *shards, int W, int64_t dim, uint32_t es, bool addresses, WeightShards *h, bool *direct) {
@@ -55,7 +55,7 @@ rog_status lay_weights(const Shard *shards, int W, int64_t dim, uint32_t es, boo
             if (st != ROG_OK) return st;
         }
         h->s[r] = WeightShard{shards[r].weight, shards[r].row_stride * es, uint32_t(shards[r].width), uint32_t(v)};
-        if (shards[r].width && !aligned(shards[r].weight, shards[r].width > 1 ? uint64_t(h->s[r].stride) : 0, uint64_t(dim) * es)) *direct = false;
+        if (shards[r].width && !aligned(shards[r].weight, shards[r].width > 1 ? uint64_t(h->s[r].stride) : 0)) *direct = false;
         v += uint64_t(shards[r].width);
     }
     h->W = uint32_t(W);
@@ -120,7 +120,7 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     p->packs = has_tokens && rows >= kPackFrom;
     lay_tiles(&a.sh, tile_columns(p->form));
     const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
-    if (!p->packs && !aligned(hidden, rows > 1 ? uint64_t(hidden_stride) * 2 : 0, kbytes)) p->direct = false;
+    if (!p->packs && !aligned(hidden, rows > 1 ? uint64_t(hidden_stride) * 2 : 0)) p->direct = false;
     const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);
@@ -318,6 +318,8 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     k.g_stride = a.g_stride;
     k.part = in<float>(workspace, part);
     k.part_seg = p->running ? 0 : seg_floats;
+    // along rows, where a row's end inside 16 bytes would be read past, only whole ones
+    p->direct_back = p->direct && kbytes % 16 == 0;
     k.d_hidden = d_hidden;
     k.d_stride = d_hidden_stride * 2;
     p->join_grid = 0;
@@ -412,7 +414,7 @@ rog_status plan_linear_i8(const int8_t *q, int64_t q_stride, const float *scale,
     }
     p->form = form_of(rows);
     lay_tiles(&a.sh, tile_columns(p->form));
-    if (!aligned(q, rows > 1 ? uint64_t(q_stride) : 0, uint64_t(dim))) p->direct = false;
+    if (!aligned(q, rows > 1 ? uint64_t(q_stride) : 0)) p->direct = false;
     const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);

@@ -311,3 +311,20 @@ def test_linear_i8_strides_leave_what_is_between_rows(gpu, n, dtype):
     out = rog.rog_linear_i8(q, s, [w], [r], out=[buf[:, 5:305]])
     assert torch.equal(out[0].cpu(), ref.linear_i8_cpu(q, s, w, r, dtype))
     assert bool((buf[:, :5] == 7).all()) and bool((buf[:, 305:] == 7).all())
+
+
+@pytest.mark.parametrize("n", [1, 40, 100, 300])
+@pytest.mark.parametrize("dim", [10, 42, 100, 1000])
+def test_rows_that_end_inside_16_bytes(gpu, n, dim):
+    # 4-byte aligned rows whose last 16 bytes are the next row's too: elements past K must count for nothing
+    h, ws, tokens = ref.head(n, [300, 77], dim, BF16, gpu)
+    check_score(h, ws, tokens)
+    if dim % 2 == 0:
+        gen = torch.Generator(device=gpu)
+        gen.manual_seed(n)
+        d = dim // 2 * 4
+        q = torch.randint(-128, 128, (n, d), generator=gen, device=gpu, dtype=torch.int8)
+        w = torch.randint(-128, 128, (333, d), generator=gen, device=gpu, dtype=torch.int8)
+        s, r = torch.rand(n, device=gpu), torch.rand(333, device=gpu)
+        out = rog.rog_linear_i8(q, s, [w], [r], dtype=F32)[0]
+        assert torch.equal(out.cpu(), ref.linear_i8_cpu(q, s, w, r, F32))
