@@ -133,10 +133,7 @@ struct RowSteps {
     }
     // Brings the next step to `to`, zeros past the rows.
     __device__ __forceinline__ void stage(uint8_t *to) {
-        // past the last whole step: that one again, which nobody reads
-        const uint32_t whole = kbytes / kStepBytes, last = whole ? whole - 1 : 0;
-        bring<false>(to, k < last ? k : last);
-        ++k;
+        bring<false>(to, k++);         // past the last whole step zeros
     }
     // Brings the last step, which is not whole: zeros past K.
     __device__ __forceinline__ void stage_tail(uint8_t *to) const {
@@ -147,7 +144,7 @@ struct RowSteps {
     __device__ __forceinline__ void bring(uint8_t *to, uint32_t step) const {
         const uint32_t at = step * kStepBytes;
         if constexpr (STRAIGHT) {
-            const auto r = window(base, TAIL || kbytes >= kStepBytes ? rows_bytes : 0);   // no whole step: nothing is read
+            const auto r = window(base, TAIL || at + kStepBytes <= kbytes ? rows_bytes : 0);
             const bool inside = !TAIL || at + unit < kbytes;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -159,7 +156,8 @@ struct RowSteps {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const uint32_t off = (threadIdx.x / 4 + i * kRows) * uint32_t(stride);
-                v[i] = off < rows_bytes ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes) : vec16{0, 0, 0, 0};
+                v[i] = off < rows_bytes && (TAIL || at + kStepBytes <= kbytes) ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes)
+                                                                               : vec16{0, 0, 0, 0};
             }
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
@@ -261,6 +259,20 @@ struct ColSteps {
         __device__ __forceinline__ void refresh() { asm volatile("" : "+v"(lane)); }
     };
 };
+
+// Lanes 32 apart, and lanes 16 apart: of a pair of registers the lower lanes' values in first, the upper lanes' in
+// second, in both halves: (a, b) gives a's halves to the lower lanes and b's to the upper ones.
+struct Halves {
+    float first, second;
+};
+__device__ __forceinline__ Halves halves32(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(f32_bits(a), f32_bits(b), false, false);
+    return Halves{bits_f32(r[0]), bits_f32(r[1])};
+}
+__device__ __forceinline__ Halves halves16(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(f32_bits(a), f32_bits(b), false, false);
+    return Halves{bits_f32(r[0]), bits_f32(r[1])};
+}
 
 // Two fragments of sixteen consecutive rows of M each, a and b, in a lane of quarter q rows 4 q and on of each: has
 // the lane hold eight consecutive ones, from row 8 * eight_of(q) of the 32 on, in a and then b.

@@ -117,7 +117,7 @@ __device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32
 }
 
 template <int OT, class F, bool DIRECT>
-__global__ __launch_bounds__(F::kThreads) void rog_linear_i8_kernel(LinearI8Args p) {
+__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_i8_kernel(LinearI8Args p) {
     constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN;
     typedef RowProduct<kTypeI8, F, DIRECT, 1, F::kWide> Product;
     typedef typename Product::A A;

@@ -34,35 +34,71 @@ __device__ __forceinline__ Part join(const Part &a, const Part &b) {
     return o;
 }
 
-// The state of a leaf from the eight logits of it that each lane holds: lanes 16, 32 and 48 on hold the rest.
-__device__ __forceinline__ Part leaf_of(const float (&x)[8], float scale) {
+// The largest of a leaf's logits, of which each lane holds eight: lanes 16, 32 and 48 on hold the rest.
+__device__ __forceinline__ float largest_of(const float (&x)[8]) {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = max_nan(top, x[i]);
-    top = max_nan(top, __shfl_xor(top, 16));
-    top = max_nan(top, __shfl_xor(top, 32));
-    Part p;
-    p.m = top * scale;
-    const float at = base_of(p.m);
-    float s[8], t[8];
+    Halves h = halves32(top, top);
+    top = max_nan(h.first, h.second);
+    h = halves16(top, top);
+    return max_nan(h.first, h.second);
+}
+
+// s and t of the lane's eight logits about the leaf's m.
+__device__ __forceinline__ void sums_of(const float (&x)[8], float scale, float m, float &s, float &t) {
+    const float at = base_of(m);
+    float e[8], u[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = __builtin_fmaf(x[i], scale, -at);
-        s[i] = exp2_fast(d);
-        t[i] = s[i] * fmaxf(d, kFar);
+    for (int i = 0; i < 8; i += 2) {
+        const float d0 = __builtin_fmaf(x[i], scale, -at), d1 = __builtin_fmaf(x[i + 1], scale, -at);
+        e[i] = exp2_fast(d0);
+        e[i + 1] = exp2_fast(d1);
+        u[i / 2] = __builtin_fmaf(e[i + 1], fmaxf(d1, kFar), e[i] * fmaxf(d0, kFar));
     }
+    s = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    t = (u[0] + u[1]) + (u[2] + u[3]);
+}
+
+// The sum over the four lanes that hold a leaf.
+__device__ __forceinline__ float leaf_sum(float v) {
+    Halves h = halves32(v, v);
+    v = h.first + h.second;
+    h = halves16(v, v);
+    return h.first + h.second;
+}
+// The same of four leaves: quarters 0, 2, 1, 3 of the wave get leaf 0, 1, 2, 3.
+__device__ __forceinline__ float leaf_sums(const float (&v)[4]) {
+    Halves h = halves32(v[0], v[1]);
+    const float a = h.first + h.second;
+    h = halves32(v[2], v[3]);
+    const float b = h.first + h.second;
+    h = halves16(a, b);
+    return h.first + h.second;
+}
+
+// The joined state of LEAVES consecutive leaves (1, 2 or 4), the same in all lanes that hold a row.
+template <int LEAVES>
+__device__ __forceinline__ Part leaves_of(const float (&x)[LEAVES][8], float scale) {
+    float m[LEAVES], s[LEAVES], t[LEAVES];
 #pragma unroll
-    for (int d = 4; d; d /= 2)
-#pragma unroll
-        for (int i = 0; i < d; ++i) {
-            s[i] += s[i + d];
-            t[i] += t[i + d];
-        }
-    s[0] += __shfl_xor(s[0], 16);
-    t[0] += __shfl_xor(t[0], 16);
-    p.s = s[0] + __shfl_xor(s[0], 32);
-    p.t = t[0] + __shfl_xor(t[0], 32);
-    return p;
+    for (int f = 0; f < LEAVES; ++f) {
+        m[f] = largest_of(x[f]) * scale;
+        sums_of(x[f], scale, m[f], s[f], t[f]);
+    }
+    if constexpr (LEAVES == 4) {
+        // a leaf in each quarter, joined across them
+        const uint32_t quarter = threadIdx.x / 16 % 4;
+        Part p = {quarter & 2 ? (quarter & 1 ? m[3] : m[1]) : (quarter & 1 ? m[2] : m[0]), leaf_sums(s), leaf_sums(t)};
+        Halves hm = halves32(p.m, p.m), hs = halves32(p.s, p.s), ht = halves32(p.t, p.t);
+        p = join(Part{hm.first, hs.first, ht.first}, Part{hm.second, hs.second, ht.second});
+        hm = halves16(p.m, p.m), hs = halves16(p.s, p.s), ht = halves16(p.t, p.t);
+        return join(Part{hm.first, hs.first, ht.first}, Part{hm.second, hs.second, ht.second});
+    } else {
+        Part p = {m[0], leaf_sum(s[0]), leaf_sum(t[0])};
+        if constexpr (LEAVES == 2) p = join(p, Part{m[1], leaf_sum(s[1]), leaf_sum(t[1])});
+        return p;
+    }
 }
 
 __device__ __forceinline__ void put_part(float *states, uint64_t at, const Part &p) {
@@ -71,7 +107,7 @@ __device__ __forceinline__ void put_part(float *states, uint64_t at, const Part 
 }
 
 template <int DT, class F, bool DIRECT>
-__global__ __launch_bounds__(F::kThreads) void rog_linear_score_kernel(ScoreArgs p) {
+__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_score_kernel(ScoreArgs p) {
     constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2;
     typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
     typedef typename Product::A A;
@@ -87,46 +123,48 @@ __global__ __launch_bounds__(F::kThreads) void rog_linear_score_kernel(ScoreArgs
     B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
+    // the rows' tokens as columns of the tile, all others past it
+    __shared__ uint32_t targets[BN];
+    if (threadIdx.x < BN) {
+        const uint32_t n = n0 + threadIdx.x;
+        const int64_t tok = p.tokens && n < rows ? p.tokens[p.index ? p.index[n] : n] - int64_t(sh.col0) - int64_t(v0) : -1;
+        targets[threadIdx.x] = tok >= 0 && tok < BM && uint32_t(tok) + v0 < sh.width ? uint32_t(tok) : 1u << 30;
+    }
     typename Mat<DT>::Acc acc[FM][FN] = {};
     Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
     // lane l holds columns v0 + m0 + 32 f + 8 (l / 16) + 0 .. 7 of leaf f, row n0 + w0 + 16 j + l % 16
     __shared__ Part shared_parts[F::kShare][F::kShare > 1 ? BN : 1];
-    const uint32_t first = v0 + m0 + l / 16 * 8;
+    const uint32_t own = 8 * (l / 16);
+    if (v0 + m0 + FM * 16 > sh.width) {
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (v0 + m0 + 32 * (f / 2) + own + 4 * (f % 2) + i >= sh.width)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) acc[f][j][i] = -kInf;
+    }
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
         const uint32_t n = n0 + w0 + 16 * j + l % 16;
-        int64_t tok = -1;
-        if (p.tokens && n < rows) tok = p.tokens[p.index ? p.index[n] : n];
-        const int64_t own = tok - int64_t(sh.col0) - int64_t(first);
-        Part part[LEAVES];
+        // the row's token among the wave's columns
+        const uint32_t hit = targets[w0 + 16 * j + l % 16] - m0;
+        if (__ballot(hit < FM * 16)) {
 #pragma unroll
-        for (int f = 0; f < LEAVES; ++f) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4];
-            if (own >= 32 * f && own < 32 * f + 8 && first + uint32_t(own) < sh.width) {
-                float hit = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) hit = own - 32 * f == i ? x[i] : hit;
-                p.target[n] = hit;
-            }
-            if (v0 + m0 + 32 * f + 32 > sh.width)
-#pragma unroll
-                for (uint32_t i = 0; i < 8; ++i)
-                    if (first + 32 * f + i >= sh.width) x[i] = -kInf;
-            part[f] = leaf_of(x, p.scale);
+            for (uint32_t c = 0; c < FM * 4; ++c)
+                if (hit == 32 * (c / 8) + own + c % 8) p.target[n] = acc[c / 4][j][c % 4];
         }
+        float x[LEAVES][8];
 #pragma unroll
-        for (int d = 1; d < LEAVES; d *= 2)
-#pragma unroll
-            for (int f = 0; f + d < LEAVES; f += 2 * d) part[f] = join(part[f], part[f + d]);
+        for (int c = 0; c < FM * 4; ++c) x[c / 8][c % 8] = acc[c / 4][j][c % 4];
+        const Part part = leaves_of<LEAVES>(x, p.scale);
         if constexpr (F::kShare == 1) {
             const uint32_t block = p.sh.block0[r] + (v0 + m0) / kLinearBlock;
             if (l < 16 && n < rows && block < p.sh.block0[r + 1])
-                put_part(p.states, uint64_t(n) * p.row_step + uint64_t(block) * p.block_step, part[0]);
+                put_part(p.states, uint64_t(n) * p.row_step + uint64_t(block) * p.block_step, part);
         } else if (l < 16) {
-            shared_parts[m0 / (FM * 16)][w0 + 16 * j + l] = part[0];
+            shared_parts[m0 / (FM * 16)][w0 + 16 * j + l] = part;
         }
     }
     if constexpr (F::kShare > 1) {
@@ -256,8 +294,38 @@ __global__ __launch_bounds__(kPackThreads) void rog_linear_pack_kernel(PackArgs 
     }
 }
 
+constexpr float kLog2E = 1.44269504088896341f;
+
+// What a row's coefficients are made of: G = 2^y (c0 + c1 y) with y = x log2(e) / T - at, and g more at the token.
+struct RowOf {
+    float at, c0, c1, g;
+    float again;                       // binary16: from the row's scale to that of all rows
+    uint32_t target;                   // the token as a column of the tile, else past it
+};
+template <int DT>
+__device__ __forceinline__ RowOf coef_row(const GradArgs &p, uint32_t row, int64_t first, uint32_t columns) {
+    const int64_t tok = p.tokens[row];
+    const float lse = p.lse[row], h = p.entropy[row];
+    float g = p.g_logp[row], gh = p.g_entropy ? p.g_entropy[row] : 0.0f;
+    RowOf r;
+    // binary16: one copy by a scale of the row's own for d_hidden, one by that of all rows for d_weights
+    const float by = DT == ROG_DTYPE_F16 ? power_for(most_of(g, gh, p.inv_t)) : 1.0f;
+    r.again = DT == ROG_DTYPE_F16 ? *p.g_scale / by : 1.0f;
+    g *= p.inv_t * by;
+    gh *= p.inv_t * by;
+    if (tok >= int64_t(p.sh.vocab)) g = __builtin_nanf("");
+    const bool empty = lse == -kInf;
+    if (empty) g = gh = 0.0f;
+    r.at = empty ? kInf : lse * kLog2E;
+    r.c0 = -__builtin_fmaf(gh, h, g);
+    r.c1 = -gh * kLn2;
+    r.g = g;
+    r.target = tok >= first && tok - first < int64_t(columns) ? uint32_t(tok - first) : 1u << 30;
+    return r;
+}
+
 template <int DT, class F, bool DIRECT>
-__global__ __launch_bounds__(F::kThreads) void rog_linear_coef_kernel(GradArgs p) {
+__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_coef_kernel(GradArgs p) {
     constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2, SPLIT = int(kGradTile) / BM;
     typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
     typedef typename Product::A A;
@@ -274,50 +342,45 @@ __global__ __launch_bounds__(F::kThreads) void rog_linear_coef_kernel(GradArgs p
     B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
+    __shared__ RowOf row_of[BN];
+    if (threadIdx.x < BN && n0 + threadIdx.x < rows) row_of[threadIdx.x] = coef_row<DT>(p, p.index[n0 + threadIdx.x], int64_t(sh.col0) + v0, BM);
     typename Mat<DT>::Acc acc[FM][FN] = {};
     Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
-    constexpr float kLog2E = 1.44269504088896341f;
-    const float scale = p.inv_t * kLog2E, all = DT == ROG_DTYPE_F16 ? *p.g_scale : 1.0f;
-    const uint32_t first = v0 + m0 + l / 16 * 8;
+    const float scale = p.inv_t * kLog2E;
+    const uint32_t own = 8 * (l / 16);
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
         const uint32_t n = n0 + w0 + 16 * j + l % 16;
-        if (n >= rows) continue;
-        const uint32_t row = p.index[n];
-        const int64_t tok = p.tokens[row];
-        const int64_t own = tok - int64_t(sh.col0) - int64_t(first);
-        const float lse = p.lse[row], h = p.entropy[row];
-        float g = p.g_logp[row], gh = p.g_entropy ? p.g_entropy[row] : 0.0f;
-        // binary16: one copy by a scale of the row's own for d_hidden, one by that of all rows for d_weights
-        const float by = DT == ROG_DTYPE_F16 ? power_for(most_of(g, gh, p.inv_t)) : 1.0f, again = all / by;
-        g *= p.inv_t * by;
-        gh *= p.inv_t * by;
-        if (tok >= int64_t(p.sh.vocab)) g = __builtin_nanf("");
-        const bool empty = lse == -kInf;
-        if (empty) g = gh = 0.0f;
-        const float at2 = empty ? kInf : lse * kLog2E;
-        const float c0 = __builtin_fmaf(gh, h, g), c1 = gh * kLn2;       // -G = p (g + gh (log p + H))
+        const RowOf row = row_of[w0 + 16 * j + l % 16];
+        const uint32_t hit = row.target - m0;
+        const bool hits = __ballot(hit < FM * 16) != 0;
 #pragma unroll
         for (int f = 0; f < LEAVES; ++f) {
             float d[8];
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i) {
-                const float y = __builtin_fmaf(acc[2 * f + i / 4][j][i % 4], scale, -at2);
-                const float q = exp2_fast(y);
-                d[i] = -q * __builtin_fmaf(c1, fmaxf(y, kFar), c0);
-                if (own == 32 * f + i) d[i] += g;
-                if (first + 32 * f + i >= sh.width) d[i] = 0.0f;
+                const float y = __builtin_fmaf(acc[2 * f + i / 4][j][i % 4], scale, -row.at);
+                d[i] = exp2_fast(y) * __builtin_fmaf(row.c1, fmaxf(y, kFar), row.c0);
             }
+            if (hits)
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i)
+                    if (hit == 32 * f + own + i) d[i] += row.g;
+            if (v0 + m0 + 32 * f + 32 > sh.width)
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i)
+                    if (v0 + m0 + 32 * f + own + i >= sh.width) d[i] = 0.0f;
+            if (n >= rows) continue;
             vec16 v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(d + 2 * i);
             typedef __attribute__((address_space(1))) vec16 gvec16_out;
-            const uint64_t to = uint64_t(n) * uint64_t(p.g_stride) + (uint64_t(at.m) * BM + m0 + l / 16 * 8 + 32 * f) * 2;
+            const uint64_t to = uint64_t(n) * uint64_t(p.g_stride) + (uint64_t(at.m) * BM + m0 + own + 32 * f) * 2;
             *(gvec16_out *)((uint8_t *)p.g + to) = v;
             if constexpr (DT == ROG_DTYPE_F16) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] *= again;
+                for (int i = 0; i < 8; ++i) d[i] *= row.again;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(d + 2 * i);
                 *(gvec16_out *)((uint8_t *)p.g_all + to) = v;
