@@ -169,7 +169,10 @@ struct Form {
     static constexpr int kShare = COLUMNS / WM < int(kLinearBlock) ? int(kLinearBlock) / (COLUMNS / WM) : 1;
     static_assert(COLUMNS % kLinearBlock == 0 && COLUMNS / WM % 32 == 0 && COLUMNS / WM <= int(kLinearBlock), "whole leaves, blocks");
 };
-typedef Form<128, 32, 4, 1, 4, false> FormFew;
+#ifndef ROG_FEWST
+#define ROG_FEWST 4
+#endif
+typedef Form<128, 32, 4, 1, ROG_FEWST, false> FormFew;
 typedef Form<128, 64, 4, 1, 3, false> FormSome;
 typedef Form<128, 128, 2, 2, 4, true> FormMid;
 typedef Form<256, 256, 2, 4, 4, true> FormWide;
@@ -216,8 +219,12 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
                             rog_dtype dtype, float temperature, const int64_t *tokens, const float *lse, const float *entropy,
                             const float *g_logp, const float *g_entropy, void *d_hidden, int64_t d_hidden_stride,
                             const rog_grad_shard *d_weights, void *workspace, size_t workspace_bytes, bool addresses, GradPlan *p);
-// Sets coef and back to piece i, and their grids.
-void lay_piece(GradPlan *p, uint32_t i, uint32_t *coef_grid, uint32_t *back_grid);
+// Workgroups of a piece's launches.
+struct PieceGrid {
+    uint32_t coefficients, states, weights;
+};
+// Sets coef and back to piece i (pieces are laid one after the other).
+PieceGrid lay_piece(GradPlan *p, uint32_t i);
 rog_status plan_quantize(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q, int64_t q_stride,
                          float *scale, QuantizeArgs *a);
 rog_status plan_linear_i8(const int8_t *q, int64_t q_stride, const float *scale, size_t rows, int64_t dim, const rog_i8_shard *shards, int W,

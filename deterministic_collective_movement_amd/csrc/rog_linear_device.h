@@ -65,6 +65,13 @@ __device__ __forceinline__ uint32_t fresh_thread() {
     asm volatile("" : "+v"(t));
     return t;
 }
+// The kernel's one argument, to read anew likewise.
+template <class Args>
+__device__ __forceinline__ const Args &fresh_args() {
+    auto p = (const __attribute__((address_space(4))) Args *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const Args *)p;
+}
 // A window on [base, base + bytes), the same for all lanes.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const uint8_t *base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(uniform(base)), 0, int(uniform(bytes)), kBufferWord3);
@@ -314,12 +321,19 @@ constexpr int kStages = 4;
 
 // The shared memory of a tile: arrays of their own, so that the compiler can tell a
 // load in flight to one from a read of another (through one array it waits for all).
+#define ROG_STAGE_MEMORY(STAGES, I, A, B) __shared__ __attribute__((aligned(16))) uint8_t a##I[(STAGES) > I ? (A) : 16], b##I[(STAGES) > I ? (B) : 16]
 #define ROG_TILE_MEMORY(STAGES, A, B)                                                                           \
-    __shared__ __attribute__((aligned(16))) uint8_t a0[A], a1[A], a2[A], b0[B], b1[B], b2[B];                   \
-    __shared__ __attribute__((aligned(16))) uint8_t a3[(STAGES) > 3 ? (A) : 16], b3[(STAGES) > 3 ? (B) : 16];   \
-    const TileMemory memory = {{a0, a1, a2, a3}, {b0, b1, b2, b3}}
+    ROG_STAGE_MEMORY(STAGES, 0, A, B);                                                                          \
+    ROG_STAGE_MEMORY(STAGES, 1, A, B);                                                                          \
+    ROG_STAGE_MEMORY(STAGES, 2, A, B);                                                                          \
+    ROG_STAGE_MEMORY(STAGES, 3, A, B);                                                                          \
+    ROG_STAGE_MEMORY(STAGES, 4, A, B);                                                                          \
+    ROG_STAGE_MEMORY(STAGES, 5, A, B);                                                                          \
+    ROG_STAGE_MEMORY(STAGES, 6, A, B);                                                                          \
+    ROG_STAGE_MEMORY(STAGES, 7, A, B);                                                                          \
+    const TileMemory memory = {{a0, a1, a2, a3, a4, a5, a6, a7}, {b0, b1, b2, b3, b4, b5, b6, b7}}
 struct TileMemory {
-    uint8_t *a[kStages], *b[kStages];
+    uint8_t *a[8], *b[8];
 };
 
 // FM x FN fragments of a wave at (m0, n0) of the tile, over `steps` whole steps of K and, if `tail`, a last one that is not.
@@ -347,6 +361,8 @@ struct Tile {
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = Mat<DT>::mma(fa[set][i], fb[set][j], acc[i][j]);
     }
+    // With FOURS steps past the last whole one are multiplied as zeros, up to a multiple of four (less to hold in registers).
+    template <bool FOURS = false>
     __device__ __forceinline__ void run(A &a, B &b, uint32_t steps, bool tail, uint32_t m0, uint32_t n0, const TileMemory &mem,
                                         Acc (&acc)[FM][FN]) {
 #if defined(__HIP_DEVICE_COMPILE__)   // the compiler's host pass loses some kernels' stubs over what is in here
@@ -361,7 +377,7 @@ struct Tile {
         arrive<3 * kEach>();
         read(ra, rb, mem.a[0], mem.b[0], 0);
         // One way in and out of the loop, so that the accumulators stay where they are.
-        for (uint32_t k = 0; k + 4 <= steps; k += 4) {
+        for (uint32_t k = 0; FOURS ? k < steps : k + 4 <= steps; k += 4) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 arrive<2 * kEach>();
@@ -374,7 +390,7 @@ struct Tile {
                 Deal<FM * FN, kEach, FM * A::kReads + FN * B::kReads, 0>::slot();
             }
         }
-        const uint32_t rest = steps % 4;
+        const uint32_t rest = FOURS ? 0 : steps % 4;
         if (rest > 0) multiply(0, acc);
         arrive<0>();
         if (rest > 1) {
@@ -461,37 +477,86 @@ struct RowLines {
     }
 };
 
-// FM x FN fragments of a wave at (m0, n0) over `lines` steps of 128 bytes of K, STAGES - 1 of them in flight.
-template <int DT, int FM, int FN, int STAGES, class A, class B>
+// A step of 64 rows of K, 64 elements (a line) each.  As ColSteps, with two rows in the 256 bytes of the banks: the
+// 32-byte pieces p of a row are at p ^ turn(row).
+template <int THREADS, bool DIRECT>
+struct ColLines {
+    static constexpr int kBytes = 64 * 128;
+    static constexpr int kRows = THREADS / 8, kLoads = 64 / kRows;
+    static __device__ __forceinline__ uint32_t turn(uint32_t row) { return (row >> 1 & 1) | (row >> 3 & 1) << 1; }
+    const uint8_t *from;               // of the next step
+    uint32_t left, col_bytes;          // rows of K from there on, bytes of a row
+    int64_t stride;
+    __device__ __forceinline__ ColLines(const void *b, int64_t s, uint32_t rows, uint32_t cols_left)
+        : from(uniform(b)), left(uniform(rows)), col_bytes(cols_left * 2), stride(s) {}
+    __device__ __forceinline__ void stage(uint8_t *to) {
+        const uint32_t row = threadIdx.x / 8;
+        const auto r = window(from, (left < 64 ? left : 64) * uint32_t(stride));
+        vec16 v[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t k = row + i * kRows, at = (threadIdx.x % 8 ^ 2 * turn(k)) * 16;
+            if constexpr (DIRECT) {
+                lbyte *p = (lbyte *)to + (i * THREADS + uniform(threadIdx.x / 64) * 64) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16,
+                                                         at < col_bytes ? k * uint32_t(stride) + at : kOutside, 0, 0, 0);
+            } else {
+                v[i] = k < left ? row_bytes<2>((gbyte *)from + uint64_t(k) * uint64_t(stride), at, col_bytes) : vec16{0, 0, 0, 0};
+            }
+        }
+        if constexpr (!DIRECT)
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
+        from += 64 * uint32_t(stride);
+        left = left > 64 ? left - 64 : 0;
+    }
+    static __device__ __forceinline__ vec16 get(const uint8_t *from, uint32_t col0, int f, int ks) {
+        const uint32_t l = threadIdx.x % 64, j = l % 16, k = ks * 32 + l / 16 * 8 + j / 4;
+        const lbyte *p = (const lbyte *)from + k * 128 + ((col0 / 16 + f) ^ turn(k)) * 32 + 8 * (j % 4);
+        struct { s16x4 lo, hi; } v = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)p),
+                                      __builtin_amdgcn_ds_read_tr16_b64_v4i16((ls16x4 *)(p + 4 * 128))};
+        return __builtin_bit_cast(vec16, v);
+    }
+};
+
+// FM x FN fragments of a wave at (m0, n0) over `lines` steps of 128 bytes of K, GROUP of them at a time, up to
+// STAGES - GROUP in flight.
+template <int DT, int FM, int FN, int STAGES, int GROUP, class A, class B>
 struct Stream {
     typedef typename Mat<DT>::Acc Acc;
+    static_assert(STAGES % GROUP == 0 && STAGES >= 2 * GROUP, "whole groups");
     static __device__ __forceinline__ void run(A &a, B &b, uint32_t lines, uint32_t m0, uint32_t n0, const TileMemory &mem, Acc (&acc)[FM][FN]) {
 #if defined(__HIP_DEVICE_COMPILE__)   // as in Tile
         constexpr int kEach = A::kLoads + B::kLoads;
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) {
+        for (int i = 0; i < STAGES - GROUP; ++i) {
             a.stage(mem.a[i]);
             b.stage(mem.b[i]);
         }
         // past the last step zeros are multiplied, which leaves the sums as they are
         for (uint32_t k = 0; k < lines; k += STAGES) {
 #pragma unroll
-            for (int i = 0; i < STAGES; ++i) {
-                arrive<(STAGES - 2) * kEach>();
-                a.stage(mem.a[(i + STAGES - 1) % STAGES]);
-                b.stage(mem.b[(i + STAGES - 1) % STAGES]);
+            for (int i = 0; i < STAGES; i += GROUP) {
+                arrive<(STAGES - 2 * GROUP) * kEach>();
+                vec16 fa[2 * GROUP][FM], fb[2 * GROUP][FN];
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    vec16 fa[FM], fb[FN];
+                for (int g = 0; g < 2 * GROUP; ++g) {
 #pragma unroll
-                    for (int f = 0; f < FM; ++f) fa[f] = A::get(mem.a[i], m0, f, ks);
+                    for (int f = 0; f < FM; ++f) fa[g][f] = A::get(mem.a[i + g / 2], m0, f, g % 2);
 #pragma unroll
-                    for (int f = 0; f < FN; ++f) fb[f] = B::get(mem.b[i], n0, f, ks);
+                    for (int f = 0; f < FN; ++f) fb[g][f] = B::get(mem.b[i + g / 2], n0, f, g % 2);
+                }
+#pragma unroll
+                for (int g = 0; g < GROUP; ++g) {
+                    a.stage(mem.a[(i + g + STAGES - GROUP) % STAGES]);
+                    b.stage(mem.b[(i + g + STAGES - GROUP) % STAGES]);
+                }
+#pragma unroll
+                for (int g = 0; g < 2 * GROUP; ++g)
 #pragma unroll
                     for (int f = 0; f < FM; ++f)
 #pragma unroll
-                        for (int j = 0; j < FN; ++j) acc[f][j] = Mat<DT>::mma(fa[f], fb[j], acc[f][j]);
-                }
+                        for (int j = 0; j < FN; ++j) acc[f][j] = Mat<DT>::mma(fa[g][f], fb[g][j], acc[f][j]);
             }
         }
         arrive<0>();
@@ -519,7 +584,7 @@ struct RowProduct<DT, F, DIRECT, ES, false> {
     typedef RowLines<false, F::kRows, F::kThreads, DIRECT, ES> B;
     template <class Acc>
     static __device__ __forceinline__ void run(A &a, B &b, uint32_t kbytes, uint32_t m0, uint32_t n0, const TileMemory &mem, Acc &acc) {
-        Stream<DT, F::kFM, F::kFN, F::kStages, A, B>::run(a, b, (kbytes + 127) / 128, m0, n0, mem, acc);
+        Stream<DT, F::kFM, F::kFN, F::kStages, 1, A, B>::run(a, b, (kbytes + 127) / 128, m0, n0, mem, acc);
     }
 };
 

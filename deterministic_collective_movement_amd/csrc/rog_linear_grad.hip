@@ -50,14 +50,81 @@ __device__ __forceinline__ void pair_all(f32x4 (&acc)[FM][FN]) {
             }
 }
 
-constexpr int kBM = 256;   // elements of the states and weights of a tile
-
 // What takes the scale of a row's coefficients off again.
 template <int DT, class Args>
 __device__ __forceinline__ float unscale(const Args &p, uint32_t row) {
     if constexpr (DT != ROG_DTYPE_F16) return 1.0f;
     else return 1.0f / power_for(most_of(p.g_logp[row], p.g_entropy ? p.g_entropy[row] : 0.0f, p.inv_t));
 }
+
+// A tile's sums of a segment to its partial sums, or added to the running ones, or to the end.
+template <int DT, int FM, int FN, int WN>
+__device__ __forceinline__ void put_states(uint32_t s, uint32_t d0, uint32_t n0, uint32_t rows, f32x4 (&acc)[FM][FN]) {
+    const BackArgs &p = fresh_args<BackArgs>();
+    const bool running = p.part_seg == 0, first = running && p.first && s == 0, last = running && p.last && s + 1 == p.segs;
+            pair_all(acc);
+            const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
+                    float *part = p.part + uint64_t(s) * p.part_seg;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const uint32_t n = n0 + w0 + 16 * j + l % 16;
+                if (n >= rows) continue;
+                const uint32_t row = p.index[n];
+                const float inv = last ? unscale<DT>(p, row) : 1.0f;
+                uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
+#pragma unroll
+                for (int f = 0; f < FM / 2; ++f) {
+                    const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
+                    if (d >= p.dim) continue;
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4];
+                    gf32x4_out *at = (gf32x4_out *)(part + uint64_t(n) * p.dim_pad + d);
+                    if (running && !first) {
+                        const f32x4 lo = at[0], hi = at[1];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = (i < 4 ? lo[i % 4] : hi[i % 4]) + x[i];
+                    }
+                    if (last) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] *= inv;
+                        put8<DT>(out + d * 2, x, p.dim - d);
+                    } else {
+                        at[0] = f32x4{x[0], x[1], x[2], x[3]};
+                        at[1] = f32x4{x[4], x[5], x[6], x[7]};
+                    }
+                }
+            }
+}
+
+// A tile's sums for columns v0 on and elements d0 on of shard r.
+template <int DT, int FM, int FN, int WN>
+__device__ __forceinline__ void put_weights(uint32_t r, uint32_t v0, uint32_t d0, uint32_t width, f32x4 (&acc)[FM][FN]) {
+    const BackArgs &p = fresh_args<BackArgs>();
+    pair_all(acc);
+    const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
+    const float inv = DT == ROG_DTYPE_F16 ? 1.0f / *p.g_scale : 1.0f;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const uint32_t v = v0 + w0 + 16 * j + l % 16;
+        if (v >= width) continue;
+        uint8_t *out = static_cast<uint8_t *>(p.dw[r]) + uint64_t(v) * uint64_t(p.dw_stride[r]);
+#pragma unroll
+        for (int f = 0; f < FM / 2; ++f) {
+            const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
+            if (d >= p.dim) continue;
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4] * inv;
+            put8<DT>(out + d * 2, x, p.dim - d);
+        }
+    }
+}
+
+#ifndef ROG_GROUP
+#define ROG_GROUP 2
+#endif
+constexpr int kBM = 256;   // elements of the states and weights of a tile
 
 template <int DT, int BN, int WM, int WN, bool DIRECT>
 __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint32_t rows, const TileMemory &memory) {
@@ -82,42 +149,9 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
         f32x4 acc[FM][FN] = {};
         const uint32_t wave = fresh_thread() / 64;
         if (s != begin) __syncthreads();               // the last slab's readers
-        Tile<DT, FM, FN, A, B>().run(a, b, (cols + 31) / 32, false, wave / WN * (FM * 16), wave % WN * (FN * 16), memory, acc);
+        Tile<DT, FM, FN, A, B>().template run<true>(a, b, (cols + 31) / 32, false, wave / WN * (FM * 16), wave % WN * (FN * 16), memory, acc);
 
-        pair_all(acc);
-        const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
-        const bool first = running && p.first && s == 0, last = running && p.last && s + 1 == p.segs;
-        float *part = p.part + uint64_t(s) * p.part_seg;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const uint32_t n = n0 + w0 + 16 * j + l % 16;
-            if (n >= rows) continue;
-            const uint32_t row = p.index[n];
-            const float inv = last ? unscale<DT>(p, row) : 1.0f;
-            uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
-#pragma unroll
-            for (int f = 0; f < FM / 2; ++f) {
-                const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
-                if (d >= p.dim) continue;
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4];
-                gf32x4_out *at = (gf32x4_out *)(part + uint64_t(n) * p.dim_pad + d);
-                if (running && !first) {
-                    const f32x4 lo = at[0], hi = at[1];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = (i < 4 ? lo[i % 4] : hi[i % 4]) + x[i];
-                }
-                if (last) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= inv;
-                    put8<DT>(out + d * 2, x, p.dim - d);
-                } else {
-                    at[0] = f32x4{x[0], x[1], x[2], x[3]};
-                    at[1] = f32x4{x[4], x[5], x[6], x[7]};
-                }
-            }
-        }
+        put_states<DT, FM, FN, WN>(s, d0, n0, rows, acc);
     }
 }
 
@@ -126,49 +160,98 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
     constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
     typedef ColSteps<kBM, THREADS, true> A;
     typedef ColSteps<BN, THREADS, true> B;
-    const TileAt at = tile_at(id, p.dim_tiles, p.tiles * (256 / BN));
-    const uint32_t tile = p.tile_begin + at.n / (256 / BN), d0 = at.m * kBM;
-    const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * 256 + at.n % (256 / BN) * BN;
-    const uint32_t width = p.sh.s[r].width;
-    if (v0 >= width) return;
+    static_assert(BN == int(kGradTile), "a tile of the piece");
+    const TileAt at = tile_at(id, p.dim_tiles, p.tiles);
+    const uint32_t tile = p.tile_begin + at.n, d0 = at.m * kBM;
+    const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * kGradTile, width = p.sh.s[r].width;
     A a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
     B b(static_cast<const uint8_t *>(p.g_all) + uint64_t(at.n) * BN * 2, p.g_stride, rows, BN);
-    const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
-    const uint32_t m0 = wave / WN * (FM * 16), w0 = wave % WN * (FN * 16);
+    const uint32_t wave = fresh_thread() / 64;
     f32x4 acc[FM][FN] = {};
-    Tile<DT, FM, FN, A, B>().run(a, b, (rows + 31) / 32, false, m0, w0, memory, acc);
+    Tile<DT, FM, FN, A, B>().run(a, b, (rows + 31) / 32, false, wave / WN * (FM * 16), wave % WN * (FN * 16), memory, acc);
 
-    pair_all(acc);
-    const float inv = DT == ROG_DTYPE_F16 ? 1.0f / *p.g_scale : 1.0f;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const uint32_t v = v0 + w0 + 16 * j + l % 16;
-        if (v >= width) continue;
-        uint8_t *out = static_cast<uint8_t *>(p.dw[r]) + uint64_t(v) * uint64_t(p.dw_stride[r]);
-#pragma unroll
-        for (int f = 0; f < FM / 2; ++f) {
-            const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
-            if (d >= p.dim) continue;
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4] * inv;
-            put8<DT>(out + d * 2, x, p.dim - d);
-        }
-    }
+    put_weights<DT, FM, FN, WN>(r, v0, d0, width, acc);
 }
 
 // The states' tiles first: their chains are the longer ones of all but large batches.
 template <int DT, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
-    constexpr int BV = BN < 128 ? 128 : BN;
-    ROG_TILE_MEMORY(kStages, kBM * kStepBytes, BV * kStepBytes);
+    ROG_TILE_MEMORY(kStages, kBM * kStepBytes, BN * kStepBytes);
     const uint32_t rows = uniform(*p.a.count), states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
     if (blockIdx.x < states) {
         back_states<DT, BN, WM, WN, DIRECT>(p, blockIdx.x, rows, memory);
         return;
     }
     const uint32_t id = blockIdx.x - states;
-    if (id < p.dim_tiles * p.tiles * (256 / BV)) back_weights<DT, BV, WM, WN>(p, id, rows, memory);
+    if (id < p.dim_tiles * p.tiles) back_weights<DT, BN, WM, WN>(p, id, rows, memory);
+}
+
+// The same for up to 64 rows, bound by the weights' and their gradients' bytes.  d_hidden: 64 elements of a
+// segment for all rows, with seven lines of each operand's rows in flight (a chain over a segment cannot be cut
+// further, so a workgroup has to bring its share of the weights fast).
+constexpr int kFewElements = 64, kFewSide = 128, kFewThreads = 256, kFewStages = 8;
+template <int DT, bool DIRECT>
+__global__ __launch_bounds__(kFewThreads) void rog_linear_few_states_kernel(BackArgs p) {
+    typedef ColLines<kFewThreads, DIRECT> A;
+    typedef RowLines<false, 64, kFewThreads, true, 2> B;
+    ROG_TILE_MEMORY(kFewStages, A::kBytes, B::kBytes);
+    const uint32_t rows = uniform(*p.a.count), dim_tiles = (p.dim + kFewElements - 1) / kFewElements;
+    if (!rows) return;
+    const uint32_t s = blockIdx.x / dim_tiles, d0 = blockIdx.x % dim_tiles * kFewElements, seg = p.seg_begin + s;
+    uint32_t r = 0;
+    while (seg >= p.seg0[r + 1]) ++r;
+    const WeightShard sh = p.sh.s[r];
+    const uint32_t tile = (seg - p.seg0[r]) * p.seg_tiles, v0 = tile * kGradTile;
+    const uint32_t cols = sh.width - v0 < p.seg_tiles * kGradTile ? sh.width - v0 : p.seg_tiles * kGradTile;
+    A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride) + d0 * 2, sh.stride, cols, p.dim - d0);
+    B b(static_cast<const uint8_t *>(p.g) + uint64_t(p.sh.tile0[r] + tile - p.tile_begin) * kGradTile * 2, p.g_stride, rows,
+        (cols + 63) / 64 * 128);
+    const uint32_t wave = threadIdx.x / 64;
+    f32x4 acc[2][2] = {};
+    Stream<DT, 2, 2, kFewStages, ROG_GROUP, A, B>::run(a, b, (cols + 63) / 64, wave / 2 * 32, wave % 2 * 32, memory, acc);
+    put_states<DT, 2, 2, 2>(s, d0, 0, rows, acc);
+}
+
+// d_weight: 128 columns x 128 elements, whose K is at most two steps.
+template <int DT>
+__global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(BackArgs p) {
+    typedef ColSteps<kFewSide, kFewThreads, true> C;
+    ROG_TILE_MEMORY(2, C::kBytes, C::kBytes);
+    const uint32_t rows = uniform(*p.a.count), sides = (p.dim + kFewSide - 1) / kFewSide;
+    const uint32_t part = blockIdx.x / sides, d0 = blockIdx.x % sides * kFewSide;       // of the piece's parts of 128 columns
+    const uint32_t tile = p.tile_begin + part / 2, r = shard_of_tile(p.sh, tile);
+    const uint32_t v0 = (tile - p.sh.tile0[r]) * kGradTile + part % 2 * kFewSide, width = p.sh.s[r].width;
+    if (v0 >= width) return;
+    C a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
+    C b(static_cast<const uint8_t *>(p.g_all) + uint64_t(part) * kFewSide * 2, p.g_stride, rows, kFewSide);
+    const uint32_t wave = threadIdx.x / 64;
+    f32x4 acc[4][4] = {};
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint32_t m0 = wave / 2 * 64, w0 = wave % 2 * 64;
+    const typename C::template Reader<0> ra(m0), rb(w0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        a.stage(memory.a[i]);
+        b.stage(memory.b[i]);
+    }
+    arrive<0>();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        vec16 fa[4], fb[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            fa[f] = ra.get(memory.a[i], f);
+            fb[f] = rb.get(memory.b[i], f);
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[f][j] = Mat<DT>::mma(fa[f], fb[j], acc[f][j]);
+    }
+    put_weights<DT, 4, 4, 2>(r, v0, d0, width, acc);
+#else
+    (void)acc, (void)memory, (void)wave;
+#endif
 }
 
 // Adds the segments' partial sums of a row in their order.
@@ -204,12 +287,13 @@ hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const A
 }
 
 template <int DT>
-hipError_t launch_back(const GradPlan &p, const BackArgs &a, uint32_t grid, hipStream_t s) {
+hipError_t launch_back(const GradPlan &p, const BackArgs &a, const PieceGrid &grid, hipStream_t s) {
     if (p.form == kFormWide)
-        return p.direct_back ? launch(rog_linear_back_kernel<DT, 256, 2, 4, true>, grid, 512, a, s)
-                        : launch(rog_linear_back_kernel<DT, 256, 2, 4, false>, grid, 512, a, s);
-    return p.direct_back ? launch(rog_linear_back_kernel<DT, 64, 4, 1, true>, grid, 256, a, s)
-                    : launch(rog_linear_back_kernel<DT, 64, 4, 1, false>, grid, 256, a, s);
+        return p.direct_back ? launch(rog_linear_back_kernel<DT, 256, 2, 4, true>, grid.states + grid.weights, 512, a, s)
+                             : launch(rog_linear_back_kernel<DT, 256, 2, 4, false>, grid.states + grid.weights, 512, a, s);
+    const hipError_t e = p.direct_back ? launch(rog_linear_few_states_kernel<DT, true>, grid.states, kFewThreads, a, s)
+                                       : launch(rog_linear_few_states_kernel<DT, false>, grid.states, kFewThreads, a, s);
+    return e != hipSuccess ? e : launch(rog_linear_few_weights_kernel<DT>, grid.weights, kFewThreads, a, s);
 }
 
 }  // namespace
@@ -230,11 +314,10 @@ ROG_API rog_status rog_linear_logprob_grad(const void *hidden, int64_t hidden_st
     if (st != ROG_OK || rows == 0) return st;
     hipError_t e = launch_pack(p.pack, stream);
     for (uint32_t i = 0; i < p.pieces && e == hipSuccess; ++i) {
-        uint32_t coef_grid = 0, back_grid = 0;
-        lay_piece(&p, i, &coef_grid, &back_grid);
-        e = launch_coefficients(p, p.coef, coef_grid, stream);
-        if (e == hipSuccess) e = dtype == ROG_DTYPE_BF16 ? launch_back<ROG_DTYPE_BF16>(p, p.back, back_grid, stream)
-                                                         : launch_back<ROG_DTYPE_F16>(p, p.back, back_grid, stream);
+        const PieceGrid grid = lay_piece(&p, i);
+        e = launch_coefficients(p, p.coef, grid.coefficients, stream);
+        if (e == hipSuccess) e = dtype == ROG_DTYPE_BF16 ? launch_back<ROG_DTYPE_BF16>(p, p.back, grid, stream)
+                                                         : launch_back<ROG_DTYPE_F16>(p, p.back, grid, stream);
     }
     if (e == hipSuccess && p.join_grid)
         e = dtype == ROG_DTYPE_BF16 ? launch(rog_linear_back_join_kernel<ROG_DTYPE_BF16>, p.join_grid, 256, p.join, stream)

@@ -210,7 +210,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
         segs += uint32_t(ceil_div(a.sh.tile0[r + 1] - a.sh.tile0[r], k.seg_tiles));
     }
     k.seg0[W] = segs;
-    p->running = uint64_t(k.dim_tiles) * k.row_tiles >= 128;
+    p->running = p->form == kFormWide && uint64_t(k.dim_tiles) * k.row_tiles >= 128;
     // Pieces are runs of whole segments: as many as the bytes allow.
     const uint64_t tile_bytes = std::max<uint64_t>(1, rows) * kGradTile * 2;
     uint64_t tiles = std::max<uint64_t>(1, ROG_LINEAR_PIECE_BYTES / tile_bytes);
@@ -235,7 +235,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     }
     p->piece_tiles = std::max(p->piece_tiles, 1u);
     const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2;
-    const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 2;
+    const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * 4 * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 4;
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
     const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), rows_at = w.take(rows * packed);
@@ -333,7 +333,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     return ROG_OK;
 }
 
-void lay_piece(GradPlan *p, uint32_t i, uint32_t *coef_grid, uint32_t *back_grid) {
+PieceGrid lay_piece(GradPlan *p, uint32_t i) {
     GradArgs &a = p->coef;
     BackArgs &k = p->back;
     const uint32_t W = a.sh.W, segs = k.seg0[W];
@@ -356,8 +356,9 @@ full:
     k.last = s == segs;
     a.tile_begin = k.tile_begin;
     a.tiles = k.tiles;
-    *coef_grid = k.tiles * k.row_tiles * (kGradTile / tile_columns(p->form));
-    *back_grid = (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles + k.dim_tiles * k.tiles * (p->form == kFormWide ? 1 : 2);
+    const uint32_t coefficients = k.tiles * k.row_tiles * (kGradTile / tile_columns(p->form));
+    if (p->form == kFormWide) return PieceGrid{coefficients, (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles, k.dim_tiles * k.tiles};
+    return PieceGrid{coefficients, k.segs * uint32_t(ceil_div(k.dim, 64)), uint32_t(ceil_div(k.dim, 128)) * k.tiles * 2};
 }
 
 rog_status plan_quantize(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q, int64_t q_stride,
@@ -447,7 +448,7 @@ ROG_API rog_status rog_linear_logprob_grad_plan(const rog_weight_shard *shards, 
                                                 nullptr, 0, nullptr, nullptr, 0, false, &p);
     if (st != ROG_OK) return st;
     *info = rog_linear_plan_info{rows ? rog::kGradTile : 0, rows ? (p.form == rog::kFormWide ? 256u : 64u) : 0, rows ? p.pieces : 0,
-                                 rows ? 1 + 2 * p.pieces + !p.running : 0, p.workspace_bytes};
+                                 rows ? 1 + (p.form == rog::kFormWide ? 2 : 3) * p.pieces + !p.running : 0, p.workspace_bytes};
     return ROG_OK;
 }
 

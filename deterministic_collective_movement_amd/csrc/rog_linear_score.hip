@@ -235,49 +235,56 @@ __global__ __launch_bounds__(ROWS == 1 ? 256 : 64 * ROWS) void rog_linear_join_k
     if (p.lse) p.lse[row] = lse;
 }
 
-// Packs the scored rows in their order: a workgroup counts those before its rows, then copies its own.
-constexpr uint32_t kPackRows = 32, kPackThreads = 256;
+// Packs the scored rows in their order: a workgroup counts those before its ROWS rows, then its waves copy them.
+constexpr uint32_t kPackThreads = 256;
+template <uint32_t ROWS>
 __global__ __launch_bounds__(kPackThreads) void rog_linear_pack_kernel(PackArgs p) {
-    __shared__ uint32_t sums[kPackThreads / 64], own[kPackRows];
-    __shared__ float most[kPackThreads / 64];
-    const uint32_t row0 = blockIdx.x * kPackRows, t = threadIdx.x;
+    constexpr uint32_t WAVES = kPackThreads / 64;
+    __shared__ uint32_t sums[WAVES];
+    __shared__ float most[WAVES];
+    const uint32_t row0 = blockIdx.x * ROWS, t = threadIdx.x, wave = t / 64, l = t % 64;
     uint32_t before = 0;
     for (uint32_t i = t; i < row0; i += kPackThreads) before += p.tokens[i] >= 0;
+    const uint64_t own = __ballot(l < ROWS && row0 + l < p.rows && p.tokens[row0 + l] >= 0);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
-    if (t % 64 == 0) sums[t / 64] = before;
-    if (t < kPackRows) own[t] = row0 + t < p.rows && p.tokens[row0 + t] >= 0;
+    if (l == 0) sums[wave] = before;
     __syncthreads();
     before = 0;
-    for (uint32_t i = 0; i < kPackThreads / 64; ++i) before += sums[i];
-    const uint32_t wave = t / 64, l = t % 64;
-    for (uint32_t i = 0; i < kPackRows && row0 + i < p.rows; ++i) {
+    for (uint32_t i = 0; i < WAVES; ++i) before += sums[i];
+    for (uint32_t i = wave; i < ROWS && row0 + i < p.rows; i += WAVES) {
         const uint32_t row = row0 + i;
-        const bool kept = own[i];
-        if (i % (kPackThreads / 64) == wave) {
+        if (own >> i & 1) {
+            const uint32_t at_row = before + uint32_t(__popcll(own & ((uint64_t(1) << i) - 1)));
             gbyte *from = (gbyte *)p.x + uint64_t(row) * uint64_t(p.stride);
-            if (kept) {
+            __attribute__((address_space(1))) uint8_t *to =
+                (__attribute__((address_space(1))) uint8_t *)p.packed + uint64_t(at_row) * p.packed_bytes;
+            for (uint32_t at = l * 16; at < p.packed_bytes; at += 4096) {
+                vec16 v[4];
+#pragma unroll
+                for (uint32_t u = 0; u < 4; ++u) v[u] = row_bytes<2>(from, at + u * 1024, p.kbytes);
+#pragma unroll
+                for (uint32_t u = 0; u < 4; ++u)
+                    if (at + u * 1024 < p.packed_bytes) *(gvec16any_out *)(to + at + u * 1024) = v[u];
+            }
+            if (l == 0) p.index[at_row] = row;
+        } else {
+            if (p.zero) {
                 __attribute__((address_space(1))) uint8_t *to =
-                    (__attribute__((address_space(1))) uint8_t *)p.packed + uint64_t(before) * p.packed_bytes;
-                for (uint32_t at = l * 16; at < p.packed_bytes; at += 1024)
-                    *(gvec16any_out *)(to + at) = row_bytes<2>(from, at, p.kbytes);
-                if (l == 0) p.index[before] = row;
-            } else {
-                if (p.zero) {
-                    __attribute__((address_space(1))) uint16_t *to =
-                        (__attribute__((address_space(1))) uint16_t *)((uint8_t *)p.zero + uint64_t(row) * uint64_t(p.zero_stride));
-                    for (uint32_t at = l; at < p.kbytes / 2; at += 64) to[at] = 0;
-                }
-                if (l == 0) {
-                    if (p.logp) p.logp[row] = 0;
-                    if (p.entropy) p.entropy[row] = 0;
-                    if (p.lse) p.lse[row] = 0;
-                }
+                    (__attribute__((address_space(1))) uint8_t *)p.zero + uint64_t(row) * uint64_t(p.zero_stride);
+                const uint32_t whole = p.kbytes & ~15u;
+                for (uint32_t at = l * 16; at < whole; at += 1024) *(gvec16any_out *)(to + at) = vec16any{0, 0, 0, 0};
+                if (whole + l * 2 < p.kbytes) *(__attribute__((address_space(1))) uint16_t *)(to + whole + l * 2) = 0;
+            }
+            if (l == 0) {
+                if (p.logp) p.logp[row] = 0;
+                if (p.entropy) p.entropy[row] = 0;
+                if (p.lse) p.lse[row] = 0;
             }
         }
-        before += kept;
     }
-    if (t == 0 && row0 + kPackRows >= p.rows) *p.count = before;
+    before += uint32_t(__popcll(own));
+    if (t == 0 && row0 + ROWS >= p.rows) *p.count = before;
     if (!p.g_scale || blockIdx.x) return;
     // one scale of all rows' coefficients, for the products that sum over rows
     float m = 0;
@@ -423,7 +430,9 @@ hipError_t launch_coef(const GradPlan &p, const GradArgs &a, uint32_t grid, hipS
 }  // namespace
 
 hipError_t launch_pack(const PackArgs &a, hipStream_t s) {
-    return launch(rog_linear_pack_kernel, (a.rows + kPackRows - 1) / kPackRows, kPackThreads, a, s);
+    // every workgroup reads the tokens before its rows: few rows each while there are few tokens
+    return a.rows <= 16384 ? launch(rog_linear_pack_kernel<8>, (a.rows + 7) / 8, kPackThreads, a, s)
+                           : launch(rog_linear_pack_kernel<64>, (a.rows + 63) / 64, kPackThreads, a, s);
 }
 
 hipError_t launch_coefficients(const GradPlan &p, const GradArgs &a, uint32_t grid, hipStream_t s) {
