@@ -164,18 +164,21 @@ template <int COLUMNS, int ROWS, int WM, int WN, int STAGES, bool WIDE>
 struct Form {
     static constexpr int kColumns = COLUMNS, kRows = ROWS, kWM = WM, kWN = WN, kStages = STAGES, kThreads = 64 * WM * WN;
     static constexpr int kFM = COLUMNS / WM / 16, kFN = ROWS / WN / 16;
-    static constexpr bool kWide = WIDE;
+    static constexpr bool kWide = WIDE, kTail = COLUMNS == 256;   // the largest tile: see place_of()
     // waves that share a block of columns
     static constexpr int kShare = COLUMNS / WM < int(kLinearBlock) ? int(kLinearBlock) / (COLUMNS / WM) : 1;
     static_assert(COLUMNS % kLinearBlock == 0 && COLUMNS / WM % 32 == 0 && COLUMNS / WM <= int(kLinearBlock), "whole leaves, blocks");
 };
-#ifndef ROG_FEWST
-#define ROG_FEWST 4
-#endif
-typedef Form<128, 32, 4, 1, ROG_FEWST, false> FormFew;
+typedef Form<128, 32, 4, 1, 4, false> FormFew;
 typedef Form<128, 64, 4, 1, 3, false> FormSome;
 typedef Form<128, 128, 2, 2, 4, true> FormMid;
 typedef Form<256, 256, 2, 4, 4, true> FormWide;
+typedef Form<128, 128, 2, 4, 4, true> FormQuarter;   // of a wide tile, by as many threads
+constexpr uint32_t kCus = 256;         // workgroups of the wide form that run at a time
+#ifndef ROG_TAIL_SPLIT
+#define ROG_TAIL_SPLIT 64
+#endif
+constexpr uint32_t kTailSplit = ROG_TAIL_SPLIT;
 enum { kFormFew = 0, kFormSome = 1, kFormMid = 2, kFormWide = 3 };
 
 struct ScorePlan {

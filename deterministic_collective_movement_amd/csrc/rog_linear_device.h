@@ -616,6 +616,22 @@ __device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tm, uint32_t tn)
     return TileAt{group * kGroup + in % gm, in / gm};
 }
 
+// A workgroup's tile of the wide form: the tiles past the last whole round of the
+// CUs are dealt out in quarters (kTailSplit) where they would leave half of the
+// CUs or more idle.
+struct Place {
+    TileAt at;
+    uint32_t quarter;                  // 4: the whole tile
+    bool none;
+};
+__device__ __forceinline__ Place place_of(uint32_t id, uint32_t tm, uint32_t tn) {
+    const uint32_t all = tm * tn, over = all % kCus, whole = over <= kTailSplit ? all - over : all;
+    if (id < whole) return Place{tile_at(id, tm, tn), 4, false};
+    const uint32_t q = id - whole;
+    if (whole == all || q >= 4 * over) return Place{TileAt{0, 0}, 4, true};
+    return Place{tile_at(whole + q / 4, tm, tn), q % 4, false};
+}
+
 __device__ __forceinline__ uint32_t shard_of_tile(const WeightShards &h, uint32_t tile) {
     uint32_t r = 0;
     while (tile >= h.tile0[r + 1]) ++r;

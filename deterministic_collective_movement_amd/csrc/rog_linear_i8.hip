@@ -116,19 +116,15 @@ __device__ __forceinline__ void put_out(uint8_t *to, const float (&x)[8], uint32
     }
 }
 
+// The tile of F's size at columns v0 of shard r and rows n0.
 template <int OT, class F, bool DIRECT>
-__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_i8_kernel(LinearI8Args p) {
-    constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN;
+__device__ __forceinline__ void i8_tile(const LinearI8Args &p, uint32_t r, uint32_t v0, uint32_t n0, const TileMemory &memory) {
+    constexpr int FM = F::kFM, FN = F::kFN;
     typedef RowProduct<kTypeI8, F, DIRECT, 1, F::kWide> Product;
-    typedef typename Product::A A;
-    typedef typename Product::B B;
-    ROG_TILE_MEMORY(F::kStages, A::kBytes, B::kBytes);
-    const uint32_t rows = p.a.rows, tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
-    const TileAt at = tile_at(blockIdx.x, tm, tn);
-    const uint32_t r = shard_of_tile(p.sh, at.m), v0 = (at.m - p.sh.tile0[r]) * BM, n0 = at.n * BN;
     const WeightShard sh = p.sh.s[r];
-    A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
-    B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
+    const uint32_t rows = p.a.rows;
+    typename Product::A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    typename Product::B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
     i32x4 acc[FM][FN] = {};
@@ -153,6 +149,29 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_i8_k
             for (int i = 0; i < 8; ++i) x[i] = float(acc[2 * f + i / 4][j][i % 4]) * s * scale[i];
             put_out<OT>(static_cast<uint8_t *>(p.out[r]) + uint64_t(n) * uint64_t(p.out_stride[r]) + uint64_t(v) * OS, x, left);
         }
+    }
+}
+
+template <int OT, class F, bool DIRECT>
+__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_i8_kernel(LinearI8Args p) {
+    typedef RowProduct<kTypeI8, F, DIRECT, 1, F::kWide> Product;
+    constexpr uint32_t BM = F::kColumns, BN = F::kRows;
+    ROG_TILE_MEMORY(F::kStages, Product::A::kBytes, Product::B::kBytes);
+    const uint32_t tm = p.sh.tile0[p.sh.W], tn = (p.a.rows + BN - 1) / BN;
+    if constexpr (F::kTail) {
+        const Place o = place_of(blockIdx.x, tm, tn);
+        if (o.none) return;
+        const uint32_t r = shard_of_tile(p.sh, o.at.m), v0 = (o.at.m - p.sh.tile0[r]) * BM, n0 = o.at.n * BN;
+        if (o.quarter == 4) {
+            i8_tile<OT, F, DIRECT>(p, r, v0, n0, memory);
+        } else {
+            const uint32_t v = v0 + o.quarter % 2 * FormQuarter::kColumns, n = n0 + o.quarter / 2 * FormQuarter::kRows;
+            if (v < p.sh.s[r].width && n < p.a.rows) i8_tile<OT, FormQuarter, DIRECT>(p, r, v, n, memory);
+        }
+    } else {
+        const TileAt at = tile_at(blockIdx.x, tm, tn);
+        const uint32_t r = shard_of_tile(p.sh, at.m);
+        i8_tile<OT, F, DIRECT>(p, r, (at.m - p.sh.tile0[r]) * BM, at.n * BN, memory);
     }
 }
 

@@ -23,6 +23,9 @@ constexpr double kLog2E = 1.4426950408889634;
 #ifndef ROG_LINEAR_ROW_PAD
 #define ROG_LINEAR_ROW_PAD 256
 #endif
+#ifndef ROG_MID_TILES
+#define ROG_MID_TILES 128
+#endif
 #ifndef ROG_LINEAR_PIECE_BYTES
 #define ROG_LINEAR_PIECE_BYTES (256ull << 20)
 #endif
@@ -76,13 +79,20 @@ void lay_tiles(WeightShards *h, uint32_t tile) {
 }
 
 // The tile for so many rows.
-int32_t form_of(uint64_t rows) {
-    return rows <= FormFew::kRows ? kFormFew : rows <= FormSome::kRows ? kFormSome : rows <= FormMid::kRows ? kFormMid : kFormWide;
+int32_t form_of(uint64_t rows, const WeightShards &h) {
+    if (rows <= FormSome::kRows) return rows <= FormFew::kRows ? kFormFew : kFormSome;
+    uint64_t wide = 0;
+    for (uint32_t r = 0; r < h.W; ++r) wide += ceil_div(h.s[r].width, FormWide::kColumns);
+    wide *= ceil_div(rows, FormWide::kRows);
+    return rows <= FormMid::kRows || wide <= ROG_MID_TILES ? kFormMid : kFormWide;
 }
 constexpr uint32_t kFormColumns[] = {FormFew::kColumns, FormSome::kColumns, FormMid::kColumns, FormWide::kColumns};
 constexpr uint32_t kFormRows[] = {FormFew::kRows, FormSome::kRows, FormMid::kRows, FormWide::kRows};
 uint32_t tile_columns(int32_t form) { return kFormColumns[form]; }
 uint32_t tile_rows(int32_t form) { return kFormRows[form]; }
+
+// Workgroups for so many tiles: the wide form deals some of them out in quarters, by the rows that there turn out to be.
+uint64_t groups_of(uint64_t tiles, int32_t form) { return form == kFormWide && tiles ? tiles + 3 * kTailSplit : tiles; }
 
 constexpr uint64_t kPackFrom = 65;   // rows from which the scored ones are packed
 
@@ -116,12 +126,12 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     if (rows >= kMaxVocab) return ROG_ERR_TOO_LARGE;
     if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false);
     if (st != ROG_OK) return st;
-    p->form = form_of(rows);
+    p->form = form_of(rows, a.sh);
     p->packs = has_tokens && rows >= kPackFrom;
     lay_tiles(&a.sh, tile_columns(p->form));
     const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
     if (!p->packs && !aligned(hidden, rows > 1 ? uint64_t(hidden_stride) * 2 : 0)) p->direct = false;
-    const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
+    const uint64_t groups = groups_of(a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form)), p->form);
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);
     const uint32_t blocks = a.sh.block0[W], rows_pad = uint32_t(up(rows, 16));
@@ -234,7 +244,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
         ++p->pieces;
     }
     p->piece_tiles = std::max(p->piece_tiles, 1u);
-    const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2;
+    const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2 + 3 * kTailSplit;
     const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * 4 * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 4;
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
@@ -356,7 +366,7 @@ full:
     k.last = s == segs;
     a.tile_begin = k.tile_begin;
     a.tiles = k.tiles;
-    const uint32_t coefficients = k.tiles * k.row_tiles * (kGradTile / tile_columns(p->form));
+    const uint32_t coefficients = uint32_t(groups_of(k.tiles * uint64_t(k.row_tiles) * (kGradTile / tile_columns(p->form)), p->form));
     if (p->form == kFormWide) return PieceGrid{coefficients, (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles, k.dim_tiles * k.tiles};
     return PieceGrid{coefficients, k.segs * uint32_t(ceil_div(k.dim, 64)), uint32_t(ceil_div(k.dim, 128)) * k.tiles * 2};
 }
@@ -413,10 +423,10 @@ rog_status plan_linear_i8(const int8_t *q, int64_t q_stride, const float *scale,
                 (s < r && overlap(o, matrix(a.out[s], rows, a.out_stride[s], uint64_t(a.sh.s[s].width) * os))))
                 return ROG_ERR_OVERLAP;
     }
-    p->form = form_of(rows);
+    p->form = form_of(rows, a.sh);
     lay_tiles(&a.sh, tile_columns(p->form));
     if (!aligned(q, rows > 1 ? uint64_t(q_stride) : 0)) p->direct = false;
-    const uint64_t groups = a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form));
+    const uint64_t groups = groups_of(a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form)), p->form);
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);
     a.a = LinearRows{q, q_stride, nullptr, uint32_t(rows), uint32_t(dim)};

@@ -106,25 +106,18 @@ __device__ __forceinline__ void put_part(float *states, uint64_t at, const Part 
     *((gstate *)states + at) = f32x4{p.m, p.s, p.t, 0};
 }
 
+// The tile of F's size at columns v0 of shard r and rows n0.
 template <int DT, class F, bool DIRECT>
-__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_score_kernel(ScoreArgs p) {
+__device__ __forceinline__ void score_tile(const ScoreArgs &p, uint32_t r, uint32_t v0, uint32_t n0, uint32_t rows, const TileMemory &memory,
+                                           uint32_t *targets, Part *shared_parts) {
     constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2;
     typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
-    typedef typename Product::A A;
-    typedef typename Product::B B;
-    ROG_TILE_MEMORY(F::kStages, A::kBytes, B::kBytes);
-    const uint32_t rows = uniform(p.a.count ? *p.a.count : p.a.rows);
-    const uint32_t tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
-    if (blockIdx.x >= tm * tn) return;
-    const TileAt at = tile_at(blockIdx.x, tm, tn);
-    const uint32_t r = shard_of_tile(p.sh, at.m), v0 = (at.m - p.sh.tile0[r]) * BM, n0 = at.n * BN;
     const WeightShard sh = p.sh.s[r];
-    A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
-    B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
+    typename Product::A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    typename Product::B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
     // the rows' tokens as columns of the tile, all others past it
-    __shared__ uint32_t targets[BN];
     if (threadIdx.x < BN) {
         const uint32_t n = n0 + threadIdx.x;
         const int64_t tok = p.tokens && n < rows ? p.tokens[p.index ? p.index[n] : n] - int64_t(sh.col0) - int64_t(v0) : -1;
@@ -134,7 +127,6 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_scor
     Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
     // lane l holds columns v0 + m0 + 32 f + 8 (l / 16) + 0 .. 7 of leaf f, row n0 + w0 + 16 j + l % 16
-    __shared__ Part shared_parts[F::kShare][F::kShare > 1 ? BN : 1];
     const uint32_t own = 8 * (l / 16);
     if (v0 + m0 + FM * 16 > sh.width) {
 #pragma unroll
@@ -164,7 +156,7 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_scor
             if (l < 16 && n < rows && block < p.sh.block0[r + 1])
                 put_part(p.states, uint64_t(n) * p.row_step + uint64_t(block) * p.block_step, part);
         } else if (l < 16) {
-            shared_parts[m0 / (FM * 16)][w0 + 16 * j + l] = part;
+            shared_parts[m0 / (FM * 16) * BN + w0 + 16 * j + l] = part;
         }
     }
     if constexpr (F::kShare > 1) {
@@ -173,10 +165,36 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_scor
         __syncthreads();
         const uint32_t n = n0 + threadIdx.x;
         if (threadIdx.x < BN && n < rows) {
-            Part all = join(shared_parts[0][threadIdx.x], shared_parts[1][threadIdx.x]);
-            if constexpr (F::kShare == 4) all = join(all, join(shared_parts[2][threadIdx.x], shared_parts[3][threadIdx.x]));
+            Part all = join(shared_parts[threadIdx.x], shared_parts[BN + threadIdx.x]);
+            if constexpr (F::kShare == 4) all = join(all, join(shared_parts[2 * BN + threadIdx.x], shared_parts[3 * BN + threadIdx.x]));
             put_part(p.states, uint64_t(n) * p.row_step + uint64_t(p.sh.block0[r] + v0 / kLinearBlock) * p.block_step, all);
         }
+    }
+}
+
+template <int DT, class F, bool DIRECT>
+__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_score_kernel(ScoreArgs p) {
+    typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
+    constexpr uint32_t BM = F::kColumns, BN = F::kRows;
+    ROG_TILE_MEMORY(F::kStages, Product::A::kBytes, Product::B::kBytes);
+    __shared__ uint32_t targets[BN];
+    __shared__ Part parts[F::kTail ? FormQuarter::kShare * FormQuarter::kRows : F::kShare > 1 ? F::kShare * BN : 1];
+    const uint32_t rows = uniform(p.a.count ? *p.a.count : p.a.rows), tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
+    if constexpr (F::kTail) {
+        const Place o = place_of(blockIdx.x, tm, tn);
+        if (o.none) return;
+        const uint32_t r = shard_of_tile(p.sh, o.at.m), v0 = (o.at.m - p.sh.tile0[r]) * BM, n0 = o.at.n * BN;
+        if (o.quarter == 4) {
+            score_tile<DT, F, DIRECT>(p, r, v0, n0, rows, memory, targets, parts);
+        } else {
+            const uint32_t v = v0 + o.quarter % 2 * FormQuarter::kColumns, n = n0 + o.quarter / 2 * FormQuarter::kRows;
+            if (v < p.sh.s[r].width && n < rows) score_tile<DT, FormQuarter, DIRECT>(p, r, v, n, rows, memory, targets, parts);
+        }
+    } else {
+        if (blockIdx.x >= tm * tn) return;
+        const TileAt at = tile_at(blockIdx.x, tm, tn);
+        const uint32_t r = shard_of_tile(p.sh, at.m);
+        score_tile<DT, F, DIRECT>(p, r, (at.m - p.sh.tile0[r]) * BM, at.n * BN, rows, memory, targets, parts);
     }
 }
 
@@ -331,25 +349,18 @@ __device__ __forceinline__ RowOf coef_row(const GradArgs &p, uint32_t row, int64
     return r;
 }
 
+// The tile of F's size at columns v0 of shard r, which are columns g0 of the piece, and rows n0.
 template <int DT, class F, bool DIRECT>
-__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_coef_kernel(GradArgs p) {
-    constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2, SPLIT = int(kGradTile) / BM;
+__device__ __forceinline__ void coef_tile(const GradArgs &p, uint32_t r, uint32_t v0, uint32_t g0, uint32_t n0, uint32_t rows,
+                                          const TileMemory &memory, RowOf *row_of) {
+    constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2;
     typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
-    typedef typename Product::A A;
-    typedef typename Product::B B;
-    ROG_TILE_MEMORY(F::kStages, A::kBytes, B::kBytes);
-    const uint32_t rows = uniform(*p.a.count), tm = p.tiles * SPLIT, tn = (rows + BN - 1) / BN;
-    if (blockIdx.x >= tm * tn) return;
-    const TileAt at = tile_at(blockIdx.x, tm, tn);
-    const uint32_t tile = p.tile_begin + at.m / SPLIT;
-    const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * kGradTile + at.m % SPLIT * BM, n0 = at.n * BN;
     const WeightShard sh = p.sh.s[r];
-    if (v0 >= sh.width) return;        // nobody reads the coefficients of such a part
-    A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
-    B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
+    if (v0 >= sh.width || n0 >= rows) return;        // nobody reads the coefficients of such a part
+    typename Product::A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride), sh.stride, sh.width - v0, p.a.kbytes);
+    typename Product::B b(static_cast<const uint8_t *>(p.a.x) + uint64_t(n0) * uint64_t(p.a.stride), p.a.stride, rows - n0, p.a.kbytes);
     const uint32_t wave = threadIdx.x / 64, l = threadIdx.x % 64;
     const uint32_t m0 = wave / F::kWN * (FM * 16), w0 = wave % F::kWN * (FN * 16);
-    __shared__ RowOf row_of[BN];
     if (threadIdx.x < BN && n0 + threadIdx.x < rows) row_of[threadIdx.x] = coef_row<DT>(p, p.index[n0 + threadIdx.x], int64_t(sh.col0) + v0, BM);
     typename Mat<DT>::Acc acc[FM][FN] = {};
     Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
@@ -383,7 +394,7 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_coef
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = narrow_word<DT>(d + 2 * i);
             typedef __attribute__((address_space(1))) vec16 gvec16_out;
-            const uint64_t to = uint64_t(n) * uint64_t(p.g_stride) + (uint64_t(at.m) * BM + m0 + own + 32 * f) * 2;
+            const uint64_t to = uint64_t(n) * uint64_t(p.g_stride) + (uint64_t(g0) + m0 + own + 32 * f) * 2;
             *(gvec16_out *)((uint8_t *)p.g + to) = v;
             if constexpr (DT == ROG_DTYPE_F16) {
 #pragma unroll
@@ -393,6 +404,34 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_coef
                 *(gvec16_out *)((uint8_t *)p.g_all + to) = v;
             }
         }
+    }
+}
+
+template <int DT, class F, bool DIRECT>
+__global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_coef_kernel(GradArgs p) {
+    typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
+    constexpr uint32_t BM = F::kColumns, BN = F::kRows, SPLIT = kGradTile / BM;
+    ROG_TILE_MEMORY(F::kStages, Product::A::kBytes, Product::B::kBytes);
+    __shared__ RowOf row_of[BN];
+    const uint32_t rows = uniform(*p.a.count), tm = p.tiles * SPLIT, tn = (rows + BN - 1) / BN;
+    TileAt at;
+    uint32_t quarter = 4;
+    if constexpr (F::kTail) {
+        const Place o = place_of(blockIdx.x, tm, tn);
+        if (o.none) return;
+        at = o.at;
+        quarter = o.quarter;
+    } else {
+        if (blockIdx.x >= tm * tn) return;
+        at = tile_at(blockIdx.x, tm, tn);
+    }
+    const uint32_t tile = p.tile_begin + at.m / SPLIT, r = shard_of_tile(p.sh, tile);
+    const uint32_t v0 = (tile - p.sh.tile0[r]) * kGradTile + at.m % SPLIT * BM;
+    if (!F::kTail || quarter == 4) {
+        coef_tile<DT, F, DIRECT>(p, r, v0, at.m * BM, at.n * BN, rows, memory, row_of);
+    } else if constexpr (F::kTail) {
+        const uint32_t m = quarter % 2 * FormQuarter::kColumns, n = quarter / 2 * FormQuarter::kRows;
+        coef_tile<DT, FormQuarter, DIRECT>(p, r, v0 + m, at.m * BM + m, at.n * BN + n, rows, memory, row_of);
     }
 }
 
