@@ -1,5 +1,5 @@
 // rog_binding.cpp -- the quick way through the Python binding's argument
-// marshalling, for the vocabulary-side operators: a CPython module that reads
+// marshalling, for the vocabulary-side operators and the head's products: a CPython module that reads
 // tensors' addresses, types and shapes directly and calls the C interface
 // (include/rog.h).  Every function returns True if the call was enqueued and
 // False if anything about it is out of the ordinary -- an argument that the
@@ -24,6 +24,10 @@ struct Bound {
     decltype(&rog_logprob_ex) logprob = nullptr;
     decltype(&rog_logprob_grad) grad = nullptr;
     decltype(&rog_policy_loss) loss = nullptr;
+    decltype(&rog_linear_logprob) linear_logprob = nullptr;
+    decltype(&rog_linear_logprob_grad) linear_grad = nullptr;
+    decltype(&rog_quantize_i8) quantize = nullptr;
+    decltype(&rog_linear_i8) linear_i8 = nullptr;
     int max_peers = 0;
     PyObject *current_device = nullptr, *raw_stream = nullptr, *capturing = nullptr;
 } bound;
@@ -122,6 +126,59 @@ struct Shards {
             }
             if (t->size(0) != rows || t->scalar_type() != type || !on(*t, device) || (t->size(1) > 1 && t->stride(1) != 1)) return false;
             s[i] = rog_logit_shard{t->data_ptr(), t->stride(0), t->size(1)};
+        }
+        return true;
+    }
+};
+
+// A matrix that is contiguous within its rows; rows or columns of -1: any.
+struct Matrix {
+    void *p;
+    int64_t stride, rows, columns;
+    at::ScalarType type;
+    int device;
+    bool read(PyObject *o) {
+        const at::Tensor *t = tensor(o);
+        if (!t || t->dim() != 2 || !t->is_cuda() || (t->size(1) > 1 && t->stride(1) != 1)) return false;
+        *this = Matrix{t->data_ptr(), t->stride(0), t->size(0), t->size(1), t->scalar_type(), t->get_device()};
+        return true;
+    }
+    bool is(int64_t r, int64_t c, at::ScalarType want, int d) const { return rows == r && columns == c && type == want && device == d; }
+};
+
+// The items of a list or tuple of between 1 and 64, and no more than the library takes.
+bool items(PyObject *list, Py_ssize_t *n) {
+    if (!PyList_Check(list) && !PyTuple_Check(list)) return false;
+    *n = PySequence_Fast_GET_SIZE(list);
+    return *n >= 1 && *n <= 64 && *n <= bound.max_peers;
+}
+
+// Hidden states and the head's W weight matrices (a list or tuple).
+struct Head {
+    Matrix h;
+    rog_weight_shard s[64];
+    Py_ssize_t W = 0;
+    rog_dtype dtype = ROG_DTYPE_BF16;
+    bool read(PyObject *hidden, PyObject *list) {
+        if (!h.read(hidden) || !items(list, &W)) return false;
+        if (h.type != at::kChar && (!dtype_of(h.type, &dtype) || dtype == ROG_DTYPE_F32)) return false;
+        for (Py_ssize_t i = 0; i < W; ++i) {
+            Matrix m;
+            if (!m.read(PySequence_Fast_GET_ITEM(list, i)) || !m.is(m.rows, h.columns, h.type, h.device)) return false;
+            s[i] = rog_weight_shard{m.p, m.stride, m.rows};
+        }
+        return true;
+    }
+    // W matrices to write, of the weights' shapes, or [rows][width] of `type`.
+    bool outputs(PyObject *list, bool weights, at::ScalarType type, rog_grad_shard *g) const {
+        Py_ssize_t n;
+        if (!items(list, &n) || n != W) return false;
+        for (Py_ssize_t i = 0; i < W; ++i) {
+            Matrix m;
+            if (!m.read(PySequence_Fast_GET_ITEM(list, i)) ||
+                !m.is(weights ? s[i].width : h.rows, weights ? h.columns : s[i].width, type, h.device))
+                return false;
+            g[i] = rog_grad_shard{m.p, m.stride};
         }
         return true;
     }
@@ -239,6 +296,101 @@ PyObject *py_loss(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// linear_logprob(hidden, weights, tokens, temperature, out)
+PyObject *py_linear_logprob(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return answer([&] {
+        Head head;
+        float temperature;
+        rog_logprob_out out{};
+        const int64_t *tokens;
+        if (n != 5 || !head.read(a[0], a[1]) || head.h.type == at::kChar || !number(a[3], &temperature) || !PyTuple_Check(a[4]) ||
+            PyTuple_GET_SIZE(a[4]) != 5)
+            return false;
+        PyObject *const *o = &PyTuple_GET_ITEM(a[4], 0);
+        const int64_t rows = head.h.rows;
+        const int device = head.h.device;
+        if (!vector(a[2], rows, at::kLong, device, &tokens) || !vector(o[0], rows, at::kFloat, device, &out.logp) ||
+            !vector(o[1], rows, at::kFloat, device, &out.entropy) || !vector(o[2], rows, at::kFloat, device, &out.lse) ||
+            o[3] != Py_None || o[4] != Py_None)
+            return false;
+        const Where at(device, true);
+        return at.ok && launched([&] {
+            return bound.linear_logprob(head.h.p, head.h.stride, size_t(rows), head.h.columns, head.s, int(head.W), head.dtype, temperature,
+                                        tokens, &out, at.ws.address, at.ws.bytes, at.hip());
+        });
+    });
+}
+
+// linear_grad(hidden, weights, tokens, lse, entropy, g_logp, g_entropy, temperature, d_hidden, d_weights)
+PyObject *py_linear_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return answer([&] {
+        Head head;
+        Matrix d;
+        rog_grad_shard g[64];
+        float temperature;
+        const int64_t *tokens;
+        const float *v[4];
+        if (n != 10 || !head.read(a[0], a[1]) || head.h.type == at::kChar || !number(a[7], &temperature) || a[2] == Py_None) return false;
+        if (!d.read(a[8]) || !d.is(head.h.rows, head.h.columns, head.h.type, head.h.device) || !head.outputs(a[9], true, head.h.type, g))
+            return false;
+        if (!vector(a[2], head.h.rows, at::kLong, head.h.device, &tokens)) return false;
+        for (int i = 0; i < 4; ++i)
+            if ((i < 3 && a[3 + i] == Py_None) || !vector(a[3 + i], head.h.rows, at::kFloat, head.h.device, &v[i])) return false;
+        const Where at(head.h.device, true);
+        return at.ok && launched([&] {
+            return bound.linear_grad(head.h.p, head.h.stride, size_t(head.h.rows), head.h.columns, head.s, int(head.W), head.dtype,
+                                     temperature, tokens, v[0], v[1], v[2], v[3], d.p, d.stride, g, at.ws.address, at.ws.bytes, at.hip());
+        });
+    });
+}
+
+// quantize(x, q, scale)
+PyObject *py_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return answer([&] {
+        Matrix x, q;
+        rog_dtype dtype;
+        float *scale;
+        if (n != 3 || !x.read(a[0]) || !q.read(a[1]) || !dtype_of(x.type, &dtype) || !q.is(x.rows, x.columns, at::kChar, x.device) ||
+            a[2] == Py_None || !vector(a[2], x.rows, at::kFloat, x.device, &scale))
+            return false;
+        const Where at(x.device, false);
+        return at.ok && launched([&] {
+            return bound.quantize(x.p, x.stride, size_t(x.rows), x.columns, dtype, static_cast<int8_t *>(q.p), q.stride, scale, at.hip());
+        });
+    });
+}
+
+// linear_i8(q, scale, weights, weight_scales, out)
+PyObject *py_linear_i8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return answer([&] {
+        Head head;
+        rog_i8_shard s[64];
+        rog_grad_shard out[64];
+        rog_dtype dtype;
+        const float *scale;
+        Py_ssize_t scales;
+        Matrix first;
+        if (n != 5 || !head.read(a[0], a[2]) || head.h.type != at::kChar || a[1] == Py_None ||
+            !vector(a[1], head.h.rows, at::kFloat, head.h.device, &scale) || !items(a[3], &scales) || scales != head.W)
+            return false;
+        for (Py_ssize_t i = 0; i < head.W; ++i) {
+            PyObject *const r = PySequence_Fast_GET_ITEM(a[3], i);
+            const float *p;
+            if (r == Py_None || !vector(r, head.s[i].width, at::kFloat, head.h.device, &p)) return false;
+            s[i] = rog_i8_shard{static_cast<const int8_t *>(head.s[i].weight), head.s[i].row_stride, head.s[i].width, p};
+        }
+        Py_ssize_t outs;
+        if (!items(a[4], &outs) || !first.read(PySequence_Fast_GET_ITEM(a[4], 0)) || !dtype_of(first.type, &dtype) ||
+            !head.outputs(a[4], false, first.type, out))
+            return false;
+        const Where at(head.h.device, false);
+        return at.ok && launched([&] {
+            return bound.linear_i8(static_cast<const int8_t *>(head.h.p), head.h.stride, scale, size_t(head.h.rows), head.h.columns, s,
+                                   int(head.W), dtype, out, at.hip());
+        });
+    });
+}
+
 // workspace(device, stream, address, bytes): a stream's own workspace, made or grown
 PyObject *py_workspace(PyObject *, PyObject *args) {
     int device;
@@ -249,19 +401,31 @@ PyObject *py_workspace(PyObject *, PyObject *args) {
     Py_RETURN_NONE;
 }
 
-// bind(logprob_ex, logprob_grad, policy_loss, max_peers, current_device, raw_stream, is_capturing):
-// the entry points' addresses and torch's callables
+// bind(entry points, max_peers, current_device, raw_stream, is_capturing): the entry
+// points' addresses, in the order of `Bound`, and torch's callables
 PyObject *py_bind(PyObject *, PyObject *args) {
-    unsigned long long logprob, grad, loss;
+    PyObject *entries, *device, *stream, *capturing;
     int max_peers;
-    PyObject *device, *stream, *capturing;
-    if (!PyArg_ParseTuple(args, "KKKiOOO", &logprob, &grad, &loss, &max_peers, &device, &stream, &capturing)) return nullptr;
+    if (!PyArg_ParseTuple(args, "O!iOOO", &PyTuple_Type, &entries, &max_peers, &device, &stream, &capturing)) return nullptr;
+    unsigned long long e[7];
+    if (PyTuple_GET_SIZE(entries) != 7) {
+        PyErr_SetString(PyExc_ValueError, "seven entry points");
+        return nullptr;
+    }
+    for (int i = 0; i < 7; ++i) {
+        e[i] = PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(entries, i));
+        if (PyErr_Occurred()) return nullptr;
+    }
     Py_INCREF(device);
     Py_INCREF(stream);
     Py_INCREF(capturing);
-    bound.logprob = reinterpret_cast<decltype(bound.logprob)>(logprob);
-    bound.grad = reinterpret_cast<decltype(bound.grad)>(grad);
-    bound.loss = reinterpret_cast<decltype(bound.loss)>(loss);
+    bound.logprob = reinterpret_cast<decltype(bound.logprob)>(e[0]);
+    bound.grad = reinterpret_cast<decltype(bound.grad)>(e[1]);
+    bound.loss = reinterpret_cast<decltype(bound.loss)>(e[2]);
+    bound.linear_logprob = reinterpret_cast<decltype(bound.linear_logprob)>(e[3]);
+    bound.linear_grad = reinterpret_cast<decltype(bound.linear_grad)>(e[4]);
+    bound.quantize = reinterpret_cast<decltype(bound.quantize)>(e[5]);
+    bound.linear_i8 = reinterpret_cast<decltype(bound.linear_i8)>(e[6]);
     bound.max_peers = max_peers;
     bound.current_device = device;
     bound.raw_stream = stream;
@@ -275,6 +439,10 @@ PyCFunction fn(F *f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<voi
 PyMethodDef methods[] = {{"logprob", fn(&py_logprob), METH_FASTCALL, nullptr},
                          {"grad", fn(&py_grad), METH_FASTCALL, nullptr},
                          {"loss", fn(&py_loss), METH_FASTCALL, nullptr},
+                         {"linear_logprob", fn(&py_linear_logprob), METH_FASTCALL, nullptr},
+                         {"linear_grad", fn(&py_linear_grad), METH_FASTCALL, nullptr},
+                         {"quantize", fn(&py_quantize), METH_FASTCALL, nullptr},
+                         {"linear_i8", fn(&py_linear_i8), METH_FASTCALL, nullptr},
                          {"workspace", py_workspace, METH_VARARGS, nullptr},
                          {"bind", py_bind, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

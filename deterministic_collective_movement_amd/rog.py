@@ -668,12 +668,16 @@ def _made_on(stream, device: torch.device):
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device))
 
 
-def _own_workspace(nbytes: int, device: torch.device, stream, handle: int):
-    """(address, bytes) of the stream's workspace, made or grown to hold ``nbytes``."""
+def _own_workspace(nbytes: int, device: torch.device, stream, handle: int, counters: bool = True):
+    """(address, bytes) of the stream's workspace, made or grown to hold ``nbytes``.
+    ``counters``: the call needs the counters at its front cleared."""
     if nbytes == 0:
         return _NO_WORKSPACE
     if _capturing(stream, device):
         # a graph's replays may run beside eager calls on this stream: the graph gets its own, cleared in the graph
+        if not counters:
+            with _made_on(stream, device):
+                return torch.empty(nbytes, dtype=torch.uint8, device=device).data_ptr(), nbytes
         t = rog_workspace(nbytes, device, stream)
         return t.data_ptr(), nbytes
     key = (device.index, handle)
@@ -692,7 +696,9 @@ def _own_workspace(nbytes: int, device: torch.device, stream, handle: int):
 _is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 _raw_stream_of = _raw_stream or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 if _binding is not None:
-    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rog_logprob_ex, _lib.rog_logprob_grad, _lib.rog_policy_loss)),
+    _binding.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rog_logprob_ex, _lib.rog_logprob_grad, _lib.rog_policy_loss,
+                                                                        _lib.rog_linear_logprob, _lib.rog_linear_logprob_grad,
+                                                                        _lib.rog_quantize_i8, _lib.rog_linear_i8)),
                   _lib.rog_max_peers(), _current_device, _raw_stream_of, _is_capturing)
 
 
@@ -705,7 +711,7 @@ def _capturing(stream, device: torch.device) -> bool:
         return _is_capturing()
 
 
-def _with_workspace(call, need, what: str, workspace, device: torch.device, stream, handle: int) -> None:
+def _with_workspace(call, need, what: str, workspace, device: torch.device, stream, handle: int, counters: bool = True) -> None:
     """``call(address, bytes)`` with the caller's workspace or the stream's own.
     The library refuses one that is too small before it enqueues anything, so
     ``need()``, the bytes it asks for, is only looked up where the stream's own
@@ -723,7 +729,7 @@ def _with_workspace(call, need, what: str, workspace, device: torch.device, stre
             return
         if status != ROG_ERR_INVALID_ARGUMENT or got[1] >= need():
             _check(status, what)
-    _check(call(*_own_workspace(need(), device, stream, handle)), what)
+    _check(call(*_own_workspace(need(), device, stream, handle, counters)), what)
 
 
 def _vector_error(t, what: str, n: int, dtype: torch.dtype, device: torch.device):
@@ -1056,6 +1062,11 @@ def rog_linear_logprob(hidden: torch.Tensor, weights: Sequence[torch.Tensor], to
     row stride.  ``out``: a RogLogprob (or five tensors, the last two None) to
     write, None for what is not wanted.  The outputs have no gradient function:
     ``rog_linear_logprob_grad`` gives the gradients."""
+    if out is not None and workspace is None and stream is None:
+        if type(out) is not RogLogprob:
+            out = RogLogprob(*out)
+        if _binding is not None and _binding.linear_logprob(hidden, weights, tokens, temperature, out):
+            return out
     device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, weights, _PRODUCT_DTYPES)
     f32 = torch.float32
     if out is None:
@@ -1074,7 +1085,7 @@ def rog_linear_logprob(hidden: torch.Tensor, weights: Sequence[torch.Tensor], to
         _with_workspace(lambda ws, n: _lib.rog_linear_logprob(at, stride, rows, dim, packed, W, dt, temperature, tok, outs, ws, n, handle),
                         lambda: _linear_plan(_lib.rog_linear_logprob_plan, "rog_linear_logprob", packed, W, rows, dim, dt,
                                              int(tokens is not None)).workspace_bytes,
-                        "rog_linear_logprob", workspace, device, stream, handle)
+                        "rog_linear_logprob", workspace, device, stream, handle, counters=False)
     return out
 
 
@@ -1086,6 +1097,11 @@ def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor
     states and in every shard's weights, from rog_linear_logprob's ``lse`` and
     ``entropy`` of the same states, weights and temperature.  Rows that are not
     scored get zeros.  ``out``: a RogLinearGrad (or (d_hidden, W matrices)) to write."""
+    if out is not None and workspace is None and stream is None:
+        if type(out) is not RogLinearGrad:
+            out = RogLinearGrad(out[0], list(out[1]))
+        if _binding is not None and _binding.linear_grad(hidden, weights, tokens, lse, entropy, g_logp, g_entropy, temperature, out[0], out[1]):
+            return out
     device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, weights, _PRODUCT_DTYPES)
     W = len(weights)
     if out is None:
@@ -1111,7 +1127,7 @@ def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor
                                                                    d_stride, grads, ws, n, handle),
                         lambda: _linear_plan(_lib.rog_linear_logprob_grad_plan, "rog_linear_logprob_grad", packed, W, rows, dim,
                                              dt).workspace_bytes,
-                        "rog_linear_logprob_grad", workspace, device, stream, handle)
+                        "rog_linear_logprob_grad", workspace, device, stream, handle, counters=False)
     return out
 
 
@@ -1133,6 +1149,8 @@ def rog_quantize_i8(x: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = Non
             out = RogQuantized(torch.empty(rows, dim, dtype=torch.int8, device=device), torch.empty(rows, dtype=torch.float32, device=device))
     elif type(out) is not RogQuantized:
         out = RogQuantized(*out)
+    if stream is None and _binding is not None and _binding.quantize(x, out[0], out[1]):
+        return out
     q_at, q_stride = _row_matrix(out.q, "out.q", rows, dim, torch.int8, device)
     s_at = _addresses(out[1:], ("out.scale",), rows, torch.float32, device, idx)[0]
     with _on_device(device) if _current_device() != idx else _HERE:
@@ -1151,6 +1169,8 @@ def rog_linear_i8(q: torch.Tensor, scale: torch.Tensor, weights: Sequence[torch.
     ``q``: [rows, dim] int8 and ``scale``: [rows] float32, as rog_quantize_i8 gives
     them; ``weights``: W shards [width_r, dim] int8; ``weight_scales``: W vectors
     [width_r] float32."""
+    if out is not None and stream is None and _binding is not None and _binding.linear_i8(q, scale, weights, weight_scales, out):
+        return out if isinstance(out, list) else list(out)
     device, idx, rows, dim, _, at, stride, _ = _head_bytes(q, weights, (torch.int8,))
     W = len(weights)
     if out is None:
