@@ -94,7 +94,7 @@ struct GradArgs {
     const int64_t *tokens;
     const uint32_t *index;
     const float *lse, *entropy, *g_logp, *g_entropy, *g_scale;
-    float inv_t;
+    float inv_t, scale;                // 1 / temperature, log2(e) / temperature
     void *g, *g_all;                   // [rows][g_stride / 2] coefficients of the piece's columns; binary16: by the rows' own
                                        // scales, and by that of all (else one array)
     int64_t g_stride;                  // bytes

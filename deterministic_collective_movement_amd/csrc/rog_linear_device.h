@@ -72,6 +72,10 @@ __device__ __forceinline__ const Args &fresh_args() {
     asm volatile("" : "+s"(p));
     return *(const Args *)p;
 }
+// Bytes from the first of `rows` rows of `row_bytes` to the end of the last: rows may be less than a row apart, or the same.
+__device__ __forceinline__ uint32_t extent_of(int32_t rows, uint32_t stride, uint32_t row_bytes) {
+    return rows > 0 ? uint32_t(rows - 1) * stride + row_bytes : 0;
+}
 // A window on [base, base + bytes), the same for all lanes.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const uint8_t *base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(uniform(base)), 0, int(uniform(bytes)), kBufferWord3);
@@ -124,7 +128,7 @@ struct RowSteps {
     static constexpr int kReads = 1;                     // shared memory instructions of a fragment
     static_assert(ROWS % kRows == 0 && kRows % 32 == 0, "whole waves, one swizzle for all of a lane's rows");
     const uint8_t *base;
-    uint32_t rows_bytes;               // of the rows that there are (a tile's are below 2^30)
+    uint32_t rows, bytes;              // rows that there are, and their extent (below 2^31)
     uint32_t kbytes;
     int64_t stride;
     uint32_t voff[kLoads];             // the lane's units
@@ -132,7 +136,8 @@ struct RowSteps {
     uint32_t k = 0;                    // the next step
     // rows_left: rows from `base` on that exist
     __device__ __forceinline__ RowSteps(const void *b, int64_t s, uint32_t rows_left, uint32_t kb)
-        : base(uniform(b)), rows_bytes(uniform((rows_left < ROWS ? rows_left : ROWS) * uint32_t(s))), kbytes(uniform(kb)), stride(s) {
+        : base(uniform(b)), rows(uniform(rows_left < ROWS ? rows_left : ROWS)), bytes(uniform(extent_of(rows, uint32_t(s), kb))),
+          kbytes(uniform(kb)), stride(s) {
         const uint32_t row = threadIdx.x / 4;
         unit = (threadIdx.x % 4 ^ swizzle<M_SIDE>(row)) * 16;
 #pragma unroll
@@ -151,7 +156,7 @@ struct RowSteps {
     __device__ __forceinline__ void bring(uint8_t *to, uint32_t step) const {
         const uint32_t at = step * kStepBytes;
         if constexpr (STRAIGHT) {
-            const auto r = window(base, TAIL || at + kStepBytes <= kbytes ? rows_bytes : 0);
+            const auto r = window(base, TAIL || at + kStepBytes <= kbytes ? bytes : 0);
             const bool inside = !TAIL || at + unit < kbytes;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -162,8 +167,8 @@ struct RowSteps {
             vec16 v[kLoads];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const uint32_t off = (threadIdx.x / 4 + i * kRows) * uint32_t(stride);
-                v[i] = off < rows_bytes && (TAIL || at + kStepBytes <= kbytes) ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes)
+                const uint32_t row = threadIdx.x / 4 + i * kRows, off = row * uint32_t(stride);
+                v[i] = row < rows && (TAIL || at + kStepBytes <= kbytes) ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes)
                                                                                : vec16{0, 0, 0, 0};
             }
 #pragma unroll
@@ -209,13 +214,14 @@ struct ColSteps {
     static_assert(kRows % 16 == 0 || kRows == 8 || kRows == 4, "see `turn`");
     static_assert(kLoads * THREADS == 32 * kUnits && kUnits >= 16, "whole loads of rows of 256 bytes and more");
     const uint8_t *from;               // of the next step
-    uint32_t left, col_bytes;          // rows of K from there on, bytes of a row
+    int32_t left;                      // rows of K from there on; below 0 past the last step (signed: a scalar has no saturating difference)
+    uint32_t col_bytes;                // bytes of a row
     int64_t stride;
     uint32_t row, unit;
     uint32_t voff[kLoads];             // the lane's units
     static __device__ __forceinline__ uint32_t turn(uint32_t row) { return 4 * (row % 4) + 2 * (row / 8 % 2); }   // of units
     __device__ __forceinline__ ColSteps(const void *b, int64_t s, uint32_t rows_, uint32_t cols_left)
-        : from(uniform(b)), left(uniform(rows_)), col_bytes(cols_left * 2), stride(s) {
+        : from(uniform(b)), left(int32_t(uniform(rows_))), col_bytes(uniform((cols_left < COLS ? cols_left : COLS) * 2)), stride(s) {
         row = threadIdx.x / kUnits;
         unit = threadIdx.x % kUnits;
 #pragma unroll
@@ -227,7 +233,7 @@ struct ColSteps {
     __device__ __forceinline__ void stage(uint8_t *to) {
         if constexpr (DIRECT) {
             // a row past the last is past the window; in the last, nothing past the columns is read
-            const auto r = window(from, (left < 32 ? left : 32) * uint32_t(stride));
+            const auto r = window(from, extent_of(left < 32 ? left : 32, uint32_t(stride), col_bytes));
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 lbyte *p = (lbyte *)to + (i * THREADS + uniform(threadIdx.x / 64) * 64) * 16;
@@ -237,13 +243,13 @@ struct ColSteps {
             vec16 v[kLoads];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                v[i] = row + i * kRows < left ? row_bytes<2>((gbyte *)from + uint64_t(row + i * kRows) * uint64_t(stride), at(i), col_bytes)
+                v[i] = int32_t(row + i * kRows) < left ? row_bytes<2>((gbyte *)from + uint64_t(row + i * kRows) * uint64_t(stride), at(i), col_bytes)
                                               : vec16{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
         }
         from += 32 * uint32_t(stride);
-        left = left > 32 ? left - 32 : 0;
+        left -= 32;
     }
     __device__ __forceinline__ void stage_tail(uint8_t *to) { stage(to); }   // K ends with a row
     // Fragments (sixteen consecutive columns) of a wave's columns from col0 on, a multiple of its fragments' columns
@@ -433,11 +439,12 @@ struct RowLines {
         return (q & 1) | (q >> 2 & 1) << 1 | ((q >> 1 ^ q >> 2) & 1) << 2;
     }
     const uint8_t *base;
-    uint32_t rows_bytes, kbytes;
+    uint32_t rows, bytes, kbytes;
     int64_t stride;
     uint32_t at = 0;                   // of the next step in the rows
     __device__ __forceinline__ RowLines(const void *b, int64_t s, uint32_t rows_left, uint32_t kb)
-        : base(uniform(b)), rows_bytes(uniform((rows_left < ROWS ? rows_left : ROWS) * uint32_t(s))), kbytes(uniform(kb)), stride(s) {}
+        : base(uniform(b)), rows(uniform(rows_left < ROWS ? rows_left : ROWS)), bytes(uniform(extent_of(rows, uint32_t(s), kb))),
+          kbytes(uniform(kb)), stride(s) {}
     // Brings the next step to `to`, zeros past the rows and past K.
     __device__ __forceinline__ void stage(uint8_t *to) {
         // A step in which a row ends inside 16 bytes goes through registers.  Its loads are waited for, and
@@ -450,7 +457,7 @@ struct RowLines {
     __device__ __forceinline__ void bring(uint8_t *to) const {
         const uint32_t row = threadIdx.x / 8;
         if constexpr (STRAIGHT) {
-            const auto r = window(base, rows_bytes);
+            const auto r = window(base, bytes);
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const uint32_t unit = (threadIdx.x % 8 ^ turn(row + i * kRows)) * 16;
@@ -463,7 +470,7 @@ struct RowLines {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const uint32_t unit = (threadIdx.x % 8 ^ turn(row + i * kRows)) * 16, off = (row + i * kRows) * uint32_t(stride);
-                v[i] = off < rows_bytes ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes) : vec16{0, 0, 0, 0};
+                v[i] = row + i * kRows < rows ? row_bytes<ES>((gbyte *)base + off, at + unit, kbytes) : vec16{0, 0, 0, 0};
             }
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
@@ -485,13 +492,14 @@ struct ColLines {
     static constexpr int kRows = THREADS / 8, kLoads = 64 / kRows;
     static __device__ __forceinline__ uint32_t turn(uint32_t row) { return (row >> 1 & 1) | (row >> 3 & 1) << 1; }
     const uint8_t *from;               // of the next step
-    uint32_t left, col_bytes;          // rows of K from there on, bytes of a row
+    int32_t left;                      // rows of K from there on; below 0 past the last step (signed: a scalar has no saturating difference)
+    uint32_t col_bytes;                // bytes of a row
     int64_t stride;
     __device__ __forceinline__ ColLines(const void *b, int64_t s, uint32_t rows, uint32_t cols_left)
-        : from(uniform(b)), left(uniform(rows)), col_bytes(cols_left * 2), stride(s) {}
+        : from(uniform(b)), left(int32_t(uniform(rows))), col_bytes(uniform((cols_left < 64 ? cols_left : 64) * 2)), stride(s) {}
     __device__ __forceinline__ void stage(uint8_t *to) {
         const uint32_t row = threadIdx.x / 8;
-        const auto r = window(from, (left < 64 ? left : 64) * uint32_t(stride));
+        const auto r = window(from, extent_of(left < 64 ? left : 64, uint32_t(stride), col_bytes));
         vec16 v[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -501,14 +509,14 @@ struct ColLines {
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)p, 16,
                                                          at < col_bytes ? k * uint32_t(stride) + at : kOutside, 0, 0, 0);
             } else {
-                v[i] = k < left ? row_bytes<2>((gbyte *)from + uint64_t(k) * uint64_t(stride), at, col_bytes) : vec16{0, 0, 0, 0};
+                v[i] = int32_t(k) < left ? row_bytes<2>((gbyte *)from + uint64_t(k) * uint64_t(stride), at, col_bytes) : vec16{0, 0, 0, 0};
             }
         }
         if constexpr (!DIRECT)
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *(lvec16 *)((lbyte *)to + (i * THREADS + threadIdx.x) * 16) = v[i];
         from += 64 * uint32_t(stride);
-        left = left > 64 ? left - 64 : 0;
+        left -= 64;
     }
     static __device__ __forceinline__ vec16 get(const uint8_t *from, uint32_t col0, int f, int ks) {
         const uint32_t l = threadIdx.x % 64, j = l % 16, k = ks * 32 + l / 16 * 8 + j / 4;

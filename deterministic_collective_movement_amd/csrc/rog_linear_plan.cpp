@@ -23,6 +23,8 @@ constexpr double kLog2E = 1.4426950408889634;
 #ifndef ROG_LINEAR_ROW_PAD
 #define ROG_LINEAR_ROW_PAD 256
 #endif
+// Large tiles up to which 128 x 128 ones are taken instead: half of the CUs or fewer would be at work (200 rows of
+// 32000 x 2048 56.5 us with 125 large tiles, 50.1 with 500; 600 rows of 16000 x 2048 60 with 189, 68 with 625).
 #ifndef ROG_MID_TILES
 #define ROG_MID_TILES 128
 #endif
@@ -33,13 +35,16 @@ constexpr double kLog2E = 1.4426950408889634;
 inline bool product_type(rog_dtype t) { return t == ROG_DTYPE_BF16 || t == ROG_DTYPE_F16; }
 inline uint64_t up(uint64_t v, uint64_t unit) { return ceil_div(v, unit) * unit; }
 
-// A matrix of `rows` rows of `width` elements: address, stride and extent.
-rog_status check_matrix(const void *p, int64_t stride, uint64_t rows, uint64_t width, uint32_t es, bool spread) {
+// A matrix of `rows` rows of `width` elements: address, stride and extent; `bytes` gets its stride in bytes (one row
+// has none).
+rog_status check_matrix(const void *p, int64_t stride, uint64_t rows, uint64_t width, uint32_t es, bool spread, int64_t *bytes) {
     if (stride < 0) return ROG_ERR_INVALID_ARGUMENT;
     if (rows && width && (!p || addr(p) % es)) return ROG_ERR_INVALID_ARGUMENT;
+    if (rows <= 1) stride = 0;
     if (spread && rows > 1 && uint64_t(stride) < width) return ROG_ERR_INVALID_ARGUMENT;
-    if (uint64_t(stride) * es >= kMaxLinearStride) return ROG_ERR_TOO_LARGE;
-    return fits(addr(p), rows, uint64_t(stride) * es, width * es) ? ROG_OK : ROG_ERR_TOO_LARGE;
+    if (uint64_t(stride) >= kMaxLinearStride / es) return ROG_ERR_TOO_LARGE;
+    *bytes = stride * es;
+    return fits(addr(p), rows, uint64_t(*bytes), width * es) ? ROG_OK : ROG_ERR_TOO_LARGE;
 }
 
 // Loads of 16 bytes go straight to the shared memory from rows that begin on 4 bytes.
@@ -53,12 +58,13 @@ rog_status lay_weights(const Shard *shards, int W, int64_t dim, uint32_t es, boo
     for (int r = 0; r < W; ++r) {
         if (shards[r].width < 0) return ROG_ERR_INVALID_ARGUMENT;
         if (uint64_t(shards[r].width) >= kMaxVocab || v + uint64_t(shards[r].width) >= kMaxVocab) return ROG_ERR_TOO_LARGE;
+        int64_t stride = 0;
         if (addresses) {
-            const rog_status st = check_matrix(shards[r].weight, shards[r].row_stride, uint64_t(shards[r].width), uint64_t(dim), es, false);
+            const rog_status st = check_matrix(shards[r].weight, shards[r].row_stride, uint64_t(shards[r].width), uint64_t(dim), es, false, &stride);
             if (st != ROG_OK) return st;
         }
-        h->s[r] = WeightShard{shards[r].weight, shards[r].row_stride * es, uint32_t(shards[r].width), uint32_t(v)};
-        if (shards[r].width && !aligned(shards[r].weight, shards[r].width > 1 ? uint64_t(h->s[r].stride) : 0)) *direct = false;
+        h->s[r] = WeightShard{shards[r].weight, stride, uint32_t(shards[r].width), uint32_t(v)};
+        if (shards[r].width && !aligned(shards[r].weight, uint64_t(stride))) *direct = false;
         v += uint64_t(shards[r].width);
     }
     h->W = uint32_t(W);
@@ -124,13 +130,14 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     rog_status st = lay_weights(shards, W, dim, 2, addresses, &a.sh, &p->direct);
     if (st != ROG_OK) return st;
     if (rows >= kMaxVocab) return ROG_ERR_TOO_LARGE;
-    if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false);
+    int64_t h_stride = 0;
+    if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false, &h_stride);
     if (st != ROG_OK) return st;
     p->form = form_of(rows, a.sh);
     p->packs = has_tokens && rows >= kPackFrom;
     lay_tiles(&a.sh, tile_columns(p->form));
     const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
-    if (!p->packs && !aligned(hidden, rows > 1 ? uint64_t(hidden_stride) * 2 : 0)) p->direct = false;
+    if (!p->packs && !aligned(hidden, uint64_t(h_stride))) p->direct = false;
     const uint64_t groups = groups_of(a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form)), p->form);
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);
@@ -154,11 +161,11 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
         for (int j = 0; j < i; ++j)
             if (overlap(outs[i], outs[j])) return ROG_ERR_OVERLAP;
         if (tokens && overlap(outs[i], flat(tokens, rows * 8))) return ROG_ERR_OVERLAP;
-        if (overlap(outs[i], matrix(hidden, rows, hidden_stride * 2, kbytes))) return ROG_ERR_OVERLAP;
+        if (overlap(outs[i], matrix(hidden, rows, h_stride, kbytes))) return ROG_ERR_OVERLAP;
         for (int r = 0; r < W; ++r)
             if (overlap(outs[i], matrix(a.sh.s[r].w, a.sh.s[r].width, a.sh.s[r].stride, kbytes))) return ROG_ERR_OVERLAP;
     }
-    a.a = LinearRows{hidden, hidden_stride * 2, nullptr, uint32_t(rows), uint32_t(kbytes)};
+    a.a = LinearRows{hidden, h_stride, nullptr, uint32_t(rows), uint32_t(kbytes)};
     a.tokens = tokens;
     a.index = nullptr;
     a.scale = float(kLog2E / double(temperature));
@@ -167,7 +174,7 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     if (p->packs) {
         p->pack = PackArgs{};
         p->pack.x = hidden;
-        p->pack.stride = hidden_stride * 2;
+        p->pack.stride = h_stride;
         p->pack.tokens = tokens;
         p->pack.rows = uint32_t(rows);
         p->pack.kbytes = uint32_t(kbytes);
@@ -200,7 +207,8 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (st != ROG_OK) return st;
     if (a.sh.vocab == 0) return ROG_ERR_INVALID_ARGUMENT;
     if (rows >= kMaxVocab) return ROG_ERR_TOO_LARGE;
-    if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false);
+    int64_t h_stride = 0;
+    if (addresses) st = check_matrix(hidden, hidden_stride, rows, uint64_t(dim), 2, false, &h_stride);
     if (st != ROG_OK) return st;
     lay_tiles(&a.sh, kGradTile);
     const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
@@ -259,12 +267,13 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (!tokens || !lse || !entropy || !g_logp || !d_weights || addr(tokens) % 8 ||
         (addr(lse) | addr(entropy) | addr(g_logp) | addr(g_entropy)) % 4)
         return ROG_ERR_INVALID_ARGUMENT;
-    st = check_matrix(d_hidden, d_hidden_stride, rows, uint64_t(dim), 2, true);
+    int64_t d_stride = 0;
+    st = check_matrix(d_hidden, d_hidden_stride, rows, uint64_t(dim), 2, true, &d_stride);
     if (st != ROG_OK) return st;
     if (!workspace || addr(workspace) % 16 || workspace_bytes < p->workspace_bytes) return ROG_ERR_INVALID_ARGUMENT;
-    const Strip work = flat(workspace, p->workspace_bytes), dh = matrix(d_hidden, rows, d_hidden_stride * 2, kbytes);
+    const Strip work = flat(workspace, p->workspace_bytes), dh = matrix(d_hidden, rows, d_stride, kbytes);
     if (work.at > UINTPTR_MAX - work.width) return ROG_ERR_TOO_LARGE;
-    const Strip x = matrix(hidden, rows, hidden_stride * 2, kbytes);
+    const Strip x = matrix(hidden, rows, h_stride, kbytes);
     const Strip vectors[5] = {flat(lse, rows * 4), flat(entropy, rows * 4), flat(g_logp, rows * 4),
                               flat(g_entropy, g_entropy ? rows * 4 : 0), flat(tokens, rows * 8)};
     if (overlap(work, dh) || overlap(work, x) || overlap(dh, x)) return ROG_ERR_OVERLAP;
@@ -273,11 +282,10 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     for (int r = 0; r < W; ++r) {
         const uint64_t width = a.sh.s[r].width;
         if (width) {
-            st = check_matrix(d_weights[r].grad, d_weights[r].row_stride, width, uint64_t(dim), 2, true);
+            st = check_matrix(d_weights[r].grad, d_weights[r].row_stride, width, uint64_t(dim), 2, true, &k.dw_stride[r]);
             if (st != ROG_OK) return st;
         }
         k.dw[r] = d_weights[r].grad;
-        k.dw_stride[r] = width ? d_weights[r].row_stride * 2 : 0;
         const Strip dw = matrix(k.dw[r], width, k.dw_stride[r], kbytes), wr = matrix(a.sh.s[r].w, width, a.sh.s[r].stride, kbytes);
         if (overlap(dw, work) || overlap(dw, dh) || overlap(dw, x) || overlap(wr, work) || overlap(wr, dh)) return ROG_ERR_OVERLAP;
         for (const Strip &v : vectors)
@@ -291,7 +299,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     PackArgs &c = p->pack;
     c = PackArgs{};
     c.x = hidden;
-    c.stride = hidden_stride * 2;
+    c.stride = h_stride;
     c.tokens = tokens;
     c.rows = uint32_t(rows);
     c.kbytes = uint32_t(kbytes);
@@ -300,7 +308,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     c.count = in<uint32_t>(workspace, count);
     c.packed = in<void>(workspace, rows_at);
     c.zero = d_hidden;
-    c.zero_stride = d_hidden_stride * 2;
+    c.zero_stride = d_stride;
     c.g_logp = g_logp;
     c.g_entropy = g_entropy;
     c.g_scale = dtype == ROG_DTYPE_F16 ? in<float>(workspace, g_scale) : nullptr;
@@ -314,6 +322,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     a.g_entropy = g_entropy;
     a.g_scale = c.g_scale;
     a.inv_t = c.inv_t;
+    a.scale = float(kLog2E / double(temperature));
     a.g = in<void>(workspace, g);
     a.g_all = in<void>(workspace, g_all);
     a.g_stride = int64_t(g_row);
@@ -331,7 +340,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     // along rows, where a row's end inside 16 bytes would be read past, only whole ones
     p->direct_back = p->direct && kbytes % 16 == 0;
     k.d_hidden = d_hidden;
-    k.d_stride = d_hidden_stride * 2;
+    k.d_stride = d_stride;
     p->join_grid = 0;
     if (!p->running) {
         const uint64_t groups = ceil_div(rows * (k.dim_pad / 8), 256);
@@ -376,14 +385,15 @@ rog_status plan_quantize(const void *x, int64_t row_stride, size_t rows, int64_t
     if (!known(dtype) || dim < 1) return ROG_ERR_INVALID_ARGUMENT;
     if (rows >= uint64_t(1) << 23 || uint64_t(dim) >= kMaxDim) return ROG_ERR_TOO_LARGE;
     const uint32_t es = esize(dtype);
-    rog_status st = check_matrix(x, row_stride, rows, uint64_t(dim), es, false);
-    if (st == ROG_OK) st = check_matrix(q, q_stride, rows, uint64_t(dim), 1, true);
+    int64_t x_bytes = 0, q_bytes = 0;
+    rog_status st = check_matrix(x, row_stride, rows, uint64_t(dim), es, false, &x_bytes);
+    if (st == ROG_OK) st = check_matrix(q, q_stride, rows, uint64_t(dim), 1, true, &q_bytes);
     if (st != ROG_OK || rows == 0) return st;
     if (!scale || addr(scale) % 4) return ROG_ERR_INVALID_ARGUMENT;
-    const Strip xs = matrix(x, rows, row_stride * es, uint64_t(dim) * es), qs = matrix(q, rows, q_stride, uint64_t(dim)), s = flat(scale, rows * 4);
+    const Strip xs = matrix(x, rows, x_bytes, uint64_t(dim) * es), qs = matrix(q, rows, q_bytes, uint64_t(dim)), s = flat(scale, rows * 4);
     if (s.at > UINTPTR_MAX - s.width) return ROG_ERR_TOO_LARGE;
     if (overlap(xs, qs) || overlap(xs, s) || overlap(qs, s)) return ROG_ERR_OVERLAP;
-    *a = QuantizeArgs{x, row_stride * es, q, q_stride, scale, uint32_t(rows), uint32_t(dim)};
+    *a = QuantizeArgs{x, x_bytes, q, q_bytes, scale, uint32_t(rows), uint32_t(dim)};
     return ROG_OK;
 }
 
@@ -396,11 +406,12 @@ rog_status plan_linear_i8(const int8_t *q, int64_t q_stride, const float *scale,
     rog_status st = lay_weights(shards, W, dim, 1, true, &a.sh, &p->direct);
     if (st != ROG_OK) return st;
     if (rows >= kMaxVocab) return ROG_ERR_TOO_LARGE;
-    st = check_matrix(q, q_stride, rows, uint64_t(dim), 1, false);
+    int64_t q_bytes = 0;
+    st = check_matrix(q, q_stride, rows, uint64_t(dim), 1, false, &q_bytes);
     if (st != ROG_OK || rows == 0) return st;
     if (!scale || addr(scale) % 4 || !out) return ROG_ERR_INVALID_ARGUMENT;
     const uint32_t os = esize(out_dtype);
-    const Strip qs = matrix(q, rows, q_stride, uint64_t(dim)), ss = flat(scale, rows * 4);
+    const Strip qs = matrix(q, rows, q_bytes, uint64_t(dim)), ss = flat(scale, rows * 4);
     for (int r = 0; r < W; ++r) {
         const uint64_t width = a.sh.s[r].width;
         a.scale[r] = shards[r].scale;
@@ -425,11 +436,11 @@ rog_status plan_linear_i8(const int8_t *q, int64_t q_stride, const float *scale,
     }
     p->form = form_of(rows, a.sh);
     lay_tiles(&a.sh, tile_columns(p->form));
-    if (!aligned(q, rows > 1 ? uint64_t(q_stride) : 0)) p->direct = false;
+    if (!aligned(q, uint64_t(q_bytes))) p->direct = false;
     const uint64_t groups = groups_of(a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form)), p->form);
     if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);
-    a.a = LinearRows{q, q_stride, nullptr, uint32_t(rows), uint32_t(dim)};
+    a.a = LinearRows{q, q_bytes, nullptr, uint32_t(rows), uint32_t(dim)};
     a.row_scale = scale;
     return ROG_OK;
 }

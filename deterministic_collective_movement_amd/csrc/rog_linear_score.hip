@@ -365,7 +365,7 @@ __device__ __forceinline__ void coef_tile(const GradArgs &p, uint32_t r, uint32_
     typename Mat<DT>::Acc acc[FM][FN] = {};
     Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
-    const float scale = p.inv_t * kLog2E;
+    const float scale = p.scale;       // that of the log probabilities
     const uint32_t own = 8 * (l / 16);
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
