@@ -55,7 +55,8 @@ struct ScoreArgs {
     const int64_t *tokens;             // of row i (NULL: none)
     const uint32_t *index;             // packed rows: the caller's row (NULL: row i itself)
     float scale;                       // log2(e) / temperature
-    float *target;                     // [rows] scaled logit of the row's token
+    float *target;                     // [rows] logit of the row's token
+    float *rests;                      // [rows][4] as a state: the token's block without it, and the block's number
     float *states;                     // m, s, t, 0 of a row's block at row * row_step + block * block_step, in fours
     uint32_t row_step, block_step;
     WeightShards sh;
@@ -65,7 +66,7 @@ struct ScoreArgs {
 struct JoinArgs {
     const int64_t *tokens;
     const uint32_t *index, *count;
-    const float *target, *states;
+    const float *target, *rests, *states;
     float *logp, *entropy, *lse;
     uint32_t rows, row_step, block_step;
     uint32_t vocab, blocks;

@@ -146,7 +146,7 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     a.row_step = p->form == kFormWide ? 1 : blocks;
     a.block_step = p->form == kFormWide ? rows_pad : 1;
     Layout w;
-    const uint64_t target = w.take(rows * 4), states = w.take(uint64_t(blocks) * rows_pad * 16);
+    const uint64_t target = w.take(rows * 4), rests = w.take(rows * 16), states = w.take(uint64_t(blocks) * rows_pad * 16);
     const uint64_t index = w.take(p->packs ? rows * 4 : 0), count = w.take(p->packs ? 4 : 0), rows_at = w.take(p->packs ? rows * packed : 0);
     p->workspace_bytes = rows ? w.at : 0;
     if (rows == 0 || !addresses) return ROG_OK;
@@ -170,6 +170,7 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     a.index = nullptr;
     a.scale = float(kLog2E / double(temperature));
     a.target = in<float>(workspace, target);
+    a.rests = in<float>(workspace, rests);
     a.states = in<float>(workspace, states);
     if (p->packs) {
         p->pack = PackArgs{};
@@ -188,7 +189,7 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
         a.a = LinearRows{p->pack.packed, int64_t(packed), p->pack.count, uint32_t(rows), uint32_t(kbytes)};
         a.index = p->pack.index;
     }
-    p->join = JoinArgs{tokens, a.index, a.a.count, a.target, a.states, out->logp, out->entropy, out->lse, uint32_t(rows), a.row_step,
+    p->join = JoinArgs{tokens, a.index, a.a.count, a.target, a.rests, a.states, out->logp, out->entropy, out->lse, uint32_t(rows), a.row_step,
                        a.block_step, a.sh.vocab, blocks, a.scale};
     return ROG_OK;
 }

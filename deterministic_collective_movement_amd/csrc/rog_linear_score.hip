@@ -101,15 +101,15 @@ __device__ __forceinline__ Part leaves_of(const float (&x)[LEAVES][8], float sca
     }
 }
 
-__device__ __forceinline__ void put_part(float *states, uint64_t at, const Part &p) {
+__device__ __forceinline__ void put_part(float *states, uint64_t at, const Part &p, uint32_t more = 0) {
     typedef __attribute__((address_space(1))) f32x4 gstate;
-    *((gstate *)states + at) = f32x4{p.m, p.s, p.t, 0};
+    *((gstate *)states + at) = f32x4{p.m, p.s, p.t, bits_f32(more)};
 }
 
 // The tile of F's size at columns v0 of shard r and rows n0.
 template <int DT, class F, bool DIRECT>
 __device__ __forceinline__ void score_tile(const ScoreArgs &p, uint32_t r, uint32_t v0, uint32_t n0, uint32_t rows, const TileMemory &memory,
-                                           uint32_t *targets, Part *shared_parts) {
+                                           uint32_t *targets, Part *shared_parts, Part *shared_rests) {
     constexpr int BM = F::kColumns, BN = F::kRows, FM = F::kFM, FN = F::kFN, LEAVES = FM / 2;
     typedef RowProduct<DT, F, DIRECT, 2, F::kWide> Product;
     const WeightShard sh = p.sh.s[r];
@@ -142,21 +142,29 @@ __device__ __forceinline__ void score_tile(const ScoreArgs &p, uint32_t r, uint3
         const uint32_t n = n0 + w0 + 16 * j + l % 16;
         // the row's token among the wave's columns
         const uint32_t hit = targets[w0 + 16 * j + l % 16] - m0;
-        if (__ballot(hit < FM * 16)) {
-#pragma unroll
-            for (uint32_t c = 0; c < FM * 4; ++c)
-                if (hit == 32 * (c / 8) + own + c % 8) p.target[n] = acc[c / 4][j][c % 4];
-        }
         float x[LEAVES][8];
 #pragma unroll
         for (int c = 0; c < FM * 4; ++c) x[c / 8][c % 8] = acc[c / 4][j][c % 4];
         const Part part = leaves_of<LEAVES>(x, p.scale);
+        Part rest = part;              // the same without the token, where it is among them
+        if (__ballot(hit < FM * 16)) {
+#pragma unroll
+            for (uint32_t c = 0; c < FM * 4; ++c)
+                if (hit == 32 * (c / 8) + own + c % 8) {
+                    p.target[n] = x[c / 8][c % 8];
+                    x[c / 8][c % 8] = -kInf;
+                }
+            rest = leaves_of<LEAVES>(x, p.scale);
+        }
         if constexpr (F::kShare == 1) {
             const uint32_t block = p.sh.block0[r] + (v0 + m0) / kLinearBlock;
-            if (l < 16 && n < rows && block < p.sh.block0[r + 1])
+            if (l < 16 && n < rows && block < p.sh.block0[r + 1]) {
                 put_part(p.states, uint64_t(n) * p.row_step + uint64_t(block) * p.block_step, part);
+                if (hit < FM * 16) put_part(p.rests, n, rest, block);
+            }
         } else if (l < 16) {
             shared_parts[m0 / (FM * 16) * BN + w0 + 16 * j + l] = part;
+            shared_rests[m0 / (FM * 16) * BN + w0 + 16 * j + l] = rest;
         }
     }
     if constexpr (F::kShare > 1) {
@@ -165,9 +173,14 @@ __device__ __forceinline__ void score_tile(const ScoreArgs &p, uint32_t r, uint3
         __syncthreads();
         const uint32_t n = n0 + threadIdx.x;
         if (threadIdx.x < BN && n < rows) {
-            Part all = join(shared_parts[threadIdx.x], shared_parts[BN + threadIdx.x]);
-            if constexpr (F::kShare == 4) all = join(all, join(shared_parts[2 * BN + threadIdx.x], shared_parts[3 * BN + threadIdx.x]));
-            put_part(p.states, uint64_t(n) * p.row_step + uint64_t(p.sh.block0[r] + v0 / kLinearBlock) * p.block_step, all);
+            const auto joined = [&](const Part *of) {
+                of += threadIdx.x;
+                const Part all = join(of[0], of[BN]);
+                return F::kShare == 4 ? join(all, join(of[2 * BN], of[3 * BN])) : all;
+            };
+            const uint32_t block = p.sh.block0[r] + v0 / kLinearBlock;
+            put_part(p.states, uint64_t(n) * p.row_step + uint64_t(block) * p.block_step, joined(shared_parts));
+            if (targets[threadIdx.x] < BM) put_part(p.rests, n, joined(shared_rests), block);
         }
     }
 }
@@ -178,24 +191,33 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_scor
     constexpr uint32_t BM = F::kColumns, BN = F::kRows;
     ROG_TILE_MEMORY(F::kStages, Product::A::kBytes, Product::B::kBytes);
     __shared__ uint32_t targets[BN];
-    __shared__ Part parts[F::kTail ? FormQuarter::kShare * FormQuarter::kRows : F::kShare > 1 ? F::kShare * BN : 1];
+    constexpr uint32_t kParts = F::kTail ? FormQuarter::kShare * FormQuarter::kRows : F::kShare > 1 ? F::kShare * BN : 1;
+    __shared__ Part parts[kParts], rests[kParts];
     const uint32_t rows = uniform(p.a.count ? *p.a.count : p.a.rows), tm = p.sh.tile0[p.sh.W], tn = (rows + BN - 1) / BN;
     if constexpr (F::kTail) {
         const Place o = place_of(blockIdx.x, tm, tn);
         if (o.none) return;
         const uint32_t r = shard_of_tile(p.sh, o.at.m), v0 = (o.at.m - p.sh.tile0[r]) * BM, n0 = o.at.n * BN;
         if (o.quarter == 4) {
-            score_tile<DT, F, DIRECT>(p, r, v0, n0, rows, memory, targets, parts);
+            score_tile<DT, F, DIRECT>(p, r, v0, n0, rows, memory, targets, parts, rests);
         } else {
             const uint32_t v = v0 + o.quarter % 2 * FormQuarter::kColumns, n = n0 + o.quarter / 2 * FormQuarter::kRows;
-            if (v < p.sh.s[r].width && n < rows) score_tile<DT, FormQuarter, DIRECT>(p, r, v, n, rows, memory, targets, parts);
+            if (v < p.sh.s[r].width && n < rows) score_tile<DT, FormQuarter, DIRECT>(p, r, v, n, rows, memory, targets, parts, rests);
         }
     } else {
         if (blockIdx.x >= tm * tn) return;
         const TileAt at = tile_at(blockIdx.x, tm, tn);
         const uint32_t r = shard_of_tile(p.sh, at.m);
-        score_tile<DT, F, DIRECT>(p, r, (at.m - p.sh.tile0[r]) * BM, at.n * BN, rows, memory, targets, parts);
+        score_tile<DT, F, DIRECT>(p, r, (at.m - p.sh.tile0[r]) * BM, at.n * BN, rows, memory, targets, parts, rests);
     }
+}
+
+// The log probability of a token of logit x beside the others: -log(1 + R), R = sum over them of 2^{(x_j - x) scale}.  A token
+// that is nearly sure keeps its digits so (of 1 - p = 10^-4 the sum of all terms holds three).
+__device__ __forceinline__ float sure_of(float x, float scale, const Part &rest) {
+    if (rest.m == -kInf) return x == -kInf ? -kInf : 0.0f;
+    const float d = __builtin_fmaf(x, scale, -rest.m);       // exact but for one rounding
+    return d > -60.0f ? -log1pf(rest.s * exp2f(-d)) : (d - log2f(rest.s)) * kLn2;
 }
 
 // Joins a row's blocks: chunk c of 64 takes every 64th block from the c-th on, one
@@ -206,13 +228,20 @@ constexpr uint32_t kJoinWide = 16;
 template <uint32_t ROWS>
 __global__ __launch_bounds__(ROWS == 1 ? 256 : 64 * ROWS) void rog_linear_join_kernel(JoinArgs p) {
     constexpr uint32_t THREADS = ROWS == 1 ? 256 : 64 * ROWS, EACH = ROWS == 1 ? 4 : ROWS, DEEP = 4;
-    __shared__ Part others[ROWS == 1 ? 1 : THREADS];
+    __shared__ Part others[ROWS == 1 ? 1 : THREADS], other_rests[ROWS == 1 ? 1 : THREADS];
     typedef const __attribute__((address_space(1))) f32x4 gstate;
     const uint32_t rows = p.count ? *p.count : p.rows, chunk = ROWS == 1 ? threadIdx.x % 64 : threadIdx.x / ROWS;
     const uint32_t n = blockIdx.x * EACH + (ROWS == 1 ? threadIdx.x / 64 : threadIdx.x % ROWS);
     if (blockIdx.x * EACH >= rows) return;
-    Part all = {-kInf, 0, 0};
+    // all of the row's columns, and all but its token
+    Part all = {-kInf, 0, 0}, rest = all;
+    uint32_t row = 0;
+    int64_t tok = 0;
     if (n < rows) {
+        row = p.index ? p.index[n] : n;
+        tok = p.tokens ? p.tokens[row] : 0;
+        const f32x4 cut = ((gstate *)p.rests)[n];      // of no meaning where there is no such token
+        const uint32_t cut_block = p.logp && tok >= 0 && tok < int64_t(p.vocab) ? f32_bits(cut[3]) : 0xFFFFFFFFu;
         gstate *from = (gstate *)p.states + uint64_t(n) * p.row_step;
         // a few blocks' loads at a time; past the last an empty state, which changes nothing
         for (uint32_t b = chunk; b < p.blocks; b += 64 * DEEP) {
@@ -220,33 +249,39 @@ __global__ __launch_bounds__(ROWS == 1 ? 256 : 64 * ROWS) void rog_linear_join_k
 #pragma unroll
             for (uint32_t i = 0; i < DEEP; ++i) v[i] = b + 64 * i < p.blocks ? from[uint64_t(b + 64 * i) * p.block_step] : f32x4{-kInf, 0, 0, 0};
 #pragma unroll
-            for (uint32_t i = 0; i < DEEP; ++i) all = join(all, Part{v[i][0], v[i][1], v[i][2]});
+            for (uint32_t i = 0; i < DEEP; ++i) {
+                all = join(all, Part{v[i][0], v[i][1], v[i][2]});
+                if (b + 64 * i == cut_block) v[i] = cut;
+                rest = join(rest, Part{v[i][0], v[i][1], v[i][2]});
+            }
         }
     }
     for (uint32_t d = 32; d; d /= 2) {
         if constexpr (ROWS == 1) {
             all = join(all, Part{__shfl_xor(all.m, d), __shfl_xor(all.s, d), __shfl_xor(all.t, d)});
+            rest = join(rest, Part{__shfl_xor(rest.m, d), __shfl_xor(rest.s, d), __shfl_xor(rest.t, d)});
         } else {
             __syncthreads();
-            if (chunk >= d && chunk < 2 * d) others[threadIdx.x] = all;
+            if (chunk >= d && chunk < 2 * d) {
+                others[threadIdx.x] = all;
+                other_rests[threadIdx.x] = rest;
+            }
             __syncthreads();
-            if (chunk < d) all = join(all, others[threadIdx.x + d * ROWS]);
+            if (chunk < d) {
+                all = join(all, others[threadIdx.x + d * ROWS]);
+                rest = join(rest, other_rests[threadIdx.x + d * ROWS]);
+            }
         }
     }
     if (chunk || n >= rows) return;
-    const uint32_t row = p.index ? p.index[n] : n;
-    const int64_t tok = p.tokens ? p.tokens[row] : 0;
     float logp = 0, entropy = 0, lse = 0;
     if (tok >= 0) {
-        const float log_s = log2f(all.s), at = base_of(all.m);
+        const float log_s = log2f(all.s);
         const bool empty = all.m == -kInf;
         lse = empty ? -kInf : (all.m + log_s) * kLn2;
         entropy = empty ? 0.0f : fmaxf(0.0f, (log_s - all.t / all.s) * kLn2);
         if (!(all.s == all.s)) entropy = all.s;
-        if (p.logp) {
-            logp = tok >= int64_t(p.vocab) ? __builtin_nanf("")
-                   : empty                 ? -kInf : (__builtin_fmaf(p.target[n], p.scale, -at) - log_s) * kLn2;
-        }
+        if (p.logp) logp = !(all.s == all.s) || tok >= int64_t(p.vocab) ? __builtin_nanf("") : empty ? -kInf : sure_of(p.target[n], p.scale, rest);
     }
     if (p.logp) p.logp[row] = logp;
     if (p.entropy) p.entropy[row] = entropy;
