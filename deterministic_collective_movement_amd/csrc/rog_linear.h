@@ -115,7 +115,7 @@ struct BackArgs {
     uint32_t tile_begin, tiles;
     uint32_t seg_begin, segs;          // segments of the piece
     uint32_t row_tiles, dim_tiles;     // upper bounds of the grid
-    float *part;                       // partial sums of d_hidden: [segs][rows][dim_pad], or one running sum
+    float *part;                       // sums of d_hidden: of each of the piece's segments [rows][dim_pad], or running ones
     uint64_t part_seg;                 // floats from a segment's to the next (0: running)
     uint32_t dim_pad;
     uint32_t first, last;              // the running sum's first and last piece
@@ -129,10 +129,13 @@ struct BackArgs {
     int64_t dw_stride[kMaxPeers];      // bytes
 };
 
+// Adds a piece's partial sums to the running ones in the segments' order; after the last piece to d_hidden.
 struct BackJoinArgs {
     const float *part;
+    float *running;
     uint64_t part_seg;
     uint32_t segs, dim_pad, dim;
+    uint32_t first, last;
     const uint32_t *index, *count;
     const float *g_logp, *g_entropy;
     float inv_t;
@@ -197,14 +200,13 @@ constexpr uint32_t kGradTile = 256;
 
 struct GradPlan {
     rog_dtype dtype;
-    int32_t form;                      // few, some or wide
+    int32_t form;                      // few and some: up to 64 rows; mid: few tiles; wide
     bool direct, direct_back, running;
     uint32_t pieces, piece_tiles;      // tiles of a piece: whole segments' or all
     PackArgs pack;
     GradArgs coef;
     BackArgs back;
     BackJoinArgs join;
-    uint32_t join_grid;
     uint64_t workspace_bytes;
 };
 
@@ -225,7 +227,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
                             const rog_grad_shard *d_weights, void *workspace, size_t workspace_bytes, bool addresses, GradPlan *p);
 // Workgroups of a piece's launches.
 struct PieceGrid {
-    uint32_t coefficients, states, weights;
+    uint32_t coefficients, states, weights, join;
 };
 // Sets coef and back to piece i (pieces are laid one after the other).
 PieceGrid lay_piece(GradPlan *p, uint32_t i);

@@ -173,21 +173,50 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
     put_weights<DT, FM, FN, WN>(r, v0, d0, width, acc);
 }
 
-// The states' tiles first: their chains are the longer ones of all but large batches.
+// The longer chains first: the states' run over a segment's (or, running, the piece's) columns, the weights' over the
+// rows.
 template <int DT, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
     ROG_TILE_MEMORY(kStages, kBM * kStepBytes, BN * kStepBytes);
     const uint32_t rows = uniform(*p.a.count), states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
-    if (blockIdx.x < states) {
-        back_states<DT, BN, WM, WN, DIRECT>(p, blockIdx.x, rows, memory);
-        return;
-    }
-    const uint32_t id = blockIdx.x - states;
-    if (id < p.dim_tiles * p.tiles) back_weights<DT, BN, WM, WN>(p, id, rows, memory);
+    const uint32_t weights = p.dim_tiles * p.tiles, before = rows > (p.part_seg ? p.seg_tiles : p.tiles) * kGradTile ? weights : 0;
+    const uint32_t id = blockIdx.x;
+    if (id >= before && id - before < states) back_states<DT, BN, WM, WN, DIRECT>(p, id - before, rows, memory);
+    else if (id < states + weights) back_weights<DT, BN, WM, WN>(p, before ? id : id - states, rows, memory);
 }
 
-// The same for up to 64 rows, bound by the weights' and their gradients' bytes.  d_hidden: 64 elements of a
-// segment for all rows, with seven lines of each operand's rows in flight (a chain over a segment cannot be cut
+// FM x FN fragments of a wave over two steps of K, brought together.
+template <int DT, int FM, int FN, class C>
+struct BothSteps {
+    static __device__ __forceinline__ void run(C &a, C &b, uint32_t m0, uint32_t n0, const TileMemory &mem, f32x4 (&acc)[FM][FN]) {
+#if defined(__HIP_DEVICE_COMPILE__)   // as in Tile
+        const typename C::template Reader<0> ra(m0), rb(n0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            a.stage(mem.a[i]);
+            b.stage(mem.b[i]);
+        }
+        arrive<0>();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            vec16 fa[FM], fb[FN];
+#pragma unroll
+            for (int f = 0; f < FM; ++f) fa[f] = ra.get(mem.a[i], f);
+#pragma unroll
+            for (int f = 0; f < FN; ++f) fb[f] = rb.get(mem.b[i], f);
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[f][j] = Mat<DT>::mma(fa[f], fb[j], acc[f][j]);
+        }
+#else
+        (void)a, (void)b, (void)m0, (void)n0, (void)mem, (void)acc;
+#endif
+    }
+};
+
+// The same for few rows or few tiles.  d_hidden: 64 elements of a
+// segment for 64 rows, with seven lines of each operand's rows in flight (a chain over a segment cannot be cut
 // further, so a workgroup has to bring its share of the weights fast).
 constexpr int kFewElements = 64, kFewSide = 128, kFewThreads = 256, kFewStages = 8;
 template <int DT, bool DIRECT>
@@ -195,28 +224,29 @@ __global__ __launch_bounds__(kFewThreads) void rog_linear_few_states_kernel(Back
     typedef ColLines<kFewThreads, DIRECT> A;
     typedef RowLines<false, 64, kFewThreads, true, 2> B;
     ROG_TILE_MEMORY(kFewStages, A::kBytes, B::kBytes);
-    const uint32_t rows = uniform(*p.a.count), dim_tiles = (p.dim + kFewElements - 1) / kFewElements;
-    if (!rows) return;
-    const uint32_t s = blockIdx.x / dim_tiles, d0 = blockIdx.x % dim_tiles * kFewElements, seg = p.seg_begin + s;
+    const uint32_t rows = uniform(*p.a.count), dim_tiles = (p.dim + kFewElements - 1) / kFewElements, each = dim_tiles * p.row_tiles;
+    const uint32_t s = blockIdx.x / each, d0 = blockIdx.x % dim_tiles * kFewElements, n0 = blockIdx.x % each / dim_tiles * 64;
+    const uint32_t seg = p.seg_begin + s;
+    if (n0 >= rows) return;
     uint32_t r = 0;
     while (seg >= p.seg0[r + 1]) ++r;
     const WeightShard sh = p.sh.s[r];
     const uint32_t tile = (seg - p.seg0[r]) * p.seg_tiles, v0 = tile * kGradTile;
     const uint32_t cols = sh.width - v0 < p.seg_tiles * kGradTile ? sh.width - v0 : p.seg_tiles * kGradTile;
     A a(static_cast<const uint8_t *>(sh.w) + uint64_t(v0) * uint64_t(sh.stride) + d0 * 2, sh.stride, cols, p.dim - d0);
-    B b(static_cast<const uint8_t *>(p.g) + uint64_t(p.sh.tile0[r] + tile - p.tile_begin) * kGradTile * 2, p.g_stride, rows,
-        (cols + 63) / 64 * 128);
+    B b(static_cast<const uint8_t *>(p.g) + uint64_t(n0) * uint64_t(p.g_stride) + uint64_t(p.sh.tile0[r] + tile - p.tile_begin) * kGradTile * 2,
+        p.g_stride, rows - n0, (cols + 63) / 64 * 128);
     const uint32_t wave = threadIdx.x / 64;
     f32x4 acc[2][2] = {};
     Stream<DT, 2, 2, kFewStages, ROG_GROUP, A, B>::run(a, b, (cols + 63) / 64, wave / 2 * 32, wave % 2 * 32, memory, acc);
-    put_states<DT, 2, 2, 2>(s, d0, 0, rows, acc);
+    put_states<DT, 2, 2, 2>(s, d0, n0, rows, acc);
 }
 
-// d_weight: 128 columns x 128 elements, whose K is at most two steps.
-template <int DT>
+// d_weight: 128 columns x 128 elements; of up to 64 rows both steps of K at once.
+template <int DT, bool FEW>
 __global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(BackArgs p) {
     typedef ColSteps<kFewSide, kFewThreads, true> C;
-    ROG_TILE_MEMORY(2, C::kBytes, C::kBytes);
+    ROG_TILE_MEMORY(FEW ? 2 : kStages, C::kBytes, C::kBytes);
     const uint32_t rows = uniform(*p.a.count), sides = (p.dim + kFewSide - 1) / kFewSide;
     const uint32_t part = blockIdx.x / sides, d0 = blockIdx.x % sides * kFewSide;       // of the piece's parts of 128 columns
     const uint32_t tile = p.tile_begin + part / 2, r = shard_of_tile(p.sh, tile);
@@ -224,60 +254,53 @@ __global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(Bac
     if (v0 >= width) return;
     C a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
     C b(static_cast<const uint8_t *>(p.g_all) + uint64_t(part) * kFewSide * 2, p.g_stride, rows, kFewSide);
-    const uint32_t wave = threadIdx.x / 64;
+    const uint32_t wave = threadIdx.x / 64, m0 = wave / 2 * 64, w0 = wave % 2 * 64;
     f32x4 acc[4][4] = {};
-#if defined(__HIP_DEVICE_COMPILE__)
-    const uint32_t m0 = wave / 2 * 64, w0 = wave % 2 * 64;
-    const typename C::template Reader<0> ra(m0), rb(w0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        a.stage(memory.a[i]);
-        b.stage(memory.b[i]);
-    }
-    arrive<0>();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        vec16 fa[4], fb[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            fa[f] = ra.get(memory.a[i], f);
-            fb[f] = rb.get(memory.b[i], f);
-        }
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[f][j] = Mat<DT>::mma(fa[f], fb[j], acc[f][j]);
-    }
+    if constexpr (FEW) BothSteps<DT, 4, 4, C>::run(a, b, m0, w0, memory, acc);
+    else Tile<DT, 4, 4, C, C>().run(a, b, (rows + 31) / 32, false, m0, w0, memory, acc);
     put_weights<DT, 4, 4, 2>(r, v0, d0, width, acc);
-#else
-    (void)acc, (void)memory, (void)wave;
-#endif
 }
 
 // Adds the segments' partial sums of a row in their order.
 template <int DT>
 __global__ __launch_bounds__(256) void rog_linear_back_join_kernel(BackJoinArgs p) {
-    const uint32_t rows = *p.count, vecs = p.dim_pad / 8;
+    const uint32_t rows = *p.count, vecs = p.dim_pad / 8;   // a thread has eight elements of a row
     const uint64_t id = uint64_t(blockIdx.x) * 256 + threadIdx.x;
     const uint32_t n = uint32_t(id / vecs), d = uint32_t(id % vecs) * 8;
     if (n >= rows || d >= p.dim) return;
-    const float *part = p.part + uint64_t(n) * p.dim_pad + d;
     typedef const __attribute__((address_space(1))) f32x4 gf32x4;
+    const uint64_t at = uint64_t(n) * p.dim_pad + d;
     float x[8];
-    for (uint32_t s = 0; s < p.segs; ++s) {
-        const f32x4 lo = ((gf32x4 *)(part + s * p.part_seg))[0], hi = ((gf32x4 *)(part + s * p.part_seg))[1];
+    if (!p.first) {
+        const f32x4 lo = ((gf32x4 *)(p.running + at))[0], hi = ((gf32x4 *)(p.running + at))[1];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float v = i < 4 ? lo[i % 4] : hi[i % 4];
-            x[i] = s ? x[i] + v : v;
+        for (int i = 0; i < 8; ++i) x[i] = i < 4 ? lo[i % 4] : hi[i % 4];
+    }
+    constexpr uint32_t DEEP = 8;       // segments' loads at a time
+    for (uint32_t s = 0; s < p.segs; s += DEEP) {
+        f32x4 v[DEEP][2];
+#pragma unroll
+        for (uint32_t u = 0; u < DEEP; ++u) {
+            const float *from = p.part + (s + u < p.segs ? s + u : s) * p.part_seg + at;
+            v[u][0] = ((gf32x4 *)from)[0];
+            v[u][1] = ((gf32x4 *)from)[1];
         }
+#pragma unroll
+        for (uint32_t u = 0; u < DEEP; ++u)
+            if (s + u < p.segs)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = p.first && s + u == 0 ? v[u][i / 4][i % 4] : x[i] + v[u][i / 4][i % 4];
+    }
+    if (!p.last) {
+        ((gf32x4_out *)(p.running + at))[0] = f32x4{x[0], x[1], x[2], x[3]};
+        ((gf32x4_out *)(p.running + at))[1] = f32x4{x[4], x[5], x[6], x[7]};
+        return;
     }
     const uint32_t row = p.index[n];
     const float inv = unscale<DT>(p, row);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] *= inv;
-    uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
-    put8<DT>(out + d * 2, x, p.dim - d);
+    put8<DT>(static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride) + d * 2, x, p.dim - d);
 }
 
 template <class Args>
@@ -293,7 +316,9 @@ hipError_t launch_back(const GradPlan &p, const BackArgs &a, const PieceGrid &gr
                              : launch(rog_linear_back_kernel<DT, 256, 2, 4, false>, grid.states + grid.weights, 512, a, s);
     const hipError_t e = p.direct_back ? launch(rog_linear_few_states_kernel<DT, true>, grid.states, kFewThreads, a, s)
                                        : launch(rog_linear_few_states_kernel<DT, false>, grid.states, kFewThreads, a, s);
-    return e != hipSuccess ? e : launch(rog_linear_few_weights_kernel<DT>, grid.weights, kFewThreads, a, s);
+    if (e != hipSuccess) return e;
+    return p.form == kFormMid ? launch(rog_linear_few_weights_kernel<DT, false>, grid.weights, kFewThreads, a, s)
+                              : launch(rog_linear_few_weights_kernel<DT, true>, grid.weights, kFewThreads, a, s);
 }
 
 }  // namespace
@@ -318,10 +343,10 @@ ROG_API rog_status rog_linear_logprob_grad(const void *hidden, int64_t hidden_st
         e = launch_coefficients(p, p.coef, grid.coefficients, stream);
         if (e == hipSuccess) e = dtype == ROG_DTYPE_BF16 ? launch_back<ROG_DTYPE_BF16>(p, p.back, grid, stream)
                                                          : launch_back<ROG_DTYPE_F16>(p, p.back, grid, stream);
+        if (e == hipSuccess && grid.join)
+            e = dtype == ROG_DTYPE_BF16 ? launch(rog_linear_back_join_kernel<ROG_DTYPE_BF16>, grid.join, 256, p.join, stream)
+                                        : launch(rog_linear_back_join_kernel<ROG_DTYPE_F16>, grid.join, 256, p.join, stream);
     }
-    if (e == hipSuccess && p.join_grid)
-        e = dtype == ROG_DTYPE_BF16 ? launch(rog_linear_back_join_kernel<ROG_DTYPE_BF16>, p.join_grid, 256, p.join, stream)
-                                    : launch(rog_linear_back_join_kernel<ROG_DTYPE_F16>, p.join_grid, 256, p.join, stream);
     if (e != hipSuccess) {
         g_last_hip_error = int(e);
         return ROG_ERR_LAUNCH;

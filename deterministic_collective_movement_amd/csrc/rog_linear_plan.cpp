@@ -100,6 +100,7 @@ uint32_t tile_rows(int32_t form) { return kFormRows[form]; }
 // Workgroups for so many tiles: the wide form deals some of them out in quarters, by the rows that there turn out to be.
 uint64_t groups_of(uint64_t tiles, int32_t form) { return form == kFormWide && tiles ? tiles + 3 * kTailSplit : tiles; }
 
+constexpr uint64_t kMidCubes = 224, kMidCubesFew = 1024;   // of 256 rows x 256 columns x 256 elements: up to these the mid form
 constexpr uint64_t kPackFrom = 65;   // rows from which the scored ones are packed
 
 // A workspace, laid out front to back: behind the arrival counters of the other operators, which stay zero.
@@ -213,7 +214,12 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (st != ROG_OK) return st;
     lay_tiles(&a.sh, kGradTile);
     const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
-    p->form = rows <= FormFew::kRows ? kFormFew : rows <= FormSome::kRows ? kFormSome : kFormWide;
+    p->form = rows > FormSome::kRows ? kFormWide : rows > FormFew::kRows ? kFormSome : kFormFew;
+    // Little work is spread wider in the small tiles, and up to 128 rows leave half of a large one empty (us, mid and
+    // wide: 544 x 5830 x 128 40 and 51, 243 x 1020 x 384 30 and 45, 1024 x 16000 x 256 85 and 66,
+    // 100 x 32000 x 2048 121 and 207, 128 x 131072 x 4096 1112 and 865).
+    if (p->form == kFormWide && ceil_div(rows, 256) * a.sh.tile0[W] * ceil_div(uint64_t(dim), 256) <= (rows <= 128 ? kMidCubesFew : kMidCubes))
+        p->form = kFormMid;
     const uint32_t bn = p->form == kFormWide ? 256 : 64;
     k = BackArgs{};
     k.sh = a.sh;
@@ -221,7 +227,9 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     k.dim_pad = uint32_t(up(uint64_t(dim), 64));
     k.dim_tiles = uint32_t(ceil_div(uint64_t(dim), 256));
     k.row_tiles = uint32_t(ceil_div(rows, bn));
-    // Segments go by the width of the states alone, so that the sums' order does.
+    // Segments go by the width of the states alone, so that the sums' order does: a segment's sums go through memory,
+    // which costs large batches of narrow states most, while short segments are short chains for small batches (us, of
+    // half these tiles and of these: 8192 x 32000 x 320 911 and 854, 544 x 5830 x 128 37 and 40).
     k.seg_tiles = dim >= 2048 ? 32 : dim >= 512 ? 16 : 8;
     uint32_t segs = 0;
     for (int r = 0; r < W; ++r) {
@@ -229,6 +237,8 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
         segs += uint32_t(ceil_div(a.sh.tile0[r + 1] - a.sh.tile0[r], k.seg_tiles));
     }
     k.seg0[W] = segs;
+    // A tile's sums stay with one workgroup for all of a piece's segments where there are enough tiles for that (us, from
+    // 64 and from 128 tiles: 8192 x 50257 x 768, of 96, 2636 and 2374).
     p->running = p->form == kFormWide && uint64_t(k.dim_tiles) * k.row_tiles >= 128;
     // Pieces are runs of whole segments: as many as the bytes allow.
     const uint64_t tile_bytes = std::max<uint64_t>(1, rows) * kGradTile * 2;
@@ -253,7 +263,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
         ++p->pieces;
     }
     p->piece_tiles = std::max(p->piece_tiles, 1u);
-    const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2 + 3 * kTailSplit;
+    const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2 + 3 * kTailSplit;   // of any form's at most
     const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * 4 * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 4;
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
@@ -261,7 +271,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     const uint64_t g_row = uint64_t(most_tiles) * kGradTile * 2 + ROG_LINEAR_ROW_PAD, g_bytes = rows * g_row;
     const uint64_t g = w.take(g_bytes), g_all = dtype == ROG_DTYPE_F16 ? w.take(g_bytes) : g;
     const uint64_t seg_floats = rows * uint64_t(k.dim_pad);
-    const uint64_t part = w.take(seg_floats * 4 * (p->running ? 1 : segs));
+    const uint64_t part = w.take(p->running ? 0 : seg_floats * 4 * most_segs), running = w.take(p->running || p->pieces > 1 ? seg_floats * 4 : 0);
     p->workspace_bytes = rows ? w.at : 0;
     if (rows == 0 || !addresses) return ROG_OK;
 
@@ -336,18 +346,16 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     k.g = a.g;
     k.g_all = a.g_all;
     k.g_stride = a.g_stride;
-    k.part = in<float>(workspace, part);
+    k.part = in<float>(workspace, p->running ? running : part);
     k.part_seg = p->running ? 0 : seg_floats;
     // along rows, where a row's end inside 16 bytes would be read past, only whole ones
     p->direct_back = p->direct && kbytes % 16 == 0;
     k.d_hidden = d_hidden;
     k.d_stride = d_stride;
-    p->join_grid = 0;
     if (!p->running) {
-        const uint64_t groups = ceil_div(rows * (k.dim_pad / 8), 256);
-        if (groups >= uint64_t(1) << 24) return ROG_ERR_TOO_LARGE;
-        p->join_grid = uint32_t(groups);
-        p->join = BackJoinArgs{k.part, k.part_seg, segs, k.dim_pad, k.dim, k.index, c.count, g_logp, g_entropy, c.inv_t, uint32_t(rows), d_hidden, k.d_stride};
+        if (ceil_div(rows * (k.dim_pad / 8), 256) >= uint64_t(1) << 24) return ROG_ERR_TOO_LARGE;
+        p->join = BackJoinArgs{k.part, in<float>(workspace, running), k.part_seg, 0, k.dim_pad, k.dim, 0, 0, k.index, c.count,
+                               g_logp, g_entropy, c.inv_t, uint32_t(rows), d_hidden, k.d_stride};
     }
     a.tile_begin = a.tiles = k.seg_begin = k.segs = 0;
     return ROG_OK;
@@ -357,10 +365,8 @@ PieceGrid lay_piece(GradPlan *p, uint32_t i) {
     GradArgs &a = p->coef;
     BackArgs &k = p->back;
     const uint32_t W = a.sh.W, segs = k.seg0[W];
-    float *const part = p->back.part;
     uint32_t s = k.seg_begin + k.segs;          // where the last piece ended
     k.tile_begin = a.tile_begin + a.tiles;
-    k.part = part + (p->running ? 0 : uint64_t(k.segs) * k.part_seg);
     k.seg_begin = s;
     k.segs = k.tiles = 0;
     for (uint32_t r = 0; r < W && s < segs; ++r)
@@ -376,9 +382,23 @@ full:
     k.last = s == segs;
     a.tile_begin = k.tile_begin;
     a.tiles = k.tiles;
-    const uint32_t coefficients = uint32_t(groups_of(k.tiles * uint64_t(k.row_tiles) * (kGradTile / tile_columns(p->form)), p->form));
-    if (p->form == kFormWide) return PieceGrid{coefficients, (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles, k.dim_tiles * k.tiles};
-    return PieceGrid{coefficients, k.segs * uint32_t(ceil_div(k.dim, 64)), uint32_t(ceil_div(k.dim, 128)) * k.tiles * 2};
+    PieceGrid g = {};
+    if (p->form == kFormWide) {
+        g.coefficients = uint32_t(groups_of(uint64_t(k.tiles) * k.row_tiles, p->form));
+        g.states = (p->running ? 1 : k.segs) * k.dim_tiles * k.row_tiles;
+        g.weights = k.dim_tiles * k.tiles;
+    } else {
+        g.coefficients = k.tiles * 2 * uint32_t(ceil_div(k.a.rows, tile_rows(p->form)));
+        g.states = k.segs * uint32_t(ceil_div(k.dim, 64)) * k.row_tiles;
+        g.weights = uint32_t(ceil_div(k.dim, 128)) * k.tiles * 2;
+    }
+    if (!p->running) {
+        p->join.segs = k.segs;
+        p->join.first = k.first;
+        p->join.last = k.last;
+        g.join = uint32_t(ceil_div(k.a.rows * uint64_t(k.dim_pad / 8), 256));
+    }
+    return g;
 }
 
 rog_status plan_quantize(const void *x, int64_t row_stride, size_t rows, int64_t dim, rog_dtype dtype, int8_t *q, int64_t q_stride,
@@ -470,7 +490,7 @@ ROG_API rog_status rog_linear_logprob_grad_plan(const rog_weight_shard *shards, 
                                                 nullptr, 0, nullptr, nullptr, 0, false, &p);
     if (st != ROG_OK) return st;
     *info = rog_linear_plan_info{rows ? rog::kGradTile : 0, rows ? (p.form == rog::kFormWide ? 256u : 64u) : 0, rows ? p.pieces : 0,
-                                 rows ? 1 + (p.form == rog::kFormWide ? 2 : 3) * p.pieces + !p.running : 0, p.workspace_bytes};
+                                 rows ? 1 + (p.form == rog::kFormWide ? 2 + !p.running : 4) * p.pieces : 0, p.workspace_bytes};
     return ROG_OK;
 }
 

@@ -496,6 +496,7 @@ template <int DT, bool DIRECT>
 hipError_t launch_coef(const GradPlan &p, const GradArgs &a, uint32_t grid, hipStream_t s) {
     switch (p.form) {
     case kFormWide: return launch(rog_linear_coef_kernel<DT, FormWide, DIRECT>, grid, FormWide::kThreads, a, s);
+    case kFormMid: return launch(rog_linear_coef_kernel<DT, FormMid, DIRECT>, grid, FormMid::kThreads, a, s);
     case kFormSome: return launch(rog_linear_coef_kernel<DT, FormSome, DIRECT>, grid, FormSome::kThreads, a, s);
     default: return launch(rog_linear_coef_kernel<DT, FormFew, DIRECT>, grid, FormFew::kThreads, a, s);
     }

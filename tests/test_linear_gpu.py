@@ -174,6 +174,33 @@ def test_grad_large_batch_in_one_running_sum(gpu):
     check_grad(h, ws, tokens)
 
 
+WIDE = [
+    (1500, [4000, 3001], 515, F16, 0.8),      # large tiles, rows that have to be laid out anew
+    (600, [9000, 9001], 264, F16, 1.0),
+    (2500, [6000], 300, F16, 1.2),            # more rows than a segment has columns
+    (2500, [60000], 64, BF16, 1.0),           # two pieces whose segments are joined
+    (20, [1060000], 16, BF16, 1.0),           # the same of few rows
+    (100, [1060000], 16, F16, 1.0),
+]
+
+
+@pytest.mark.parametrize("n,widths,dim,dtype,T", WIDE)
+def test_grad_large(gpu, n, widths, dim, dtype, T):
+    h, ws, tokens = ref.head(n, widths, dim, dtype, gpu, pad=0.25)
+    check_grad(h, ws, tokens, T)
+
+
+def test_grad_of_a_state_has_the_same_bits_in_a_large_batch(gpu):
+    h, ws, tokens = ref.head(1500, [5000, 3001], 600, BF16, gpu)
+    g, gh = torch.randn(1500, device=gpu), 0.1 * torch.randn(1500, device=gpu)
+    s = rog.rog_linear_logprob(h, ws, tokens)
+    whole = rog.rog_linear_logprob_grad(h, ws, tokens, s.lse, s.entropy, g, gh).d_hidden
+    for rows in ([3], list(range(40)), list(range(0, 1500, 8)), list(range(0, 1500, 3))):
+        i = torch.tensor(rows, device=gpu)
+        part = rog.rog_linear_logprob_grad(h[i], ws, tokens[i], s.lse[i], s.entropy[i], g[i], gh[i]).d_hidden
+        assert torch.equal(part, whole[i]), len(rows)
+
+
 @pytest.mark.parametrize("n", [30, 200])
 def test_grad_strides_leave_what_is_between_rows(gpu, n):
     h, ws, tokens = ref.head(n, [300, 401], 120, BF16, gpu, extra=5)
