@@ -130,24 +130,27 @@ __device__ __forceinline__ void i8_tile(const LinearI8Args &p, uint32_t r, uint3
     i32x4 acc[FM][FN] = {};
     Product::run(a, b, p.a.kbytes, m0, w0, memory, acc);
 
-    constexpr uint32_t OS = Logit<OT>::kSize;
+    constexpr uint32_t OS = Logit<OT>::kSize, LEAVES = FM / 2;
+    const uint32_t v = v0 + m0 + l / 16 * 8;
+    float scale[LEAVES][8];
 #pragma unroll
-    for (int f = 0; f < FM / 2; ++f) {
-        const uint32_t v = v0 + m0 + 32 * f + l / 16 * 8;
-        if (v >= sh.width) continue;
-        const uint32_t left = sh.width - v;
-        float scale[8];
+    for (uint32_t f = 0; f < LEAVES; ++f)
 #pragma unroll
-        for (uint32_t i = 0; i < 8; ++i) scale[i] = i < left ? p.scale[r][v + i] : 0.0f;
+        for (uint32_t i = 0; i < 8; ++i) scale[f][i] = v + 32 * f + i < sh.width ? p.scale[r][v + 32 * f + i] : 0.0f;
+    // a row's leaves one after the other, so that its lines are whole before they leave the cache
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const uint32_t n = n0 + w0 + 16 * j + l % 16;
-            if (n >= rows) continue;
-            const float s = p.row_scale[n];
+    for (int j = 0; j < FN; ++j) {
+        const uint32_t n = n0 + w0 + 16 * j + l % 16;
+        if (n >= rows) continue;
+        const float s = p.row_scale[n];
+        uint8_t *out = static_cast<uint8_t *>(p.out[r]) + uint64_t(n) * uint64_t(p.out_stride[r]) + uint64_t(v) * OS;
+#pragma unroll
+        for (uint32_t f = 0; f < LEAVES; ++f) {
+            if (v + 32 * f >= sh.width) continue;
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = float(acc[2 * f + i / 4][j][i % 4]) * s * scale[i];
-            put_out<OT>(static_cast<uint8_t *>(p.out[r]) + uint64_t(n) * uint64_t(p.out_stride[r]) + uint64_t(v) * OS, x, left);
+            for (int i = 0; i < 8; ++i) x[i] = float(acc[2 * f + i / 4][j][i % 4]) * s * scale[f][i];
+            put_out<OT>(out + 32 * f * OS, x, sh.width - v - 32 * f);
         }
     }
 }
