@@ -173,16 +173,22 @@ struct Form {
     static constexpr int kShare = COLUMNS / WM < int(kLinearBlock) ? int(kLinearBlock) / (COLUMNS / WM) : 1;
     static_assert(COLUMNS % kLinearBlock == 0 && COLUMNS / WM % 32 == 0 && COLUMNS / WM <= int(kLinearBlock), "whole leaves, blocks");
 };
+// Up to 64 rows a call is bound by the weights' bytes: small tiles, whole lines, two or three of them in flight per
+// workgroup and two workgroups per CU (one 32003 x 512 bf16 head: 7.6 us, 4.3 TB/s; 64 rows of 131072 x 4096: 178 us,
+// 6.1 TB/s).  Past that by the matrix units: 256 x 256 take 128 elements of an operand from the shared memory per
+// 16 x 16 x 32 instruction and lane group, the least of the tiles tried (8192 rows of 131072 x 4096: 256 x 128 by
+// eight waves 1060 TFLOP/s and by four 1134, 256 x 256 by 2 x 2 waves 1183, by 2 x 4 1380); eight waves are two per
+// SIMD, with 128 accumulators of their 256 registers each.
 typedef Form<128, 32, 4, 1, 4, false> FormFew;
 typedef Form<128, 64, 4, 1, 3, false> FormSome;
 typedef Form<128, 128, 2, 2, 4, true> FormMid;
 typedef Form<256, 256, 2, 4, 4, true> FormWide;
 typedef Form<128, 128, 2, 4, 4, true> FormQuarter;   // of a wide tile, by as many threads
 constexpr uint32_t kCus = 256;         // workgroups of the wide form that run at a time
-#ifndef ROG_TAIL_SPLIT
-#define ROG_TAIL_SPLIT 64
-#endif
-constexpr uint32_t kTailSplit = ROG_TAIL_SPLIT;
+// Tiles past the last whole round of the CUs up to which they are dealt in quarters: a round of quarters takes less than half of a
+// round of tiles, and 64 tiles are one round of them (1021 x 50257 x 1600 binary16, 20 tiles past the third round: 181 us
+// without, 169 with; splitting up to 128 or 192 tiles gained nothing more).
+constexpr uint32_t kTailSplit = 64;
 enum { kFormFew = 0, kFormSome = 1, kFormMid = 2, kFormWide = 3 };
 
 struct ScorePlan {

@@ -625,8 +625,7 @@ __device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tm, uint32_t tn)
 }
 
 // A workgroup's tile of the wide form: the tiles past the last whole round of the
-// CUs are dealt out in quarters (kTailSplit) where they would leave half of the
-// CUs or more idle.
+// CUs are dealt out in quarters where they are few (kTailSplit).
 struct Place {
     TileAt at;
     uint32_t quarter;                  // 4: the whole tile

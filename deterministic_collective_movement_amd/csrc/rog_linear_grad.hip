@@ -121,9 +121,6 @@ __device__ __forceinline__ void put_weights(uint32_t r, uint32_t v0, uint32_t d0
     }
 }
 
-#ifndef ROG_GROUP
-#define ROG_GROUP 2
-#endif
 constexpr int kBM = 256;   // elements of the states and weights of a tile
 
 template <int DT, int BN, int WM, int WN, bool DIRECT>
@@ -173,8 +170,11 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
     put_weights<DT, FM, FN, WN>(r, v0, d0, width, acc);
 }
 
-// The longer chains first: the states' run over a segment's (or, running, the piece's) columns, the weights' over the
-// rows.
+// Both products of a piece, in tiles of 256 x 256.  The longer chains first: the states' run over a segment's (or, running, the piece's)
+// columns, the weights' over the rows (8192 x 32000 x 320: 911 us so, 1033 with the states' always first).  Bound by the
+// matrix units (4096 x 32768 of 4096 bf16, 3584 rows scored: 1.55 ms, 1240 TFLOP/s): ds_read_b64_tr_b16 brings half the
+// bytes of ds_read_b128 per instruction, so an operand with K along its rows costs twice the reads of one with rows
+// along K, and the weights' product has two.
 template <int DT, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
     ROG_TILE_MEMORY(kStages, kBM * kStepBytes, BN * kStepBytes);
@@ -215,10 +215,11 @@ struct BothSteps {
     }
 };
 
-// The same for few rows or few tiles.  d_hidden: 64 elements of a
-// segment for 64 rows, with seven lines of each operand's rows in flight (a chain over a segment cannot be cut
-// further, so a workgroup has to bring its share of the weights fast).
-constexpr int kFewElements = 64, kFewSide = 128, kFewThreads = 256, kFewStages = 8;
+// The same for few rows or little work.  d_hidden: 64 elements of a segment for 64 rows, up to seven lines of each
+// operand's rows in flight and two multiplied at a time: a chain over a segment cannot be cut further, so a workgroup
+// has to bring its share of the weights fast (33 x 32003 x 1024: the call 69.3, 58.3 and 64.1 us with 1, 2 and 4 lines
+// at a time; the kernel 23 us for the 66 MB of weights, 128 workgroups with a CU each).
+constexpr int kFewElements = 64, kFewSide = 128, kFewThreads = 256, kFewStages = 8, kFewGroup = 2;
 template <int DT, bool DIRECT>
 __global__ __launch_bounds__(kFewThreads) void rog_linear_few_states_kernel(BackArgs p) {
     typedef ColLines<kFewThreads, DIRECT> A;
@@ -238,11 +239,12 @@ __global__ __launch_bounds__(kFewThreads) void rog_linear_few_states_kernel(Back
         p.g_stride, rows - n0, (cols + 63) / 64 * 128);
     const uint32_t wave = threadIdx.x / 64;
     f32x4 acc[2][2] = {};
-    Stream<DT, 2, 2, kFewStages, ROG_GROUP, A, B>::run(a, b, (cols + 63) / 64, wave / 2 * 32, wave % 2 * 32, memory, acc);
+    Stream<DT, 2, 2, kFewStages, kFewGroup, A, B>::run(a, b, (cols + 63) / 64, wave / 2 * 32, wave % 2 * 32, memory, acc);
     put_states<DT, 2, 2, 2>(s, d0, n0, rows, acc);
 }
 
-// d_weight: 128 columns x 128 elements; of up to 64 rows both steps of K at once.
+// d_weight: 128 columns x 128 elements; of up to 64 rows both steps of K at once.  Bound by the gradient's bytes (33 x 32003 x 1024:
+// 17.7 us for 66 MB, 3.7 TB/s; a workgroup is one load, one product and one write).
 template <int DT, bool FEW>
 __global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(BackArgs p) {
     typedef ColSteps<kFewSide, kFewThreads, true> C;
@@ -261,7 +263,8 @@ __global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(Bac
     put_weights<DT, 4, 4, 2>(r, v0, d0, width, acc);
 }
 
-// Adds the segments' partial sums of a row in their order.
+// Adds the segments' partial sums of a row in their order, eight of them in flight (893 x 1600, 13 segments: 19.7 us
+// for 75 MB; 33 x 1024, 8 segments: 4.7).
 template <int DT>
 __global__ __launch_bounds__(256) void rog_linear_back_join_kernel(BackJoinArgs p) {
     const uint32_t rows = *p.count, vecs = p.dim_pad / 8;   // a thread has eight elements of a row

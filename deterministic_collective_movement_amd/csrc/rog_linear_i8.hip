@@ -17,7 +17,9 @@ namespace {
 
 // A row per workgroup: the largest magnitude, then the quotients.  Rows of up to
 // kHeld vectors of 16 bytes per thread stay in registers between the two, longer ones are
-// read again from the caches.
+// read again from the caches.  The division is the correctly rounded one, so any plain form gives the same integers.  One row of
+// 2048 bf16 3.0 us, 48 of 4096 4.8 (a launch), 4093 of 5120 binary16 21 us (63 MB, 3.0 TB/s), a fiftieth of
+// the product behind it.
 constexpr uint32_t kQuantThreads = 256;
 constexpr int kHeld = 4;
 
@@ -155,6 +157,11 @@ __device__ __forceinline__ void i8_tile(const LinearI8Args &p, uint32_t r, uint3
     }
 }
 
+// The product, its scales and one rounding to the output.  Many rows: 4093 x 50257 x 5120 to binary16 1.00-1.03 ms, 2060 TOP/s
+// (a large library product of 8-bit integers reaches 2339), of which the main loop alone runs at 2870 and the rest are 411 MB
+// of outputs, written between a tile's product and the next one's: by leaves of all rows instead of by rows, a line
+// was evicted before it was whole, 775 MB and 1.10 ms.  Few rows are bound by the weights' bytes (48 x 131072 x 4096:
+// 107-118 us, 4.6-5.2 TB/s; one row of 32000 x 2048 13.6 us, 4.8 TB/s).
 template <int OT, class F, bool DIRECT>
 __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_i8_kernel(LinearI8Args p) {
     typedef RowProduct<kTypeI8, F, DIRECT, 1, F::kWide> Product;

@@ -20,17 +20,13 @@ constexpr double kLog2E = 1.4426950408889634;
 // Bytes behind a row of coefficients, whose own are a multiple of 512: with rows 2^16 bytes apart a tile's
 // rows fall on few of the memory's channels (4096 rows of 65536 x 4096: 5.78 ms without, 5.24 with 256,
 // 5.29 / 5.51 / 5.32 with 128 / 512 / 1024).
-#ifndef ROG_LINEAR_ROW_PAD
-#define ROG_LINEAR_ROW_PAD 256
-#endif
+constexpr uint64_t kRowPad = 256;
 // Large tiles up to which 128 x 128 ones are taken instead: half of the CUs or fewer would be at work (200 rows of
 // 32000 x 2048 56.5 us with 125 large tiles, 50.1 with 500; 600 rows of 16000 x 2048 60 with 189, 68 with 625).
-#ifndef ROG_MID_TILES
-#define ROG_MID_TILES 128
-#endif
-#ifndef ROG_LINEAR_PIECE_BYTES
-#define ROG_LINEAR_PIECE_BYTES (256ull << 20)
-#endif
+constexpr uint64_t kMidTiles = 128;
+// Bytes of a piece's coefficients: written once and read twice, they fit the Infinity Cache, and a piece of a large batch
+// is still eight rounds of the CUs and more (4096 rows of 65536 x 4096: 128, 256 and 512 MiB within 2 %).
+constexpr uint64_t kPieceBytes = 256ull << 20;
 
 inline bool product_type(rog_dtype t) { return t == ROG_DTYPE_BF16 || t == ROG_DTYPE_F16; }
 inline uint64_t up(uint64_t v, uint64_t unit) { return ceil_div(v, unit) * unit; }
@@ -90,7 +86,7 @@ int32_t form_of(uint64_t rows, const WeightShards &h) {
     uint64_t wide = 0;
     for (uint32_t r = 0; r < h.W; ++r) wide += ceil_div(h.s[r].width, FormWide::kColumns);
     wide *= ceil_div(rows, FormWide::kRows);
-    return rows <= FormMid::kRows || wide <= ROG_MID_TILES ? kFormMid : kFormWide;
+    return rows <= FormMid::kRows || wide <= kMidTiles ? kFormMid : kFormWide;
 }
 constexpr uint32_t kFormColumns[] = {FormFew::kColumns, FormSome::kColumns, FormMid::kColumns, FormWide::kColumns};
 constexpr uint32_t kFormRows[] = {FormFew::kRows, FormSome::kRows, FormMid::kRows, FormWide::kRows};
@@ -101,7 +97,10 @@ uint32_t tile_rows(int32_t form) { return kFormRows[form]; }
 uint64_t groups_of(uint64_t tiles, int32_t form) { return form == kFormWide && tiles ? tiles + 3 * kTailSplit : tiles; }
 
 constexpr uint64_t kMidCubes = 224, kMidCubesFew = 1024;   // of 256 rows x 256 columns x 256 elements: up to these the mid form
-constexpr uint64_t kPackFrom = 65;   // rows from which the scored ones are packed
+// Rows from which the scored ones are packed: few rows are one tile whether scored or not, and a launch is 4 us more;
+// of many the tiles of rows that do not count are saved (8192 x 4096: 25 us, where every eighth row that does not count
+// takes an eighth of 6.5 ms with it).
+constexpr uint64_t kPackFrom = 65;
 
 // A workspace, laid out front to back: behind the arrival counters of the other operators, which stay zero.
 struct Layout {
@@ -242,7 +241,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     p->running = p->form == kFormWide && uint64_t(k.dim_tiles) * k.row_tiles >= 128;
     // Pieces are runs of whole segments: as many as the bytes allow.
     const uint64_t tile_bytes = std::max<uint64_t>(1, rows) * kGradTile * 2;
-    uint64_t tiles = std::max<uint64_t>(1, ROG_LINEAR_PIECE_BYTES / tile_bytes);
+    uint64_t tiles = std::max<uint64_t>(1, kPieceBytes / tile_bytes);
     p->piece_tiles = uint32_t(std::min<uint64_t>(std::max<uint64_t>(tiles, k.seg_tiles), 4096));
     // Count them as lay_piece() walks.
     p->pieces = 0;
@@ -268,7 +267,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
     const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), rows_at = w.take(rows * packed);
-    const uint64_t g_row = uint64_t(most_tiles) * kGradTile * 2 + ROG_LINEAR_ROW_PAD, g_bytes = rows * g_row;
+    const uint64_t g_row = uint64_t(most_tiles) * kGradTile * 2 + kRowPad, g_bytes = rows * g_row;
     const uint64_t g = w.take(g_bytes), g_all = dtype == ROG_DTYPE_F16 ? w.take(g_bytes) : g;
     const uint64_t seg_floats = rows * uint64_t(k.dim_pad);
     const uint64_t part = w.take(p->running ? 0 : seg_floats * 4 * most_segs), running = w.take(p->running || p->pieces > 1 ? seg_floats * 4 : 0);

@@ -565,8 +565,10 @@ typedef struct {
  *          and such rows take no time where there are more than 64 rows.
  *
  * Logits are binary32 and not rounded to the states' type, so a row's numbers
- * are nearer to the formula than rog_logprob's over logits of two bytes.  A NaN or
- * +inf among a row's logits makes its numbers NaN.
+ * are nearer to the formula than rog_logprob's over logits of two bytes.  The log
+ * probability is formed from the terms beside the token, so a token that is nearly
+ * sure keeps its digits (about 10^-6 of the value, beside what the logits' own sums
+ * leave open).  A NaN or +inf among a row's logits makes its numbers NaN.
  *
  * Errors as rog_logprob.
  */
