@@ -201,6 +201,17 @@ def test_grad_of_a_state_has_the_same_bits_in_a_large_batch(gpu):
         assert torch.equal(part, whole[i]), len(rows)
 
 
+def test_grad_large_of_rows_that_are_not_scored(gpu):
+    h, ws, tokens = ref.head(2100, [6000], 520, F16, gpu)
+    one = torch.ones(2100, device=gpu)
+    for scored in (0, 1, 70):
+        tokens[scored:] = -1
+        s = rog.rog_linear_logprob(h, ws, tokens)
+        r = rog.rog_linear_logprob_grad(h, ws, tokens, s.lse, s.entropy, one)
+        assert bool((r.d_hidden[scored:] == 0).all()) and bool((r.d_weights[0] == 0).all()) == (scored == 0)
+        tokens[:] = torch.arange(2100, device=gpu)
+
+
 @pytest.mark.parametrize("n", [30, 200])
 def test_grad_strides_leave_what_is_between_rows(gpu, n):
     h, ws, tokens = ref.head(n, [300, 401], 120, BF16, gpu, extra=5)
