@@ -127,6 +127,9 @@ struct BackArgs {
     uint32_t seg_tiles;                // tiles of a segment
     void *dw[kMaxPeers];
     int64_t dw_stride[kMaxPeers];      // bytes
+    uint32_t splits;                   // parts of the rows that the weights' gradients are summed over apart
+    float *dw_part;                    // their sums: [splits][columns of the piece][dim_pad], if there are several
+    uint64_t dw_part_split;            // floats from a part's to the next
 };
 
 // Adds a piece's partial sums to the running ones in the segments' order; after the last piece to d_hidden.
@@ -233,7 +236,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
                             const rog_grad_shard *d_weights, void *workspace, size_t workspace_bytes, bool addresses, GradPlan *p);
 // Workgroups of a piece's launches.
 struct PieceGrid {
-    uint32_t coefficients, states, weights, join;
+    uint32_t coefficients, states, weights, join, weights_join;
 };
 // Sets coef and back to piece i (pieces are laid one after the other).
 PieceGrid lay_piece(GradPlan *p, uint32_t i);

@@ -97,9 +97,19 @@ __device__ __forceinline__ void put_states(uint32_t s, uint32_t d0, uint32_t n0,
             }
 }
 
-// A tile's sums for columns v0 on and elements d0 on of shard r.
+// The rows of part `split`: whole lines of 64, the same number but for the last.
+struct RowPart {
+    uint32_t first, rows;
+};
+__device__ __forceinline__ RowPart part_of(uint32_t split, uint32_t splits, uint32_t rows) {
+    if (splits == 1) return RowPart{0, rows};
+    const uint32_t each = ((rows + splits - 1) / splits + 63) / 64 * 64, first = split * each;
+    return RowPart{first < rows ? first : 0, first >= rows ? 0 : rows - first < each ? rows - first : each};
+}
+
+// A tile's sums for columns v0 on and elements d0 on of shard r, of part `split` of the rows.
 template <int DT, int FM, int FN, int WN>
-__device__ __forceinline__ void put_weights(uint32_t r, uint32_t v0, uint32_t d0, uint32_t width, f32x4 (&acc)[FM][FN]) {
+__device__ __forceinline__ void put_weights(uint32_t split, uint32_t r, uint32_t v0, uint32_t d0, uint32_t width, f32x4 (&acc)[FM][FN]) {
     const BackArgs &p = fresh_args<BackArgs>();
     pair_all(acc);
     const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
@@ -113,6 +123,13 @@ __device__ __forceinline__ void put_weights(uint32_t r, uint32_t v0, uint32_t d0
         for (int f = 0; f < FM / 2; ++f) {
             const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
             if (d >= p.dim) continue;
+            if (p.splits > 1) {
+                const uint32_t column = (p.sh.tile0[r] - p.tile_begin) * kGradTile + v;      // of the piece
+                gf32x4_out *at = (gf32x4_out *)(p.dw_part + split * p.dw_part_split + uint64_t(column) * p.dim_pad + d);
+                at[0] = acc[2 * f][j];
+                at[1] = acc[2 * f + 1][j];
+                continue;
+            }
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4] * inv;
@@ -158,16 +175,19 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
     typedef ColSteps<kBM, THREADS, true> A;
     typedef ColSteps<BN, THREADS, true> B;
     static_assert(BN == int(kGradTile), "a tile of the piece");
-    const TileAt at = tile_at(id, p.dim_tiles, p.tiles);
+    const uint32_t all = p.dim_tiles * p.tiles, split = id / all;
+    const RowPart part = part_of(split, p.splits, rows);
+    const TileAt at = tile_at(id % all, p.dim_tiles, p.tiles);
     const uint32_t tile = p.tile_begin + at.n, d0 = at.m * kBM;
     const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * kGradTile, width = p.sh.s[r].width;
-    A a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
-    B b(static_cast<const uint8_t *>(p.g_all) + uint64_t(at.n) * BN * 2, p.g_stride, rows, BN);
+    A a(static_cast<const uint8_t *>(p.a.x) + uint64_t(part.first) * uint64_t(p.a.stride) + d0 * 2, p.a.stride, part.rows,
+        uint32_t(p.a.stride) / 2 - d0);
+    B b(static_cast<const uint8_t *>(p.g_all) + uint64_t(part.first) * uint64_t(p.g_stride) + uint64_t(at.n) * BN * 2, p.g_stride, part.rows, BN);
     const uint32_t wave = fresh_thread() / 64;
     f32x4 acc[FM][FN] = {};
-    Tile<DT, FM, FN, A, B>().run(a, b, (rows + 31) / 32, false, wave / WN * (FM * 16), wave % WN * (FN * 16), memory, acc);
+    Tile<DT, FM, FN, A, B>().run(a, b, (part.rows + 31) / 32, false, wave / WN * (FM * 16), wave % WN * (FN * 16), memory, acc);
 
-    put_weights<DT, FM, FN, WN>(r, v0, d0, width, acc);
+    put_weights<DT, FM, FN, WN>(split, r, v0, d0, width, acc);
 }
 
 // Both products of a piece, in tiles of 256 x 256.  The longer chains first: the states' run over a segment's (or, running, the piece's)
@@ -179,7 +199,7 @@ template <int DT, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
     ROG_TILE_MEMORY(kStages, kBM * kStepBytes, BN * kStepBytes);
     const uint32_t rows = uniform(*p.a.count), states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
-    const uint32_t weights = p.dim_tiles * p.tiles, before = rows > (p.part_seg ? p.seg_tiles : p.tiles) * kGradTile ? weights : 0;
+    const uint32_t weights = p.dim_tiles * p.tiles * p.splits, before = rows / p.splits > (p.part_seg ? p.seg_tiles : p.tiles) * kGradTile ? weights : 0;
     const uint32_t id = blockIdx.x;
     if (id >= before && id - before < states) back_states<DT, BN, WM, WN, DIRECT>(p, id - before, rows, memory);
     else if (id < states + weights) back_weights<DT, BN, WM, WN>(p, before ? id : id - states, rows, memory);
@@ -250,17 +270,21 @@ __global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(Bac
     typedef ColSteps<kFewSide, kFewThreads, true> C;
     ROG_TILE_MEMORY(FEW ? 2 : kStages, C::kBytes, C::kBytes);
     const uint32_t rows = uniform(*p.a.count), sides = (p.dim + kFewSide - 1) / kFewSide;
-    const uint32_t part = blockIdx.x / sides, d0 = blockIdx.x % sides * kFewSide;       // of the piece's parts of 128 columns
+    const uint32_t all = sides * p.tiles * 2, split = FEW ? 0 : blockIdx.x / all, id = blockIdx.x - split * all;
+    const RowPart of = part_of(split, FEW ? 1 : p.splits, rows);
+    const uint32_t part = id / sides, d0 = id % sides * kFewSide;       // of the piece's parts of 128 columns
     const uint32_t tile = p.tile_begin + part / 2, r = shard_of_tile(p.sh, tile);
     const uint32_t v0 = (tile - p.sh.tile0[r]) * kGradTile + part % 2 * kFewSide, width = p.sh.s[r].width;
     if (v0 >= width) return;
-    C a(static_cast<const uint8_t *>(p.a.x) + d0 * 2, p.a.stride, rows, uint32_t(p.a.stride) / 2 - d0);
-    C b(static_cast<const uint8_t *>(p.g_all) + uint64_t(part) * kFewSide * 2, p.g_stride, rows, kFewSide);
+    C a(static_cast<const uint8_t *>(p.a.x) + uint64_t(of.first) * uint64_t(p.a.stride) + d0 * 2, p.a.stride, of.rows,
+        uint32_t(p.a.stride) / 2 - d0);
+    C b(static_cast<const uint8_t *>(p.g_all) + uint64_t(of.first) * uint64_t(p.g_stride) + uint64_t(part) * kFewSide * 2, p.g_stride, of.rows,
+        kFewSide);
     const uint32_t wave = threadIdx.x / 64, m0 = wave / 2 * 64, w0 = wave % 2 * 64;
     f32x4 acc[4][4] = {};
     if constexpr (FEW) BothSteps<DT, 4, 4, C>::run(a, b, m0, w0, memory, acc);
-    else Tile<DT, 4, 4, C, C>().run(a, b, (rows + 31) / 32, false, m0, w0, memory, acc);
-    put_weights<DT, 4, 4, 2>(r, v0, d0, width, acc);
+    else Tile<DT, 4, 4, C, C>().run(a, b, (of.rows + 31) / 32, false, m0, w0, memory, acc);
+    put_weights<DT, 4, 4, 2>(split, r, v0, d0, width, acc);
 }
 
 // Adds the segments' partial sums of a row in their order, eight of them in flight (893 x 1600, 13 segments: 19.7 us
@@ -306,6 +330,31 @@ __global__ __launch_bounds__(256) void rog_linear_back_join_kernel(BackJoinArgs 
     put8<DT>(static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride) + d * 2, x, p.dim - d);
 }
 
+// Adds the parts' sums of a column of the piece in their order; a thread has eight elements.
+template <int DT>
+__global__ __launch_bounds__(256) void rog_linear_weights_join_kernel(BackArgs p) {
+    const uint32_t vecs = p.dim_pad / 8;
+    const uint64_t id = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint32_t column = uint32_t(id / vecs), d = uint32_t(id % vecs) * 8;
+    if (column >= p.tiles * kGradTile || d >= p.dim) return;
+    const uint32_t tile = p.tile_begin + column / kGradTile, r = shard_of_tile(p.sh, tile);
+    const uint32_t v = (tile - p.sh.tile0[r]) * kGradTile + column % kGradTile;
+    if (v >= p.sh.s[r].width) return;
+    typedef const __attribute__((address_space(1))) f32x4 gf32x4;
+    const float *from = p.dw_part + uint64_t(column) * p.dim_pad + d;
+    f32x4 lo = ((gf32x4 *)from)[0], hi = ((gf32x4 *)from)[1];
+    for (uint32_t s = 1; s < p.splits; ++s) {
+        from += p.dw_part_split;
+        lo = lo + ((gf32x4 *)from)[0];
+        hi = hi + ((gf32x4 *)from)[1];
+    }
+    const float inv = DT == ROG_DTYPE_F16 ? 1.0f / *p.g_scale : 1.0f;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (i < 4 ? lo[i % 4] : hi[i % 4]) * inv;
+    put8<DT>(static_cast<uint8_t *>(p.dw[r]) + uint64_t(v) * uint64_t(p.dw_stride[r]) + d * 2, x, p.dim - d);
+}
+
 template <class Args>
 hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
     void *list[] = {const_cast<Args *>(&args)};
@@ -349,6 +398,9 @@ ROG_API rog_status rog_linear_logprob_grad(const void *hidden, int64_t hidden_st
         if (e == hipSuccess && grid.join)
             e = dtype == ROG_DTYPE_BF16 ? launch(rog_linear_back_join_kernel<ROG_DTYPE_BF16>, grid.join, 256, p.join, stream)
                                         : launch(rog_linear_back_join_kernel<ROG_DTYPE_F16>, grid.join, 256, p.join, stream);
+        if (e == hipSuccess && grid.weights_join)
+            e = dtype == ROG_DTYPE_BF16 ? launch(rog_linear_weights_join_kernel<ROG_DTYPE_BF16>, grid.weights_join, 256, p.back, stream)
+                                        : launch(rog_linear_weights_join_kernel<ROG_DTYPE_F16>, grid.weights_join, 256, p.back, stream);
     }
     if (e != hipSuccess) {
         g_last_hip_error = int(e);

@@ -96,6 +96,10 @@ uint32_t tile_rows(int32_t form) { return kFormRows[form]; }
 // Workgroups for so many tiles: the wide form deals some of them out in quarters, by the rows that there turn out to be.
 uint64_t groups_of(uint64_t tiles, int32_t form) { return form == kFormWide && tiles ? tiles + 3 * kTailSplit : tiles; }
 
+// Rows of a part at least, where the weights' sums are cut: a part's sums go through memory and are joined (us, whole and in parts
+// of 1024, 2048 and 4096 rows and more: 65536 x 1000 x 256 1326, 302, 254, 261; 8192 x 4000 x 320 218, 134, 124, 155;
+// 4096 x 4000 x 512 128, 136, 133, 127).
+constexpr uint64_t kPartRows = 2048;
 constexpr uint64_t kMidCubes = 224, kMidCubesFew = 1024;   // of 256 rows x 256 columns x 256 elements: up to these the mid form
 // Rows from which the scored ones are packed: few rows are one tile whether scored or not, and a launch is 4 us more;
 // of many the tiles of rows that do not count are saved (8192 x 4096: 25 us, where every eighth row that does not count
@@ -263,7 +267,10 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     }
     p->piece_tiles = std::max(p->piece_tiles, 1u);
     const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2 + 3 * kTailSplit;   // of any form's at most
-    const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * 4 * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 4;
+    const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * 4 * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 4 + kCus;
+    // The weights' sums over many rows are cut where their tiles leave CUs idle.
+    const uint64_t sums = p->form == kFormWide ? uint64_t(k.dim_tiles) * most_tiles : ceil_div(uint64_t(dim), 128) * most_tiles * 2;
+    k.splits = sums ? uint32_t(std::max<uint64_t>(1, std::min<uint64_t>(kCus / sums, rows / kPartRows))) : 1;
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
     const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), rows_at = w.take(rows * packed);
@@ -271,6 +278,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     const uint64_t g = w.take(g_bytes), g_all = dtype == ROG_DTYPE_F16 ? w.take(g_bytes) : g;
     const uint64_t seg_floats = rows * uint64_t(k.dim_pad);
     const uint64_t part = w.take(p->running ? 0 : seg_floats * 4 * most_segs), running = w.take(p->running || p->pieces > 1 ? seg_floats * 4 : 0);
+    const uint64_t split_floats = uint64_t(most_tiles) * kGradTile * k.dim_pad, dw_part = w.take(k.splits > 1 ? split_floats * 4 * k.splits : 0);
     p->workspace_bytes = rows ? w.at : 0;
     if (rows == 0 || !addresses) return ROG_OK;
 
@@ -347,6 +355,8 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     k.g_stride = a.g_stride;
     k.part = in<float>(workspace, p->running ? running : part);
     k.part_seg = p->running ? 0 : seg_floats;
+    k.dw_part = in<float>(workspace, dw_part);
+    k.dw_part_split = split_floats;
     // along rows, where a row's end inside 16 bytes would be read past, only whole ones
     p->direct_back = p->direct && kbytes % 16 == 0;
     k.d_hidden = d_hidden;
@@ -391,6 +401,8 @@ full:
         g.states = k.segs * uint32_t(ceil_div(k.dim, 64)) * k.row_tiles;
         g.weights = uint32_t(ceil_div(k.dim, 128)) * k.tiles * 2;
     }
+    g.weights *= k.splits;
+    if (k.splits > 1) g.weights_join = uint32_t(ceil_div(uint64_t(k.tiles) * kGradTile * (k.dim_pad / 8), 256));
     if (!p->running) {
         p->join.segs = k.segs;
         p->join.first = k.first;
@@ -489,7 +501,7 @@ ROG_API rog_status rog_linear_logprob_grad_plan(const rog_weight_shard *shards, 
                                                 nullptr, 0, nullptr, nullptr, 0, false, &p);
     if (st != ROG_OK) return st;
     *info = rog_linear_plan_info{rows ? rog::kGradTile : 0, rows ? (p.form == rog::kFormWide ? 256u : 64u) : 0, rows ? p.pieces : 0,
-                                 rows ? 1 + (p.form == rog::kFormWide ? 2 + !p.running : 4) * p.pieces : 0, p.workspace_bytes};
+                                 rows ? 1 + (p.form == rog::kFormWide ? 2 + !p.running : 4) * p.pieces + (p.back.splits > 1) * p.pieces : 0, p.workspace_bytes};
     return ROG_OK;
 }
 

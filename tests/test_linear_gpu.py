@@ -181,6 +181,9 @@ WIDE = [
     (2500, [60000], 64, BF16, 1.0),           # two pieces whose segments are joined
     (20, [1060000], 16, BF16, 1.0),           # the same of few rows
     (100, [1060000], 16, F16, 1.0),
+    (9000, [130, 255], 33, F16, 1.0),         # many rows, few weights: sums over parts of the rows
+    (9000, [1000, 700], 520, BF16, 0.9),
+    (70000, [200], 520, F16, 1.0),            # the same in large tiles
 ]
 
 
