@@ -5,11 +5,12 @@
 // False if anything about it is out of the ordinary -- an argument that the
 // library would refuse, a workspace that has to be made or grown, a stream
 // that is being captured -- and has then enqueued nothing: rog.py takes the
-// call from there, and raises what is to be raised.  It holds no tensor and
-// allocates nothing.  (Through ctypes alone these calls take 4 to 6
+// call from there, and raises what is to be raised.  It keeps no tensor, and
+// allocates but the head's products' workspaces.  (Through ctypes alone these calls take 4 to 6
 // microseconds of Python beside 3 to 4 of launching.)
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <mutex>
@@ -28,6 +29,8 @@ struct Bound {
     decltype(&rog_linear_logprob_grad) linear_grad = nullptr;
     decltype(&rog_quantize_i8) quantize = nullptr;
     decltype(&rog_linear_i8) linear_i8 = nullptr;
+    decltype(&rog_linear_logprob_plan) linear_logprob_plan = nullptr;
+    decltype(&rog_linear_logprob_grad_plan) linear_grad_plan = nullptr;
     int max_peers = 0;
     PyObject *current_device = nullptr, *raw_stream = nullptr, *capturing = nullptr;
 } bound;
@@ -184,6 +187,18 @@ struct Head {
     }
 };
 
+// A workspace of one call's own, made on the current stream by torch's allocator:
+// the head's products hand data from launch to launch through it, and another
+// thread's call on the same stream may come between two of them.  It goes back when
+// the call has enqueued them all, for what is enqueued on this stream behind them.
+struct Scratch {
+    at::Tensor t;
+    Scratch(int device, size_t bytes) {
+        if (bytes) t = at::empty({int64_t(bytes)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, c10::DeviceIndex(device)));
+    }
+    void *address() const { return t.defined() ? t.data_ptr() : nullptr; }
+};
+
 bool number(PyObject *o, float *f) {
     const double v = PyFloat_AsDouble(o);
     *f = float(v);
@@ -313,10 +328,14 @@ PyObject *py_linear_logprob(PyObject *, PyObject *const *a, Py_ssize_t n) {
             !vector(o[1], rows, at::kFloat, device, &out.entropy) || !vector(o[2], rows, at::kFloat, device, &out.lse) ||
             o[3] != Py_None || o[4] != Py_None)
             return false;
-        const Where at(device, true);
-        return at.ok && launched([&] {
+        const Where at(device, false);
+        rog_linear_plan_info need;
+        if (!at.ok || bound.linear_logprob_plan(head.s, int(head.W), size_t(rows), head.h.columns, head.dtype, tokens != nullptr, &need) != ROG_OK)
+            return false;
+        const Scratch ws(device, need.workspace_bytes);
+        return launched([&] {
             return bound.linear_logprob(head.h.p, head.h.stride, size_t(rows), head.h.columns, head.s, int(head.W), head.dtype, temperature,
-                                        tokens, &out, at.ws.address, at.ws.bytes, at.hip());
+                                        tokens, &out, ws.address(), need.workspace_bytes, at.hip());
         });
     });
 }
@@ -336,10 +355,13 @@ PyObject *py_linear_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!vector(a[2], head.h.rows, at::kLong, head.h.device, &tokens)) return false;
         for (int i = 0; i < 4; ++i)
             if ((i < 3 && a[3 + i] == Py_None) || !vector(a[3 + i], head.h.rows, at::kFloat, head.h.device, &v[i])) return false;
-        const Where at(head.h.device, true);
-        return at.ok && launched([&] {
+        const Where at(head.h.device, false);
+        rog_linear_plan_info need;
+        if (!at.ok || bound.linear_grad_plan(head.s, int(head.W), size_t(head.h.rows), head.h.columns, head.dtype, &need) != ROG_OK) return false;
+        const Scratch ws(head.h.device, need.workspace_bytes);
+        return launched([&] {
             return bound.linear_grad(head.h.p, head.h.stride, size_t(head.h.rows), head.h.columns, head.s, int(head.W), head.dtype,
-                                     temperature, tokens, v[0], v[1], v[2], v[3], d.p, d.stride, g, at.ws.address, at.ws.bytes, at.hip());
+                                     temperature, tokens, v[0], v[1], v[2], v[3], d.p, d.stride, g, ws.address(), need.workspace_bytes, at.hip());
         });
     });
 }
@@ -407,12 +429,12 @@ PyObject *py_bind(PyObject *, PyObject *args) {
     PyObject *entries, *device, *stream, *capturing;
     int max_peers;
     if (!PyArg_ParseTuple(args, "O!iOOO", &PyTuple_Type, &entries, &max_peers, &device, &stream, &capturing)) return nullptr;
-    unsigned long long e[7];
-    if (PyTuple_GET_SIZE(entries) != 7) {
-        PyErr_SetString(PyExc_ValueError, "seven entry points");
+    unsigned long long e[9];
+    if (PyTuple_GET_SIZE(entries) != 9) {
+        PyErr_SetString(PyExc_ValueError, "nine entry points");
         return nullptr;
     }
-    for (int i = 0; i < 7; ++i) {
+    for (int i = 0; i < 9; ++i) {
         e[i] = PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(entries, i));
         if (PyErr_Occurred()) return nullptr;
     }
@@ -426,6 +448,8 @@ PyObject *py_bind(PyObject *, PyObject *args) {
     bound.linear_grad = reinterpret_cast<decltype(bound.linear_grad)>(e[4]);
     bound.quantize = reinterpret_cast<decltype(bound.quantize)>(e[5]);
     bound.linear_i8 = reinterpret_cast<decltype(bound.linear_i8)>(e[6]);
+    bound.linear_logprob_plan = reinterpret_cast<decltype(bound.linear_logprob_plan)>(e[7]);
+    bound.linear_grad_plan = reinterpret_cast<decltype(bound.linear_grad_plan)>(e[8]);
     bound.max_peers = max_peers;
     bound.current_device = device;
     bound.raw_stream = stream;

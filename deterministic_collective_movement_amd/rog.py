@@ -644,6 +644,8 @@ _MAX_TOP_K = int(_lib.rog_max_top_k())
 
 # One workspace per stream, so that calls on different streams never share one;
 # zero-filled when it is made, as the library asks, and left ready by every call.
+# Threads that share a stream share it: a call is one launch, and launches on a
+# stream do not overlap.  (The head's products are several: _with_scratch.)
 _workspaces: dict = {}
 _workspaces_lock = threading.Lock()
 _NO_WORKSPACE = (None, 0)
@@ -668,16 +670,12 @@ def _made_on(stream, device: torch.device):
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device))
 
 
-def _own_workspace(nbytes: int, device: torch.device, stream, handle: int, counters: bool = True):
-    """(address, bytes) of the stream's workspace, made or grown to hold ``nbytes``.
-    ``counters``: the call needs the counters at its front cleared."""
+def _own_workspace(nbytes: int, device: torch.device, stream, handle: int):
+    """(address, bytes) of the stream's workspace, made or grown to hold ``nbytes``."""
     if nbytes == 0:
         return _NO_WORKSPACE
     if _capturing(stream, device):
         # a graph's replays may run beside eager calls on this stream: the graph gets its own, cleared in the graph
-        if not counters:
-            with _made_on(stream, device):
-                return torch.empty(nbytes, dtype=torch.uint8, device=device).data_ptr(), nbytes
         t = rog_workspace(nbytes, device, stream)
         return t.data_ptr(), nbytes
     key = (device.index, handle)
@@ -698,7 +696,8 @@ _raw_stream_of = _raw_stream or (lambda device: torch.cuda.current_stream(device
 if _binding is not None:
     _binding.bind(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.rog_logprob_ex, _lib.rog_logprob_grad, _lib.rog_policy_loss,
                                                                         _lib.rog_linear_logprob, _lib.rog_linear_logprob_grad,
-                                                                        _lib.rog_quantize_i8, _lib.rog_linear_i8)),
+                                                                        _lib.rog_quantize_i8, _lib.rog_linear_i8,
+                                                                        _lib.rog_linear_logprob_plan, _lib.rog_linear_logprob_grad_plan)),
                   _lib.rog_max_peers(), _current_device, _raw_stream_of, _is_capturing)
 
 
@@ -711,7 +710,7 @@ def _capturing(stream, device: torch.device) -> bool:
         return _is_capturing()
 
 
-def _with_workspace(call, need, what: str, workspace, device: torch.device, stream, handle: int, counters: bool = True) -> None:
+def _with_workspace(call, need, what: str, workspace, device: torch.device, stream, handle: int) -> None:
     """``call(address, bytes)`` with the caller's workspace or the stream's own.
     The library refuses one that is too small before it enqueues anything, so
     ``need()``, the bytes it asks for, is only looked up where the stream's own
@@ -729,7 +728,26 @@ def _with_workspace(call, need, what: str, workspace, device: torch.device, stre
             return
         if status != ROG_ERR_INVALID_ARGUMENT or got[1] >= need():
             _check(status, what)
-    _check(call(*_own_workspace(need(), device, stream, handle, counters)), what)
+    _check(call(*_own_workspace(need(), device, stream, handle)), what)
+
+
+def _with_scratch(call, need, what: str, workspace, device: torch.device, stream) -> None:
+    """``call(address, bytes)`` with the caller's workspace or one of the call's own,
+    from torch's allocator.  For calls of several launches that hand data to each
+    other through it: another thread's call on the same stream may come between
+    two of them.  Once all are enqueued its memory goes back, for whatever is
+    enqueued on this stream behind them."""
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", device)
+        _check(call(workspace.data_ptr(), _nbytes(workspace)), what)
+        return
+    nbytes = need()
+    if nbytes == 0:
+        _check(call(*_NO_WORKSPACE), what)
+        return
+    with _made_on(stream, device):
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _check(call(scratch.data_ptr(), nbytes), what)
 
 
 def _vector_error(t, what: str, n: int, dtype: torch.dtype, device: torch.device):
@@ -1082,10 +1100,10 @@ def rog_linear_logprob(hidden: torch.Tensor, weights: Sequence[torch.Tensor], to
     W, dt = len(weights), DTYPES[dtype]
     with _on_device(device) if _current_device() != idx else _HERE:
         handle = _stream_handle(stream, device)
-        _with_workspace(lambda ws, n: _lib.rog_linear_logprob(at, stride, rows, dim, packed, W, dt, temperature, tok, outs, ws, n, handle),
-                        lambda: _linear_plan(_lib.rog_linear_logprob_plan, "rog_linear_logprob", packed, W, rows, dim, dt,
-                                             int(tokens is not None)).workspace_bytes,
-                        "rog_linear_logprob", workspace, device, stream, handle, counters=False)
+        _with_scratch(lambda ws, n: _lib.rog_linear_logprob(at, stride, rows, dim, packed, W, dt, temperature, tok, outs, ws, n, handle),
+                      lambda: _linear_plan(_lib.rog_linear_logprob_plan, "rog_linear_logprob", packed, W, rows, dim, dt,
+                                           int(tokens is not None)).workspace_bytes,
+                      "rog_linear_logprob", workspace, device, stream)
     return out
 
 
@@ -1123,11 +1141,11 @@ def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor
     grads, dt = _PACK_GRADS[W](*vals), DTYPES[dtype]
     with _on_device(device) if _current_device() != idx else _HERE:
         handle = _stream_handle(stream, device)
-        _with_workspace(lambda ws, n: _lib.rog_linear_logprob_grad(at, stride, rows, dim, packed, W, dt, temperature, tok, *vec, d_at,
-                                                                   d_stride, grads, ws, n, handle),
-                        lambda: _linear_plan(_lib.rog_linear_logprob_grad_plan, "rog_linear_logprob_grad", packed, W, rows, dim,
-                                             dt).workspace_bytes,
-                        "rog_linear_logprob_grad", workspace, device, stream, handle, counters=False)
+        _with_scratch(lambda ws, n: _lib.rog_linear_logprob_grad(at, stride, rows, dim, packed, W, dt, temperature, tok, *vec, d_at,
+                                                                 d_stride, grads, ws, n, handle),
+                      lambda: _linear_plan(_lib.rog_linear_logprob_grad_plan, "rog_linear_logprob_grad", packed, W, rows, dim,
+                                           dt).workspace_bytes,
+                      "rog_linear_logprob_grad", workspace, device, stream)
     return out
 
 

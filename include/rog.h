@@ -320,7 +320,8 @@ ROG_API rog_status rog_reduce_many(const rog_reduce_desc *descs, int n, int W, r
  *  - A workspace is device memory of the caller, aligned to 16 bytes.  It is
  *    zero-filled by the caller once, before its first use; every call leaves
  *    it ready for the next.  Calls that may run at the same time (on different
- *    streams) each need their own.
+ *    streams) each need their own.  Calls on one stream may share one, from
+ *    several threads too: each is one launch (not so the head's products, below).
  *  - All sums and row statistics are held in binary32 or binary64.
  *  - Logits are read inside their rows, or inside the aligned 32-bit word that
  *    holds some of a row's bytes; what is read beyond a row is never used.
@@ -524,9 +525,12 @@ ROG_API size_t rog_policy_loss_workspace_bytes(size_t n);
  *    or on alignment or strides.
  *  - A call may be several kernel launches on `stream`, one after the other;
  *    nothing else is enqueued.
- *  - The workspaces need no clearing of their own; the one that rog_workspace-style
- *    callers keep zero-filled for the other operators may serve these too (its
- *    arrival counters are left zero).
+ *  - The launches hand data from one to the next through the workspace, so a call
+ *    needs it to itself until all of them are enqueued: threads that call on one
+ *    stream at the same time each bring their own (or take turns), as calls on
+ *    different streams do.  It needs no clearing; the one that callers keep
+ *    zero-filled for the other operators may serve these too (its arrival
+ *    counters are left zero).
  *  - dim is 1 .. 2^17 - 1; row strides are below 2^22 bytes (ROG_ERR_TOO_LARGE).
  *    Any alignment to the element; calls whose rows all begin and end on 16 bytes
  *    are faster.
