@@ -349,7 +349,9 @@ PyObject *py_linear_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
         float temperature;
         const int64_t *tokens;
         const float *v[4];
-        if (n != 10 || !head.read(a[0], a[1]) || head.h.type == at::kChar || !number(a[7], &temperature) || a[2] == Py_None) return false;
+        // without rows the library enqueues nothing: rog.py fills the weights' gradients
+        if (n != 10 || !head.read(a[0], a[1]) || head.h.type == at::kChar || !number(a[7], &temperature) || a[2] == Py_None || head.h.rows == 0)
+            return false;
         if (!d.read(a[8]) || !d.is(head.h.rows, head.h.columns, head.h.type, head.h.device) || !head.outputs(a[9], true, head.h.type, g))
             return false;
         if (!vector(a[2], head.h.rows, at::kLong, head.h.device, &tokens)) return false;

@@ -1114,7 +1114,7 @@ def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor
     """Gradient of sum_i (g_logp[i] logp[i] + g_entropy[i] entropy[i]) in the hidden
     states and in every shard's weights, from rog_linear_logprob's ``lse`` and
     ``entropy`` of the same states, weights and temperature.  Rows that are not
-    scored get zeros.  ``out``: a RogLinearGrad (or (d_hidden, W matrices)) to write."""
+    scored get zeros, and so do the weights where there are no rows.  ``out``: a RogLinearGrad (or (d_hidden, W matrices)) to write."""
     if out is not None and workspace is None and stream is None:
         if type(out) is not RogLinearGrad:
             out = RogLinearGrad(out[0], list(out[1]))
@@ -1146,6 +1146,11 @@ def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor
                       lambda: _linear_plan(_lib.rog_linear_logprob_grad_plan, "rog_linear_logprob_grad", packed, W, rows, dim,
                                            dt).workspace_bytes,
                       "rog_linear_logprob_grad", workspace, device, stream)
+        if rows == 0:
+            # the library enqueues nothing: a sum over no rows is zero
+            with _made_on(stream, device):
+                for g in out.d_weights:
+                    g.zero_()
     return out
 
 

@@ -602,7 +602,9 @@ ROG_API rog_status rog_linear_logprob_plan(const rog_weight_shard *shards, int W
  * A row that is not scored gets zeros and its state is not used.  A token of V or
  * more, or a NaN in the row's inputs, makes the row's gradient and every weight's
  * NaN, as the formula has it.  V is at least 1.  d_weight's bits depend on the
- * scored rows in their order.
+ * scored rows in their order.  With rows == 0 nothing is enqueued (ROG_OK):
+ * the weights' gradients, then sums over no rows, are left as they are, and a caller
+ * who reads them fills them with zeros (the Python binding does).
  *
  * d_weights  W gradients [width][dim], row strides of their own (>= dim).
  * Errors as rog_logprob_grad; no output may overlap an input or another output.
