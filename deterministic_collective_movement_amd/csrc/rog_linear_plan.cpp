@@ -143,7 +143,8 @@ rog_status plan_linear_logprob(const void *hidden, int64_t hidden_stride, size_t
     const uint64_t kbytes = uint64_t(dim) * 2, packed = up(kbytes, kPackUnit);
     if (!p->packs && !aligned(hidden, uint64_t(h_stride))) p->direct = false;
     const uint64_t groups = groups_of(a.sh.tile0[W] * ceil_div(rows, tile_rows(p->form)), p->form);
-    if (groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
+    // the join has 64 threads per row, of whole workgroups of 16 rows: a dispatch counts work-items in 32 bits
+    if (groups >= kMaxGroups || up(rows, 16) * 64 >= uint64_t(1) << 32) return ROG_ERR_TOO_LARGE;
     p->grid = uint32_t(groups);
     const uint32_t blocks = a.sh.block0[W], rows_pad = uint32_t(up(rows, 16));
     // a row's states together where a wave joins a row, else a block's

@@ -574,7 +574,7 @@ typedef struct {
  * sure keeps its digits (about 10^-6 of the value, beside what the logits' own sums
  * leave open).  A NaN or +inf among a row's logits makes its numbers NaN.
  *
- * Errors as rog_logprob.
+ * Errors as rog_logprob; rows are at most 2^26 - 16 (ROG_ERR_TOO_LARGE).
  */
 ROG_API rog_status rog_linear_logprob(const void *hidden, int64_t hidden_stride, size_t rows, int64_t dim,
                                       const rog_weight_shard *shards, int W, rog_dtype dtype, float temperature,
