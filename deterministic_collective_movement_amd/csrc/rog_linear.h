@@ -88,6 +88,8 @@ struct PackArgs {
     const float *g_logp, *g_entropy;   // binary16: the largest of them sets the scale
     float *g_scale;
     float inv_t;
+    uint32_t *parts;                   // of the weights' sums: weight_parts() of the scored rows (NULL: not wanted)
+    uint32_t dim_tiles, tiles, seg_tiles;
 };
 
 struct GradArgs {
@@ -127,7 +129,8 @@ struct BackArgs {
     uint32_t seg_tiles;                // tiles of a segment
     void *dw[kMaxPeers];
     int64_t dw_stride[kMaxPeers];      // bytes
-    uint32_t splits;                   // parts of the rows that the weights' gradients are summed over apart
+    uint32_t splits;                   // parts of the rows that the weights' gradients are summed over apart, at most
+    const uint32_t *parts;             // device: how many there are (read if there may be several)
     float *dw_part;                    // their sums: [splits][columns of the piece][dim_pad], if there are several
     uint64_t dw_part_split;            // floats from a part's to the next
 };
@@ -206,6 +209,29 @@ struct ScorePlan {
 
 // Columns of a tile of the gradient's pieces.
 constexpr uint32_t kGradTile = 256;
+// Bytes of a piece's coefficients (one segment at least): written once and read twice, they fit the Infinity Cache, and a
+// piece of a large batch is still eight rounds of the CUs and more (4096 rows of 65536 x 4096: 128, 256 and 512 MiB within 2 %).
+constexpr uint64_t kPieceBytes = 256ull << 20;
+constexpr uint32_t kMostPieceTiles = 4096;
+// Rows of a part at least, where the weights' sums are cut: a part's sums go through memory and are joined (us, whole and in parts
+// of 1024, 2048 and 4096 rows and more: 65536 x 1000 x 256 1326, 302, 254, 261; 8192 x 4000 x 320 218, 134, 124, 155;
+// 4096 x 4000 x 512 128, 136, 133, 127).
+constexpr uint32_t kPartRows = 2048;
+
+// Tiles of a piece for so many rows.
+__host__ __device__ inline uint32_t piece_tiles(uint64_t rows, uint32_t seg_tiles) {
+    const uint64_t tiles = kPieceBytes / ((rows ? rows : 1) * kGradTile * 2);
+    return uint32_t(tiles < seg_tiles ? seg_tiles : tiles > kMostPieceTiles ? kMostPieceTiles : tiles);
+}
+
+// Parts that the weights' sums over `rows` scored rows are cut into: where a piece's 256 x 256 tiles of the weights would
+// leave CUs idle, as many as there are CUs for.  The sums' order goes by this, so it goes by the scored rows (which
+// the device counts) and not by the rows of the call, nor by the form or the pieces that those decide.
+__host__ __device__ inline uint32_t weight_parts(uint32_t rows, uint32_t dim_tiles, uint32_t tiles, uint32_t seg_tiles) {
+    const uint32_t piece = piece_tiles(rows, seg_tiles), sums = dim_tiles * (tiles < piece ? tiles : piece);
+    const uint32_t idle = kCus / sums, most = rows / kPartRows, parts = idle < most ? idle : most;
+    return parts ? parts : 1;
+}
 
 struct GradPlan {
     rog_dtype dtype;

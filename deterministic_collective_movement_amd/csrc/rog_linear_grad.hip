@@ -101,15 +101,16 @@ __device__ __forceinline__ void put_states(uint32_t s, uint32_t d0, uint32_t n0,
 struct RowPart {
     uint32_t first, rows;
 };
-__device__ __forceinline__ RowPart part_of(uint32_t split, uint32_t splits, uint32_t rows) {
-    if (splits == 1) return RowPart{0, rows};
-    const uint32_t each = ((rows + splits - 1) / splits + 63) / 64 * 64, first = split * each;
+__device__ __forceinline__ RowPart part_of(uint32_t split, uint32_t parts, uint32_t rows) {
+    if (parts == 1) return RowPart{0, rows};
+    const uint32_t each = ((rows + parts - 1) / parts + 63) / 64 * 64, first = split * each;
     return RowPart{first < rows ? first : 0, first >= rows ? 0 : rows - first < each ? rows - first : each};
 }
+__device__ __forceinline__ uint32_t parts_of(const BackArgs &p) { return p.splits > 1 ? uniform(*p.parts) : 1; }
 
 // A tile's sums for columns v0 on and elements d0 on of shard r, of part `split` of the rows.
 template <int DT, int FM, int FN, int WN>
-__device__ __forceinline__ void put_weights(uint32_t split, uint32_t r, uint32_t v0, uint32_t d0, uint32_t width, f32x4 (&acc)[FM][FN]) {
+__device__ __forceinline__ void put_weights(uint32_t split, uint32_t parts, uint32_t r, uint32_t v0, uint32_t d0, uint32_t width, f32x4 (&acc)[FM][FN]) {
     const BackArgs &p = fresh_args<BackArgs>();
     pair_all(acc);
     const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
@@ -123,7 +124,7 @@ __device__ __forceinline__ void put_weights(uint32_t split, uint32_t r, uint32_t
         for (int f = 0; f < FM / 2; ++f) {
             const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
             if (d >= p.dim) continue;
-            if (p.splits > 1) {
+            if (parts > 1) {
                 const uint32_t column = (p.sh.tile0[r] - p.tile_begin) * kGradTile + v;      // of the piece
                 gf32x4_out *at = (gf32x4_out *)(p.dw_part + split * p.dw_part_split + uint64_t(column) * p.dim_pad + d);
                 at[0] = acc[2 * f][j];
@@ -170,13 +171,13 @@ __device__ __forceinline__ void back_states(const BackArgs &p, uint32_t id, uint
 }
 
 template <int DT, int BN, int WM, int WN>
-__device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uint32_t rows, const TileMemory &memory) {
+__device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uint32_t parts, uint32_t rows, const TileMemory &memory) {
     constexpr int THREADS = 64 * WM * WN, FM = kBM / WM / 16, FN = BN / WN / 16;
     typedef ColSteps<kBM, THREADS, true> A;
     typedef ColSteps<BN, THREADS, true> B;
     static_assert(BN == int(kGradTile), "a tile of the piece");
     const uint32_t all = p.dim_tiles * p.tiles, split = id / all;
-    const RowPart part = part_of(split, p.splits, rows);
+    const RowPart part = part_of(split, parts, rows);
     const TileAt at = tile_at(id % all, p.dim_tiles, p.tiles);
     const uint32_t tile = p.tile_begin + at.n, d0 = at.m * kBM;
     const uint32_t r = shard_of_tile(p.sh, tile), v0 = (tile - p.sh.tile0[r]) * kGradTile, width = p.sh.s[r].width;
@@ -187,7 +188,7 @@ __device__ __forceinline__ void back_weights(const BackArgs &p, uint32_t id, uin
     f32x4 acc[FM][FN] = {};
     Tile<DT, FM, FN, A, B>().run(a, b, (part.rows + 31) / 32, false, wave / WN * (FM * 16), wave % WN * (FN * 16), memory, acc);
 
-    put_weights<DT, FM, FN, WN>(split, r, v0, d0, width, acc);
+    put_weights<DT, FM, FN, WN>(split, parts, r, v0, d0, width, acc);
 }
 
 // Both products of a piece, in tiles of 256 x 256.  The longer chains first: the states' run over a segment's (or, running, the piece's)
@@ -199,10 +200,10 @@ template <int DT, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(64 * WM * WN) void rog_linear_back_kernel(BackArgs p) {
     ROG_TILE_MEMORY(kStages, kBM * kStepBytes, BN * kStepBytes);
     const uint32_t rows = uniform(*p.a.count), states = (p.part_seg ? p.segs : 1) * p.dim_tiles * ((rows + BN - 1) / BN);
-    const uint32_t weights = p.dim_tiles * p.tiles * p.splits, before = rows / p.splits > (p.part_seg ? p.seg_tiles : p.tiles) * kGradTile ? weights : 0;
+    const uint32_t parts = parts_of(p), weights = p.dim_tiles * p.tiles * parts, before = rows / parts > (p.part_seg ? p.seg_tiles : p.tiles) * kGradTile ? weights : 0;
     const uint32_t id = blockIdx.x;
     if (id >= before && id - before < states) back_states<DT, BN, WM, WN, DIRECT>(p, id - before, rows, memory);
-    else if (id < states + weights) back_weights<DT, BN, WM, WN>(p, before ? id : id - states, rows, memory);
+    else if (id < states + weights) back_weights<DT, BN, WM, WN>(p, before ? id : id - states, parts, rows, memory);
 }
 
 // FM x FN fragments of a wave over two steps of K, brought together.
@@ -271,7 +272,9 @@ __global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(Bac
     ROG_TILE_MEMORY(FEW ? 2 : kStages, C::kBytes, C::kBytes);
     const uint32_t rows = uniform(*p.a.count), sides = (p.dim + kFewSide - 1) / kFewSide;
     const uint32_t all = sides * p.tiles * 2, split = FEW ? 0 : blockIdx.x / all, id = blockIdx.x - split * all;
-    const RowPart of = part_of(split, FEW ? 1 : p.splits, rows);
+    const uint32_t parts = FEW ? 1 : parts_of(p);
+    if (split >= parts) return;
+    const RowPart of = part_of(split, parts, rows);
     const uint32_t part = id / sides, d0 = id % sides * kFewSide;       // of the piece's parts of 128 columns
     const uint32_t tile = p.tile_begin + part / 2, r = shard_of_tile(p.sh, tile);
     const uint32_t v0 = (tile - p.sh.tile0[r]) * kGradTile + part % 2 * kFewSide, width = p.sh.s[r].width;
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(kFewThreads) void rog_linear_few_weights_kernel(Bac
     f32x4 acc[4][4] = {};
     if constexpr (FEW) BothSteps<DT, 4, 4, C>::run(a, b, m0, w0, memory, acc);
     else Tile<DT, 4, 4, C, C>().run(a, b, (of.rows + 31) / 32, false, m0, w0, memory, acc);
-    put_weights<DT, 4, 4, 2>(split, r, v0, d0, width, acc);
+    put_weights<DT, 4, 4, 2>(split, parts, r, v0, d0, width, acc);
 }
 
 // Adds the segments' partial sums of a row in their order, eight of them in flight (893 x 1600, 13 segments: 19.7 us
@@ -333,7 +336,8 @@ __global__ __launch_bounds__(256) void rog_linear_back_join_kernel(BackJoinArgs 
 // Adds the parts' sums of a column of the piece in their order; a thread has eight elements.
 template <int DT>
 __global__ __launch_bounds__(256) void rog_linear_weights_join_kernel(BackArgs p) {
-    const uint32_t vecs = p.dim_pad / 8;
+    const uint32_t vecs = p.dim_pad / 8, parts = parts_of(p);
+    if (parts == 1) return;            // the sums are where they belong
     const uint64_t id = uint64_t(blockIdx.x) * 256 + threadIdx.x;
     const uint32_t column = uint32_t(id / vecs), d = uint32_t(id % vecs) * 8;
     if (column >= p.tiles * kGradTile || d >= p.dim) return;
@@ -343,7 +347,7 @@ __global__ __launch_bounds__(256) void rog_linear_weights_join_kernel(BackArgs p
     typedef const __attribute__((address_space(1))) f32x4 gf32x4;
     const float *from = p.dw_part + uint64_t(column) * p.dim_pad + d;
     f32x4 lo = ((gf32x4 *)from)[0], hi = ((gf32x4 *)from)[1];
-    for (uint32_t s = 1; s < p.splits; ++s) {
+    for (uint32_t s = 1; s < parts; ++s) {
         from += p.dw_part_split;
         lo = lo + ((gf32x4 *)from)[0];
         hi = hi + ((gf32x4 *)from)[1];

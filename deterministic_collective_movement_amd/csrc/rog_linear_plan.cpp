@@ -15,8 +15,6 @@ constexpr uint64_t kMaxGroups = uint64_t(1) << 22;   // workgroups of a launch (
 constexpr float kMinTemperature = 1.0f / 1024, kMaxTemperature = 1024.0f;
 constexpr double kLog2E = 1.4426950408889634;
 
-// Tunables, measured on MI355X; a variant build may override one with -D.
-// Bytes of the coefficients' piece of the vocabulary (one segment at least).
 // Bytes behind a row of coefficients, whose own are a multiple of 512: with rows 2^16 bytes apart a tile's
 // rows fall on few of the memory's channels (4096 rows of 65536 x 4096: 5.78 ms without, 5.24 with 256,
 // 5.29 / 5.51 / 5.32 with 128 / 512 / 1024).
@@ -24,9 +22,6 @@ constexpr uint64_t kRowPad = 256;
 // Large tiles up to which 128 x 128 ones are taken instead: half of the CUs or fewer would be at work (200 rows of
 // 32000 x 2048 56.5 us with 125 large tiles, 50.1 with 500; 600 rows of 16000 x 2048 60 with 189, 68 with 625).
 constexpr uint64_t kMidTiles = 128;
-// Bytes of a piece's coefficients: written once and read twice, they fit the Infinity Cache, and a piece of a large batch
-// is still eight rounds of the CUs and more (4096 rows of 65536 x 4096: 128, 256 and 512 MiB within 2 %).
-constexpr uint64_t kPieceBytes = 256ull << 20;
 
 inline bool product_type(rog_dtype t) { return t == ROG_DTYPE_BF16 || t == ROG_DTYPE_F16; }
 inline uint64_t up(uint64_t v, uint64_t unit) { return ceil_div(v, unit) * unit; }
@@ -96,10 +91,6 @@ uint32_t tile_rows(int32_t form) { return kFormRows[form]; }
 // Workgroups for so many tiles: the wide form deals some of them out in quarters, by the rows that there turn out to be.
 uint64_t groups_of(uint64_t tiles, int32_t form) { return form == kFormWide && tiles ? tiles + 3 * kTailSplit : tiles; }
 
-// Rows of a part at least, where the weights' sums are cut: a part's sums go through memory and are joined (us, whole and in parts
-// of 1024, 2048 and 4096 rows and more: 65536 x 1000 x 256 1326, 302, 254, 261; 8192 x 4000 x 320 218, 134, 124, 155;
-// 4096 x 4000 x 512 128, 136, 133, 127).
-constexpr uint64_t kPartRows = 2048;
 constexpr uint64_t kMidCubes = 224, kMidCubesFew = 1024;   // of 256 rows x 256 columns x 256 elements: up to these the mid form
 // Rows from which the scored ones are packed: few rows are one tile whether scored or not, and a launch is 4 us more;
 // of many the tiles of rows that do not count are saved (8192 x 4096: 25 us, where every eighth row that does not count
@@ -245,9 +236,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     // 64 and from 128 tiles: 8192 x 50257 x 768, of 96, 2636 and 2374).
     p->running = p->form == kFormWide && uint64_t(k.dim_tiles) * k.row_tiles >= 128;
     // Pieces are runs of whole segments: as many as the bytes allow.
-    const uint64_t tile_bytes = std::max<uint64_t>(1, rows) * kGradTile * 2;
-    uint64_t tiles = std::max<uint64_t>(1, kPieceBytes / tile_bytes);
-    p->piece_tiles = uint32_t(std::min<uint64_t>(std::max<uint64_t>(tiles, k.seg_tiles), 4096));
+    p->piece_tiles = piece_tiles(rows, k.seg_tiles);
     // Count them as lay_piece() walks.
     p->pieces = 0;
     uint32_t most_tiles = 0, most_segs = 0;
@@ -266,15 +255,13 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
         most_segs = std::max(most_segs, n);
         ++p->pieces;
     }
-    p->piece_tiles = std::max(p->piece_tiles, 1u);
     const uint64_t coef_groups = uint64_t(most_tiles) * k.row_tiles * 2 + 3 * kTailSplit;   // of any form's at most
     const uint64_t back_groups = uint64_t(p->running ? 1 : most_segs) * k.dim_tiles * 4 * k.row_tiles + uint64_t(k.dim_tiles) * most_tiles * 4 + kCus;
-    // The weights' sums over many rows are cut where their tiles leave CUs idle.
-    const uint64_t sums = p->form == kFormWide ? uint64_t(k.dim_tiles) * most_tiles : ceil_div(uint64_t(dim), 128) * most_tiles * 2;
-    k.splits = sums ? uint32_t(std::max<uint64_t>(1, std::min<uint64_t>(kCus / sums, rows / kPartRows))) : 1;
+    // The weights' sums over many rows are cut where their tiles leave CUs idle, into the more the more rows are scored.
+    k.splits = weight_parts(uint32_t(rows), k.dim_tiles, a.sh.tile0[W], k.seg_tiles);
     if (coef_groups >= kMaxGroups || back_groups >= kMaxGroups) return ROG_ERR_TOO_LARGE;
     Layout w;
-    const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), rows_at = w.take(rows * packed);
+    const uint64_t index = w.take(rows * 4), count = w.take(4), g_scale = w.take(4), parts = w.take(4), rows_at = w.take(rows * packed);
     const uint64_t g_row = uint64_t(most_tiles) * kGradTile * 2 + kRowPad, g_bytes = rows * g_row;
     const uint64_t g = w.take(g_bytes), g_all = dtype == ROG_DTYPE_F16 ? w.take(g_bytes) : g;
     const uint64_t seg_floats = rows * uint64_t(k.dim_pad);
@@ -328,6 +315,10 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     c.packed = in<void>(workspace, rows_at);
     c.zero = d_hidden;
     c.zero_stride = d_stride;
+    c.parts = k.splits > 1 ? in<uint32_t>(workspace, parts) : nullptr;
+    c.dim_tiles = k.dim_tiles;
+    c.tiles = a.sh.tile0[W];
+    c.seg_tiles = k.seg_tiles;
     c.g_logp = g_logp;
     c.g_entropy = g_entropy;
     c.g_scale = dtype == ROG_DTYPE_F16 ? in<float>(workspace, g_scale) : nullptr;
@@ -356,6 +347,7 @@ rog_status plan_linear_grad(const void *hidden, int64_t hidden_stride, size_t ro
     k.g_stride = a.g_stride;
     k.part = in<float>(workspace, p->running ? running : part);
     k.part_seg = p->running ? 0 : seg_floats;
+    k.parts = c.parts;
     k.dw_part = in<float>(workspace, dw_part);
     k.dw_part_split = split_floats;
     // along rows, where a row's end inside 16 bytes would be read past, only whole ones

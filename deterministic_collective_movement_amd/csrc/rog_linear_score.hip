@@ -345,7 +345,10 @@ __global__ __launch_bounds__(kPackThreads) void rog_linear_pack_kernel(PackArgs 
         }
     }
     before += uint32_t(__popcll(own));
-    if (t == 0 && row0 + ROWS >= p.rows) *p.count = before;
+    if (t == 0 && row0 + ROWS >= p.rows) {
+        *p.count = before;
+        if (p.parts) *p.parts = weight_parts(before, p.dim_tiles, p.tiles, p.seg_tiles);
+    }
     if (!p.g_scale || blockIdx.x) return;
     // one scale of all rows' coefficients, for the products that sum over rows
     float m = 0;
