@@ -20,6 +20,10 @@ struct Part {
     float m, s, t;
 };
 constexpr float kFar = -1000.0f;   // 2^kFar is 0, and 0 times it is 0
+// A state's m is rounded, and its terms' exponents x log2(e) / T - m take the rest of that along, up to 2^(e - 25) of
+// |m| = 2^e either way: s is then off by as much and m + log2 s is right.  From here on the rest would leave exponents' range,
+// so x log2(e) / T is rounded as m is before the difference.  (Columns masked by -10^10 to -10^38 were NaN without.)
+constexpr float kHuge = 1073741824.0f;
 
 __device__ __forceinline__ float base_of(float m) { return m == -kInf ? 0.0f : m; }
 
@@ -45,13 +49,21 @@ __device__ __forceinline__ float largest_of(const float (&x)[8]) {
     return max_nan(h.first, h.second);
 }
 
+// x log2(e) / T - m; HUGE: m may be huge.
+template <bool HUGE>
+__device__ __forceinline__ float beyond(float x, float scale, float m) {
+    const float d = __builtin_fmaf(x, scale, -m);
+    return HUGE && fabsf(m) >= kHuge ? x * scale - m : d;
+}
+
 // s and t of the lane's eight logits about the leaf's m.
+template <bool HUGE>
 __device__ __forceinline__ void sums_of(const float (&x)[8], float scale, float m, float &s, float &t) {
     const float at = base_of(m);
     float e[8], u[4];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        const float d0 = __builtin_fmaf(x[i], scale, -at), d1 = __builtin_fmaf(x[i + 1], scale, -at);
+        const float d0 = beyond<HUGE>(x[i], scale, at), d1 = beyond<HUGE>(x[i + 1], scale, at);
         e[i] = exp2_fast(d0);
         e[i + 1] = exp2_fast(d1);
         u[i / 2] = __builtin_fmaf(e[i + 1], fmaxf(d1, kFar), e[i] * fmaxf(d0, kFar));
@@ -80,11 +92,18 @@ __device__ __forceinline__ float leaf_sums(const float (&v)[4]) {
 // The joined state of LEAVES consecutive leaves (1, 2 or 4), the same in all lanes that hold a row.
 template <int LEAVES>
 __device__ __forceinline__ Part leaves_of(const float (&x)[LEAVES][8], float scale) {
-    float m[LEAVES], s[LEAVES], t[LEAVES];
+    float m[LEAVES], s[LEAVES], t[LEAVES], most = 0;
 #pragma unroll
     for (int f = 0; f < LEAVES; ++f) {
         m[f] = largest_of(x[f]) * scale;
-        sums_of(x[f], scale, m[f], s[f], t[f]);
+        most = fmaxf(most, fabsf(m[f]));
+    }
+    if (__ballot(most >= kHuge)) {     // also where a leaf has no columns
+#pragma unroll
+        for (int f = 0; f < LEAVES; ++f) sums_of<true>(x[f], scale, m[f], s[f], t[f]);
+    } else {
+#pragma unroll
+        for (int f = 0; f < LEAVES; ++f) sums_of<false>(x[f], scale, m[f], s[f], t[f]);
     }
     if constexpr (LEAVES == 4) {
         // a leaf in each quarter, joined across them
@@ -221,7 +240,7 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_scor
 // that is nearly sure keeps its digits so (of 1 - p = 10^-4 the sum of all terms holds three).
 __device__ __forceinline__ float sure_of(float x, float scale, const Part &rest) {
     if (rest.m == -kInf) return x == -kInf ? -kInf : 0.0f;
-    const float d = __builtin_fmaf(x, scale, -rest.m);       // exact but for one rounding
+    const float d = beyond<true>(x, scale, rest.m);          // exact but for one rounding
     return d > -60.0f ? -log1pf(rest.s * exp2f(-d)) : (d - log2f(rest.s)) * kLn2;
 }
 
@@ -283,11 +302,11 @@ __global__ __launch_bounds__(ROWS == 1 ? 256 : 64 * ROWS) void rog_linear_join_k
     float logp = 0, entropy = 0, lse = 0;
     if (tok >= 0) {
         const float log_s = log2f(all.s);
-        const bool empty = all.m == -kInf;
-        lse = empty ? -kInf : (all.m + log_s) * kLn2;
-        entropy = empty ? 0.0f : fmaxf(0.0f, (log_s - all.t / all.s) * kLn2);
-        if (!(all.s == all.s)) entropy = all.s;
-        if (p.logp) logp = !(all.s == all.s) || tok >= int64_t(p.vocab) ? __builtin_nanf("") : empty ? -kInf : sure_of(p.target[n], p.scale, rest);
+        const bool empty = all.m == -kInf, bad = !(all.s == all.s) || all.m == kInf;   // of a NaN, of +inf (also by the scale)
+        const float nan = __builtin_nanf("");
+        lse = bad ? nan : empty ? -kInf : (all.m + log_s) * kLn2;
+        entropy = bad ? nan : empty ? 0.0f : fmaxf(0.0f, (log_s - all.t / all.s) * kLn2);
+        if (p.logp) logp = bad || tok >= int64_t(p.vocab) ? nan : empty ? -kInf : sure_of(p.target[n], p.scale, rest);
     }
     if (p.logp) p.logp[row] = logp;
     if (p.entropy) p.entropy[row] = entropy;

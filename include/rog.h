@@ -572,7 +572,10 @@ typedef struct {
  * are nearer to the formula than rog_logprob's over logits of two bytes.  The log
  * probability is formed from the terms beside the token, so a token that is nearly
  * sure keeps its digits (about 10^-6 of the value, beside what the logits' own sums
- * leave open).  A NaN or +inf among a row's logits makes its numbers NaN.
+ * leave open).  A NaN or +inf among a row's logits makes its numbers NaN.  The
+ * row's statistics are held as x log2(e) / temperature in binary32, so a logit
+ * of more than 2.35 * 10^38 * temperature counts as infinite, with its sign;
+ * columns masked by any large negative value have probability 0.
  *
  * Errors as rog_logprob; rows are at most 2^26 - 16 (ROG_ERR_TOO_LARGE).
  */
