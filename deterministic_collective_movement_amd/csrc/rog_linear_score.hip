@@ -389,9 +389,20 @@ constexpr float kLog2E = 1.44269504088896341f;
 // What a row's coefficients are made of: G = 2^y (c0 + c1 y) with y = x log2(e) / T - at, and g more at the token.
 struct RowOf {
     float at, c0, c1, g;
+    float uniform;                     // y where the row is uniform over its largest logits: -entropy log2(e)
     float again;                       // binary16: from the row's scale to that of all rows
     uint32_t target;                   // the token as a column of the tile, else past it
 };
+// |at| from which lse's rounding is looked after, up to 4.5 half steps of it (m's, its sum's with log2 s, three products with
+// ln 2 and log2(e)) and what log2 s and the entropy leave: a row that is uniform over its largest logits (sure of one
+// token, or masked as a whole) has y = -entropy log2(e) at each of them, so a y that lies within the rounding of that is
+// taken to be that, and p is at most 1.  Any other y that happens to lie there moves by less than one more rounding of lse.
+constexpr float kLarge = 16384.0f;
+__device__ __forceinline__ float settled(float y, float at, float uniform) {
+    const bool near = fabsf(y - uniform) <= __builtin_fmaf(fabsf(at), 4.5f * 0x1p-24f, 0x1p-15f);
+    return !(fabsf(at) >= kLarge) || at == kInf ? y : near ? uniform : y > 0.0f ? 0.0f : y;
+}
+
 template <int DT>
 __device__ __forceinline__ RowOf coef_row(const GradArgs &p, uint32_t row, int64_t first, uint32_t columns) {
     const int64_t tok = p.tokens[row];
@@ -410,6 +421,7 @@ __device__ __forceinline__ RowOf coef_row(const GradArgs &p, uint32_t row, int64
     r.c0 = -__builtin_fmaf(gh, h, g);
     r.c1 = -gh * kLn2;
     r.g = g;
+    r.uniform = -h * kLog2E;
     r.target = tok >= first && tok - first < int64_t(columns) ? uint32_t(tok - first) : 1u << 30;
     return r;
 }
@@ -437,15 +449,17 @@ __device__ __forceinline__ void coef_tile(const GradArgs &p, uint32_t r, uint32_
         const uint32_t n = n0 + w0 + 16 * j + l % 16;
         const RowOf row = row_of[w0 + 16 * j + l % 16];
         const uint32_t hit = row.target - m0;
-        const bool hits = __ballot(hit < FM * 16) != 0;
+        const bool hits = __ballot(hit < FM * 16) != 0, large = __ballot(fabsf(row.at) >= kLarge) != 0;
 #pragma unroll
         for (int f = 0; f < LEAVES; ++f) {
             float d[8];
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
-                const float y = __builtin_fmaf(acc[2 * f + i / 4][j][i % 4], scale, -row.at);
-                d[i] = exp2_fast(y) * __builtin_fmaf(row.c1, fmaxf(y, kFar), row.c0);
-            }
+            for (uint32_t i = 0; i < 8; ++i) d[i] = __builtin_fmaf(acc[2 * f + i / 4][j][i % 4], scale, -row.at);
+            if (large)
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) d[i] = settled(d[i], row.at, row.uniform);
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) d[i] = exp2_fast(d[i]) * __builtin_fmaf(row.c1, fmaxf(d[i], kFar), row.c0);
             if (hits)
 #pragma unroll
                 for (uint32_t i = 0; i < 8; ++i)

@@ -121,3 +121,25 @@ def test_rows_that_are_uniform_over_large_logits(gpu, n, T, c):
     assert bool(((r.lse.double() - x - math.log(k)).abs() <= 2.0 ** -21 * abs(x) + 1e-5).all())
     assert bool(((r.logp.double() + math.log(k)).abs() <= 2e-6).all())
     assert bool(((r.entropy.double() - math.log(k)).abs() <= 2e-5).all())
+
+
+@pytest.mark.parametrize("n", [3, 40, 100, 300])
+@pytest.mark.parametrize("T", [1.0, 0.7, 3.0])
+@pytest.mark.parametrize("c", LARGE)
+def test_gradient_of_rows_that_are_uniform_over_large_logits(gpu, n, T, c):
+    """p is 1 / k at each of the k, whatever lse's rounding leaves open."""
+    h, ws, tokens, top, _ = uniform(gpu, n, T, c)
+    r = rog.rog_linear_logprob(h, ws, tokens, temperature=T)
+    g = torch.randn(n, device=gpu)
+    d = rog.rog_linear_logprob_grad(h, ws, tokens, r.lse, r.entropy, g, 0.3 * g, temperature=T)
+    G = torch.zeros(n, 512, dtype=torch.float64, device=gpu)
+    G[:, top] = -1.0 / len(top)
+    G[torch.arange(n, device=gpu), tokens] += 1.0
+    G *= g.double()[:, None] / T
+    want, size = G.t() @ h.double(), G.abs().t() @ h.double().abs()
+    # G rounded once, the sum once; p to lse's rounding below 2^14 / log2(e) and to that of e^{-H} above, log p + H likewise
+    tol = 2.0 ** -8 * (want.abs() + size) + 0.004 * size + 1e-6
+    assert bool(((d.d_weights[0].double() - want).abs() <= tol).all())
+    # the top columns' other weights are 0, and G is 0 outside; element 0 is a sum of terms of up to |g| |c| / T, which
+    # pass the binary32 range (3.4e38) where c is 1e38 and |g| / T above 3.4
+    assert bool((d.d_hidden[:, 1:] == 0).all()) and (abs(c) > 1e37 or bool(torch.isfinite(d.d_hidden).all()))
