@@ -1150,7 +1150,7 @@ def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor
             # the library enqueues nothing: a sum over no rows is zero
             with _made_on(stream, device):
                 for g in out.d_weights:
-                    g.zero_()
+                    g.detach().zero_()
     return out
 
 

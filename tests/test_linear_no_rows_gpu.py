@@ -53,6 +53,14 @@ def test_on_a_stream_by_name_and_captured(gpu):
         assert all(bool((g == 0).all()) for g in out.d_weights)
 
 
+def test_outputs_that_require_gradients(gpu):
+    # written like any other output: in no autograd graph
+    h, ws, tokens, none = inputs(gpu, torch.bfloat16)
+    out = rog.RogLinearGrad(torch.empty_like(h), [torch.full_like(w, 7.0).requires_grad_() for w in ws])
+    rog.rog_linear_logprob_grad(h, ws, tokens, none, none, none, out=out)
+    assert all(g.is_leaf and bool((g == 0).all()) for g in out.d_weights)
+
+
 def test_refusals_stay(gpu):
     h, ws, tokens, none = inputs(gpu, torch.bfloat16)
     with pytest.raises(ValueError):
