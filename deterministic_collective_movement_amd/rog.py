@@ -1021,14 +1021,14 @@ def _row_matrix(t, what: str, rows: Optional[int], cols: Optional[int], dtype: t
     return t.data_ptr(), stride
 
 
-def _head_bytes(hidden, weights, dtypes):
+def _head_bytes(hidden, what: str, weights, dtypes):
     """(device, its index, rows, dim, dtype, address and stride of the states, packed rog_weight_shard array)."""
     if not isinstance(hidden, torch.Tensor):
-        raise TypeError("hidden must be a torch.Tensor")
+        raise TypeError("%s must be a torch.Tensor" % what)
     device, dtype = hidden.device, hidden.dtype
     if dtype not in dtypes:
-        raise ValueError("hidden states are %s (got %s)" % (" or ".join(str(d)[6:] for d in dtypes), dtype))
-    at, stride = _row_matrix(hidden, "hidden", None, None, dtype, device)
+        raise ValueError("%s is %s (got %s)" % (what, " or ".join(str(d)[6:] for d in dtypes), dtype))
+    at, stride = _row_matrix(hidden, what, None, None, dtype, device)
     rows, dim = hidden.shape
     if len(weights) == 0:
         raise ValueError("need at least one shard of weights")
@@ -1085,7 +1085,7 @@ def rog_linear_logprob(hidden: torch.Tensor, weights: Sequence[torch.Tensor], to
             out = RogLogprob(*out)
         if _binding is not None and _binding.linear_logprob(hidden, weights, tokens, temperature, out):
             return out
-    device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, weights, _PRODUCT_DTYPES)
+    device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, "hidden", weights, _PRODUCT_DTYPES)
     f32 = torch.float32
     if out is None:
         new = lambda: torch.empty(rows, dtype=f32, device=device)  # noqa: E731
@@ -1120,7 +1120,7 @@ def rog_linear_logprob_grad(hidden: torch.Tensor, weights: Sequence[torch.Tensor
             out = RogLinearGrad(out[0], list(out[1]))
         if _binding is not None and _binding.linear_grad(hidden, weights, tokens, lse, entropy, g_logp, g_entropy, temperature, out[0], out[1]):
             return out
-    device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, weights, _PRODUCT_DTYPES)
+    device, idx, rows, dim, dtype, at, stride, packed = _head_bytes(hidden, "hidden", weights, _PRODUCT_DTYPES)
     W = len(weights)
     if out is None:
         with _made_on(stream, device):
@@ -1194,7 +1194,7 @@ def rog_linear_i8(q: torch.Tensor, scale: torch.Tensor, weights: Sequence[torch.
     [width_r] float32."""
     if out is not None and stream is None and _binding is not None and _binding.linear_i8(q, scale, weights, weight_scales, out):
         return out if isinstance(out, list) else list(out)
-    device, idx, rows, dim, _, at, stride, _ = _head_bytes(q, weights, (torch.int8,))
+    device, idx, rows, dim, _, at, stride, _ = _head_bytes(q, "q", weights, (torch.int8,))
     W = len(weights)
     if out is None:
         if dtype not in DTYPES:
