@@ -645,4 +645,17 @@ __device__ __forceinline__ uint32_t shard_of_tile(const WeightShards &h, uint32_
     return r;
 }
 
+// Host: enqueues a kernel of one argument structure, and what a call answers then.
+template <class Args>
+inline hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
+    void *list[] = {const_cast<Args *>(&args)};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
+}
+
+inline rog_status launched(hipError_t e) {
+    if (e == hipSuccess) return ROG_OK;
+    g_last_hip_error = int(e);
+    return ROG_ERR_LAUNCH;
+}
+
 }  // namespace rog

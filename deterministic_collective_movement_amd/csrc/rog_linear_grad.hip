@@ -62,39 +62,39 @@ template <int DT, int FM, int FN, int WN>
 __device__ __forceinline__ void put_states(uint32_t s, uint32_t d0, uint32_t n0, uint32_t rows, f32x4 (&acc)[FM][FN]) {
     const BackArgs &p = fresh_args<BackArgs>();
     const bool running = p.part_seg == 0, first = running && p.first && s == 0, last = running && p.last && s + 1 == p.segs;
-            pair_all(acc);
-            const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
-                    float *part = p.part + uint64_t(s) * p.part_seg;
+    pair_all(acc);
+    const uint32_t t = fresh_thread(), l = t % 64, m0 = t / 64 / WN * (FM * 16), w0 = t / 64 % WN * (FN * 16);
+    float *part = p.part + uint64_t(s) * p.part_seg;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const uint32_t n = n0 + w0 + 16 * j + l % 16;
-                if (n >= rows) continue;
-                const uint32_t row = p.index[n];
-                const float inv = last ? unscale<DT>(p, row) : 1.0f;
-                uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
+    for (int j = 0; j < FN; ++j) {
+        const uint32_t n = n0 + w0 + 16 * j + l % 16;
+        if (n >= rows) continue;
+        const uint32_t row = p.index[n];
+        const float inv = last ? unscale<DT>(p, row) : 1.0f;
+        uint8_t *out = static_cast<uint8_t *>(p.d_hidden) + uint64_t(row) * uint64_t(p.d_stride);
 #pragma unroll
-                for (int f = 0; f < FM / 2; ++f) {
-                    const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
-                    if (d >= p.dim) continue;
-                    float x[8];
+        for (int f = 0; f < FM / 2; ++f) {
+            const uint32_t d = d0 + m0 + 32 * f + 8 * eight_of(l / 16);
+            if (d >= p.dim) continue;
+            float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4];
-                    gf32x4_out *at = (gf32x4_out *)(part + uint64_t(n) * p.dim_pad + d);
-                    if (running && !first) {
-                        const f32x4 lo = at[0], hi = at[1];
+            for (int i = 0; i < 8; ++i) x[i] = acc[2 * f + i / 4][j][i % 4];
+            gf32x4_out *at = (gf32x4_out *)(part + uint64_t(n) * p.dim_pad + d);
+            if (running && !first) {
+                const f32x4 lo = at[0], hi = at[1];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = (i < 4 ? lo[i % 4] : hi[i % 4]) + x[i];
-                    }
-                    if (last) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] *= inv;
-                        put8<DT>(out + d * 2, x, p.dim - d);
-                    } else {
-                        at[0] = f32x4{x[0], x[1], x[2], x[3]};
-                        at[1] = f32x4{x[4], x[5], x[6], x[7]};
-                    }
-                }
+                for (int i = 0; i < 8; ++i) x[i] = (i < 4 ? lo[i % 4] : hi[i % 4]) + x[i];
             }
+            if (last) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= inv;
+                put8<DT>(out + d * 2, x, p.dim - d);
+            } else {
+                at[0] = f32x4{x[0], x[1], x[2], x[3]};
+                at[1] = f32x4{x[4], x[5], x[6], x[7]};
+            }
+        }
+    }
 }
 
 // The rows of part `split`: whole lines of 64, the same number but for the last.
@@ -359,12 +359,6 @@ __global__ __launch_bounds__(256) void rog_linear_weights_join_kernel(BackArgs p
     put8<DT>(static_cast<uint8_t *>(p.dw[r]) + uint64_t(v) * uint64_t(p.dw_stride[r]) + d * 2, x, p.dim - d);
 }
 
-template <class Args>
-hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
-    void *list[] = {const_cast<Args *>(&args)};
-    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
-}
-
 template <int DT>
 hipError_t launch_back(const GradPlan &p, const BackArgs &a, const PieceGrid &grid, hipStream_t s) {
     if (p.form == kFormWide)
@@ -406,11 +400,7 @@ ROG_API rog_status rog_linear_logprob_grad(const void *hidden, int64_t hidden_st
             e = dtype == ROG_DTYPE_BF16 ? launch(rog_linear_weights_join_kernel<ROG_DTYPE_BF16>, grid.weights_join, 256, p.back, stream)
                                         : launch(rog_linear_weights_join_kernel<ROG_DTYPE_F16>, grid.weights_join, 256, p.back, stream);
     }
-    if (e != hipSuccess) {
-        g_last_hip_error = int(e);
-        return ROG_ERR_LAUNCH;
-    }
-    return ROG_OK;
+    return launched(e);
 }
 
 }  // extern "C"

@@ -185,12 +185,6 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_i8_k
     }
 }
 
-template <class Args>
-hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
-    void *list[] = {const_cast<Args *>(&args)};
-    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
-}
-
 template <int DT>
 hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t s) {
     const bool held = uint64_t(a.dim) * Logit<DT>::kSize <= kHeld * kQuantThreads * 16;
@@ -209,12 +203,6 @@ hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
 template <int OT>
 hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
     return p.direct ? launch_i8<OT, true>(p, s) : launch_i8<OT, false>(p, s);
-}
-
-rog_status launched(hipError_t e) {
-    if (e == hipSuccess) return ROG_OK;
-    g_last_hip_error = int(e);
-    return ROG_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -517,18 +517,6 @@ __global__ __launch_bounds__(F::kThreads, F::kWide ? 2 : 1) void rog_linear_coef
     }
 }
 
-rog_status launched(hipError_t e) {
-    if (e == hipSuccess) return ROG_OK;
-    g_last_hip_error = int(e);
-    return ROG_ERR_LAUNCH;
-}
-
-template <class Args>
-hipError_t launch(void (*kernel)(Args), uint32_t grid, uint32_t threads, const Args &args, hipStream_t stream) {
-    void *list[] = {const_cast<Args *>(&args)};
-    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(threads), list, 0, stream);
-}
-
 template <int DT, bool DIRECT>
 hipError_t launch_score(const ScorePlan &p, hipStream_t s) {
     switch (p.form) {
