@@ -184,13 +184,14 @@ struct Form {
 // 64 rows of 131072 x 4096: 178 us, 6.1 TB/s).  Four slabs of 128 + 32 rows are those 80 KiB, and the score's and the
 // coefficients' tiles have their rows' numbers beside them: three there (scores with four slabs and one workgroup per
 // CU, and with three and two, us: 16 x 131072 x 4096 192.7 and 186.5, 4 x 50257 x 1600 35.6 and 31.5, 7 x 100000 x 768 40.8
-// and 34.1, 1 x 32003 x 4096 48.1 and 43.0, 3 x 65536 x 5120 122.6 and 123.5, 1 x 131072 x 2048 116 and 121.5; the 8-bit product,
-// with two workgroups either way, 16 x 131072 x 4096 104.7 with four and 105.4).  Past that by the matrix units: 256 x 256 take 128 elements of an operand from the shared memory per
+// and 34.1, 3 x 65536 x 5120 122.6 and 123.5, 1 x 131072 x 2048 116 and 121.5), but where a CU has no second
+// workgroup anyway (in a graph, 1 x 32003 x 512 13.6 with four and 13.95 with three, 3 x 32003 x 1024 19.1 and 19.7).  The
+// 8-bit product has two with four slabs (16 x 131072 x 4096 104.7, with three 105.4).  Past that by the matrix units: 256 x 256 take 128 elements of an operand from the shared memory per
 // 16 x 16 x 32 instruction and lane group, the least of the tiles tried (8192 rows of 131072 x 4096: 256 x 128 by
 // eight waves 1060 TFLOP/s and by four 1134, 256 x 256 by 2 x 2 waves 1183, by 2 x 4 1380); eight waves are two per
 // SIMD, with 128 accumulators of their 256 registers each.
 typedef Form<128, 32, 4, 1, 3, false> FormFew;
-typedef Form<128, 32, 4, 1, 4, false> FormFewI8;
+typedef Form<128, 32, 4, 1, 4, false> FormFewDeep;
 typedef Form<128, 64, 4, 1, 3, false> FormSome;
 typedef Form<128, 128, 2, 2, 4, true> FormMid;
 typedef Form<256, 256, 2, 4, 4, true> FormWide;

@@ -197,7 +197,7 @@ hipError_t launch_i8(const LinearI8Plan &p, hipStream_t s) {
     case kFormWide: return launch(rog_linear_i8_kernel<OT, FormWide, DIRECT>, p.grid, FormWide::kThreads, p.args, s);
     case kFormMid: return launch(rog_linear_i8_kernel<OT, FormMid, DIRECT>, p.grid, FormMid::kThreads, p.args, s);
     case kFormSome: return launch(rog_linear_i8_kernel<OT, FormSome, DIRECT>, p.grid, FormSome::kThreads, p.args, s);
-    default: return launch(rog_linear_i8_kernel<OT, FormFewI8, DIRECT>, p.grid, FormFewI8::kThreads, p.args, s);
+    default: return launch(rog_linear_i8_kernel<OT, FormFewDeep, DIRECT>, p.grid, FormFewDeep::kThreads, p.args, s);
     }
 }
 template <int OT>

@@ -523,7 +523,9 @@ hipError_t launch_score(const ScorePlan &p, hipStream_t s) {
     case kFormWide: return launch(rog_linear_score_kernel<DT, FormWide, DIRECT>, p.grid, FormWide::kThreads, p.args, s);
     case kFormMid: return launch(rog_linear_score_kernel<DT, FormMid, DIRECT>, p.grid, FormMid::kThreads, p.args, s);
     case kFormSome: return launch(rog_linear_score_kernel<DT, FormSome, DIRECT>, p.grid, FormSome::kThreads, p.args, s);
-    default: return launch(rog_linear_score_kernel<DT, FormFew, DIRECT>, p.grid, FormFew::kThreads, p.args, s);
+    default:
+        return p.grid <= kCus ? launch(rog_linear_score_kernel<DT, FormFewDeep, DIRECT>, p.grid, FormFewDeep::kThreads, p.args, s)
+                              : launch(rog_linear_score_kernel<DT, FormFew, DIRECT>, p.grid, FormFew::kThreads, p.args, s);
     }
 }
 
@@ -533,7 +535,9 @@ hipError_t launch_coef(const GradPlan &p, const GradArgs &a, uint32_t grid, hipS
     case kFormWide: return launch(rog_linear_coef_kernel<DT, FormWide, DIRECT>, grid, FormWide::kThreads, a, s);
     case kFormMid: return launch(rog_linear_coef_kernel<DT, FormMid, DIRECT>, grid, FormMid::kThreads, a, s);
     case kFormSome: return launch(rog_linear_coef_kernel<DT, FormSome, DIRECT>, grid, FormSome::kThreads, a, s);
-    default: return launch(rog_linear_coef_kernel<DT, FormFew, DIRECT>, grid, FormFew::kThreads, a, s);
+    default:
+        return grid <= kCus ? launch(rog_linear_coef_kernel<DT, FormFewDeep, DIRECT>, grid, FormFewDeep::kThreads, a, s)
+                            : launch(rog_linear_coef_kernel<DT, FormFew, DIRECT>, grid, FormFew::kThreads, a, s);
     }
 }
 
