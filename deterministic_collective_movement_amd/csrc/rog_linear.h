@@ -198,8 +198,9 @@ typedef Form<256, 256, 2, 4, 4, true> FormWide;
 typedef Form<128, 128, 2, 4, 4, true> FormQuarter;   // of a wide tile, by as many threads
 constexpr uint32_t kCus = 256;         // workgroups of the wide form that run at a time
 // Tiles past the last whole round of the CUs up to which they are dealt in quarters: a round of quarters takes less than half of a
-// round of tiles, and 64 tiles are one round of them (1021 x 50257 x 1600 binary16, 20 tiles past the third round: 181 us
-// without, 169 with; splitting up to 128 or 192 tiles gained nothing more).
+// round of tiles, and 64 tiles are one round of them (us, whole and in quarters: 1024 rows of K 1600 with 20, 40, 64, 88, 100,
+// 128 and 160 tiles past the third round 188 and 179, 187 and 172, 188 and 175, 188 and 190, 189 and 190.5, 189 and 191,
+// 192 and 210; of K 4096 with 40, 88, 128 and 160 past the first 188 and 155, 190 and 195, 194 and 203, 200 and 243).
 constexpr uint32_t kTailSplit = 64;
 enum { kFormFew = 0, kFormSome = 1, kFormMid = 2, kFormWide = 3 };
 

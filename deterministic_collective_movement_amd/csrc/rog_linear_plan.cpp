@@ -91,7 +91,12 @@ uint32_t tile_rows(int32_t form) { return kFormRows[form]; }
 // Workgroups for so many tiles: the wide form deals some of them out in quarters, by the rows that there turn out to be.
 uint64_t groups_of(uint64_t tiles, int32_t form) { return form == kFormWide && tiles ? tiles + 3 * kTailSplit : tiles; }
 
-constexpr uint64_t kMidCubes = 224, kMidCubesFew = 1024;   // of 256 rows x 256 columns x 256 elements: up to these the mid form
+// Cubes of 256 rows x 256 columns x 256 elements up to which the mid form is taken, and the same for up to 128 rows.  There the
+// crossing lies between 1000 and 3000 cubes, lower for narrow states (us, mid and wide: 128 x 28672 x 1024, 448 cubes,
+// 77 and 118; 70 x 50257 x 1000 binary16, 788, 126 and 123; 100 x 32000 x 2048, 1000, 121 and 210; 70 x 50257 x 1600
+// binary16, 1379, 166 and 148; 128 x 50257 x 2048, 1576, 216 and 260; 100 x 32000 x 4096, 2000, 275 and 312;
+// 128 x 131072 x 1024, 2048, 294 and 248; 100 x 50257 x 4096, 3152, 431 and 345; 100 x 131072 x 2048, 4096, 561 and 475).
+constexpr uint64_t kMidCubes = 224, kMidCubesFew = 1024;
 // Rows from which the scored ones are packed: few rows are one tile whether scored or not, and a launch is 4 us more;
 // of many the tiles of rows that do not count are saved (8192 x 4096: 25 us, where every eighth row that does not count
 // takes an eighth of 6.5 ms with it).

@@ -426,7 +426,13 @@ __device__ __forceinline__ RowOf coef_row(const GradArgs &p, uint32_t row, int64
     return r;
 }
 
-// The tile of F's size at columns v0 of shard r, which are columns g0 of the piece, and rows n0.
+// The tile of F's size at columns v0 of shard r, which are columns g0 of the piece, and rows n0.  G is rounded to the
+// weights' type here, the type that the matrix units take: held in two parts, which would keep 16 bits of it in
+// bf16 and 22 in binary16, both products behind it would take twice the instructions, 10 N V D operations in all instead of
+// 6, and G's memory and traffic double.  Rounded once it is off by half a step, as the outputs are by theirs (errors against
+// 64 bits 2.4-2.7e-3 of the norm in bf16 and 3e-4 in binary16; of binary32 coefficients, with the output's rounding
+// alone, 1.7e-3 and 2.1e-4).  Calls of few rows have the same coefficients, so that a row's bits do not depend on how many
+// there are.
 template <int DT, class F, bool DIRECT>
 __device__ __forceinline__ void coef_tile(const GradArgs &p, uint32_t r, uint32_t v0, uint32_t g0, uint32_t n0, uint32_t rows,
                                           const TileMemory &memory, RowOf *row_of) {

@@ -532,8 +532,8 @@ ROG_API size_t rog_policy_loss_workspace_bytes(size_t n);
  *    zero-filled for the other operators may serve these too (its arrival
  *    counters are left zero).
  *  - dim is 1 .. 2^17 - 1; row strides are below 2^22 bytes (ROG_ERR_TOO_LARGE).
- *    Any alignment to the element; calls whose rows all begin and end on 16 bytes
- *    are faster.
+ *    Any alignment to the element; rows that begin on 4 bytes are faster, and for
+ *    the gradient rows of a multiple of 16 bytes.
  * ======================================================================== */
 
 /* One shard of a head: column j's weights are weight[j * row_stride + 0 .. dim). */
