@@ -180,7 +180,7 @@ struct Form {
     static_assert(COLUMNS % kLinearBlock == 0 && COLUMNS / WM % 32 == 0 && COLUMNS / WM <= int(kLinearBlock), "whole leaves, blocks");
 };
 // Up to 64 rows a call is bound by the weights' bytes: small tiles, whole lines, one or two of them in flight per
-// workgroup and two workgroups per CU, which have 80 KiB of shared memory each (one 32003 x 512 bf16 head: 7.6 us, 4.3 TB/s;
+// workgroup and two workgroups per CU, which have 80 KiB of shared memory each (one 32003 x 512 bf16 head: 7.7 us, 4.2 TB/s;
 // 64 rows of 131072 x 4096: 178 us, 6.1 TB/s).  Four slabs of 128 + 32 rows are those 80 KiB, and the score's and the
 // coefficients' tiles have their rows' numbers beside them: three there (scores with four slabs and one workgroup per
 // CU, and with three and two, us: 16 x 131072 x 4096 192.7 and 186.5, 4 x 50257 x 1600 35.6 and 31.5, 7 x 100000 x 768 40.8
