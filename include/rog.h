@@ -603,7 +603,7 @@ ROG_API rog_status rog_linear_logprob_plan(const rog_weight_shard *shards, int W
  * sums are binary32, and each output is rounded once.  g_entropy may be NULL (0).
  *
  * p_j has the rounding of lse in it, which at |lse| = 2^e holds it to a factor of
- * e^{2^(e - 21)}.  Rows that are uniform over their largest logits (sure of one token,
+ * e^{2^(e - 20)}.  Rows that are uniform over their largest logits (sure of one token,
  * masked as a whole) have p_j = e^{-entropy} there and are right at any size.
  *
  * A row that is not scored gets zeros and its state is not used.  A token of V or

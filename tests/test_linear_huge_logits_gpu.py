@@ -143,3 +143,36 @@ def test_gradient_of_rows_that_are_uniform_over_large_logits(gpu, n, T, c):
     # the top columns' other weights are 0, and G is 0 outside; element 0 is a sum of terms of up to |g| |c| / T, which
     # pass the binary32 range (3.4e38) where c is 1e38 and |g| / T above 3.4
     assert bool((d.d_hidden[:, 1:] == 0).all()) and (abs(c) > 1e37 or bool(torch.isfinite(d.d_hidden).all()))
+
+
+@pytest.mark.parametrize("n", [3, 40, 100, 300])
+@pytest.mark.parametrize("c", [64.0, 1024.0, 8192.0, 2.0 ** 14, 2.0 ** 15, -2.0 ** 15, 2.0 ** 17, -2.0 ** 18, 2.0 ** 20])
+def test_gradient_of_rows_of_near_values(gpu, n, c):
+    """Values half an integer apart, far from zero: what one binary32 lse leaves open, twice at most."""
+    V = 515
+    h = torch.zeros(n, 64, dtype=BF16, device=gpu)
+    w = torch.zeros(V, 64, dtype=BF16, device=gpu)
+    h[:, 0] = 1.0
+    w[:, 0] = c
+    h[:, 1] = torch.arange(n, device=gpu) % 4 + 1.0
+    w[:, 1] = torch.arange(V, device=gpu) * 5 % 7 * 0.5             # every logit is exact in binary32
+    h[:, 2:] = torch.randn(n, 62, device=gpu)                       # over weights of 0: for the weights' gradients alone
+    tokens = torch.arange(n, device=gpu) * 11 % V
+    x = h[:, :2].double() @ w[:, :2].double().t()
+    r = rog.rog_linear_logprob(h, [w], tokens)
+    lse = torch.logsumexp(x, 1)
+    p, g, gh = torch.softmax(x, 1), torch.randn(n, device=gpu), 0.3 * torch.randn(n, device=gpu)
+    lp = torch.log_softmax(x, 1)
+    H = -(p * lp).sum(1)
+    assert bool(((r.logp.double() - lp[torch.arange(n, device=gpu), tokens]).abs() <= 1e-5).all())
+    assert bool(((r.entropy.double() - H).abs() <= 3e-5).all()) and bool(((r.lse.double() - lse).abs() <= 2.0 ** -22 * lse.abs() + 1e-5).all())
+    d = rog.rog_linear_logprob_grad(h, [w], tokens, r.lse, r.entropy, g, gh)
+    G = -g.double()[:, None] * p - gh.double()[:, None] * p * (lp + H[:, None])
+    G[torch.arange(n, device=gpu), tokens] += g.double()
+    left = 2.0 ** -20 * lse.abs()[:, None] + 1e-4                   # of log p
+    a = g.double().abs()[:, None] + gh.double().abs()[:, None] * (lp.abs() + H[:, None] + 1)
+    tol = p * torch.expm1(left) * a * (2 + left)
+    tol = tol + ref.HALF[BF16] * (G.abs() + tol)
+    want, size = G.t() @ h.double(), h.double().abs()
+    tol = tol.t() @ size + (n + 64) * 2 * 2.0 ** -24 * (G.abs().t() @ size)
+    assert bool(((d.d_weights[0].double() - want).abs() <= tol + ref.HALF[BF16] * (want.abs() + tol)).all())
